@@ -258,6 +258,153 @@ pkd_status pkd_cache_write(const void* key, const void* value, pkd_dtype in_dtyp
                            void* kv_cache, pkd_dtype kv_dtype, float k_scale, float v_scale, void* stream);
 
 /*
+ * Rotary step of a layer in one launch: queries rotated, keys rotated and
+ * appended to the paged cache with their values (pkd_cache_write with the
+ * position rotation on the way).
+ *
+ *   q             device [num_tokens, num_heads, head_dim], in_dtype (bf16 or fp16),
+ *                 q_stride elements between tokens; NULL with num_heads == 0
+ *   key, value    device [num_tokens, num_kv_heads, head_dim], in_dtype
+ *                 (strides: multiples of 8 elements; all pointers 16-byte aligned)
+ *   positions     device int64 [num_tokens]
+ *   cos_sin       device fp32 [max_position, rotary_dim], 16-byte aligned: row p
+ *                 holds rotary_dim/2 cosines, then rotary_dim/2 sines of position p
+ *   slot_mapping  device int64 [num_tokens], as for pkd_cache_write; slots >= 0
+ *                 must be distinct (two tokens in one slot race)
+ *   kv_cache      as for pkd_cache_write
+ *   q_out         device [num_tokens, num_heads, head_dim], q_out_dtype, q_out_stride
+ *                 elements between tokens: in_dtype, or PKD_FP8_E4M3 for
+ *                 e4m3(rot(q) / q_scale), the pre-quantised q of an fp8 decode.
+ *                 May be q itself (same dtype and stride); no other overlap.
+ *
+ * Pair j of a head is (x[j], x[j + rotary_dim/2]), or (x[2j], x[2j+1]) when
+ * interleaved is not 0; it becomes (x1 c - x2 s, x2 c + x1 s).  Dims from
+ * rotary_dim on are copied.  Computed in fp32, rounded once to the type that
+ * is stored; values are stored as pkd_cache_write stores them.  A token whose
+ * position lies outside [0, max_position) writes nothing; a token whose slot
+ * is negative (padding) or past the cache writes its q_out row only.
+ * Limits: head_dim 64 or 128; rotary_dim a multiple of 16 up to head_dim.
+ */
+pkd_status pkd_rope_cache_write(const void* q, int64_t q_stride, const void* key, int64_t key_stride,
+                                const void* value, int64_t value_stride, pkd_dtype in_dtype,
+                                const int64_t* positions, const float* cos_sin, int64_t max_position,
+                                int rotary_dim, int interleaved, const int64_t* slot_mapping,
+                                int64_t num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                int page_size, int64_t num_pages, void* kv_cache, pkd_dtype kv_dtype,
+                                float k_scale, float v_scale, void* q_out, int64_t q_out_stride,
+                                pkd_dtype q_out_dtype, float q_scale, void* stream);
+
+/*
+ * Score modifications and masks of pkd_paged_attention; zero-initialised: none.
+ *   softcap       c > 0: the scaled score s becomes c * tanh(s / c)
+ *   alibi_slopes  device fp32 [num_heads]: slope * |position - key| is then
+ *                 subtracted (a distance bias), or NULL
+ *   window        w > 0: a token at position p sees keys from p - (w - 1) on
+ *   prefix_lens   device int32 [batch]: with PKD_FLAG_CAUSAL, keys below the
+ *                 request's prefix_lens entry are visible to all its tokens (a
+ *                 prefix mask; the window still applies), or NULL
+ *   doc_start     device int32 [total_tokens]: first key that a query token
+ *                 sees (a document mask for packed documents), or NULL
+ */
+typedef struct {
+    float softcap;
+    const float* alibi_slopes;
+    int window;
+    const int32_t* prefix_lens;
+    const int32_t* doc_start;
+} pkd_score_options;
+
+/*
+ * Workspace bytes of pkd_paged_attention, and the kernel it launches.  Host
+ * only; the plan is fixed by these arguments (of the options: the window, and
+ * whether prefix_lens is given).
+ * 0 / NULL for an invalid request (the reason is in pkd_last_error).
+ */
+size_t pkd_paged_attention_workspace_size(int batch, int64_t total_tokens, int max_query_len, int num_heads,
+                                          int num_kv_heads, int head_dim, int page_size, int max_kv_len,
+                                          pkd_dtype kv_dtype, const pkd_score_options* options);
+const char* pkd_paged_attention_kernel_name(int batch, int64_t total_tokens, int max_query_len, int num_heads,
+                                            int num_kv_heads, int head_dim, int page_size, int max_kv_len,
+                                            pkd_dtype kv_dtype, const pkd_score_options* options);
+
+/*
+ * Attention of ragged query tokens over a paged cache: whole prompts, chunks
+ * of prompts, and steps of single tokens, mixed in one call, with capped
+ * scores, a distance bias, and window, prefix and document masks.
+ *
+ *   q            device [total_tokens, num_heads, head_dim], q_dtype == kv_dtype,
+ *                q_stride elements between tokens (a multiple of 16 bytes)
+ *   kv_cache, block_table, seq_lens  as for pkd_paged_decode; seq_lens[b] = L counts
+ *                the keys of request b including those of its query tokens
+ *                (already in the cache)
+ *   query_start  device int32 [batch + 1]: request b's query tokens are rows
+ *                [query_start[b], query_start[b + 1]) of q, at most max_query_len;
+ *                rows of q outside every request are neither read into a result
+ *                nor written in out and lse
+ *   out          device [total_tokens, num_heads, head_dim] contiguous, out_dtype
+ *   lse          device fp32 [total_tokens, num_heads] natural-log LSE, or NULL
+ *   workspace    at least pkd_paged_attention_workspace_size bytes, 256-byte
+ *                aligned, zeroed once (pkd_workspace_init); every call leaves it
+ *                ready for the next of this function or pkd_prefix_decode, whatever
+ *                its plan.  Calls that may overlap (streams, graphs) need one each.
+ *                pkd_workspace_check reads its status word (PKD_EDEVICE_BOUNDS also
+ *                for a query_start that falls, leaves [0, total_tokens] or holds
+ *                more than max_query_len tokens: clamped)
+ *   flags        PKD_FLAG_CAUSAL or 0
+ *
+ * Token i of request b (n tokens) has position p = L - n + i.  It sees keys
+ * [0, L), with PKD_FLAG_CAUSAL those up to p (and its prefix_lens), less what
+ * the window and doc_start exclude.  A token that sees no key gets out = 0 and
+ * lse = -inf.  Keys that no token of a request sees are not read into results;
+ * a value that one token sees and another one does not must be finite for the
+ * second (its weight there is 0).
+ * Limits: head_dim 64 or 128; page_size a multiple of 16; num_heads/num_kv_heads
+ * <= 128; batch <= 4096; scale * q_scale * k_scale > 0; fp8 caches need head_dim
+ * 128 and max_query_len * num_heads/num_kv_heads <= 16.
+ */
+pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_stride, const void* kv_cache,
+                               pkd_dtype kv_dtype, int64_t num_pages, const int32_t* block_table,
+                               int64_t block_table_stride, const int32_t* seq_lens, const int32_t* query_start,
+                               int batch, int64_t total_tokens, int max_query_len, int num_heads, int num_kv_heads,
+                               int head_dim, int page_size, int max_kv_len, float scale, float q_scale,
+                               float k_scale, float v_scale, const pkd_score_options* options, void* out,
+                               pkd_dtype out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                               unsigned flags, void* stream);
+
+/*
+ * Decode of a batch whose requests share long prefixes, each prefix computed
+ * once for all its requests.
+ *
+ *   q             device [batch, sq, num_heads, head_dim], q_dtype == kv_dtype
+ *   prefix_table  device int32 [groups, prefix_table_stride], prefix_lens device
+ *                 int32 [groups]: the pages and length of each shared prefix, in
+ *                 the same kv_cache
+ *   group_start   device int32 [groups + 1], rising: requests [group_start[g],
+ *                 group_start[g + 1]) follow prefix g; others follow none
+ *   block_table, seq_lens  the requests' own keys, after the prefix (seq_lens[b]
+ *                 keys; the first page of a request's row starts behind the prefix)
+ *   out, lse      as for pkd_paged_decode, over the prefix's and the own keys
+ *   softcap       as in pkd_score_options (0: none)
+ *   flags         PKD_FLAG_CAUSAL: token i sees its request's own keys up to
+ *                 position seq_lens[b] - sq + i; the prefix is seen whole
+ *
+ * The workspace is as for pkd_paged_attention.  max_prefix_len and max_kv_len
+ * bound prefix_lens and seq_lens.  Limits as for
+ * pkd_paged_attention, groups <= 4096; fp8 caches are not supported.
+ */
+size_t pkd_prefix_decode_workspace_size(int batch, int sq, int num_heads, int num_kv_heads, int head_dim,
+                                        int page_size, int groups, int max_prefix_len, int max_kv_len,
+                                        pkd_dtype kv_dtype);
+pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_cache, pkd_dtype kv_dtype,
+                             int64_t num_pages, const int32_t* prefix_table, int64_t prefix_table_stride,
+                             const int32_t* prefix_lens, const int32_t* group_start, int groups, int max_prefix_len,
+                             const int32_t* block_table, int64_t block_table_stride, const int32_t* seq_lens,
+                             int batch, int sq, int num_heads, int num_kv_heads, int head_dim, int page_size,
+                             int max_kv_len, float scale, float q_scale, float k_scale, float v_scale,
+                             float softcap, void* out, pkd_dtype out_dtype, float* lse, void* workspace,
+                             size_t workspace_bytes, unsigned flags, void* stream);
+
+/*
  * DASH segmented attention with its combine [DASH flash_dash_attention].
  *
  *   q        device [n, num_heads, head_dim], dtype (bf16 or fp16)

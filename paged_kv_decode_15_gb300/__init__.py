@@ -9,6 +9,9 @@ Entry points (same names as the C ABI in include/pkd.h, without the prefix):
   segmented_attention(q, k, v, used, bias, bs, local, out, ...)
   lse_merge(part_out, part_lse, prior=None, live=None, out=None, lse_out=None)
   workspace_size(...), workspace_init(ws), workspace_check(ws)
+  rope_cache_write(q, key, value, positions, cos_sin, slot_mapping, kv_cache, ...)
+  paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, ...)
+  prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, scale, ...)
 """
 from __future__ import annotations
 
@@ -30,7 +33,15 @@ SYMBOLS = ("pkd_version", "pkd_last_error", "pkd_paged_decode_workspace_size", "
            "pkd_workspace_init",
            "pkd_workspace_check", "pkd_paged_decode", "pkd_paged_decode_static", "pkd_paged_decode_static_check",
            "pkd_cache_write",
-           "pkd_segmented_attention", "pkd_segmented_attention_paged", "pkd_lse_merge")
+           "pkd_segmented_attention", "pkd_segmented_attention_paged", "pkd_lse_merge",
+           "pkd_rope_cache_write", "pkd_paged_attention_workspace_size", "pkd_paged_attention_kernel_name",
+           "pkd_paged_attention", "pkd_prefix_decode_workspace_size", "pkd_prefix_decode")
+
+
+class ScoreOptions(ctypes.Structure):
+    """pkd_score_options of the C ABI."""
+    _fields_ = [("softcap", ctypes.c_float), ("alibi_slopes", ctypes.c_void_p), ("window", ctypes.c_int),
+                ("prefix_lens", ctypes.c_void_p), ("doc_start", ctypes.c_void_p)]
 
 
 class PkdError(RuntimeError):
@@ -77,7 +88,20 @@ def load_library(path: str = LIB_PATH):
     lib.pkd_segmented_attention_paged.argtypes = [P, I, P, I64, P, I64, P, P, P, I, I, I, I, I, I, I, I, I,
                                                   P, P, P, P]
     lib.pkd_lse_merge.argtypes = [P, P, P, P, I, I, I, I, P, I, P, P]
-    for name in ("pkd_workspace_init", "pkd_workspace_check", "pkd_paged_decode", "pkd_paged_decode_static",
+    O = ctypes.POINTER(ScoreOptions)
+    lib.pkd_rope_cache_write.argtypes = [P, I64, P, I64, P, I64, I, P, P, I64, I, I, P, I64, I, I, I, I, I64, P, I, F,
+                                         F, P, I64, I, F, P]
+    lib.pkd_paged_attention_workspace_size.argtypes = [I, I64, I, I, I, I, I, I, I, O]
+    lib.pkd_paged_attention_workspace_size.restype = SZ
+    lib.pkd_paged_attention_kernel_name.argtypes = [I, I64, I, I, I, I, I, I, I, O]
+    lib.pkd_paged_attention_kernel_name.restype = ctypes.c_char_p
+    lib.pkd_paged_attention.argtypes = [P, I, I64, P, I, I64, P, I64, P, P, I, I64, I, I, I, I, I, I, F, F, F, F, O, P,
+                                        I, P, P, SZ, U, P]
+    lib.pkd_prefix_decode_workspace_size.argtypes = [I, I, I, I, I, I, I, I, I, I]
+    lib.pkd_prefix_decode_workspace_size.restype = SZ
+    lib.pkd_prefix_decode.argtypes = [P, I, P, I, I64, P, I64, P, P, I, I, P, I64, P, I, I, I, I, I, I, I, F, F, F, F,
+                                      F, P, I, P, P, SZ, U, P]
+    for name in ("pkd_rope_cache_write", "pkd_paged_attention", "pkd_prefix_decode", "pkd_workspace_init", "pkd_workspace_check", "pkd_paged_decode", "pkd_paged_decode_static",
                  "pkd_paged_decode_static_check", "pkd_cache_write", "pkd_segmented_attention", "pkd_segmented_attention_paged", "pkd_lse_merge"):
         getattr(lib, name).restype = I
     _lib = lib
@@ -318,3 +342,248 @@ def cache_write(key, value, slot_mapping, kv_cache, k_scale=1.0, v_scale=1.0, st
                                _ptr(slot_mapping), T, Hkv, D, P, num_pages, _ptr(kv_cache), dtype_code(kv_cache.dtype),
                                float(k_scale), float(v_scale), _stream(stream)))
     return kv_cache
+
+
+def _one_device(*tensors):
+    """The CUDA device that all the given tensors (name, tensor or None) live on."""
+    device = None
+    for name, t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{name} is on {t.device}, other arguments on {device}")
+    return device
+
+
+def _stream_on(device, stream):
+    """The raw stream of a call on `device`: the given one, or the device's current stream."""
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if s.device != device:
+        raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
+    return s
+
+
+def _token_rows(t, name):
+    """Token stride of t [T, heads, D], whose tokens must be contiguous rows of heads * D."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] with contiguous rows per token")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+
+_call_ws: dict = {}
+
+
+def _call_workspace(nbytes, device, stream):
+    """A zeroed workspace for a call on `stream`: one kept per stream (grown as
+    needed), or, while the stream is capturing, one of the graph's own (zeroed
+    by the graph), so that two graphs never share one."""
+    with torch.cuda.stream(stream):
+        if torch.cuda.is_current_stream_capturing():
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            workspace_init(ws, stream)
+            return ws
+        key = (device.index, stream.cuda_stream)
+        ws = _call_ws.get(key)
+        if ws is None or ws.numel() < nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            workspace_init(ws, stream)
+            _call_ws[key] = ws
+        return ws
+
+
+def rope_cache_write(q, key, value, positions, cos_sin, slot_mapping, kv_cache, *, interleaved=False, q_out=None,
+                     q_out_dtype=None, q_scale=1.0, k_scale=1.0, v_scale=1.0, stream=None):
+    """Rotate q and key by position and append key and value to the paged cache.
+
+    q [T, Hq, D] (or None), key, value [T, Hkv, D] (bf16/fp16; rows of a token
+    contiguous, any token stride); positions, slot_mapping int64 [T]; cos_sin
+    fp32 [max_position, rotary_dim]; kv_cache [num_pages, Hkv, P, 2D] (the input
+    type, or uint8 / float8_e4m3fn).  Returns the rotated q (q_out, allocated
+    when not given; of type q_out_dtype: q's, or e4m3(q / q_scale)).
+    """
+    lib = load_library()
+    device = _one_device(("key", key), ("q", q), ("value", value), ("positions", positions), ("cos_sin", cos_sin),
+                         ("slot_mapping", slot_mapping), ("kv_cache", kv_cache), ("q_out", q_out))
+    ks, vs = _token_rows(key, "key"), _token_rows(value, "value")
+    T, Hkv, D = key.shape
+    num_pages, _, P, _ = kv_cache.shape
+    if value.shape != key.shape or value.dtype != key.dtype:
+        raise ValueError("value must have key's shape and dtype")
+    if kv_cache.shape[1] != Hkv or kv_cache.shape[3] != 2 * D or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache must be contiguous [num_pages, num_kv_heads, page_size, 2 * head_dim]")
+    if positions.dtype != torch.int64 or slot_mapping.dtype != torch.int64 or cos_sin.dtype != torch.float32:
+        raise TypeError("positions and slot_mapping must be int64, cos_sin float32")
+    if positions.shape != (T,) or slot_mapping.shape != (T,) or not (
+            positions.is_contiguous() and slot_mapping.is_contiguous() and cos_sin.is_contiguous()):
+        raise ValueError("positions and slot_mapping must be contiguous [T], cos_sin contiguous")
+    Hq = qs = qos = 0
+    in_dt = q_dt = dtype_code(key.dtype)
+    with torch.cuda.device(device):
+        s = _stream_on(device, stream)
+        if q is not None:
+            qs, Hq = _token_rows(q, "q"), q.shape[1]
+            if q.dtype != key.dtype or q.shape[0] != T or q.shape[2] != D:
+                raise ValueError("q must be [T, num_heads, head_dim] of key's dtype")
+            if q_out is None:
+                with torch.cuda.stream(s):
+                    q_out = torch.empty((T, Hq, D), dtype=q_out_dtype or q.dtype, device=device)
+            elif q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+            qos, q_dt = _token_rows(q_out, "q_out"), dtype_code(q_out.dtype)
+        _check(lib.pkd_rope_cache_write(
+            _ptr(q), qs, key.data_ptr(), ks, value.data_ptr(), vs, in_dt, positions.data_ptr(), cos_sin.data_ptr(),
+            cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0, slot_mapping.data_ptr(), T, Hq, Hkv, D, P,
+            num_pages, kv_cache.data_ptr(), dtype_code(kv_cache.dtype), k_scale, v_scale, _ptr(q_out), qos, q_dt,
+            q_scale, s.cuda_stream))
+    return q_out
+
+
+def _options(device, T, Hq, B, window, softcap, alibi_slopes, prefix_lens, doc_start):
+    for name, t, dtype, n in (("alibi_slopes", alibi_slopes, torch.float32, Hq),
+                              ("prefix_lens", prefix_lens, torch.int32, B), ("doc_start", doc_start, torch.int32, T)):
+        if t is not None and (t.dtype != dtype or t.shape != (n,) or not t.is_contiguous() or t.device != device):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} on {device}")
+    return ScoreOptions(softcap, alibi_slopes.data_ptr() if alibi_slopes is not None else None, window,
+                        prefix_lens.data_ptr() if prefix_lens is not None else None,
+                        doc_start.data_ptr() if doc_start is not None else None)
+
+
+def _check_paged(q, kv_cache, block_table, seq_lens, what="block_table"):
+    D = q.shape[-1]
+    if kv_cache.dim() != 4 or kv_cache.shape[3] != 2 * D or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache must be contiguous [num_pages, num_kv_heads, page_size, 2 * head_dim]")
+    if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        raise TypeError(f"{what} and its lengths must be int32")
+    if block_table.dim() != 2 or (block_table.stride(1) != 1 and block_table.shape[1] > 1) or \
+            seq_lens.shape != (block_table.shape[0],) or not seq_lens.is_contiguous():
+        raise ValueError(f"{what} must be [batch, columns] with contiguous rows, its lengths contiguous [batch]")
+    return block_table.stride(0) if block_table.shape[0] > 1 else max(block_table.stride(0), block_table.shape[1])
+
+
+def paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, *, causal=True, window=0, softcap=0.0,
+                    alibi_slopes=None, prefix_lens=None, doc_start=None, max_query_len=None, max_kv_len=None,
+                    q_scale=1.0, k_scale=1.0, v_scale=1.0, out=None, lse=None, out_dtype=None, workspace=None,
+                    stream=None):
+    """Attention of ragged query tokens over the paged cache (prompts, chunks, steps).
+
+    q [T, Hq, D] (the cache's type; any token stride); request b's tokens are
+    rows query_start[b] : query_start[b + 1] (int32 [B + 1]), the last of its
+    seq_lens[b] keys.  softcap: c * tanh(s / c); alibi_slopes fp32 [Hq]: minus
+    slope * distance; window: keys from position - (window - 1) on; prefix_lens
+    int32 [B]: keys that all of a request's tokens see; doc_start int32 [T]:
+    first key of each token's document.  max_query_len (default T) and
+    max_kv_len (default the table's capacity) bound the lengths on the host.
+    Returns (out [T, Hq, D], lse fp32 [T, Hq]).
+    """
+    lib = load_library()
+    device = _one_device(("q", q), ("kv_cache", kv_cache), ("block_table", block_table), ("seq_lens", seq_lens),
+                         ("query_start", query_start), ("out", out), ("lse", lse), ("workspace", workspace))
+    qs = _token_rows(q, "q")
+    stride = _check_paged(q, kv_cache, block_table, seq_lens)
+    T, Hq, D = q.shape
+    num_pages, Hkv, P, _ = kv_cache.shape
+    B = block_table.shape[0]
+    if query_start.dtype != torch.int32 or query_start.shape != (B + 1,) or not query_start.is_contiguous():
+        raise ValueError("query_start must be a contiguous int32 tensor [batch + 1]")
+    opt = _options(device, T, Hq, B, int(window), float(softcap), alibi_slopes, prefix_lens, doc_start)
+    if max_query_len is None:
+        max_query_len = max(T, 1)
+    if max_kv_len is None:
+        max_kv_len = block_table.shape[1] * P
+    kv_dt = dtype_code(kv_cache.dtype)
+    with torch.cuda.device(device):
+        s = _stream_on(device, stream)
+        with torch.cuda.stream(s):
+            if out is None:
+                out = torch.empty((T, Hq, D), dtype=out_dtype or (torch.bfloat16 if kv_dt == FP8_E4M3 else q.dtype),
+                                  device=device)
+            if lse is None:
+                lse = torch.empty((T, Hq), dtype=torch.float32, device=device)
+        _check_out(out, lse, (T, Hq, D))
+        need = lib.pkd_paged_attention_workspace_size(B, T, max_query_len, Hq, Hkv, D, P, max_kv_len, kv_dt, opt)
+        if need == 0:
+            raise PkdError(EUNSUPPORTED, lib.pkd_last_error().decode())
+        if workspace is None:
+            workspace = _call_workspace(need, device, s)
+        _check(lib.pkd_paged_attention(
+            q.data_ptr(), dtype_code(q.dtype), qs, kv_cache.data_ptr(), kv_dt, num_pages, block_table.data_ptr(),
+            stride, seq_lens.data_ptr(), query_start.data_ptr(), B, T, max_query_len, Hq, Hkv, D, P, max_kv_len,
+            scale, q_scale, k_scale, v_scale, opt, out.data_ptr(), dtype_code(out.dtype), lse.data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), FLAG_CAUSAL if causal else 0,
+            s.cuda_stream))
+    return out, lse
+
+
+def _check_out(out, lse, shape):
+    if out.shape != shape or not out.is_contiguous() or lse.shape != shape[:-1] or not lse.is_contiguous() or \
+            lse.dtype != torch.float32:
+        raise ValueError(f"out must be contiguous {tuple(shape)}, lse contiguous float32 {tuple(shape[:-1])}")
+
+
+def prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, scale, *, group_start=None,
+                  causal=False, softcap=0.0, max_prefix_len=None, max_kv_len=None, q_scale=1.0, k_scale=1.0,
+                  v_scale=1.0, out=None, lse=None, out_dtype=None, workspace=None, stream=None):
+    """Decode of a batch whose requests share prefixes, each computed once.
+
+    q [B, sq, Hq, D]; prefix_table int32 [groups, columns] and prefix_lens int32
+    [groups]: the shared prefixes' pages; group_start int32 [groups + 1]: requests
+    group_start[g] : group_start[g + 1] follow prefix g (default: one group of
+    all); block_table, seq_lens: the requests' own keys behind the prefix.
+    Returns (out [B, sq, Hq, D], lse fp32 [B, sq, Hq]) over both.
+    """
+    lib = load_library()
+    device = _one_device(("q", q), ("kv_cache", kv_cache), ("prefix_table", prefix_table),
+                         ("prefix_lens", prefix_lens), ("block_table", block_table), ("seq_lens", seq_lens),
+                         ("group_start", group_start), ("out", out), ("lse", lse), ("workspace", workspace))
+    if q.dim() != 4 or not q.is_contiguous():
+        raise ValueError("q must be contiguous [batch, sq, num_heads, head_dim]")
+    stride = _check_paged(q, kv_cache, block_table, seq_lens)
+    pstride = _check_paged(q, kv_cache, prefix_table, prefix_lens, "prefix_table")
+    B, sq, Hq, D = q.shape
+    num_pages, Hkv, P, _ = kv_cache.shape
+    groups = prefix_table.shape[0]
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must have one row per request")
+    if max_prefix_len is None:
+        max_prefix_len = prefix_table.shape[1] * P
+    if max_kv_len is None:
+        max_kv_len = block_table.shape[1] * P
+    kv_dt = dtype_code(kv_cache.dtype)
+    with torch.cuda.device(device):
+        s = _stream_on(device, stream)
+        with torch.cuda.stream(s):
+            if group_start is None:
+                if groups != 1:
+                    raise ValueError("group_start is needed with more than one prefix")
+                group_start = _whole_batch(B, device)
+            elif group_start.dtype != torch.int32 or group_start.shape != (groups + 1,) or \
+                    not group_start.is_contiguous():
+                raise ValueError("group_start must be a contiguous int32 tensor [groups + 1]")
+            if out is None:
+                out = torch.empty((B, sq, Hq, D), dtype=out_dtype or (
+                    torch.bfloat16 if kv_dt == FP8_E4M3 else q.dtype), device=device)
+            if lse is None:
+                lse = torch.empty((B, sq, Hq), dtype=torch.float32, device=device)
+        _check_out(out, lse, (B, sq, Hq, D))
+        need = lib.pkd_prefix_decode_workspace_size(B, sq, Hq, Hkv, D, P, groups, max_prefix_len, max_kv_len, kv_dt)
+        if need == 0:
+            raise PkdError(EUNSUPPORTED, lib.pkd_last_error().decode())
+        if workspace is None:
+            workspace = _call_workspace(need, device, s)
+        _check(lib.pkd_prefix_decode(
+            q.data_ptr(), dtype_code(q.dtype), kv_cache.data_ptr(), kv_dt, num_pages, prefix_table.data_ptr(),
+            pstride, prefix_lens.data_ptr(), group_start.data_ptr(), groups, max_prefix_len, block_table.data_ptr(),
+            stride, seq_lens.data_ptr(), B, sq, Hq, Hkv, D, P, max_kv_len, scale, q_scale, k_scale, v_scale, softcap,
+            out.data_ptr(), dtype_code(out.dtype), lse.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), FLAG_CAUSAL if causal else 0, s.cuda_stream))
+    return out, lse
+
+
+def _whole_batch(B, device):
+    """group_start of a single group: {0, B}, made on the device."""
+    return torch.arange(0, 2 * B, max(B, 1), dtype=torch.int32, device=device) if B else \
+        torch.zeros(2, dtype=torch.int32, device=device)

@@ -11,6 +11,7 @@
 #include <string>
 
 #include "../../include/pkd.h"
+#include "attend_launch.h"
 #include "decode_common.cuh"
 #include "decode_tc05.cuh"
 #include "launch.h"
@@ -278,8 +279,9 @@ pkd_status get_map(CUtensorMap& out, const void* base, int rank, uint64_t d0, ui
 // Boxes of the stage map: a whole 16-key stage (every chunk), or the tcgen05
 // kernel's stage: a 4-D view {chunk elements, 8 rows, chunk, 8-row group}
 // whose box {all, 8, all, 2} lands a 16-key stage as two 8-row groups, each
-// holding every chunk of its rows.
-enum StageBox { kStageFull = 0, kStageTcGroup = 2 };
+// holding every chunk of its rows; kStageTcHalf: the same with the K (or V)
+// chunks of the rows only.
+enum StageBox { kStageFull = 0, kStageTcGroup = 2, kStageTcHalf = 3 };
 
 pkd_status get_stage_map(CUtensorMap& out, const void* cache, uint64_t rows, int row_bytes, pkd_dtype dt,
                          StageBox mode = kStageFull) {
@@ -287,7 +289,7 @@ pkd_status get_stage_map(CUtensorMap& out, const void* cache, uint64_t rows, int
     MapKey k;
     std::memset(&k, 0, sizeof k);
     k.base = cache; k.d0 = 128 / elt; k.d1 = rows; k.d2 = row_bytes / 128; k.s1 = row_bytes; k.s2 = 128;
-    k.rank = mode == kStageTcGroup ? 140 : 103; k.dtype = dt;
+    k.rank = mode == kStageTcGroup ? 140 : mode == kStageTcHalf ? 141 : 103; k.dtype = dt;
     MapCache& c = map_cache();
     {
         std::lock_guard<std::mutex> g(c.mu);
@@ -304,11 +306,12 @@ pkd_status get_stage_map(CUtensorMap& out, const void* cache, uint64_t rows, int
                                                    : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     CUtensorMap m;
     CUresult r;
-    if (mode == kStageTcGroup) {
+    if (mode == kStageTcGroup || mode == kStageTcHalf) {
         // rows is a multiple of 16 (page_size is)
         cuuint64_t dims[4] = {k.d0, 8, k.d2, k.d1 / 8};
         cuuint64_t strides[3] = {k.s1, k.s2, 8 * k.s1};
-        cuuint32_t box[4] = {(cuuint32_t)(128 / elt), 8, (cuuint32_t)(row_bytes / 128), 2};
+        const int chunks = row_bytes / 128;
+        cuuint32_t box[4] = {(cuuint32_t)(128 / elt), 8, (cuuint32_t)(mode == kStageTcHalf ? chunks / 2 : chunks), 2};
         cuuint32_t estr[4] = {1, 1, 1, 1};
         r = enc(&m, t, 4, const_cast<void*>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -334,11 +337,13 @@ pkd_status get_stage_map(CUtensorMap& out, const void* cache, uint64_t rows, int
 // The q rows of one (request, kv head) as a TMA box: q [tokens, Hq, D] viewed
 // as {D, Hq, tokens}, box {64 dims, G heads, sq tokens}, 128-byte swizzle, so
 // that one copy lands 64 dims of rows r = i*G + g at 128 bytes per row.
-pkd_status get_q_map(CUtensorMap& out, const void* q, int D, int Hq, uint64_t tokens, int G, int sq, pkd_dtype dt) {
+pkd_status get_q_map(CUtensorMap& out, const void* q, int D, int Hq, uint64_t tokens, int G, int sq, pkd_dtype dt,
+                     int64_t token_stride = 0) {
+    if (token_stride == 0) token_stride = (int64_t)Hq * D;
     MapKey k;
     std::memset(&k, 0, sizeof k);
     k.base = q; k.d0 = (uint64_t)D; k.d1 = (uint64_t)Hq; k.d2 = tokens; k.s1 = (uint64_t)D * 2;
-    k.s2 = (uint64_t)Hq * D * 2; k.rank = 1000 + G * 64 + sq; k.dtype = dt;
+    k.s2 = (uint64_t)token_stride * 2; k.rank = 1000 + G * 256 + sq; k.dtype = dt;
     MapCache& c = map_cache();
     {
         std::lock_guard<std::mutex> g(c.mu);
@@ -370,6 +375,19 @@ pkd_status get_q_map(CUtensorMap& out, const void* q, int D, int Hq, uint64_t to
 }
 
 }  // namespace
+
+pkd_status pkd::stage_map(CUtensorMap& out, const void* cache, uint64_t rows, int row_bytes, pkd_dtype dt) {
+    return get_stage_map(out, cache, rows, row_bytes, dt);
+}
+
+pkd_status pkd::half_stage_map(CUtensorMap& out, const void* cache, uint64_t rows, int row_bytes, pkd_dtype dt) {
+    return get_stage_map(out, cache, rows, row_bytes, dt, kStageTcHalf);
+}
+
+pkd_status pkd::query_map(CUtensorMap& out, const void* q, int D, int Hq, uint64_t tokens, int64_t token_stride, int G,
+                          int box_tokens, pkd_dtype dt) {
+    return get_q_map(out, q, D, Hq, tokens, G, box_tokens, dt, token_stride);
+}
 
 int pkd::report_status(int st, const char* fmt, ...) {
     char buf[512];

@@ -1,0 +1,746 @@
+// Ragged paged attention on the 5th-generation tensor cores: query blocks of
+// any length against the paged cache, accumulators in tensor memory (TMEM).
+//
+// The query rows of one (request, kv head) are its tokens times the heads of the
+// kv head, packed token-major: row i * G + g.  A work item is two tiles of up
+// to 128 rows (TOK = 128 / G whole tokens each) against a range of keys, walked
+// in tiles of 128 keys.  Per key tile and row tile:
+//   S = Q K^T     tcgen05.mma, M = 128 rows, N = 128 keys: both operands in
+//                 shared memory, K-major, 128-byte swizzle, as TMA lands them
+//   softmax       one row per thread (TMEM lane = row): no shuffles.  The
+//                 reference maximum moves only when a row's maximum grows by more
+//                 than 2^8 (O and l are then rescaled by the row's own warp)
+//   O += P V      P in TMEM over the spent S (A operand from tensor memory),
+//                 V in shared memory read MN-major
+// Two row tiles share every K/V tile, and while the softmax of one runs, the
+// tensor cores work on the other's products: a key tile of both costs
+// 2 x (S + O) = 4 products of 128x128xD against one softmax pass per tile.
+//
+// Warp roles (512 threads): warps 0-3 and 4-7 the softmax of tile 0 and 1, warps
+// 8-11 the epilogue (O out of TMEM, normalised, written -- or a partial result
+// when the keys are split), warp 12 loads (work items, Q, K, V by TMA), warp 13
+// issues the products.  Registers follow the roles (setmaxnreg).
+// Work items are handed out by an atomic counter in the workspace, the longest of
+// a request first, so CTAs finish together whatever the lengths; results do not
+// depend on who computes an item.  Every wait is bounded.
+#pragma once
+
+#include "attend.cuh"
+#include "tc05.cuh"
+
+namespace pkd {
+
+constexpr int kPtKeys = 128;       // keys per tile
+constexpr int kPtRows = 128;       // rows per tile (TMEM lanes)
+constexpr int kPtThreads = 512;
+constexpr int kPtItems = 4;        // work-item ring
+constexpr int kPtMaxBatch = 4096;  // requests whose tile prefix the CTA keeps in shared memory
+constexpr float kPtRescale = 8.f;  // log2 units: P stays below 2^8 between rescales
+
+struct PtItem {
+    int b, hk, q0, n, L, prefix;   // request, kv head, first query token, query tokens, length, prefix keys
+    int tok0;                      // first token (of the request) of the item's rows
+    int t0, t1, ntiles;            // keys of this item, tiles of 128 from t0
+    int lo_all, hi_all;            // keys outside are seen by no row of the unit
+    int split, nsplit, unit;
+    int jb[2], je[2];              // key tiles [jb, je) of row tile t (empty: none)
+    int bad, end;                  // bad: some page lies outside the pool
+    int pad[2];
+};
+
+// NU K/V units; K and V of a key tile are one unit each
+template <int D>
+struct PtShape {
+    static constexpr int ROWB = D * 2;
+    static constexpr int GROUP = 8 * ROWB;               // 8 keys: D / 64 regions of 8 x 128 bytes
+    static constexpr int UNIT = kPtKeys / 8 * GROUP;     // 32 KB at D = 128
+    static constexpr int NU = D == 128 ? 4 : 8;
+    static constexpr int QTILE = kPtRows * ROWB;
+    static constexpr int OFF_KV = 0;
+    static constexpr int OFF_Q = NU * UNIT;
+    static constexpr int OFF_STAT = OFF_Q + 2 * QTILE;   // float [2 tiles][m, l][128]
+    static constexpr int OFF_ITEM = OFF_STAT + 2 * 2 * kPtRows * 4;
+    static constexpr int OFF_PREF = OFF_ITEM + kPtItems * static_cast<int>(sizeof(PtItem));
+    static constexpr int OFF_SCAN = OFF_PREF + (kPtMaxBatch + 4) * 4;  // 16 warp sums, an arrival flag
+    static constexpr int OFF_BAR = (OFF_SCAN + 128 + 7) & ~7;
+    // units full/empty, Q full/empty, S full, P full, O step done, O full/drained, stats full/free, item full/empty, drain
+    static constexpr int B_UF = 0, B_UE = B_UF + NU, B_QF = B_UE + NU, B_QE = B_QF + 1, B_SF = B_QE + 1;
+    static constexpr int B_PF = B_SF + 2, B_OD = B_PF + 2, B_OF = B_OD + 2, B_OE = B_OF + 2, B_XF = B_OE + 2;
+    static constexpr int B_XE = B_XF + 2, B_IF = B_XE + 2, B_IE = B_IF + kPtItems, B_DR = B_IE + kPtItems;
+    static constexpr int NBAR = B_DR + 1;
+    static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
+    static constexpr int SMEM = OFF_TMEM + 16 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
+    static_assert(SMEM > 114 * 1024, "one CTA per SM: all 512 TMEM columns are its own");
+};
+
+__device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, const AttendParams& p) {
+    return __all_sync(kFull, mbar_wait(bar, parity, p.status));
+}
+
+// a*b + c on two floats at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Merge the partial results of one row by LSE (log2 units): a warp per row,
+// lane l holds dims l * D/32 ...; parts s at part_lse[s * lse_step] and
+// part_out[s * lse_step * D].  Partials come from other CTAs: L2 loads.
+template <int D>
+__device__ __forceinline__ void pt_merge_row(const float* pl, const float* po, long long step, int np, int lane,
+                                             float (&acc)[D / 32], float& mx, float& ws) {
+    constexpr int E = D / 32;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    mx = -INFINITY;
+    ws = 0.f;
+    for (int s = lane; s < np; s += 32) mx = fmaxf(mx, __ldcg(pl + s * step));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    if (mx == -INFINITY) return;
+    for (int s0 = 0; s0 < np; s0 += 32) {
+        const float l = s0 + lane < np ? __ldcg(pl + (s0 + lane) * step) : -INFINITY;
+        const float wl = l == -INFINITY ? 0.f : fast_exp2(l - mx);
+        ws += wl;
+        const int m = min(32, np - s0);
+#pragma unroll 4
+        for (int j = 0; j < m; ++j) {
+            const float w = __shfl_sync(kFull, wl, j);
+            if (w == 0.f) continue;  // an empty part is never read
+            const float* src = po + (s0 + j) * step * D + lane * E;
+            if constexpr (E == 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+                acc[0] = fmaf(w, v.x, acc[0]);
+                acc[1] = fmaf(w, v.y, acc[1]);
+                acc[2] = fmaf(w, v.z, acc[2]);
+                acc[3] = fmaf(w, v.w, acc[3]);
+            } else {
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+                acc[0] = fmaf(w, v.x, acc[0]);
+                acc[1] = fmaf(w, v.y, acc[1]);
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(kFull, ws, o);
+}
+
+// kPartials: every result is left as a partial one (for a merge that follows)
+template <int D, bool kBF16, bool kCap, bool kBias>
+__global__ void __launch_bounds__(kPtThreads, 1)
+attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
+                     const AttendParams p, const int partials) {
+    using S = PtShape<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb0 = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);
+    PtItem* items = reinterpret_cast<PtItem*>(smem + S::OFF_ITEM);
+    float* stats = reinterpret_cast<float*>(smem + S::OFF_STAT);
+    int* pref = reinterpret_cast<int*>(smem + S::OFF_PREF);
+    int* scan = reinterpret_cast<int*>(smem + S::OFF_SCAN);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + S::OFF_TMEM);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = p.G, TOK = kPtRows / G;  // whole tokens per row tile
+    auto bar = [&](int i) { return smem_u32(bars + i); };
+
+    // ------------------------------------------------------------ set-up
+    if (tid == 0) {
+        for (int i = 0; i < S::NU; ++i) {
+            mbar_init(bar(S::B_UF + i), 1);
+            mbar_init(bar(S::B_UE + i), 1);
+        }
+        mbar_init(bar(S::B_QF), 1);
+        mbar_init(bar(S::B_QE), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(S::B_SF + i), 1);
+            mbar_init(bar(S::B_PF + i), 4);
+            mbar_init(bar(S::B_OD + i), 1);
+            mbar_init(bar(S::B_OF + i), 1);
+            mbar_init(bar(S::B_OE + i), 4);
+            mbar_init(bar(S::B_XF + i), 4);
+            mbar_init(bar(S::B_XE + i), 4);
+        }
+        for (int i = 0; i < kPtItems; ++i) {
+            mbar_init(bar(S::B_IF + i), 1);
+            mbar_init(bar(S::B_IE + i), 1 + 8 + 4);  // the issuing thread, softmax and epilogue warps
+        }
+        mbar_init(bar(S::B_DR), 1);
+        fence_barrier_init();
+    }
+    if (warp == 13) {
+        tc05::alloc(smem_u32(tslot), 512);  // S/P: columns 0-255, O: 256 + D * tile
+        tc05::relinquish_alloc_permit();
+    }
+    // prefix of the requests' row-tile pairs (units of one kv head)
+    {
+        int run = 0;
+        for (int b0 = 0; b0 < p.B; b0 += kPtThreads) {
+            const int b = b0 + tid;
+            int v = 0;
+            if (b < p.B) {
+                int q0, n;
+                request_tokens(p, b, q0, n, blockIdx.x == 0);
+                v = (n + 2 * TOK - 1) / (2 * TOK);
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, v, o);
+                if (lane >= o) v += y;
+            }
+            if (lane == 31) scan[warp] = v;
+            __syncthreads();
+            int before = run;
+            for (int k = 0; k < kPtThreads / 32; ++k) {
+                const int s = scan[k];
+                if (k < warp) before += s;
+                run += s;
+            }
+            if (b < p.B) pref[b + 1] = before + v;
+            __syncthreads();
+        }
+        if (tid == 0) pref[0] = 0;
+    }
+    tc05::fence_before_sync();
+    __syncthreads();
+    tc05::fence_after_sync();
+    const uint32_t tmem = *tslot;
+    constexpr uint32_t kIdS = tc05::idesc_f16(kBF16, kPtRows, kPtKeys, false, false);  // S = Q K^T
+    constexpr uint32_t kIdO = tc05::idesc_f16(kBF16, kPtRows, D, false, true);         // O += P V
+
+    if (warp >= 12) {
+        reg_dec<72>();
+        if (warp == 12) {
+            // ------------------------------------------------------ loads
+            if (lane == 0) {
+                prefetch_tmap(&kvmap);
+                prefetch_tmap(&qmap);
+            }
+            const uint64_t pol = policy_evict_first();
+            uint64_t keep;
+            asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+            const int total = pref[p.B] * p.Hkv * p.max_splits;
+            int idx = blockIdx.x;
+            int u = 0, nq = 0, it = 0;
+            bool ok = true;
+            for (;;) {
+                // the next index is drawn while this item loads
+                int next = 0;
+                if (lane == 0) next = static_cast<int>(gridDim.x) + atomicAdd(p.queue, 1);
+                if (idx >= total) {
+                    const int slot = it % kPtItems;
+                    if (it >= kPtItems && !pt_wait(bar(S::B_IE + slot), ((it / kPtItems) - 1) & 1, p)) ok = false;
+                    if (lane == 0) {
+                        items[slot].end = 1;
+                        mbar_arrive(bar(S::B_IF + slot));
+                    }
+                    __syncwarp();
+                    break;
+                }
+                // item idx: splits innermost, then the row tiles of a (request, kv
+                // head) from the last (the longest, causal) to the first
+                const int split = idx % p.max_splits, r1 = idx / p.max_splits;
+                int lo_b = 0, hi_b = p.B;
+                while (hi_b - lo_b > 1) {
+                    const int mid = (lo_b + hi_b) >> 1;
+                    if (static_cast<long long>(pref[mid]) * p.Hkv <= r1) lo_b = mid; else hi_b = mid;
+                }
+                const int b = lo_b, npair = pref[b + 1] - pref[b], r2 = r1 - pref[b] * p.Hkv;
+                const int hk = r2 / npair, pair = npair - 1 - (r2 - hk * npair);
+                int q0, n;
+                request_tokens(p, b, q0, n, false);
+                const int L = request_len(p, b, pair == 0 && hk == 0 && split == 0 && lane == 0);
+                const int prefix = p.prefix_lens ? p.prefix_lens[b] : 0;
+                const int tok0 = pair * 2 * TOK;
+                int lo[2], hi[2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int a0 = tok0 + t * TOK, a1 = min(a0 + TOK, n);
+                    int l = 0x7fffffff, h = 0;
+                    for (int i = a0 + lane; i < a1; i += 32) {
+                        int x, y;
+                        token_keys(p, q0, n, L, prefix, i, x, y);
+                        if (x < y) {
+                            l = min(l, x);
+                            h = max(h, y);
+                        }
+                    }
+                    lo[t] = __reduce_min_sync(kFull, l);
+                    hi[t] = __reduce_max_sync(kFull, h);
+                }
+                const int lo_all = min(lo[0], lo[1]), hi_all = max(hi[0], hi[1]);
+                const int begin = lo_all & ~(kStageTok - 1);  // 16-key stages never cross a page
+                int nsplit = hi_all > 0 ? (hi_all - begin + p.chunk - 1) / p.chunk : 0;
+                if (nsplit > p.max_splits) {
+                    if (lane == 0) atomicOr(p.status, kErrBounds);
+                    nsplit = p.max_splits;
+                }
+                if (split >= max(nsplit, 1)) {  // nothing here
+                    idx = __shfl_sync(kFull, next, 0);
+                    continue;
+                }
+                const int t0 = nsplit ? begin + split * p.chunk : 0;
+                const int t1 = nsplit ? min(t0 + p.chunk, hi_all) : 0;
+                const int ntiles = (t1 - t0 + kPtKeys - 1) / kPtKeys;
+                // a page outside the pool anywhere in the item: the softmax checks its keys
+                const int32_t* row = p.block_table + static_cast<long long>(b) * p.bt_stride;
+                int bad = 0;
+                if (ntiles) {
+                    const int c1 = page_div(t1 - 1, p.pmagic, p.pmshift);
+                    for (int c = page_div(t0, p.pmagic, p.pmshift) + lane; c <= c1; c += 32)
+                        bad |= row[c] < 0 || row[c] >= p.num_pages;
+                    bad = __any_sync(kFull, bad);
+                    if (bad && lane == 0) atomicOr(p.status, kErrBounds);
+                }
+                const int slot = it % kPtItems;
+                if (it >= kPtItems && !pt_wait(bar(S::B_IE + slot), ((it / kPtItems) - 1) & 1, p)) { ok = false; break; }
+                if (lane == 0) {
+                    PtItem& I = items[slot];
+                    I.b = b; I.hk = hk; I.q0 = q0; I.n = n; I.L = L; I.prefix = prefix; I.tok0 = tok0;
+                    I.t0 = t0; I.t1 = t1; I.ntiles = ntiles; I.lo_all = lo_all; I.hi_all = hi_all;
+                    I.split = split; I.nsplit = nsplit; I.unit = (pref[b] + pair) * p.Hkv + hk;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int a = max(lo[t], t0), z = min(hi[t], t1);
+                        I.jb[t] = a < z ? (a - t0) / kPtKeys : 0;
+                        I.je[t] = a < z ? (z - t0 + kPtKeys - 1) / kPtKeys : 0;
+                    }
+                    I.bad = bad; I.end = 0;
+                    mbar_arrive(bar(S::B_IF + slot));
+                }
+                __syncwarp();
+                ++it;
+                if (ntiles) {
+                    // Q of the item's tiles (64-dim regions), once the last item's products have read theirs
+                    if (nq >= 1 && !pt_wait(bar(S::B_QE), (nq - 1) & 1, p)) { ok = false; break; }
+                    const int tiles = tok0 + TOK < n ? 2 : 1;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar(S::B_QF), tiles * (D / 64) * TOK * G * 128);
+                        for (int t = 0; t < tiles; ++t)
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_load_3d(sb0 + S::OFF_Q + t * S::QTILE + h * kPtRows * 128, &qmap, 64 * h, hk * G,
+                                            q0 + tok0 + t * TOK, bar(S::B_QF), pol);
+                    }
+                    __syncwarp();
+                    ++nq;
+                    auto entry = [&](int j) {
+                        const int tok = t0 + j * kPtKeys + lane * kStageTok;
+                        return lane < kPtKeys / kStageTok && tok < t1 ? row[page_div(tok, p.pmagic, p.pmshift)] : -1;
+                    };
+                    int pg = entry(0);
+                    for (int j = 0; j < ntiles && ok; ++j) {
+                        const int pg_next = j + 1 < ntiles ? entry(j + 1) : -1;
+                        const int tok = t0 + j * kPtKeys + lane * kStageTok;
+                        const bool load = pg >= 0 && pg < p.num_pages;
+                        const int bytes = __popc(__ballot_sync(kFull, load)) * 2 * S::GROUP;
+                        const int krow = load ? (pg * p.Hkv + hk) * p.P + (tok - page_div(tok, p.pmagic, p.pmshift) * p.P) : 0;
+#pragma unroll 1
+                        for (int v = 0; v < 2; ++v, ++u) {
+                            const int us = u % S::NU;
+                            if (u >= S::NU && !pt_wait(bar(S::B_UE + us), ((u / S::NU) - 1) & 1, p)) { ok = false; break; }
+                            if (lane == 0) mbar_arrive_expect_tx(bar(S::B_UF + us), bytes);
+                            __syncwarp();
+                            if (load)
+                                tma_load_4d(sb0 + S::OFF_KV + us * S::UNIT + 2 * lane * S::GROUP, &kvmap, 0, 0,
+                                            v * (D / 64), krow >> 3, bar(S::B_UF + us), keep);
+                        }
+                        pg = pg_next;
+                    }
+                    if (!ok) break;
+                }
+                idx = __shfl_sync(kFull, next, 0);
+            }
+            if (!ok) {
+                // let every issued copy land before the CTA leaves
+                if (lane == 0) atomicOr(p.status, kErrTimeout);
+                for (int j = max(0, u - S::NU); j < u; ++j) mbar_wait(bar(S::B_UF + j % S::NU), (j / S::NU) & 1);
+                if (nq) mbar_wait(bar(S::B_QF), (nq - 1) & 1);
+            }
+        } else if (warp == 13) {
+            // --------------------------------------------------- products
+            if (lane == 0) {
+                bool ok = true;
+                int u = 0, nq = 0;
+                int np[2] = {0, 0}, no[2] = {0, 0};  // P tiles consumed, accumulations begun
+                for (int it = 0; ok; ++it) {
+                    const int slot = it % kPtItems;
+                    if (!mbar_wait(bar(S::B_IF + slot), (it / kPtItems) & 1, p.status)) { ok = false; break; }
+                    const PtItem& I = items[slot];
+                    if (I.end) break;
+                    const int ntiles = I.ntiles;
+                    const int jb[2] = {I.jb[0], I.jb[1]}, je[2] = {I.je[0], I.je[1]};
+                    mbar_arrive(bar(S::B_IE + slot));
+                    if (!ntiles) continue;
+                    if (!mbar_wait(bar(S::B_QF), nq & 1, p.status)) { ok = false; break; }
+                    ++nq;
+                    auto k_ready = [&](int j) {
+                        const int x = u + 2 * j;
+                        return mbar_wait(bar(S::B_UF + x % S::NU), (x / S::NU) & 1, p.status);
+                    };
+                    auto qk = [&](int t, int j) {
+                        const uint32_t k = sb0 + S::OFF_KV + ((u + 2 * j) % S::NU) * S::UNIT;
+                        const uint32_t q = sb0 + S::OFF_Q + t * S::QTILE;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc05::mma_f16(tmem + kPtKeys * t,
+                                          tc05::smem_desc(q + (kk >> 2) * kPtRows * 128 + (kk & 3) * 32, 16, 1024),
+                                          tc05::smem_desc(k + (kk >> 2) * 1024 + (kk & 3) * 32, 16, S::GROUP), kIdS,
+                                          kk > 0);
+                        tc05::commit(bar(S::B_SF + t));
+                    };
+                    ok = k_ready(0);
+                    tc05::fence_after_sync();
+                    for (int t = 0; ok && t < 2; ++t)
+                        if (jb[t] == 0 && je[t] > 0) qk(t, 0);
+                    tc05::commit(bar(S::B_UE + u % S::NU));
+                    for (int j = 0; ok && j < ntiles; ++j) {
+                        const int vu = u + 2 * j + 1;
+                        ok = mbar_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p.status);
+                        bool have_k = false;
+                        for (int t = 0; ok && t < 2; ++t) {
+                            if (j >= jb[t] && j < je[t]) {
+                                ok = mbar_wait(bar(S::B_PF + t), np[t] & 1, p.status);
+                                ++np[t];
+                                if (ok && j == jb[t]) {
+                                    // a new accumulation: the epilogue has drained the last one
+                                    if (no[t] >= 1) ok = mbar_wait(bar(S::B_OE + t), (no[t] - 1) & 1, p.status);
+                                    ++no[t];
+                                }
+                                if (!ok) break;
+                                tc05::fence_after_sync();
+                                const uint32_t v = sb0 + S::OFF_KV + (vu % S::NU) * S::UNIT;
+#pragma unroll
+                                for (int kk = 0; kk < kPtKeys / 16; ++kk)
+                                    tc05::mma_f16_ts(tmem + 256 + D * t, tmem + kPtKeys * t + 8 * kk,
+                                                     tc05::smem_desc(v + 2 * kk * S::GROUP, 1024, S::GROUP), kIdO,
+                                                     j > jb[t] || kk > 0);
+                                tc05::commit(bar(S::B_OD + t));
+                                if (j == je[t] - 1) tc05::commit(bar(S::B_OF + t));
+                            }
+                            if (t == 1) tc05::commit(bar(S::B_UE + vu % S::NU));
+                            if (j + 1 < ntiles) {
+                                if (!have_k) {
+                                    ok = k_ready(j + 1);
+                                    have_k = true;
+                                    if (!ok) break;
+                                    tc05::fence_after_sync();
+                                }
+                                // in issue order behind this tile's O product, which has read the P under S
+                                if (j + 1 >= jb[t] && j + 1 < je[t]) qk(t, j + 1);
+                                if (t == 1) tc05::commit(bar(S::B_UE + (u + 2 * (j + 1)) % S::NU));
+                            }
+                        }
+                    }
+                    tc05::commit(bar(S::B_QE));
+                    u += 2 * ntiles;
+                }
+                if (!ok) atomicOr(p.status, kErrTimeout);
+                // every product issued has completed before TMEM is freed
+                tc05::commit(bar(S::B_DR));
+                mbar_wait(bar(S::B_DR), 0);
+            }
+            __syncwarp();
+        }
+    } else if (warp < 8) {
+        // ------------------------------------------------------- softmax
+        reg_inc<176>();
+        const int t = warp >> 2, q4 = warp & 3, r = 32 * q4 + lane;  // row of tile t = TMEM lane
+        const uint32_t lane_addr = static_cast<uint32_t>(32 * q4) << 16;
+        const uint32_t s_addr = tmem + lane_addr + kPtKeys * t, o_addr = tmem + lane_addr + 256 + D * t;
+        const int ri = r / G, rg = r - ri * G;
+        int ns = 0, no = 0, u = 0;  // key tiles, accumulations done by this tile; K/V units before the item
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            const int slot = it % kPtItems;
+            if (!pt_wait(bar(S::B_IF + slot), (it / kPtItems) & 1, p)) { ok = false; break; }
+            const PtItem& I = items[slot];
+            if (I.end) break;
+            const int jb = I.jb[t], je = I.je[t], t0 = I.t0, ntiles = I.ntiles;
+            if (jb < je) {
+                const int tok = I.tok0 + t * TOK + ri;
+                const bool valid = ri < TOK && tok < I.n;
+                const bool warp_on = __any_sync(kFull, valid);
+                int lo = 0, hi = 0x7fffffff;
+                if (valid) token_keys(p, I.q0, I.n, I.L, I.prefix, tok, lo, hi);
+                float slope = 0.f;
+                const int pos = I.L - I.n + tok;
+                if constexpr (kBias)
+                    if (valid) slope = p.slopes[I.hk * G + rg] * kLog2e;
+                const bool lead = t == 0 || !(I.jb[0] < I.je[0]);  // zeroes V rows of tiles that both walk
+                const int jb0 = I.jb[0], je0 = I.je[0], bad = I.bad, lo_all = I.lo_all, hi_all = min(I.hi_all, I.t1);
+                const int32_t* table = p.block_table + static_cast<long long>(I.b) * p.bt_stride;
+                float m_used = -INFINITY, l = 0.f;
+                for (int j = jb; j < je; ++j, ++ns) {
+                    const int tk = t0 + j * kPtKeys;
+                    if (!pt_wait(bar(S::B_SF + t), ns & 1, p)) { ok = false; break; }
+                    unsigned stages = 0xff;  // 16-key stages whose page is in the pool
+                    if (bad) {
+                        stages = 0;
+                        for (int s = 0; s < 8; ++s) {
+                            const int k = tk + 16 * s;
+                            const int pg = k < I.t1 ? table[page_div(k, p.pmagic, p.pmshift)] : -1;
+                            if (pg >= 0 && pg < p.num_pages) stages |= 1u << s;
+                        }
+                    }
+                    if (warp_on) {
+                        tc05::fence_after_sync();
+                        uint32_t sr[4][32];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tc05::ld_32x32b_x32(s_addr + 32 * c, sr[c]);
+                        tc05::wait_ld();
+                        const float scale2 = (kCap || kBias) ? 1.f : p.scale_log2;
+                        if constexpr (kCap || kBias) {
+#pragma unroll
+                            for (int c = 0; c < 128; ++c) {
+                                float x = __uint_as_float(sr[c >> 5][c & 31]);
+                                x = kCap ? capped(x, p.cap_in, p.cap_log2) : x * p.scale_log2;
+                                if constexpr (kBias) x = fmaf(-slope, fabsf(static_cast<float>(pos - tk - c)), x);
+                                sr[c >> 5][c & 31] = __float_as_uint(x);
+                            }
+                        }
+                        const int c0 = lo - tk, c1 = min(hi, hi_all) - tk;
+                        if (__any_sync(kFull, valid && (c0 > 0 || c1 < kPtKeys)) || bad) {
+#pragma unroll
+                            for (int c = 0; c < 128; ++c)
+                                if (c < c0 || c >= c1 || !(stages >> (c >> 4) & 1))
+                                    sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+                        }
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(sr[k][c]));
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
+                        const bool need = top > m_used + kPtRescale;
+                        if (__any_sync(kFull, need)) {
+                            // the rows that need it take the new maximum as reference; O and l follow
+                            const float m_new = need ? top : m_used;
+                            const float alpha = need ? fast_exp2(m_used - m_new) : 1.f;
+                            m_used = m_new;
+                            l *= alpha;
+                            if (j > jb) {
+                                if (!pt_wait(bar(S::B_OD + t), (ns - 1) & 1, p)) { ok = false; break; }
+                                tc05::fence_after_sync();
+#pragma unroll
+                                for (int c = 0; c < D; c += 16) {
+                                    uint32_t o[16];
+                                    tc05::ld_32x32b_x16(o_addr + c, o);
+                                    tc05::wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                    tc05::st_32x32b_x16(o_addr + c, o);
+                                }
+                                tc05::wait_st();
+                            }
+                        }
+                        const float m_sub = m_used == -INFINITY ? 0.f : m_used;
+                        const float2 sc = make_float2(scale2, scale2), ms = make_float2(-m_sub, -m_sub);
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t pk[32];
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                const int k = 64 * h + 2 * c;
+                                float2 x = make_float2(__uint_as_float(sr[k >> 5][k & 31]),
+                                                       __uint_as_float(sr[k >> 5][(k & 31) + 1]));
+                                x = fma2(x, sc, ms);
+                                x.x = fast_exp2(x.x);
+                                x.y = fast_exp2(x.y);
+                                // l sums the fp32 weights; the product takes them rounded to the operand type
+                                sum[c & 1] = add2(sum[c & 1], x);
+                                pk[c] = pack2<kBF16>(x.x, x.y);
+                            }
+                            tc05::st_32x32b_x32(s_addr + 32 * h, pk);
+                        }
+                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                        tc05::wait_st();
+                    }
+                    // V rows that no row of the unit sees (stale slots, skipped pages)
+                    // are zeroed: their weight 0 must not meet a NaN
+                    const bool zeroes = lead || j < jb0 || j >= je0;
+                    if (zeroes && (bad || tk < lo_all || tk + kPtKeys > hi_all)) {
+                        const int vu = u + 2 * j + 1, key = tk + r;
+                        if (!pt_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p)) { ok = false; break; }
+                        if (key < lo_all || key >= hi_all || !(stages >> (r >> 4) & 1)) {
+                            uint8_t* vrow = smem + S::OFF_KV + (vu % S::NU) * S::UNIT + (r >> 3) * S::GROUP + (r & 7) * 128;
+#pragma unroll
+                            for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    *reinterpret_cast<uint4*>(vrow + h * 1024 + ((e + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async();
+                    }
+                    tc05::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(S::B_PF + t));
+                }
+                if (!ok) break;
+                // row statistics for the epilogue
+                if (no >= 1 && !pt_wait(bar(S::B_XE + t), (no - 1) & 1, p)) { ok = false; break; }
+                ++no;
+                stats[(2 * t) * kPtRows + r] = m_used;
+                stats[(2 * t + 1) * kPtRows + r] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S::B_XF + t));
+            }
+            u += 2 * ntiles;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(S::B_IE + slot));
+        }
+        if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
+    } else {
+        // ------------------------------------------------------ epilogue
+        reg_dec<88>();
+        const int q4 = warp & 3, r = 32 * q4 + lane;
+        const uint32_t lane_addr = static_cast<uint32_t>(32 * q4) << 16;
+        const int ri = r / G, rg = r - ri * G;
+        int no[2] = {0, 0};
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            const int slot = it % kPtItems;
+            if (!pt_wait(bar(S::B_IF + slot), (it / kPtItems) & 1, p)) { ok = false; break; }
+            const PtItem& I = items[slot];
+            if (I.end) break;
+            const int q0 = I.q0, n = I.n, tok0 = I.tok0, hk = I.hk, split = I.split, nsplit = I.nsplit, unit = I.unit;
+            const bool whole = nsplit <= 1 && !partials;
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
+                const int tok = tok0 + t * TOK + ri;
+                const bool valid = ri < TOK && tok < n;
+                const bool live = I.jb[t] < I.je[t];
+                const long long row = static_cast<long long>(q0 + tok) * p.Hq + hk * G + rg;  // output row
+                const long long prow = static_cast<long long>(split) * p.T * p.Hq + row;      // partial row
+                float m = -INFINITY, l = 0.f;
+                if (live) {
+                    if (!pt_wait(bar(S::B_XF + t), no[t] & 1, p) || !pt_wait(bar(S::B_OF + t), no[t] & 1, p)) { ok = false; break; }
+                    ++no[t];
+                    m = stats[(2 * t) * kPtRows + r];
+                    l = stats[(2 * t + 1) * kPtRows + r];
+                    tc05::fence_after_sync();
+                }
+                const float inv = l > 0.f ? (whole ? p.v_scale : 1.f) / l : 0.f;
+                const bool write_o = valid && (whole || l > 0.f);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    if (live) {
+                        tc05::ld_32x32b_x32(tmem + lane_addr + 256 + D * t + c, o);
+                        tc05::wait_ld();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = l > 0.f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+                    if (!write_o) {
+                    } else if (!whole) {
+                        float4* dst = reinterpret_cast<float4*>(p.part_out + prow * D + c);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            __stcg(dst + e, make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                        __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
+                    } else if (p.out_dtype == 3) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + row * D + c);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float x = __uint_as_float(o[8 * e + 2 * k]), y = __uint_as_float(o[8 * e + 2 * k + 1]);
+                                h[k] = p.out_dtype == 0 ? pack2<true>(x, y) : pack2<false>(x, y);
+                            }
+                            dst[e] = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (live) {
+                    tc05::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(S::B_OE + t));
+                        mbar_arrive(bar(S::B_XE + t));
+                    }
+                }
+                if (valid) {
+                    const float l2 = l > 0.f ? m + __log2f(l) : -INFINITY;
+                    if (!whole)
+                        __stcg(p.part_lse + prow, l2);
+                    else if (p.lse)
+                        p.lse[row] = l2 * kLn2;
+                }
+            }
+            if (!ok) break;
+            if (!partials && nsplit > 1) {
+                // publish this part (the group's barrier, then one arrival with release
+                // semantics); the arrival that completes the unit merges its rows
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (tid == 256) scan[24] = atom_add_acq_rel_gpu(p.counters + unit);
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (scan[24] == nsplit - 1) {
+                    const int rows = min(2 * TOK, n - tok0) * G;
+                    for (int x = q4; x < rows; x += 4) {
+                        const long long row = static_cast<long long>(q0 + tok0 + x / G) * p.Hq + hk * G + x % G;
+                        const long long step = static_cast<long long>(p.T) * p.Hq;
+                        float acc[D / 32], mx, ws;
+                        pt_merge_row<D>(p.part_lse + row, p.part_out + row * D, step, nsplit, lane, acc, mx, ws);
+                        const float sc = ws > 0.f ? p.v_scale / ws : 0.f;
+#pragma unroll
+                        for (int e = 0; e < D / 32; ++e)
+                            store_out(p.out, row * D + lane * (D / 32) + e, acc[e] * sc, p.out_dtype);
+                        if (lane == 0 && p.lse) p.lse[row] = ws > 0.f ? (mx + __log2f(ws)) * kLn2 : -INFINITY;
+                    }
+                    if (tid == 256) p.counters[unit] = 0;  // every part has arrived: ready for the next call
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(S::B_IE + slot));
+        }
+        if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
+    }
+
+    // ---------------------------------------------------------- tear-down
+    tc05::fence_before_sync();
+    __syncthreads();
+    if (warp == 13) {
+        tc05::fence_after_sync();
+        tc05::dealloc(tmem, 512);
+    }
+    // the last CTA to leave resets the item counter for the next call
+    if (tid == 0) {
+        const int prev = atom_add_acq_rel_gpu(p.queue + 1);
+        if (prev == static_cast<int>(gridDim.x) - 1) {
+            p.queue[0] = 0;
+            p.queue[1] = 0;
+        }
+    }
+}
+
+}  // namespace pkd

@@ -1,0 +1,31 @@
+// Launch of the tcgen05 ragged-attention kernel for one head_dim and type.
+#pragma once
+
+#include "attend_launch.h"
+#include "attend_prompt.cuh"
+
+namespace pkd {
+
+template <int D, bool kBF16, bool kCap, bool kBias>
+static cudaError_t launch_prompt_one(const CUtensorMap& kvmap, const CUtensorMap& qmap, const AttendParams& p,
+                                     bool partials, int grid, cudaStream_t stream) {
+    auto kern = attend_prompt_kernel<D, kBF16, kCap, kBias>;
+    static PerDevice state;
+    cudaError_t e = kernel_setup(state, kern, kPtThreads, PtShape<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kPtThreads, PtShape<D>::SMEM, stream>>>(kvmap, qmap, p, partials ? 1 : 0);
+    return cudaGetLastError();
+}
+
+template <int D, bool kBF16>
+static cudaError_t launch_prompt_typed(const CUtensorMap& kvmap, const CUtensorMap& qmap, const AttendParams& p,
+                                       bool partials, int grid, cudaStream_t stream) {
+    const bool cap = p.cap_log2 > 0.f, bias = p.slopes != nullptr;
+    if (cap)
+        return bias ? launch_prompt_one<D, kBF16, true, true>(kvmap, qmap, p, partials, grid, stream)
+                    : launch_prompt_one<D, kBF16, true, false>(kvmap, qmap, p, partials, grid, stream);
+    return bias ? launch_prompt_one<D, kBF16, false, true>(kvmap, qmap, p, partials, grid, stream)
+                : launch_prompt_one<D, kBF16, false, false>(kvmap, qmap, p, partials, grid, stream);
+}
+
+}  // namespace pkd

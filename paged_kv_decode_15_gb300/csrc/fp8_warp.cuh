@@ -77,12 +77,9 @@ struct Fp8MmaWarp : MmaWarp<128, false, MT, NT, true> {
         }
     }
 
-    template <class Visible>
-    __device__ __forceinline__ void consume(uint32_t st, int half, int nvalid, bool masked, float scale2,
-                                            float bias2, Visible visible, int lane) {
-        // S = Q K^T on e4m3: the K tile is one 128-byte box per key row
+    // S = Q K^T on e4m3: the K tile is one 128-byte box per key row
+    __device__ __forceinline__ void qk_e4m3(uint32_t st, float (&sacc)[MT][2][4], int lane) const {
         const int mi = lane >> 3, ri = lane & 7;
-        float sacc[MT][2][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -99,6 +96,27 @@ struct Fp8MmaWarp : MmaWarp<128, false, MT, NT, true> {
                 mma16832_e4m3(sacc[mt][1], q8[mt][kk], b10, b11);
             }
         }
+    }
+
+    // A stage whose logits are score(q.k, row, kt), masked or not.
+    template <class Score, class Visible>
+    __device__ __forceinline__ void consume_scored(uint32_t st, int half, int nvalid, bool masked, Score score,
+                                                   Visible visible, int lane) {
+        float sacc[MT][2][4];
+        uint32_t pb[NT][2];
+        qk_e4m3(st, sacc, lane);
+        if (masked)
+            Base::template softmax_scored<true>(sacc, pb, nvalid, score, visible, lane);
+        else
+            Base::template softmax_scored<false>(sacc, pb, nvalid, score, visible, lane);
+        pv_e4m3(st + half, pb, lane);
+    }
+
+    template <class Visible>
+    __device__ __forceinline__ void consume(uint32_t st, int half, int nvalid, bool masked, float scale2,
+                                            float bias2, Visible visible, int lane) {
+        float sacc[MT][2][4];
+        qk_e4m3(st, sacc, lane);
         uint32_t pb[NT][2];
         if (masked)
             Base::template softmax<true>(sacc, pb, nvalid, scale2, bias2, visible, lane);

@@ -205,12 +205,20 @@ struct MmaWarp {
         pv(vt, pb, lane);
     }
 
-    // Online softmax of S: updates the row statistics, rescales O when a
-    // row's maximum moved, and returns P^T (rounded to the operand type) as
-    // the B fragments of the P.V product.
     template <bool kMasked, class Visible>
     __device__ __forceinline__ void softmax(float (&sacc)[MT][2][4], uint32_t (&pb)[NT][2], int nvalid,
                                             float scale2, float bias2, Visible visible, int lane) {
+        softmax_scored<kMasked>(
+            sacc, pb, nvalid, [&](float acc, int, int) { return fmaf(acc, scale2, bias2); }, visible, lane);
+    }
+
+    // Online softmax of S: updates the row statistics, rescales O when a
+    // row's maximum moved, and returns P^T (rounded to the operand type) as
+    // the B fragments of the P.V product.  score(q.k, row, kt) is the logit of
+    // key kt for query row `row` in log2 units.
+    template <bool kMasked, class Score, class Visible>
+    __device__ __forceinline__ void softmax_scored(float (&sacc)[MT][2][4], uint32_t (&pb)[NT][2], int nvalid,
+                                                   Score score, Visible visible, int lane) {
         const int g = lane >> 2, tg = lane & 3;
         float alpha[MT][2];
         bool grew = false;
@@ -226,9 +234,9 @@ struct MmaWarp {
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float s = fmaf(sacc[mt][n][2 * h + e], scale2, bias2);
+                        const int kt = n * 8 + 2 * tg + e;
+                        float s = score(sacc[mt][n][2 * h + e], row, kt);
                         if constexpr (kMasked) {
-                            const int kt = n * 8 + 2 * tg + e;
                             if (!(kt < nvalid && visible(row, kt))) s = -INFINITY;
                         }
                         sacc[mt][n][2 * h + e] = s;
@@ -290,6 +298,20 @@ struct MmaWarp {
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma16816<kBF16>(oacc[dt][n], va, pb[n][0], pb[n][1]);
         }
+    }
+
+    // A stage whose logits are score(q.k, row, kt), masked or not.
+    template <class Score, class Visible>
+    __device__ __forceinline__ void consume_scored(uint32_t st, int half, int nvalid, bool masked, Score score,
+                                                   Visible visible, int lane) {
+        float sacc[MT][2][4];
+        uint32_t pb[NT][2];
+        qk(st, sacc, lane);
+        if (masked)
+            softmax_scored<true>(sacc, pb, nvalid, score, visible, lane);
+        else
+            softmax_scored<false>(sacc, pb, nvalid, score, visible, lane);
+        pv(st + half, pb, lane);
     }
 
     // Full or masked stage, chosen per call (the choice is warp-uniform).
