@@ -24,6 +24,7 @@ constexpr size_t kPartials = kHeader + size_t(kMaxUnits) * 4;
 constexpr int kSms = 152;         // the plan is a host function: GB300's SM count
 constexpr int kStepCtas = 2048;   // as for the decode grid
 constexpr int kStepMaxChunk = 4096;
+constexpr int kMaxKeys = 1 << 29; // keys of a request: sums of a key index and a chunk fit 32 bits
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 int up(int x, int a) { return (x + a - 1) / a * a; }
@@ -50,6 +51,7 @@ pkd_status check_shape(int B, long long T, int Hq, int Hkv, int D, int P, int ma
         return report(PKD_EUNSUPPORTED, "kv dtype %d not supported (bf16, fp16, fp8-e4m3)", (int)kv);
     if (kv == PKD_FP8_E4M3 && D != 128) return report(PKD_EUNSUPPORTED, "fp8 caches need head_dim 128");
     if (B > pkd::kPtMaxBatch) return report(PKD_EUNSUPPORTED, "batch %d > %d", B, pkd::kPtMaxBatch);
+    if (max_kv_len > kMaxKeys) return report(PKD_EUNSUPPORTED, "lengths of up to %d keys are not supported (2^29)", max_kv_len);
     if (Hkv > 65535) return report(PKD_EUNSUPPORTED, "num_kv_heads %d > 65535", Hkv);
     if (T * Hq >= 1ll << 31) return report(PKD_EUNSUPPORTED, "tokens*num_heads must be < 2^31");
     return PKD_OK;
@@ -99,10 +101,11 @@ pkd_status plan_attend(int B, long long T, int max_q, int Hq, int Hkv, int D, in
     const long long floor_chunk = partials ? 256 : 512;
     long long chunk = std::max((vis + splits - 1) / splits, floor_chunk);
     chunk = (chunk + pkd::kPtKeys - 1) / pkd::kPtKeys * pkd::kPtKeys;
-    pl.chunk = (int)std::min(chunk, (1ll << 31) - 1024);
+    pl.chunk = (int)chunk;
     // + 15: an item's keys start on a 16-key boundary
     pl.max_splits = vis > 0 ? (int)((vis + 15 + pl.chunk - 1) / pl.chunk) : 1;
-    if (least * Hkv >= kSms && !partials) pl.max_splits = 1, pl.chunk = 0x7ffffc00;
+    // unsplit: a chunk beyond every length (first key + chunk stays below 2^31)
+    if (least * Hkv >= kSms && !partials) pl.max_splits = 1, pl.chunk = kMaxKeys;
     if (pl.units * pl.max_splits >= 1ll << 31) return report(PKD_EUNSUPPORTED, "too many work items");
     const size_t parts = (partials || pl.max_splits > 1) ? rows * pl.max_splits : 0;
     if (pl.max_splits > 1 && !partials && pl.units > kMaxUnits)
@@ -135,6 +138,8 @@ struct PrefixPlan {
 
 pkd_status plan_prefix(int B, int sq, int Hq, int Hkv, int D, int P, int groups, int max_prefix_len, int max_kv_len,
                        pkd_dtype kv, PrefixPlan& pl) {
+    if (max_prefix_len > kMaxKeys)
+        return report(PKD_EUNSUPPORTED, "prefixes of up to %d keys are not supported (2^29)", max_prefix_len);
     if (sq < 1 || groups < 1 || max_prefix_len < 0)
         return report(PKD_EINVAL, "invalid shape: sq=%d groups=%d max_prefix_len=%d", sq, groups, max_prefix_len);
     pkd_status st = check_shape(B, (long long)B * sq, Hq, Hkv, D, P, max_kv_len, kv);
@@ -346,7 +351,7 @@ pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_strid
     a.prefix_lens = o.prefix_lens;
     a.doc_start = o.doc_start;
     a.slopes = o.alibi_slopes;
-    a.window = o.window > 0 ? o.window : 0;
+    a.window = o.window > 0 ? std::min(o.window, 2 * kMaxKeys) : 0;  // positions less a window stay above -2^31
     a.causal = (flags & PKD_FLAG_CAUSAL) ? 1 : 0;
     a.max_q = max_query_len;
     a.out = out;

@@ -128,6 +128,16 @@ def test_few_rows_over_many_keys_split(D, Hq, Hkv):
     verify(c, "split prefix", prefix_lens=[2995, 0, 11], softcap=15.0)
 
 
+@pytest.mark.parametrize("window", [1030, 900, 2 ** 31 - 1])
+def test_unsplit_prompts_whose_keys_start_late(window):
+    """Enough row tiles to leave the keys unsplit, first keys past 1024."""
+    c = ref.Paged(lens=[2500], news=[40], Hq=1024, Hkv=8, D=64, dtype="fp16", seed=16)
+    import paged_kv_decode_15_gb300 as pkd
+    need = pkd.load_library().pkd_paged_attention_workspace_size(1, 40, 40, 1024, 8, 64, 16, 2512, pkd.FP16, None)
+    assert need == (1 << 20) + 256
+    verify(c, "late", window=window)
+
+
 def test_large_scores_move_the_reference_maximum():
     """Scores that grow by hundreds along the keys: accumulators are rescaled."""
     c = ref.Paged(lens=[700], news=[300], Hq=2, Hkv=1, D=64, dtype="fp16", seed=4)

@@ -64,6 +64,7 @@ def attend(lib, opt=None, **over):
     (dict(scale=-1.0), pkd.EINVAL, "scale"), (dict(scale=float("nan")), pkd.EINVAL, "scale"),
     (dict(flags=pkd.FLAG_HOST_IO), pkd.EUNSUPPORTED, "FLAG_CAUSAL"), (dict(starts=None), pkd.EINVAL, "query_start"),
     (dict(num_pages=1 << 40), pkd.EUNSUPPORTED, "cache too large"), (dict(T=1 << 40), pkd.EUNSUPPORTED, "2^31"),
+    (dict(max_kv=(1 << 29) + 1, stride=1 << 30), pkd.EUNSUPPORTED, "2^29"),
     (dict(lens=None), pkd.EINVAL, "null"), (dict(q=ctypes.c_void_p(0x10008)), pkd.EINVAL, "misaligned")])
 def test_paged_attention_refusals(lib, over, code, needle):
     assert attend(lib, **over) == code
@@ -113,7 +114,7 @@ def prefix(lib, **over):
 
 @pytest.mark.parametrize("over,code,needle", [
     (dict(groups=0), pkd.EINVAL, "groups"), (dict(groups=5000), pkd.EUNSUPPORTED, "groups"),
-    (dict(sq=0), pkd.EINVAL, "sq"), (dict(cap=-1.0), pkd.EINVAL, "softcap"), (dict(pstride=6), pkd.EINVAL, "prefix_table"),
+    (dict(sq=0), pkd.EINVAL, "sq"), (dict(max_prefix=(1 << 29) + 1, pstride=1 << 30), pkd.EUNSUPPORTED, "2^29"), (dict(cap=-1.0), pkd.EINVAL, "softcap"), (dict(pstride=6), pkd.EINVAL, "prefix_table"),
     (dict(gstart=None), pkd.EINVAL, "group_start"), (dict(plens=None), pkd.EINVAL, "null"),
     (dict(ws_bytes=1 << 20), pkd.EINVAL, "workspace"), (dict(flags=pkd.FLAG_GRID), pkd.EUNSUPPORTED, "FLAG_CAUSAL"),
     (dict(Hq=6, Hkv=4), pkd.EUNSUPPORTED, "multiple"), (dict(max_prefix=-1), pkd.EINVAL, "max_prefix_len")])
