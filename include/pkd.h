@@ -359,8 +359,8 @@ const char* pkd_paged_attention_kernel_name(int batch, int64_t total_tokens, int
  * a value that one token sees and another one does not must be finite for the
  * second (its weight there is 0).
  * Limits: head_dim 64 or 128; page_size a multiple of 16; num_heads/num_kv_heads
- * <= 128; batch <= 4096; scale * q_scale * k_scale > 0; fp8 caches need head_dim
- * 128 and max_query_len * num_heads/num_kv_heads <= 16.
+ * <= 128; batch <= 4096; max_kv_len <= 2^29; scale * q_scale * k_scale > 0; fp8
+ * caches need head_dim 128.
  */
 pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_stride, const void* kv_cache,
                                pkd_dtype kv_dtype, int64_t num_pages, const int32_t* block_table,
@@ -380,7 +380,8 @@ pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_strid
  *                 int32 [groups]: the pages and length of each shared prefix, in
  *                 the same kv_cache
  *   group_start   device int32 [groups + 1], rising: requests [group_start[g],
- *                 group_start[g + 1]) follow prefix g; others follow none
+ *                 group_start[g + 1]) follow prefix g; others follow none.  NULL
+ *                 with one group: every request follows it
  *   block_table, seq_lens  the requests' own keys, after the prefix (seq_lens[b]
  *                 keys; the first page of a request's row starts behind the prefix)
  *   out, lse      as for pkd_paged_decode, over the prefix's and the own keys
@@ -390,7 +391,7 @@ pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_strid
  *
  * The workspace is as for pkd_paged_attention.  max_prefix_len and max_kv_len
  * bound prefix_lens and seq_lens.  Limits as for
- * pkd_paged_attention, groups <= 4096; fp8 caches are not supported.
+ * pkd_paged_attention, groups <= 4096.
  */
 size_t pkd_prefix_decode_workspace_size(int batch, int sq, int num_heads, int num_kv_heads, int head_dim,
                                         int page_size, int groups, int max_prefix_len, int max_kv_len,

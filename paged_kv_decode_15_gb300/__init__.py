@@ -16,6 +16,7 @@ Entry points (same names as the C ABI in include/pkd.h, without the prefix):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -344,55 +345,66 @@ def cache_write(key, value, slot_mapping, kv_cache, k_scale=1.0, v_scale=1.0, st
     return kv_cache
 
 
-def _one_device(*tensors):
-    """The CUDA device that all the given tensors (name, tensor or None) live on."""
-    device = None
-    for name, t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name} is on {t.device}, other arguments on {device}")
-    return device
+# Host time of the calls below counts in a decode step: they compare device
+# indexes, take raw stream handles and enter a device or stream context only
+# where it differs from the current one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _stream_on(device, stream):
-    """The raw stream of a call on `device`: the given one, or the device's current stream."""
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if s.device != device:
-        raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
-    return s
+def _one_device(**tensors):
+    """The index of the CUDA device that all the given tensors (or None) live on."""
+    index = None
+    for name, t in tensors.items():
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if index is None:
+                index = d
+            elif d != index:
+                raise ValueError(f"{name} is on cuda:{d}, other arguments on cuda:{index}")
+    return index
 
 
-def _token_rows(t, name):
+def _elsewhere(index, stream):
+    """A context for a call whose device or stream is not the current one, or None."""
+    if stream is not None:
+        if stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+        if stream.cuda_stream != _raw_stream(index) or torch.cuda.current_device() != index:
+            return torch.cuda.stream(stream)
+    elif torch.cuda.current_device() != index:
+        return torch.cuda.device(index)
+    return None
+
+
+def _token_rows(t, shape, name):
     """Token stride of t [T, heads, D], whose tokens must be contiguous rows of heads * D."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
+    T, H, D = shape
+    a, b, c = t.stride()
+    if c != 1 or (b != D and H > 1):
         raise ValueError(f"{name} must be [tokens, heads, head_dim] with contiguous rows per token")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+    return a if T > 1 else max(a, H * D)
 
 
 _call_ws: dict = {}
 
 
-def _call_workspace(nbytes, device, stream):
-    """A zeroed workspace for a call on `stream`: one kept per stream (grown as
-    needed), or, while the stream is capturing, one of the graph's own (zeroed
-    by the graph), so that two graphs never share one."""
-    with torch.cuda.stream(stream):
-        if torch.cuda.is_current_stream_capturing():
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-            workspace_init(ws, stream)
-            return ws
-        key = (device.index, stream.cuda_stream)
-        ws = _call_ws.get(key)
-        if ws is None or ws.numel() < nbytes:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-            workspace_init(ws, stream)
-            _call_ws[key] = ws
+def _call_workspace(nbytes, index, stream):
+    """A zeroed workspace for a call on the current stream: one kept per stream
+    (grown as needed), or, while the stream is capturing, one of the graph's own
+    (zeroed by the graph), so that two graphs never share one."""
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+        _check(load_library().pkd_workspace_init(ws.data_ptr(), nbytes, stream))
         return ws
+    ws = _call_ws.get((index, stream))
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+        _check(load_library().pkd_workspace_init(ws.data_ptr(), nbytes, stream))
+        _call_ws[(index, stream)] = ws
+    return ws
 
 
 def rope_cache_write(q, key, value, positions, cos_sin, slot_mapping, kv_cache, *, interleaved=False, q_out=None,
@@ -405,63 +417,112 @@ def rope_cache_write(q, key, value, positions, cos_sin, slot_mapping, kv_cache, 
     type, or uint8 / float8_e4m3fn).  Returns the rotated q (q_out, allocated
     when not given; of type q_out_dtype: q's, or e4m3(q / q_scale)).
     """
-    lib = load_library()
-    device = _one_device(("key", key), ("q", q), ("value", value), ("positions", positions), ("cos_sin", cos_sin),
-                         ("slot_mapping", slot_mapping), ("kv_cache", kv_cache), ("q_out", q_out))
-    ks, vs = _token_rows(key, "key"), _token_rows(value, "value")
-    T, Hkv, D = key.shape
-    num_pages, _, P, _ = kv_cache.shape
-    if value.shape != key.shape or value.dtype != key.dtype:
+    index = _one_device(key=key, q=q, value=value, positions=positions, cos_sin=cos_sin, slot_mapping=slot_mapping,
+                        kv_cache=kv_cache, q_out=q_out)
+    ctx = _elsewhere(index, stream)
+    if ctx is not None:
+        with ctx:
+            return rope_cache_write(q, key, value, positions, cos_sin, slot_mapping, kv_cache, interleaved=interleaved,
+                                    q_out=q_out, q_out_dtype=q_out_dtype, q_scale=q_scale, k_scale=k_scale,
+                                    v_scale=v_scale)
+    lib = _lib or load_library()
+    shape = key.shape
+    T, Hkv, D = shape
+    num_pages, cache_heads, P, twoD = kv_cache.shape
+    if value.shape != shape or value.dtype != key.dtype:
         raise ValueError("value must have key's shape and dtype")
-    if kv_cache.shape[1] != Hkv or kv_cache.shape[3] != 2 * D or not kv_cache.is_contiguous():
+    if cache_heads != Hkv or twoD != 2 * D or not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be contiguous [num_pages, num_kv_heads, page_size, 2 * head_dim]")
     if positions.dtype != torch.int64 or slot_mapping.dtype != torch.int64 or cos_sin.dtype != torch.float32:
         raise TypeError("positions and slot_mapping must be int64, cos_sin float32")
-    if positions.shape != (T,) or slot_mapping.shape != (T,) or not (
+    max_position, rotary_dim = cos_sin.shape
+    if positions.dim() != 1 or slot_mapping.dim() != 1 or positions.numel() != T or slot_mapping.numel() != T or not (
             positions.is_contiguous() and slot_mapping.is_contiguous() and cos_sin.is_contiguous()):
         raise ValueError("positions and slot_mapping must be contiguous [T], cos_sin contiguous")
+    ks, vs = _token_rows(key, shape, "key"), _token_rows(value, shape, "value")
     Hq = qs = qos = 0
     in_dt = q_dt = dtype_code(key.dtype)
-    with torch.cuda.device(device):
-        s = _stream_on(device, stream)
-        if q is not None:
-            qs, Hq = _token_rows(q, "q"), q.shape[1]
-            if q.dtype != key.dtype or q.shape[0] != T or q.shape[2] != D:
-                raise ValueError("q must be [T, num_heads, head_dim] of key's dtype")
-            if q_out is None:
-                with torch.cuda.stream(s):
-                    q_out = torch.empty((T, Hq, D), dtype=q_out_dtype or q.dtype, device=device)
-            elif q_out.shape != q.shape:
+    if q is not None:
+        qshape = q.shape
+        Hq = qshape[1]
+        if q.dtype != key.dtype or qshape[0] != T or qshape[2] != D:
+            raise ValueError("q must be [T, num_heads, head_dim] of key's dtype")
+        qs = _token_rows(q, qshape, "q")
+        if q_out is None:
+            q_out = torch.empty(qshape, dtype=q_out_dtype or q.dtype, device=q.device)
+            qos = Hq * D
+        else:
+            if q_out.shape != qshape:
                 raise ValueError("q_out must have q's shape")
-            qos, q_dt = _token_rows(q_out, "q_out"), dtype_code(q_out.dtype)
-        _check(lib.pkd_rope_cache_write(
-            _ptr(q), qs, key.data_ptr(), ks, value.data_ptr(), vs, in_dt, positions.data_ptr(), cos_sin.data_ptr(),
-            cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0, slot_mapping.data_ptr(), T, Hq, Hkv, D, P,
-            num_pages, kv_cache.data_ptr(), dtype_code(kv_cache.dtype), k_scale, v_scale, _ptr(q_out), qos, q_dt,
-            q_scale, s.cuda_stream))
+            qos = _token_rows(q_out, qshape, "q_out")
+        q_dt = dtype_code(q_out.dtype)
+    status = lib.pkd_rope_cache_write(
+        q.data_ptr() if q is not None else None, qs, key.data_ptr(), ks, value.data_ptr(), vs, in_dt,
+        positions.data_ptr(), cos_sin.data_ptr(), max_position, rotary_dim, 1 if interleaved else 0,
+        slot_mapping.data_ptr(), T, Hq, Hkv, D, P, num_pages, kv_cache.data_ptr(), dtype_code(kv_cache.dtype), k_scale,
+        v_scale, q_out.data_ptr() if q is not None else None, qos, q_dt, q_scale, _raw_stream(index))
+    if status:
+        _check(status)
     return q_out
 
 
-def _options(device, T, Hq, B, window, softcap, alibi_slopes, prefix_lens, doc_start):
+def _options(index, T, Hq, B, window, softcap, alibi_slopes, prefix_lens, doc_start):
+    if alibi_slopes is prefix_lens is doc_start is None and not window and not softcap:
+        return None
     for name, t, dtype, n in (("alibi_slopes", alibi_slopes, torch.float32, Hq),
                               ("prefix_lens", prefix_lens, torch.int32, B), ("doc_start", doc_start, torch.int32, T)):
-        if t is not None and (t.dtype != dtype or t.shape != (n,) or not t.is_contiguous() or t.device != device):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} on {device}")
+        if t is not None and (t.dtype != dtype or t.dim() != 1 or t.numel() != n or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n}")
     return ScoreOptions(softcap, alibi_slopes.data_ptr() if alibi_slopes is not None else None, window,
                         prefix_lens.data_ptr() if prefix_lens is not None else None,
                         doc_start.data_ptr() if doc_start is not None else None)
 
 
-def _check_paged(q, kv_cache, block_table, seq_lens, what="block_table"):
-    D = q.shape[-1]
+def _check_paged(D, kv_cache, block_table, seq_lens, what="block_table"):
+    """(rows, columns, row stride) of a block table, checked with its lengths and the cache."""
     if kv_cache.dim() != 4 or kv_cache.shape[3] != 2 * D or not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be contiguous [num_pages, num_kv_heads, page_size, 2 * head_dim]")
     if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise TypeError(f"{what} and its lengths must be int32")
-    if block_table.dim() != 2 or (block_table.stride(1) != 1 and block_table.shape[1] > 1) or \
-            seq_lens.shape != (block_table.shape[0],) or not seq_lens.is_contiguous():
+    if block_table.dim() != 2:
+        raise ValueError(f"{what} must be [batch, columns]")
+    rows, columns = block_table.shape
+    a, b = block_table.stride()
+    if (b != 1 and columns > 1) or seq_lens.dim() != 1 or seq_lens.numel() != rows or not seq_lens.is_contiguous():
         raise ValueError(f"{what} must be [batch, columns] with contiguous rows, its lengths contiguous [batch]")
-    return block_table.stride(0) if block_table.shape[0] > 1 else max(block_table.stride(0), block_table.shape[1])
+    return rows, columns, a if rows > 1 else max(a, columns)
+
+
+def _results(out, lse, shape, dtype, device):
+    """out and lse of a call: the given ones, checked, or new ones."""
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+    elif out.shape != shape or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous {tuple(shape)}")
+    if lse is None:
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+    elif lse.shape != shape[:-1] or not lse.is_contiguous() or lse.dtype != torch.float32:
+        raise ValueError(f"lse must be contiguous float32 {tuple(shape[:-1])}")
+    return out, lse
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_bytes(*plan):
+    """Workspace bytes of a paged_attention plan (window and prefix mask last)."""
+    opt = ScoreOptions(0.0, None, plan[-2], 16 if plan[-1] else None, None)
+    n = load_library().pkd_paged_attention_workspace_size(*plan[:-2], opt)
+    if n == 0:
+        raise PkdError(EUNSUPPORTED, load_library().pkd_last_error().decode())
+    return n
+
+
+@functools.lru_cache(maxsize=4096)
+def _prefix_bytes(*plan):
+    """Workspace bytes of a prefix_decode plan."""
+    n = load_library().pkd_prefix_decode_workspace_size(*plan)
+    if n == 0:
+        raise PkdError(EUNSUPPORTED, load_library().pkd_last_error().decode())
+    return n
 
 
 def paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, *, causal=True, window=0, softcap=0.0,
@@ -479,49 +540,45 @@ def paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, *, c
     max_kv_len (default the table's capacity) bound the lengths on the host.
     Returns (out [T, Hq, D], lse fp32 [T, Hq]).
     """
-    lib = load_library()
-    device = _one_device(("q", q), ("kv_cache", kv_cache), ("block_table", block_table), ("seq_lens", seq_lens),
-                         ("query_start", query_start), ("out", out), ("lse", lse), ("workspace", workspace))
-    qs = _token_rows(q, "q")
-    stride = _check_paged(q, kv_cache, block_table, seq_lens)
-    T, Hq, D = q.shape
+    index = _one_device(q=q, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, query_start=query_start,
+                        alibi_slopes=alibi_slopes, prefix_lens=prefix_lens, doc_start=doc_start, out=out, lse=lse,
+                        workspace=workspace)
+    ctx = _elsewhere(index, stream)
+    if ctx is not None:
+        with ctx:
+            return paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, causal=causal, window=window,
+                                   softcap=softcap, alibi_slopes=alibi_slopes, prefix_lens=prefix_lens,
+                                   doc_start=doc_start, max_query_len=max_query_len, max_kv_len=max_kv_len,
+                                   q_scale=q_scale, k_scale=k_scale, v_scale=v_scale, out=out, lse=lse,
+                                   out_dtype=out_dtype, workspace=workspace)
+    lib = _lib or load_library()
+    shape = q.shape
+    T, Hq, D = shape
+    qs = _token_rows(q, shape, "q")
+    B, columns, stride = _check_paged(D, kv_cache, block_table, seq_lens)
     num_pages, Hkv, P, _ = kv_cache.shape
-    B = block_table.shape[0]
-    if query_start.dtype != torch.int32 or query_start.shape != (B + 1,) or not query_start.is_contiguous():
+    if query_start.dtype != torch.int32 or query_start.dim() != 1 or query_start.numel() != B + 1 or \
+            not query_start.is_contiguous():
         raise ValueError("query_start must be a contiguous int32 tensor [batch + 1]")
-    opt = _options(device, T, Hq, B, int(window), float(softcap), alibi_slopes, prefix_lens, doc_start)
+    opt = _options(index, T, Hq, B, window, softcap, alibi_slopes, prefix_lens, doc_start)
     if max_query_len is None:
         max_query_len = max(T, 1)
     if max_kv_len is None:
-        max_kv_len = block_table.shape[1] * P
-    kv_dt = dtype_code(kv_cache.dtype)
-    with torch.cuda.device(device):
-        s = _stream_on(device, stream)
-        with torch.cuda.stream(s):
-            if out is None:
-                out = torch.empty((T, Hq, D), dtype=out_dtype or (torch.bfloat16 if kv_dt == FP8_E4M3 else q.dtype),
-                                  device=device)
-            if lse is None:
-                lse = torch.empty((T, Hq), dtype=torch.float32, device=device)
-        _check_out(out, lse, (T, Hq, D))
-        need = lib.pkd_paged_attention_workspace_size(B, T, max_query_len, Hq, Hkv, D, P, max_kv_len, kv_dt, opt)
-        if need == 0:
-            raise PkdError(EUNSUPPORTED, lib.pkd_last_error().decode())
-        if workspace is None:
-            workspace = _call_workspace(need, device, s)
-        _check(lib.pkd_paged_attention(
-            q.data_ptr(), dtype_code(q.dtype), qs, kv_cache.data_ptr(), kv_dt, num_pages, block_table.data_ptr(),
-            stride, seq_lens.data_ptr(), query_start.data_ptr(), B, T, max_query_len, Hq, Hkv, D, P, max_kv_len,
-            scale, q_scale, k_scale, v_scale, opt, out.data_ptr(), dtype_code(out.dtype), lse.data_ptr(),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), FLAG_CAUSAL if causal else 0,
-            s.cuda_stream))
+        max_kv_len = columns * P
+    q_dt, kv_dt = dtype_code(q.dtype), dtype_code(kv_cache.dtype)
+    out, lse = _results(out, lse, shape, out_dtype or (torch.bfloat16 if kv_dt == FP8_E4M3 else q.dtype), q.device)
+    s = _raw_stream(index)
+    if workspace is None:
+        workspace = _call_workspace(_attention_bytes(B, T, max_query_len, Hq, Hkv, D, P, max_kv_len, kv_dt, window,
+                                                     prefix_lens is not None), index, s)
+    status = lib.pkd_paged_attention(
+        q.data_ptr(), q_dt, qs, kv_cache.data_ptr(), kv_dt, num_pages, block_table.data_ptr(), stride,
+        seq_lens.data_ptr(), query_start.data_ptr(), B, T, max_query_len, Hq, Hkv, D, P, max_kv_len, scale, q_scale,
+        k_scale, v_scale, opt, out.data_ptr(), dtype_code(out.dtype), lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), FLAG_CAUSAL if causal else 0, s)
+    if status:
+        _check(status)
     return out, lse
-
-
-def _check_out(out, lse, shape):
-    if out.shape != shape or not out.is_contiguous() or lse.shape != shape[:-1] or not lse.is_contiguous() or \
-            lse.dtype != torch.float32:
-        raise ValueError(f"out must be contiguous {tuple(shape)}, lse contiguous float32 {tuple(shape[:-1])}")
 
 
 def prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, scale, *, group_start=None,
@@ -535,55 +592,48 @@ def prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens,
     all); block_table, seq_lens: the requests' own keys behind the prefix.
     Returns (out [B, sq, Hq, D], lse fp32 [B, sq, Hq]) over both.
     """
-    lib = load_library()
-    device = _one_device(("q", q), ("kv_cache", kv_cache), ("prefix_table", prefix_table),
-                         ("prefix_lens", prefix_lens), ("block_table", block_table), ("seq_lens", seq_lens),
-                         ("group_start", group_start), ("out", out), ("lse", lse), ("workspace", workspace))
+    index = _one_device(q=q, kv_cache=kv_cache, prefix_table=prefix_table, prefix_lens=prefix_lens,
+                        block_table=block_table, seq_lens=seq_lens, group_start=group_start, out=out, lse=lse,
+                        workspace=workspace)
+    ctx = _elsewhere(index, stream)
+    if ctx is not None:
+        with ctx:
+            return prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, scale,
+                                 group_start=group_start, causal=causal, softcap=softcap, max_prefix_len=max_prefix_len,
+                                 max_kv_len=max_kv_len, q_scale=q_scale, k_scale=k_scale, v_scale=v_scale, out=out,
+                                 lse=lse, out_dtype=out_dtype, workspace=workspace)
+    lib = _lib or load_library()
     if q.dim() != 4 or not q.is_contiguous():
         raise ValueError("q must be contiguous [batch, sq, num_heads, head_dim]")
-    stride = _check_paged(q, kv_cache, block_table, seq_lens)
-    pstride = _check_paged(q, kv_cache, prefix_table, prefix_lens, "prefix_table")
-    B, sq, Hq, D = q.shape
+    shape = q.shape
+    B, sq, Hq, D = shape
+    rows, columns, stride = _check_paged(D, kv_cache, block_table, seq_lens)
+    groups, pcolumns, pstride = _check_paged(D, kv_cache, prefix_table, prefix_lens, "prefix_table")
     num_pages, Hkv, P, _ = kv_cache.shape
-    groups = prefix_table.shape[0]
-    if block_table.shape[0] != B:
+    if rows != B:
         raise ValueError("block_table must have one row per request")
+    if group_start is None:
+        if groups != 1:
+            raise ValueError("group_start is needed with more than one prefix")
+    elif group_start.dtype != torch.int32 or group_start.dim() != 1 or group_start.numel() != groups + 1 or \
+            not group_start.is_contiguous():
+        raise ValueError("group_start must be a contiguous int32 tensor [groups + 1]")
     if max_prefix_len is None:
-        max_prefix_len = prefix_table.shape[1] * P
+        max_prefix_len = pcolumns * P
     if max_kv_len is None:
-        max_kv_len = block_table.shape[1] * P
-    kv_dt = dtype_code(kv_cache.dtype)
-    with torch.cuda.device(device):
-        s = _stream_on(device, stream)
-        with torch.cuda.stream(s):
-            if group_start is None:
-                if groups != 1:
-                    raise ValueError("group_start is needed with more than one prefix")
-                group_start = _whole_batch(B, device)
-            elif group_start.dtype != torch.int32 or group_start.shape != (groups + 1,) or \
-                    not group_start.is_contiguous():
-                raise ValueError("group_start must be a contiguous int32 tensor [groups + 1]")
-            if out is None:
-                out = torch.empty((B, sq, Hq, D), dtype=out_dtype or (
-                    torch.bfloat16 if kv_dt == FP8_E4M3 else q.dtype), device=device)
-            if lse is None:
-                lse = torch.empty((B, sq, Hq), dtype=torch.float32, device=device)
-        _check_out(out, lse, (B, sq, Hq, D))
-        need = lib.pkd_prefix_decode_workspace_size(B, sq, Hq, Hkv, D, P, groups, max_prefix_len, max_kv_len, kv_dt)
-        if need == 0:
-            raise PkdError(EUNSUPPORTED, lib.pkd_last_error().decode())
-        if workspace is None:
-            workspace = _call_workspace(need, device, s)
-        _check(lib.pkd_prefix_decode(
-            q.data_ptr(), dtype_code(q.dtype), kv_cache.data_ptr(), kv_dt, num_pages, prefix_table.data_ptr(),
-            pstride, prefix_lens.data_ptr(), group_start.data_ptr(), groups, max_prefix_len, block_table.data_ptr(),
-            stride, seq_lens.data_ptr(), B, sq, Hq, Hkv, D, P, max_kv_len, scale, q_scale, k_scale, v_scale, softcap,
-            out.data_ptr(), dtype_code(out.dtype), lse.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), FLAG_CAUSAL if causal else 0, s.cuda_stream))
+        max_kv_len = columns * P
+    q_dt, kv_dt = dtype_code(q.dtype), dtype_code(kv_cache.dtype)
+    out, lse = _results(out, lse, shape, out_dtype or (torch.bfloat16 if kv_dt == FP8_E4M3 else q.dtype), q.device)
+    s = _raw_stream(index)
+    if workspace is None:
+        workspace = _call_workspace(_prefix_bytes(B, sq, Hq, Hkv, D, P, groups, max_prefix_len, max_kv_len, kv_dt),
+                                    index, s)
+    status = lib.pkd_prefix_decode(
+        q.data_ptr(), q_dt, kv_cache.data_ptr(), kv_dt, num_pages, prefix_table.data_ptr(), pstride,
+        prefix_lens.data_ptr(), group_start.data_ptr() if group_start is not None else None, groups, max_prefix_len,
+        block_table.data_ptr(), stride, seq_lens.data_ptr(), B, sq, Hq, Hkv, D, P, max_kv_len, scale, q_scale, k_scale,
+        v_scale, softcap, out.data_ptr(), dtype_code(out.dtype), lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), FLAG_CAUSAL if causal else 0, s)
+    if status:
+        _check(status)
     return out, lse
-
-
-def _whole_batch(B, device):
-    """group_start of a single group: {0, B}, made on the device."""
-    return torch.arange(0, 2 * B, max(B, 1), dtype=torch.int32, device=device) if B else \
-        torch.zeros(2, dtype=torch.int32, device=device)

@@ -342,8 +342,8 @@ pkd_status get_q_map(CUtensorMap& out, const void* q, int D, int Hq, uint64_t to
     if (token_stride == 0) token_stride = (int64_t)Hq * D;
     MapKey k;
     std::memset(&k, 0, sizeof k);
-    k.base = q; k.d0 = (uint64_t)D; k.d1 = (uint64_t)Hq; k.d2 = tokens; k.s1 = (uint64_t)D * 2;
-    k.s2 = (uint64_t)token_stride * 2; k.rank = 1000 + G * 256 + sq; k.dtype = dt;
+    k.base = q; k.d0 = (uint64_t)D; k.d1 = (uint64_t)Hq; k.d2 = tokens; k.s1 = (uint64_t)D * elt_bytes(dt);
+    k.s2 = (uint64_t)token_stride * elt_bytes(dt); k.rank = 1000 + G * 256 + sq; k.dtype = dt;
     MapCache& c = map_cache();
     {
         std::lock_guard<std::mutex> g(c.mu);
@@ -355,10 +355,12 @@ pkd_status get_q_map(CUtensorMap& out, const void* q, int D, int Hq, uint64_t to
     }
     EncodeTiledFn enc = encode_fn();
     if (!enc) return fail(PKD_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const CUtensorMapDataType t = dt == PKD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUtensorMapDataType t = dt == PKD_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                  : dt == PKD_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     cuuint64_t dims[3] = {k.d0, k.d1, k.d2};
     cuuint64_t strides[2] = {k.s1, k.s2};
-    cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)sq};
+    cuuint32_t box[3] = {(cuuint32_t)(128 / elt_bytes(dt)), (cuuint32_t)G, (cuuint32_t)sq};
     cuuint32_t estr[3] = {1, 1, 1};
     CUtensorMap m;
     CUresult r = enc(&m, t, 3, const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

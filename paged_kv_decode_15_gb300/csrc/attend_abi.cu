@@ -125,9 +125,6 @@ pkd_status plan_paged_attention(int B, long long T, int max_q, int Hq, int Hkv, 
     // a window bounds the span of a request's keys, unless prefix keys are seen past the position
     if (o.window > 0 && !o.prefix_lens) vis = std::min(vis, (long long)o.window + max_q - 1 + 15);
     const bool step = (long long)max_q * (Hq / Hkv) <= 16;
-    if (!step && kv == PKD_FP8_E4M3)
-        return report(PKD_EUNSUPPORTED, "fp8 caches with more than 16 query rows per kv head (max_query_len %d x %d) "
-                      "are not supported", max_q, Hq / Hkv);
     return plan_attend(B, T, max_q, Hq, Hkv, D, P, vis, kv, false, step, pl);
 }
 
@@ -147,8 +144,6 @@ pkd_status plan_prefix(int B, int sq, int Hq, int Hkv, int D, int P, int groups,
     if (groups > pkd::kPtMaxBatch) return report(PKD_EUNSUPPORTED, "groups %d > %d", groups, pkd::kPtMaxBatch);
     const int T = B * sq;
     const bool step = (long long)sq * (Hq / Hkv) <= 16;
-    if (kv == PKD_FP8_E4M3)
-        return report(PKD_EUNSUPPORTED, "fp8 caches are not supported");
     st = plan_attend(groups, T, T > 0 ? T : 1, Hq, Hkv, D, P, max_prefix_len, kv, true, false, pl.pre);
     if (st != PKD_OK) return st;
     st = plan_attend(B, T, sq, Hq, Hkv, D, P, max_kv_len, kv, false, step, pl.own);
@@ -286,9 +281,13 @@ cudaError_t pkd::launch_attend_prompt(int D, int kv_dtype, const CUtensorMap& kv
     int grid = 1;
     cudaError_t e = persistent_grid(1, (int)std::min(items, 1ll << 20), grid);
     if (e != cudaSuccess) return e;
-    const bool bf16 = kv_dtype == PKD_BF16;
-    return D == 128 ? launch_prompt_d128(bf16, kvmap, qmap, p, partials, grid, stream)
-                    : launch_prompt_d64(bf16, kvmap, qmap, p, partials, grid, stream);
+    if (kv_dtype == PKD_FP8_E4M3)
+        return D == 128 ? launch_prompt_fp8_d128(kvmap, qmap, p, partials, grid, stream) : cudaErrorInvalidValue;
+    if (kv_dtype == PKD_BF16)
+        return D == 128 ? launch_prompt_bf16_d128(kvmap, qmap, p, partials, grid, stream)
+                        : launch_prompt_bf16_d64(kvmap, qmap, p, partials, grid, stream);
+    return D == 128 ? launch_prompt_fp16_d128(kvmap, qmap, p, partials, grid, stream)
+                    : launch_prompt_fp16_d64(kvmap, qmap, p, partials, grid, stream);
 }
 
 extern "C" {
@@ -395,7 +394,8 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
     if (st != PKD_OK) return st;
     st = check_table(prefix_table, prefix_table_stride, prefix_lens, max_prefix_len, page_size, "prefix_table");
     if (st != PKD_OK) return st;
-    if (!group_start || !aligned(group_start, 4)) return report(PKD_EINVAL, "group_start is null or misaligned");
+    if ((!group_start && groups != 1) || !aligned(group_start, 4))
+        return report(PKD_EINVAL, "group_start is misaligned, or null with more than one group");
 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const long long T = (long long)batch * sq;
@@ -411,6 +411,7 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
     a.seq_lens = prefix_lens;
     a.query_start = group_start;
     a.q_mul = sq;
+    a.sq = (int)T;  // without group_start: one group of every request
     a.max_q = (int)T;
     a.v_scale = 1.f;
     st = launch_pass(a, pl.pre, kv_cache, kv_dtype, head_dim, true, s, "pkd_prefix_decode prefix launch");

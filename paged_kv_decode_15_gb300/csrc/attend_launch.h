@@ -16,10 +16,11 @@ cudaError_t launch_attend_step(int D, int kv_dtype, int NT, const CUtensorMap& t
 // persistent CTAs.  partials: leave every result as a partial one.
 cudaError_t launch_attend_prompt(int D, int kv_dtype, const CUtensorMap& kvmap, const CUtensorMap& qmap,
                                  const AttendParams& p, bool partials, long long items, cudaStream_t stream);
-cudaError_t launch_prompt_d128(bool bf16, const CUtensorMap& kvmap, const CUtensorMap& qmap, const AttendParams& p,
-                               bool partials, int grid, cudaStream_t stream);
-cudaError_t launch_prompt_d64(bool bf16, const CUtensorMap& kvmap, const CUtensorMap& qmap, const AttendParams& p,
-                              bool partials, int grid, cudaStream_t stream);
+#define PKD_PROMPT(name)                                                                                       \
+    cudaError_t launch_prompt_##name(const CUtensorMap& kvmap, const CUtensorMap& qmap, const AttendParams& p, \
+                                     bool partials, int grid, cudaStream_t stream);
+PKD_PROMPT(bf16_d128) PKD_PROMPT(fp16_d128) PKD_PROMPT(fp8_d128) PKD_PROMPT(bf16_d64) PKD_PROMPT(fp16_d64)
+#undef PKD_PROMPT
 
 // Joins the partial results of the shared prefix with those of the requests' own keys.
 struct PrefixMergeParams {

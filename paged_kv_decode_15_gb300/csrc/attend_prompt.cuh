@@ -19,7 +19,9 @@
 // Warp roles (512 threads): warps 0-3 and 4-7 the softmax of tile 0 and 1, warps
 // 8-11 the epilogue (O out of TMEM, normalised, written -- or a partial result
 // when the keys are split), warp 12 loads (work items, Q, K, V by TMA), warp 13
-// issues the products.  Registers follow the roles (setmaxnreg).
+// issues the products; for e4m3 caches S is an e4m3 product and warps 14-15 widen
+// V to fp16 in shared memory ahead of the O product (P is rounded to fp16 then).
+// Registers follow the roles (setmaxnreg).
 // Work items are handed out by an atomic counter in the workspace, the longest of
 // a request first, so CTAs finish together whatever the lengths; results do not
 // depend on who computes an item.  Every wait is bounded.
@@ -48,16 +50,28 @@ struct PtItem {
     int pad[2];
 };
 
-// NU K/V units; K and V of a key tile are one unit each
-template <int D>
+// Types of q and the cache.
+enum PtType { kPtBF16 = 0, kPtFP16 = 1, kPtFP8 = 2 };
+
+// NU K/V units; K and V of a key tile are one unit each (units of K have even
+// numbers, NU is even, so a slot always holds the one or the other).  e4m3: the
+// raw V units are widened to fp16 into two buffers of their own.
+template <int D, int kType>
 struct PtShape {
-    static constexpr int ROWB = D * 2;
-    static constexpr int GROUP = 8 * ROWB;               // 8 keys: D / 64 regions of 8 x 128 bytes
-    static constexpr int UNIT = kPtKeys / 8 * GROUP;     // 32 KB at D = 128
-    static constexpr int NU = D == 128 ? 4 : 8;
+    static constexpr bool FP8 = kType == kPtFP8;
+    static constexpr int ROWB = D * (FP8 ? 1 : 2);
+    static constexpr int REGIONS = ROWB / 128;           // 128-byte regions of a row
+    static constexpr int GROUP = 8 * ROWB;               // 8 keys: REGIONS regions of 8 x 128 bytes
+    static constexpr int UNIT = kPtKeys / 8 * GROUP;     // 32 KB at D = 128, 16-bit
+    static constexpr int NU = FP8 ? 6 : D == 128 ? 4 : 8;
+    static constexpr int NV = FP8 ? 2 : 0;               // widened V tiles
+    static constexpr int VGROUP = 8 * D * 2;             // 8 keys of V as the O product reads them
+    static constexpr int VUNIT = kPtKeys / 8 * VGROUP;
     static constexpr int QTILE = kPtRows * ROWB;
     static constexpr int OFF_KV = 0;
-    static constexpr int OFF_Q = NU * UNIT;
+    static constexpr int OFF_V = NU * UNIT;
+    static constexpr int OFF_Q = OFF_V + NV * VUNIT;
+    static_assert(NU % 2 == 0 && (!FP8 || D == 128), "unit parity; e4m3 rows are one region");
     static constexpr int OFF_STAT = OFF_Q + 2 * QTILE;   // float [2 tiles][m, l][128]
     static constexpr int OFF_ITEM = OFF_STAT + 2 * 2 * kPtRows * 4;
     static constexpr int OFF_PREF = OFF_ITEM + kPtItems * static_cast<int>(sizeof(PtItem));
@@ -66,7 +80,8 @@ struct PtShape {
     // units full/empty, Q full/empty, S full, P full, O step done, O full/drained, stats full/free, item full/empty, drain
     static constexpr int B_UF = 0, B_UE = B_UF + NU, B_QF = B_UE + NU, B_QE = B_QF + 1, B_SF = B_QE + 1;
     static constexpr int B_PF = B_SF + 2, B_OD = B_PF + 2, B_OF = B_OD + 2, B_OE = B_OF + 2, B_XF = B_OE + 2;
-    static constexpr int B_XE = B_XF + 2, B_IF = B_XE + 2, B_IE = B_IF + kPtItems, B_DR = B_IE + kPtItems;
+    static constexpr int B_XE = B_XF + 2, B_IF = B_XE + 2, B_IE = B_IF + kPtItems, B_DR = B_IE + kPtItems + 2 * NV;
+    static constexpr int B_VF = B_IE + kPtItems, B_VE = B_VF + NV;  // widened V full/empty
     static constexpr int NBAR = B_DR + 1;
     static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_TMEM + 16 + 1024;
@@ -150,11 +165,12 @@ __device__ __forceinline__ void pt_merge_row(const float* pl, const float* po, l
 }
 
 // kPartials: every result is left as a partial one (for a merge that follows)
-template <int D, bool kBF16, bool kCap, bool kBias>
+template <int D, int kType, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kPtThreads, 1)
 attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
                      const AttendParams p, const int partials) {
-    using S = PtShape<D>;
+    using S = PtShape<D, kType>;
+    constexpr bool kFp8 = kType == kPtFP8, kBF16 = kType == kPtBF16;  // e4m3: P and V in fp16
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb0 = smem_u32(smem);
@@ -172,7 +188,11 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
     if (tid == 0) {
         for (int i = 0; i < S::NU; ++i) {
             mbar_init(bar(S::B_UF + i), 1);
-            mbar_init(bar(S::B_UE + i), 1);
+            mbar_init(bar(S::B_UE + i), kFp8 && (i & 1) ? 2 : 1);  // raw V: both widening warps
+        }
+        for (int i = 0; i < S::NV; ++i) {
+            mbar_init(bar(S::B_VF + i), 2);
+            mbar_init(bar(S::B_VE + i), 1);
         }
         mbar_init(bar(S::B_QF), 1);
         mbar_init(bar(S::B_QE), 1);
@@ -187,7 +207,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
         }
         for (int i = 0; i < kPtItems; ++i) {
             mbar_init(bar(S::B_IF + i), 1);
-            mbar_init(bar(S::B_IE + i), 1 + 8 + 4);  // the issuing thread, softmax and epilogue warps
+            mbar_init(bar(S::B_IE + i), 1 + 8 + 4 + (kFp8 ? 2 : 0));  // the issuing thread; softmax, epilogue, widening warps
         }
         mbar_init(bar(S::B_DR), 1);
         fence_barrier_init();
@@ -229,7 +249,8 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
     __syncthreads();
     tc05::fence_after_sync();
     const uint32_t tmem = *tslot;
-    constexpr uint32_t kIdS = tc05::idesc_f16(kBF16, kPtRows, kPtKeys, false, false);  // S = Q K^T
+    constexpr uint32_t kIdS = kFp8 ? tc05::idesc_e4m3(kPtRows, kPtKeys)
+                                   : tc05::idesc_f16(kBF16, kPtRows, kPtKeys, false, false);  // S = Q K^T
     constexpr uint32_t kIdO = tc05::idesc_f16(kBF16, kPtRows, D, false, true);         // O += P V
 
     if (warp >= 12) {
@@ -339,9 +360,9 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     if (nq >= 1 && !pt_wait(bar(S::B_QE), (nq - 1) & 1, p)) { ok = false; break; }
                     const int tiles = tok0 + TOK < n ? 2 : 1;
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(bar(S::B_QF), tiles * (D / 64) * TOK * G * 128);
+                        mbar_arrive_expect_tx(bar(S::B_QF), tiles * S::REGIONS * TOK * G * 128);
                         for (int t = 0; t < tiles; ++t)
-                            for (int h = 0; h < D / 64; ++h)
+                            for (int h = 0; h < S::REGIONS; ++h)
                                 tma_load_3d(sb0 + S::OFF_Q + t * S::QTILE + h * kPtRows * 128, &qmap, 64 * h, hk * G,
                                             q0 + tok0 + t * TOK, bar(S::B_QF), pol);
                     }
@@ -366,7 +387,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                             __syncwarp();
                             if (load)
                                 tma_load_4d(sb0 + S::OFF_KV + us * S::UNIT + 2 * lane * S::GROUP, &kvmap, 0, 0,
-                                            v * (D / 64), krow >> 3, bar(S::B_UF + us), keep);
+                                            v * S::REGIONS, krow >> 3, bar(S::B_UF + us), keep);
                         }
                         pg = pg_next;
                     }
@@ -384,7 +405,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             // --------------------------------------------------- products
             if (lane == 0) {
                 bool ok = true;
-                int u = 0, nq = 0;
+                int u = 0, nq = 0, nv = 0;  // nv: widened V tiles
                 int np[2] = {0, 0}, no[2] = {0, 0};  // P tiles consumed, accumulations begun
                 for (int it = 0; ok; ++it) {
                     const int slot = it % kPtItems;
@@ -405,11 +426,14 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                         const uint32_t k = sb0 + S::OFF_KV + ((u + 2 * j) % S::NU) * S::UNIT;
                         const uint32_t q = sb0 + S::OFF_Q + t * S::QTILE;
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            tc05::mma_f16(tmem + kPtKeys * t,
-                                          tc05::smem_desc(q + (kk >> 2) * kPtRows * 128 + (kk & 3) * 32, 16, 1024),
-                                          tc05::smem_desc(k + (kk >> 2) * 1024 + (kk & 3) * 32, 16, S::GROUP), kIdS,
-                                          kk > 0);
+                        for (int kk = 0; kk < S::ROWB / 32; ++kk) {
+                            const uint64_t qd = tc05::smem_desc(q + (kk >> 2) * kPtRows * 128 + (kk & 3) * 32, 16, 1024);
+                            const uint64_t kd = tc05::smem_desc(k + (kk >> 2) * 1024 + (kk & 3) * 32, 16, S::GROUP);
+                            if constexpr (kFp8)
+                                tc05::mma_e4m3(tmem + kPtKeys * t, qd, kd, kIdS, kk > 0);
+                            else
+                                tc05::mma_f16(tmem + kPtKeys * t, qd, kd, kIdS, kk > 0);
+                        }
                         tc05::commit(bar(S::B_SF + t));
                     };
                     ok = k_ready(0);
@@ -418,8 +442,11 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                         if (jb[t] == 0 && je[t] > 0) qk(t, 0);
                     tc05::commit(bar(S::B_UE + u % S::NU));
                     for (int j = 0; ok && j < ntiles; ++j) {
-                        const int vu = u + 2 * j + 1;
-                        ok = mbar_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p.status);
+                        const int vu = u + 2 * j + 1, vb = kFp8 ? (nv + j) % 2 : 0;
+                        ok = kFp8 ? mbar_wait(bar(S::B_VF + vb), ((nv + j) >> 1) & 1, p.status)
+                                  : mbar_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p.status);
+                        const uint32_t v = sb0 + (kFp8 ? S::OFF_V + vb * S::VUNIT : S::OFF_KV + (vu % S::NU) * S::UNIT);
+                        const uint32_t v_free = kFp8 ? bar(S::B_VE + vb) : bar(S::B_UE + vu % S::NU);
                         bool have_k = false;
                         for (int t = 0; ok && t < 2; ++t) {
                             if (j >= jb[t] && j < je[t]) {
@@ -432,16 +459,15 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                                 }
                                 if (!ok) break;
                                 tc05::fence_after_sync();
-                                const uint32_t v = sb0 + S::OFF_KV + (vu % S::NU) * S::UNIT;
 #pragma unroll
                                 for (int kk = 0; kk < kPtKeys / 16; ++kk)
                                     tc05::mma_f16_ts(tmem + 256 + D * t, tmem + kPtKeys * t + 8 * kk,
-                                                     tc05::smem_desc(v + 2 * kk * S::GROUP, 1024, S::GROUP), kIdO,
+                                                     tc05::smem_desc(v + 2 * kk * S::VGROUP, 1024, S::VGROUP), kIdO,
                                                      j > jb[t] || kk > 0);
                                 tc05::commit(bar(S::B_OD + t));
                                 if (j == je[t] - 1) tc05::commit(bar(S::B_OF + t));
                             }
-                            if (t == 1) tc05::commit(bar(S::B_UE + vu % S::NU));
+                            if (t == 1) tc05::commit(v_free);
                             if (j + 1 < ntiles) {
                                 if (!have_k) {
                                     ok = k_ready(j + 1);
@@ -457,6 +483,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     }
                     tc05::commit(bar(S::B_QE));
                     u += 2 * ntiles;
+                    nv += ntiles;
                 }
                 if (!ok) atomicOr(p.status, kErrTimeout);
                 // every product issued has completed before TMEM is freed
@@ -464,6 +491,64 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                 mbar_wait(bar(S::B_DR), 0);
             }
             __syncwarp();
+        } else if constexpr (kFp8) {
+            // ---------------------------------- V of e4m3 caches, widened
+            // every e4m3 value is exact in fp16; the 16-bit tile has the layout of a
+            // 16-bit cache's.  A thread widens two key rows; rows that no query row
+            // of the unit sees become zeros (their weight 0 must not meet a NaN)
+            const int x = (warp - 14) * 32 + lane;
+            int u = 0, nv = 0;
+            bool ok = true;
+            for (int it = 0; ok; ++it) {
+                const int slot = it % kPtItems;
+                if (!pt_wait(bar(S::B_IF + slot), (it / kPtItems) & 1, p)) { ok = false; break; }
+                const PtItem& I = items[slot];
+                if (I.end) break;
+                const int ntiles = I.ntiles, t0 = I.t0, lo_all = I.lo_all, hi_all = min(I.hi_all, I.t1), bad = I.bad;
+                const int32_t* table = p.block_table + static_cast<long long>(I.b) * p.bt_stride;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S::B_IE + slot));
+                for (int j = 0; j < ntiles; ++j, ++nv) {
+                    const int vu = u + 2 * j + 1, vb = nv & 1;
+                    if (!pt_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p)) { ok = false; break; }
+                    if (nv >= 2 && !pt_wait(bar(S::B_VE + vb), ((nv >> 1) - 1) & 1, p)) { ok = false; break; }
+                    const uint8_t* raw = smem + S::OFF_KV + (vu % S::NU) * S::UNIT;
+                    uint8_t* wide = smem + S::OFF_V + vb * S::VUNIT;
+#pragma unroll 1
+                    for (int r = x; r < kPtKeys; r += 64) {
+                        const int key = t0 + j * kPtKeys + r, sw = r & 7;
+                        bool seen = key >= lo_all && key < hi_all;
+                        if (bad && seen) {
+                            const int pg = table[page_div(key, p.pmagic, p.pmshift)];
+                            seen = pg >= 0 && pg < p.num_pages;
+                        }
+                        const uint8_t* src = raw + (r >> 3) * S::GROUP + sw * 128;
+                        uint8_t* dst = wide + (r >> 3) * S::VGROUP + sw * 128;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const uint4 e = *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4));
+                            uint4 a = make_uint4(0, 0, 0, 0), b = a;
+                            if (seen) {
+                                a = make_uint4(e4m3x2_to_f16x2(e.x), e4m3x2_to_f16x2(e.x >> 16), e4m3x2_to_f16x2(e.y),
+                                               e4m3x2_to_f16x2(e.y >> 16));
+                                b = make_uint4(e4m3x2_to_f16x2(e.z), e4m3x2_to_f16x2(e.z >> 16), e4m3x2_to_f16x2(e.w),
+                                               e4m3x2_to_f16x2(e.w >> 16));
+                            }
+                            uint8_t* half = dst + (c >> 2) * 1024;
+                            *reinterpret_cast<uint4*>(half + (((2 * (c & 3)) ^ sw) << 4)) = a;
+                            *reinterpret_cast<uint4*>(half + (((2 * (c & 3) + 1) ^ sw) << 4)) = b;
+                        }
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(S::B_VF + vb));
+                        mbar_arrive(bar(S::B_UE + vu % S::NU));
+                    }
+                }
+                u += 2 * ntiles;
+            }
+            if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
         }
     } else if (warp < 8) {
         // ------------------------------------------------------- softmax
@@ -582,14 +667,14 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     }
                     // V rows that no row of the unit sees (stale slots, skipped pages)
                     // are zeroed: their weight 0 must not meet a NaN
-                    const bool zeroes = lead || j < jb0 || j >= je0;
+                    const bool zeroes = !kFp8 && (lead || j < jb0 || j >= je0);
                     if (zeroes && (bad || tk < lo_all || tk + kPtKeys > hi_all)) {
                         const int vu = u + 2 * j + 1, key = tk + r;
                         if (!pt_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p)) { ok = false; break; }
                         if (key < lo_all || key >= hi_all || !(stages >> (r >> 4) & 1)) {
                             uint8_t* vrow = smem + S::OFF_KV + (vu % S::NU) * S::UNIT + (r >> 3) * S::GROUP + (r & 7) * 128;
 #pragma unroll
-                            for (int h = 0; h < D / 64; ++h)
+                            for (int h = 0; h < S::REGIONS; ++h)
 #pragma unroll
                                 for (int e = 0; e < 8; ++e)
                                     *reinterpret_cast<uint4*>(vrow + h * 1024 + ((e + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);

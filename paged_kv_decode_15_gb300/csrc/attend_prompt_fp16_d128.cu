@@ -1,0 +1,11 @@
+// The tcgen05 ragged-attention kernel: fp16, head_dim 128.
+#include "attend_prompt_launch.cuh"
+
+namespace pkd {
+
+cudaError_t launch_prompt_fp16_d128(const CUtensorMap& kvmap, const CUtensorMap& qmap, const AttendParams& p, bool partials,
+                               int grid, cudaStream_t stream) {
+    return launch_prompt_typed<128, kPtFP16>(kvmap, qmap, p, partials, grid, stream);
+}
+
+}  // namespace pkd

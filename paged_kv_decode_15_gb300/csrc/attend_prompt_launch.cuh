@@ -6,26 +6,26 @@
 
 namespace pkd {
 
-template <int D, bool kBF16, bool kCap, bool kBias>
+template <int D, int kType, bool kCap, bool kBias>
 static cudaError_t launch_prompt_one(const CUtensorMap& kvmap, const CUtensorMap& qmap, const AttendParams& p,
                                      bool partials, int grid, cudaStream_t stream) {
-    auto kern = attend_prompt_kernel<D, kBF16, kCap, kBias>;
+    auto kern = attend_prompt_kernel<D, kType, kCap, kBias>;
     static PerDevice state;
-    cudaError_t e = kernel_setup(state, kern, kPtThreads, PtShape<D>::SMEM);
+    cudaError_t e = kernel_setup(state, kern, kPtThreads, PtShape<D, kType>::SMEM);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kPtThreads, PtShape<D>::SMEM, stream>>>(kvmap, qmap, p, partials ? 1 : 0);
+    kern<<<grid, kPtThreads, PtShape<D, kType>::SMEM, stream>>>(kvmap, qmap, p, partials ? 1 : 0);
     return cudaGetLastError();
 }
 
-template <int D, bool kBF16>
+template <int D, int kType>
 static cudaError_t launch_prompt_typed(const CUtensorMap& kvmap, const CUtensorMap& qmap, const AttendParams& p,
                                        bool partials, int grid, cudaStream_t stream) {
     const bool cap = p.cap_log2 > 0.f, bias = p.slopes != nullptr;
     if (cap)
-        return bias ? launch_prompt_one<D, kBF16, true, true>(kvmap, qmap, p, partials, grid, stream)
-                    : launch_prompt_one<D, kBF16, true, false>(kvmap, qmap, p, partials, grid, stream);
-    return bias ? launch_prompt_one<D, kBF16, false, true>(kvmap, qmap, p, partials, grid, stream)
-                : launch_prompt_one<D, kBF16, false, false>(kvmap, qmap, p, partials, grid, stream);
+        return bias ? launch_prompt_one<D, kType, true, true>(kvmap, qmap, p, partials, grid, stream)
+                    : launch_prompt_one<D, kType, true, false>(kvmap, qmap, p, partials, grid, stream);
+    return bias ? launch_prompt_one<D, kType, false, true>(kvmap, qmap, p, partials, grid, stream)
+                : launch_prompt_one<D, kType, false, false>(kvmap, qmap, p, partials, grid, stream);
 }
 
 }  // namespace pkd

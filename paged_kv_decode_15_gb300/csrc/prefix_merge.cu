@@ -16,8 +16,8 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixMergePara
     // the request's group: group_start[g] <= b < group_start[g + 1]
     const int b = row / p.rows_per_request;
     int np = 0;
-    if (b >= p.group_start[0] && b < p.group_start[p.groups]) {
-        int lo = 0, hi = p.groups;
+    if (!p.group_start || (b >= p.group_start[0] && b < p.group_start[p.groups])) {
+        int lo = 0, hi = p.group_start ? p.groups : 1;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (p.group_start[mid] <= b) lo = mid; else hi = mid;

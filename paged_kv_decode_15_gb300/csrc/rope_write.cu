@@ -34,13 +34,27 @@ struct RopeParams {
     long long q_stride, k_stride, v_stride, q_out_stride, max_position, num_slots;
     int Hq, Hkv, P, rd;
     float q_scale, k_scale, v_scale;
-    float q_inv, k_inv, v_inv;  // 1/scale when exact (power of two), else 0
+    float q_inv, k_inv, v_inv;  // 1/scale where rope_divide holds, else 0
 };
 
 __device__ __forceinline__ uint32_t rope_e4m3x2(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// x / scale, correctly rounded, from y = 1/scale correctly rounded: q = x y is
+// within an ulp, the remainder x - q scale is exact in one fma, and q + r y
+// rounds to the quotient (Markstein, 1990; y's significand not all ones, no
+// underflow that e4m3 would see: the host checks the scale's range).  Beyond
+// e4m3's range, where r may overflow, q itself saturates the same; a zero q
+// keeps its sign.
+// rope_prompt (32768 tokens, e4m3) takes this instead of a division per value.
+__device__ __forceinline__ float rope_divide(float x, float scale, float y) {
+    const float q = x * y;
+    const float r = fmaf(-q, scale, x);
+    const float a = fabsf(q);
+    return a > 0.f && a < 1024.f ? fmaf(r, y, q) : q;
 }
 
 template <bool kBF16>
@@ -66,8 +80,8 @@ __device__ __forceinline__ void rope_store(uint8_t* dst, const float (&f)[8], bo
     uint32_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = inv != 0.f ? f[2 * i] * inv : __fdiv_rn(f[2 * i], scale);
-        const float b = inv != 0.f ? f[2 * i + 1] * inv : __fdiv_rn(f[2 * i + 1], scale);
+        const float a = inv != 0.f ? rope_divide(f[2 * i], scale, inv) : __fdiv_rn(f[2 * i], scale);
+        const float b = inv != 0.f ? rope_divide(f[2 * i + 1], scale, inv) : __fdiv_rn(f[2 * i + 1], scale);
         h[i] = rope_e4m3x2(a, b);
     }
     *reinterpret_cast<uint2*>(dst) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
@@ -169,11 +183,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopePara
     }
 }
 
-// 1/s when s is a power of two in the normal range (x * inv == x / s then), else 0
-static float exact_inverse(float s) {
+// 1/s, correctly rounded, where rope_divide is exact: s within 2^+-60 and its
+// significand not all ones; else 0 (an IEEE division per value).
+static float division_inverse(float s) {
     int e;
     const float m = frexpf(s, &e);
-    return (m == 0.5f && e > -120 && e < 120) ? 1.0f / s : 0.0f;
+    return e > -60 && e < 60 && m != 1.0f - 0x1p-24f ? 1.0f / s : 0.0f;
 }
 
 template <int D>
@@ -258,9 +273,9 @@ extern "C" pkd_status pkd_rope_cache_write(const void* q, int64_t q_stride, cons
     p.q_scale = q_scale;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
-    p.q_inv = pkd::exact_inverse(q_scale);
-    p.k_inv = pkd::exact_inverse(k_scale);
-    p.v_inv = pkd::exact_inverse(v_scale);
+    p.q_inv = pkd::division_inverse(q_scale);
+    p.k_inv = pkd::division_inverse(k_scale);
+    p.v_inv = pkd::division_inverse(v_scale);
     const bool q8 = num_heads > 0 && q_out_dtype == PKD_FP8_E4M3, kv8 = kv_dtype == PKD_FP8_E4M3;
     const cudaError_t e = head_dim == 128
         ? pkd::launch_rope<128>(p, num_tokens, in_dtype == PKD_BF16, q8, kv8, interleaved != 0, (cudaStream_t)stream)

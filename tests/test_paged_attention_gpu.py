@@ -86,7 +86,8 @@ def test_steps_with_split_keys(dtype, D, Hkv):
 
 # --------------------------------------------------------------- prompts
 @pytest.mark.parametrize("dtype,Hq,Hkv,D,P", [("bf16", 4, 1, 128, 16), ("fp16", 2, 2, 64, 64), ("bf16", 7, 1, 64, 48),
-                                              ("fp16", 8, 1, 128, 32), ("bf16", 1, 1, 128, 16)])
+                                              ("fp16", 8, 1, 128, 32), ("bf16", 1, 1, 128, 16), ("fp8", 4, 2, 128, 32),
+                                              ("fp8", 9, 1, 128, 16)])
 @pytest.mark.parametrize("mod", ["plain", "cap", "bias", "cap+bias", "window", "dense"])
 def test_prompts(dtype, Hq, Hkv, D, P, mod):
     lens = [1, 17, 129, 200, 333]
@@ -103,8 +104,9 @@ def test_prompts(dtype, Hq, Hkv, D, P, mod):
     verify(c, mod, **kw)
 
 
-def test_prompts_with_prefix_and_document_masks():
-    c = ref.Paged(lens=[300, 0, 260, 90], news=[290, 0, 40, 90], Hq=8, Hkv=2, D=128, seed=5, extra_tokens=3)
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_prompts_with_prefix_and_document_masks(dtype):
+    c = ref.Paged(lens=[300, 0, 260, 90], news=[290, 0, 40, 90], Hq=8, Hkv=2, D=128, dtype=dtype, seed=5, extra_tokens=3)
     verify(c, "prefix", prefix_lens=[100, 3, 250, 0])
     verify(c, "prefix+window", prefix_lens=[100, 3, 250, 60], window=30)
     rng = np.random.default_rng(1)
@@ -116,10 +118,10 @@ def test_prompts_with_prefix_and_document_masks():
     verify(c, "docs+cap", doc_start=doc, softcap=20.0)
 
 
-@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 1), (64, 12, 2)])
-def test_few_rows_over_many_keys_split(D, Hq, Hkv):
+@pytest.mark.parametrize("dtype,D,Hq,Hkv", [("bf16", 128, 8, 1), ("bf16", 64, 12, 2), ("fp8", 128, 8, 2)])
+def test_few_rows_over_many_keys_split(dtype, D, Hq, Hkv):
     """A small chunk of queries on a long context: the keys are split and merged."""
-    c = ref.Paged(lens=[3000, 1024, 40], news=[20, 5, 40], Hq=Hq, Hkv=Hkv, D=D, seed=2)
+    c = ref.Paged(lens=[3000, 1024, 40], news=[20, 5, 40], Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, seed=2)
     import paged_kv_decode_15_gb300 as pkd
     need = pkd.load_library().pkd_paged_attention_workspace_size(3, c.T, 40, Hq, Hkv, D, 16, 3008, pkd.BF16, None)
     assert need > (1 << 20) + 256 + c.T * Hq * D * 4  # partial results are planned
@@ -183,15 +185,16 @@ def test_padding_tokens_and_strided_queries(news):
     ref.check(out[:n].cpu(), lse[:n].cpu(), [x[:n] for x in r], "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
 @pytest.mark.parametrize("news", [[1, 1], [70, 40]])
-def test_bad_pages_are_skipped_and_reported(news):
+def test_bad_pages_are_skipped_and_reported(news, dtype):
     import paged_kv_decode_15_gb300 as pkd
-    c = ref.Paged(lens=[100, 90], news=news, Hq=4, Hkv=2, D=128, seed=11)
+    c = ref.Paged(lens=[100, 90], news=news, Hq=4, Hkv=2, D=128, dtype=dtype, seed=11)
     c.table[0, 2] = -1
     c.table[1, 0] = c.num_pages
     out, lse, status = run(c)
     assert status == pkd.EDEVICE_BOUNDS
-    ref.check(out, lse, c.reference(), "bf16")
+    ref.check(out, lse, c.reference(), dtype)
 
 
 def test_bad_lengths_and_starts_are_clamped_and_reported():

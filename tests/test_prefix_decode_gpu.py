@@ -78,7 +78,8 @@ class Shared:
 
 
 @pytest.mark.parametrize("dtype,Hq,Hkv,D,P,sq", [("bf16", 8, 2, 128, 16, 1), ("fp16", 4, 4, 64, 32, 2),
-                                                 ("bf16", 14, 2, 64, 48, 1), ("fp16", 16, 2, 128, 16, 4)])
+                                                 ("bf16", 14, 2, 64, 48, 1), ("fp16", 16, 2, 128, 16, 4),
+                                                 ("fp8", 8, 2, 128, 64, 1), ("fp8", 16, 2, 128, 16, 3)])
 @pytest.mark.parametrize("causal,cap", [(False, 0.0), (True, 8.0)])
 def test_groups(dtype, Hq, Hkv, D, P, sq, causal, cap):
     s = Shared(prefixes=[700, 1, 130], group_start=[0, 5, 6, 9], own=[sq, 70, 33, 5, 200, 17, 4, 16, 90], sq=sq, Hq=Hq,

@@ -134,3 +134,26 @@ def test_zero_angle_is_the_plain_cache_write():
         q = pkd.rope_cache_write(d[:, :4], d[:, 4:8], d[:, 8:], pos, table.cuda(), slots.cuda(), a, **scales)
         pkd.cache_write(d[:, 4:8], d[:, 8:], slots.cuda(), b, **scales)
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)) and torch.equal(q, d[:, :4])
+
+
+def test_every_16_bit_value_is_divided_as_by_the_plain_cache_write():
+    """All bit patterns of both types, scales of every kind: powers of two, ordinary
+    ones, a significand of all ones, and far ones (the IEEE division)."""
+    import paged_kv_decode_15_gb300 as pkd
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    table = torch.cat([torch.ones(1, 64), torch.zeros(1, 64)], -1).cuda()
+    pos, slots = torch.zeros(256, dtype=torch.int64, device="cuda"), torch.arange(256, device="cuda")
+    odd = float(np.float32(2.0) - np.float32(2.0 ** -23)) / 64
+    for dtype in (torch.bfloat16, torch.float16):
+        x = bits.view(dtype).view(256, 2, 128).cuda()
+        for ks, vs in ((0.0137, 1.0 / 64), (odd, 3.3e-7), (41.7, 2.0 ** -70), (2.0 ** 66 * 1.1, 1.0)):
+            a, b = (torch.zeros((16, 2, 16, 256), dtype=torch.uint8, device="cuda") for _ in range(2))
+            pkd.rope_cache_write(None, x, x, pos, table, slots, a, k_scale=ks, v_scale=vs)
+            pkd.cache_write(x, x, slots, b, k_scale=ks, v_scale=vs)
+            # values: the same bytes.  Keys went through x1 * 1 - x2 * 0: an infinity of the pair becomes NaN,
+            # and -0 - (-0) = +0 for x1 = -0, x2 < 0; so finite pairs are compared as numbers
+            f8 = [t.view(torch.float8_e4m3fn).float()[..., :128] for t in (a, b)]
+            fine = torch.stack([x.float()[..., :64], x.float()[..., 64:]], -1).isfinite().all(-1).repeat(1, 1, 2)
+            fine = fine.view(16, 16, 2, 128).transpose(1, 2)
+            values, keys = int((a != b)[..., 128:].sum()), int((f8[0] != f8[1])[fine].sum())
+            assert (values, keys) == (0, 0), (dtype, ks, vs, values, keys)

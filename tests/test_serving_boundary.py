@@ -115,7 +115,7 @@ def prefix(lib, **over):
 @pytest.mark.parametrize("over,code,needle", [
     (dict(groups=0), pkd.EINVAL, "groups"), (dict(groups=5000), pkd.EUNSUPPORTED, "groups"),
     (dict(sq=0), pkd.EINVAL, "sq"), (dict(max_prefix=(1 << 29) + 1, pstride=1 << 30), pkd.EUNSUPPORTED, "2^29"), (dict(cap=-1.0), pkd.EINVAL, "softcap"), (dict(pstride=6), pkd.EINVAL, "prefix_table"),
-    (dict(gstart=None), pkd.EINVAL, "group_start"), (dict(plens=None), pkd.EINVAL, "null"),
+    (dict(gstart=None, groups=2), pkd.EINVAL, "group_start"), (dict(plens=None), pkd.EINVAL, "null"),
     (dict(ws_bytes=1 << 20), pkd.EINVAL, "workspace"), (dict(flags=pkd.FLAG_GRID), pkd.EUNSUPPORTED, "FLAG_CAUSAL"),
     (dict(Hq=6, Hkv=4), pkd.EUNSUPPORTED, "multiple"), (dict(max_prefix=-1), pkd.EINVAL, "max_prefix_len")])
 def test_prefix_decode_refusals(lib, over, code, needle):
