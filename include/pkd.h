@@ -314,6 +314,10 @@ typedef struct {
     const int32_t* doc_start;
 } pkd_score_options;
 
+/* Bytes at the start of a workspace of pkd_paged_attention or pkd_prefix_decode
+ * that must be zero before its first use (the rest is written before it is read). */
+#define PKD_ATTENTION_WORKSPACE_HEAD (256 + 4 * 65536)
+
 /*
  * Workspace bytes of pkd_paged_attention, and the kernel it launches.  Host
  * only; the plan is fixed by these arguments (of the options: the window, and
@@ -344,8 +348,8 @@ const char* pkd_paged_attention_kernel_name(int batch, int64_t total_tokens, int
  *   out          device [total_tokens, num_heads, head_dim] contiguous, out_dtype
  *   lse          device fp32 [total_tokens, num_heads] natural-log LSE, or NULL
  *   workspace    at least pkd_paged_attention_workspace_size bytes, 256-byte
- *                aligned, zeroed once (pkd_workspace_init); every call leaves it
- *                ready for the next of this function or pkd_prefix_decode, whatever
+ *                aligned, its first PKD_ATTENTION_WORKSPACE_HEAD bytes zeroed once
+ *                (pkd_workspace_init); every call leaves it ready for the next of this function or pkd_prefix_decode, whatever
  *                its plan.  Calls that may overlap (streams, graphs) need one each.
  *                pkd_workspace_check reads its status word (PKD_EDEVICE_BOUNDS also
  *                for a query_start that falls, leaves [0, total_tokens] or holds
@@ -359,7 +363,7 @@ const char* pkd_paged_attention_kernel_name(int batch, int64_t total_tokens, int
  * a value that one token sees and another one does not must be finite for the
  * second (its weight there is 0).
  * Limits: head_dim 64 or 128; page_size a multiple of 16; num_heads/num_kv_heads
- * <= 128; batch <= 4096; max_kv_len <= 2^29; scale * q_scale * k_scale > 0; fp8
+ * <= 128; batch <= 4096, batch * num_kv_heads <= 65536; max_kv_len <= 2^29; scale * q_scale * k_scale > 0; fp8
  * caches need head_dim 128.
  */
 pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_stride, const void* kv_cache,

@@ -389,6 +389,7 @@ def _token_rows(t, shape, name):
 
 
 _call_ws: dict = {}
+_WS_HEAD = 256 + 4 * 65536  # PKD_ATTENTION_WORKSPACE_HEAD
 
 
 def _call_workspace(nbytes, index, stream):
@@ -397,12 +398,12 @@ def _call_workspace(nbytes, index, stream):
     (zeroed by the graph), so that two graphs never share one."""
     if torch.cuda.is_current_stream_capturing():
         ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
-        _check(load_library().pkd_workspace_init(ws.data_ptr(), nbytes, stream))
+        _check(load_library().pkd_workspace_init(ws.data_ptr(), _WS_HEAD, stream))
         return ws
     ws = _call_ws.get((index, stream))
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
-        _check(load_library().pkd_workspace_init(ws.data_ptr(), nbytes, stream))
+        _check(load_library().pkd_workspace_init(ws.data_ptr(), _WS_HEAD, stream))
         _call_ws[(index, stream)] = ws
     return ws
 

@@ -19,8 +19,9 @@ using pkd::report;
 // any plan that fits in it.
 constexpr size_t kHeader = 256;
 constexpr size_t kQueueWord[2] = {16, 32};
-constexpr int kMaxUnits = 1 << 18;
+constexpr int kMaxUnits = 1 << 16;
 constexpr size_t kPartials = kHeader + size_t(kMaxUnits) * 4;
+static_assert(kPartials == PKD_ATTENTION_WORKSPACE_HEAD, "the zeroed part");
 constexpr int kSms = 152;         // the plan is a host function: GB300's SM count
 constexpr int kStepCtas = 2048;   // as for the decode grid
 constexpr int kStepMaxChunk = 4096;
@@ -181,6 +182,7 @@ void fill(pkd::AttendParams& a, const AttendPlan& pl, uint8_t* ws, int pass, siz
         // c tanh(s / c) with s = scale q.k: e^{2 s / c} = 2^(q.k * cap_in)
         a.cap_in = 2.f * scale2 / softcap;
         a.cap_log2 = softcap * pkd::kLog2e;
+        a.cap_y = scale2 / (softcap * pkd::kLog2e);
     }
     a.wait_ns = pkd::kWaitNs;
 }

@@ -27,6 +27,8 @@
 // depend on who computes an item.  Every wait is bounded.
 #pragma once
 
+#include <type_traits>
+
 #include "attend.cuh"
 #include "tc05.cuh"
 
@@ -37,7 +39,12 @@ constexpr int kPtRows = 128;       // rows per tile (TMEM lanes)
 constexpr int kPtThreads = 512;
 constexpr int kPtItems = 4;        // work-item ring
 constexpr int kPtMaxBatch = 4096;  // requests whose tile prefix the CTA keeps in shared memory
-constexpr float kPtRescale = 8.f;  // log2 units: P stays below 2^8 between rescales
+constexpr int kPtL2Bytes = 64 << 20;  // keys and values walked together
+// A row's reference moves when its maximum has grown by more than this (log2
+// units).  The weights only must not overflow the operand type: bf16 has fp32's
+// range, fp16 ends at 2^16.  (With 2^8 for both, half of the key tiles of scores
+// with a spread of 3 made some warp repeat its pass.)
+constexpr float kPtRescaleBF16 = 40.f, kPtRescaleFP16 = 14.f;
 
 struct PtItem {
     int b, hk, q0, n, L, prefix;   // request, kv head, first query token, query tokens, length, prefix keys
@@ -89,6 +96,19 @@ struct PtShape {
     static_assert(SMEM > 114 * 1024, "one CTA per SM: all 512 TMEM columns are its own");
 };
 
+// 16-key stages of the tile from key tk whose page lies in the pool (items with a bad page only).
+__device__ __forceinline__ unsigned pt_stages(const AttendParams& p, const PtItem& I, int tk) {
+    const int32_t* table = p.block_table + static_cast<long long>(I.b) * p.bt_stride;
+    unsigned stages = 0;
+#pragma unroll 1
+    for (int s = 0; s < kPtKeys / kStageTok; ++s) {
+        const int k = tk + kStageTok * s;
+        const int pg = k < I.t1 ? table[page_div(k, p.pmagic, p.pmshift)] : -1;
+        if (pg >= 0 && pg < p.num_pages) stages |= 1u << s;
+    }
+    return stages;
+}
+
 __device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, const AttendParams& p) {
     return __all_sync(kFull, mbar_wait(bar, parity, p.status));
 }
@@ -111,6 +131,113 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "=f"(d.x), "=f"(d.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// What a softmax thread needs to turn its row's products into weights.
+struct PtScore {
+    float scale2, cap_in, cap_log2, cap_y;
+    float slope, base;   // bias: slope in log2 units; position - first key of the tile
+    int c0, c1;          // keys [c0, c1) of the tile are seen
+    unsigned stages;     // 16-key stages whose page is in the pool
+};
+
+template <bool kMasked>
+__device__ __forceinline__ bool pt_seen(const PtScore& w, int k) {
+    return !kMasked || (k >= w.c0 && k < w.c1 && (w.stages >> (k >> 4) & 1));
+}
+
+// The reference a row starts from: the largest logit among 32 keys.
+template <bool kBias, bool kCap, bool kMasked>
+__device__ __forceinline__ float pt_top(const uint32_t (&s)[32], int k0, const PtScore& w, float top) {
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+        float a = __uint_as_float(s[c]), b = __uint_as_float(s[c + 1]);
+        if constexpr (kBias) {
+            // (capped logits are below q.k scaled by as much as the reference may lie off,
+            // so with a bias the cap counts)
+            a = kCap ? capped(a, w.cap_in, w.cap_log2) : a * w.scale2;
+            b = kCap ? capped(b, w.cap_in, w.cap_log2) : b * w.scale2;
+            a = fmaf(-w.slope, fabsf(w.base - static_cast<float>(k0 + c)), a);
+            b = fmaf(-w.slope, fabsf(w.base - static_cast<float>(k0 + c + 1)), b);
+        }
+        top = max3(top, pt_seen<kMasked>(w, k0 + c) ? a : -INFINITY, pt_seen<kMasked>(w, k0 + c + 1) ? b : -INFINITY);
+    }
+    return top;
+}
+
+// The weights 2^(x - m) of 32 keys (k0 .. k0 + 31 of the tile) from their
+// products s, packed to the operand type, with their fp32 sum and the running
+// maximum: of q.k (the logit rises with it), with a bias of x - m.
+// Capped logits, kPoly: c tanh(y), y = scale q.k / c, as q.k scaled times P(y^2),
+// P of degree 5 interpolating tanh(y)/y at the Chebyshev points of y^2 in [0, 0.5]
+// (tanh off by 8e-8 at most in fp32), all on packed FMAs; `far` keeps the largest
+// |q.k|, and a tile with |y| > 0.7 is done again by exponential and reciprocal
+// (capped(): three special-function results per key instead of one).
+// A bias is linear in the key where no key lies behind its row's position
+// (unmasked tiles); masked tiles take the distance's magnitude.
+template <bool kBF16, bool kCap, bool kPoly, bool kBias, bool kMasked>
+__device__ __forceinline__ void pt_weights(const uint32_t (&s)[32], uint32_t* pk, int k0, const PtScore& w, float m,
+                                           float2 (&sum)[2], float& top, float& far) {
+    const float nb = kBias ? -w.slope * w.base - m : 0.f;
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+        const int k = k0 + c;
+        const float2 qk = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        float2 add = both(-m), x;  // what the scaled score needs to be the exponent
+        if constexpr (kBias) {
+            if constexpr (kMasked)
+                add = make_float2(fmaf(-w.slope, fabsf(w.base - static_cast<float>(k)), -m),
+                                  fmaf(-w.slope, fabsf(w.base - static_cast<float>(k + 1)), -m));
+            else
+                add = make_float2(fmaf(w.slope, static_cast<float>(k), nb), fmaf(w.slope, static_cast<float>(k + 1), nb));
+        }
+        if constexpr (kCap && kPoly) {
+            const float2 y = mul2(qk, both(w.cap_y)), z = mul2(y, y);
+            float2 t = fma2(z, both(-0.0050308364f), both(0.019959657f));
+            t = fma2(z, t, both(-0.05350069f));
+            t = fma2(z, t, both(0.13328016f));
+            t = fma2(z, t, both(-0.33333108f));
+            t = fma2(z, t, both(1.0f));
+            x = fma2(t, mul2(qk, both(w.scale2)), add);
+            far = max3(far, fabsf(qk.x), fabsf(qk.y));
+        } else if constexpr (kCap) {
+            x = add2(make_float2(capped(qk.x, w.cap_in, w.cap_log2), capped(qk.y, w.cap_in, w.cap_log2)), add);
+        } else {
+            x = fma2(qk, both(w.scale2), add);
+        }
+        if constexpr (kMasked) {
+            x.x = pt_seen<kMasked>(w, k) ? x.x : -INFINITY;
+            x.y = pt_seen<kMasked>(w, k + 1) ? x.y : -INFINITY;
+        }
+        if constexpr (kBias)
+            top = max3(top, x.x, x.y);
+        else if constexpr (kMasked)
+            top = max3(top, pt_seen<kMasked>(w, k) ? qk.x : -INFINITY, pt_seen<kMasked>(w, k + 1) ? qk.y : -INFINITY);
+        else
+            top = max3(top, qk.x, qk.y);
+        x.x = fast_exp2(x.x);
+        x.y = fast_exp2(x.y);
+        // l sums the fp32 weights; the product takes them rounded to the operand type
+        sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], x);
+        pk[c >> 1] = pack2<kBF16>(x.x, x.y);
+    }
 }
 
 template <int N>
@@ -207,7 +334,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
         }
         for (int i = 0; i < kPtItems; ++i) {
             mbar_init(bar(S::B_IF + i), 1);
-            mbar_init(bar(S::B_IE + i), 1 + 8 + 4 + (kFp8 ? 2 : 0));  // the issuing thread; softmax, epilogue, widening warps
+            mbar_init(bar(S::B_IE + i), 1 + 8 + 4 + (kFp8 ? 2 : 0));  // the issuing warp; softmax, epilogue, widening warps
         }
         mbar_init(bar(S::B_DR), 1);
         fence_barrier_init();
@@ -282,8 +409,10 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     __syncwarp();
                     break;
                 }
-                // item idx: splits innermost, then the row tiles of a (request, kv
-                // head) from the last (the longest, causal) to the first
+                // item idx: splits innermost; within a request groups of kv heads
+                // whose keys and values fit half of L2 together, in each the row tiles
+                // from the last (the longest, causal) to the first, all heads of the
+                // group per tile -- the short items come last
                 const int split = idx % p.max_splits, r1 = idx / p.max_splits;
                 int lo_b = 0, hi_b = p.B;
                 while (hi_b - lo_b > 1) {
@@ -291,10 +420,12 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     if (static_cast<long long>(pref[mid]) * p.Hkv <= r1) lo_b = mid; else hi_b = mid;
                 }
                 const int b = lo_b, npair = pref[b + 1] - pref[b], r2 = r1 - pref[b] * p.Hkv;
-                const int hk = r2 / npair, pair = npair - 1 - (r2 - hk * npair);
                 int q0, n;
                 request_tokens(p, b, q0, n, false);
-                const int L = request_len(p, b, pair == 0 && hk == 0 && split == 0 && lane == 0);
+                const int L = request_len(p, b, r2 == 0 && split == 0 && lane == 0);
+                const int group = max(1, min(p.Hkv, kPtL2Bytes / (2 * S::ROWB) / max(L, 1)));
+                const int g = r2 / (npair * group), width = min(group, p.Hkv - g * group), r3 = r2 - g * npair * group;
+                const int pair = npair - 1 - r3 / width, hk = g * group + r3 % width;
                 const int prefix = p.prefix_lens ? p.prefix_lens[b] : 0;
                 const int tok0 = pair * 2 * TOK;
                 int lo[2], hi[2];
@@ -403,90 +534,102 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             }
         } else if (warp == 13) {
             // --------------------------------------------------- products
-            if (lane == 0) {
-                bool ok = true;
-                int u = 0, nq = 0, nv = 0;  // nv: widened V tiles
-                int np[2] = {0, 0}, no[2] = {0, 0};  // P tiles consumed, accumulations begun
-                for (int it = 0; ok; ++it) {
-                    const int slot = it % kPtItems;
-                    if (!mbar_wait(bar(S::B_IF + slot), (it / kPtItems) & 1, p.status)) { ok = false; break; }
-                    const PtItem& I = items[slot];
-                    if (I.end) break;
-                    const int ntiles = I.ntiles;
-                    const int jb[2] = {I.jb[0], I.jb[1]}, je[2] = {I.je[0], I.je[1]};
-                    mbar_arrive(bar(S::B_IE + slot));
-                    if (!ntiles) continue;
-                    if (!mbar_wait(bar(S::B_QF), nq & 1, p.status)) { ok = false; break; }
-                    ++nq;
-                    auto k_ready = [&](int j) {
-                        const int x = u + 2 * j;
-                        return mbar_wait(bar(S::B_UF + x % S::NU), (x / S::NU) & 1, p.status);
-                    };
-                    auto qk = [&](int t, int j) {
-                        const uint32_t k = sb0 + S::OFF_KV + ((u + 2 * j) % S::NU) * S::UNIT;
-                        const uint32_t q = sb0 + S::OFF_Q + t * S::QTILE;
+            // The whole warp walks the items, converged, so that descriptors stay in
+            // uniform registers; one elected lane issues (with the loop under a lane
+            // test instead, a product took 115 cycles to issue, twice its run time).
+            const bool one = tc05::elect_one();
+            bool ok = true;
+            int u = 0, nq = 0, nv = 0;  // nv: widened V tiles
+            int np[2] = {0, 0}, no[2] = {0, 0};  // P tiles consumed, accumulations begun
+            for (int it = 0; ok; ++it) {
+                const int slot = it % kPtItems;
+                if (!pt_wait(bar(S::B_IF + slot), (it / kPtItems) & 1, p)) { ok = false; break; }
+                const PtItem& I = items[slot];
+                if (I.end) break;
+                const int ntiles = I.ntiles;
+                const int jb[2] = {I.jb[0], I.jb[1]}, je[2] = {I.je[0], I.je[1]};
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S::B_IE + slot));
+                if (!ntiles) continue;
+                if (!pt_wait(bar(S::B_QF), nq & 1, p)) { ok = false; break; }
+                ++nq;
+                auto k_ready = [&](int j) {
+                    const int x = u + 2 * j;
+                    return pt_wait(bar(S::B_UF + x % S::NU), (x / S::NU) & 1, p);
+                };
+                auto qk = [&](int t, int j) {
+                    const uint64_t qd = tc05::smem_desc(sb0 + S::OFF_Q + t * S::QTILE, 16, 1024);
+                    const uint64_t kd = tc05::smem_desc(sb0 + S::OFF_KV + ((u + 2 * j) % S::NU) * S::UNIT, 16, S::GROUP);
 #pragma unroll
-                        for (int kk = 0; kk < S::ROWB / 32; ++kk) {
-                            const uint64_t qd = tc05::smem_desc(q + (kk >> 2) * kPtRows * 128 + (kk & 3) * 32, 16, 1024);
-                            const uint64_t kd = tc05::smem_desc(k + (kk >> 2) * 1024 + (kk & 3) * 32, 16, S::GROUP);
-                            if constexpr (kFp8)
-                                tc05::mma_e4m3(tmem + kPtKeys * t, qd, kd, kIdS, kk > 0);
-                            else
-                                tc05::mma_f16(tmem + kPtKeys * t, qd, kd, kIdS, kk > 0);
-                        }
-                        tc05::commit(bar(S::B_SF + t));
-                    };
-                    ok = k_ready(0);
-                    tc05::fence_after_sync();
-                    for (int t = 0; ok && t < 2; ++t)
-                        if (jb[t] == 0 && je[t] > 0) qk(t, 0);
-                    tc05::commit(bar(S::B_UE + u % S::NU));
-                    for (int j = 0; ok && j < ntiles; ++j) {
-                        const int vu = u + 2 * j + 1, vb = kFp8 ? (nv + j) % 2 : 0;
-                        ok = kFp8 ? mbar_wait(bar(S::B_VF + vb), ((nv + j) >> 1) & 1, p.status)
-                                  : mbar_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p.status);
-                        const uint32_t v = sb0 + (kFp8 ? S::OFF_V + vb * S::VUNIT : S::OFF_KV + (vu % S::NU) * S::UNIT);
-                        const uint32_t v_free = kFp8 ? bar(S::B_VE + vb) : bar(S::B_UE + vu % S::NU);
-                        bool have_k = false;
-                        for (int t = 0; ok && t < 2; ++t) {
-                            if (j >= jb[t] && j < je[t]) {
-                                ok = mbar_wait(bar(S::B_PF + t), np[t] & 1, p.status);
-                                ++np[t];
-                                if (ok && j == jb[t]) {
-                                    // a new accumulation: the epilogue has drained the last one
-                                    if (no[t] >= 1) ok = mbar_wait(bar(S::B_OE + t), (no[t] - 1) & 1, p.status);
-                                    ++no[t];
-                                }
-                                if (!ok) break;
-                                tc05::fence_after_sync();
+                    for (int kk = 0; kk < S::ROWB / 32; ++kk) {
+                        const uint64_t qk_ = qd + (((kk >> 2) * kPtRows * 128 + (kk & 3) * 32) >> 4);
+                        const uint64_t kk_ = kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
+                        if (!one) continue;
+                        if constexpr (kFp8)
+                            tc05::mma_e4m3(tmem + kPtKeys * t, qk_, kk_, kIdS, kk > 0);
+                        else
+                            tc05::mma_f16(tmem + kPtKeys * t, qk_, kk_, kIdS, kk > 0);
+                    }
+                    if (one) tc05::commit(bar(S::B_SF + t));
+                };
+                ok = k_ready(0);
+                tc05::fence_after_sync();
+                for (int t = 0; ok && t < 2; ++t)
+                    if (jb[t] == 0 && je[t] > 0) qk(t, 0);
+                if (one) tc05::commit(bar(S::B_UE + u % S::NU));
+                for (int j = 0; ok && j < ntiles; ++j) {
+                    const int vu = u + 2 * j + 1, vb = kFp8 ? (nv + j) % 2 : 0;
+                    ok = kFp8 ? pt_wait(bar(S::B_VF + vb), ((nv + j) >> 1) & 1, p)
+                              : pt_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p);
+                    const uint64_t vd = tc05::smem_desc(
+                        sb0 + (kFp8 ? S::OFF_V + vb * S::VUNIT : S::OFF_KV + (vu % S::NU) * S::UNIT), 1024, S::VGROUP);
+                    const uint32_t v_free = kFp8 ? bar(S::B_VE + vb) : bar(S::B_UE + vu % S::NU);
+                    bool have_k = false;
 #pragma unroll
-                                for (int kk = 0; kk < kPtKeys / 16; ++kk)
+                    for (int t = 0; t < 2; ++t) {
+                        if (!ok) break;
+                        if (j >= jb[t] && j < je[t]) {
+                            ok = pt_wait(bar(S::B_PF + t), np[t] & 1, p);
+                            ++np[t];
+                            if (ok && j == jb[t]) {
+                                // a new accumulation: the epilogue has drained the last one
+                                if (no[t] >= 1) ok = pt_wait(bar(S::B_OE + t), (no[t] - 1) & 1, p);
+                                ++no[t];
+                            }
+                            if (!ok) break;
+                            tc05::fence_after_sync();
+                            const bool more = j > jb[t];
+#pragma unroll
+                            for (int kk = 0; kk < kPtKeys / 16; ++kk)
+                                if (one)
                                     tc05::mma_f16_ts(tmem + 256 + D * t, tmem + kPtKeys * t + 8 * kk,
-                                                     tc05::smem_desc(v + 2 * kk * S::VGROUP, 1024, S::VGROUP), kIdO,
-                                                     j > jb[t] || kk > 0);
+                                                     vd + ((2 * kk * S::VGROUP) >> 4), kIdO, more || kk > 0);
+                            if (one) {
                                 tc05::commit(bar(S::B_OD + t));
                                 if (j == je[t] - 1) tc05::commit(bar(S::B_OF + t));
                             }
-                            if (t == 1) tc05::commit(v_free);
-                            if (j + 1 < ntiles) {
-                                if (!have_k) {
-                                    ok = k_ready(j + 1);
-                                    have_k = true;
-                                    if (!ok) break;
-                                    tc05::fence_after_sync();
-                                }
-                                // in issue order behind this tile's O product, which has read the P under S
-                                if (j + 1 >= jb[t] && j + 1 < je[t]) qk(t, j + 1);
-                                if (t == 1) tc05::commit(bar(S::B_UE + (u + 2 * (j + 1)) % S::NU));
+                        }
+                        if (t == 1 && one) tc05::commit(v_free);
+                        if (j + 1 < ntiles) {
+                            if (!have_k) {
+                                ok = k_ready(j + 1);
+                                have_k = true;
+                                if (!ok) break;
+                                tc05::fence_after_sync();
                             }
+                            // in issue order behind this tile's O product, which has read the P under S
+                            if (j + 1 >= jb[t] && j + 1 < je[t]) qk(t, j + 1);
+                            if (t == 1 && one) tc05::commit(bar(S::B_UE + (u + 2 * (j + 1)) % S::NU));
                         }
                     }
-                    tc05::commit(bar(S::B_QE));
-                    u += 2 * ntiles;
-                    nv += ntiles;
                 }
-                if (!ok) atomicOr(p.status, kErrTimeout);
-                // every product issued has completed before TMEM is freed
+                if (one) tc05::commit(bar(S::B_QE));
+                u += 2 * ntiles;
+                nv += ntiles;
+            }
+            if (!ok && one) atomicOr(p.status, kErrTimeout);
+            // every product issued has completed before TMEM is freed
+            if (one) {
                 tc05::commit(bar(S::B_DR));
                 mbar_wait(bar(S::B_DR), 0);
             }
@@ -575,62 +718,105 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                 const int pos = I.L - I.n + tok;
                 if constexpr (kBias)
                     if (valid) slope = p.slopes[I.hk * G + rg] * kLog2e;
+                const int bad = I.bad, lo_all = I.lo_all, hi_all = min(I.hi_all, I.t1);
+                // key tiles [zl, zh) need no V row zeroed by this tile, [ml, mh) no mask
+                // (bias: and lie before every row's position)
                 const bool lead = t == 0 || !(I.jb[0] < I.je[0]);  // zeroes V rows of tiles that both walk
-                const int jb0 = I.jb[0], je0 = I.je[0], bad = I.bad, lo_all = I.lo_all, hi_all = min(I.hi_all, I.t1);
-                const int32_t* table = p.block_table + static_cast<long long>(I.b) * p.bt_stride;
+                const int jb0 = I.jb[0], je0 = I.je[0];
+                const int zl = lo_all > t0 ? 1 : 0, zh = bad ? 0 : (hi_all - t0) / kPtKeys;
+                int ml, mh;
+                {
+                    int l0 = valid ? lo : 0, h0 = valid ? min(hi, hi_all) : 0x7fffffff;
+                    if (kBias && valid) h0 = min(h0, pos + 1);
+                    ml = (__reduce_max_sync(kFull, l0) - t0 + kPtKeys - 1) / kPtKeys;
+                    mh = bad ? 0 : (__reduce_min_sync(kFull, h0) - t0) / kPtKeys;  // below 0: rounded up, still masked
+                    if (__reduce_min_sync(kFull, h0) < t0) mh = 0;
+                }
                 float m_used = -INFINITY, l = 0.f;
+                bool wide = false;  // capped: some |y| was above the polynomial's range
                 for (int j = jb; j < je; ++j, ++ns) {
                     const int tk = t0 + j * kPtKeys;
                     if (!pt_wait(bar(S::B_SF + t), ns & 1, p)) { ok = false; break; }
-                    unsigned stages = 0xff;  // 16-key stages whose page is in the pool
-                    if (bad) {
-                        stages = 0;
-                        for (int s = 0; s < 8; ++s) {
-                            const int k = tk + 16 * s;
-                            const int pg = k < I.t1 ? table[page_div(k, p.pmagic, p.pmshift)] : -1;
-                            if (pg >= 0 && pg < p.num_pages) stages |= 1u << s;
-                        }
-                    }
                     if (warp_on) {
                         tc05::fence_after_sync();
-                        uint32_t sr[4][32];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) tc05::ld_32x32b_x32(s_addr + 32 * c, sr[c]);
-                        tc05::wait_ld();
-                        const float scale2 = (kCap || kBias) ? 1.f : p.scale_log2;
-                        if constexpr (kCap || kBias) {
-#pragma unroll
-                            for (int c = 0; c < 128; ++c) {
-                                float x = __uint_as_float(sr[c >> 5][c & 31]);
-                                x = kCap ? capped(x, p.cap_in, p.cap_log2) : x * p.scale_log2;
-                                if constexpr (kBias) x = fmaf(-slope, fabsf(static_cast<float>(pos - tk - c)), x);
-                                sr[c >> 5][c & 31] = __float_as_uint(x);
+                        PtScore w{p.scale_log2, p.cap_in, p.cap_log2, p.cap_y, slope, static_cast<float>(pos - tk),
+                                  lo - tk, min(hi, hi_all) - tk, bad ? pt_stages(p, I, tk) : 0xffu};
+                        const bool masked = j < ml || j >= mh;
+                        uint32_t a[32], b[32];
+                        if (j == jb) {
+                            // the row's first reference: its maximum over the tile
+                            float top = -INFINITY;
+                            auto tops = [&](auto mask) {
+                                constexpr bool kMasked = decltype(mask)::value;
+                                tc05::ld_32x32b_x32(s_addr, a);
+                                tc05::wait_ld(a);
+                                tc05::ld_32x32b_x32(s_addr + 32, b);
+                                top = pt_top<kBias, kCap, kMasked>(a, 0, w, top);
+                                tc05::wait_ld(b);
+                                tc05::ld_32x32b_x32(s_addr + 64, a);
+                                top = pt_top<kBias, kCap, kMasked>(b, 32, w, top);
+                                tc05::wait_ld(a);
+                                tc05::ld_32x32b_x32(s_addr + 96, b);
+                                top = pt_top<kBias, kCap, kMasked>(a, 64, w, top);
+                                tc05::wait_ld(b);
+                                top = pt_top<kBias, kCap, kMasked>(b, 96, w, top);
+                            };
+                            if (masked)
+                                tops(std::true_type{});
+                            else
+                                tops(std::false_type{});
+                            m_used = kBias || top == -INFINITY ? top
+                                     : kCap ? capped(top, p.cap_in, p.cap_log2) : top * p.scale_log2;
+                        }
+                        // one pass: weights against the reference, the tile's maximum beside
+                        // them.  Where a row's maximum has outgrown the reference (or a capped
+                        // score the polynomial) the pass is repeated, O and l rescaled.
+                        uint32_t pk[64];
+                        float2 sum[2];
+#pragma unroll 1
+                        for (;;) {
+                            const float m = m_used == -INFINITY ? 0.f : m_used;
+                            float top = -INFINITY, far = 0.f;
+                            sum[0] = sum[1] = make_float2(0.f, 0.f);
+                            auto pass = [&](auto poly, auto mask) {
+                                constexpr bool kPoly = decltype(poly)::value, kMasked = decltype(mask)::value;
+                                tc05::ld_32x32b_x32(s_addr, a);
+                                tc05::wait_ld(a);
+                                tc05::ld_32x32b_x32(s_addr + 32, b);
+                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(a, pk, 0, w, m, sum, top, far);
+                                tc05::wait_ld(b);
+                                tc05::ld_32x32b_x32(s_addr + 64, a);
+                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(b, pk + 16, 32, w, m, sum, top, far);
+                                tc05::wait_ld(a);
+                                tc05::ld_32x32b_x32(s_addr + 96, b);
+                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(a, pk + 32, 64, w, m, sum, top, far);
+                                tc05::wait_ld(b);
+                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(b, pk + 48, 96, w, m, sum, top, far);
+                            };
+                            if (kCap && (wide || masked))
+                                pass(std::false_type{}, std::true_type{});
+                            else if (masked)
+                                pass(std::true_type{}, std::true_type{});
+                            else
+                                pass(std::true_type{}, std::false_type{});
+                            if constexpr (kCap) {
+                                // (far stays 0 in a pass that does not depend on it)
+                                if (__any_sync(kFull, far * p.cap_y > 0.7f)) {
+                                    wide = true;
+                                    continue;
+                                }
                             }
-                        }
-                        const int c0 = lo - tk, c1 = min(hi, hi_all) - tk;
-                        if (__any_sync(kFull, valid && (c0 > 0 || c1 < kPtKeys)) || bad) {
-#pragma unroll
-                            for (int c = 0; c < 128; ++c)
-                                if (c < c0 || c >= c1 || !(stages >> (c >> 4) & 1))
-                                    sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
-                        }
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(sr[k][c]));
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
-                        const bool need = top > m_used + kPtRescale;
-                        if (__any_sync(kFull, need)) {
-                            // the rows that need it take the new maximum as reference; O and l follow
-                            const float m_new = need ? top : m_used;
-                            const float alpha = need ? fast_exp2(m_used - m_new) : 1.f;
-                            m_used = m_new;
+                            top = kBias ? top + m
+                                  : top == -INFINITY ? top : kCap ? capped(top, p.cap_in, p.cap_log2) : top * p.scale_log2;
+                            const bool need = top > m_used + (kBF16 ? kPtRescaleBF16 : kPtRescaleFP16);
+                            if (!__any_sync(kFull, need)) break;
+                            const float alpha = need ? fast_exp2(m_used - top) : 1.f;
+                            if (need) m_used = top;
                             l *= alpha;
                             if (j > jb) {
                                 if (!pt_wait(bar(S::B_OD + t), (ns - 1) & 1, p)) { ok = false; break; }
                                 tc05::fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                                 for (int c = 0; c < D; c += 16) {
                                     uint32_t o[16];
                                     tc05::ld_32x32b_x16(o_addr + c, o);
@@ -642,36 +828,18 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                                 tc05::wait_st();
                             }
                         }
-                        const float m_sub = m_used == -INFINITY ? 0.f : m_used;
-                        const float2 sc = make_float2(scale2, scale2), ms = make_float2(-m_sub, -m_sub);
-                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t pk[32];
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                const int k = 64 * h + 2 * c;
-                                float2 x = make_float2(__uint_as_float(sr[k >> 5][k & 31]),
-                                                       __uint_as_float(sr[k >> 5][(k & 31) + 1]));
-                                x = fma2(x, sc, ms);
-                                x.x = fast_exp2(x.x);
-                                x.y = fast_exp2(x.y);
-                                // l sums the fp32 weights; the product takes them rounded to the operand type
-                                sum[c & 1] = add2(sum[c & 1], x);
-                                pk[c] = pack2<kBF16>(x.x, x.y);
-                            }
-                            tc05::st_32x32b_x32(s_addr + 32 * h, pk);
-                        }
+                        if (!ok) break;
+                        tc05::st_32x32b_x32(s_addr, reinterpret_cast<const uint32_t(&)[32]>(pk[0]));
+                        tc05::st_32x32b_x32(s_addr + 32, reinterpret_cast<const uint32_t(&)[32]>(pk[32]));
                         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                         tc05::wait_st();
                     }
                     // V rows that no row of the unit sees (stale slots, skipped pages)
                     // are zeroed: their weight 0 must not meet a NaN
-                    const bool zeroes = !kFp8 && (lead || j < jb0 || j >= je0);
-                    if (zeroes && (bad || tk < lo_all || tk + kPtKeys > hi_all)) {
+                    if (!kFp8 && (j < zl || j >= zh) && (lead || j < jb0 || j >= je0)) {
                         const int vu = u + 2 * j + 1, key = tk + r;
                         if (!pt_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p)) { ok = false; break; }
-                        if (key < lo_all || key >= hi_all || !(stages >> (r >> 4) & 1)) {
+                        if (key < lo_all || key >= hi_all || (bad && !(pt_stages(p, I, tk) >> (r >> 4) & 1))) {
                             uint8_t* vrow = smem + S::OFF_KV + (vu % S::NU) * S::UNIT + (r >> 3) * S::GROUP + (r & 7) * 128;
 #pragma unroll
                             for (int h = 0; h < S::REGIONS; ++h)

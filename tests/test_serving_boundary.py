@@ -98,7 +98,7 @@ def test_plans_and_kernel_choice(lib):
     assert size(4, 4, 1, 32, 8, 128, 16, 131072, pkd.BF16, pkd.ScoreOptions(0.0, None, 512, None, None)) < whole
     assert size(4, 4, 1, 32, 8, 128, 16, 131072, pkd.BF16, pkd.ScoreOptions(0.0, None, 512, 0x10000, None)) == whole
     # prompts that fill the GPU are not split: no partial results
-    base = (1 << 20) + 256
+    base = 256 + 4 * 65536
     assert size(8, 20000, 4000, 32, 8, 128, 16, 8192, pkd.BF16, None) == base
     assert size(1, 64, 64, 8, 1, 128, 16, 65536, pkd.BF16, None) > base
 
