@@ -363,7 +363,7 @@ const char* pkd_paged_attention_kernel_name(int batch, int64_t total_tokens, int
  * a value that one token sees and another one does not must be finite for the
  * second (its weight there is 0).
  * Limits: head_dim 64 or 128; page_size a multiple of 16; num_heads/num_kv_heads
- * <= 128; batch <= 4096, batch * num_kv_heads <= 65536; max_kv_len <= 2^29; scale * q_scale * k_scale > 0; fp8
+ * <= 128; batch <= 2048, batch * num_kv_heads <= 65536; max_kv_len <= 2^29; scale * q_scale * k_scale > 0; fp8
  * caches need head_dim 128.
  */
 pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_stride, const void* kv_cache,
@@ -395,7 +395,7 @@ pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_strid
  *
  * The workspace is as for pkd_paged_attention.  max_prefix_len and max_kv_len
  * bound prefix_lens and seq_lens.  Limits as for
- * pkd_paged_attention, groups <= 4096.
+ * pkd_paged_attention, groups <= 2048.
  */
 size_t pkd_prefix_decode_workspace_size(int batch, int sq, int num_heads, int num_kv_heads, int head_dim,
                                         int page_size, int groups, int max_prefix_len, int max_kv_len,

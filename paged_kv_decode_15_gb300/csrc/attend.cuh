@@ -36,7 +36,7 @@ struct AttendParams {
     int pmshift;
     float scale_log2;             // logit = q.k * scale_log2 (log2 units), without a cap
     float cap_in, cap_log2;       // with one: cap_log2 * tanh(q.k * cap_in / (2 log2 e)); cap_log2 = 0: none
-    float cap_y;                  // scale / cap: the tanh's argument per q.k
+    float cap_c[5], cap_far;      // the capped logit as q.k times a polynomial in (q.k)^2, for |q.k| <= cap_far
     float v_scale;
     uint64_t wait_ns;
 };

@@ -98,7 +98,8 @@ pkd_status plan_attend(int B, long long T, int max_q, int Hq, int Hkv, int D, in
     // the keys are split while the row tiles alone leave SMs idle: about two
     // items per SM, chunks of whole tiles, at least 512 keys (256 for partials,
     // whose join is a launch of its own)
-    long long splits = least * Hkv >= kSms ? 1 : (2 * kSms + least * Hkv - 1) / (least * Hkv);
+    // (partials: one item per SM, a shared prefix's items being alike)
+    long long splits = least * Hkv >= kSms ? 1 : partials ? kSms / (least * Hkv) : (2 * kSms + least * Hkv - 1) / (least * Hkv);
     const long long floor_chunk = partials ? 256 : 512;
     long long chunk = std::max((vis + splits - 1) / splits, floor_chunk);
     chunk = (chunk + pkd::kPtKeys - 1) / pkd::kPtKeys * pkd::kPtKeys;
@@ -182,7 +183,15 @@ void fill(pkd::AttendParams& a, const AttendPlan& pl, uint8_t* ws, int pass, siz
         // c tanh(s / c) with s = scale q.k: e^{2 s / c} = 2^(q.k * cap_in)
         a.cap_in = 2.f * scale2 / softcap;
         a.cap_log2 = softcap * pkd::kLog2e;
-        a.cap_y = scale2 / (softcap * pkd::kLog2e);
+        // tanh(y) = y P(y^2) for |y| <= 0.6, P interpolating tanh(y)/y at the five
+        // Chebyshev points of y^2 in [0, 0.36] (off by 4e-8 at most); y = k q.k, and k
+        // and the scale go into the coefficients where they stay in fp32's range
+        static const double c[5] = {0.99999992596295, -0.3333230204036953, 0.1331006442560933, -0.05209665340812269,
+                                    0.015468751301830112};
+        const double k = (double)scale2 / ((double)softcap * pkd::kLog2e);
+        double power = scale2;
+        for (int i = 0; i < 5; ++i, power *= k * k) a.cap_c[i] = (float)(c[i] * power);
+        a.cap_far = k > 2e-4 && k < 1e3 && scale2 > 1e-6f && scale2 < 1e6f ? (float)(0.6 / k) : -1.f;
     }
     a.wait_ns = pkd::kWaitNs;
 }

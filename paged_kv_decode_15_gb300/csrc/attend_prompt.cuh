@@ -16,12 +16,13 @@
 // tensor cores work on the other's products: a key tile of both costs
 // 2 x (S + O) = 4 products of 128x128xD against one softmax pass per tile.
 //
-// Warp roles (512 threads): warps 0-3 and 4-7 the softmax of tile 0 and 1, warps
-// 8-11 the epilogue (O out of TMEM, normalised, written -- or a partial result
-// when the keys are split), warp 12 loads (work items, Q, K, V by TMA), warp 13
-// issues the products; for e4m3 caches S is an e4m3 product and warps 14-15 widen
+// Warp roles (384 threads): warps 0-3 and 4-7 the softmax of tile 0 and 1 and, at an
+// item's end, its epilogue (O out of TMEM, normalised, written -- or a partial
+// result when the keys are split), warp 8 loads (work items, Q, K, V by TMA), warp
+// 9 issues the products; for e4m3 caches S is an e4m3 product and warps 10-11 widen
 // V to fp16 in shared memory ahead of the O product (P is rounded to fp16 then).
-// Registers follow the roles (setmaxnreg).
+// Registers follow the roles (setmaxnreg).  (An epilogue group of its own left the
+// softmax 176 registers and spills: 8192-token prompt 523 us.)
 // Work items are handed out by an atomic counter in the workspace, the longest of
 // a request first, so CTAs finish together whatever the lengths; results do not
 // depend on who computes an item.  Every wait is bounded.
@@ -36,9 +37,9 @@ namespace pkd {
 
 constexpr int kPtKeys = 128;       // keys per tile
 constexpr int kPtRows = 128;       // rows per tile (TMEM lanes)
-constexpr int kPtThreads = 512;
+constexpr int kPtThreads = 384;
 constexpr int kPtItems = 4;        // work-item ring
-constexpr int kPtMaxBatch = 4096;  // requests whose tile prefix the CTA keeps in shared memory
+constexpr int kPtMaxBatch = 2048;  // requests whose tile prefix the CTA keeps in shared memory
 constexpr int kPtL2Bytes = 64 << 20;  // keys and values walked together
 // A row's reference moves when its maximum has grown by more than this (log2
 // units).  The weights only must not overflow the operand type: bf16 has fp32's
@@ -79,16 +80,15 @@ struct PtShape {
     static constexpr int OFF_V = NU * UNIT;
     static constexpr int OFF_Q = OFF_V + NV * VUNIT;
     static_assert(NU % 2 == 0 && (!FP8 || D == 128), "unit parity; e4m3 rows are one region");
-    static constexpr int OFF_STAT = OFF_Q + 2 * QTILE;   // float [2 tiles][m, l][128]
-    static constexpr int OFF_ITEM = OFF_STAT + 2 * 2 * kPtRows * 4;
+    static constexpr int OFF_STAGE = OFF_Q + 2 * QTILE;  // 2 KB per softmax warp: 64 bytes of 32 rows
+    static constexpr int OFF_ITEM = OFF_STAGE + 8 * 2048;
     static constexpr int OFF_PREF = OFF_ITEM + kPtItems * static_cast<int>(sizeof(PtItem));
     static constexpr int OFF_SCAN = OFF_PREF + (kPtMaxBatch + 4) * 4;  // 16 warp sums, an arrival flag
     static constexpr int OFF_BAR = (OFF_SCAN + 128 + 7) & ~7;
-    // units full/empty, Q full/empty, S full, P full, O step done, O full/drained, stats full/free, item full/empty, drain
+    // units full/empty, Q full/empty, S full, P full, O step done, O full/drained, item full/empty, widened V, drain
     static constexpr int B_UF = 0, B_UE = B_UF + NU, B_QF = B_UE + NU, B_QE = B_QF + 1, B_SF = B_QE + 1;
-    static constexpr int B_PF = B_SF + 2, B_OD = B_PF + 2, B_OF = B_OD + 2, B_OE = B_OF + 2, B_XF = B_OE + 2;
-    static constexpr int B_XE = B_XF + 2, B_IF = B_XE + 2, B_IE = B_IF + kPtItems, B_DR = B_IE + kPtItems + 2 * NV;
-    static constexpr int B_VF = B_IE + kPtItems, B_VE = B_VF + NV;  // widened V full/empty
+    static constexpr int B_PF = B_SF + 2, B_OD = B_PF + 2, B_OF = B_OD + 2, B_OE = B_OF + 2, B_IF = B_OE + 2;
+    static constexpr int B_IE = B_IF + kPtItems, B_VF = B_IE + kPtItems, B_VE = B_VF + NV, B_DR = B_VE + NV;
     static constexpr int NBAR = B_DR + 1;
     static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_TMEM + 16 + 1024;
@@ -152,7 +152,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // What a softmax thread needs to turn its row's products into weights.
 struct PtScore {
-    float scale2, cap_in, cap_log2, cap_y;
+    float scale2, cap_in, cap_log2;
     float slope, base;   // bias: slope in log2 units; position - first key of the tile
     int c0, c1;          // keys [c0, c1) of the tile are seen
     unsigned stages;     // 16-key stages whose page is in the pool
@@ -185,16 +185,15 @@ __device__ __forceinline__ float pt_top(const uint32_t (&s)[32], int k0, const P
 // The weights 2^(x - m) of 32 keys (k0 .. k0 + 31 of the tile) from their
 // products s, packed to the operand type, with their fp32 sum and the running
 // maximum: of q.k (the logit rises with it), with a bias of x - m.
-// Capped logits, kPoly: c tanh(y), y = scale q.k / c, as q.k scaled times P(y^2),
-// P of degree 5 interpolating tanh(y)/y at the Chebyshev points of y^2 in [0, 0.5]
-// (tanh off by 8e-8 at most in fp32), all on packed FMAs; `far` keeps the largest
-// |q.k|, and a tile with |y| > 0.7 is done again by exponential and reciprocal
-// (capped(): three special-function results per key instead of one).
+// Capped logits, kPoly: q.k times a polynomial in its square (cap_c), on packed
+// FMAs; `far` keeps the largest |q.k|, and a tile beyond the polynomial's range is
+// done again by exponential and reciprocal (capped(): three special-function
+// results per key instead of one).
 // A bias is linear in the key where no key lies behind its row's position
 // (unmasked tiles); masked tiles take the distance's magnitude.
 template <bool kBF16, bool kCap, bool kPoly, bool kBias, bool kMasked>
-__device__ __forceinline__ void pt_weights(const uint32_t (&s)[32], uint32_t* pk, int k0, const PtScore& w, float m,
-                                           float2 (&sum)[2], float& top, float& far) {
+__device__ __forceinline__ void pt_weights(const uint32_t (&s)[32], uint32_t* pk, int k0, const PtScore& w,
+                                           const float (&cc)[5], float m, float2 (&sum)[2], float& top, float& far) {
     const float nb = kBias ? -w.slope * w.base - m : 0.f;
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {
@@ -209,13 +208,12 @@ __device__ __forceinline__ void pt_weights(const uint32_t (&s)[32], uint32_t* pk
                 add = make_float2(fmaf(w.slope, static_cast<float>(k), nb), fmaf(w.slope, static_cast<float>(k + 1), nb));
         }
         if constexpr (kCap && kPoly) {
-            const float2 y = mul2(qk, both(w.cap_y)), z = mul2(y, y);
-            float2 t = fma2(z, both(-0.0050308364f), both(0.019959657f));
-            t = fma2(z, t, both(-0.05350069f));
-            t = fma2(z, t, both(0.13328016f));
-            t = fma2(z, t, both(-0.33333108f));
-            t = fma2(z, t, both(1.0f));
-            x = fma2(t, mul2(qk, both(w.scale2)), add);
+            const float2 z = mul2(qk, qk);
+            float2 t = fma2(z, both(cc[4]), both(cc[3]));
+            t = fma2(z, t, both(cc[2]));
+            t = fma2(z, t, both(cc[1]));
+            t = fma2(z, t, both(cc[0]));
+            x = fma2(t, qk, add);
             far = max3(far, fabsf(qk.x), fabsf(qk.y));
         } else if constexpr (kCap) {
             x = add2(make_float2(capped(qk.x, w.cap_in, w.cap_log2), capped(qk.y, w.cap_in, w.cap_log2)), add);
@@ -303,7 +301,6 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
     const uint32_t sb0 = smem_u32(smem);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);
     PtItem* items = reinterpret_cast<PtItem*>(smem + S::OFF_ITEM);
-    float* stats = reinterpret_cast<float*>(smem + S::OFF_STAT);
     int* pref = reinterpret_cast<int*>(smem + S::OFF_PREF);
     int* scan = reinterpret_cast<int*>(smem + S::OFF_SCAN);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + S::OFF_TMEM);
@@ -329,17 +326,15 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             mbar_init(bar(S::B_OD + i), 1);
             mbar_init(bar(S::B_OF + i), 1);
             mbar_init(bar(S::B_OE + i), 4);
-            mbar_init(bar(S::B_XF + i), 4);
-            mbar_init(bar(S::B_XE + i), 4);
         }
         for (int i = 0; i < kPtItems; ++i) {
             mbar_init(bar(S::B_IF + i), 1);
-            mbar_init(bar(S::B_IE + i), 1 + 8 + 4 + (kFp8 ? 2 : 0));  // the issuing warp; softmax, epilogue, widening warps
+            mbar_init(bar(S::B_IE + i), 1 + 8 + (kFp8 ? 2 : 0));  // the issuing, softmax and widening warps
         }
         mbar_init(bar(S::B_DR), 1);
         fence_barrier_init();
     }
-    if (warp == 13) {
+    if (warp == 9) {
         tc05::alloc(smem_u32(tslot), 512);  // S/P: columns 0-255, O: 256 + D * tile
         tc05::relinquish_alloc_permit();
     }
@@ -380,9 +375,9 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                                    : tc05::idesc_f16(kBF16, kPtRows, kPtKeys, false, false);  // S = Q K^T
     constexpr uint32_t kIdO = tc05::idesc_f16(kBF16, kPtRows, D, false, true);         // O += P V
 
-    if (warp >= 12) {
-        reg_dec<72>();
-        if (warp == 12) {
+    if (warp >= 8) {
+        reg_dec<88>();
+        if (warp == 8) {
             // ------------------------------------------------------ loads
             if (lane == 0) {
                 prefetch_tmap(&kvmap);
@@ -393,138 +388,154 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
             const int total = pref[p.B] * p.Hkv * p.max_splits;
             int idx = blockIdx.x;
-            int u = 0, nq = 0, it = 0;
+            int u = 0, nq = 0, npub = 0;
             bool ok = true;
-            for (;;) {
-                // the next index is drawn while this item loads
-                int next = 0;
-                if (lane == 0) next = static_cast<int>(gridDim.x) + atomicAdd(p.queue, 1);
-                if (idx >= total) {
-                    const int slot = it % kPtItems;
-                    if (it >= kPtItems && !pt_wait(bar(S::B_IE + slot), ((it / kPtItems) - 1) & 1, p)) ok = false;
+            // Decode and publish the next item (or the end).  Called one item ahead, once
+            // the ring is full of the current item's tiles, so that its chain of loads
+            // (lengths, table) is hidden.
+            auto publish = [&]() {
+                for (;;) {
+                    const int slot = npub % kPtItems;
+                    if (idx >= total) {
+                        if (npub >= kPtItems && !pt_wait(bar(S::B_IE + slot), ((npub / kPtItems) - 1) & 1, p)) return false;
+                        if (lane == 0) {
+                            items[slot].end = 1;
+                            mbar_arrive(bar(S::B_IF + slot));
+                        }
+                        __syncwarp();
+                        ++npub;
+                        return true;
+                    }
+                    int next = 0;
+                    if (lane == 0) next = static_cast<int>(gridDim.x) + atomicAdd(p.queue, 1);
+                    // item idx: splits innermost; within a request groups of kv heads
+                    // whose keys and values fit half of L2 together, in each the row tiles
+                    // from the last (the longest, causal) to the first, all heads of the
+                    // group per tile -- the short items come last
+                    const int split = idx % p.max_splits, r1 = idx / p.max_splits;
+                    int lo_b = 0, hi_b = p.B;
+                    while (hi_b - lo_b > 1) {
+                        const int mid = (lo_b + hi_b) >> 1;
+                        if (static_cast<long long>(pref[mid]) * p.Hkv <= r1) lo_b = mid; else hi_b = mid;
+                    }
+                    const int b = lo_b, npair = pref[b + 1] - pref[b], r2 = r1 - pref[b] * p.Hkv;
+                    int q0, n;
+                    request_tokens(p, b, q0, n, false);
+                    const int L = request_len(p, b, r2 == 0 && split == 0 && lane == 0);
+                    const int prefix = p.prefix_lens ? p.prefix_lens[b] : 0;
+                    const int group = max(1, min(p.Hkv, kPtL2Bytes / (2 * S::ROWB) / max(L, 1)));
+                    const int g = r2 / (npair * group), width = min(group, p.Hkv - g * group), r3 = r2 - g * npair * group;
+                    const int pair = npair - 1 - r3 / width, hk = g * group + r3 % width;
+                    const int tok0 = pair * 2 * TOK;
+                    int lo[2], hi[2];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int a0 = tok0 + t * TOK, a1 = min(a0 + TOK, n);
+                        int l = 0x7fffffff, h = 0;
+                        for (int i = a0 + lane; i < a1; i += 32) {
+                            int x, y;
+                            token_keys(p, q0, n, L, prefix, i, x, y);
+                            if (x < y) {
+                                l = min(l, x);
+                                h = max(h, y);
+                            }
+                        }
+                        lo[t] = __reduce_min_sync(kFull, l);
+                        hi[t] = __reduce_max_sync(kFull, h);
+                    }
+                    const int lo_all = min(lo[0], lo[1]), hi_all = max(hi[0], hi[1]);
+                    const int begin = lo_all & ~(kStageTok - 1);  // 16-key stages never cross a page
+                    int nsplit = hi_all > 0 ? (hi_all - begin + p.chunk - 1) / p.chunk : 0;
+                    if (nsplit > p.max_splits) {
+                        if (lane == 0) atomicOr(p.status, kErrBounds);
+                        nsplit = p.max_splits;
+                    }
+                    if (split >= max(nsplit, 1)) {  // nothing here
+                        idx = __shfl_sync(kFull, next, 0);
+                        continue;
+                    }
+                    const int t0 = nsplit ? begin + split * p.chunk : 0;
+                    const int t1 = nsplit ? min(t0 + p.chunk, hi_all) : 0;
+                    const int ntiles = (t1 - t0 + kPtKeys - 1) / kPtKeys;
+                    // a page outside the pool anywhere in the item: the softmax checks its keys
+                    const int32_t* row = p.block_table + static_cast<long long>(b) * p.bt_stride;
+                    int bad = 0;
+                    if (ntiles) {
+                        const int c1 = page_div(t1 - 1, p.pmagic, p.pmshift);
+                        for (int c = page_div(t0, p.pmagic, p.pmshift) + lane; c <= c1; c += 32)
+                            bad |= row[c] < 0 || row[c] >= p.num_pages;
+                        bad = __any_sync(kFull, bad);
+                        if (bad && lane == 0) atomicOr(p.status, kErrBounds);
+                    }
+                    if (npub >= kPtItems && !pt_wait(bar(S::B_IE + slot), ((npub / kPtItems) - 1) & 1, p)) return false;
                     if (lane == 0) {
-                        items[slot].end = 1;
+                        PtItem& I = items[slot];
+                        I.b = b; I.hk = hk; I.q0 = q0; I.n = n; I.L = L; I.prefix = prefix; I.tok0 = tok0;
+                        I.t0 = t0; I.t1 = t1; I.ntiles = ntiles; I.lo_all = lo_all; I.hi_all = hi_all;
+                        I.split = split; I.nsplit = nsplit; I.unit = (pref[b] + pair) * p.Hkv + hk;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const int a = max(lo[t], t0), z = min(hi[t], t1);
+                            I.jb[t] = a < z ? (a - t0) / kPtKeys : 0;
+                            I.je[t] = a < z ? (z - t0 + kPtKeys - 1) / kPtKeys : 0;
+                        }
+                        I.bad = bad; I.end = 0;
                         mbar_arrive(bar(S::B_IF + slot));
                     }
                     __syncwarp();
-                    break;
-                }
-                // item idx: splits innermost; within a request groups of kv heads
-                // whose keys and values fit half of L2 together, in each the row tiles
-                // from the last (the longest, causal) to the first, all heads of the
-                // group per tile -- the short items come last
-                const int split = idx % p.max_splits, r1 = idx / p.max_splits;
-                int lo_b = 0, hi_b = p.B;
-                while (hi_b - lo_b > 1) {
-                    const int mid = (lo_b + hi_b) >> 1;
-                    if (static_cast<long long>(pref[mid]) * p.Hkv <= r1) lo_b = mid; else hi_b = mid;
-                }
-                const int b = lo_b, npair = pref[b + 1] - pref[b], r2 = r1 - pref[b] * p.Hkv;
-                int q0, n;
-                request_tokens(p, b, q0, n, false);
-                const int L = request_len(p, b, r2 == 0 && split == 0 && lane == 0);
-                const int group = max(1, min(p.Hkv, kPtL2Bytes / (2 * S::ROWB) / max(L, 1)));
-                const int g = r2 / (npair * group), width = min(group, p.Hkv - g * group), r3 = r2 - g * npair * group;
-                const int pair = npair - 1 - r3 / width, hk = g * group + r3 % width;
-                const int prefix = p.prefix_lens ? p.prefix_lens[b] : 0;
-                const int tok0 = pair * 2 * TOK;
-                int lo[2], hi[2];
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int a0 = tok0 + t * TOK, a1 = min(a0 + TOK, n);
-                    int l = 0x7fffffff, h = 0;
-                    for (int i = a0 + lane; i < a1; i += 32) {
-                        int x, y;
-                        token_keys(p, q0, n, L, prefix, i, x, y);
-                        if (x < y) {
-                            l = min(l, x);
-                            h = max(h, y);
-                        }
-                    }
-                    lo[t] = __reduce_min_sync(kFull, l);
-                    hi[t] = __reduce_max_sync(kFull, h);
-                }
-                const int lo_all = min(lo[0], lo[1]), hi_all = max(hi[0], hi[1]);
-                const int begin = lo_all & ~(kStageTok - 1);  // 16-key stages never cross a page
-                int nsplit = hi_all > 0 ? (hi_all - begin + p.chunk - 1) / p.chunk : 0;
-                if (nsplit > p.max_splits) {
-                    if (lane == 0) atomicOr(p.status, kErrBounds);
-                    nsplit = p.max_splits;
-                }
-                if (split >= max(nsplit, 1)) {  // nothing here
+                    ++npub;
                     idx = __shfl_sync(kFull, next, 0);
+                    return true;
+                }
+            };
+            ok = publish();
+            for (int it = 0; ok; ++it) {
+                // the item's slot is not reused before this warp publishes four items on
+                const PtItem& I = items[it % kPtItems];
+                if (I.end) break;
+                const int hk = I.hk, t0 = I.t0, t1 = I.t1, ntiles = I.ntiles;
+                const int32_t* row = p.block_table + static_cast<long long>(I.b) * p.bt_stride;
+                if (!ntiles) {
+                    ok = publish();
                     continue;
                 }
-                const int t0 = nsplit ? begin + split * p.chunk : 0;
-                const int t1 = nsplit ? min(t0 + p.chunk, hi_all) : 0;
-                const int ntiles = (t1 - t0 + kPtKeys - 1) / kPtKeys;
-                // a page outside the pool anywhere in the item: the softmax checks its keys
-                const int32_t* row = p.block_table + static_cast<long long>(b) * p.bt_stride;
-                int bad = 0;
-                if (ntiles) {
-                    const int c1 = page_div(t1 - 1, p.pmagic, p.pmshift);
-                    for (int c = page_div(t0, p.pmagic, p.pmshift) + lane; c <= c1; c += 32)
-                        bad |= row[c] < 0 || row[c] >= p.num_pages;
-                    bad = __any_sync(kFull, bad);
-                    if (bad && lane == 0) atomicOr(p.status, kErrBounds);
-                }
-                const int slot = it % kPtItems;
-                if (it >= kPtItems && !pt_wait(bar(S::B_IE + slot), ((it / kPtItems) - 1) & 1, p)) { ok = false; break; }
+                // Q of the item's tiles (128-byte regions), once the last item's products have read theirs
+                if (nq >= 1 && !pt_wait(bar(S::B_QE), (nq - 1) & 1, p)) { ok = false; break; }
                 if (lane == 0) {
-                    PtItem& I = items[slot];
-                    I.b = b; I.hk = hk; I.q0 = q0; I.n = n; I.L = L; I.prefix = prefix; I.tok0 = tok0;
-                    I.t0 = t0; I.t1 = t1; I.ntiles = ntiles; I.lo_all = lo_all; I.hi_all = hi_all;
-                    I.split = split; I.nsplit = nsplit; I.unit = (pref[b] + pair) * p.Hkv + hk;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int a = max(lo[t], t0), z = min(hi[t], t1);
-                        I.jb[t] = a < z ? (a - t0) / kPtKeys : 0;
-                        I.je[t] = a < z ? (z - t0 + kPtKeys - 1) / kPtKeys : 0;
-                    }
-                    I.bad = bad; I.end = 0;
-                    mbar_arrive(bar(S::B_IF + slot));
+                    const int tiles = I.tok0 + TOK < I.n ? 2 : 1;
+                    mbar_arrive_expect_tx(bar(S::B_QF), tiles * S::REGIONS * TOK * G * 128);
+                    for (int t = 0; t < tiles; ++t)
+                        for (int h = 0; h < S::REGIONS; ++h)
+                            tma_load_3d(sb0 + S::OFF_Q + t * S::QTILE + h * kPtRows * 128, &qmap, 64 * h, hk * G,
+                                        I.q0 + I.tok0 + t * TOK, bar(S::B_QF), pol);
                 }
                 __syncwarp();
-                ++it;
-                if (ntiles) {
-                    // Q of the item's tiles (64-dim regions), once the last item's products have read theirs
-                    if (nq >= 1 && !pt_wait(bar(S::B_QE), (nq - 1) & 1, p)) { ok = false; break; }
-                    const int tiles = tok0 + TOK < n ? 2 : 1;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(bar(S::B_QF), tiles * S::REGIONS * TOK * G * 128);
-                        for (int t = 0; t < tiles; ++t)
-                            for (int h = 0; h < S::REGIONS; ++h)
-                                tma_load_3d(sb0 + S::OFF_Q + t * S::QTILE + h * kPtRows * 128, &qmap, 64 * h, hk * G,
-                                            q0 + tok0 + t * TOK, bar(S::B_QF), pol);
-                    }
-                    __syncwarp();
-                    ++nq;
-                    auto entry = [&](int j) {
-                        const int tok = t0 + j * kPtKeys + lane * kStageTok;
-                        return lane < kPtKeys / kStageTok && tok < t1 ? row[page_div(tok, p.pmagic, p.pmshift)] : -1;
-                    };
-                    int pg = entry(0);
-                    for (int j = 0; j < ntiles && ok; ++j) {
-                        const int pg_next = j + 1 < ntiles ? entry(j + 1) : -1;
-                        const int tok = t0 + j * kPtKeys + lane * kStageTok;
-                        const bool load = pg >= 0 && pg < p.num_pages;
-                        const int bytes = __popc(__ballot_sync(kFull, load)) * 2 * S::GROUP;
-                        const int krow = load ? (pg * p.Hkv + hk) * p.P + (tok - page_div(tok, p.pmagic, p.pmshift) * p.P) : 0;
+                ++nq;
+                auto entry = [&](int j) {
+                    const int tok = t0 + j * kPtKeys + lane * kStageTok;
+                    return lane < kPtKeys / kStageTok && tok < t1 ? row[page_div(tok, p.pmagic, p.pmshift)] : -1;
+                };
+                int pg = entry(0);
+                const int ahead = min(ntiles, S::NU / 2) - 1;  // the ring is full behind this tile
+                for (int j = 0; j < ntiles && ok; ++j) {
+                    const int pg_next = j + 1 < ntiles ? entry(j + 1) : -1;
+                    const int tok = t0 + j * kPtKeys + lane * kStageTok;
+                    const bool load = pg >= 0 && pg < p.num_pages;
+                    const int bytes = __popc(__ballot_sync(kFull, load)) * 2 * S::GROUP;
+                    const int krow = load ? (pg * p.Hkv + hk) * p.P + (tok - page_div(tok, p.pmagic, p.pmshift) * p.P) : 0;
 #pragma unroll 1
-                        for (int v = 0; v < 2; ++v, ++u) {
-                            const int us = u % S::NU;
-                            if (u >= S::NU && !pt_wait(bar(S::B_UE + us), ((u / S::NU) - 1) & 1, p)) { ok = false; break; }
-                            if (lane == 0) mbar_arrive_expect_tx(bar(S::B_UF + us), bytes);
-                            __syncwarp();
-                            if (load)
-                                tma_load_4d(sb0 + S::OFF_KV + us * S::UNIT + 2 * lane * S::GROUP, &kvmap, 0, 0,
-                                            v * S::REGIONS, krow >> 3, bar(S::B_UF + us), keep);
-                        }
-                        pg = pg_next;
+                    for (int v = 0; v < 2; ++v, ++u) {
+                        const int us = u % S::NU;
+                        if (u >= S::NU && !pt_wait(bar(S::B_UE + us), ((u / S::NU) - 1) & 1, p)) { ok = false; break; }
+                        if (lane == 0) mbar_arrive_expect_tx(bar(S::B_UF + us), bytes);
+                        __syncwarp();
+                        if (load)
+                            tma_load_4d(sb0 + S::OFF_KV + us * S::UNIT + 2 * lane * S::GROUP, &kvmap, 0, 0,
+                                        v * S::REGIONS, krow >> 3, bar(S::B_UF + us), keep);
                     }
-                    if (!ok) break;
+                    if (ok && j == ahead) ok = publish();
+                    pg = pg_next;
                 }
-                idx = __shfl_sync(kFull, next, 0);
             }
             if (!ok) {
                 // let every issued copy land before the CTA leaves
@@ -532,7 +543,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                 for (int j = max(0, u - S::NU); j < u; ++j) mbar_wait(bar(S::B_UF + j % S::NU), (j / S::NU) & 1);
                 if (nq) mbar_wait(bar(S::B_QF), (nq - 1) & 1);
             }
-        } else if (warp == 13) {
+        } else if (warp == 9) {
             // --------------------------------------------------- products
             // The whole warp walks the items, converged, so that descriptors stay in
             // uniform registers; one elected lane issues (with the loop under a lane
@@ -577,6 +588,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                 for (int t = 0; ok && t < 2; ++t)
                     if (jb[t] == 0 && je[t] > 0) qk(t, 0);
                 if (one) tc05::commit(bar(S::B_UE + u % S::NU));
+                if (one && ntiles == 1) tc05::commit(bar(S::B_QE));
                 for (int j = 0; ok && j < ntiles; ++j) {
                     const int vu = u + 2 * j + 1, vb = kFp8 ? (nv + j) % 2 : 0;
                     ok = kFp8 ? pt_wait(bar(S::B_VF + vb), ((nv + j) >> 1) & 1, p)
@@ -619,11 +631,13 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                             }
                             // in issue order behind this tile's O product, which has read the P under S
                             if (j + 1 >= jb[t] && j + 1 < je[t]) qk(t, j + 1);
-                            if (t == 1 && one) tc05::commit(bar(S::B_UE + (u + 2 * (j + 1)) % S::NU));
+                            if (t == 1 && one) {
+                                tc05::commit(bar(S::B_UE + (u + 2 * (j + 1)) % S::NU));
+                                if (j + 1 == ntiles - 1) tc05::commit(bar(S::B_QE));  // Q is spent
+                            }
                         }
                     }
                 }
-                if (one) tc05::commit(bar(S::B_QE));
                 u += 2 * ntiles;
                 nv += ntiles;
             }
@@ -639,7 +653,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             // every e4m3 value is exact in fp16; the 16-bit tile has the layout of a
             // 16-bit cache's.  A thread widens two key rows; rows that no query row
             // of the unit sees become zeros (their weight 0 must not meet a NaN)
-            const int x = (warp - 14) * 32 + lane;
+            const int x = (warp - 10) * 32 + lane;
             int u = 0, nv = 0;
             bool ok = true;
             for (int it = 0; ok; ++it) {
@@ -693,14 +707,14 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             }
             if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
         }
-    } else if (warp < 8) {
-        // ------------------------------------------------------- softmax
-        reg_inc<176>();
+    } else {
+        // ------------------------------------------ softmax and epilogue
+        reg_inc<208>();
         const int t = warp >> 2, q4 = warp & 3, r = 32 * q4 + lane;  // row of tile t = TMEM lane
         const uint32_t lane_addr = static_cast<uint32_t>(32 * q4) << 16;
         const uint32_t s_addr = tmem + lane_addr + kPtKeys * t, o_addr = tmem + lane_addr + 256 + D * t;
         const int ri = r / G, rg = r - ri * G;
-        int ns = 0, no = 0, u = 0;  // key tiles, accumulations done by this tile; K/V units before the item
+        int ns = 0, no = 0, u = 0;  // key tiles walked, accumulations drained; K/V units before the item
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const int slot = it % kPtItems;
@@ -708,6 +722,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             const PtItem& I = items[slot];
             if (I.end) break;
             const int jb = I.jb[t], je = I.je[t], t0 = I.t0, ntiles = I.ntiles;
+            float m_used = -INFINITY, l = 0.f;
             if (jb < je) {
                 const int tok = I.tok0 + t * TOK + ri;
                 const bool valid = ri < TOK && tok < I.n;
@@ -732,14 +747,15 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     mh = bad ? 0 : (__reduce_min_sync(kFull, h0) - t0) / kPtKeys;  // below 0: rounded up, still masked
                     if (__reduce_min_sync(kFull, h0) < t0) mh = 0;
                 }
-                float m_used = -INFINITY, l = 0.f;
-                bool wide = false;  // capped: some |y| was above the polynomial's range
+                // capped scores beyond the polynomial's range: two tiles in a row make the
+                // warp take the special functions for the next four
+                int wide = kCap && p.cap_far < 0.f ? 1 << 30 : 0;
                 for (int j = jb; j < je; ++j, ++ns) {
                     const int tk = t0 + j * kPtKeys;
                     if (!pt_wait(bar(S::B_SF + t), ns & 1, p)) { ok = false; break; }
                     if (warp_on) {
                         tc05::fence_after_sync();
-                        PtScore w{p.scale_log2, p.cap_in, p.cap_log2, p.cap_y, slope, static_cast<float>(pos - tk),
+                        PtScore w{p.scale_log2, p.cap_in, p.cap_log2, slope, static_cast<float>(pos - tk),
                                   lo - tk, min(hi, hi_all) - tk, bad ? pt_stages(p, I, tk) : 0xffu};
                         const bool masked = j < ml || j >= mh;
                         uint32_t a[32], b[32];
@@ -783,17 +799,17 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                                 tc05::ld_32x32b_x32(s_addr, a);
                                 tc05::wait_ld(a);
                                 tc05::ld_32x32b_x32(s_addr + 32, b);
-                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(a, pk, 0, w, m, sum, top, far);
+                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(a, pk, 0, w, p.cap_c, m, sum, top, far);
                                 tc05::wait_ld(b);
                                 tc05::ld_32x32b_x32(s_addr + 64, a);
-                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(b, pk + 16, 32, w, m, sum, top, far);
+                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(b, pk + 16, 32, w, p.cap_c, m, sum, top, far);
                                 tc05::wait_ld(a);
                                 tc05::ld_32x32b_x32(s_addr + 96, b);
-                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(a, pk + 32, 64, w, m, sum, top, far);
+                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(a, pk + 32, 64, w, p.cap_c, m, sum, top, far);
                                 tc05::wait_ld(b);
-                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(b, pk + 48, 96, w, m, sum, top, far);
+                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(b, pk + 48, 96, w, p.cap_c, m, sum, top, far);
                             };
-                            if (kCap && (wide || masked))
+                            if (kCap && wide > 4)
                                 pass(std::false_type{}, std::true_type{});
                             else if (masked)
                                 pass(std::true_type{}, std::true_type{});
@@ -801,8 +817,8 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                                 pass(std::true_type{}, std::false_type{});
                             if constexpr (kCap) {
                                 // (far stays 0 in a pass that does not depend on it)
-                                if (__any_sync(kFull, far * p.cap_y > 0.7f)) {
-                                    wide = true;
+                                if (__any_sync(kFull, far > p.cap_far) && wide <= 4) {
+                                    wide = 8;
                                     continue;
                                 }
                             }
@@ -829,6 +845,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                             }
                         }
                         if (!ok) break;
+                        if (kCap && wide > 0) --wide;
                         tc05::st_32x32b_x32(s_addr, reinterpret_cast<const uint32_t(&)[32]>(pk[0]));
                         tc05::st_32x32b_x32(s_addr + 32, reinterpret_cast<const uint32_t(&)[32]>(pk[32]));
                         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -854,125 +871,108 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     if (lane == 0) mbar_arrive(bar(S::B_PF + t));
                 }
                 if (!ok) break;
-                // row statistics for the epilogue
-                if (no >= 1 && !pt_wait(bar(S::B_XE + t), (no - 1) & 1, p)) { ok = false; break; }
-                ++no;
-                stats[(2 * t) * kPtRows + r] = m_used;
-                stats[(2 * t + 1) * kPtRows + r] = l;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(S::B_XF + t));
             }
-            u += 2 * ntiles;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(S::B_IE + slot));
-        }
-        if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
-    } else {
-        // ------------------------------------------------------ epilogue
-        reg_dec<88>();
-        const int q4 = warp & 3, r = 32 * q4 + lane;
-        const uint32_t lane_addr = static_cast<uint32_t>(32 * q4) << 16;
-        const int ri = r / G, rg = r - ri * G;
-        int no[2] = {0, 0};
-        bool ok = true;
-        for (int it = 0; ok; ++it) {
-            const int slot = it % kPtItems;
-            if (!pt_wait(bar(S::B_IF + slot), (it / kPtItems) & 1, p)) { ok = false; break; }
-            const PtItem& I = items[slot];
-            if (I.end) break;
-            const int q0 = I.q0, n = I.n, tok0 = I.tok0, hk = I.hk, split = I.split, nsplit = I.nsplit, unit = I.unit;
-            const bool whole = nsplit <= 1 && !partials;
-#pragma unroll 1
-            for (int t = 0; t < 2; ++t) {
-                const int tok = tok0 + t * TOK + ri;
-                const bool valid = ri < TOK && tok < n;
-                const bool live = I.jb[t] < I.je[t];
-                const long long row = static_cast<long long>(q0 + tok) * p.Hq + hk * G + rg;  // output row
-                const long long prow = static_cast<long long>(split) * p.T * p.Hq + row;      // partial row
-                float m = -INFINITY, l = 0.f;
+            // ---- the item's result (a tile without keys in it: nothing, or zeros)
+            const int n = I.n, tok = I.tok0 + t * TOK + ri;
+            if (I.tok0 + t * TOK < n) {
+                const bool valid = ri < TOK && tok < n, live = jb < je;
+                const int nsplit = I.nsplit, row = (I.q0 + tok) * p.Hq + I.hk * G + rg;  // below T * Hq < 2^31
+                const bool whole = nsplit <= 1 && !partials;
+                const long long part0 = whole ? 0 : static_cast<long long>(I.split) * p.T * p.Hq;
+                const float inv = l > 0.f ? (whole ? p.v_scale : 1.f) / l : 0.f;
                 if (live) {
-                    if (!pt_wait(bar(S::B_XF + t), no[t] & 1, p) || !pt_wait(bar(S::B_OF + t), no[t] & 1, p)) { ok = false; break; }
-                    ++no[t];
-                    m = stats[(2 * t) * kPtRows + r];
-                    l = stats[(2 * t + 1) * kPtRows + r];
+                    if (!pt_wait(bar(S::B_OF + t), no & 1, p)) { ok = false; break; }
+                    ++no;
                     tc05::fence_after_sync();
                 }
-                const float inv = l > 0.f ? (whole ? p.v_scale : 1.f) / l : 0.f;
-                const bool write_o = valid && (whole || l > 0.f);
+                // 64 output bytes of every row at a time through the warp's staging area, so
+                // that a store instruction covers 64 consecutive bytes of eight rows
+                const int kind = whole ? p.out_dtype : 3, elt = kind == 3 ? 4 : 2;
+                const int dst_row = valid && (whole || l > 0.f) ? row : -1;
+                uint8_t* dst0 = whole ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(p.part_out + part0 * D);
+                uint8_t* stage = smem + S::OFF_STAGE + warp * 2048;
+                auto flush = [&](const uint32_t (&h)[16], int byte) {
+                    const int sw = (lane >> 1) & 3;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ sw) << 4)) =
+                            make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = 8 * i + (lane >> 2);
+                        const int dr = __shfl_sync(kFull, dst_row, rr);
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+                        if (dr >= 0)
+                            __stcg(reinterpret_cast<uint4*>(dst0 + static_cast<long long>(dr) * (D * elt) + byte + (lane & 3) * 16), v);
+                    }
+                    __syncwarp();
+                };
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     if (live) {
-                        tc05::ld_32x32b_x32(tmem + lane_addr + 256 + D * t + c, o);
-                        tc05::wait_ld();
+                        tc05::ld_32x32b_x32(o_addr + c, o);
+                        tc05::wait_ld(o);
+                        if (c == D - 32) {
+                            // drained: the next item's O product may begin
+                            tc05::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(S::B_OE + t));
+                        }
                     }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = l > 0.f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
-                    if (!write_o) {
-                    } else if (!whole) {
-                        float4* dst = reinterpret_cast<float4*>(p.part_out + prow * D + c);
+                    uint32_t h[16];
+                    if (kind == 3) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            __stcg(dst + e, make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                                        __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
-                    } else if (p.out_dtype == 3) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + row * D + c);
+                        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + c);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t h[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float x = __uint_as_float(o[8 * e + 2 * k]), y = __uint_as_float(o[8 * e + 2 * k + 1]);
-                                h[k] = p.out_dtype == 0 ? pack2<true>(x, y) : pack2<false>(x, y);
-                            }
-                            dst[e] = make_uint4(h[0], h[1], h[2], h[3]);
+                            for (int e = 0; e < 16; ++e) h[e] = o[16 * half + e];
+                            flush(h, 4 * c + 64 * half);
                         }
-                    }
-                    __syncwarp();
-                }
-                if (live) {
-                    tc05::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(S::B_OE + t));
-                        mbar_arrive(bar(S::B_XE + t));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float x = __uint_as_float(o[2 * e]), y = __uint_as_float(o[2 * e + 1]);
+                            h[e] = kind == 0 ? pack2<true>(x, y) : pack2<false>(x, y);
+                        }
+                        flush(h, 2 * c);
                     }
                 }
                 if (valid) {
-                    const float l2 = l > 0.f ? m + __log2f(l) : -INFINITY;
+                    const float l2 = l > 0.f ? m_used + __log2f(l) : -INFINITY;
                     if (!whole)
-                        __stcg(p.part_lse + prow, l2);
+                        __stcg(p.part_lse + part0 + row, l2);
                     else if (p.lse)
                         p.lse[row] = l2 * kLn2;
                 }
-            }
-            if (!ok) break;
-            if (!partials && nsplit > 1) {
-                // publish this part (the group's barrier, then one arrival with release
-                // semantics); the arrival that completes the unit merges its rows
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (tid == 256) scan[24] = atom_add_acq_rel_gpu(p.counters + unit);
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (scan[24] == nsplit - 1) {
-                    const int rows = min(2 * TOK, n - tok0) * G;
-                    for (int x = q4; x < rows; x += 4) {
-                        const long long row = static_cast<long long>(q0 + tok0 + x / G) * p.Hq + hk * G + x % G;
+                if (!partials && nsplit > 1) {
+                    // publish this tile's part (the group's barrier, then one arrival with
+                    // release semantics); the arrival that completes the unit merges its rows
+                    const int tok_end = min(I.tok0 + 2 * TOK, n), tiles = I.tok0 + TOK < n ? 2 : 1;
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+                    if ((tid & 127) == 0) scan[24 + t] = atom_add_acq_rel_gpu(p.counters + I.unit);
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+                    if (scan[24 + t] == nsplit * tiles - 1) {
+                        const int rows = (tok_end - I.tok0) * G;
                         const long long step = static_cast<long long>(p.T) * p.Hq;
-                        float acc[D / 32], mx, ws;
-                        pt_merge_row<D>(p.part_lse + row, p.part_out + row * D, step, nsplit, lane, acc, mx, ws);
-                        const float sc = ws > 0.f ? p.v_scale / ws : 0.f;
+#pragma unroll 1
+                        for (int x = q4; x < rows; x += 4) {
+                            const long long mrow = static_cast<long long>(I.q0 + I.tok0 + x / G) * p.Hq + I.hk * G + x % G;
+                            float acc[D / 32], mx, ws;
+                            pt_merge_row<D>(p.part_lse + mrow, p.part_out + mrow * D, step, nsplit, lane, acc, mx, ws);
+                            const float sc = ws > 0.f ? p.v_scale / ws : 0.f;
 #pragma unroll
-                        for (int e = 0; e < D / 32; ++e)
-                            store_out(p.out, row * D + lane * (D / 32) + e, acc[e] * sc, p.out_dtype);
-                        if (lane == 0 && p.lse) p.lse[row] = ws > 0.f ? (mx + __log2f(ws)) * kLn2 : -INFINITY;
+                            for (int e = 0; e < D / 32; ++e)
+                                store_out(p.out, mrow * D + lane * (D / 32) + e, acc[e] * sc, p.out_dtype);
+                            if (lane == 0 && p.lse) p.lse[mrow] = ws > 0.f ? (mx + __log2f(ws)) * kLn2 : -INFINITY;
+                        }
+                        if ((tid & 127) == 0) p.counters[I.unit] = 0;  // every part has arrived: ready for the next call
                     }
-                    if (tid == 256) p.counters[unit] = 0;  // every part has arrived: ready for the next call
                 }
             }
+            u += 2 * ntiles;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(S::B_IE + slot));
         }
@@ -982,7 +982,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
     // ---------------------------------------------------------- tear-down
     tc05::fence_before_sync();
     __syncthreads();
-    if (warp == 13) {
+    if (warp == 9) {
         tc05::fence_after_sync();
         tc05::dealloc(tmem, 512);
     }
