@@ -44,7 +44,7 @@ constexpr int kPtL2Bytes = 64 << 20;  // keys and values walked together
 // A row's reference moves when its maximum has grown by more than this (log2
 // units).  The weights only must not overflow the operand type: bf16 has fp32's
 // range, fp16 ends at 2^16.  (With 2^8 for both, half of the key tiles of scores
-// with a spread of 3 made some warp repeat its pass.)
+// with a spread of 3 had some warp move its references.)
 constexpr float kPtRescaleBF16 = 40.f, kPtRescaleFP16 = 14.f;
 
 struct PtItem {
@@ -109,8 +109,22 @@ __device__ __forceinline__ unsigned pt_stages(const AttendParams& p, const PtIte
     return stages;
 }
 
+// Every lane of the warp waits, with a warp-uniform result: false after kWaitNs of
+// wall time, or once another role or CTA has reported a timeout.
 __device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, const AttendParams& p) {
-    return __all_sync(kFull, mbar_wait(bar, parity, p.status));
+    uint64_t t0 = 0;
+    bool done = true;
+#pragma unroll 1
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if (i & 255u) continue;
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitNs || (*reinterpret_cast<const volatile int32_t*>(p.status) & kErrTimeout)) {
+            done = false;
+            break;
+        }
+    }
+    return __all_sync(kFull, done);
 }
 
 // a*b + c on two floats at once
@@ -150,92 +164,89 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// What a softmax thread needs to turn its row's products into weights.
-struct PtScore {
-    float scale2, cap_in, cap_log2;
-    float slope, base;   // bias: slope in log2 units; position - first key of the tile
-    int c0, c1;          // keys [c0, c1) of the tile are seen
-    unsigned stages;     // 16-key stages whose page is in the pool
-};
+// A chunk is 32 keys of a row's tile, k0 .. k0 + 31 from the tile's first: their
+// products q.k as loaded, turned in place into what the exponential takes.
 
-template <bool kMasked>
-__device__ __forceinline__ bool pt_seen(const PtScore& w, int k) {
-    return !kMasked || (k >= w.c0 && k < w.c1 && (w.stages >> (k >> 4) & 1));
-}
-
-// The reference a row starts from: the largest logit among 32 keys.
-template <bool kBias, bool kCap, bool kMasked>
-__device__ __forceinline__ float pt_top(const uint32_t (&s)[32], int k0, const PtScore& w, float top) {
+// c tanh(scale q.k / c) in log2 units.  kPoly: q.k times a polynomial in its square
+// (for |q.k| <= cap_far) on packed FMAs; else by exponential and reciprocal
+// (capped(): two more special-function results per key).
+template <bool kPoly>
+__device__ __forceinline__ void pt_cap(uint32_t (&v)[32], const AttendParams& p) {
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {
-        float a = __uint_as_float(s[c]), b = __uint_as_float(s[c + 1]);
-        if constexpr (kBias) {
-            // (capped logits are below q.k scaled by as much as the reference may lie off,
-            // so with a bias the cap counts)
-            a = kCap ? capped(a, w.cap_in, w.cap_log2) : a * w.scale2;
-            b = kCap ? capped(b, w.cap_in, w.cap_log2) : b * w.scale2;
-            a = fmaf(-w.slope, fabsf(w.base - static_cast<float>(k0 + c)), a);
-            b = fmaf(-w.slope, fabsf(w.base - static_cast<float>(k0 + c + 1)), b);
-        }
-        top = max3(top, pt_seen<kMasked>(w, k0 + c) ? a : -INFINITY, pt_seen<kMasked>(w, k0 + c + 1) ? b : -INFINITY);
-    }
-    return top;
-}
-
-// The weights 2^(x - m) of 32 keys (k0 .. k0 + 31 of the tile) from their
-// products s, packed to the operand type, with their fp32 sum and the running
-// maximum: of q.k (the logit rises with it), with a bias of x - m.
-// Capped logits, kPoly: q.k times a polynomial in its square (cap_c), on packed
-// FMAs; `far` keeps the largest |q.k|, and a tile beyond the polynomial's range is
-// done again by exponential and reciprocal (capped(): three special-function
-// results per key instead of one).
-// A bias is linear in the key where no key lies behind its row's position
-// (unmasked tiles); masked tiles take the distance's magnitude.
-template <bool kBF16, bool kCap, bool kPoly, bool kBias, bool kMasked>
-__device__ __forceinline__ void pt_weights(const uint32_t (&s)[32], uint32_t* pk, int k0, const PtScore& w,
-                                           const float (&cc)[5], float m, float2 (&sum)[2], float& top, float& far) {
-    const float nb = kBias ? -w.slope * w.base - m : 0.f;
-#pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-        const int k = k0 + c;
-        const float2 qk = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-        float2 add = both(-m), x;  // what the scaled score needs to be the exponent
-        if constexpr (kBias) {
-            if constexpr (kMasked)
-                add = make_float2(fmaf(-w.slope, fabsf(w.base - static_cast<float>(k)), -m),
-                                  fmaf(-w.slope, fabsf(w.base - static_cast<float>(k + 1)), -m));
-            else
-                add = make_float2(fmaf(w.slope, static_cast<float>(k), nb), fmaf(w.slope, static_cast<float>(k + 1), nb));
-        }
-        if constexpr (kCap && kPoly) {
-            const float2 z = mul2(qk, qk);
-            float2 t = fma2(z, both(cc[4]), both(cc[3]));
-            t = fma2(z, t, both(cc[2]));
-            t = fma2(z, t, both(cc[1]));
-            t = fma2(z, t, both(cc[0]));
-            x = fma2(t, qk, add);
-            far = max3(far, fabsf(qk.x), fabsf(qk.y));
-        } else if constexpr (kCap) {
-            x = add2(make_float2(capped(qk.x, w.cap_in, w.cap_log2), capped(qk.y, w.cap_in, w.cap_log2)), add);
+        float2 x = make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+        if constexpr (kPoly) {
+            const float2 z = mul2(x, x);
+            float2 t = fma2(z, both(p.cap_c[4]), both(p.cap_c[3]));
+            t = fma2(z, t, both(p.cap_c[2]));
+            t = fma2(z, t, both(p.cap_c[1]));
+            t = fma2(z, t, both(p.cap_c[0]));
+            x = mul2(t, x);
         } else {
-            x = fma2(qk, both(w.scale2), add);
+            x = make_float2(capped(x.x, p.cap_in, p.cap_log2), capped(x.y, p.cap_in, p.cap_log2));
         }
-        if constexpr (kMasked) {
-            x.x = pt_seen<kMasked>(w, k) ? x.x : -INFINITY;
-            x.y = pt_seen<kMasked>(w, k + 1) ? x.y : -INFINITY;
-        }
-        if constexpr (kBias)
-            top = max3(top, x.x, x.y);
-        else if constexpr (kMasked)
-            top = max3(top, pt_seen<kMasked>(w, k) ? qk.x : -INFINITY, pt_seen<kMasked>(w, k + 1) ? qk.y : -INFINITY);
+        v[c] = __float_as_uint(x.x);
+        v[c + 1] = __float_as_uint(x.y);
+    }
+}
+
+// scale x - slope |dist - c|, dist: position minus the chunk's first key.  kBehind: no
+// key lies behind the position, the distance is linear in c.
+template <bool kBehind>
+__device__ __forceinline__ void pt_bias(uint32_t (&v)[32], float scale, float slope, float dist) {
+    const float nb = -slope * dist;
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+        float2 x = make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), add;
+        if constexpr (kBehind)
+            add = make_float2(fmaf(slope, static_cast<float>(c), nb), fmaf(slope, static_cast<float>(c + 1), nb));
         else
-            top = max3(top, qk.x, qk.y);
+            add = make_float2(-slope * fabsf(dist - static_cast<float>(c)), -slope * fabsf(dist - static_cast<float>(c + 1)));
+        x = fma2(x, both(scale), add);
+        v[c] = __float_as_uint(x.x);
+        v[c + 1] = __float_as_uint(x.y);
+    }
+}
+
+// -inf where the row does not see the key: keys [c0, c1) of the chunk are seen, and
+// of its two 16-key stages those whose bit is set.
+__device__ __forceinline__ void pt_mask(uint32_t (&v)[32], int c0, int c1, unsigned stages) {
+    const int a = max(c0, 0), b = min(c1, 32);
+    uint32_t seen = a < b ? (0xffffffffu >> (32 - (b - a))) << a : 0u;
+    if (!(stages & 1)) seen &= 0xffff0000u;
+    if (!(stages & 2)) seen &= 0x0000ffffu;
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+        if (!(seen >> c & 1)) v[c] = 0xff800000u;
+}
+
+// The largest |x| (kAbs) or x of a chunk.
+template <bool kAbs>
+__device__ __forceinline__ float pt_max(const uint32_t (&v)[32]) {
+    float top[2] = {kAbs ? 0.f : -INFINITY, kAbs ? 0.f : -INFINITY};
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+        const float x = __uint_as_float(v[c]), y = __uint_as_float(v[c + 1]);
+        float& m = top[(c >> 1) & 1];
+        m = kAbs ? max3(m, fabsf(x), fabsf(y)) : max3(m, x, y);
+    }
+    return fmaxf(top[0], top[1]);
+}
+
+// The weights 2^(scale x - m) of a chunk, packed to the operand type, and their sum:
+// l sums the fp32 weights, the product takes them rounded.
+template <bool kBF16>
+__device__ __forceinline__ float pt_weights(const uint32_t (&v)[32], uint32_t (&pk)[16], float scale, float m) {
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+        float2 x = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), both(scale), both(-m));
         x.x = fast_exp2(x.x);
         x.y = fast_exp2(x.y);
-        // l sums the fp32 weights; the product takes them rounded to the operand type
         sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], x);
         pk[c >> 1] = pack2<kBF16>(x.x, x.y);
     }
+    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
 template <int N>
@@ -488,54 +499,69 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     return true;
                 }
             };
-            ok = publish();
-            for (int it = 0; ok; ++it) {
-                // the item's slot is not reused before this warp publishes four items on
-                const PtItem& I = items[it % kPtItems];
-                if (I.end) break;
-                const int hk = I.hk, t0 = I.t0, t1 = I.t1, ntiles = I.ntiles;
-                const int32_t* row = p.block_table + static_cast<long long>(I.b) * p.bt_stride;
-                if (!ntiles) {
-                    ok = publish();
-                    continue;
-                }
-                // Q of the item's tiles (128-byte regions), once the last item's products have read theirs
-                if (nq >= 1 && !pt_wait(bar(S::B_QE), (nq - 1) & 1, p)) { ok = false; break; }
-                if (lane == 0) {
-                    const int tiles = I.tok0 + TOK < I.n ? 2 : 1;
-                    mbar_arrive_expect_tx(bar(S::B_QF), tiles * S::REGIONS * TOK * G * 128);
-                    for (int t = 0; t < tiles; ++t)
-                        for (int h = 0; h < S::REGIONS; ++h)
-                            tma_load_3d(sb0 + S::OFF_Q + t * S::QTILE + h * kPtRows * 128, &qmap, 64 * h, hk * G,
-                                        I.q0 + I.tok0 + t * TOK, bar(S::B_QF), pol);
-                }
-                __syncwarp();
-                ++nq;
-                auto entry = [&](int j) {
-                    const int tok = t0 + j * kPtKeys + lane * kStageTok;
-                    return lane < kPtKeys / kStageTok && tok < t1 ? row[page_div(tok, p.pmagic, p.pmshift)] : -1;
-                };
-                int pg = entry(0);
-                const int ahead = min(ntiles, S::NU / 2) - 1;  // the ring is full behind this tile
-                for (int j = 0; j < ntiles && ok; ++j) {
-                    const int pg_next = j + 1 < ntiles ? entry(j + 1) : -1;
-                    const int tok = t0 + j * kPtKeys + lane * kStageTok;
-                    const bool load = pg >= 0 && pg < p.num_pages;
-                    const int bytes = __popc(__ballot_sync(kFull, load)) * 2 * S::GROUP;
-                    const int krow = load ? (pg * p.Hkv + hk) * p.P + (tok - page_div(tok, p.pmagic, p.pmshift) * p.P) : 0;
+            // Round r publishes item r, loads the rest of item r - 1's tiles, then Q and the
+            // first tiles of item r.  (An item's slot is not reused before this warp
+            // publishes four items on.)
+            int hk = 0, t0 = 0, t1 = 0, ntiles = 0, j = 0, pg = -1;
+            const int32_t* row = p.block_table;
+            auto entry = [&](int x) {
+                const int tok = t0 + x * kPtKeys + lane * kStageTok;
+                return lane < kPtKeys / kStageTok && tok < t1 ? row[page_div(tok, p.pmagic, p.pmshift)] : -1;
+            };
+            for (int r = 0; ok; ++r) {
+                ok = publish();
+                bool end = false;
 #pragma unroll 1
-                    for (int v = 0; v < 2; ++v, ++u) {
-                        const int us = u % S::NU;
-                        if (u >= S::NU && !pt_wait(bar(S::B_UE + us), ((u / S::NU) - 1) & 1, p)) { ok = false; break; }
-                        if (lane == 0) mbar_arrive_expect_tx(bar(S::B_UF + us), bytes);
+                for (int part = 0; ok && part < 2; ++part) {
+                    int stop = ntiles;
+                    if (part == 1) {
+                        const PtItem& I = items[r % kPtItems];
+                        end = I.end;
+                        if (end) break;
+                        hk = I.hk;
+                        t0 = I.t0;
+                        t1 = I.t1;
+                        ntiles = I.ntiles;
+                        row = p.block_table + static_cast<long long>(I.b) * p.bt_stride;
+                        j = 0;
+                        stop = min(ntiles, S::NU / 2);  // the ring is full behind them
+                        if (!ntiles) break;
+                        pg = entry(0);
+                        // Q (128-byte regions), once the last item's products have read theirs
+                        if (nq >= 1 && !pt_wait(bar(S::B_QE), (nq - 1) & 1, p)) { ok = false; break; }
+                        if (lane == 0) {
+                            const int tiles = I.tok0 + TOK < I.n ? 2 : 1;
+                            mbar_arrive_expect_tx(bar(S::B_QF), tiles * S::REGIONS * TOK * G * 128);
+                            for (int x = 0; x < tiles * S::REGIONS; ++x) {
+                                const int t = x / S::REGIONS, h = x % S::REGIONS;
+                                tma_load_3d(sb0 + S::OFF_Q + t * S::QTILE + h * kPtRows * 128, &qmap, 64 * h, hk * G,
+                                            I.q0 + I.tok0 + t * TOK, bar(S::B_QF), pol);
+                            }
+                        }
                         __syncwarp();
-                        if (load)
-                            tma_load_4d(sb0 + S::OFF_KV + us * S::UNIT + 2 * lane * S::GROUP, &kvmap, 0, 0,
-                                        v * S::REGIONS, krow >> 3, bar(S::B_UF + us), keep);
+                        ++nq;
                     }
-                    if (ok && j == ahead) ok = publish();
-                    pg = pg_next;
+#pragma unroll 1
+                    for (; j < stop && ok; ++j) {
+                        const int pg_next = j + 1 < ntiles ? entry(j + 1) : -1;
+                        const int tok = t0 + j * kPtKeys + lane * kStageTok;
+                        const bool load = pg >= 0 && pg < p.num_pages;
+                        const int bytes = __popc(__ballot_sync(kFull, load)) * 2 * S::GROUP;
+                        const int krow = load ? (pg * p.Hkv + hk) * p.P + (tok - page_div(tok, p.pmagic, p.pmshift) * p.P) : 0;
+#pragma unroll 1
+                        for (int v = 0; v < 2; ++v, ++u) {
+                            const int us = u % S::NU;
+                            if (u >= S::NU && !pt_wait(bar(S::B_UE + us), ((u / S::NU) - 1) & 1, p)) { ok = false; break; }
+                            if (lane == 0) mbar_arrive_expect_tx(bar(S::B_UF + us), bytes);
+                            __syncwarp();
+                            if (load)
+                                tma_load_4d(sb0 + S::OFF_KV + us * S::UNIT + 2 * lane * S::GROUP, &kvmap, 0, 0,
+                                            v * S::REGIONS, krow >> 3, bar(S::B_UF + us), keep);
+                        }
+                        pg = pg_next;
+                    }
                 }
+                if (end) break;
             }
             if (!ok) {
                 // let every issued copy land before the CTA leaves
@@ -550,89 +576,78 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             // test instead, a product took 115 cycles to issue, twice its run time).
             const bool one = tc05::elect_one();
             bool ok = true;
-            int u = 0, nq = 0, nv = 0;  // nv: widened V tiles
-            int np[2] = {0, 0}, no[2] = {0, 0};  // P tiles consumed, accumulations begun
+            int u = 0, nq = 0, nv = 0;      // K/V units, Q loads, widened V tiles before the item
+            int np0 = 0, np1 = 0, no0 = 0, no1 = 0;  // per tile: P tiles consumed, accumulations begun
             for (int it = 0; ok; ++it) {
                 const int slot = it % kPtItems;
                 if (!pt_wait(bar(S::B_IF + slot), (it / kPtItems) & 1, p)) { ok = false; break; }
                 const PtItem& I = items[slot];
                 if (I.end) break;
-                const int ntiles = I.ntiles;
-                const int jb[2] = {I.jb[0], I.jb[1]}, je[2] = {I.je[0], I.je[1]};
+                const int ntiles = I.ntiles, jb0 = I.jb[0], je0 = I.je[0], jb1 = I.jb[1], je1 = I.je[1];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(S::B_IE + slot));
                 if (!ntiles) continue;
                 if (!pt_wait(bar(S::B_QF), nq & 1, p)) { ok = false; break; }
                 ++nq;
-                auto k_ready = [&](int j) {
-                    const int x = u + 2 * j;
-                    return pt_wait(bar(S::B_UF + x % S::NU), (x / S::NU) & 1, p);
-                };
-                auto qk = [&](int t, int j) {
-                    const uint64_t qd = tc05::smem_desc(sb0 + S::OFF_Q + t * S::QTILE, 16, 1024);
-                    const uint64_t kd = tc05::smem_desc(sb0 + S::OFF_KV + ((u + 2 * j) % S::NU) * S::UNIT, 16, S::GROUP);
-#pragma unroll
-                    for (int kk = 0; kk < S::ROWB / 32; ++kk) {
-                        const uint64_t qk_ = qd + (((kk >> 2) * kPtRows * 128 + (kk & 3) * 32) >> 4);
-                        const uint64_t kk_ = kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
-                        if (!one) continue;
-                        if constexpr (kFp8)
-                            tc05::mma_e4m3(tmem + kPtKeys * t, qk_, kk_, kIdS, kk > 0);
-                        else
-                            tc05::mma_f16(tmem + kPtKeys * t, qk_, kk_, kIdS, kk > 0);
-                    }
-                    if (one) tc05::commit(bar(S::B_SF + t));
-                };
-                ok = k_ready(0);
-                tc05::fence_after_sync();
-                for (int t = 0; ok && t < 2; ++t)
-                    if (jb[t] == 0 && je[t] > 0) qk(t, 0);
-                if (one) tc05::commit(bar(S::B_UE + u % S::NU));
-                if (one && ntiles == 1) tc05::commit(bar(S::B_QE));
-                for (int j = 0; ok && j < ntiles; ++j) {
-                    const int vu = u + 2 * j + 1, vb = kFp8 ? (nv + j) % 2 : 0;
-                    ok = kFp8 ? pt_wait(bar(S::B_VF + vb), ((nv + j) >> 1) & 1, p)
-                              : pt_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p);
+                // round j: the O products of key tile j, the S products of key tile j + 1.  A tile's
+                // S product goes in issue order behind its O product, which has read the P under S.
+#pragma unroll 1
+                for (int j = -1; ok && j < ntiles; ++j) {
+                    const int ku = u + 2 * (j + 1), vu = u + 2 * j + 1, vb = kFp8 ? (nv + j) & 1 : 0;
+                    if (j >= 0)
+                        ok = kFp8 ? pt_wait(bar(S::B_VF + vb), ((nv + j) >> 1) & 1, p)
+                                  : pt_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p);
                     const uint64_t vd = tc05::smem_desc(
-                        sb0 + (kFp8 ? S::OFF_V + vb * S::VUNIT : S::OFF_KV + (vu % S::NU) * S::UNIT), 1024, S::VGROUP);
-                    const uint32_t v_free = kFp8 ? bar(S::B_VE + vb) : bar(S::B_UE + vu % S::NU);
-                    bool have_k = false;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (!ok) break;
-                        if (j >= jb[t] && j < je[t]) {
-                            ok = pt_wait(bar(S::B_PF + t), np[t] & 1, p);
-                            ++np[t];
-                            if (ok && j == jb[t]) {
-                                // a new accumulation: the epilogue has drained the last one
-                                if (no[t] >= 1) ok = pt_wait(bar(S::B_OE + t), (no[t] - 1) & 1, p);
-                                ++no[t];
+                        sb0 + (kFp8 ? S::OFF_V + vb * S::VUNIT : S::OFF_KV + ((vu + S::NU) % S::NU) * S::UNIT), 1024, S::VGROUP);
+                    const uint64_t kd = tc05::smem_desc(sb0 + S::OFF_KV + (ku % S::NU) * S::UNIT, 16, S::GROUP);
+#pragma unroll 1
+                    for (int t = 0; ok && t < 2; ++t) {
+                        const int jb = t ? jb1 : jb0, je = t ? je1 : je0;
+                        const uint32_t s_addr = tmem + kPtKeys * t, o_addr = tmem + 256 + D * t;
+                        if (j >= jb && j < je) {
+                            ok = pt_wait(bar(S::B_PF + t), (t ? np1 : np0) & 1, p);
+                            if (t) ++np1; else ++np0;
+                            if (ok && j == jb) {
+                                // a new accumulation: the last one has been read out
+                                const int no = t ? no1 : no0;
+                                if (no >= 1) ok = pt_wait(bar(S::B_OE + t), (no - 1) & 1, p);
+                                if (t) ++no1; else ++no0;
                             }
                             if (!ok) break;
                             tc05::fence_after_sync();
-                            const bool more = j > jb[t];
+                            const bool more = j > jb;
 #pragma unroll
                             for (int kk = 0; kk < kPtKeys / 16; ++kk)
                                 if (one)
-                                    tc05::mma_f16_ts(tmem + 256 + D * t, tmem + kPtKeys * t + 8 * kk,
-                                                     vd + ((2 * kk * S::VGROUP) >> 4), kIdO, more || kk > 0);
+                                    tc05::mma_f16_ts(o_addr, s_addr + 8 * kk, vd + ((2 * kk * S::VGROUP) >> 4), kIdO, more || kk > 0);
                             if (one) {
                                 tc05::commit(bar(S::B_OD + t));
-                                if (j == je[t] - 1) tc05::commit(bar(S::B_OF + t));
+                                if (j == je - 1) tc05::commit(bar(S::B_OF + t));
                             }
                         }
-                        if (t == 1 && one) tc05::commit(v_free);
+                        if (j >= 0 && t == 1 && one) tc05::commit(kFp8 ? bar(S::B_VE + vb) : bar(S::B_UE + vu % S::NU));
                         if (j + 1 < ntiles) {
-                            if (!have_k) {
-                                ok = k_ready(j + 1);
-                                have_k = true;
+                            if (t == 0) {
+                                ok = pt_wait(bar(S::B_UF + ku % S::NU), (ku / S::NU) & 1, p);
                                 if (!ok) break;
                                 tc05::fence_after_sync();
                             }
-                            // in issue order behind this tile's O product, which has read the P under S
-                            if (j + 1 >= jb[t] && j + 1 < je[t]) qk(t, j + 1);
+                            if (j + 1 >= jb && j + 1 < je) {
+                                const uint64_t qd = tc05::smem_desc(sb0 + S::OFF_Q + t * S::QTILE, 16, 1024);
+#pragma unroll
+                                for (int kk = 0; kk < S::ROWB / 32; ++kk) {
+                                    const uint64_t x = qd + (((kk >> 2) * kPtRows * 128 + (kk & 3) * 32) >> 4);
+                                    const uint64_t y = kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
+                                    if (!one) continue;
+                                    if constexpr (kFp8)
+                                        tc05::mma_e4m3(s_addr, x, y, kIdS, kk > 0);
+                                    else
+                                        tc05::mma_f16(s_addr, x, y, kIdS, kk > 0);
+                                }
+                                if (one) tc05::commit(bar(S::B_SF + t));
+                            }
                             if (t == 1 && one) {
-                                tc05::commit(bar(S::B_UE + (u + 2 * (j + 1)) % S::NU));
+                                tc05::commit(bar(S::B_UE + ku % S::NU));
                                 if (j + 1 == ntiles - 1) tc05::commit(bar(S::B_QE));  // Q is spent
                             }
                         }
@@ -734,106 +749,53 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                 if constexpr (kBias)
                     if (valid) slope = p.slopes[I.hk * G + rg] * kLog2e;
                 const int bad = I.bad, lo_all = I.lo_all, hi_all = min(I.hi_all, I.t1);
-                // key tiles [zl, zh) need no V row zeroed by this tile, [ml, mh) no mask
-                // (bias: and lie before every row's position)
+                // key tiles [zl, zh) need no V row zeroed by this tile; keys [ml, mh) need no mask
                 const bool lead = t == 0 || !(I.jb[0] < I.je[0]);  // zeroes V rows of tiles that both walk
                 const int jb0 = I.jb[0], je0 = I.je[0];
                 const int zl = lo_all > t0 ? 1 : 0, zh = bad ? 0 : (hi_all - t0) / kPtKeys;
-                int ml, mh;
-                {
-                    int l0 = valid ? lo : 0, h0 = valid ? min(hi, hi_all) : 0x7fffffff;
-                    if (kBias && valid) h0 = min(h0, pos + 1);
-                    ml = (__reduce_max_sync(kFull, l0) - t0 + kPtKeys - 1) / kPtKeys;
-                    mh = bad ? 0 : (__reduce_min_sync(kFull, h0) - t0) / kPtKeys;  // below 0: rounded up, still masked
-                    if (__reduce_min_sync(kFull, h0) < t0) mh = 0;
-                }
-                // capped scores beyond the polynomial's range: two tiles in a row make the
-                // warp take the special functions for the next four
-                int wide = kCap && p.cap_far < 0.f ? 1 << 30 : 0;
+                const int ml = __reduce_max_sync(kFull, valid ? lo : 0);
+                // (with a bias no key from there on lies behind some row's position)
+                const int mh = bad ? 0 : __reduce_min_sync(kFull, valid ? min(min(hi, hi_all), kBias ? pos + 1 : hi_all) : 0x7fffffff);
                 for (int j = jb; j < je; ++j, ++ns) {
                     const int tk = t0 + j * kPtKeys;
                     if (!pt_wait(bar(S::B_SF + t), ns & 1, p)) { ok = false; break; }
                     if (warp_on) {
                         tc05::fence_after_sync();
-                        PtScore w{p.scale_log2, p.cap_in, p.cap_log2, slope, static_cast<float>(pos - tk),
-                                  lo - tk, min(hi, hi_all) - tk, bad ? pt_stages(p, I, tk) : 0xffu};
-                        const bool masked = j < ml || j >= mh;
+                        const unsigned stages = bad ? pt_stages(p, I, tk) : 0xffu;
+                        // Chunk by chunk, the next one loading: where a row's maximum has outgrown
+                        // its reference (always at the first chunk it sees) the reference moves
+                        // and O, l and the tile's earlier weights follow; then the chunk's weights,
+                        // written over its products.
                         uint32_t a[32], b[32];
-                        if (j == jb) {
-                            // the row's first reference: its maximum over the tile
-                            float top = -INFINITY;
-                            auto tops = [&](auto mask) {
-                                constexpr bool kMasked = decltype(mask)::value;
-                                tc05::ld_32x32b_x32(s_addr, a);
-                                tc05::wait_ld(a);
-                                tc05::ld_32x32b_x32(s_addr + 32, b);
-                                top = pt_top<kBias, kCap, kMasked>(a, 0, w, top);
-                                tc05::wait_ld(b);
-                                tc05::ld_32x32b_x32(s_addr + 64, a);
-                                top = pt_top<kBias, kCap, kMasked>(b, 32, w, top);
-                                tc05::wait_ld(a);
-                                tc05::ld_32x32b_x32(s_addr + 96, b);
-                                top = pt_top<kBias, kCap, kMasked>(a, 64, w, top);
-                                tc05::wait_ld(b);
-                                top = pt_top<kBias, kCap, kMasked>(b, 96, w, top);
-                            };
-                            if (masked)
-                                tops(std::true_type{});
-                            else
-                                tops(std::false_type{});
-                            m_used = kBias || top == -INFINITY ? top
-                                     : kCap ? capped(top, p.cap_in, p.cap_log2) : top * p.scale_log2;
-                        }
-                        // one pass: weights against the reference, the tile's maximum beside
-                        // them.  Where a row's maximum has outgrown the reference (or a capped
-                        // score the polynomial) the pass is repeated, O and l rescaled.
-                        uint32_t pk[64];
-                        float2 sum[2];
-#pragma unroll 1
-                        for (;;) {
-                            const float m = m_used == -INFINITY ? 0.f : m_used;
-                            float top = -INFINITY, far = 0.f;
-                            sum[0] = sum[1] = make_float2(0.f, 0.f);
-                            auto pass = [&](auto poly, auto mask) {
-                                constexpr bool kPoly = decltype(poly)::value, kMasked = decltype(mask)::value;
-                                tc05::ld_32x32b_x32(s_addr, a);
-                                tc05::wait_ld(a);
-                                tc05::ld_32x32b_x32(s_addr + 32, b);
-                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(a, pk, 0, w, p.cap_c, m, sum, top, far);
-                                tc05::wait_ld(b);
-                                tc05::ld_32x32b_x32(s_addr + 64, a);
-                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(b, pk + 16, 32, w, p.cap_c, m, sum, top, far);
-                                tc05::wait_ld(a);
-                                tc05::ld_32x32b_x32(s_addr + 96, b);
-                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(a, pk + 32, 64, w, p.cap_c, m, sum, top, far);
-                                tc05::wait_ld(b);
-                                pt_weights<kBF16, kCap, kPoly, kBias, kMasked>(b, pk + 48, 96, w, p.cap_c, m, sum, top, far);
-                            };
-                            if (kCap && wide > 4)
-                                pass(std::false_type{}, std::true_type{});
-                            else if (masked)
-                                pass(std::true_type{}, std::true_type{});
-                            else
-                                pass(std::true_type{}, std::false_type{});
+                        auto chunk = [&](uint32_t (&v)[32], int k0) {
+                            const int k = tk + k0;
+                            const bool masked = k < ml || k + 32 > mh;
+                            float scale = p.scale_log2;
                             if constexpr (kCap) {
-                                // (far stays 0 in a pass that does not depend on it)
-                                if (__any_sync(kFull, far > p.cap_far) && wide <= 4) {
-                                    wide = 8;
-                                    continue;
-                                }
+                                if (__any_sync(kFull, pt_max<true>(v) > p.cap_far))
+                                    pt_cap<false>(v, p);
+                                else
+                                    pt_cap<true>(v, p);
+                                scale = 1.f;
                             }
-                            top = kBias ? top + m
-                                  : top == -INFINITY ? top : kCap ? capped(top, p.cap_in, p.cap_log2) : top * p.scale_log2;
+                            if constexpr (kBias) {
+                                if (masked)
+                                    pt_bias<false>(v, scale, slope, static_cast<float>(pos - k));
+                                else
+                                    pt_bias<true>(v, scale, slope, static_cast<float>(pos - k));
+                                scale = 1.f;
+                            }
+                            if (masked) pt_mask(v, lo - k, min(hi, hi_all) - k, stages >> (k0 >> 4));
+                            const float top = pt_max<false>(v) * scale;
                             const bool need = top > m_used + (kBF16 ? kPtRescaleBF16 : kPtRescaleFP16);
-                            if (!__any_sync(kFull, need)) break;
-                            const float alpha = need ? fast_exp2(m_used - top) : 1.f;
-                            if (need) m_used = top;
-                            l *= alpha;
-                            if (j > jb) {
-                                if (!pt_wait(bar(S::B_OD + t), (ns - 1) & 1, p)) { ok = false; break; }
+                            if (__any_sync(kFull, need)) {
+                                const float alpha = need ? fast_exp2(m_used - top) : 1.f;
+                                if (need) m_used = top;
+                                l *= alpha;
+                                if (j > jb && !pt_wait(bar(S::B_OD + t), (ns - 1) & 1, p)) ok = false;
                                 tc05::fence_after_sync();
 #pragma unroll 1
-                                for (int c = 0; c < D; c += 16) {
+                                for (int c = 0; c < D && j > jb && ok; c += 16) {
                                     uint32_t o[16];
                                     tc05::ld_32x32b_x16(o_addr + c, o);
                                     tc05::wait_ld();
@@ -841,15 +803,40 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                                     for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                                     tc05::st_32x32b_x16(o_addr + c, o);
                                 }
+                                // (a weight written already is rounded a second time)
+#pragma unroll 1
+                                for (int c = 0; c < k0 / 2; c += 16) {
+                                    uint32_t o[16];
+                                    tc05::ld_32x32b_x16(s_addr + c, o);
+                                    tc05::wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        float x, y;
+                                        if constexpr (kBF16) bf16x2_to_f32(o[e], x, y); else f16x2_to_f32(o[e], x, y);
+                                        o[e] = pack2<kBF16>(x * alpha, y * alpha);
+                                    }
+                                    tc05::st_32x32b_x16(s_addr + c, o);
+                                }
                                 tc05::wait_st();
                             }
+                            const float m = m_used == -INFINITY ? 0.f : m_used;
+                            uint32_t pk[16];
+                            l += pt_weights<kBF16>(v, pk, scale, m);
+                            tc05::st_32x32b_x16(s_addr + k0 / 2, pk);
+                        };
+                        tc05::ld_32x32b_x32(s_addr, a);
+                        tc05::wait_ld(a);
+#pragma unroll 1
+                        for (int k0 = 0; k0 < kPtKeys; k0 += 64) {
+                            tc05::ld_32x32b_x32(s_addr + k0 + 32, b);
+                            chunk(a, k0);
+                            tc05::wait_ld(b);
+                            if (k0 == 0) tc05::ld_32x32b_x32(s_addr + 64, a);
+                            chunk(b, k0 + 32);
+                            tc05::wait_ld(a);
                         }
-                        if (!ok) break;
-                        if (kCap && wide > 0) --wide;
-                        tc05::st_32x32b_x32(s_addr, reinterpret_cast<const uint32_t(&)[32]>(pk[0]));
-                        tc05::st_32x32b_x32(s_addr + 32, reinterpret_cast<const uint32_t(&)[32]>(pk[32]));
-                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                         tc05::wait_st();
+                        if (!ok) break;
                     }
                     // V rows that no row of the unit sees (stale slots, skipped pages)
                     // are zeroed: their weight 0 must not meet a NaN
