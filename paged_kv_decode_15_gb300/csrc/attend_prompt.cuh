@@ -53,13 +53,19 @@ struct PtItem {
     int t0, t1, ntiles;            // keys of this item, tiles of 128 from t0
     int lo_all, hi_all;            // keys outside are seen by no row of the unit
     int split, nsplit, unit;
-    int jb[2], je[2];              // key tiles [jb, je) of row tile t (empty: none)
+    int jb[2], je[2];              // steps [jb, je) of row tile t (empty: none); step j is key tile pt_tile(j)
     int bad, end;                  // bad: some page lies outside the pool
     int pad[2];
 };
 
 // Types of q and the cache.
 enum PtType { kPtBF16 = 0, kPtFP16 = 1, kPtFP8 = 2 };
+
+// Key tile of step j.  With a distance bias the walk runs from the last tile to the
+// first: a row meets its largest logits first, and its reference stays (rising,
+// slopes near 1 moved it at every tile: 8192-token prompt 992 us).
+template <bool kBias>
+__device__ __forceinline__ int pt_tile(int j, int ntiles) { return kBias ? ntiles - 1 - j : j; }
 
 // NU K/V units; K and V of a key tile are one unit each (units of K have even
 // numbers, NU is even, so a slot always holds the one or the other).  e4m3: the
@@ -387,7 +393,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
     constexpr uint32_t kIdO = tc05::idesc_f16(kBF16, kPtRows, D, false, true);         // O += P V
 
     if (warp >= 8) {
-        reg_dec<88>();
+        reg_dec<104>();
         if (warp == 8) {
             // ------------------------------------------------------ loads
             if (lane == 0) {
@@ -487,8 +493,9 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             const int a = max(lo[t], t0), z = min(hi[t], t1);
-                            I.jb[t] = a < z ? (a - t0) / kPtKeys : 0;
-                            I.je[t] = a < z ? (z - t0 + kPtKeys - 1) / kPtKeys : 0;
+                            const int first = (a - t0) / kPtKeys, past = (z - t0 + kPtKeys - 1) / kPtKeys;
+                            I.jb[t] = a >= z ? 0 : kBias ? ntiles - past : first;
+                            I.je[t] = a >= z ? 0 : kBias ? ntiles - first : past;
                         }
                         I.bad = bad; I.end = 0;
                         mbar_arrive(bar(S::B_IF + slot));
@@ -505,7 +512,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             int hk = 0, t0 = 0, t1 = 0, ntiles = 0, j = 0, pg = -1;
             const int32_t* row = p.block_table;
             auto entry = [&](int x) {
-                const int tok = t0 + x * kPtKeys + lane * kStageTok;
+                const int tok = t0 + pt_tile<kBias>(x, ntiles) * kPtKeys + lane * kStageTok;
                 return lane < kPtKeys / kStageTok && tok < t1 ? row[page_div(tok, p.pmagic, p.pmshift)] : -1;
             };
             for (int r = 0; ok; ++r) {
@@ -544,7 +551,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
 #pragma unroll 1
                     for (; j < stop && ok; ++j) {
                         const int pg_next = j + 1 < ntiles ? entry(j + 1) : -1;
-                        const int tok = t0 + j * kPtKeys + lane * kStageTok;
+                        const int tok = t0 + pt_tile<kBias>(j, ntiles) * kPtKeys + lane * kStageTok;
                         const bool load = pg >= 0 && pg < p.num_pages;
                         const int bytes = __popc(__ballot_sync(kFull, load)) * 2 * S::GROUP;
                         const int krow = load ? (pg * p.Hkv + hk) * p.P + (tok - page_div(tok, p.pmagic, p.pmshift) * p.P) : 0;
@@ -577,13 +584,13 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             const bool one = tc05::elect_one();
             bool ok = true;
             int u = 0, nq = 0, nv = 0;      // K/V units, Q loads, widened V tiles before the item
-            int np0 = 0, np1 = 0, no0 = 0, no1 = 0;  // per tile: P tiles consumed, accumulations begun
+            int np[2] = {0, 0}, no[2] = {0, 0};  // per tile: P tiles consumed, accumulations begun
             for (int it = 0; ok; ++it) {
                 const int slot = it % kPtItems;
                 if (!pt_wait(bar(S::B_IF + slot), (it / kPtItems) & 1, p)) { ok = false; break; }
                 const PtItem& I = items[slot];
                 if (I.end) break;
-                const int ntiles = I.ntiles, jb0 = I.jb[0], je0 = I.je[0], jb1 = I.jb[1], je1 = I.je[1];
+                const int ntiles = I.ntiles, jbs[2] = {I.jb[0], I.jb[1]}, jes[2] = {I.je[0], I.je[1]};
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(S::B_IE + slot));
                 if (!ntiles) continue;
@@ -600,18 +607,18 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     const uint64_t vd = tc05::smem_desc(
                         sb0 + (kFp8 ? S::OFF_V + vb * S::VUNIT : S::OFF_KV + ((vu + S::NU) % S::NU) * S::UNIT), 1024, S::VGROUP);
                     const uint64_t kd = tc05::smem_desc(sb0 + S::OFF_KV + (ku % S::NU) * S::UNIT, 16, S::GROUP);
-#pragma unroll 1
-                    for (int t = 0; ok && t < 2; ++t) {
-                        const int jb = t ? jb1 : jb0, je = t ? je1 : je0;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (!ok) break;
+                        const int jb = jbs[t], je = jes[t];
                         const uint32_t s_addr = tmem + kPtKeys * t, o_addr = tmem + 256 + D * t;
                         if (j >= jb && j < je) {
-                            ok = pt_wait(bar(S::B_PF + t), (t ? np1 : np0) & 1, p);
-                            if (t) ++np1; else ++np0;
+                            ok = pt_wait(bar(S::B_PF + t), np[t] & 1, p);
+                            ++np[t];
                             if (ok && j == jb) {
                                 // a new accumulation: the last one has been read out
-                                const int no = t ? no1 : no0;
-                                if (no >= 1) ok = pt_wait(bar(S::B_OE + t), (no - 1) & 1, p);
-                                if (t) ++no1; else ++no0;
+                                if (no[t] >= 1) ok = pt_wait(bar(S::B_OE + t), (no[t] - 1) & 1, p);
+                                ++no[t];
                             }
                             if (!ok) break;
                             tc05::fence_after_sync();
@@ -688,7 +695,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     uint8_t* wide = smem + S::OFF_V + vb * S::VUNIT;
 #pragma unroll 1
                     for (int r = x; r < kPtKeys; r += 64) {
-                        const int key = t0 + j * kPtKeys + r, sw = r & 7;
+                        const int key = t0 + pt_tile<kBias>(j, ntiles) * kPtKeys + r, sw = r & 7;
                         bool seen = key >= lo_all && key < hi_all;
                         if (bad && seen) {
                             const int pg = table[page_div(key, p.pmagic, p.pmshift)];
@@ -724,7 +731,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
         }
     } else {
         // ------------------------------------------ softmax and epilogue
-        reg_inc<208>();
+        reg_inc<200>();
         const int t = warp >> 2, q4 = warp & 3, r = 32 * q4 + lane;  // row of tile t = TMEM lane
         const uint32_t lane_addr = static_cast<uint32_t>(32 * q4) << 16;
         const uint32_t s_addr = tmem + lane_addr + kPtKeys * t, o_addr = tmem + lane_addr + 256 + D * t;
@@ -756,91 +763,114 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                 const int ml = __reduce_max_sync(kFull, valid ? lo : 0);
                 // (with a bias no key from there on lies behind some row's position)
                 const int mh = bad ? 0 : __reduce_min_sync(kFull, valid ? min(min(hi, hi_all), kBias ? pos + 1 : hi_all) : 0x7fffffff);
+                int wide = 0;  // tiles left before a capped score out of the polynomial's range counts no more
+                constexpr float kRescale = kBF16 ? kPtRescaleBF16 : kPtRescaleFP16;
                 for (int j = jb; j < je; ++j, ++ns) {
-                    const int tk = t0 + j * kPtKeys;
+                    const int kt = pt_tile<kBias>(j, ntiles), tk = t0 + kt * kPtKeys;
                     if (!pt_wait(bar(S::B_SF + t), ns & 1, p)) { ok = false; break; }
                     if (warp_on) {
                         tc05::fence_after_sync();
-                        const unsigned stages = bad ? pt_stages(p, I, tk) : 0xffu;
-                        // Chunk by chunk, the next one loading: where a row's maximum has outgrown
-                        // its reference (always at the first chunk it sees) the reference moves
-                        // and O, l and the tile's earlier weights follow; then the chunk's weights,
-                        // written over its products.
-                        uint32_t a[32], b[32];
-                        auto chunk = [&](uint32_t (&v)[32], int k0) {
-                            const int k = tk + k0;
-                            const bool masked = k < ml || k + 32 > mh;
-                            float scale = p.scale_log2;
-                            if constexpr (kCap) {
-                                if (__any_sync(kFull, pt_max<true>(v) > p.cap_far))
-                                    pt_cap<false>(v, p);
-                                else
-                                    pt_cap<true>(v, p);
-                                scale = 1.f;
+                        uint32_t v[2][32];
+                        tc05::ld_32x32b_x32(s_addr, v[0]);
+                        const bool masked = tk < ml || tk + kPtKeys > mh;
+                        const float scale = (kCap || kBias) ? 1.f : p.scale_log2;
+                        bool done = false;
+                        if (!masked && j > jb && !(kCap && wide > 0)) {
+                            // A tile that every row sees whole, in one pass of straight-line code
+                            // against the reference of the tiles before it.  Its maximum comes out
+                            // beside the weights: they count only if no row has outgrown its reference
+                            // (and no capped score the polynomial).  (Decided chunk by chunk, the
+                            // pass took 1460 cycles, not 950.)
+                            const float m = m_used == -INFINITY ? 0.f : m_used;
+                            uint32_t pk[4][16];
+                            float sum = 0.f, top = -INFINITY, far = 0.f;
+                            tc05::wait_ld(v[0]);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t (&x)[32] = v[c & 1];
+                                if (c < 3) tc05::ld_32x32b_x32(s_addr + 32 * (c + 1), v[(c + 1) & 1]);
+                                if constexpr (kCap) {
+                                    far = fmaxf(far, pt_max<true>(x));
+                                    pt_cap<true>(x, p);
+                                }
+                                if constexpr (kBias) pt_bias<true>(x, kCap ? 1.f : p.scale_log2, slope, static_cast<float>(pos - tk - 32 * c));
+                                top = fmaxf(top, pt_max<false>(x));
+                                sum += pt_weights<kBF16>(x, pk[c], scale, m);
+                                if (c < 3) tc05::wait_ld(v[(c + 1) & 1]);
                             }
-                            if constexpr (kBias) {
-                                if (masked)
-                                    pt_bias<false>(v, scale, slope, static_cast<float>(pos - k));
-                                else
-                                    pt_bias<true>(v, scale, slope, static_cast<float>(pos - k));
-                                scale = 1.f;
+                            const bool grown = top * scale > m_used + kRescale, out = kCap && far > p.cap_far;
+                            done = !__any_sync(kFull, grown || out);
+                            if (done) {
+                                l += sum;
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) tc05::st_32x32b_x16(s_addr + 16 * c, pk[c]);
+                            } else {
+                                if (kCap && __any_sync(kFull, out)) wide = 8;
+                                tc05::ld_32x32b_x32(s_addr, v[0]);
                             }
-                            if (masked) pt_mask(v, lo - k, min(hi, hi_all) - k, stages >> (k0 >> 4));
-                            const float top = pt_max<false>(v) * scale;
-                            const bool need = top > m_used + (kBF16 ? kPtRescaleBF16 : kPtRescaleFP16);
+                        }
+                        if (!done) {
+                            // Any other tile, in two rolled passes: the maximum, with which the
+                            // references move (O and l follow), then the weights, written over
+                            // products that are spent
+                            const unsigned stages = bad ? pt_stages(p, I, tk) : 0xffu;
+                            const int c0 = lo - tk, c1 = min(hi, hi_all) - tk;
+                            auto logits = [&](int c) {
+                                tc05::wait_ld(v[0]);
+                                if constexpr (kCap) {
+                                    if (__any_sync(kFull, pt_max<true>(v[0]) > p.cap_far))
+                                        pt_cap<false>(v[0], p);
+                                    else
+                                        pt_cap<true>(v[0], p);
+                                }
+                                if constexpr (kBias) pt_bias<false>(v[0], kCap ? 1.f : p.scale_log2, slope, static_cast<float>(pos - tk - 32 * c));
+                                if (masked) pt_mask(v[0], c0 - 32 * c, c1 - 32 * c, stages >> (2 * c));
+                            };
+                            float top = -INFINITY;
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c) {
+                                if (c) tc05::ld_32x32b_x32(s_addr + 32 * c, v[0]);
+                                logits(c);
+                                top = fmaxf(top, pt_max<false>(v[0]));
+                            }
+                            top *= scale;
+                            const bool need = top > m_used + kRescale;
                             if (__any_sync(kFull, need)) {
                                 const float alpha = need ? fast_exp2(m_used - top) : 1.f;
                                 if (need) m_used = top;
                                 l *= alpha;
-                                if (j > jb && !pt_wait(bar(S::B_OD + t), (ns - 1) & 1, p)) ok = false;
-                                tc05::fence_after_sync();
+                                if (j > jb) {
+                                    if (!pt_wait(bar(S::B_OD + t), (ns - 1) & 1, p)) { ok = false; break; }
+                                    tc05::fence_after_sync();
 #pragma unroll 1
-                                for (int c = 0; c < D && j > jb && ok; c += 16) {
-                                    uint32_t o[16];
-                                    tc05::ld_32x32b_x16(o_addr + c, o);
-                                    tc05::wait_ld();
+                                    for (int c = 0; c < D; c += 16) {
+                                        uint32_t o[16];
+                                        tc05::ld_32x32b_x16(o_addr + c, o);
+                                        tc05::wait_ld();
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                    tc05::st_32x32b_x16(o_addr + c, o);
-                                }
-                                // (a weight written already is rounded a second time)
-#pragma unroll 1
-                                for (int c = 0; c < k0 / 2; c += 16) {
-                                    uint32_t o[16];
-                                    tc05::ld_32x32b_x16(s_addr + c, o);
-                                    tc05::wait_ld();
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) {
-                                        float x, y;
-                                        if constexpr (kBF16) bf16x2_to_f32(o[e], x, y); else f16x2_to_f32(o[e], x, y);
-                                        o[e] = pack2<kBF16>(x * alpha, y * alpha);
+                                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                        tc05::st_32x32b_x16(o_addr + c, o);
                                     }
-                                    tc05::st_32x32b_x16(s_addr + c, o);
+                                    tc05::wait_st();
                                 }
-                                tc05::wait_st();
                             }
                             const float m = m_used == -INFINITY ? 0.f : m_used;
-                            uint32_t pk[16];
-                            l += pt_weights<kBF16>(v, pk, scale, m);
-                            tc05::st_32x32b_x16(s_addr + k0 / 2, pk);
-                        };
-                        tc05::ld_32x32b_x32(s_addr, a);
-                        tc05::wait_ld(a);
 #pragma unroll 1
-                        for (int k0 = 0; k0 < kPtKeys; k0 += 64) {
-                            tc05::ld_32x32b_x32(s_addr + k0 + 32, b);
-                            chunk(a, k0);
-                            tc05::wait_ld(b);
-                            if (k0 == 0) tc05::ld_32x32b_x32(s_addr + 64, a);
-                            chunk(b, k0 + 32);
-                            tc05::wait_ld(a);
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t pk[16];
+                                tc05::ld_32x32b_x32(s_addr + 32 * c, v[0]);
+                                logits(c);
+                                l += pt_weights<kBF16>(v[0], pk, scale, m);
+                                tc05::st_32x32b_x16(s_addr + 16 * c, pk);
+                            }
+                            if (kCap && wide > 0) --wide;
                         }
                         tc05::wait_st();
                         if (!ok) break;
                     }
                     // V rows that no row of the unit sees (stale slots, skipped pages)
                     // are zeroed: their weight 0 must not meet a NaN
-                    if (!kFp8 && (j < zl || j >= zh) && (lead || j < jb0 || j >= je0)) {
+                    if (!kFp8 && (kt < zl || kt >= zh) && (lead || j < jb0 || j >= je0)) {
                         const int vu = u + 2 * j + 1, key = tk + r;
                         if (!pt_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p)) { ok = false; break; }
                         if (key < lo_all || key >= hi_all || (bad && !(pt_stages(p, I, tk) >> (r >> 4) & 1))) {
