@@ -815,25 +815,37 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                             // products that are spent
                             const unsigned stages = bad ? pt_stages(p, I, tk) : 0xffu;
                             const int c0 = lo - tk, c1 = min(hi, hi_all) - tk;
-                            auto logits = [&](int c) {
-                                tc05::wait_ld(v[0]);
+                            auto logits = [&](uint32_t (&x)[32], int c) {
                                 if constexpr (kCap) {
-                                    if (__any_sync(kFull, pt_max<true>(v[0]) > p.cap_far))
-                                        pt_cap<false>(v[0], p);
+                                    if (__any_sync(kFull, pt_max<true>(x) > p.cap_far))
+                                        pt_cap<false>(x, p);
                                     else
-                                        pt_cap<true>(v[0], p);
+                                        pt_cap<true>(x, p);
                                 }
-                                if constexpr (kBias) pt_bias<false>(v[0], kCap ? 1.f : p.scale_log2, slope, static_cast<float>(pos - tk - 32 * c));
-                                if (masked) pt_mask(v[0], c0 - 32 * c, c1 - 32 * c, stages >> (2 * c));
+                                if constexpr (kBias) pt_bias<false>(x, kCap ? 1.f : p.scale_log2, slope, static_cast<float>(pos - tk - 32 * c));
+                                if (masked) pt_mask(x, c0 - 32 * c, c1 - 32 * c, stages >> (2 * c));
+                            };
+                            // (without a bias the logit rises with q.k: the largest product gives the largest)
+                            auto tops = [&](uint32_t (&x)[32], int c) {
+                                if constexpr (kBias)
+                                    logits(x, c);
+                                else if (masked)
+                                    pt_mask(x, c0 - 32 * c, c1 - 32 * c, stages >> (2 * c));
+                                return pt_max<false>(x);
                             };
                             float top = -INFINITY;
+                            tc05::wait_ld(v[0]);
 #pragma unroll 1
-                            for (int c = 0; c < 4; ++c) {
-                                if (c) tc05::ld_32x32b_x32(s_addr + 32 * c, v[0]);
-                                logits(c);
-                                top = fmaxf(top, pt_max<false>(v[0]));
+                            for (int c = 0; c < 4; c += 2) {
+                                tc05::ld_32x32b_x32(s_addr + 32 * c + 32, v[1]);
+                                top = fmaxf(top, tops(v[0], c));
+                                tc05::wait_ld(v[1]);
+                                tc05::ld_32x32b_x32(s_addr + (c ? 0 : 64), v[0]);  // then the first chunk again
+                                top = fmaxf(top, tops(v[1], c + 1));
+                                tc05::wait_ld(v[0]);
                             }
-                            top *= scale;
+                            if constexpr (!kBias)
+                                top = top == -INFINITY ? top : kCap ? capped(top, p.cap_in, p.cap_log2) : top * p.scale_log2;
                             const bool need = top > m_used + kRescale;
                             if (__any_sync(kFull, need)) {
                                 const float alpha = need ? fast_exp2(m_used - top) : 1.f;
@@ -856,12 +868,18 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                             }
                             const float m = m_used == -INFINITY ? 0.f : m_used;
 #pragma unroll 1
-                            for (int c = 0; c < 4; ++c) {
+                            for (int c = 0; c < 4; c += 2) {
                                 uint32_t pk[16];
-                                tc05::ld_32x32b_x32(s_addr + 32 * c, v[0]);
-                                logits(c);
+                                tc05::ld_32x32b_x32(s_addr + 32 * c + 32, v[1]);
+                                logits(v[0], c);
                                 l += pt_weights<kBF16>(v[0], pk, scale, m);
+                                tc05::wait_ld(v[1]);
+                                if (c == 0) tc05::ld_32x32b_x32(s_addr + 64, v[0]);
                                 tc05::st_32x32b_x16(s_addr + 16 * c, pk);
+                                logits(v[1], c + 1);
+                                l += pt_weights<kBF16>(v[1], pk, scale, m);
+                                tc05::wait_ld(v[0]);
+                                tc05::st_32x32b_x16(s_addr + 16 * c + 16, pk);
                             }
                             if (kCap && wide > 0) --wide;
                         }
