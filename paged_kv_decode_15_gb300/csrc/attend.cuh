@@ -41,6 +41,11 @@ struct AttendParams {
     uint64_t wait_ns;
 };
 
+// Programmatic dependent launch: let the next launch start (every CTA says so once),
+// and wait for the launch before this one to have completed (no wait without one).
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Query tokens [q0, q0 + n) of request b, clamped to [0, T] and to max_q
 // tokens; a bad query_start raises the status word when `report` is set.
 __device__ __forceinline__ void request_tokens(const AttendParams& p, int b, int& q0, int& n, bool report) {
@@ -94,6 +99,88 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // (2^inf, 2^-inf) give +-1.
 __device__ __forceinline__ float capped(float qk, float cap_in, float cap_log2) {
     return cap_log2 * fmaf(-2.f, rcp_approx(1.f + fast_exp2(qk * cap_in)), 1.f);
+}
+
+// The D / 32 dims of a row that lane `lane` holds (from lane * D / 32 on).
+template <int D>
+__device__ __forceinline__ void load_row(const float* row, int lane, float (&v)[D / 32]) {
+    if constexpr (D == 128) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(row) + lane);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(row) + lane);
+        v[0] = x.x; v[1] = x.y;
+    }
+}
+
+// out[row] = v * scale, rounded once to its type.
+template <int D>
+__device__ __forceinline__ void store_row(void* out, long long row, const float (&v)[D / 32], float scale, int lane,
+                                          int dtype) {
+    float x[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) x[e] = v[e] * scale;
+    if (dtype == 3) {
+        float* dst = static_cast<float*>(out) + row * D + lane * (D / 32);
+        if constexpr (D == 128)
+            *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+        else
+            *reinterpret_cast<float2*>(dst) = make_float2(x[0], x[1]);
+    } else {
+        uint32_t h[D / 64];
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e)
+            h[e] = dtype == 0 ? pack2<true>(x[2 * e], x[2 * e + 1]) : pack2<false>(x[2 * e], x[2 * e + 1]);
+        uint16_t* dst = static_cast<uint16_t*>(out) + row * D + lane * (D / 32);
+        if constexpr (D == 128)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[1]);
+        else
+            *reinterpret_cast<uint32_t*>(dst) = h[0];
+    }
+}
+
+// Merge the partial results of one row by LSE (log2 units), a warp per row: part s
+// has its LSE at pl[s * step] and its output at po + s * step * D.  All LSEs first,
+// one per lane, then eight outputs in flight; a part without keys is never
+// read.  Partials come from other CTAs: L2 loads.  acc: the weighted sum, mx: the
+// largest LSE, ws: the sum of the weights.
+template <int D>
+__device__ __forceinline__ void merge_row(const float* pl, const float* po, long long step, int np, int lane,
+                                          float (&acc)[D / 32], float& mx, float& ws) {
+    constexpr int E = D / 32, N = 8;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    mx = -INFINITY;
+    ws = 0.f;
+    const float first = lane < np ? __ldcg(pl + lane * step) : -INFINITY;
+    mx = first;
+    for (int s = 32 + lane; s < np; s += 32) mx = fmaxf(mx, __ldcg(pl + s * step));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    if (mx == -INFINITY) return;
+    for (int s0 = 0; s0 < np; s0 += 32) {
+        const float l = s0 == 0 ? first : s0 + lane < np ? __ldcg(pl + (s0 + lane) * step) : -INFINITY;
+        const float wl = l == -INFINITY ? 0.f : fast_exp2(l - mx);
+        ws += wl;
+        const int m = min(32, np - s0);
+        for (int j = 0; j < m; j += N) {
+            float v[N][E], w[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                w[i] = __shfl_sync(kFull, wl, (j + i) & 31);
+                if (j + i >= m) w[i] = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+                if (w[i] > 0.f) load_row<D>(po + (s0 + j + i) * step * D, lane, v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(w[i], v[i][e], acc[e]);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(kFull, ws, o);
 }
 
 }  // namespace pkd

@@ -79,7 +79,10 @@ pkd_status plan_attend(int B, long long T, int max_q, int Hq, int Hkv, int D, in
         // about kStepCtas CTAs, chunks of 256 to 4096 keys (the decode grid's rule)
         const long long units = std::max(1ll, (long long)B * Hkv);
         long long splits = std::max((kStepCtas + units - 1) / units, (vis + kStepMaxChunk - 1) / kStepMaxChunk);
-        long long chunk = std::max((vis + splits - 1) / std::max(splits, 1ll), 256ll);
+        // a batch that leaves SMs idle at that goes down to 128 (one request of 611
+        // keys: 8.9 us, 256 keys 10.0, 512 12.5, 64 9.1)
+        const long long least = units * ((vis + 255) / 256) < 2 * kSms ? 128 : 256;
+        long long chunk = std::max((vis + splits - 1) / std::max(splits, 1ll), least);
         chunk = (chunk + P - 1) / P * P;
         if (chunk / P > pkd::kMaxCtaPages) chunk = (long long)pkd::kMaxCtaPages * P;
         pl.chunk = (int)chunk;
@@ -98,8 +101,12 @@ pkd_status plan_attend(int B, long long T, int max_q, int Hq, int Hkv, int D, in
     // the keys are split while the row tiles alone leave SMs idle: about two
     // items per SM, chunks of whole tiles, at least 512 keys (256 for partials,
     // whose join is a launch of its own)
-    // (partials: one item per SM, a shared prefix's items being alike)
-    long long splits = least * Hkv >= kSms ? 1 : partials ? kSms / (least * Hkv) : (2 * kSms + least * Hkv - 1) / (least * Hkv);
+    // (partials: one item per SM for a single prefix, whose items are alike, else three)
+    long long splits = least * Hkv >= kSms ? 1 : (2 * kSms + least * Hkv - 1) / (least * Hkv);
+    if (partials) {
+        splits = B == 1 ? kSms / (least * Hkv) : 3 * kSms / (most * Hkv);
+        if (splits < 1) splits = 1;
+    }
     const long long floor_chunk = partials ? 256 : 512;
     long long chunk = std::max((vis + splits - 1) / splits, floor_chunk);
     chunk = (chunk + pkd::kPtKeys - 1) / pkd::kPtKeys * pkd::kPtKeys;
@@ -202,7 +209,7 @@ pkd_status cuda_fail(cudaError_t e, const char* what) {
 
 // One pass on the planned kernel.
 pkd_status launch_pass(const pkd::AttendParams& a, const AttendPlan& pl, const void* kv_cache, pkd_dtype kv, int D,
-                       bool partials, cudaStream_t stream, const char* what) {
+                       bool partials, bool overlap, cudaStream_t stream, const char* what) {
     const uint64_t rows = (uint64_t)a.num_pages * a.Hkv * a.P;
     const int row_bytes = 2 * D * elt_bytes(kv);
     cudaError_t e;
@@ -237,14 +244,15 @@ pkd_status launch_pass(const pkd::AttendParams& a, const AttendPlan& pl, const v
         d.pmshift = a.pmshift;
         d.v_scale = a.v_scale;
         d.wait_ns = a.wait_ns;
-        e = pkd::launch_attend_step(D, (int)kv, pl.rows > 8 ? 2 : 1, tmap, a, d, dim3(a.max_splits, a.Hkv, a.B), stream);
+        e = pkd::launch_attend_step(D, (int)kv, pl.rows > 8 ? 2 : 1, tmap, a, d, dim3(a.max_splits, a.Hkv, a.B), overlap,
+                                    stream);
     } else {
         CUtensorMap kvmap, qmap;
         pkd_status st = pkd::half_stage_map(kvmap, kv_cache, rows, row_bytes, kv);
         if (st != PKD_OK) return st;
         st = pkd::query_map(qmap, a.q, D, a.Hq, (uint64_t)a.T, a.q_stride, a.G, pkd::kPtRows / a.G, kv);
         if (st != PKD_OK) return st;
-        e = pkd::launch_attend_prompt(D, (int)kv, kvmap, qmap, a, partials, pl.units * pl.max_splits, stream);
+        e = pkd::launch_attend_prompt(D, (int)kv, kvmap, qmap, a, partials, overlap, pl.units * pl.max_splits, stream);
     }
     return e == cudaSuccess ? PKD_OK : cuda_fail(e, what);
 }
@@ -288,17 +296,18 @@ const pkd_score_options kNoOptions = {0.f, nullptr, 0, nullptr, nullptr};
 }  // namespace
 
 cudaError_t pkd::launch_attend_prompt(int D, int kv_dtype, const CUtensorMap& kvmap, const CUtensorMap& qmap,
-                                      const AttendParams& p, bool partials, long long items, cudaStream_t stream) {
+                                      const AttendParams& p, bool partials, bool overlap, long long items,
+                                      cudaStream_t stream) {
     int grid = 1;
     cudaError_t e = persistent_grid(1, (int)std::min(items, 1ll << 20), grid);
     if (e != cudaSuccess) return e;
     if (kv_dtype == PKD_FP8_E4M3)
-        return D == 128 ? launch_prompt_fp8_d128(kvmap, qmap, p, partials, grid, stream) : cudaErrorInvalidValue;
+        return D == 128 ? launch_prompt_fp8_d128(kvmap, qmap, p, partials, overlap, grid, stream) : cudaErrorInvalidValue;
     if (kv_dtype == PKD_BF16)
-        return D == 128 ? launch_prompt_bf16_d128(kvmap, qmap, p, partials, grid, stream)
-                        : launch_prompt_bf16_d64(kvmap, qmap, p, partials, grid, stream);
-    return D == 128 ? launch_prompt_fp16_d128(kvmap, qmap, p, partials, grid, stream)
-                    : launch_prompt_fp16_d64(kvmap, qmap, p, partials, grid, stream);
+        return D == 128 ? launch_prompt_bf16_d128(kvmap, qmap, p, partials, overlap, grid, stream)
+                        : launch_prompt_bf16_d64(kvmap, qmap, p, partials, overlap, grid, stream);
+    return D == 128 ? launch_prompt_fp16_d128(kvmap, qmap, p, partials, overlap, grid, stream)
+                    : launch_prompt_fp16_d64(kvmap, qmap, p, partials, overlap, grid, stream);
 }
 
 extern "C" {
@@ -368,7 +377,8 @@ pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_strid
     a.lse = lse;
     a.out_dtype = (int)out_dtype;
     a.v_scale = v_scale;
-    return launch_pass(a, pl, kv_cache, kv_dtype, head_dim, false, (cudaStream_t)stream, "pkd_paged_attention launch");
+    return launch_pass(a, pl, kv_cache, kv_dtype, head_dim, false, false, (cudaStream_t)stream,
+                       "pkd_paged_attention launch");
 }
 
 size_t pkd_prefix_decode_workspace_size(int batch, int sq, int num_heads, int num_kv_heads, int head_dim,
@@ -425,9 +435,9 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
     a.sq = (int)T;  // without group_start: one group of every request
     a.max_q = (int)T;
     a.v_scale = 1.f;
-    st = launch_pass(a, pl.pre, kv_cache, kv_dtype, head_dim, true, s, "pkd_prefix_decode prefix launch");
+    st = launch_pass(a, pl.pre, kv_cache, kv_dtype, head_dim, true, false, s, "pkd_prefix_decode prefix launch");
     if (st != PKD_OK) return st;
-    // each request's own keys
+    // each request's own keys: beside the prefix (programmatic dependent launch)
     pkd::AttendParams b;
     fill(b, pl.own, ws, 1, pl.off_own, batch, T, num_heads, num_kv_heads, page_size, max_kv_len, num_pages, scale2,
          softcap);
@@ -443,7 +453,7 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
     b.lse = reinterpret_cast<float*>(ws + pl.off_own_lse);
     b.out_dtype = PKD_FP32;
     b.v_scale = 1.f;
-    st = launch_pass(b, pl.own, kv_cache, kv_dtype, head_dim, false, s, "pkd_prefix_decode launch");
+    st = launch_pass(b, pl.own, kv_cache, kv_dtype, head_dim, false, true, s, "pkd_prefix_decode launch");
     if (st != PKD_OK) return st;
     pkd::PrefixMergeParams m;
     std::memset(&m, 0, sizeof m);

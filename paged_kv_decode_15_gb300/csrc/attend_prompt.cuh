@@ -264,48 +264,6 @@ __device__ __forceinline__ void reg_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Merge the partial results of one row by LSE (log2 units): a warp per row,
-// lane l holds dims l * D/32 ...; parts s at part_lse[s * lse_step] and
-// part_out[s * lse_step * D].  Partials come from other CTAs: L2 loads.
-template <int D>
-__device__ __forceinline__ void pt_merge_row(const float* pl, const float* po, long long step, int np, int lane,
-                                             float (&acc)[D / 32], float& mx, float& ws) {
-    constexpr int E = D / 32;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    mx = -INFINITY;
-    ws = 0.f;
-    for (int s = lane; s < np; s += 32) mx = fmaxf(mx, __ldcg(pl + s * step));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-    if (mx == -INFINITY) return;
-    for (int s0 = 0; s0 < np; s0 += 32) {
-        const float l = s0 + lane < np ? __ldcg(pl + (s0 + lane) * step) : -INFINITY;
-        const float wl = l == -INFINITY ? 0.f : fast_exp2(l - mx);
-        ws += wl;
-        const int m = min(32, np - s0);
-#pragma unroll 4
-        for (int j = 0; j < m; ++j) {
-            const float w = __shfl_sync(kFull, wl, j);
-            if (w == 0.f) continue;  // an empty part is never read
-            const float* src = po + (s0 + j) * step * D + lane * E;
-            if constexpr (E == 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-                acc[0] = fmaf(w, v.x, acc[0]);
-                acc[1] = fmaf(w, v.y, acc[1]);
-                acc[2] = fmaf(w, v.z, acc[2]);
-                acc[3] = fmaf(w, v.w, acc[3]);
-            } else {
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-                acc[0] = fmaf(w, v.x, acc[0]);
-                acc[1] = fmaf(w, v.y, acc[1]);
-            }
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(kFull, ws, o);
-}
-
 // kPartials: every result is left as a partial one (for a merge that follows)
 template <int D, int kType, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kPtThreads, 1)
@@ -326,6 +284,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
     auto bar = [&](int i) { return smem_u32(bars + i); };
 
     // ------------------------------------------------------------ set-up
+    launch_dependents();  // the next launch may fill SMs that this one leaves
     if (tid == 0) {
         for (int i = 0; i < S::NU; ++i) {
             mbar_init(bar(S::B_UF + i), 1);
@@ -996,11 +955,9 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                         for (int x = q4; x < rows; x += 4) {
                             const long long mrow = static_cast<long long>(I.q0 + I.tok0 + x / G) * p.Hq + I.hk * G + x % G;
                             float acc[D / 32], mx, ws;
-                            pt_merge_row<D>(p.part_lse + mrow, p.part_out + mrow * D, step, nsplit, lane, acc, mx, ws);
+                            merge_row<D>(p.part_lse + mrow, p.part_out + mrow * D, step, nsplit, lane, acc, mx, ws);
                             const float sc = ws > 0.f ? p.v_scale / ws : 0.f;
-#pragma unroll
-                            for (int e = 0; e < D / 32; ++e)
-                                store_out(p.out, mrow * D + lane * (D / 32) + e, acc[e] * sc, p.out_dtype);
+                            store_row<D>(p.out, mrow, acc, sc, lane, p.out_dtype);
                             if (lane == 0 && p.lse) p.lse[mrow] = ws > 0.f ? (mx + __log2f(ws)) * kLn2 : -INFINITY;
                         }
                         if ((tid & 127) == 0) p.counters[I.unit] = 0;  // every part has arrived: ready for the next call
@@ -1021,6 +978,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
         tc05::fence_after_sync();
         tc05::dealloc(tmem, 512);
     }
+    wait_dependency();  // its own end implies that of the launch it overlaps
     // the last CTA to leave resets the item counter for the next call
     if (tid == 0) {
         const int prev = atom_add_acq_rel_gpu(p.queue + 1);

@@ -4,8 +4,8 @@
 namespace pkd {
 
 cudaError_t launch_prompt_fp8_d128(const CUtensorMap& kvmap, const CUtensorMap& qmap, const AttendParams& p, bool partials,
-                               int grid, cudaStream_t stream) {
-    return launch_prompt_typed<128, kPtFP8>(kvmap, qmap, p, partials, grid, stream);
+                               bool overlap, int grid, cudaStream_t stream) {
+    return launch_prompt_typed<128, kPtFP8>(kvmap, qmap, p, partials, overlap, grid, stream);
 }
 
 }  // namespace pkd

@@ -7,8 +7,8 @@
 // 16-key stages through its own ring of TMA copies, products on mma.sync
 // (the rows are too few for a tcgen05 tile), partial results merged by LSE by
 // the last chunk to arrive.  Memory bound: every visible key is read once.
-// The row intervals, positions and slopes of the (at most 16) rows are kept
-// in shared memory; a stage inside every row's interval skips the mask.
+// A lane holds two of the (at most 16) rows: their intervals, positions and slopes
+// stay in registers; a stage inside every row's interval skips the mask.
 #pragma once
 
 #include "attend.cuh"
@@ -32,8 +32,7 @@ struct StepShape {
     static constexpr int OFF_BARS = BIG;
     static constexpr int OFF_PAGES = OFF_BARS + kNW * NBUF * 8;
     static constexpr int OFF_Q = OFF_PAGES + kMaxCtaPages * 4 + 16;
-    static constexpr int OFF_ROWS = OFF_Q + (W::kCtaQ ? kStepRows * QSTRIDE : 0);  // lo, hi, pos, slope
-    static constexpr int OFF_ML = OFF_ROWS + 4 * kStepRows * 4;
+    static constexpr int OFF_ML = OFF_Q + (W::kCtaQ ? kStepRows * QSTRIDE : 0);
     static constexpr int OFF_FLAG = OFF_ML + 2 * kNW * kStepRows * 4;
     static constexpr int SMEM = OFF_FLAG + 16 + 1024;
 };
@@ -47,18 +46,13 @@ __device__ __forceinline__ const uint8_t* step_q_row(const AttendParams& a, int 
 }
 
 template <class W, int D, int ELT, int NBUF>
-__global__ void __launch_bounds__(kNW * 32, W::kMinBlocks)
-attend_step_kernel(const __grid_constant__ CUtensorMap tmap, const AttendParams a, const DecodeParams d) {
+__device__ __forceinline__ void attend_step(const CUtensorMap& tmap, const AttendParams& a, const DecodeParams& d) {
     using S = StepShape<W, D, ELT, NBUF>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::OFF_BARS);
     int* pages = reinterpret_cast<int*>(smem + S::OFF_PAGES);
     uint8_t* qs = smem + S::OFF_Q;
-    int* row_lo = reinterpret_cast<int*>(smem + S::OFF_ROWS);
-    int* row_hi = row_lo + kStepRows;
-    int* row_pos = row_hi + kStepRows;
-    float* row_slope = reinterpret_cast<float*>(row_pos + kStepRows);
     float* wm = reinterpret_cast<float*>(smem + S::OFF_ML);
     float* wl = wm + kNW * kStepRows;
     int* flag = reinterpret_cast<int*>(smem + S::OFF_FLAG);
@@ -92,39 +86,32 @@ attend_step_kernel(const __grid_constant__ CUtensorMap tmap, const AttendParams 
     w.nsplit = hi_all > 0 ? (hi_all - begin + a.chunk - 1) / a.chunk : 0;
     if (w.split >= max(w.nsplit, 1)) return;
 
-    // local launch parameters in the decode kernels' terms: this request's rows
-    // as rows 0 .. M-1 of query 0, its outputs and partial slots behind them
-    DecodeParams p = d;
-    p.sq = n;
-    p.M = M;
-    const long long orow = static_cast<long long>(q0) - static_cast<long long>(w.b) * n;
-    p.out = static_cast<uint8_t*>(d.out) + orow * a.Hq * D * (d.out_dtype == 3 ? 4 : 2);
-    p.lse = d.lse ? d.lse + orow * a.Hq : nullptr;
-    const long long unit = static_cast<long long>(w.b) * a.Hkv + w.hk;
-    p.part_out = d.part_out + unit * a.max_splits * (d.M - M) * D;
-    p.part_lse = d.part_lse + unit * a.max_splits * (d.M - M);
     if (w.nsplit == 0) {
         for (int e = tid; e < M * D; e += blockDim.x) {
-            store_out(p.out, out_index(p, w.b, w.hk, e / D, e % D, D), 0.f, p.out_dtype);
-            if (e % D == 0 && p.lse) p.lse[out_index(p, w.b, w.hk, e / D, 0, 1)] = -INFINITY;
+            const int r = e / D, i = r / a.G;
+            const long long row = static_cast<long long>(q0 + i) * a.Hq + w.hk * a.G + (r - i * a.G);
+            store_out(d.out, row * D + e % D, 0.f, d.out_dtype);
+            if (e % D == 0 && d.lse) d.lse[row] = -INFINITY;
         }
         return;
     }
+    const DecodeParams& p = d;  // the stage helpers' parameters
     w.t0 = begin + w.split * a.chunk;
     w.t1 = min(w.t0 + a.chunk, hi_all);
-    for (int r = tid; r < kStepRows; r += blockDim.x) {
-        int lo = 0, hi = 0, pos = 0;
-        float slope = 0.f;
+    // this lane's rows g and g + 8
+    const int g = lane >> 2, tg = lane & 3;
+    int row_lo[2], row_hi[2], row_pos[2];
+    float row_slope[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = 8 * h + g, i = r / a.G;
+        row_lo[h] = row_hi[h] = row_pos[h] = 0;
+        row_slope[h] = 0.f;
         if (r < M) {
-            const int i = r / a.G;
-            token_keys(a, q0, n, L, prefix, i, lo, hi);
-            pos = L - n + i;
-            if (a.slopes) slope = a.slopes[w.hk * a.G + (r - i * a.G)] * kLog2e;
+            token_keys(a, q0, n, L, prefix, i, row_lo[h], row_hi[h]);
+            row_pos[h] = L - n + i - 2 * tg;  // less the lane's first key of a stage
+            if (a.slopes) row_slope[h] = a.slopes[w.hk * a.G + (r - i * a.G)] * kLog2e;
         }
-        row_lo[r] = lo;
-        row_hi[r] = hi;
-        row_pos[r] = pos;
-        row_slope[r] = slope;
     }
 
     const int nst = (w.t1 - w.t0 + kStageTok - 1) / kStageTok;
@@ -167,7 +154,6 @@ attend_step_kernel(const __grid_constant__ CUtensorMap tmap, const AttendParams 
         wp.load_q(smem_u32(qs), S::QSTRIDE, lane);
     } else {
         // e4m3 A fragments straight from global memory (zero padding rows)
-        const int g = lane >> 2, tg = lane & 3;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = h * 8 + g;
@@ -209,14 +195,22 @@ attend_step_kernel(const __grid_constant__ CUtensorMap tmap, const AttendParams 
             __syncwarp();
         }
         const bool masked = nvalid < kStageTok || tok0 < lo_in || tok0 + kStageTok > hi_in;
+        // the distance of the lane's first key of the stage; the others lie constants behind it
+        float dist[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) dist[h] = bias ? static_cast<float>(row_pos[h] - tok0) : 0.f;
         wp.consume_scored(
             st, S::HALF, nvalid, masked,
-            [&](float qk, int row, int kt) {
+            [&](float qk, int, int h, int kt) {
                 float s = cap_log2 > 0.f ? capped(qk, cap_in, cap_log2) : qk * scale2;
-                if (bias) s = fmaf(-row_slope[row], fabsf(static_cast<float>(row_pos[row] - tok0 - kt)), s);
+                if (bias) s = fmaf(-row_slope[h], fabsf(dist[h] - static_cast<float>(kt - 2 * tg)), s);
                 return s;
             },
-            [&](int row, int kt) { return tok0 + kt >= row_lo[row] && tok0 + kt < row_hi[row]; }, lane);
+            [&](int row, int kt) {
+                const int h = row >> 3;
+                return tok0 + kt >= (h ? row_lo[1] : row_lo[0]) && tok0 + kt < (h ? row_hi[1] : row_hi[0]);
+            },
+            lane);
         __syncwarp();
         if (lane == 0 && k + NBUF < my_n) {
             fence_proxy_async();
@@ -235,7 +229,68 @@ attend_step_kernel(const __grid_constant__ CUtensorMap tmap, const AttendParams 
     float* O = reinterpret_cast<float*>(smem);
     wp.store(O + warp * kStepRows * S::OSTRIDE, wm + warp * kStepRows, wl + warp * kStepRows, S::OSTRIDE, lane);
     __syncthreads();
-    cta_finish<D, S::OSTRIDE>(p, w, O, wm, wl, kStepRows, flag);
+
+    // ---- a warp per row: the warps' states joined, then written, or left as a partial
+    // result that the last chunk's CTA to arrive merges by LSE
+    constexpr int E = D / 32;
+    const bool single = w.nsplit == 1;
+    const long long slots = (static_cast<long long>(w.b) * a.Hkv + w.hk) * a.max_splits * d.M;  // [split][row] of the unit
+    auto out_row = [&](int r) {
+        const int i = r / a.G;
+        return static_cast<long long>(q0 + i) * a.Hq + w.hk * a.G + (r - i * a.G);
+    };
+    for (int r = warp; r < M; r += kNW) {
+        float mx = -INFINITY, lsum = 0.f, o[E];
+#pragma unroll
+        for (int k = 0; k < kNW; ++k) mx = fmaxf(mx, wm[k * kStepRows + r]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+        if (mx != -INFINITY) {
+#pragma unroll
+            for (int k = 0; k < kNW; ++k) {
+                const float s = fast_exp2(wm[k * kStepRows + r] - mx);
+                lsum += wl[k * kStepRows + r] * s;
+                const float* src = O + (k * kStepRows + r) * S::OSTRIDE + lane * E;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(src[e], s, o[e]);
+            }
+        }
+        const float inv = lsum > 0.f ? 1.f / lsum : 0.f, l2 = lsum > 0.f ? mx + __log2f(lsum) : -INFINITY;
+        if (single) {
+            store_row<D>(d.out, out_row(r), o, inv * a.v_scale, lane, d.out_dtype);
+            if (lane == 0 && d.lse) d.lse[out_row(r)] = l2 * kLn2;
+        } else {
+            const long long slot = slots + static_cast<long long>(w.split) * d.M + r;
+#pragma unroll
+            for (int e = 0; e < E; ++e) __stcg(d.part_out + slot * D + lane * E + e, o[e] * inv);
+            if (lane == 0) __stcg(d.part_lse + slot, l2);
+        }
+    }
+    if (single) return;
+    __syncthreads();
+    const long long unit = static_cast<long long>(w.b) * a.Hkv + w.hk;
+    if (tid == 0) {
+        const int last = atom_add_acq_rel_gpu(a.counters + unit) == w.nsplit - 1;
+        if (last) a.counters[unit] = 0;  // every part has arrived: ready for the next call
+        *flag = last;
+    }
+    __syncthreads();
+    if (!*flag) return;
+    for (int r = warp; r < M; r += kNW) {
+        float acc[E], mx, ws;
+        merge_row<D>(d.part_lse + slots + r, d.part_out + (slots + r) * D, d.M, w.nsplit, lane, acc, mx, ws);
+        store_row<D>(d.out, out_row(r), acc, ws > 0.f ? a.v_scale / ws : 0.f, lane, d.out_dtype);
+        if (lane == 0 && d.lse) d.lse[out_row(r)] = ws > 0.f ? (mx + __log2f(ws)) * kLn2 : -INFINITY;
+    }
+}
+
+// kMin: CTAs per SM that the register budget aims for
+template <class W, int D, int ELT, int NBUF, int kMin>
+__global__ void __launch_bounds__(kNW * 32, kMin)
+attend_step_kernel(const __grid_constant__ CUtensorMap tmap, const AttendParams a, const DecodeParams d) {
+    launch_dependents();
+    attend_step<W, D, ELT, NBUF>(tmap, a, d);
+    wait_dependency();  // its own end implies that of the launch it overlaps
 }
 
 }  // namespace pkd

@@ -98,7 +98,7 @@ struct Fp8MmaWarp : MmaWarp<128, false, MT, NT, true> {
         }
     }
 
-    // A stage whose logits are score(q.k, row, kt), masked or not.
+    // A stage whose logits are score(q.k, row, h, kt), masked or not.
     template <class Score, class Visible>
     __device__ __forceinline__ void consume_scored(uint32_t st, int half, int nvalid, bool masked, Score score,
                                                    Visible visible, int lane) {

@@ -209,13 +209,13 @@ struct MmaWarp {
     __device__ __forceinline__ void softmax(float (&sacc)[MT][2][4], uint32_t (&pb)[NT][2], int nvalid,
                                             float scale2, float bias2, Visible visible, int lane) {
         softmax_scored<kMasked>(
-            sacc, pb, nvalid, [&](float acc, int, int) { return fmaf(acc, scale2, bias2); }, visible, lane);
+            sacc, pb, nvalid, [&](float acc, int, int, int) { return fmaf(acc, scale2, bias2); }, visible, lane);
     }
 
     // Online softmax of S: updates the row statistics, rescales O when a
     // row's maximum moved, and returns P^T (rounded to the operand type) as
-    // the B fragments of the P.V product.  score(q.k, row, kt) is the logit of
-    // key kt for query row `row` in log2 units.
+    // the B fragments of the P.V product.  score(q.k, row, h, kt) is the logit of
+    // key kt for query row `row` (row half h of its tile) in log2 units.
     template <bool kMasked, class Score, class Visible>
     __device__ __forceinline__ void softmax_scored(float (&sacc)[MT][2][4], uint32_t (&pb)[NT][2], int nvalid,
                                                    Score score, Visible visible, int lane) {
@@ -235,7 +235,7 @@ struct MmaWarp {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int kt = n * 8 + 2 * tg + e;
-                        float s = score(sacc[mt][n][2 * h + e], row, kt);
+                        float s = score(sacc[mt][n][2 * h + e], row, h, kt);
                         if constexpr (kMasked) {
                             if (!(kt < nvalid && visible(row, kt))) s = -INFINITY;
                         }
@@ -300,7 +300,7 @@ struct MmaWarp {
         }
     }
 
-    // A stage whose logits are score(q.k, row, kt), masked or not.
+    // A stage whose logits are score(q.k, row, h, kt), masked or not.
     template <class Score, class Visible>
     __device__ __forceinline__ void consume_scored(uint32_t st, int half, int nvalid, bool masked, Score score,
                                                    Visible visible, int lane) {

@@ -3,8 +3,8 @@
 //
 // One warp per output row; lane l holds dims l * D/32 onwards.  Everything it
 // reads was written by the launches before it and mostly still lies in L2.
+#include "attend.cuh"
 #include "attend_launch.h"
-#include "attend_prompt.cuh"
 
 namespace pkd {
 
@@ -25,33 +25,30 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixMergePara
         const int len = min(max(p.prefix_lens[lo], 0), p.max_prefix_len);
         np = min((len + p.chunk - 1) / p.chunk, p.max_splits);
     }
+    wait_dependency();  // the two passes before it
     float acc[E], mx, ws;
-    pt_merge_row<D>(p.part_lse + row, p.part_out + static_cast<long long>(row) * D, p.rows, np, lane, acc, mx, ws);
+    merge_row<D>(p.part_lse + row, p.part_out + static_cast<long long>(row) * D, p.rows, np, lane, acc, mx, ws);
     const float own = p.own_lse[row] * kLog2e;
     if (own != -INFINITY) {
         const float top = fmaxf(mx, own);
         const float a = mx == -INFINITY ? 0.f : fast_exp2(mx - top), w = fast_exp2(own - top);
-        const float* src = p.own_out + static_cast<long long>(row) * D + lane * E;
+        float own_row[E];
+        load_row<D>(p.own_out + static_cast<long long>(row) * D, lane, own_row);
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * src[e];
+        for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * own_row[e];
         ws = ws * a + w;
         mx = top;
     }
     const float sc = ws > 0.f ? p.v_scale / ws : 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        store_out(p.out, static_cast<long long>(row) * D + lane * E + e, acc[e] * sc, p.out_dtype);
+    store_row<D>(p.out, row, acc, sc, lane, p.out_dtype);
     if (lane == 0 && p.lse) p.lse[row] = ws > 0.f ? (mx + __log2f(ws)) * kLn2 : -INFINITY;
 }
 
 cudaError_t launch_prefix_merge(int D, const PrefixMergeParams& p, cudaStream_t stream) {
     if (p.rows == 0) return cudaSuccess;
-    const unsigned grid = static_cast<unsigned>((p.rows + 3) / 4);
-    if (D == 128)
-        prefix_merge_kernel<128><<<grid, 128, 0, stream>>>(p);
-    else
-        prefix_merge_kernel<64><<<grid, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+    const dim3 grid(static_cast<unsigned>((p.rows + 3) / 4));
+    return D == 128 ? launch_kernel(prefix_merge_kernel<128>, grid, 128, 0, true, stream, p)
+                    : launch_kernel(prefix_merge_kernel<64>, grid, 128, 0, true, stream, p);
 }
 
 }  // namespace pkd
