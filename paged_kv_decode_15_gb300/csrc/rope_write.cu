@@ -18,6 +18,8 @@
 #include <cmath>
 
 #include "launch.h"
+#include "packed.cuh"
+#include "page_math.h"
 #include "ptx.cuh"
 
 namespace pkd {
@@ -34,7 +36,9 @@ struct RopeParams {
     long long q_stride, k_stride, v_stride, q_out_stride, max_position, num_slots;
     int Hq, Hkv, P, rd;
     float q_scale, k_scale, v_scale;
-    float q_inv, k_inv, v_inv;  // 1/scale where rope_divide holds, else 0
+    float q_inv, k_inv, v_inv;  // 1/scale where rope_store8 takes it, else 0
+    uint32_t pmagic;            // slot / P for slots below 2^31
+    int pmshift;
 };
 
 __device__ __forceinline__ uint32_t rope_e4m3x2(float lo, float hi) {
@@ -43,55 +47,64 @@ __device__ __forceinline__ uint32_t rope_e4m3x2(float lo, float hi) {
     return r;
 }
 
-// x / scale, correctly rounded, from y = 1/scale correctly rounded: q = x y is
-// within an ulp, the remainder x - q scale is exact in one fma, and q + r y
-// rounds to the quotient (Markstein, 1990; y's significand not all ones, no
-// underflow that e4m3 would see: the host checks the scale's range).  Beyond
-// e4m3's range, where r may overflow, q itself saturates the same; a zero q
-// keeps its sign.
-// rope_prompt (32768 tokens, e4m3) takes this instead of a division per value.
-__device__ __forceinline__ float rope_divide(float x, float scale, float y) {
-    const float q = x * y;
-    const float r = fmaf(-q, scale, x);
-    const float a = fabsf(q);
-    return a > 0.f && a < 1024.f ? fmaf(r, y, q) : q;
-}
-
 template <bool kBF16>
-__device__ __forceinline__ void rope_widen(const uint4& v, float (&f)[8]) {
+__device__ __forceinline__ void rope_widen(const uint4& v, float2 (&f)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (kBF16)
-            bf16x2_to_f32(w[i], f[2 * i], f[2 * i + 1]);
+            bf16x2_to_f32(w[i], f[i].x, f[i].y);
         else
-            f16x2_to_f32(w[i], f[2 * i], f[2 * i + 1]);
+            f16x2_to_f32(w[i], f[i].x, f[i].y);
     }
 }
 
-// Eight values to `dst`: rounded to the 16-bit type, or as e4m3(x / scale).
 template <bool kBF16>
-__device__ __forceinline__ void rope_store(uint8_t* dst, const float (&f)[8], bool fp8, float scale, float inv) {
-    if (!fp8) {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(pack2<kBF16>(f[0], f[1]), pack2<kBF16>(f[2], f[3]),
-                                                    pack2<kBF16>(f[4], f[5]), pack2<kBF16>(f[6], f[7]));
-        return;
-    }
-    uint32_t h[4];
+__device__ __forceinline__ void rope_store16(uint8_t* dst, const float2 (&f)[4]) {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack2<kBF16>(f[0].x, f[0].y), pack2<kBF16>(f[1].x, f[1].y),
+                                                pack2<kBF16>(f[2].x, f[2].y), pack2<kBF16>(f[3].x, f[3].y));
+}
+
+// Eight values as e4m3(x / scale), the quotient correctly rounded, from their
+// negatives n = -x.  With y = 1/scale correctly rounded, q = n (-y) is within an ulp
+// of the quotient, the remainder r = q scale + n is exact in one fma, and q - r y
+// rounds to the quotient (Markstein, 1990; y's significand not all ones, no
+// underflow that e4m3 would see: the host checks the scale's range and passes
+// y = 0 where a division is needed).  Taken from -x, a zero keeps its sign.  Eight
+// with one far beyond e4m3's range, whose remainder could overflow, are divided.
+// All on packed operations (with a division per value
+// rope_prompt_fp8 took 207 us, with the correction in single ones 171 us).
+__device__ __forceinline__ void rope_store8(uint8_t* dst, const float2 (&n)[4], float scale, float y) {
+    float2 q[4];
+    float top = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = inv != 0.f ? rope_divide(f[2 * i], scale, inv) : __fdiv_rn(f[2 * i], scale);
-        const float b = inv != 0.f ? rope_divide(f[2 * i + 1], scale, inv) : __fdiv_rn(f[2 * i + 1], scale);
-        h[i] = rope_e4m3x2(a, b);
+        q[i] = mul2(n[i], both(-y));
+        top = max3(top, fabsf(q[i].x), fabsf(q[i].y));
+    }
+    uint32_t h[4];
+    if (y != 0.f && top < 1073741824.f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            q[i] = fma2(fma2(q[i], both(scale), n[i]), both(-y), q[i]);
+            h[i] = rope_e4m3x2(q[i].x, q[i].y);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = rope_e4m3x2(__fdiv_rn(-n[i].x, scale), __fdiv_rn(-n[i].y, scale));
     }
     *reinterpret_cast<uint2*>(dst) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeHeads = 3;  // heads in flight per thread
 
+// Heads in flight per thread and blocks per SM.  The e4m3 forms have the arithmetic
+// to hide too and go by threads: rope_prompt_fp8 takes 122 us with one head and ten
+// blocks, 151 us with three heads and the five blocks that their registers leave.
 template <int D, bool kBF16, bool kQ8, bool kKV8, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kQ8 || kKV8 ? 10 : 7) rope_write_kernel(const RopeParams p) {
+    constexpr int kRopeHeads = kQ8 || kKV8 ? 1 : 3;
+    constexpr bool kNegTurn = kQ8 && kKV8;   // every turned value goes to e4m3: turned to its negative
     constexpr int U = D / 16;                // threads per head
     constexpr int HS = kRopeThreads / U;     // heads side by side
     constexpr int KE = kKV8 ? 1 : 2, QE = kQ8 ? 1 : 2;
@@ -111,7 +124,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopePara
     };
     const bool known = pos >= 0 && pos < p.max_position;
     const bool cached = slot >= 0 && slot < p.num_slots;
-    float c[8], s[8];
+    // cache row of the token's slot in head 0 (heads are P rows apart)
+    long long row0 = 0;
+    if (cached) {
+        const long long page = p.num_slots <= 0x7fffffffll ? page_div(static_cast<int>(slot), p.pmagic, p.pmshift) : slot / p.P;
+        row0 = page * p.Hkv * p.P + (slot - page * p.P);
+    }
+    float2 c[4], s[4];  // cosines and sines of the thread's eight pairs
     for (int base = hs; base < H; base += kRopeHeads * HS) {
         uint4 a[kRopeHeads], b[kRopeHeads];
 #pragma unroll
@@ -127,9 +146,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopePara
         if (!known) return;  // a position outside the table: nothing of the token is written
         if (base == hs && turn) {
             const float4* row = reinterpret_cast<const float4*>(p.table + pos * p.rd) + 2 * u;
-            const float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(row + p.rd / 8), s1 = __ldg(row + p.rd / 8 + 1);
-            c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w; c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
-            s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w; s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
+            float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(row + p.rd / 8), s1 = __ldg(row + p.rd / 8 + 1);
+            if constexpr (kNegTurn) {
+                c0 = make_float4(-c0.x, -c0.y, -c0.z, -c0.w); c1 = make_float4(-c1.x, -c1.y, -c1.z, -c1.w);
+                s0 = make_float4(-s0.x, -s0.y, -s0.z, -s0.w); s1 = make_float4(-s1.x, -s1.y, -s1.z, -s1.w);
+            }
+            c[0] = make_float2(c0.x, c0.y); c[1] = make_float2(c0.z, c0.w); c[2] = make_float2(c1.x, c1.y); c[3] = make_float2(c1.z, c1.w);
+            s[0] = make_float2(s0.x, s0.y); s[1] = make_float2(s0.z, s0.w); s[2] = make_float2(s1.x, s1.y); s[3] = make_float2(s1.z, s1.w);
         }
 #pragma unroll
         for (int i = 0; i < kRopeHeads; ++i) {
@@ -138,52 +161,54 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopePara
             const bool is_q = h < p.Hq, val = h >= p.Hq + p.Hkv;
             if (!is_q && !cached) continue;
             const int d0 = val ? 16 * u : e0, d1 = val ? 16 * u + 8 : e1;
+            const bool fp8 = is_q ? kQ8 : kKV8;
             uint8_t* dst;
-            if (is_q) {
+            if (is_q)
                 dst = p.q_out + QE * (t * p.q_out_stride + h * D);
-            } else {
-                const long long page = slot / p.P;
-                const int off = static_cast<int>(slot - page * p.P), hk = val ? h - p.Hq - p.Hkv : h - p.Hq;
-                dst = p.cache + KE * (((page * p.Hkv + hk) * p.P + off) * 2 * D + (val ? D : 0));
-            }
-            if ((val || !turn) && !(is_q ? kQ8 : kKV8)) {  // the input's bits
+            else
+                dst = p.cache + KE * ((row0 + static_cast<long long>(val ? h - p.Hq - p.Hkv : h - p.Hq) * p.P) * 2 * D + (val ? D : 0));
+            if ((val || !turn) && !fp8) {  // the input's bits
                 *reinterpret_cast<uint4*>(dst + 2 * d0) = a[i];
                 *reinterpret_cast<uint4*>(dst + 2 * d1) = b[i];
                 continue;
             }
-            float x[8], y[8];
+            float2 x[4], y[4];
+            if (fp8 && (val || !turn || !kNegTurn)) {  // rope_store8 takes negatives
+                a[i] = make_uint4(a[i].x ^ 0x80008000u, a[i].y ^ 0x80008000u, a[i].z ^ 0x80008000u, a[i].w ^ 0x80008000u);
+                b[i] = make_uint4(b[i].x ^ 0x80008000u, b[i].y ^ 0x80008000u, b[i].z ^ 0x80008000u, b[i].w ^ 0x80008000u);
+            }
             rope_widen<kBF16>(a[i], x);
             rope_widen<kBF16>(b[i], y);
             if (!val && turn) {
-                if constexpr (kInterleaved) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float x1 = x[2 * j], x2 = x[2 * j + 1], y1 = y[2 * j], y2 = y[2 * j + 1];
-                        x[2 * j] = x1 * c[j] - x2 * s[j];
-                        x[2 * j + 1] = x2 * c[j] + x1 * s[j];
-                        y[2 * j] = y1 * c[4 + j] - y2 * s[4 + j];
-                        y[2 * j + 1] = y2 * c[4 + j] + y1 * s[4 + j];
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float x1 = x[j], x2 = y[j];
-                        x[j] = x1 * c[j] - x2 * s[j];
-                        y[j] = x2 * c[j] + x1 * s[j];
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (kInterleaved) {
+                        // pairs (x[j].x, x[j].y) and (y[j].x, y[j].y): table entries j and 4 + j
+                        const float cx = j & 1 ? c[j >> 1].y : c[j >> 1].x, sx = j & 1 ? s[j >> 1].y : s[j >> 1].x;
+                        const float cy = j & 1 ? c[2 + (j >> 1)].y : c[2 + (j >> 1)].x, sy = j & 1 ? s[2 + (j >> 1)].y : s[2 + (j >> 1)].x;
+                        x[j] = fma2(x[j], both(cx), mul2(make_float2(x[j].y, x[j].x), make_float2(-sx, sx)));
+                        y[j] = fma2(y[j], both(cy), mul2(make_float2(y[j].y, y[j].x), make_float2(-sy, sy)));
+                    } else {
+                        const float2 x1 = x[j], x2 = y[j];
+                        x[j] = fma2(x1, c[j], mul2(x2, make_float2(-s[j].x, -s[j].y)));
+                        y[j] = fma2(x2, c[j], mul2(x1, s[j]));
                     }
                 }
             }
-            const int elt = is_q ? QE : KE;
-            const bool fp8 = is_q ? kQ8 : kKV8;
-            const float scale = is_q ? p.q_scale : val ? p.v_scale : p.k_scale;
-            const float inv = is_q ? p.q_inv : val ? p.v_inv : p.k_inv;
-            rope_store<kBF16>(dst + elt * d0, x, fp8, scale, inv);
-            rope_store<kBF16>(dst + elt * d1, y, fp8, scale, inv);
+            if (fp8) {
+                const float scale = is_q ? p.q_scale : val ? p.v_scale : p.k_scale;
+                const float inv = is_q ? p.q_inv : val ? p.v_inv : p.k_inv;
+                rope_store8(dst + d0, x, scale, inv);
+                rope_store8(dst + d1, y, scale, inv);
+            } else {
+                rope_store16<kBF16>(dst + 2 * d0, x);
+                rope_store16<kBF16>(dst + 2 * d1, y);
+            }
         }
     }
 }
 
-// 1/s, correctly rounded, where rope_divide is exact: s within 2^+-60 and its
+// 1/s, correctly rounded, where rope_store8 is exact with it: s within 2^+-60 and its
 // significand not all ones; else 0 (an IEEE division per value).
 static float division_inverse(float s) {
     int e;
@@ -270,6 +295,7 @@ extern "C" pkd_status pkd_rope_cache_write(const void* q, int64_t q_stride, cons
     p.Hkv = num_kv_heads;
     p.P = page_size;
     p.rd = rotary_dim;
+    pkd::page_magic(page_size, p.pmagic, p.pmshift);
     p.q_scale = q_scale;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
