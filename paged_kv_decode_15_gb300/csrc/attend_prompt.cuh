@@ -42,6 +42,9 @@ constexpr int kPtThreads = 384;
 constexpr int kPtItems = 4;        // work-item ring
 constexpr int kPtMaxBatch = 2048;  // requests whose tile prefix the CTA keeps in shared memory
 constexpr int kPtL2Bytes = 64 << 20;  // keys and values walked together
+// Row-tile pairs that a launch orders by weight (with a document mask, whose weights
+// take a look at every token, at most kPtMaxDocOrder), and items per CTA up to which it does.
+constexpr int kPtMaxOrder = 512, kPtMaxDocOrder = 192, kPtOrderItems = 16;
 // A row's reference moves when its maximum has grown by more than this (log2
 // units).  The weights only must not overflow the operand type: bf16 has fp32's
 // range, fp16 ends at 2^16.  (With 2^8 for both, half of the key tiles of scores
@@ -90,8 +93,10 @@ struct PtShape {
     static constexpr int OFF_STAGE = OFF_Q + 2 * QTILE;  // 2 KB per softmax warp: 64 bytes of 32 rows
     static constexpr int OFF_ITEM = OFF_STAGE + 8 * 2048;
     static constexpr int OFF_PREF = OFF_ITEM + kPtItems * static_cast<int>(sizeof(PtItem));
-    static constexpr int OFF_SCAN = OFF_PREF + (kPtMaxBatch + 4) * 4;  // 16 warp sums, an arrival flag
-    static constexpr int OFF_BAR = (OFF_SCAN + 128 + 7) & ~7;
+    static constexpr int OFF_SCAN = OFF_PREF + (kPtMaxBatch + 4) * 4;  // 16 warp sums, arrival flags
+    static constexpr int OFF_ORDER = OFF_SCAN + 128;     // uint16 [kPtMaxOrder]: row-tile pairs, longest first
+    static constexpr int OFF_BAR = (OFF_ORDER + kPtMaxOrder * 2 + 7) & ~7;
+    static_assert(8 * 2048 >= kPtMaxOrder * 2, "weights fit the staging area");
     // units full/empty, Q full/empty, S full, P full, O step done, O full/drained, item full/empty, widened V, drain
     static constexpr int B_UF = 0, B_UE = B_UF + NU, B_QF = B_UE + NU, B_QE = B_QF + 1, B_SF = B_QE + 1;
     static constexpr int B_PF = B_SF + 2, B_OD = B_PF + 2, B_OF = B_OD + 2, B_OE = B_OF + 2, B_IF = B_OE + 2;
@@ -114,6 +119,16 @@ __device__ __forceinline__ unsigned pt_stages(const AttendParams& p, const PtIte
         if (pg >= 0 && pg < p.num_pages) stages |= 1u << s;
     }
     return stages;
+}
+
+// The request whose units (row-tile pairs times `mul`) hold unit r; pref: prefix of the pairs.
+__device__ __forceinline__ int pt_request(const int* pref, int B, int mul, int r) {
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<long long>(pref[mid]) * mul <= r) lo = mid; else hi = mid;
+    }
+    return lo;
 }
 
 // Every lane of the warp waits, with a warp-uniform result: false after kWaitNs of
@@ -242,6 +257,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
     PtItem* items = reinterpret_cast<PtItem*>(smem + S::OFF_ITEM);
     int* pref = reinterpret_cast<int*>(smem + S::OFF_PREF);
     int* scan = reinterpret_cast<int*>(smem + S::OFF_SCAN);
+    uint16_t* order = reinterpret_cast<uint16_t*>(smem + S::OFF_ORDER);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + S::OFF_TMEM);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.G, TOK = kPtRows / G;  // whole tokens per row tile
@@ -306,6 +322,46 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             __syncthreads();
         }
         if (tid == 0) pref[0] = 0;
+        __syncthreads();
+    }
+    // Few items per CTA: the longest are handed out first, whatever the lengths and
+    // masks.  Every CTA ranks the pairs alike, by key tiles and then by number
+    // (packed documents, 416 items on 152 CTAs: the last CTA ended after twice the mean time).
+    const int npairs = pref[p.B];
+    const bool ordered = npairs > 1 && npairs <= (p.doc_start ? kPtMaxDocOrder : kPtMaxOrder) &&
+                         npairs * p.Hkv > static_cast<int>(gridDim.x) &&
+                         npairs * p.Hkv <= kPtOrderItems * static_cast<int>(gridDim.x);
+    if (ordered) {
+        uint16_t* weight = reinterpret_cast<uint16_t*>(smem + S::OFF_STAGE);
+        // a thread per pair -- its first and last token bound the others' keys -- or,
+        // with documents, a warp that looks at every token
+        const int width = p.doc_start ? 32 : 1;
+        for (int x = tid / width; x < npairs; x += kPtThreads / width) {
+            const int b = pt_request(pref, p.B, 1, x);
+            int q0, n, lo = 0x7fffffff, hi = 0;
+            request_tokens(p, b, q0, n, false);
+            const int L = request_len(p, b, false), prefix = p.prefix_lens ? p.prefix_lens[b] : 0;
+            const int a0 = (x - pref[b]) * 2 * TOK, a1 = min(a0 + 2 * TOK, n);
+            const int step = width == 1 ? max(a1 - 1 - a0, 1) : 32;
+            for (int i = a0 + (width == 1 ? 0 : lane); i < a1; i += step) {
+                int k0, k1;
+                token_keys(p, q0, n, L, prefix, i, k0, k1);
+                if (k0 < k1) lo = min(lo, k0), hi = max(hi, k1);
+            }
+            if (width == 32) {
+                lo = __reduce_min_sync(kFull, lo);
+                hi = __reduce_max_sync(kFull, hi);
+            }
+            weight[x] = static_cast<uint16_t>(min(65535, hi > lo ? (hi - lo + kPtKeys - 1) / kPtKeys : 0));
+        }
+        __syncthreads();
+        for (int x = tid; x < npairs; x += kPtThreads) {
+            const int mine = weight[x];
+            int rank = 0;
+#pragma unroll 4
+            for (int y = 0; y < npairs; ++y) rank += weight[y] > mine || (weight[y] == mine && y < x);
+            order[rank] = static_cast<uint16_t>(x);
+        }
     }
     tc05::fence_before_sync();
     __syncthreads();
@@ -348,24 +404,31 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     }
                     int next = 0;
                     if (lane == 0) next = static_cast<int>(gridDim.x) + atomicAdd(p.queue, 1);
-                    // item idx: splits innermost; within a request groups of kv heads
-                    // whose keys and values fit half of L2 together, in each the row tiles
-                    // from the last (the longest, causal) to the first, all heads of the
-                    // group per tile -- the short items come last
+                    // item idx: splits innermost, then the kv heads of a pair, by `order`; or
+                    // request by request groups of kv heads whose keys and values fit half of
+                    // L2 together, in each the row tiles from the last (the longest, causal) to
+                    // the first, all heads of the group per tile
                     const int split = idx % p.max_splits, r1 = idx / p.max_splits;
-                    int lo_b = 0, hi_b = p.B;
-                    while (hi_b - lo_b > 1) {
-                        const int mid = (lo_b + hi_b) >> 1;
-                        if (static_cast<long long>(pref[mid]) * p.Hkv <= r1) lo_b = mid; else hi_b = mid;
+                    int b, pair, hk;
+                    if (ordered) {
+                        hk = r1 % p.Hkv;
+                        pair = order[r1 / p.Hkv];
+                        b = pt_request(pref, p.B, 1, pair);
+                        pair -= pref[b];
+                    } else {
+                        b = pt_request(pref, p.B, p.Hkv, r1);
                     }
-                    const int b = lo_b, npair = pref[b + 1] - pref[b], r2 = r1 - pref[b] * p.Hkv;
                     int q0, n;
                     request_tokens(p, b, q0, n, false);
-                    const int L = request_len(p, b, r2 == 0 && split == 0 && lane == 0);
+                    if (!ordered) {
+                        const int npair = pref[b + 1] - pref[b], r2 = r1 - pref[b] * p.Hkv;
+                        const int group = max(1, min(p.Hkv, kPtL2Bytes / (2 * S::ROWB) / max(request_len(p, b, false), 1)));
+                        const int g = r2 / (npair * group), width = min(group, p.Hkv - g * group), r3 = r2 - g * npair * group;
+                        pair = npair - 1 - r3 / width;
+                        hk = g * group + r3 % width;
+                    }
+                    const int L = request_len(p, b, pair == 0 && hk == 0 && split == 0 && lane == 0);
                     const int prefix = p.prefix_lens ? p.prefix_lens[b] : 0;
-                    const int group = max(1, min(p.Hkv, kPtL2Bytes / (2 * S::ROWB) / max(L, 1)));
-                    const int g = r2 / (npair * group), width = min(group, p.Hkv - g * group), r3 = r2 - g * npair * group;
-                    const int pair = npair - 1 - r3 / width, hk = g * group + r3 % width;
                     const int tok0 = pair * 2 * TOK;
                     int lo[2], hi[2];
 #pragma unroll
