@@ -296,7 +296,7 @@ pkd_status pkd_rope_cache_write(const void* q, int64_t q_stride, const void* key
 
 /*
  * Score modifications and masks of pkd_paged_attention; zero-initialised: none.
- *   softcap       c > 0: the scaled score s becomes c * tanh(s / c)
+ *   softcap       c > 0 (1e-20 to 1e20): the scaled score s becomes c * tanh(s / c)
  *   alibi_slopes  device fp32 [num_heads]: slope * |position - key| is then
  *                 subtracted (a distance bias), or NULL
  *   window        w > 0: a token at position p sees keys from p - (w - 1) on

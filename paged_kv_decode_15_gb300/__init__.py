@@ -18,6 +18,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+from threading import get_ident as _thread
 
 import torch
 
@@ -345,15 +346,21 @@ def cache_write(key, value, slot_mapping, kv_cache, k_scale=1.0, v_scale=1.0, st
     return kv_cache
 
 
-# Host time of the calls below counts in a decode step: they compare device
-# indexes, take raw stream handles and enter a device or stream context only
-# where it differs from the current one.
+# The host time of the calls below is most of a small step's: they compare device
+# indexes, take raw stream handles, enter a device or stream context only where it
+# differs from the current one, and check what is right in few expressions; the
+# helpers that say what is wrong run only then.
+_I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
+_CODES = {torch.bfloat16: BF16, torch.float16: FP16, torch.uint8: FP8_E4M3, torch.float8_e4m3fn: FP8_E4M3,
+          torch.float32: FP32}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_capturing = torch.cuda.is_current_stream_capturing
 
 
-def _one_device(**tensors):
-    """The index of the CUDA device that all the given tensors (or None) live on."""
+def _device_error(**tensors):
+    """Raise for tensors that are not all on one CUDA device."""
     index = None
     for name, t in tensors.items():
         if t is not None:
@@ -364,24 +371,29 @@ def _one_device(**tensors):
                 index = d
             elif d != index:
                 raise ValueError(f"{name} is on cuda:{d}, other arguments on cuda:{index}")
-    return index
+
+
+def _code(dtype):
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
 
 
 def _elsewhere(index, stream):
-    """A context for a call whose device or stream is not the current one, or None."""
+    """The context of a call whose device or stream is not the current one, or None."""
     if stream is not None:
         if stream.device.index != index:
             raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
-        if stream.cuda_stream != _raw_stream(index) or torch.cuda.current_device() != index:
+        if stream.cuda_stream != _raw_stream(index) or _current_device() != index:
             return torch.cuda.stream(stream)
-    elif torch.cuda.current_device() != index:
+    elif _current_device() != index:
         return torch.cuda.device(index)
     return None
 
 
-def _token_rows(t, shape, name):
-    """Token stride of t [T, heads, D], whose tokens must be contiguous rows of heads * D."""
-    T, H, D = shape
+def _token_stride(t, T, H, D, name):
+    """Token stride of t [T, H, D], whose tokens must be contiguous rows of H * D."""
     a, b, c = t.stride()
     if c != 1 or (b != D and H > 1):
         raise ValueError(f"{name} must be [tokens, heads, head_dim] with contiguous rows per token")
@@ -393,18 +405,22 @@ _WS_HEAD = 256 + 4 * 65536  # PKD_ATTENTION_WORKSPACE_HEAD
 
 
 def _call_workspace(nbytes, index, stream):
-    """A zeroed workspace for a call on the current stream: one kept per stream
-    (grown as needed), or, while the stream is capturing, one of the graph's own
-    (zeroed by the graph), so that two graphs never share one."""
-    if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
-        _check(load_library().pkd_workspace_init(ws.data_ptr(), _WS_HEAD, stream))
-        return ws
-    ws = _call_ws.get((index, stream))
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
-        _check(load_library().pkd_workspace_init(ws.data_ptr(), _WS_HEAD, stream))
-        _call_ws[(index, stream)] = ws
+    """A zeroed workspace for a call on the current stream: one kept per stream and
+    host thread (grown as needed; launches of two threads' calls may alternate on a
+    stream), or, while the stream is capturing, one of the graph's own (zeroed by
+    the graph), so that two graphs never share one."""
+    if not _capturing():
+        key = (index, stream, _thread())
+        ws = _call_ws.get(key)
+        if ws is not None and ws[1] >= nbytes:
+            return ws
+    else:
+        key = None
+    t = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+    _check(load_library().pkd_workspace_init(t.data_ptr(), _WS_HEAD, stream))
+    ws = (t.data_ptr(), nbytes, t)
+    if key is not None:
+        _call_ws[key] = ws
     return ws
 
 
@@ -418,72 +434,76 @@ def rope_cache_write(q, key, value, positions, cos_sin, slot_mapping, kv_cache, 
     type, or uint8 / float8_e4m3fn).  Returns the rotated q (q_out, allocated
     when not given; of type q_out_dtype: q's, or e4m3(q / q_scale)).
     """
-    index = _one_device(key=key, q=q, value=value, positions=positions, cos_sin=cos_sin, slot_mapping=slot_mapping,
-                        kv_cache=kv_cache, q_out=q_out)
-    ctx = _elsewhere(index, stream)
-    if ctx is not None:
-        with ctx:
-            return rope_cache_write(q, key, value, positions, cos_sin, slot_mapping, kv_cache, interleaved=interleaved,
-                                    q_out=q_out, q_out_dtype=q_out_dtype, q_scale=q_scale, k_scale=k_scale,
-                                    v_scale=v_scale)
-    lib = _lib or load_library()
+    index = key.get_device()
+    if index < 0 or value.get_device() != index or positions.get_device() != index or \
+            cos_sin.get_device() != index or slot_mapping.get_device() != index or kv_cache.get_device() != index or \
+            (q is not None and q.get_device() != index) or (q_out is not None and q_out.get_device() != index):
+        _device_error(key=key, q=q, value=value, positions=positions, cos_sin=cos_sin, slot_mapping=slot_mapping,
+                      kv_cache=kv_cache, q_out=q_out)
+    if stream is not None or _current_device() != index:
+        ctx = _elsewhere(index, stream)
+        if ctx is not None:
+            with ctx:
+                return rope_cache_write(q, key, value, positions, cos_sin, slot_mapping, kv_cache,
+                                        interleaved=interleaved, q_out=q_out, q_out_dtype=q_out_dtype, q_scale=q_scale,
+                                        k_scale=k_scale, v_scale=v_scale)
     shape = key.shape
     T, Hkv, D = shape
     num_pages, cache_heads, P, twoD = kv_cache.shape
-    if value.shape != shape or value.dtype != key.dtype:
+    max_position, rotary_dim = cos_sin.shape
+    dtype = key.dtype
+    if value.shape != shape or value.dtype != dtype:
         raise ValueError("value must have key's shape and dtype")
     if cache_heads != Hkv or twoD != 2 * D or not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be contiguous [num_pages, num_kv_heads, page_size, 2 * head_dim]")
-    if positions.dtype != torch.int64 or slot_mapping.dtype != torch.int64 or cos_sin.dtype != torch.float32:
+    if positions.dtype is not _I64 or slot_mapping.dtype is not _I64 or cos_sin.dtype is not _F32:
         raise TypeError("positions and slot_mapping must be int64, cos_sin float32")
-    max_position, rotary_dim = cos_sin.shape
     if positions.dim() != 1 or slot_mapping.dim() != 1 or positions.numel() != T or slot_mapping.numel() != T or not (
             positions.is_contiguous() and slot_mapping.is_contiguous() and cos_sin.is_contiguous()):
         raise ValueError("positions and slot_mapping must be contiguous [T], cos_sin contiguous")
-    ks, vs = _token_rows(key, shape, "key"), _token_rows(value, shape, "value")
+    ks, vs = _token_stride(key, T, Hkv, D, "key"), _token_stride(value, T, Hkv, D, "value")
     Hq = qs = qos = 0
-    in_dt = q_dt = dtype_code(key.dtype)
+    qp = qop = None
+    in_dt = q_dt = _code(dtype)
     if q is not None:
-        qshape = q.shape
-        Hq = qshape[1]
-        if q.dtype != key.dtype or qshape[0] != T or qshape[2] != D:
+        qT, Hq, qD = qshape = q.shape
+        if q.dtype != dtype or qT != T or qD != D:
             raise ValueError("q must be [T, num_heads, head_dim] of key's dtype")
-        qs = _token_rows(q, qshape, "q")
+        qs, qp = _token_stride(q, T, Hq, D, "q"), q.data_ptr()
         if q_out is None:
-            q_out = torch.empty(qshape, dtype=q_out_dtype or q.dtype, device=q.device)
+            q_out = torch.empty(qshape, dtype=q_out_dtype or dtype, device=q.device)
             qos = Hq * D
         else:
             if q_out.shape != qshape:
                 raise ValueError("q_out must have q's shape")
-            qos = _token_rows(q_out, qshape, "q_out")
-        q_dt = dtype_code(q_out.dtype)
-    status = lib.pkd_rope_cache_write(
-        q.data_ptr() if q is not None else None, qs, key.data_ptr(), ks, value.data_ptr(), vs, in_dt,
-        positions.data_ptr(), cos_sin.data_ptr(), max_position, rotary_dim, 1 if interleaved else 0,
-        slot_mapping.data_ptr(), T, Hq, Hkv, D, P, num_pages, kv_cache.data_ptr(), dtype_code(kv_cache.dtype), k_scale,
-        v_scale, q_out.data_ptr() if q is not None else None, qos, q_dt, q_scale, _raw_stream(index))
+            qos = _token_stride(q_out, T, Hq, D, "q_out")
+        q_dt, qop = _code(q_out.dtype), q_out.data_ptr()
+    status = (_lib or load_library()).pkd_rope_cache_write(
+        qp, qs, key.data_ptr(), ks, value.data_ptr(), vs, in_dt, positions.data_ptr(), cos_sin.data_ptr(), max_position,
+        rotary_dim, 1 if interleaved else 0, slot_mapping.data_ptr(), T, Hq, Hkv, D, P, num_pages, kv_cache.data_ptr(),
+        _code(kv_cache.dtype), k_scale, v_scale, qop, qos, q_dt, q_scale, _raw_stream(index))
     if status:
         _check(status)
     return q_out
 
 
-def _options(index, T, Hq, B, window, softcap, alibi_slopes, prefix_lens, doc_start):
+def _options(T, Hq, B, window, softcap, alibi_slopes, prefix_lens, doc_start):
     if alibi_slopes is prefix_lens is doc_start is None and not window and not softcap:
         return None
-    for name, t, dtype, n in (("alibi_slopes", alibi_slopes, torch.float32, Hq),
-                              ("prefix_lens", prefix_lens, torch.int32, B), ("doc_start", doc_start, torch.int32, T)):
-        if t is not None and (t.dtype != dtype or t.dim() != 1 or t.numel() != n or not t.is_contiguous()):
+    if alibi_slopes is prefix_lens is doc_start is None:
+        return ScoreOptions(softcap, None, window, None, None)
+    for name, t, dtype, n in (("alibi_slopes", alibi_slopes, _F32, Hq), ("prefix_lens", prefix_lens, _I32, B),
+                              ("doc_start", doc_start, _I32, T)):
+        if t is not None and (t.dtype is not dtype or t.dim() != 1 or t.numel() != n or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n}")
     return ScoreOptions(softcap, alibi_slopes.data_ptr() if alibi_slopes is not None else None, window,
                         prefix_lens.data_ptr() if prefix_lens is not None else None,
                         doc_start.data_ptr() if doc_start is not None else None)
 
 
-def _check_paged(D, kv_cache, block_table, seq_lens, what="block_table"):
-    """(rows, columns, row stride) of a block table, checked with its lengths and the cache."""
-    if kv_cache.dim() != 4 or kv_cache.shape[3] != 2 * D or not kv_cache.is_contiguous():
-        raise ValueError("kv_cache must be contiguous [num_pages, num_kv_heads, page_size, 2 * head_dim]")
-    if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+def _check_table(block_table, seq_lens, what="block_table"):
+    """(rows, columns, row stride) of a block table, checked with its lengths."""
+    if block_table.dtype is not _I32 or seq_lens.dtype is not _I32:
         raise TypeError(f"{what} and its lengths must be int32")
     if block_table.dim() != 2:
         raise ValueError(f"{what} must be [batch, columns]")
@@ -494,6 +514,13 @@ def _check_paged(D, kv_cache, block_table, seq_lens, what="block_table"):
     return rows, columns, a if rows > 1 else max(a, columns)
 
 
+def _check_cache(D, kv_cache):
+    """(pages, kv heads, page size) of a cache of heads of D."""
+    if kv_cache.dim() != 4 or kv_cache.shape[3] != 2 * D or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache must be contiguous [num_pages, num_kv_heads, page_size, 2 * head_dim]")
+    return kv_cache.shape[:3]
+
+
 def _results(out, lse, shape, dtype, device):
     """out and lse of a call: the given ones, checked, or new ones."""
     if out is None:
@@ -501,8 +528,8 @@ def _results(out, lse, shape, dtype, device):
     elif out.shape != shape or not out.is_contiguous():
         raise ValueError(f"out must be contiguous {tuple(shape)}")
     if lse is None:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=device)
-    elif lse.shape != shape[:-1] or not lse.is_contiguous() or lse.dtype != torch.float32:
+        lse = torch.empty(shape[:-1], dtype=_F32, device=device)
+    elif lse.shape != shape[:-1] or not lse.is_contiguous() or lse.dtype is not _F32:
         raise ValueError(f"lse must be contiguous float32 {tuple(shape[:-1])}")
     return out, lse
 
@@ -541,42 +568,48 @@ def paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, *, c
     max_kv_len (default the table's capacity) bound the lengths on the host.
     Returns (out [T, Hq, D], lse fp32 [T, Hq]).
     """
-    index = _one_device(q=q, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, query_start=query_start,
-                        alibi_slopes=alibi_slopes, prefix_lens=prefix_lens, doc_start=doc_start, out=out, lse=lse,
-                        workspace=workspace)
-    ctx = _elsewhere(index, stream)
-    if ctx is not None:
-        with ctx:
-            return paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, causal=causal, window=window,
-                                   softcap=softcap, alibi_slopes=alibi_slopes, prefix_lens=prefix_lens,
-                                   doc_start=doc_start, max_query_len=max_query_len, max_kv_len=max_kv_len,
-                                   q_scale=q_scale, k_scale=k_scale, v_scale=v_scale, out=out, lse=lse,
-                                   out_dtype=out_dtype, workspace=workspace)
-    lib = _lib or load_library()
-    shape = q.shape
-    T, Hq, D = shape
-    qs = _token_rows(q, shape, "q")
-    B, columns, stride = _check_paged(D, kv_cache, block_table, seq_lens)
-    num_pages, Hkv, P, _ = kv_cache.shape
-    if query_start.dtype != torch.int32 or query_start.dim() != 1 or query_start.numel() != B + 1 or \
+    index = q.get_device()
+    if index < 0 or kv_cache.get_device() != index or block_table.get_device() != index or \
+            seq_lens.get_device() != index or query_start.get_device() != index or \
+            not (alibi_slopes is prefix_lens is doc_start is out is lse is workspace is None):
+        _device_error(q=q, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, query_start=query_start,
+                      alibi_slopes=alibi_slopes, prefix_lens=prefix_lens, doc_start=doc_start, out=out, lse=lse,
+                      workspace=workspace)
+    if stream is not None or _current_device() != index:
+        ctx = _elsewhere(index, stream)
+        if ctx is not None:
+            with ctx:
+                return paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, causal=causal,
+                                       window=window, softcap=softcap, alibi_slopes=alibi_slopes,
+                                       prefix_lens=prefix_lens, doc_start=doc_start, max_query_len=max_query_len,
+                                       max_kv_len=max_kv_len, q_scale=q_scale, k_scale=k_scale, v_scale=v_scale,
+                                       out=out, lse=lse, out_dtype=out_dtype, workspace=workspace)
+    T, Hq, D = shape = q.shape
+    qs = _token_stride(q, T, Hq, D, "q")
+    num_pages, Hkv, P = _check_cache(D, kv_cache)
+    B, columns, stride = _check_table(block_table, seq_lens)
+    if query_start.dtype is not _I32 or query_start.dim() != 1 or query_start.numel() != B + 1 or \
             not query_start.is_contiguous():
         raise ValueError("query_start must be a contiguous int32 tensor [batch + 1]")
-    opt = _options(index, T, Hq, B, window, softcap, alibi_slopes, prefix_lens, doc_start)
+    opt = _options(T, Hq, B, window, softcap, alibi_slopes, prefix_lens, doc_start)
     if max_query_len is None:
         max_query_len = max(T, 1)
     if max_kv_len is None:
         max_kv_len = columns * P
-    q_dt, kv_dt = dtype_code(q.dtype), dtype_code(kv_cache.dtype)
-    out, lse = _results(out, lse, shape, out_dtype or (torch.bfloat16 if kv_dt == FP8_E4M3 else q.dtype), q.device)
+    dtype = q.dtype
+    q_dt, kv_dt = _code(dtype), _code(kv_cache.dtype)
+    out, lse = _results(out, lse, shape, out_dtype or (_BF16 if kv_dt == FP8_E4M3 else dtype), q.device)
     s = _raw_stream(index)
     if workspace is None:
-        workspace = _call_workspace(_attention_bytes(B, T, max_query_len, Hq, Hkv, D, P, max_kv_len, kv_dt, window,
-                                                     prefix_lens is not None), index, s)
-    status = lib.pkd_paged_attention(
+        ws, ws_bytes, keep = _call_workspace(_attention_bytes(B, T, max_query_len, Hq, Hkv, D, P, max_kv_len, kv_dt,
+                                                              window, prefix_lens is not None), index, s)
+    else:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    status = (_lib or load_library()).pkd_paged_attention(
         q.data_ptr(), q_dt, qs, kv_cache.data_ptr(), kv_dt, num_pages, block_table.data_ptr(), stride,
         seq_lens.data_ptr(), query_start.data_ptr(), B, T, max_query_len, Hq, Hkv, D, P, max_kv_len, scale, q_scale,
-        k_scale, v_scale, opt, out.data_ptr(), dtype_code(out.dtype), lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), FLAG_CAUSAL if causal else 0, s)
+        k_scale, v_scale, opt, out.data_ptr(), _code(out.dtype), lse.data_ptr(), ws, ws_bytes,
+        FLAG_CAUSAL if causal else 0, s)
     if status:
         _check(status)
     return out, lse
@@ -593,48 +626,56 @@ def prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens,
     all); block_table, seq_lens: the requests' own keys behind the prefix.
     Returns (out [B, sq, Hq, D], lse fp32 [B, sq, Hq]) over both.
     """
-    index = _one_device(q=q, kv_cache=kv_cache, prefix_table=prefix_table, prefix_lens=prefix_lens,
-                        block_table=block_table, seq_lens=seq_lens, group_start=group_start, out=out, lse=lse,
-                        workspace=workspace)
-    ctx = _elsewhere(index, stream)
-    if ctx is not None:
-        with ctx:
-            return prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, scale,
-                                 group_start=group_start, causal=causal, softcap=softcap, max_prefix_len=max_prefix_len,
-                                 max_kv_len=max_kv_len, q_scale=q_scale, k_scale=k_scale, v_scale=v_scale, out=out,
-                                 lse=lse, out_dtype=out_dtype, workspace=workspace)
-    lib = _lib or load_library()
+    index = q.get_device()
+    if index < 0 or kv_cache.get_device() != index or prefix_table.get_device() != index or \
+            prefix_lens.get_device() != index or block_table.get_device() != index or \
+            seq_lens.get_device() != index or (group_start is not None and group_start.get_device() != index) or \
+            not (out is lse is workspace is None):
+        _device_error(q=q, kv_cache=kv_cache, prefix_table=prefix_table, prefix_lens=prefix_lens,
+                      block_table=block_table, seq_lens=seq_lens, group_start=group_start, out=out, lse=lse,
+                      workspace=workspace)
+    if stream is not None or _current_device() != index:
+        ctx = _elsewhere(index, stream)
+        if ctx is not None:
+            with ctx:
+                return prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, scale,
+                                     group_start=group_start, causal=causal, softcap=softcap,
+                                     max_prefix_len=max_prefix_len, max_kv_len=max_kv_len, q_scale=q_scale,
+                                     k_scale=k_scale, v_scale=v_scale, out=out, lse=lse, out_dtype=out_dtype,
+                                     workspace=workspace)
     if q.dim() != 4 or not q.is_contiguous():
         raise ValueError("q must be contiguous [batch, sq, num_heads, head_dim]")
-    shape = q.shape
-    B, sq, Hq, D = shape
-    rows, columns, stride = _check_paged(D, kv_cache, block_table, seq_lens)
-    groups, pcolumns, pstride = _check_paged(D, kv_cache, prefix_table, prefix_lens, "prefix_table")
-    num_pages, Hkv, P, _ = kv_cache.shape
+    B, sq, Hq, D = shape = q.shape
+    num_pages, Hkv, P = _check_cache(D, kv_cache)
+    rows, columns, stride = _check_table(block_table, seq_lens)
+    groups, pcolumns, pstride = _check_table(prefix_table, prefix_lens, "prefix_table")
     if rows != B:
         raise ValueError("block_table must have one row per request")
     if group_start is None:
         if groups != 1:
             raise ValueError("group_start is needed with more than one prefix")
-    elif group_start.dtype != torch.int32 or group_start.dim() != 1 or group_start.numel() != groups + 1 or \
+    elif group_start.dtype is not _I32 or group_start.dim() != 1 or group_start.numel() != groups + 1 or \
             not group_start.is_contiguous():
         raise ValueError("group_start must be a contiguous int32 tensor [groups + 1]")
     if max_prefix_len is None:
         max_prefix_len = pcolumns * P
     if max_kv_len is None:
         max_kv_len = columns * P
-    q_dt, kv_dt = dtype_code(q.dtype), dtype_code(kv_cache.dtype)
-    out, lse = _results(out, lse, shape, out_dtype or (torch.bfloat16 if kv_dt == FP8_E4M3 else q.dtype), q.device)
+    dtype = q.dtype
+    q_dt, kv_dt = _code(dtype), _code(kv_cache.dtype)
+    out, lse = _results(out, lse, shape, out_dtype or (_BF16 if kv_dt == FP8_E4M3 else dtype), q.device)
     s = _raw_stream(index)
     if workspace is None:
-        workspace = _call_workspace(_prefix_bytes(B, sq, Hq, Hkv, D, P, groups, max_prefix_len, max_kv_len, kv_dt),
-                                    index, s)
-    status = lib.pkd_prefix_decode(
+        ws, ws_bytes, keep = _call_workspace(_prefix_bytes(B, sq, Hq, Hkv, D, P, groups, max_prefix_len, max_kv_len,
+                                                           kv_dt), index, s)
+    else:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    status = (_lib or load_library()).pkd_prefix_decode(
         q.data_ptr(), q_dt, kv_cache.data_ptr(), kv_dt, num_pages, prefix_table.data_ptr(), pstride,
         prefix_lens.data_ptr(), group_start.data_ptr() if group_start is not None else None, groups, max_prefix_len,
         block_table.data_ptr(), stride, seq_lens.data_ptr(), B, sq, Hq, Hkv, D, P, max_kv_len, scale, q_scale, k_scale,
-        v_scale, softcap, out.data_ptr(), dtype_code(out.dtype), lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), FLAG_CAUSAL if causal else 0, s)
+        v_scale, softcap, out.data_ptr(), _code(out.dtype), lse.data_ptr(), ws, ws_bytes,
+        FLAG_CAUSAL if causal else 0, s)
     if status:
         _check(status)
     return out, lse

@@ -94,11 +94,15 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return y;
 }
 
-// c tanh(scale q.k / c) in log2 units: tanh(y) = 1 - 2 / (1 + e^{2y}), with
-// e^{2y} = 2^(q.k * cap_in).  Absolute error about 2^-23 of the cap; the two ends
-// (2^inf, 2^-inf) give +-1.
+// c tanh(scale q.k / c) in log2 units, y = scale q.k / c, with x = q.k * cap_in =
+// 2 y log2 e: tanh(y) = 1 - 2 / (1 + 2^x), off by 2^-23 of the cap or so; near 0,
+// where that would be lost on a large cap, y times the first terms of tanh's series
+// (|y| < 0.174, the next term below 3e-9 of y).  2^inf and 2^-inf give +-1.
 __device__ __forceinline__ float capped(float qk, float cap_in, float cap_log2) {
-    return cap_log2 * fmaf(-2.f, rcp_approx(1.f + fast_exp2(qk * cap_in)), 1.f);
+    const float x = qk * cap_in, y = x * 0.34657359f, z = y * y;
+    const float near = y * fmaf(z, fmaf(z, fmaf(z, -0.053968254f, 0.13333334f), -0.33333334f), 1.f);
+    const float far = fmaf(-2.f, rcp_approx(1.f + fast_exp2(x)), 1.f);
+    return cap_log2 * (fabsf(x) < 0.5f ? near : far);
 }
 
 // The D / 32 dims of a row that lane `lane` holds (from lane * D / 32 on).

@@ -59,8 +59,8 @@ pkd_status check_shape(int B, long long T, int Hq, int Hkv, int D, int P, int ma
 }
 
 pkd_status check_options(const pkd_score_options& o) {
-    if (!(o.softcap >= 0.f) || !std::isfinite(o.softcap))
-        return report(PKD_EINVAL, "softcap must be finite and >= 0 (0: none)");
+    if (o.softcap != 0.f && !(o.softcap >= 1e-20f && o.softcap <= 1e20f))
+        return report(PKD_EINVAL, "softcap must be 0 (none) or between 1e-20 and 1e20");
     if (!aligned(o.alibi_slopes, 4) || !aligned(o.prefix_lens, 4) || !aligned(o.doc_start, 4))
         return report(PKD_EINVAL, "alibi_slopes, prefix_lens and doc_start must be 4-byte aligned");
     return PKD_OK;

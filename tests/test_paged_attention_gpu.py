@@ -283,3 +283,77 @@ def test_key_offsets_past_32_bits():
         c.T = T
         ref.check(out.cpu(), lse.cpu(), c.reference(), "bf16")
         c.q = q
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("cap", [1e-3, 0.5, 1000.0, 1e6])
+def test_caps_of_any_size(cap, dtype):
+    """A cap far below the scores (all of them at its ends) and far above (no effect)."""
+    verify(ref.Paged(lens=[300, 40], news=[1, 1], Hq=4, Hkv=2, D=128, dtype=dtype, seed=17), "step", softcap=cap)
+    verify(ref.Paged(lens=[300, 140], news=[270, 140], Hq=4, Hkv=2, D=128, dtype=dtype, seed=17), "prompt", softcap=cap)
+
+
+@pytest.mark.parametrize("docs", [False, True])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_many_row_tiles_of_unlike_weight(docs, slopes):
+    """Enough row tiles to be ordered by their keys, of several requests, some empty."""
+    c = ref.Paged(lens=[900, 0, 60, 300, 1, 33], news=[37, 0, 30, 20, 1, 33], Hq=256, Hkv=4, D=64, seed=18, extra_tokens=1)
+    doc = np.zeros(c.T, np.int64)
+    doc[:37] = np.repeat([0, 640, 880, 899], [11, 7, 18, 1])
+    doc[37:67] = 31
+    kw = dict(slopes=slopes_of(256)) if slopes else {}
+    verify(c, "ordered", window=700, **(dict(doc_start=doc) if docs else {}), **kw)
+
+
+@pytest.mark.parametrize("news", [[3, 1], [60, 10]])
+def test_more_tokens_than_announced_are_cut_and_reported(news):
+    import paged_kv_decode_15_gb300 as pkd
+    c = ref.Paged(lens=[100, 90], news=news, Hq=4, Hkv=2, D=64, seed=19)
+    out, lse, status = run(c, max_query_len=news[0] - 1)
+    assert status == pkd.EDEVICE_BOUNDS
+    # the request's first tokens, as the last ones of its keys
+    cut = ref.Paged(lens=[100, 90], news=news, Hq=4, Hkv=2, D=64, seed=19)
+    starts = np.array([0, news[0] - 1], np.int32)
+    want = ref.attention(ref.values(cut.q), np.nan_to_num(ref.values(cut.cache)), cut.table[:1], cut.lens[:1], starts, cut.scale)
+    n = news[0] - 1
+    ref.check(out[:n], lse[:n], [x[:n] for x in want], "bf16")
+
+
+def test_calls_on_streams_of_their_own_and_from_two_threads():
+    import threading
+
+    import paged_kv_decode_15_gb300 as pkd
+    cases = [ref.Paged(lens=[3000, 500], news=n, Hq=8, Hkv=1, D=128, seed=20 + i) for i, n in enumerate(([1, 1], [33, 20]))]
+    args = [[dev(x) for x in (c.q, c.cache, c.table, c.lens, c.starts)] for c in cases]
+    want = [pkd.paged_attention(*a, c.scale, max_query_len=int(c.news.max())) for a, c in zip(args, cases)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in cases], {}
+
+    def work(i, stream):
+        for _ in range(20):
+            got[i] = pkd.paged_attention(*args[i], cases[i].scale, max_query_len=int(cases[i].news.max()), stream=stream)
+
+    for use in (streams, [None, None]):   # a stream each, then both on the default one
+        ts = [threading.Thread(target=work, args=(i, s)) for i, s in enumerate(use)]
+        [t.start() for t in ts]
+        [t.join() for t in ts]
+        torch.cuda.synchronize()
+        for i, w in enumerate(want):
+            assert torch.equal(got[i][0], w[0]) and torch.equal(got[i][1], w[1])
+
+
+def test_refusals_of_the_binding():
+    import paged_kv_decode_15_gb300 as pkd
+    c = ref.Paged(lens=[40], news=[4], Hq=4, Hkv=2, D=64, seed=22)
+    q, cache, table, lens, starts = (dev(x) for x in (c.q, c.cache, c.table, c.lens, c.starts))
+    call = lambda **kw: pkd.paged_attention(*[kw.pop(n, x) for n, x in zip(("q", "cache", "table", "lens", "starts"),
+                                                                          (q, cache, table, lens, starts))], c.scale, **kw)
+    for kw, error in ((dict(q=c.q), ValueError), (dict(q=q.transpose(0, 1)), ValueError), (dict(cache=cache[:, :, :, :64]), ValueError),
+                      (dict(table=table.long()), TypeError), (dict(lens=lens.expand(2)), ValueError), (dict(starts=starts[:1]), ValueError),
+                      (dict(prefix_lens=lens.long()), ValueError), (dict(doc_start=lens), ValueError),
+                      (dict(alibi_slopes=torch.ones(3, device="cuda")), ValueError),
+                      (dict(out=torch.empty(4, 4, 32, device="cuda")), ValueError), (dict(softcap=-1.0), pkd.PkdError),
+                      (dict(q=q.half()), pkd.PkdError), (dict(max_query_len=0), pkd.PkdError)):
+        with pytest.raises(error):
+            call(**kw)
+    assert pkd.paged_attention(q[:0], cache, table, lens, torch.zeros_like(starts), c.scale)[0].shape == (0, 4, 64)

@@ -72,9 +72,11 @@ class Shared:
         out, lse, status = self.call(**kw)
         assert status == pkd.OK
         kw.pop("group_start", None)
+        kind = kw.pop("out_dtype", None)
         c = self.c
         # two parts joined in fp32: each part's own bound, and the join's roundings inside it
-        ref.check(out.view(-1, c.Hq, c.D), lse.view(-1, c.Hq), self.reference(**kw), c.dtype)
+        ref.check(out.view(-1, c.Hq, c.D), lse.view(-1, c.Hq), self.reference(**kw), c.dtype,
+                  {torch.float32: "fp32", torch.float16: "fp16", None: None}[kind])
 
 
 @pytest.mark.parametrize("dtype,Hq,Hkv,D,P,sq", [("bf16", 8, 2, 128, 16, 1), ("fp16", 4, 4, 64, 32, 2),
@@ -187,3 +189,34 @@ def test_captured_and_replayed():
     torch.cuda.synchronize()
     s.prefixes = [333]
     ref.check(o[0].view(4, 8, 128).cpu(), o[1].view(4, 8).cpu(), s.reference(), "bf16")
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.float16])
+def test_output_types(kind):
+    Shared(prefixes=[300], group_start=[0, 3], own=[5, 60, 0], sq=1, Hq=4, Hkv=2, D=128, seed=9).verify(out_dtype=kind)
+
+
+def test_two_threads_on_one_stream():
+    import threading
+
+    import paged_kv_decode_15_gb300 as pkd
+    calls = []
+    for i in range(2):
+        s = Shared(prefixes=[900], group_start=[0, 4], own=[10, 20, 300, 1], sq=1, Hq=8, Hkv=2, D=128, seed=30 + i)
+        c = s.c
+        calls.append(([dev(c.q).view(4, 1, 8, 128), dev(c.cache), dev(c.table[:1].copy()), dev(np.array([900], np.int32)),
+                       dev(c.table[1:].copy()), dev(s.own)], c.scale))
+    want = [pkd.prefix_decode(*a, scale) for a, scale in calls]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        for _ in range(50):
+            o = pkd.prefix_decode(*calls[i][0], calls[i][1])
+            if not (torch.equal(o[0], want[i][0]) and torch.equal(o[1], want[i][1])):
+                wrong.append(i)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    assert not wrong

@@ -74,6 +74,8 @@ def test_paged_attention_refusals(lib, over, code, needle):
 @pytest.mark.parametrize("opt,flags,needle", [
     (pkd.ScoreOptions(-1.0, None, 0, None, None), pkd.FLAG_CAUSAL, "softcap"),
     (pkd.ScoreOptions(float("inf"), None, 0, None, None), pkd.FLAG_CAUSAL, "softcap"),
+    (pkd.ScoreOptions(float("nan"), None, 0, None, None), pkd.FLAG_CAUSAL, "softcap"),
+    (pkd.ScoreOptions(1e-30, None, 0, None, None), pkd.FLAG_CAUSAL, "softcap"),
     (pkd.ScoreOptions(0.0, 0x10002, 0, None, None), pkd.FLAG_CAUSAL, "aligned"),
     (pkd.ScoreOptions(0.0, None, 0, 0x10000, None), 0, "prefix_lens")])
 def test_option_refusals(lib, opt, flags, needle):
@@ -116,7 +118,7 @@ def prefix(lib, **over):
     (dict(groups=0), pkd.EINVAL, "groups"), (dict(groups=5000), pkd.EUNSUPPORTED, "groups"),
     (dict(sq=0), pkd.EINVAL, "sq"), (dict(max_prefix=(1 << 29) + 1, pstride=1 << 30), pkd.EUNSUPPORTED, "2^29"), (dict(cap=-1.0), pkd.EINVAL, "softcap"), (dict(pstride=6), pkd.EINVAL, "prefix_table"),
     (dict(gstart=None, groups=2), pkd.EINVAL, "group_start"), (dict(plens=None), pkd.EINVAL, "null"),
-    (dict(ws_bytes=1 << 20), pkd.EINVAL, "workspace"), (dict(flags=pkd.FLAG_GRID), pkd.EUNSUPPORTED, "FLAG_CAUSAL"),
+    (dict(ws_bytes=1000), pkd.EINVAL, "workspace"), (dict(flags=pkd.FLAG_GRID), pkd.EUNSUPPORTED, "FLAG_CAUSAL"),
     (dict(Hq=6, Hkv=4), pkd.EUNSUPPORTED, "multiple"), (dict(max_prefix=-1), pkd.EINVAL, "max_prefix_len")])
 def test_prefix_decode_refusals(lib, over, code, needle):
     assert prefix(lib, **over) == code
