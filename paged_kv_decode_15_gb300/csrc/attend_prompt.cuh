@@ -380,8 +380,8 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                 prefetch_tmap(&qmap);
             }
             const uint64_t pol = policy_evict_first();
-            uint64_t keep;
-            asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+            uint64_t keep;  // other row tiles read the same keys and values
+            asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
             const int total = pref[p.B] * p.Hkv * p.max_splits;
             int idx = blockIdx.x;
             int u = 0, nq = 0, npub = 0;
@@ -564,10 +564,11 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             }
         } else if (warp == 9) {
             // --------------------------------------------------- products
-            // The whole warp walks the items, converged, so that descriptors stay in
-            // uniform registers; one elected lane issues (with the loop under a lane
-            // test instead, a product took 115 cycles to issue, twice its run time).
+            // The whole warp walks the items, converged, and one elected lane issues (with
+            // the loop under a lane test instead, a product took 115 cycles to issue, more
+            // than the 75 it takes to run).
             const bool one = tc05::elect_one();
+            const uint32_t tm = tc05::uniform(tmem), qlo = tc05::uniform(tc05::desc_lo(sb0 + S::OFF_Q, 16));
             bool ok = true;
             int u = 0, nq = 0, nv = 0;      // K/V units, Q loads, widened V tiles before the item
             int np[2] = {0, 0}, no[2] = {0, 0};  // per tile: P tiles consumed, accumulations begun
@@ -590,14 +591,14 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     if (j >= 0)
                         ok = kFp8 ? pt_wait(bar(S::B_VF + vb), ((nv + j) >> 1) & 1, p)
                                   : pt_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p);
-                    const uint64_t vd = tc05::smem_desc(
-                        sb0 + (kFp8 ? S::OFF_V + vb * S::VUNIT : S::OFF_KV + ((vu + S::NU) % S::NU) * S::UNIT), 1024, S::VGROUP);
-                    const uint64_t kd = tc05::smem_desc(sb0 + S::OFF_KV + (ku % S::NU) * S::UNIT, 16, S::GROUP);
+                    const uint32_t vlo = tc05::uniform(tc05::desc_lo(
+                        sb0 + (kFp8 ? S::OFF_V + vb * S::VUNIT : S::OFF_KV + ((vu + S::NU) % S::NU) * S::UNIT), 1024));
+                    const uint32_t klo = tc05::uniform(tc05::desc_lo(sb0 + S::OFF_KV + (ku % S::NU) * S::UNIT, 16));
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (!ok) break;
                         const int jb = jbs[t], je = jes[t];
-                        const uint32_t s_addr = tmem + kPtKeys * t, o_addr = tmem + 256 + D * t;
+                        const uint32_t s_addr = tm + kPtKeys * t, o_addr = tm + 256 + D * t;
                         if (j >= jb && j < je) {
                             ok = pt_wait(bar(S::B_PF + t), np[t] & 1, p);
                             ++np[t];
@@ -612,7 +613,8 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
 #pragma unroll
                             for (int kk = 0; kk < kPtKeys / 16; ++kk)
                                 if (one)
-                                    tc05::mma_f16_ts(o_addr, s_addr + 8 * kk, vd + ((2 * kk * S::VGROUP) >> 4), kIdO, more || kk > 0);
+                                    tc05::mma_ts(o_addr, s_addr + 8 * kk, vlo + ((2 * kk * S::VGROUP) >> 4),
+                                                 tc05::desc_hi(S::VGROUP), kIdO, more || kk > 0);
                             if (one) {
                                 tc05::commit(bar(S::B_OD + t));
                                 if (j == je - 1) tc05::commit(bar(S::B_OF + t));
@@ -626,17 +628,13 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                                 tc05::fence_after_sync();
                             }
                             if (j + 1 >= jb && j + 1 < je) {
-                                const uint64_t qd = tc05::smem_desc(sb0 + S::OFF_Q + t * S::QTILE, 16, 1024);
 #pragma unroll
-                                for (int kk = 0; kk < S::ROWB / 32; ++kk) {
-                                    const uint64_t x = qd + (((kk >> 2) * kPtRows * 128 + (kk & 3) * 32) >> 4);
-                                    const uint64_t y = kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
-                                    if (!one) continue;
-                                    if constexpr (kFp8)
-                                        tc05::mma_e4m3(s_addr, x, y, kIdS, kk > 0);
-                                    else
-                                        tc05::mma_f16(s_addr, x, y, kIdS, kk > 0);
-                                }
+                                for (int kk = 0; kk < S::ROWB / 32; ++kk)
+                                    if (one)
+                                        tc05::mma_ss<kFp8>(s_addr,
+                                                           qlo + ((t * S::QTILE + (kk >> 2) * kPtRows * 128 + (kk & 3) * 32) >> 4),
+                                                           tc05::desc_hi(1024), klo + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+                                                           tc05::desc_hi(S::GROUP), kIdS, kk > 0);
                                 if (one) tc05::commit(bar(S::B_SF + t));
                             }
                             if (t == 1 && one) {
