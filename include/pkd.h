@@ -349,22 +349,24 @@ const char* pkd_paged_attention_kernel_name(int batch, int64_t total_tokens, int
  *   lse          device fp32 [total_tokens, num_heads] natural-log LSE, or NULL
  *   workspace    at least pkd_paged_attention_workspace_size bytes, 256-byte
  *                aligned, its first PKD_ATTENTION_WORKSPACE_HEAD bytes zeroed once
- *                (pkd_workspace_init); every call leaves it ready for the next of this function or pkd_prefix_decode, whatever
- *                its plan.  Calls that may overlap (streams, graphs) need one each.
+ *                (pkd_workspace_init); every call leaves it ready for the next of
+ *                this function or pkd_prefix_decode, whatever its plan.  Calls that
+ *                may overlap (streams, graphs) need one each.
  *                pkd_workspace_check reads its status word (PKD_EDEVICE_BOUNDS also
  *                for a query_start that falls, leaves [0, total_tokens] or holds
- *                more than max_query_len tokens: clamped)
+ *                more than max_query_len tokens: clamped; rows of requests that
+ *                then overlap are not all written)
  *   flags        PKD_FLAG_CAUSAL or 0
  *
  * Token i of request b (n tokens) has position p = L - n + i.  It sees keys
  * [0, L), with PKD_FLAG_CAUSAL those up to p (and its prefix_lens), less what
  * the window and doc_start exclude.  A token that sees no key gets out = 0 and
- * lse = -inf.  Keys that no token of a request sees are not read into results;
- * a value that one token sees and another one does not must be finite for the
- * second (its weight there is 0).
+ * lse = -inf.  Keys and values before the first and behind the last key that a
+ * request's tokens see do not enter its results, whatever they hold; the values
+ * between must be finite also for the tokens that do not see them (with weight 0).
  * Limits: head_dim 64 or 128; page_size a multiple of 16; num_heads/num_kv_heads
- * <= 128; batch <= 2048, batch * num_kv_heads <= 65536; max_kv_len <= 2^29; scale * q_scale * k_scale > 0; fp8
- * caches need head_dim 128.
+ * <= 128; batch <= 2048, batch * num_kv_heads <= 65536; max_kv_len <= 2^29;
+ * scale * q_scale * k_scale > 0; fp8 caches need head_dim 128.
  */
 pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_stride, const void* kv_cache,
                                pkd_dtype kv_dtype, int64_t num_pages, const int32_t* block_table,

@@ -596,6 +596,8 @@ def paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, *, c
         max_query_len = max(T, 1)
     if max_kv_len is None:
         max_kv_len = columns * P
+    if window >> 31 or max_query_len >> 31 or max_kv_len >> 31:
+        raise ValueError("window, max_query_len and max_kv_len must lie in [0, 2^31)")
     dtype = q.dtype
     q_dt, kv_dt = _code(dtype), _code(kv_cache.dtype)
     out, lse = _results(out, lse, shape, out_dtype or (_BF16 if kv_dt == FP8_E4M3 else dtype), q.device)
@@ -661,6 +663,8 @@ def prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens,
         max_prefix_len = pcolumns * P
     if max_kv_len is None:
         max_kv_len = columns * P
+    if max_prefix_len >> 31 or max_kv_len >> 31:
+        raise ValueError("max_prefix_len and max_kv_len must lie in [0, 2^31)")
     dtype = q.dtype
     q_dt, kv_dt = _code(dtype), _code(kv_cache.dtype)
     out, lse = _results(out, lse, shape, out_dtype or (_BF16 if kv_dt == FP8_E4M3 else dtype), q.device)

@@ -30,6 +30,7 @@ struct AttendParams {
     long long bt_stride, num_pages, q_stride;
     int B, T, Hq, Hkv, G, P;
     int sq, q_mul, max_q, max_kv_len;
+    int max_pairs;                // row-tile pairs of a kv head that the plan has room for (tcgen05 kernel)
     int window, causal;
     int chunk, max_splits, out_dtype;
     uint32_t pmagic;

@@ -35,7 +35,7 @@ int elt_bytes(pkd_dtype dt) { return dt == PKD_FP8_E4M3 ? 1 : dt == PKD_FP32 ? 4
 struct AttendPlan {
     bool step;                // the step grid, else the tcgen05 kernel
     int G, rows, chunk, max_splits;
-    long long units;          // split units of all kv heads at most
+    long long pairs, units;   // row-tile pairs of a kv head, split units of all kv heads, at most
     size_t lse_bytes, out_bytes;  // partial results
 };
 
@@ -97,6 +97,7 @@ pkd_status plan_attend(int B, long long T, int max_q, int Hq, int Hkv, int D, in
     // row-tile pairs: at least what all tokens fill, at most one more per request
     const int pair = 2 * (pkd::kPtRows / pl.G);
     const long long least = std::max((T + pair - 1) / pair, 1ll), most = T / pair + B;
+    pl.pairs = most;
     pl.units = most * Hkv;
     // the keys are split while the row tiles alone leave SMs idle: about two
     // items per SM, chunks of whole tiles, at least 512 keys (256 for partials,
@@ -129,7 +130,7 @@ pkd_status plan_paged_attention(int B, long long T, int max_q, int Hq, int Hkv, 
     pkd_status st = check_shape(B, T, Hq, Hkv, D, P, max_kv_len, kv);
     if (st != PKD_OK) return st;
     if (max_q < 1) return report(PKD_EINVAL, "max_query_len must be >= 1 (got %d)", max_q);
-    if (max_q > T && T > 0) max_q = (int)T;
+    max_q = (int)std::min<long long>(max_q, std::max(T, 1ll));
     long long vis = max_kv_len;
     // a window bounds the span of a request's keys, unless prefix keys are seen past the position
     if (o.window > 0 && !o.prefix_lens) vis = std::min(vis, (long long)o.window + max_q - 1 + 15);
@@ -182,6 +183,7 @@ void fill(pkd::AttendParams& a, const AttendPlan& pl, uint8_t* ws, int pass, siz
     a.q_mul = 1;
     a.max_kv_len = max_kv_len;
     a.num_pages = num_pages;
+    a.max_pairs = (int)pl.pairs;
     a.chunk = pl.chunk;
     a.max_splits = pl.max_splits;
     pkd::page_magic(P, a.pmagic, a.pmshift);
@@ -259,8 +261,8 @@ pkd_status launch_pass(const pkd::AttendParams& a, const AttendPlan& pl, const v
 
 pkd_status check_call(const void* q, pkd_dtype q_dtype, int64_t q_stride, const void* kv_cache, pkd_dtype kv_dtype,
                       int64_t num_pages, int Hq, int Hkv, int D, int P, float scale, float q_scale, float k_scale,
-                      float v_scale, const void* out, pkd_dtype out_dtype, const float* lse, const void* workspace,
-                      size_t workspace_bytes, size_t need) {
+                      float v_scale, float softcap, const void* out, pkd_dtype out_dtype, const float* lse,
+                      const void* workspace, size_t workspace_bytes, size_t need) {
     if (q_dtype != kv_dtype)
         return report(PKD_EUNSUPPORTED, "q dtype (%d) must equal the cache dtype (%d)", (int)q_dtype, (int)kv_dtype);
     if (out_dtype != PKD_BF16 && out_dtype != PKD_FP16 && out_dtype != PKD_FP32)
@@ -276,8 +278,10 @@ pkd_status check_call(const void* q, pkd_dtype q_dtype, int64_t q_stride, const 
     if (workspace_bytes < need)
         return report(PKD_EINVAL, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
     const float s = scale * q_scale * k_scale;
-    if (!(s > 0.f) || !std::isfinite(s) || !std::isfinite(v_scale))
+    if (!(s > 0.f) || !std::isfinite(s * pkd::kLog2e) || !std::isfinite(v_scale))
         return report(PKD_EINVAL, "scale*q_scale*k_scale must be positive and finite, v_scale finite");
+    if (softcap > 0.f && !std::isfinite(2.f * s * pkd::kLog2e / softcap))
+        return report(PKD_EINVAL, "softcap too small for scale*q_scale*k_scale: their quotient overflows");
     return PKD_OK;
 }
 
@@ -351,7 +355,7 @@ pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_strid
         return report(PKD_EINVAL, "prefix_lens needs PKD_FLAG_CAUSAL (without it every key is visible already)");
     if (batch == 0 || total_tokens == 0) return PKD_OK;
     st = check_call(q, q_dtype, q_stride, kv_cache, kv_dtype, num_pages, num_heads, num_kv_heads, head_dim, page_size,
-                    scale, q_scale, k_scale, v_scale, out, out_dtype, lse, workspace, workspace_bytes,
+                    scale, q_scale, k_scale, v_scale, o.softcap, out, out_dtype, lse, workspace, workspace_bytes,
                     kPartials + pl.lse_bytes + pl.out_bytes);
     if (st != PKD_OK) return st;
     st = check_table(block_table, block_table_stride, seq_lens, max_kv_len, page_size, "block_table");
@@ -408,7 +412,7 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
     if (flags & ~PKD_FLAG_CAUSAL) return report(PKD_EUNSUPPORTED, "pkd_prefix_decode takes PKD_FLAG_CAUSAL only");
     if (batch == 0) return PKD_OK;
     st = check_call(q, q_dtype, (int64_t)num_heads * head_dim, kv_cache, kv_dtype, num_pages, num_heads, num_kv_heads,
-                    head_dim, page_size, scale, q_scale, k_scale, v_scale, out, out_dtype, lse, workspace,
+                    head_dim, page_size, scale, q_scale, k_scale, v_scale, softcap, out, out_dtype, lse, workspace,
                     workspace_bytes, pl.bytes);
     if (st != PKD_OK) return st;
     st = check_table(block_table, block_table_stride, seq_lens, max_kv_len, page_size, "block_table");

@@ -296,10 +296,12 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
     }
     // prefix of the requests' row-tile pairs (units of one kv head)
     {
-        int run = 0;
+        // (unsigned: at most 384 x 2^23 pairs at a time, should requests overlap)
+        const unsigned room = p.max_pairs;
+        unsigned run = 0;
         for (int b0 = 0; b0 < p.B; b0 += kPtThreads) {
             const int b = b0 + tid;
-            int v = 0;
+            unsigned v = 0;
             if (b < p.B) {
                 int q0, n;
                 request_tokens(p, b, q0, n, blockIdx.x == 0);
@@ -307,18 +309,20 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(kFull, v, o);
+                const unsigned y = __shfl_up_sync(kFull, v, o);
                 if (lane >= o) v += y;
             }
             if (lane == 31) scan[warp] = v;
             __syncthreads();
-            int before = run;
+            unsigned before = run;
             for (int k = 0; k < kPtThreads / 32; ++k) {
-                const int s = scan[k];
+                const unsigned s = scan[k];
                 if (k < warp) before += s;
                 run += s;
             }
-            if (b < p.B) pref[b + 1] = before + v;
+            // requests of a bad query_start may overlap: pairs past the plan's are dropped
+            run = min(run, room);
+            if (b < p.B) pref[b + 1] = min(before + v, room);
             __syncthreads();
         }
         if (tid == 0) pref[0] = 0;

@@ -212,6 +212,26 @@ def test_bad_lengths_and_starts_are_clamped_and_reported():
         assert status == pkd.EDEVICE_BOUNDS and torch.equal(out, good)
 
 
+def test_requests_that_overlap_stay_inside_the_plan():
+    """A query_start that falls 299 times: every second request is all 256 tokens, 38400
+    row-tile pairs for a plan of at most 728; all requests alike, so the first's rows are right."""
+    import paged_kv_decode_15_gb300 as pkd
+    c = ref.Paged(lens=[2000], news=[256], Hq=128, Hkv=1, D=64, seed=23)
+    good, lse, status = run(c)
+    assert status == pkd.OK
+    q, cache = dev(c.q), dev(c.cache)
+    table, lens = dev(c.table).expand(600, -1).contiguous(), dev(c.lens).expand(600).contiguous()
+    starts = torch.tensor([0, 256] * 300 + [0], dtype=torch.int32, device="cuda")
+    ws = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    pkd.workspace_init(ws)
+    got = pkd.paged_attention(q, cache, table, lens, starts, c.scale, max_query_len=256, workspace=ws)
+    assert pkd.workspace_check(ws) == pkd.EDEVICE_BOUNDS
+    assert torch.equal(got[0].cpu(), good) and torch.equal(got[1].cpu(), lse)
+    assert not ws[256:256 + 4 * 65536].any(), "arrival counters are zero again"
+    again = pkd.paged_attention(q, cache, table[:1], lens[:1], dev(c.starts), c.scale, workspace=ws)
+    assert torch.equal(again[0].cpu(), good) and torch.equal(again[1].cpu(), lse)
+
+
 @pytest.mark.parametrize("news", [[1, 1, 1], [100, 37, 64]])
 def test_captured_and_replayed_on_another_stream(news):
     """Captured once, replayed on new lengths; two graphs in turn on two streams."""
@@ -353,7 +373,9 @@ def test_refusals_of_the_binding():
                       (dict(prefix_lens=lens.long()), ValueError), (dict(doc_start=lens), ValueError),
                       (dict(alibi_slopes=torch.ones(3, device="cuda")), ValueError),
                       (dict(out=torch.empty(4, 4, 32, device="cuda")), ValueError), (dict(softcap=-1.0), pkd.PkdError),
-                      (dict(q=q.half()), pkd.PkdError), (dict(max_query_len=0), pkd.PkdError)):
+                      (dict(q=q.half()), pkd.PkdError), (dict(max_query_len=0), pkd.PkdError),
+                      (dict(window=(1 << 32) + 5), ValueError), (dict(window=-1), ValueError),
+                      (dict(max_kv_len=1 << 32), ValueError), (dict(max_query_len=(1 << 32) + 4), ValueError)):
         with pytest.raises(error):
             call(**kw)
     assert pkd.paged_attention(q[:0], cache, table, lens, torch.zeros_like(starts), c.scale)[0].shape == (0, 4, 64)

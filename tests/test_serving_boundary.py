@@ -83,6 +83,13 @@ def test_option_refusals(lib, opt, flags, needle):
     assert needle in lib.pkd_last_error().decode()
 
 
+def test_cap_and_scale_whose_quotient_overflows(lib):
+    small = pkd.ScoreOptions(1e-20, None, 0, None, None)
+    assert attend(lib, small, scale=1e20) == pkd.EINVAL and "softcap too small" in lib.pkd_last_error().decode()
+    assert attend(lib, scale=3e38) == pkd.EINVAL and "scale" in lib.pkd_last_error().decode()
+    assert prefix(lib, cap=1e-20, scale=1e20) == pkd.EINVAL and "softcap too small" in lib.pkd_last_error().decode()
+
+
 def test_attention_of_nothing_is_ok(lib):
     assert attend(lib, B=0, q=None, cache=None) == pkd.OK
     assert attend(lib, T=0, q=None, cache=None) == pkd.OK
