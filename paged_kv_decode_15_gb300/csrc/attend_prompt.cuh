@@ -42,9 +42,8 @@ constexpr int kPtThreads = 384;
 constexpr int kPtItems = 4;        // work-item ring
 constexpr int kPtMaxBatch = 2048;  // requests whose tile prefix the CTA keeps in shared memory
 constexpr int kPtL2Bytes = 64 << 20;  // keys and values walked together
-// Row-tile pairs that a launch orders by weight (with a document mask, whose weights
-// take a look at every token, at most kPtMaxDocOrder), and items per CTA up to which it does.
-constexpr int kPtMaxOrder = 512, kPtMaxDocOrder = 192, kPtOrderItems = 16;
+// Row-tile pairs that a launch orders by weight, and items per CTA up to which it does.
+constexpr int kPtMaxOrder = 512, kPtOrderItems = 16;
 // A row's reference moves when its maximum has grown by more than this (log2
 // units).  The weights only must not overflow the operand type: bf16 has fp32's
 // range, fp16 ends at 2^16.  (With 2^8 for both, half of the key tiles of scores
@@ -332,29 +331,23 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
     // masks.  Every CTA ranks the pairs alike, by key tiles and then by number
     // (packed documents, 416 items on 152 CTAs: the last CTA ended after twice the mean time).
     const int npairs = pref[p.B];
-    const bool ordered = npairs > 1 && npairs <= (p.doc_start ? kPtMaxDocOrder : kPtMaxOrder) &&
-                         npairs * p.Hkv > static_cast<int>(gridDim.x) &&
+    const bool ordered = npairs > 1 && npairs <= kPtMaxOrder && npairs * p.Hkv > static_cast<int>(gridDim.x) &&
                          npairs * p.Hkv <= kPtOrderItems * static_cast<int>(gridDim.x);
     if (ordered) {
         uint16_t* weight = reinterpret_cast<uint16_t*>(smem + S::OFF_STAGE);
-        // a thread per pair -- its first and last token bound the others' keys -- or,
-        // with documents, a warp that looks at every token
-        const int width = p.doc_start ? 32 : 1;
-        for (int x = tid / width; x < npairs; x += kPtThreads / width) {
+        // A pair's weight: the keys from its first token's to its last token's.  (Only the
+        // order depends on it: a look at every token's document took 10k cycles.)
+        for (int x = tid; x < npairs; x += kPtThreads) {
             const int b = pt_request(pref, p.B, 1, x);
             int q0, n, lo = 0x7fffffff, hi = 0;
             request_tokens(p, b, q0, n, false);
             const int L = request_len(p, b, false), prefix = p.prefix_lens ? p.prefix_lens[b] : 0;
-            const int a0 = (x - pref[b]) * 2 * TOK, a1 = min(a0 + 2 * TOK, n);
-            const int step = width == 1 ? max(a1 - 1 - a0, 1) : 32;
-            for (int i = a0 + (width == 1 ? 0 : lane); i < a1; i += step) {
+            const int a0 = (x - pref[b]) * 2 * TOK, a1 = min(a0 + 2 * TOK, n) - 1;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
                 int k0, k1;
-                token_keys(p, q0, n, L, prefix, i, k0, k1);
+                token_keys(p, q0, n, L, prefix, e ? a1 : a0, k0, k1);
                 if (k0 < k1) lo = min(lo, k0), hi = max(hi, k1);
-            }
-            if (width == 32) {
-                lo = __reduce_min_sync(kFull, lo);
-                hi = __reduce_max_sync(kFull, hi);
             }
             weight[x] = static_cast<uint16_t>(min(65535, hi > lo ? (hi - lo + kPtKeys - 1) / kPtKeys : 0));
         }
@@ -761,9 +754,19 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                         uint32_t v[2][32];
                         tc05::ld_32x32b_x32(s_addr, v[0]);
                         const bool masked = tk < ml || tk + kPtKeys > mh;
+                        // A tile that every row sees whole or not at all (a document ends inside the
+                        // warp's rows) needs no mask, but those rows' weights cleared: packed
+                        // documents 99 -> 80 us.  (With a cap it would take 3% off those and cost
+                        // all other calls 1%.)
+                        auto off = [&] { return !valid || hi <= tk || lo >= tk + kPtKeys; };
+                        bool clear = false;
+                        if (!kCap && masked && !bad && j > jb) {
+                            const bool whole = lo <= tk && min(hi, kBias ? min(hi_all, pos + 1) : hi_all) >= tk + kPtKeys;
+                            clear = __all_sync(kFull, whole || off());
+                        }
                         const float scale = (kCap || kBias) ? 1.f : p.scale_log2;
                         bool done = false;
-                        if (!masked && j > jb && !(kCap && wide > 0)) {
+                        if (kCap ? !masked && j > jb && wide <= 0 : clear || (!masked && j > jb)) {
                             // A tile that every row sees whole, in one pass of straight-line code
                             // against the reference of the tiles before it.  Its maximum comes out
                             // beside the weights: they count only if no row has outgrown its reference
@@ -787,11 +790,31 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                                 if (c < 3) tc05::wait_ld(v[(c + 1) & 1]);
                             }
                             const bool grown = top * scale > m_used + kRescale, out = kCap && far > p.cap_far;
-                            done = !__any_sync(kFull, grown || out);
+                            if constexpr (kCap) {
+                                done = !__any_sync(kFull, grown || out);
+                            } else {
+                                const bool none = clear && off();
+                                done = !__any_sync(kFull, grown && !none);
+                                if (none) sum = 0.f;
+                            }
                             if (done) {
                                 l += sum;
 #pragma unroll
                                 for (int c = 0; c < 4; ++c) tc05::st_32x32b_x16(s_addr + 16 * c, pk[c]);
+                                if (!kCap && clear) {
+                                    tc05::wait_st();
+#pragma unroll 1
+                                    for (int c = 0; c < 4; ++c) {
+                                        uint32_t w[16];
+                                        tc05::ld_32x32b_x16(s_addr + 16 * c, w);
+                                        tc05::wait_ld();
+                                        if (off()) {
+#pragma unroll
+                                            for (int e = 0; e < 16; ++e) w[e] = 0u;
+                                        }
+                                        tc05::st_32x32b_x16(s_addr + 16 * c, w);
+                                    }
+                                }
                             } else {
                                 if (kCap && __any_sync(kFull, out)) wide = 8;
                                 tc05::ld_32x32b_x32(s_addr, v[0]);

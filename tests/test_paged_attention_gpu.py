@@ -118,6 +118,23 @@ def test_prompts_with_prefix_and_document_masks(dtype):
     verify(c, "docs+cap", doc_start=doc, softcap=20.0)
 
 
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("dtype,D,Hq,Hkv", [("bf16", 128, 4, 4), ("fp16", 64, 3, 1), ("fp8", 128, 4, 4)])
+def test_documents_that_end_inside_a_row_tile(dtype, D, Hq, Hkv, slopes):
+    """Many key tiles that some rows of a warp see whole and the others not at all; a key
+    that is not finite reaches the tokens of its own document only."""
+    c = ref.Paged(lens=[1500, 700], news=[700, 500], Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, seed=24, spread=3.0)
+    first, second = np.arange(800, 1500), np.arange(200, 700)
+    doc = np.concatenate([np.select([first < 811, first < 1203], [0, 811], 1203),
+                          np.select([second < 443, second < 460], [0, 443], 460)])
+    kw = dict(slopes=slopes_of(Hq)) if slopes else {}
+    verify(c, "documents", doc_start=doc, **kw)
+    good, lse, _ = run(c, doc_start=doc, **kw)
+    c.cache[c.table[0, 500 // c.P], :, 500 % c.P, :D] = float("nan" if dtype == "fp8" else "inf")
+    out, lse2, _ = run(c, doc_start=doc, **kw)
+    assert torch.equal(out[11:], good[11:]) and torch.equal(lse2[11:], lse[11:])
+
+
 @pytest.mark.parametrize("dtype,D,Hq,Hkv", [("bf16", 128, 8, 1), ("bf16", 64, 12, 2), ("fp8", 128, 8, 2)])
 def test_few_rows_over_many_keys_split(dtype, D, Hq, Hkv):
     """A small chunk of queries on a long context: the keys are split and merged."""
