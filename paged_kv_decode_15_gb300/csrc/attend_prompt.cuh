@@ -9,7 +9,7 @@
 //                 shared memory, K-major, 128-byte swizzle, as TMA lands them
 //   softmax       one row per thread (TMEM lane = row): no shuffles.  The
 //                 reference maximum moves only when a row's maximum grows by more
-//                 than 2^8 (O and l are then rescaled by the row's own warp)
+//                 than 2^40, in fp16 2^14 (O and l are then rescaled by the row's own warp)
 //   O += P V      P in TMEM over the spent S (A operand from tensor memory),
 //                 V in shared memory read MN-major
 // Two row tiles share every K/V tile, and while the softmax of one runs, the
@@ -22,7 +22,18 @@
 // 9 issues the products; for e4m3 caches S is an e4m3 product and warps 10-11 widen
 // V to fp16 in shared memory ahead of the O product (P is rounded to fp16 then).
 // Registers follow the roles (setmaxnreg).  (An epilogue group of its own left the
-// softmax 176 registers and spills: 8192-token prompt 523 us.)
+// softmax 176 registers and spills: 8192-token prompt 523 us, not 416.)
+//
+// What bounds it, D = 128 (32768-token prompt, 32 heads: 6.0 ms, 1470 TFLOP/s, 0.79 of
+// a dense library product; 8192 tokens 416 us): per row tile a loop of the softmax
+// (1540 cycles a key tile: 940 of exponentials and packing, the rest TMEM loads and
+// stores and the arrival), the issuing warp's wake-up (270), the products (1120) and
+// the softmax's (300).  Two row tiles run interleaved, so the tensor cores, 2050
+// cycles a pair, are busy two thirds of its 3200; TMEM has no columns for a third
+// tile or a second S.  An item costs another 6000 cycles or so between its last tile
+// and the next one's first, a launch 15000 before its first tile (set-up, the item's
+// chain of loads, Q and K) and as many for its first two tiles, whose code comes
+// from memory: what bounds short launches.
 // Work items are handed out by an atomic counter in the workspace, the longest of
 // a request first, so CTAs finish together whatever the lengths; results do not
 // depend on who computes an item.  Every wait is bounded.
@@ -754,24 +765,19 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                         uint32_t v[2][32];
                         tc05::ld_32x32b_x32(s_addr, v[0]);
                         const bool masked = tk < ml || tk + kPtKeys > mh;
-                        // A tile that every row sees whole or not at all (a document ends inside the
-                        // warp's rows) needs no mask, but those rows' weights cleared: packed
-                        // documents 99 -> 80 us.  (With a cap it would take 3% off those and cost
-                        // all other calls 1%.)
-                        auto off = [&] { return !valid || hi <= tk || lo >= tk + kPtKeys; };
-                        bool clear = false;
-                        if (!kCap && masked && !bad && j > jb) {
-                            const bool whole = lo <= tk && min(hi, kBias ? min(hi_all, pos + 1) : hi_all) >= tk + kPtKeys;
-                            clear = __all_sync(kFull, whole || off());
-                        }
                         const float scale = (kCap || kBias) ? 1.f : p.scale_log2;
                         bool done = false;
-                        if (kCap ? !masked && j > jb && wide <= 0 : clear || (!masked && j > jb)) {
-                            // A tile that every row sees whole, in one pass of straight-line code
-                            // against the reference of the tiles before it.  Its maximum comes out
-                            // beside the weights: they count only if no row has outgrown its reference
-                            // (and no capped score the polynomial).  (Decided chunk by chunk, the
-                            // pass took 1460 cycles, not 950.)
+                        const int c0 = lo - tk, c1 = min(hi, hi_all) - tk;
+                        auto straight = [&](auto masked_tile) {
+                            constexpr bool kMasked = decltype(masked_tile)::value;
+                            // One pass of straight-line code against the reference of the tiles
+                            // before.  The tile's maximum comes out beside the weights: they count
+                            // only if no row has outgrown its reference (and no capped score the
+                            // polynomial).  (Decided chunk by chunk, the pass took 1460 cycles, not
+                            // 950.)  Tiles with masked keys have a copy of it where neither a cap nor
+                            // a bias needs its registers (packed documents 99 -> 72 us, 8192-token
+                            // prompt 419 -> 415; with them it spills: capped prompts with a window
+                            // 179 -> 192, biased 8192-token prompt 440 -> 455).
                             const float m = m_used == -INFINITY ? 0.f : m_used;
                             uint32_t pk[4][16];
                             float sum = 0.f, top = -INFINITY, far = 0.f;
@@ -784,48 +790,37 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                                     far = fmaxf(far, pt_max<true>(x));
                                     pt_cap<true>(x, p);
                                 }
-                                if constexpr (kBias) pt_bias<true>(x, kCap ? 1.f : p.scale_log2, slope, static_cast<float>(pos - tk - 32 * c));
+                                if constexpr (kBias) {
+                                    const float dist = static_cast<float>(pos - tk - 32 * c);
+                                    pt_bias<true>(x, kCap ? 1.f : p.scale_log2, slope, dist);
+                                }
+                                if constexpr (kMasked) pt_mask(x, c0 - 32 * c, c1 - 32 * c, 3u);
                                 top = fmaxf(top, pt_max<false>(x));
                                 sum += pt_weights<kBF16>(x, pk[c], scale, m);
                                 if (c < 3) tc05::wait_ld(v[(c + 1) & 1]);
                             }
                             const bool grown = top * scale > m_used + kRescale, out = kCap && far > p.cap_far;
-                            if constexpr (kCap) {
-                                done = !__any_sync(kFull, grown || out);
-                            } else {
-                                const bool none = clear && off();
-                                done = !__any_sync(kFull, grown && !none);
-                                if (none) sum = 0.f;
-                            }
+                            done = !__any_sync(kFull, grown || out);
                             if (done) {
                                 l += sum;
 #pragma unroll
                                 for (int c = 0; c < 4; ++c) tc05::st_32x32b_x16(s_addr + 16 * c, pk[c]);
-                                if (!kCap && clear) {
-                                    tc05::wait_st();
-#pragma unroll 1
-                                    for (int c = 0; c < 4; ++c) {
-                                        uint32_t w[16];
-                                        tc05::ld_32x32b_x16(s_addr + 16 * c, w);
-                                        tc05::wait_ld();
-                                        if (off()) {
-#pragma unroll
-                                            for (int e = 0; e < 16; ++e) w[e] = 0u;
-                                        }
-                                        tc05::st_32x32b_x16(s_addr + 16 * c, w);
-                                    }
-                                }
                             } else {
                                 if (kCap && __any_sync(kFull, out)) wide = 8;
                                 tc05::ld_32x32b_x32(s_addr, v[0]);
                             }
+                        };
+                        if (j > jb && !(kCap && wide > 0)) {
+                            if (!masked)
+                                straight(std::false_type{});
+                            else if constexpr (!kCap && !kBias)
+                                if (!bad) straight(std::true_type{});
                         }
                         if (!done) {
                             // Any other tile, in two rolled passes: the maximum, with which the
                             // references move (O and l follow), then the weights, written over
                             // products that are spent
                             const unsigned stages = bad ? pt_stages(p, I, tk) : 0xffu;
-                            const int c0 = lo - tk, c1 = min(hi, hi_all) - tk;
                             auto logits = [&](uint32_t (&x)[32], int c) {
                                 if constexpr (kCap) {
                                     if (__any_sync(kFull, pt_max<true>(x) > p.cap_far))
