@@ -352,6 +352,7 @@ const char* pkd_paged_attention_kernel_name(int batch, int64_t total_tokens, int
  *                (pkd_workspace_init); every call leaves it ready for the next of
  *                this function or pkd_prefix_decode, whatever its plan.  Calls that
  *                may overlap (streams, graphs) need one each.
+ *                After PKD_ETIMEOUT zero those bytes again.
  *                pkd_workspace_check reads its status word (PKD_EDEVICE_BOUNDS also
  *                for a query_start that falls, leaves [0, total_tokens] or holds
  *                more than max_query_len tokens: clamped; rows of requests that

@@ -69,7 +69,6 @@ struct PtItem {
     int split, nsplit, unit;
     int jb[2], je[2];              // steps [jb, je) of row tile t (empty: none); step j is key tile pt_tile(j)
     int bad, end;                  // bad: some page lies outside the pool
-    int pad[2];
 };
 
 // Types of q and the cache.
