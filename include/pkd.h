@@ -345,7 +345,8 @@ const char* pkd_paged_attention_kernel_name(int batch, int64_t total_tokens, int
  *                [query_start[b], query_start[b + 1]) of q, at most max_query_len;
  *                rows of q outside every request are neither read into a result
  *                nor written in out and lse
- *   out          device [total_tokens, num_heads, head_dim] contiguous, out_dtype
+ *   out          device [total_tokens, num_heads, head_dim] contiguous, out_dtype;
+ *                no part of it may lie in q
  *   lse          device fp32 [total_tokens, num_heads] natural-log LSE, or NULL
  *   workspace    at least pkd_paged_attention_workspace_size bytes, 256-byte
  *                aligned, its first PKD_ATTENTION_WORKSPACE_HEAD bytes zeroed once
@@ -391,7 +392,8 @@ pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_strid
  *                 with one group: every request follows it
  *   block_table, seq_lens  the requests' own keys, after the prefix (seq_lens[b]
  *                 keys; the first page of a request's row starts behind the prefix)
- *   out, lse      as for pkd_paged_decode, over the prefix's and the own keys
+ *   out, lse      as for pkd_paged_decode, over the prefix's and the own keys; out
+ *                 not in q
  *   softcap       as in pkd_score_options (0: none)
  *   flags         PKD_FLAG_CAUSAL: token i sees its request's own keys up to
  *                 position seq_lens[b] - sq + i; the prefix is seen whole

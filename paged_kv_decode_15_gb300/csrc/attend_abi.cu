@@ -295,6 +295,15 @@ pkd_status check_table(const int32_t* table, int64_t stride, const int32_t* lens
     return PKD_OK;
 }
 
+// Results may be written while other CTAs still read q.
+pkd_status check_overlap(const void* q, pkd_dtype q_dtype, int64_t q_stride, const void* out, pkd_dtype out_dtype,
+                         int64_t T, int Hq, int D) {
+    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+    const uintptr_t q1 = q0 + ((T - 1) * q_stride + (int64_t)Hq * D) * elt_bytes(q_dtype);
+    const uintptr_t o1 = o0 + T * Hq * D * elt_bytes(out_dtype);
+    return q0 < o1 && o0 < q1 ? report(PKD_EINVAL, "out overlaps q") : PKD_OK;
+}
+
 const pkd_score_options kNoOptions = {0.f, nullptr, 0, nullptr, nullptr};
 
 }  // namespace
@@ -361,6 +370,8 @@ pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_strid
     st = check_table(block_table, block_table_stride, seq_lens, max_kv_len, page_size, "block_table");
     if (st != PKD_OK) return st;
     if (!query_start || !aligned(query_start, 4)) return report(PKD_EINVAL, "query_start is null or misaligned");
+    st = check_overlap(q, q_dtype, q_stride, out, out_dtype, total_tokens, num_heads, head_dim);
+    if (st != PKD_OK) return st;
     pkd::AttendParams a;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     fill(a, pl, ws, 0, kPartials, batch, total_tokens, num_heads, num_kv_heads, page_size, max_kv_len, num_pages,
@@ -421,6 +432,8 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
     if (st != PKD_OK) return st;
     if ((!group_start && groups != 1) || !aligned(group_start, 4))
         return report(PKD_EINVAL, "group_start is misaligned, or null with more than one group");
+    st = check_overlap(q, q_dtype, (int64_t)num_heads * head_dim, out, out_dtype, (int64_t)batch * sq, num_heads, head_dim);
+    if (st != PKD_OK) return st;
 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const long long T = (long long)batch * sq;

@@ -90,6 +90,13 @@ def test_cap_and_scale_whose_quotient_overflows(lib):
     assert prefix(lib, cap=1e-20, scale=1e20) == pkd.EINVAL and "softcap too small" in lib.pkd_last_error().decode()
 
 
+def test_results_over_the_queries_are_refused(lib):
+    assert attend(lib) == pkd.EINVAL and "overlaps" in lib.pkd_last_error().decode()
+    last = ctypes.c_void_p(0x10000 + 2 * (19 * 512 + 512) - 16)  # the last 16 bytes of q
+    assert attend(lib, out=last) == pkd.EINVAL and "overlaps" in lib.pkd_last_error().decode()
+    assert prefix(lib) == pkd.EINVAL and "overlaps" in lib.pkd_last_error().decode()
+
+
 def test_attention_of_nothing_is_ok(lib):
     assert attend(lib, B=0, q=None, cache=None) == pkd.OK
     assert attend(lib, T=0, q=None, cache=None) == pkd.OK
