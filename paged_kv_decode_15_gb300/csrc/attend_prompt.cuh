@@ -742,6 +742,10 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                 const bool warp_on = __any_sync(kFull, valid);
                 int lo = 0, hi = 0x7fffffff;
                 if (valid) token_keys(p, I.q0, I.n, I.L, I.prefix, tok, lo, hi);
+                // lanes without a row hold what was left in shared memory: they have no say in the
+                // warp's votes, or the roundings of its rows would depend on the CTA's last item
+                if (!valid) m_used = INFINITY;
+                const float cap_far = valid ? p.cap_far : INFINITY;
                 float slope = 0.f;
                 const int pos = I.L - I.n + tok;
                 if constexpr (kBias)
@@ -798,7 +802,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                                 sum += pt_weights<kBF16>(x, pk[c], scale, m);
                                 if (c < 3) tc05::wait_ld(v[(c + 1) & 1]);
                             }
-                            const bool grown = top * scale > m_used + kRescale, out = kCap && far > p.cap_far;
+                            const bool grown = top * scale > m_used + kRescale, out = kCap && far > cap_far;
                             done = !__any_sync(kFull, grown || out);
                             if (done) {
                                 l += sum;
@@ -820,9 +824,18 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                             // references move (O and l follow), then the weights, written over
                             // products that are spent
                             const unsigned stages = bad ? pt_stages(p, I, tk) : 0xffu;
+                            const unsigned loaded = stages & (0xffu >> max(0, 8 - (hi_all - tk + kStageTok - 1) / kStageTok));
                             auto logits = [&](uint32_t (&x)[32], int c) {
                                 if constexpr (kCap) {
-                                    if (__any_sync(kFull, pt_max<true>(x) > p.cap_far))
+                                    // (nor have keys that were not loaded)
+                                    const unsigned here = loaded >> (2 * c);
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e)
+                                        if (!(here >> e & 1)) {
+#pragma unroll
+                                            for (int i = 0; i < 16; ++i) x[16 * e + i] = 0u;
+                                        }
+                                    if (__any_sync(kFull, pt_max<true>(x) > cap_far))
                                         pt_cap<false>(x, p);
                                     else
                                         pt_cap<true>(x, p);

@@ -229,6 +229,28 @@ def test_bad_lengths_and_starts_are_clamped_and_reported():
         assert status == pkd.EDEVICE_BOUNDS and torch.equal(out, good)
 
 
+@pytest.mark.parametrize("dtype,Hq,D", [("bf16", 14, 128), ("fp16", 6, 64), ("fp8", 10, 128)])
+@pytest.mark.parametrize("cap", [0.0, 4.0])
+def test_results_do_not_depend_on_the_schedule(dtype, Hq, D, cap):
+    """Row tiles with lanes to spare and key tiles that end early, hundreds of items in any
+    order, after calls that leave large queries and keys on the SMs: the same bits every time."""
+    import paged_kv_decode_15_gb300 as pkd
+    rng = np.random.default_rng(25)
+    news = rng.integers(20, 400, 24)
+    c = ref.Paged(lens=news + rng.integers(0, 300, 24), news=news, Hq=Hq, Hkv=2, D=D, dtype=dtype, seed=26, spread=4.0)
+    args = [dev(x) for x in (c.q, c.cache, c.table, c.lens, c.starts)]
+    call = lambda: pkd.paged_attention(*args, c.scale, softcap=cap, max_query_len=400, **c.scales())
+    big = ref.Paged(lens=[400] * 40, news=[200] * 40, Hq=16, Hkv=2, D=D, dtype=dtype, seed=27, spread=50.0)
+    loud = [dev(x) for x in (big.q, big.cache, big.table, big.lens, big.starts)]
+    small = ref.Paged(lens=[400] * 40, news=[200] * 40, Hq=16, Hkv=2, D=D, dtype=dtype, seed=27, spread=0.0)
+    quiet = [dev(small.q)] + loud[1:]
+    out, lse = call()
+    for i in range(10):
+        pkd.paged_attention(*(loud if i % 2 else quiet), 1.0, softcap=cap, max_query_len=200)
+        again = call()
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
 def test_requests_that_overlap_stay_inside_the_plan():
     """A query_start that falls 299 times: every second request is all 256 tokens, 38400
     row-tile pairs for a plan of at most 728; all requests alike, so the first's rows are right."""
