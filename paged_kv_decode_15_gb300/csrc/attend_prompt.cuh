@@ -106,11 +106,12 @@ struct PtShape {
     static constexpr int OFF_ORDER = OFF_SCAN + 128;     // uint16 [kPtMaxOrder]: row-tile pairs, longest first
     static constexpr int OFF_BAR = (OFF_ORDER + kPtMaxOrder * 2 + 7) & ~7;
     static_assert(8 * 2048 >= kPtMaxOrder * 2, "weights fit the staging area");
-    // units full/empty, Q full/empty, S full, P full, O step done, O full/drained, item full/empty, widened V, drain
+    // units full/empty, Q full/empty, S full, P full, O step done, O full/drained, item full/empty, widened V,
+    // a split item's part stored/counted, drain
     static constexpr int B_UF = 0, B_UE = B_UF + NU, B_QF = B_UE + NU, B_QE = B_QF + 1, B_SF = B_QE + 1;
     static constexpr int B_PF = B_SF + 2, B_OD = B_PF + 2, B_OF = B_OD + 2, B_OE = B_OF + 2, B_IF = B_OE + 2;
-    static constexpr int B_IE = B_IF + kPtItems, B_VF = B_IE + kPtItems, B_VE = B_VF + NV, B_DR = B_VE + NV;
-    static constexpr int NBAR = B_DR + 1;
+    static constexpr int B_IE = B_IF + kPtItems, B_VF = B_IE + kPtItems, B_VE = B_VF + NV, B_JA = B_VE + NV;
+    static constexpr int B_JD = B_JA + 2, B_DR = B_JD + 2, NBAR = B_DR + 1;
     static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_TMEM + 16 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
@@ -291,6 +292,8 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             mbar_init(bar(S::B_OD + i), 1);
             mbar_init(bar(S::B_OF + i), 1);
             mbar_init(bar(S::B_OE + i), 4);
+            mbar_init(bar(S::B_JA + i), 4);
+            mbar_init(bar(S::B_JD + i), 1);
         }
         for (int i = 0; i < kPtItems; ++i) {
             mbar_init(bar(S::B_IF + i), 1);
@@ -727,7 +730,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
         const uint32_t lane_addr = static_cast<uint32_t>(32 * q4) << 16;
         const uint32_t s_addr = tmem + lane_addr + kPtKeys * t, o_addr = tmem + lane_addr + 256 + D * t;
         const int ri = r / G, rg = r - ri * G;
-        int ns = 0, no = 0, u = 0;  // key tiles walked, accumulations drained; K/V units before the item
+        int ns = 0, no = 0, nj = 0, u = 0;  // key tiles walked, accumulations drained, parts published; K/V units before the item
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const int slot = it % kPtItems;
@@ -1001,12 +1004,24 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                         p.lse[row] = l2 * kLn2;
                 }
                 if (!partials && nsplit > 1) {
-                    // publish this tile's part (the group's barrier, then one arrival with
-                    // release semantics); the arrival that completes the unit merges its rows
+                    // publish this tile's part: the four warps' arrivals, one arrival at the unit's
+                    // counter with release semantics (cumulative over the stores they ordered before
+                    // it), its result back to the four; the arrival that completes the unit merges
+                    // its rows.  Bounded waits, as everywhere: a warp that gives up leaves its
+                    // siblings no barrier to hang on.
                     const int tok_end = min(I.tok0 + 2 * TOK, n), tiles = I.tok0 + TOK < n ? 2 : 1;
-                    asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
-                    if ((tid & 127) == 0) scan[24 + t] = atom_add_acq_rel_gpu(p.counters + I.unit);
-                    asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(S::B_JA + t));
+                    if (q4 == 0) {
+                        if (!pt_wait(bar(S::B_JA + t), nj & 1, p)) { ok = false; break; }
+                        if (lane == 0) {
+                            scan[24 + t] = atom_add_acq_rel_gpu(p.counters + I.unit);
+                            mbar_arrive(bar(S::B_JD + t));
+                        }
+                        __syncwarp();
+                    }
+                    if (!pt_wait(bar(S::B_JD + t), nj & 1, p)) { ok = false; break; }
+                    ++nj;
                     if (scan[24 + t] == nsplit * tiles - 1) {
                         const int rows = (tok_end - I.tok0) * G;
                         const long long step = static_cast<long long>(p.T) * p.Hq;

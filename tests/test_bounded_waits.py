@@ -1,0 +1,36 @@
+"""Every wait between the warps of the ragged-attention kernels is bounded: shown by
+reading their sources, since a wait that is not would hang the GPU."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "paged_kv_decode_15_gb300", "csrc")
+
+
+def source(name):
+    """A source file without its comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def roles():
+    """The prompt kernel between the barrier that ends its set-up and the one of its
+    tear-down, which every warp reaches: there warps give up one by one."""
+    kernel = source("attend_prompt.cuh").split("attend_prompt_kernel(", 1)[1]
+    return kernel.split("const uint32_t tmem = *tslot;", 1)[1].rsplit("__syncthreads();", 1)[0]
+
+
+def test_no_barrier_of_several_warps_among_the_roles():
+    """A warp may give up (pt_wait) while its siblings go on: a hardware barrier of
+    several warps would then wait for it for ever."""
+    body = roles()
+    for barrier in ("bar.sync", "bar.red", "barrier.", "__syncthreads", "bar.arrive"):
+        assert barrier not in body, barrier
+
+
+def test_waits_on_memory_barriers_are_bounded():
+    body = roles()
+    assert "pt_wait(" in body and "mbar_try_wait(" not in body and "mbar_test_wait(" not in body
+    wait = source("attend_prompt.cuh").split("bool pt_wait(", 1)[1].split("\n}", 1)[0]
+    assert "kErrTimeout" in wait and "__all_sync" in wait and "break" in wait
