@@ -177,7 +177,8 @@ __device__ __forceinline__ void attend_step(const CUtensorMap& tmap, const Atten
     int timed_out = 0, consumed = 0;
     for (int k = 0; k < my_n; ++k) {
         const int buf = k % NBUF;
-        if (!mbar_wait(bar0 + 8 * buf, (k / NBUF) & 1, p.status, p.wait_ns)) {
+        // one answer for the warp: its lanes go on, or give up, together
+        if (!__all_sync(kFull, mbar_wait(bar0 + 8 * buf, (k / NBUF) & 1, p.status, p.wait_ns))) {
             timed_out = 1;
             break;
         }

@@ -34,3 +34,11 @@ def test_waits_on_memory_barriers_are_bounded():
     assert "pt_wait(" in body and "mbar_try_wait(" not in body and "mbar_test_wait(" not in body
     wait = source("attend_prompt.cuh").split("bool pt_wait(", 1)[1].split("\n}", 1)[0]
     assert "kErrTimeout" in wait and "__all_sync" in wait and "break" in wait
+
+
+def test_lanes_of_a_step_warp_give_up_together():
+    """mbar_wait answers per lane: a warp whose lanes part there would meet the shuffles
+    and products of the whole warp with some of them gone."""
+    loop = source("attend_step.cuh").split("for (int k = 0; k < my_n; ++k) {", 1)[1]
+    waits = re.findall(r"if \(([^{]*mbar_wait\([^{]*)\{", loop.split("if (timed_out)", 1)[0])
+    assert len(waits) == 1 and waits[0].startswith("!__all_sync(kFull, mbar_wait(")
