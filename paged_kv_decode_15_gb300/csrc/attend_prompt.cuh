@@ -566,12 +566,12 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                 }
                 if (end) break;
             }
-            if (!ok) {
-                // let every issued copy land before the CTA leaves
-                if (lane == 0) atomicOr(p.status, kErrTimeout);
-                for (int j = max(0, u - S::NU); j < u; ++j) mbar_wait(bar(S::B_UF + j % S::NU), (j / S::NU) & 1);
-                if (nq) mbar_wait(bar(S::B_QF), (nq - 1) & 1);
-            }
+            // Let every issued copy land before the CTA leaves, also where this warp was done
+            // and the ones that read the copies have given up: what lands later would land
+            // in the shared memory of another CTA.
+            for (int j = max(0, u - S::NU); j < u; ++j) mbar_wait(bar(S::B_UF + j % S::NU), (j / S::NU) & 1);
+            if (nq) mbar_wait(bar(S::B_QF), (nq - 1) & 1);
+            if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
         } else if (warp == 9) {
             // --------------------------------------------------- products
             // The whole warp walks the items, converged, and one elected lane issues (with

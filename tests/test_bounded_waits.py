@@ -42,3 +42,16 @@ def test_lanes_of_a_step_warp_give_up_together():
     loop = source("attend_step.cuh").split("for (int k = 0; k < my_n; ++k) {", 1)[1]
     waits = re.findall(r"if \(([^{]*mbar_wait\([^{]*)\{", loop.split("if (timed_out)", 1)[0])
     assert len(waits) == 1 and waits[0].startswith("!__all_sync(kFull, mbar_wait(")
+
+
+def test_the_loading_warp_always_waits_for_its_copies():
+    """The last copies are waited for by the warp that issued them on every way out of its
+    role, not only where it gave up itself: the warps that read them may have."""
+    role = roles().split("if (warp == 8) {", 1)[1].split("} else if (warp == 9) {", 1)[0]
+    depth, found = 0, 0
+    for line in role.splitlines():
+        if "mbar_wait(bar(S::B_UF" in line or "mbar_wait(bar(S::B_QF" in line:
+            assert depth == 0, f"under a condition: {line.strip()}"
+            found += 1
+        depth += line.count("{") - line.count("}")
+    assert found == 2 and "return" not in role.rsplit("mbar_wait(bar(S::B_UF", 1)[0].rsplit("for (int r = 0; ok; ++r)", 1)[1]
