@@ -45,7 +45,8 @@ typedef enum {
     PKD_FP32 = 3
 } pkd_dtype;
 
-/* Flags for pkd_paged_decode. */
+/* Flags for pkd_paged_decode (pkd_paged_attention and pkd_prefix_decode take
+ * PKD_FLAG_CAUSAL and PKD_FLAG_TEST_TIMEOUT). */
 #define PKD_FLAG_CAUSAL 1u      /* causal mask inside the query block, exact per-token window */
 #define PKD_FLAG_MMA_SMALL_M 2u /* tensor cores for sq*Hq/Hkv < 16 (already the default; kept for callers) */
 #define PKD_FLAG_FMA 4u         /* CUDA cores instead (only when sq*Hq/Hkv <= 8) */
@@ -66,7 +67,9 @@ typedef enum {
  * waiting up to 200 ms, so a call reports PKD_ETIMEOUT whenever a copy has not
  * landed by its first test.  The kernels still let every issued copy land
  * before they leave.  It exists to exercise the timeout path; zero the
- * workspace again (pkd_workspace_init) after such a call. */
+ * workspace again (pkd_workspace_init) after such a call.  (Of the prompts of
+ * pkd_paged_attention and pkd_prefix_decode: the waits for queries, in half of
+ * the CTAs from their second work item on.) */
 #define PKD_FLAG_TEST_TIMEOUT 64u
 
 /* Library version, major*10000 + minor*100 + patch. */
@@ -358,7 +361,7 @@ const char* pkd_paged_attention_kernel_name(int batch, int64_t total_tokens, int
  *                for a query_start that falls, leaves [0, total_tokens] or holds
  *                more than max_query_len tokens: clamped; rows of requests that
  *                then overlap are not all written)
- *   flags        PKD_FLAG_CAUSAL or 0
+ *   flags        PKD_FLAG_CAUSAL or 0 (and the diagnostic PKD_FLAG_TEST_TIMEOUT)
  *
  * Token i of request b (n tokens) has position p = L - n + i.  It sees keys
  * [0, L), with PKD_FLAG_CAUSAL those up to p (and its prefix_lens), less what
@@ -397,6 +400,7 @@ pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_strid
  *   softcap       as in pkd_score_options (0: none)
  *   flags         PKD_FLAG_CAUSAL: token i sees its request's own keys up to
  *                 position seq_lens[b] - sq + i; the prefix is seen whole
+ *                 (and the diagnostic PKD_FLAG_TEST_TIMEOUT)
  *
  * The workspace is as for pkd_paged_attention.  max_prefix_len and max_kv_len
  * bound prefix_lens and seq_lens.  Limits as for

@@ -556,7 +556,7 @@ def _prefix_bytes(*plan):
 def paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, *, causal=True, window=0, softcap=0.0,
                     alibi_slopes=None, prefix_lens=None, doc_start=None, max_query_len=None, max_kv_len=None,
                     q_scale=1.0, k_scale=1.0, v_scale=1.0, out=None, lse=None, out_dtype=None, workspace=None,
-                    stream=None):
+                    test_timeout=False, stream=None):
     """Attention of ragged query tokens over the paged cache (prompts, chunks, steps).
 
     q [T, Hq, D] (the cache's type; any token stride); request b's tokens are
@@ -566,6 +566,7 @@ def paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, *, c
     int32 [B]: keys that all of a request's tokens see; doc_start int32 [T]:
     first key of each token's document.  max_query_len (default T) and
     max_kv_len (default the table's capacity) bound the lengths on the host.
+    test_timeout sets the diagnostic PKD_FLAG_TEST_TIMEOUT.
     Returns (out [T, Hq, D], lse fp32 [T, Hq]).
     """
     index = q.get_device()
@@ -583,7 +584,8 @@ def paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, *, c
                                        window=window, softcap=softcap, alibi_slopes=alibi_slopes,
                                        prefix_lens=prefix_lens, doc_start=doc_start, max_query_len=max_query_len,
                                        max_kv_len=max_kv_len, q_scale=q_scale, k_scale=k_scale, v_scale=v_scale,
-                                       out=out, lse=lse, out_dtype=out_dtype, workspace=workspace)
+                                       out=out, lse=lse, out_dtype=out_dtype, workspace=workspace,
+                                       test_timeout=test_timeout)
     T, Hq, D = shape = q.shape
     qs = _token_stride(q, T, Hq, D, "q")
     num_pages, Hkv, P = _check_cache(D, kv_cache)
@@ -611,7 +613,7 @@ def paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, *, c
         q.data_ptr(), q_dt, qs, kv_cache.data_ptr(), kv_dt, num_pages, block_table.data_ptr(), stride,
         seq_lens.data_ptr(), query_start.data_ptr(), B, T, max_query_len, Hq, Hkv, D, P, max_kv_len, scale, q_scale,
         k_scale, v_scale, opt, out.data_ptr(), _code(out.dtype), lse.data_ptr(), ws, ws_bytes,
-        FLAG_CAUSAL if causal else 0, s)
+        (FLAG_CAUSAL if causal else 0) | (FLAG_TEST_TIMEOUT if test_timeout else 0), s)
     if status:
         _check(status)
     return out, lse
@@ -619,13 +621,14 @@ def paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, *, c
 
 def prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, scale, *, group_start=None,
                   causal=False, softcap=0.0, max_prefix_len=None, max_kv_len=None, q_scale=1.0, k_scale=1.0,
-                  v_scale=1.0, out=None, lse=None, out_dtype=None, workspace=None, stream=None):
+                  v_scale=1.0, out=None, lse=None, out_dtype=None, workspace=None, test_timeout=False, stream=None):
     """Decode of a batch whose requests share prefixes, each computed once.
 
     q [B, sq, Hq, D]; prefix_table int32 [groups, columns] and prefix_lens int32
     [groups]: the shared prefixes' pages; group_start int32 [groups + 1]: requests
     group_start[g] : group_start[g + 1] follow prefix g (default: one group of
     all); block_table, seq_lens: the requests' own keys behind the prefix.
+    test_timeout sets the diagnostic PKD_FLAG_TEST_TIMEOUT.
     Returns (out [B, sq, Hq, D], lse fp32 [B, sq, Hq]) over both.
     """
     index = q.get_device()
@@ -644,7 +647,7 @@ def prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens,
                                      group_start=group_start, causal=causal, softcap=softcap,
                                      max_prefix_len=max_prefix_len, max_kv_len=max_kv_len, q_scale=q_scale,
                                      k_scale=k_scale, v_scale=v_scale, out=out, lse=lse, out_dtype=out_dtype,
-                                     workspace=workspace)
+                                     workspace=workspace, test_timeout=test_timeout)
     if q.dim() != 4 or not q.is_contiguous():
         raise ValueError("q must be contiguous [batch, sq, num_heads, head_dim]")
     B, sq, Hq, D = shape = q.shape
@@ -679,7 +682,7 @@ def prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens,
         prefix_lens.data_ptr(), group_start.data_ptr() if group_start is not None else None, groups, max_prefix_len,
         block_table.data_ptr(), stride, seq_lens.data_ptr(), B, sq, Hq, Hkv, D, P, max_kv_len, scale, q_scale, k_scale,
         v_scale, softcap, out.data_ptr(), _code(out.dtype), lse.data_ptr(), ws, ws_bytes,
-        FLAG_CAUSAL if causal else 0, s)
+        (FLAG_CAUSAL if causal else 0) | (FLAG_TEST_TIMEOUT if test_timeout else 0), s)
     if status:
         _check(status)
     return out, lse

@@ -39,7 +39,7 @@ struct AttendParams {
     float cap_in, cap_log2;       // with one: cap_log2 * tanh(q.k * cap_in / (2 log2 e)); cap_log2 = 0: none
     float cap_c[5], cap_far;      // the capped logit as q.k times a polynomial in (q.k)^2, for |q.k| <= cap_far
     float v_scale;
-    uint64_t wait_ns;
+    uint64_t wait_ns;             // limit of a wait on a copy (0: a single test, PKD_FLAG_TEST_TIMEOUT)
 };
 
 // Programmatic dependent launch: let the next launch start (every CTA says so once),

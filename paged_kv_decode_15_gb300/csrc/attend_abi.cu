@@ -167,7 +167,7 @@ pkd_status plan_prefix(int B, int sq, int Hq, int Hkv, int D, int P, int groups,
 
 // Parameters common to the passes.
 void fill(pkd::AttendParams& a, const AttendPlan& pl, uint8_t* ws, int pass, size_t off_partials, int B, long long T,
-          int Hq, int Hkv, int P, int max_kv_len, int64_t num_pages, float scale2, float softcap) {
+          int Hq, int Hkv, int P, int max_kv_len, int64_t num_pages, float scale2, float softcap, unsigned flags) {
     std::memset(&a, 0, sizeof a);
     a.status = reinterpret_cast<int32_t*>(ws);
     a.queue = a.status + kQueueWord[pass];
@@ -202,7 +202,7 @@ void fill(pkd::AttendParams& a, const AttendPlan& pl, uint8_t* ws, int pass, siz
         for (int i = 0; i < 5; ++i, power *= k * k) a.cap_c[i] = (float)(c[i] * power);
         a.cap_far = k > 2e-4 && k < 1e3 && scale2 > 1e-6f && scale2 < 1e6f ? (float)(0.6 / k) : -1.f;
     }
-    a.wait_ns = pkd::kWaitNs;
+    a.wait_ns = (flags & PKD_FLAG_TEST_TIMEOUT) ? 0 : pkd::kWaitNs;
 }
 
 pkd_status cuda_fail(cudaError_t e, const char* what) {
@@ -359,7 +359,8 @@ pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_strid
     st = plan_paged_attention(batch, total_tokens, max_query_len, num_heads, num_kv_heads, head_dim, page_size,
                               max_kv_len, kv_dtype, o, pl);
     if (st != PKD_OK) return st;
-    if (flags & ~PKD_FLAG_CAUSAL) return report(PKD_EUNSUPPORTED, "pkd_paged_attention takes PKD_FLAG_CAUSAL only");
+    if (flags & ~(PKD_FLAG_CAUSAL | PKD_FLAG_TEST_TIMEOUT))
+        return report(PKD_EUNSUPPORTED, "pkd_paged_attention takes PKD_FLAG_CAUSAL (and PKD_FLAG_TEST_TIMEOUT) only");
     if (o.prefix_lens && !(flags & PKD_FLAG_CAUSAL))
         return report(PKD_EINVAL, "prefix_lens needs PKD_FLAG_CAUSAL (without it every key is visible already)");
     if (batch == 0 || total_tokens == 0) return PKD_OK;
@@ -375,7 +376,7 @@ pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_strid
     pkd::AttendParams a;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     fill(a, pl, ws, 0, kPartials, batch, total_tokens, num_heads, num_kv_heads, page_size, max_kv_len, num_pages,
-         scale * q_scale * k_scale * pkd::kLog2e, o.softcap);
+         scale * q_scale * k_scale * pkd::kLog2e, o.softcap, flags);
     a.q = q;
     a.q_stride = q_stride;
     a.block_table = block_table;
@@ -420,7 +421,8 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
     st = plan_prefix(batch, sq, num_heads, num_kv_heads, head_dim, page_size, groups, max_prefix_len, max_kv_len,
                      kv_dtype, pl);
     if (st != PKD_OK) return st;
-    if (flags & ~PKD_FLAG_CAUSAL) return report(PKD_EUNSUPPORTED, "pkd_prefix_decode takes PKD_FLAG_CAUSAL only");
+    if (flags & ~(PKD_FLAG_CAUSAL | PKD_FLAG_TEST_TIMEOUT))
+        return report(PKD_EUNSUPPORTED, "pkd_prefix_decode takes PKD_FLAG_CAUSAL (and PKD_FLAG_TEST_TIMEOUT) only");
     if (batch == 0) return PKD_OK;
     st = check_call(q, q_dtype, (int64_t)num_heads * head_dim, kv_cache, kv_dtype, num_pages, num_heads, num_kv_heads,
                     head_dim, page_size, scale, q_scale, k_scale, v_scale, softcap, out, out_dtype, lse, workspace,
@@ -441,7 +443,8 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
     cudaStream_t s = (cudaStream_t)stream;
     // the rows of a group's requests are one dense query block over its prefix
     pkd::AttendParams a;
-    fill(a, pl.pre, ws, 0, kPartials, groups, T, num_heads, num_kv_heads, page_size, max_prefix_len, num_pages, scale2, softcap);
+    fill(a, pl.pre, ws, 0, kPartials, groups, T, num_heads, num_kv_heads, page_size, max_prefix_len, num_pages, scale2, softcap,
+         flags);
     a.q = q;
     a.q_stride = (long long)num_heads * head_dim;
     a.block_table = prefix_table;
@@ -457,7 +460,7 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
     // each request's own keys: beside the prefix (programmatic dependent launch)
     pkd::AttendParams b;
     fill(b, pl.own, ws, 1, pl.off_own, batch, T, num_heads, num_kv_heads, page_size, max_kv_len, num_pages, scale2,
-         softcap);
+         softcap, flags);
     b.q = q;
     b.q_stride = a.q_stride;
     b.block_table = block_table;

@@ -159,6 +159,15 @@ __device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, const Att
     return __all_sync(kFull, done);
 }
 
+// The issuing warp's wait for the queries of its CTA's item `it`.  With p.wait_ns = 0
+// (diagnostic) a single test of the barrier: every second CTA gives up on its first
+// item so, the others on a later one, between an epilogue and its join.  (The same in
+// the waits for keys and values cost packed documents 2%.)
+__device__ __forceinline__ bool pt_wait_queries(uint32_t bar, uint32_t parity, const AttendParams& p, int it) {
+    if (p.wait_ns || (it == 0 && (blockIdx.x & 1))) return pt_wait(bar, parity, p);
+    return __all_sync(kFull, mbar_test_wait(bar, parity));
+}
+
 // A chunk is 32 keys of a row's tile, k0 .. k0 + 31 from the tile's first: their
 // products q.k as loaded, turned in place into what the exponential takes.
 
@@ -591,7 +600,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(S::B_IE + slot));
                 if (!ntiles) continue;
-                if (!pt_wait(bar(S::B_QF), nq & 1, p)) { ok = false; break; }
+                if (!pt_wait_queries(bar(S::B_QF), nq & 1, p, it)) { ok = false; break; }
                 ++nq;
                 // round j: the O products of key tile j, the S products of key tile j + 1.  A tile's
                 // S product goes in issue order behind its O product, which has read the P under S.
