@@ -8,7 +8,7 @@ Entry points (same names as the C ABI in include/pkd.h, without the prefix):
   paged_decode(q, kv_cache, block_table, seq_lens, scale, window, out, lse, ...)
   segmented_attention(q, k, v, used, bias, bs, local, out, ...)
   lse_merge(part_out, part_lse, prior=None, live=None, out=None, lse_out=None)
-  workspace_size(...), workspace_init(ws), workspace_check(ws)
+  workspace_size(...), workspace_init(ws), workspace_check(ws=None)
   rope_cache_write(q, key, value, positions, cos_sin, slot_mapping, kv_cache, ...)
   paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, ...)
   prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, scale, ...)
@@ -171,9 +171,28 @@ def workspace_init(ws: torch.Tensor, stream=None):
     _check(load_library().pkd_workspace_init(_ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
 
 
-def workspace_check(ws: torch.Tensor, stream=None) -> int:
-    """Synchronise, read and clear the workspace status word; returns the status code."""
-    return load_library().pkd_workspace_check(_ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+def workspace_check(ws: torch.Tensor = None, stream=None) -> int:
+    """Synchronise, read and clear the workspace status word; returns the status code.
+
+    Without ws: that of the workspace which paged_attention and prefix_decode
+    keep for this host thread and stream (default: the current one) when they
+    are given none.  Such a workspace is ready for the next call afterwards,
+    also after ETIMEOUT (its counters are zeroed again).  A call captured into
+    a graph has its workspace in the graph: pass it one of your own to read
+    its status.
+    """
+    if ws is not None:
+        return load_library().pkd_workspace_check(_ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+    s = stream if stream is not None else torch.cuda.current_stream()
+    index = s.device.index
+    kept = _call_ws.get((index, s.cuda_stream, _thread()))
+    if kept is None:
+        return OK
+    with torch.cuda.device(index):
+        status = load_library().pkd_workspace_check(kept[0], kept[1], s.cuda_stream)
+        if status == ETIMEOUT:
+            _check(load_library().pkd_workspace_init(kept[0], _WS_HEAD, s.cuda_stream))
+    return status
 
 
 _ws_cache: dict = {}
@@ -407,7 +426,7 @@ _WS_HEAD = 256 + 4 * 65536  # PKD_ATTENTION_WORKSPACE_HEAD
 def _call_workspace(nbytes, index, stream):
     """A zeroed workspace for a call on the current stream: one kept per stream and
     host thread (grown as needed; launches of two threads' calls may alternate on a
-    stream), or, while the stream is capturing, one of the graph's own (zeroed by
+    stream; workspace_check() reads its status), or, while the stream is capturing, one of the graph's own (zeroed by
     the graph), so that two graphs never share one."""
     if not _capturing():
         key = (index, stream, _thread())
@@ -566,8 +585,11 @@ def paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, *, c
     int32 [B]: keys that all of a request's tokens see; doc_start int32 [T]:
     first key of each token's document.  max_query_len (default T) and
     max_kv_len (default the table's capacity) bound the lengths on the host.
+    Lengths, pages or starts out of range are clamped or skipped; workspace_check
+    (of workspace, or of the one kept for calls without) then says so.
     test_timeout sets the diagnostic PKD_FLAG_TEST_TIMEOUT.
-    Returns (out [T, Hq, D], lse fp32 [T, Hq]).
+    Returns (out [T, Hq, D], lse fp32 [T, Hq]); rows of no request keep what was
+    in out and lse (nothing in particular where the call allocates them).
     """
     index = q.get_device()
     if index < 0 or kv_cache.get_device() != index or block_table.get_device() != index or \
@@ -628,6 +650,7 @@ def prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens,
     [groups]: the shared prefixes' pages; group_start int32 [groups + 1]: requests
     group_start[g] : group_start[g + 1] follow prefix g (default: one group of
     all); block_table, seq_lens: the requests' own keys behind the prefix.
+    workspace_check reads the status, as for paged_attention.
     test_timeout sets the diagnostic PKD_FLAG_TEST_TIMEOUT.
     Returns (out [B, sq, Hq, D], lse fp32 [B, sq, Hq]) over both.
     """

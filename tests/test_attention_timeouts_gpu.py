@@ -25,8 +25,10 @@ def _lib():
 
 
 def until_timeout(pkd, ws, call):
-    """A copy that lands before its first test is no timeout: a few tries."""
-    for _ in range(4):
+    """A copy that lands before its first test is no timeout: a few tries, each with a
+    cold L2 (256 MB written over it)."""
+    for _ in range(8):
+        torch.empty(1 << 28, dtype=torch.uint8, device="cuda").zero_()
         call()
         status = pkd.workspace_check(ws)
         if status != pkd.OK:
