@@ -8,7 +8,7 @@ Entry points (same names as the C ABI in include/pkd.h, without the prefix):
   paged_decode(q, kv_cache, block_table, seq_lens, scale, window, out, lse, ...)
   segmented_attention(q, k, v, used, bias, bs, local, out, ...)
   lse_merge(part_out, part_lse, prior=None, live=None, out=None, lse_out=None)
-  workspace_size(...), workspace_init(ws), workspace_check(ws=None)
+  workspace_size(...), workspace_init(ws), workspace_check(ws=None), release_workspaces()
   rope_cache_write(q, key, value, positions, cos_sin, slot_mapping, kv_cache, ...)
   paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, ...)
   prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, scale, ...)
@@ -18,7 +18,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
-from threading import get_ident as _thread
+import threading
 
 import torch
 
@@ -185,7 +185,7 @@ def workspace_check(ws: torch.Tensor = None, stream=None) -> int:
         return load_library().pkd_workspace_check(_ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
     s = stream if stream is not None else torch.cuda.current_stream()
     index = s.device.index
-    kept = _call_ws.get((index, s.cuda_stream, _thread()))
+    kept = _kept.workspaces.get((index, s.cuda_stream))
     if kept is None:
         return OK
     with torch.cuda.device(index):
@@ -193,6 +193,13 @@ def workspace_check(ws: torch.Tensor = None, stream=None) -> int:
         if status == ETIMEOUT:
             _check(load_library().pkd_workspace_init(kept[0], _WS_HEAD, s.cuda_stream))
     return status
+
+
+def release_workspaces():
+    """Free the workspaces that paged_attention and prefix_decode keep for this host
+    thread (the next call makes a new one); those of other threads go with their
+    threads.  Calls already queued keep theirs until they are done."""
+    _kept.workspaces.clear()
 
 
 _ws_cache: dict = {}
@@ -419,18 +426,26 @@ def _token_stride(t, T, H, D, name):
     return a if T > 1 else max(a, H * D)
 
 
-_call_ws: dict = {}
+class _Kept(threading.local):
+    """Workspaces of a host thread's calls: (device index, stream) -> (address, bytes, tensor)."""
+
+    def __init__(self):
+        self.workspaces = {}
+
+
+_kept = _Kept()
 _WS_HEAD = 256 + 4 * 65536  # PKD_ATTENTION_WORKSPACE_HEAD
 
 
 def _call_workspace(nbytes, index, stream):
     """A zeroed workspace for a call on the current stream: one kept per stream and
     host thread (grown as needed; launches of two threads' calls may alternate on a
-    stream; workspace_check() reads its status), or, while the stream is capturing, one of the graph's own (zeroed by
+    stream; freed with its thread or by release_workspaces(); workspace_check()
+    reads its status), or, while the stream is capturing, one of the graph's own (zeroed by
     the graph), so that two graphs never share one."""
     if not _capturing():
-        key = (index, stream, _thread())
-        ws = _call_ws.get(key)
+        key = (index, stream)
+        ws = _kept.workspaces.get(key)
         if ws is not None and ws[1] >= nbytes:
             return ws
     else:
@@ -439,7 +454,7 @@ def _call_workspace(nbytes, index, stream):
     _check(load_library().pkd_workspace_init(t.data_ptr(), _WS_HEAD, stream))
     ws = (t.data_ptr(), nbytes, t)
     if key is not None:
-        _call_ws[key] = ws
+        _kept.workspaces[key] = ws
     return ws
 
 

@@ -78,3 +78,48 @@ def test_calls_after_a_timeout_are_right(name):
         out, lse = call()
         ref.check(out.cpu(), lse.cpu(), want, c.dtype)
     assert pkd.workspace_check() == pkd.OK
+
+
+def test_kept_workspaces_are_freed():
+    """One a stream and thread while the thread lives, and none afterwards."""
+    import paged_kv_decode_15_gb300 as pkd
+    c = ref.Paged(lens=[4000, 3000], news=[30, 28], Hq=8, Hkv=1, D=64, seed=54)   # split keys: partial results
+    call = call_of(pkd, c)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    want = call()
+    torch.cuda.synchronize()
+
+    def work():
+        for s in streams:
+            call(stream=s)
+        torch.cuda.synchronize()
+
+    work()
+    pkd.release_workspaces()
+    before = torch.cuda.memory_allocated()
+    for _ in range(5):
+        worker = threading.Thread(target=work)
+        worker.start()
+        worker.join()
+    assert torch.cuda.memory_allocated() == before, "workspaces outlived their threads"
+    call()
+    assert torch.cuda.memory_allocated() > before, "a call keeps its workspace"
+    pkd.release_workspaces()
+    assert torch.cuda.memory_allocated() == before
+    again = call()
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+def test_a_workspace_released_while_its_calls_are_queued():
+    """Its memory is used again in the order of its stream only."""
+    import paged_kv_decode_15_gb300 as pkd
+    c = ref.Paged(lens=[4000, 3000], news=[30, 28], Hq=8, Hkv=1, D=64, seed=55)
+    call = call_of(pkd, c)
+    want = call()
+    got = []
+    for _ in range(20):
+        got.append(call())
+        pkd.release_workspaces()
+        torch.empty(1 << 22, dtype=torch.uint8, device="cuda").fill_(255)
+    for g in got:
+        assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
