@@ -27,6 +27,7 @@ struct AttendParams {
     int32_t* counters;            // arrivals per split unit
     float* part_lse;              // log2 domain
     float* part_out;
+    float4* fold;                 // tcgen05 kernel: per CTA, what long sums were folded into
     long long bt_stride, num_pages, q_stride;
     int B, T, Hq, Hkv, G, P;
     int sq, q_mul, max_q, max_kv_len;

@@ -37,6 +37,8 @@ struct AttendPlan {
     int G, rows, chunk, max_splits;
     long long pairs, units;   // row-tile pairs of a kv head, split units of all kv heads, at most
     size_t lse_bytes, out_bytes;  // partial results
+    size_t fold_bytes;        // of sums over more than kPtFold key tiles: two row tiles a CTA
+    size_t bytes() const { return lse_bytes + out_bytes + fold_bytes; }
 };
 
 pkd_status check_shape(int B, long long T, int Hq, int Hkv, int D, int P, int max_kv_len, pkd_dtype kv) {
@@ -122,6 +124,8 @@ pkd_status plan_attend(int B, long long T, int max_q, int Hq, int Hkv, int D, in
         return report(PKD_EUNSUPPORTED, "too many row tiles for split keys");
     pl.lse_bytes = up256(parts * 4);
     pl.out_bytes = up256(parts * D * 4);
+    if (std::min<long long>(vis + 15, pl.chunk) > (long long)pkd::kPtFold * pkd::kPtKeys)
+        pl.fold_bytes = (size_t)kSms * 2 * pkd::kPtRows * (D + 4) * 4;
     return PKD_OK;
 }
 
@@ -158,8 +162,8 @@ pkd_status plan_prefix(int B, int sq, int Hq, int Hkv, int D, int P, int groups,
     if (st != PKD_OK) return st;
     st = plan_attend(B, T, sq, Hq, Hkv, D, P, max_kv_len, kv, false, step, pl.own);
     if (st != PKD_OK) return st;
-    pl.off_own = kPartials + pl.pre.lse_bytes + pl.pre.out_bytes;
-    pl.off_own_lse = pl.off_own + pl.own.lse_bytes + pl.own.out_bytes;
+    pl.off_own = kPartials + pl.pre.bytes();
+    pl.off_own_lse = pl.off_own + pl.own.bytes();
     pl.off_own_out = pl.off_own_lse + up256((size_t)T * Hq * 4);
     pl.bytes = pl.off_own_out + up256((size_t)T * Hq * D * 4);
     return PKD_OK;
@@ -174,6 +178,7 @@ void fill(pkd::AttendParams& a, const AttendPlan& pl, uint8_t* ws, int pass, siz
     a.counters = reinterpret_cast<int32_t*>(ws + kHeader);
     a.part_lse = reinterpret_cast<float*>(ws + off_partials);
     a.part_out = reinterpret_cast<float*>(ws + off_partials + pl.lse_bytes);
+    a.fold = reinterpret_cast<float4*>(ws + off_partials + pl.lse_bytes + pl.out_bytes);
     a.B = B;
     a.T = (int)T;
     a.Hq = Hq;
@@ -312,7 +317,7 @@ cudaError_t pkd::launch_attend_prompt(int D, int kv_dtype, const CUtensorMap& kv
                                       const AttendParams& p, bool partials, bool overlap, long long items,
                                       cudaStream_t stream) {
     int grid = 1;
-    cudaError_t e = persistent_grid(1, (int)std::min(items, 1ll << 20), grid);
+    cudaError_t e = persistent_grid(1, (int)std::min<long long>(items, kSms), grid);
     if (e != cudaSuccess) return e;
     if (kv_dtype == PKD_FP8_E4M3)
         return D == 128 ? launch_prompt_fp8_d128(kvmap, qmap, p, partials, overlap, grid, stream) : cudaErrorInvalidValue;
@@ -331,7 +336,7 @@ size_t pkd_paged_attention_workspace_size(int batch, int64_t total_tokens, int m
     AttendPlan pl;
     const pkd_score_options& o = options ? *options : kNoOptions;
     return plan_paged_attention(batch, total_tokens, max_query_len, num_heads, num_kv_heads, head_dim, page_size,
-                                max_kv_len, kv_dtype, o, pl) == PKD_OK ? kPartials + pl.lse_bytes + pl.out_bytes : 0;
+                                max_kv_len, kv_dtype, o, pl) == PKD_OK ? kPartials + pl.bytes() : 0;
 }
 
 const char* pkd_paged_attention_kernel_name(int batch, int64_t total_tokens, int max_query_len, int num_heads,
@@ -366,7 +371,7 @@ pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_strid
     if (batch == 0 || total_tokens == 0) return PKD_OK;
     st = check_call(q, q_dtype, q_stride, kv_cache, kv_dtype, num_pages, num_heads, num_kv_heads, head_dim, page_size,
                     scale, q_scale, k_scale, v_scale, o.softcap, out, out_dtype, lse, workspace, workspace_bytes,
-                    kPartials + pl.lse_bytes + pl.out_bytes);
+                    kPartials + pl.bytes());
     if (st != PKD_OK) return st;
     st = check_table(block_table, block_table_stride, seq_lens, max_kv_len, page_size, "block_table");
     if (st != PKD_OK) return st;

@@ -61,6 +61,14 @@ constexpr int kPtMaxOrder = 512, kPtOrderItems = 16;
 // with a spread of 3 had some warp move its references.)
 constexpr float kPtRescaleBF16 = 40.f, kPtRescaleFP16 = 14.f;
 
+// Key tiles after which a row's O is folded away into the workspace and begun anew.
+// The tensor cores cut an accumulation off to fp32 after every 16 keys, so that n keys
+// of alike weight came out low by 0.85 n / 16 ulps: 2e-4 at 32768 keys, 3.2e-3 at
+// 524288, more than six half steps of fp16.  Folded every 32768 keys, no sum loses
+// more than 2048 x 2^-23 = 2^-12.  (4096 tokens on 131072 keys: 6.83 -> 6.82 ms, in fp16
+// at D = 64 5.15 -> 5.23 ms.)
+constexpr int kPtFold = 256;
+
 struct PtItem {
     int b, hk, q0, n, L, prefix;   // request, kv head, first query token, query tokens, length, prefix keys
     int tok0;                      // first token (of the request) of the item's rows
@@ -251,6 +259,19 @@ __device__ __forceinline__ float pt_weights(const uint32_t (&v)[32], uint32_t (&
         pk[c >> 1] = pack2<kBF16>(x.x, x.y);
     }
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+
+// o += f times the N folded sums at `fold` (its row's, four dims every kPtRows vectors).
+template <int N>
+__device__ __forceinline__ void pt_add_folded(uint32_t (&o)[N], const float4* fold, float f) {
+#pragma unroll
+    for (int e = 0; e < N / 4; ++e) {
+        const float4 x = __ldcg(fold + e * kPtRows);
+        o[4 * e] = __float_as_uint(fmaf(f, x.x, __uint_as_float(o[4 * e])));
+        o[4 * e + 1] = __float_as_uint(fmaf(f, x.y, __uint_as_float(o[4 * e + 1])));
+        o[4 * e + 2] = __float_as_uint(fmaf(f, x.z, __uint_as_float(o[4 * e + 2])));
+        o[4 * e + 3] = __float_as_uint(fmaf(f, x.w, __uint_as_float(o[4 * e + 3])));
+    }
 }
 
 template <int N>
@@ -628,7 +649,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                             }
                             if (!ok) break;
                             tc05::fence_after_sync();
-                            const bool more = j > jb;
+                            const bool more = (j - jb) % kPtFold != 0;  // (a fresh sum behind a fold)
 #pragma unroll
                             for (int kk = 0; kk < kPtKeys / 16; ++kk)
                                 if (one)
@@ -739,7 +760,8 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
         const uint32_t lane_addr = static_cast<uint32_t>(32 * q4) << 16;
         const uint32_t s_addr = tmem + lane_addr + kPtKeys * t, o_addr = tmem + lane_addr + 256 + D * t;
         const int ri = r / G, rg = r - ri * G;
-        int ns = 0, no = 0, nj = 0, u = 0;  // key tiles walked, accumulations drained, parts published; K/V units before the item
+        int ns = 0, u = 0;  // key tiles walked; K/V units before the item
+        int no = 0;         // twice the accumulations drained, plus the parity of the parts published (a register less)
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const int slot = it % kPtItems;
@@ -748,6 +770,12 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             if (I.end) break;
             const int jb = I.jb[t], je = I.je[t], t0 = I.t0, ntiles = I.ntiles;
             float m_used = -INFINITY, l = 0.f;
+            // where the row's O is folded away to, and behind it the reference it had then
+            auto fold_row = [&]() { return p.fold + (static_cast<int>(blockIdx.x) * 2 + t) * (D / 4 + 1) * kPtRows + r; };
+            auto fold_factor = [&](const float4* fold) {
+                const float m = __ldcg(&fold[D / 4 * kPtRows].x);
+                return m == -INFINITY ? 0.f : fast_exp2(m - m_used);
+            };
             if (jb < je) {
                 const int tok = I.tok0 + t * TOK + ri;
                 const bool valid = ri < TOK && tok < I.n;
@@ -774,6 +802,28 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                 constexpr float kRescale = kBF16 ? kPtRescaleBF16 : kPtRescaleFP16;
                 for (int j = jb; j < je; ++j, ++ns) {
                     const int kt = pt_tile<kBias>(j, ntiles), tk = t0 + kt * kPtKeys;
+                    if (j > jb && (j - jb) % kPtFold == 0 && warp_on) {
+                        // O so far, with what was folded before, to the workspace; the product
+                        // of this tile, which waits for its P, begins a new one
+                        if (!pt_wait(bar(S::B_OD + t), (ns - 1) & 1, p)) { ok = false; break; }
+                        tc05::fence_after_sync();
+                        float4* fold = fold_row();
+                        const bool any = j - jb > kPtFold;
+                        const float f = any ? fold_factor(fold) : 0.f;
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tc05::ld_32x32b_x16(o_addr + c, o);
+                            tc05::wait_ld();
+                            if (any) pt_add_folded<16>(o, fold + c / 4 * kPtRows, f);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                __stcg(fold + (c / 4 + e) * kPtRows,
+                                       make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                   __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
+                        }
+                        __stcg(&fold[D / 4 * kPtRows].x, m_used);
+                    }
                     if (!pt_wait(bar(S::B_SF + t), ns & 1, p)) { ok = false; break; }
                     if (warp_on) {
                         tc05::fence_after_sync();
@@ -945,9 +995,11 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                 const bool whole = nsplit <= 1 && !partials;
                 const long long part0 = whole ? 0 : static_cast<long long>(I.split) * p.T * p.Hq;
                 const float inv = l > 0.f ? (whole ? p.v_scale : 1.f) / l : 0.f;
+                const bool long_sum = je - jb > kPtFold;
+                const float folded = long_sum ? fold_factor(fold_row()) : 0.f;
                 if (live) {
-                    if (!pt_wait(bar(S::B_OF + t), no & 1, p)) { ok = false; break; }
-                    ++no;
+                    if (!pt_wait(bar(S::B_OF + t), no >> 1 & 1, p)) { ok = false; break; }
+                    no += 2;
                     tc05::fence_after_sync();
                 }
                 // 64 output bytes of every row at a time through the warp's staging area, so
@@ -985,6 +1037,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                             __syncwarp();
                             if (lane == 0) mbar_arrive(bar(S::B_OE + t));
                         }
+                        if (long_sum) pt_add_folded<32>(o, fold_row() + c / 4 * kPtRows, folded);
                     }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = l > 0.f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
@@ -1022,15 +1075,15 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(S::B_JA + t));
                     if (q4 == 0) {
-                        if (!pt_wait(bar(S::B_JA + t), nj & 1, p)) { ok = false; break; }
+                        if (!pt_wait(bar(S::B_JA + t), no & 1, p)) { ok = false; break; }
                         if (lane == 0) {
                             scan[24 + t] = atom_add_acq_rel_gpu(p.counters + I.unit);
                             mbar_arrive(bar(S::B_JD + t));
                         }
                         __syncwarp();
                     }
-                    if (!pt_wait(bar(S::B_JD + t), nj & 1, p)) { ok = false; break; }
-                    ++nj;
+                    if (!pt_wait(bar(S::B_JD + t), no & 1, p)) { ok = false; break; }
+                    no ^= 1;
                     if (scan[24 + t] == nsplit * tiles - 1) {
                         const int rows = (tok_end - I.tok0) * G;
                         const long long step = static_cast<long long>(p.T) * p.Hq;
