@@ -39,6 +39,9 @@ struct AttendParams {
     float scale_log2;             // logit = q.k * scale_log2 (log2 units), without a cap
     float cap_in, cap_log2;       // with one: cap_log2 * tanh(q.k * cap_in / (2 log2 e)); cap_log2 = 0: none
     float cap_c[5], cap_far;      // the capped logit as q.k times a polynomial in (q.k)^2, for |q.k| <= cap_far
+    // tcgen05 kernel: a row's weights are 2^(logit - m), m = its maximum + ref_up when the
+    // reference was set; ref_pow = 2^ref_up
+    float ref_up, ref_pow;
     float v_scale;
     uint64_t wait_ns;             // limit of a wait on a copy (0: a single test, PKD_FLAG_TEST_TIMEOUT)
 };

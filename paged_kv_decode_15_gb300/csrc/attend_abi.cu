@@ -36,10 +36,27 @@ struct AttendPlan {
     bool step;                // the step grid, else the tcgen05 kernel
     int G, rows, chunk, max_splits;
     long long pairs, units;   // row-tile pairs of a kv head, split units of all kv heads, at most
+    int ref_up;               // AttendParams: where a row's reference lies above its maximum
     size_t lse_bytes, out_bytes;  // partial results
     size_t fold_bytes;        // of sums over more than kPtFold key tiles: two row tiles a CTA
     size_t bytes() const { return lse_bytes + out_bytes + fold_bytes; }
 };
+
+// Reference of a row's weights in the tcgen05 kernel, for items of at most `keys` keys.
+// It moves when the row's maximum outgrows the room above it, and every move sends a
+// warp through the slow path (with 2^8 of room, half of the key tiles of scores with a
+// spread of 3 had one).
+// fp16 weights (fp16 and e4m3 caches) must stay below 2^16, and below 2^-14 they lose
+// bits: each is off by 2^-25 at most.  A maximum that starts at 2^up leaves 2^(15 - up)
+// of room, and the small weights together are off by keys * 2^-(25 + up) of the sum at
+// most: 2^-13 up to 2^26 keys.  (Started at 1, 131072 weights of e^-18 beside one of 1
+// were lost, 2^-9 of the sum.)  Up to 8192 keys up = 1.  bf16 has fp32's range.
+int plan_reference(long long keys, pkd_dtype kv) {
+    if (kv == PKD_BF16) return 0;
+    int up = 1;
+    while (up < 14 && keys > 1ll << (12 + up)) ++up;
+    return -up;
+}
 
 pkd_status check_shape(int B, long long T, int Hq, int Hkv, int D, int P, int max_kv_len, pkd_dtype kv) {
     if (B < 0 || T < 0 || Hq < 1 || Hkv < 1 || P < 1 || max_kv_len < 0)
@@ -118,6 +135,7 @@ pkd_status plan_attend(int B, long long T, int max_q, int Hq, int Hkv, int D, in
     pl.max_splits = vis > 0 ? (int)((vis + 15 + pl.chunk - 1) / pl.chunk) : 1;
     // unsplit: a chunk beyond every length (first key + chunk stays below 2^31)
     if (least * Hkv >= kSms && !partials) pl.max_splits = 1, pl.chunk = kMaxKeys;
+    pl.ref_up = plan_reference(std::min<long long>(vis, pl.chunk), kv);
     if (pl.units * pl.max_splits >= 1ll << 31) return report(PKD_EUNSUPPORTED, "too many work items");
     const size_t parts = (partials || pl.max_splits > 1) ? rows * pl.max_splits : 0;
     if (pl.max_splits > 1 && !partials && pl.units > kMaxUnits)
@@ -193,6 +211,8 @@ void fill(pkd::AttendParams& a, const AttendPlan& pl, uint8_t* ws, int pass, siz
     a.max_splits = pl.max_splits;
     pkd::page_magic(P, a.pmagic, a.pmshift);
     a.scale_log2 = scale2;
+    a.ref_up = (float)pl.ref_up;
+    a.ref_pow = std::ldexp(1.f, pl.ref_up);
     if (softcap > 0.f) {
         // c tanh(s / c) with s = scale q.k: e^{2 s / c} = 2^(q.k * cap_in)
         a.cap_in = 2.f * scale2 / softcap;

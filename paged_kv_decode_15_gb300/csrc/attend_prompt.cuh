@@ -8,8 +8,9 @@
 //   S = Q K^T     tcgen05.mma, M = 128 rows, N = 128 keys: both operands in
 //                 shared memory, K-major, 128-byte swizzle, as TMA lands them
 //   softmax       one row per thread (TMEM lane = row): no shuffles.  The
-//                 reference maximum moves only when a row's maximum grows by more
-//                 than 2^40, in fp16 2^14 (O and l are then rescaled by the row's own warp)
+//                 reference of its weights moves only when a row's maximum outgrows it by
+//                 2^14 to 2^40 (O and l are then rescaled by the row's own warp; how far, and
+//                 from where, is the plan's choice: AttendParams::ref_up)
 //   O += P V      P in TMEM over the spent S (A operand from tensor memory),
 //                 V in shared memory read MN-major
 // Two row tiles share every K/V tile, and while the softmax of one runs, the
@@ -55,11 +56,10 @@ constexpr int kPtMaxBatch = 2048;  // requests whose tile prefix the CTA keeps i
 constexpr int kPtL2Bytes = 64 << 20;  // keys and values walked together
 // Row-tile pairs that a launch orders by weight, and items per CTA up to which it does.
 constexpr int kPtMaxOrder = 512, kPtOrderItems = 16;
-// A row's reference moves when its maximum has grown by more than this (log2
-// units).  The weights only must not overflow the operand type: bf16 has fp32's
-// range, fp16 ends at 2^16.  (With 2^8 for both, half of the key tiles of scores
-// with a spread of 3 had some warp move its references.)
-constexpr float kPtRescaleBF16 = 40.f, kPtRescaleFP16 = 14.f;
+// A row's reference m moves when its maximum exceeds m by this (log2 units): its weights
+// 2^(logit - m) must not overflow the operand type.  bf16 has fp32's range, fp16 ends at
+// 2^16.  Where the reference lies to begin with is the plan's choice (AttendParams::ref_up).
+constexpr float kPtRoomBF16 = 40.f, kPtRoomFP16 = 15.f;
 
 // Key tiles after which a row's O is folded away into the workspace and begun anew.
 // The tensor cores cut an accumulation off to fp32 after every 16 keys, so that n keys
@@ -799,7 +799,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                 // (with a bias no key from there on lies behind some row's position)
                 const int mh = bad ? 0 : __reduce_min_sync(kFull, valid ? min(min(hi, hi_all), kBias ? pos + 1 : hi_all) : 0x7fffffff);
                 int wide = 0;  // tiles left before a capped score out of the polynomial's range counts no more
-                constexpr float kRescale = kBF16 ? kPtRescaleBF16 : kPtRescaleFP16;
+                constexpr float kRoom = kBF16 ? kPtRoomBF16 : kPtRoomFP16;
                 for (int j = jb; j < je; ++j, ++ns) {
                     const int kt = pt_tile<kBias>(j, ntiles), tk = t0 + kt * kPtKeys;
                     if (j > jb && (j - jb) % kPtFold == 0 && warp_on) {
@@ -864,7 +864,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                                 sum += pt_weights<kBF16>(x, pk[c], scale, m);
                                 if (c < 3) tc05::wait_ld(v[(c + 1) & 1]);
                             }
-                            const bool grown = top * scale > m_used + kRescale, out = kCap && far > cap_far;
+                            const bool grown = top * scale > m_used + kRoom, out = kCap && far > cap_far;
                             done = !__any_sync(kFull, grown || out);
                             if (done) {
                                 l += sum;
@@ -926,10 +926,11 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                             }
                             if constexpr (!kBias)
                                 top = top == -INFINITY ? top : kCap ? capped(top, p.cap_in, p.cap_log2) : top * p.scale_log2;
-                            const bool need = top > m_used + kRescale;
+                            const bool need = top > m_used + kRoom;
                             if (__any_sync(kFull, need)) {
-                                const float alpha = need ? fast_exp2(m_used - top) : 1.f;
-                                if (need) m_used = top;
+                                const float m_new = top + p.ref_up;
+                                const float alpha = need ? fast_exp2(m_used - m_new) : 1.f;
+                                if (need) m_used = m_new;
                                 l *= alpha;
                                 if (j > jb) {
                                     if (!pt_wait(bar(S::B_OD + t), (ns - 1) & 1, p)) { ok = false; break; }
@@ -1059,7 +1060,8 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     }
                 }
                 if (valid) {
-                    const float l2 = l > 0.f ? m_used + __log2f(l) : -INFINITY;
+                    // (both shifts are exact: l's logarithm is taken near 1)
+                    const float l2 = l > 0.f ? (m_used - p.ref_up) + __log2f(l * p.ref_pow) : -INFINITY;
                     if (!whole)
                         __stcg(p.part_lse + part0 + row, l2);
                     else if (p.lse)
