@@ -369,6 +369,8 @@ const char* pkd_paged_attention_kernel_name(int batch, int64_t total_tokens, int
  * lse = -inf.  Keys and values before the first and behind the last key that a
  * request's tokens see do not enter its results, whatever they hold; the values
  * between must be finite also for the tokens that do not see them (with weight 0).
+ * Sums run in fp32: the keys that a token sees times the largest value among
+ * them must stay below its range.
  * Limits: head_dim 64 or 128; page_size a multiple of 16; num_heads/num_kv_heads
  * <= 128; batch <= 2048, batch * num_kv_heads <= 65536; max_kv_len <= 2^29;
  * scale * q_scale * k_scale > 0; fp8 caches need head_dim 128.

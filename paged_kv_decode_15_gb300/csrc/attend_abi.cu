@@ -50,9 +50,12 @@ struct AttendPlan {
 // bits: each is off by 2^-25 at most.  A maximum that starts at 2^up leaves 2^(15 - up)
 // of room, and the small weights together are off by keys * 2^-(25 + up) of the sum at
 // most: 2^-13 up to 2^26 keys.  (Started at 1, 131072 weights of e^-18 beside one of 1
-// were lost, 2^-9 of the sum.)  Up to 8192 keys up = 1.  bf16 has fp32's range.
+// were lost, 2^-9 of the sum.)  Up to 8192 keys up = 1.
+// bf16 has fp32's range, and so has V: weights above 1 could take O out of it (with a
+// room of 2^40 above 1, values above 3e26 did).  A maximum that starts at 2^-20 has that
+// room below 1, and loses only weights below 2^-106 of its own.
 int plan_reference(long long keys, pkd_dtype kv) {
-    if (kv == PKD_BF16) return 0;
+    if (kv == PKD_BF16) return 20;
     int up = 1;
     while (up < 14 && keys > 1ll << (12 + up)) ++up;
     return -up;

@@ -9,7 +9,7 @@
 //                 shared memory, K-major, 128-byte swizzle, as TMA lands them
 //   softmax       one row per thread (TMEM lane = row): no shuffles.  The
 //                 reference of its weights moves only when a row's maximum outgrows it by
-//                 2^14 to 2^40 (O and l are then rescaled by the row's own warp; how far, and
+//                 2^14 or so (O and l are then rescaled by the row's own warp; how far, and
 //                 from where, is the plan's choice: AttendParams::ref_up)
 //   O += P V      P in TMEM over the spent S (A operand from tensor memory),
 //                 V in shared memory read MN-major
@@ -57,9 +57,10 @@ constexpr int kPtL2Bytes = 64 << 20;  // keys and values walked together
 // Row-tile pairs that a launch orders by weight, and items per CTA up to which it does.
 constexpr int kPtMaxOrder = 512, kPtOrderItems = 16;
 // A row's reference m moves when its maximum exceeds m by this (log2 units): its weights
-// 2^(logit - m) must not overflow the operand type.  bf16 has fp32's range, fp16 ends at
-// 2^16.  Where the reference lies to begin with is the plan's choice (AttendParams::ref_up).
-constexpr float kPtRoomBF16 = 40.f, kPtRoomFP16 = 15.f;
+// 2^(logit - m) must not overflow the operand type, which for fp16 ends at 2^16, and with
+// bf16, whose V has fp32's range, they stay at 1 or below, so that O does not leave it.
+// Where the reference lies to begin with is the plan's choice (AttendParams::ref_up).
+constexpr float kPtRoomBF16 = 0.f, kPtRoomFP16 = 15.f;
 
 // Key tiles after which a row's O is folded away into the workspace and begun anew.
 // The tensor cores cut an accumulation off to fp32 after every 16 keys, so that n keys

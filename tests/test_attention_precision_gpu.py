@@ -26,13 +26,14 @@ class Long:
     a head's query its gap, the scale 1/8: gap * profile is added to scores that are alike
     but for a spread of 0.05 or so."""
 
-    def __init__(self, n, T, G, Hkv, D, dtype, profile, gaps, seed=61):
+    def __init__(self, n, T, G, Hkv, D, dtype, profile, gaps, seed=61, size=1.0):
         rng = np.random.default_rng(seed)
         self.n, self.T, self.G, self.Hkv, self.D, self.dtype, self.scale, self.gaps = n, T, G, Hkv, D, dtype, 0.125, gaps
         k = rng.standard_normal((n, Hkv, D)).astype(np.float32)
         k[:, :, 0] = 8.0 * profile[:, None]
         v = 1.0 + 0.25 * rng.standard_normal((n, Hkv, D)).astype(np.float32)
         v[profile == profile.max()] = -1.0
+        v *= size
         q = 0.05 * rng.standard_normal((Hkv, len(gaps), D)).astype(np.float32)
         q[:, :, 0] = gaps
         t, P = ref.TORCH[dtype], 64
@@ -186,3 +187,33 @@ def test_a_long_prefix_of_many_requests(dtype, D):
     out, lse = pkd.prefix_decode(c.queries.view(B, 1, 256, D), c.cache, c.table, c.lens,
                                  c.table[:, :1].expand(B, 1).contiguous(), own, c.scale, out_dtype=torch.float32)
     c.check(out.view(B, 256, D), lse.view(B, 256))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n,size", [(2048, 3e34), (2048, 1e-30), (40000, 3e33)])
+@pytest.mark.parametrize("mod", ["plain", "cap", "bias"])
+def test_values_of_any_size(dtype, n, size, mod):
+    """Scores that rise by 24, 2^34.6, along the keys: the weights on the way must not take
+    large values out of fp32's range, nor small ones (fp16: of its own range)."""
+    import paged_kv_decode_15_gb300 as pkd
+    if dtype == "fp16":
+        size = {3e34: 2e4, 3e33: 2e4, 1e-30: 1e-3}[size]
+    c = Long(n, 152, 128, 2, 64, dtype, ramp(n), [0.0, 1.0, 10.0, 24.0], size=size)
+    slope = 2.0 ** -14 if mod == "bias" else 0.0
+    out, lse = pkd.paged_attention(c.queries, c.cache, c.table, c.lens, c.starts, c.scale, causal=True,
+                                   softcap=1e5 if mod == "cap" else 0.0, out_dtype=torch.float32,
+                                   alibi_slopes=torch.full((256,), slope, device="cuda") if slope else None)
+    c.check(out, lse, True, slope)
+
+
+@pytest.mark.parametrize("T", [2, 40])
+def test_large_values_in_split_keys_and_shared_prefixes(T):
+    import paged_kv_decode_15_gb300 as pkd
+    c = Long(2048, T, 8, 2, 128, "bf16", ramp(2048), [0.0, 1.0, 10.0, 24.0], size=3e34)
+    out, lse = pkd.paged_attention(c.queries, c.cache, c.table, c.lens, c.starts, c.scale, causal=False,
+                                   out_dtype=torch.float32)
+    c.check(out, lse)
+    own = torch.zeros(T, dtype=torch.int32, device="cuda")
+    out, lse = pkd.prefix_decode(c.queries.view(T, 1, 16, 128), c.cache, c.table, c.lens,
+                                 c.table[:, :1].expand(T, 1).contiguous(), own, c.scale, out_dtype=torch.float32)
+    c.check(out.view(T, 16, 128), lse.view(T, 16))
