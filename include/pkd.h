@@ -343,7 +343,7 @@ const char* pkd_paged_attention_kernel_name(int batch, int64_t total_tokens, int
  *                q_stride elements between tokens (a multiple of 16 bytes)
  *   kv_cache, block_table, seq_lens  as for pkd_paged_decode; seq_lens[b] = L counts
  *                the keys of request b including those of its query tokens
- *                (already in the cache)
+ *                (already in the cache).  block_table may be NULL with max_kv_len 0
  *   query_start  device int32 [batch + 1]: request b's query tokens are rows
  *                [query_start[b], query_start[b + 1]) of q, at most max_query_len;
  *                rows of q outside every request are neither read into a result
@@ -405,7 +405,7 @@ pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_strid
  *                 (and the diagnostic PKD_FLAG_TEST_TIMEOUT)
  *
  * The workspace is as for pkd_paged_attention.  max_prefix_len and max_kv_len
- * bound prefix_lens and seq_lens.  Limits as for
+ * bound prefix_lens and seq_lens; a table whose bound is 0 may be NULL.  Limits as for
  * pkd_paged_attention, groups <= 2048.
  */
 size_t pkd_prefix_decode_workspace_size(int batch, int sq, int num_heads, int num_kv_heads, int head_dim,

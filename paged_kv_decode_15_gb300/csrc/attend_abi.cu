@@ -314,7 +314,8 @@ pkd_status check_call(const void* q, pkd_dtype q_dtype, int64_t q_stride, const 
 }
 
 pkd_status check_table(const int32_t* table, int64_t stride, const int32_t* lens, int max_len, int P, const char* name) {
-    if (!table || !lens) return report(PKD_EINVAL, "null pointer argument");
+    // (no keys, no columns: such a table may be null, and is not read)
+    if ((!table && max_len > 0) || !lens) return report(PKD_EINVAL, "null pointer argument");
     if (!aligned(table, 4) || !aligned(lens, 4)) return report(PKD_EINVAL, "misaligned %s or lengths", name);
     const int64_t need = ((int64_t)max_len + P - 1) / P;
     if (stride < need)
