@@ -154,8 +154,9 @@ pkd_status plan_paged_attention(int B, long long T, int max_q, int Hq, int Hkv, 
                                 pkd_dtype kv, const pkd_score_options& o, AttendPlan& pl) {
     pkd_status st = check_shape(B, T, Hq, Hkv, D, P, max_kv_len, kv);
     if (st != PKD_OK) return st;
-    if (max_q < 1) return report(PKD_EINVAL, "max_query_len must be >= 1 (got %d)", max_q);
-    max_q = (int)std::min<long long>(max_q, std::max(T, 1ll));
+    // (the most that a batch of no requests brings is 0)
+    if (max_q < 0 || (max_q == 0 && T > 0)) return report(PKD_EINVAL, "max_query_len must be >= 1 (got %d)", max_q);
+    max_q = (int)std::max(1ll, std::min<long long>(max_q, T));
     long long vis = max_kv_len;
     // a window bounds the span of a request's keys, unless prefix keys are seen past the position
     if (o.window > 0 && !o.prefix_lens) vis = std::min(vis, (long long)o.window + max_q - 1 + 15);

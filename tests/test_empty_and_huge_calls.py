@@ -25,3 +25,11 @@ def test_a_table_without_columns_may_be_null(lib):
     for call, name in ((attend, "table"), (prefix, "table"), (prefix, "ptable")):
         assert call(lib, **{name: None}) == pkd.EINVAL and "null" in error(lib)
     assert prefix(lib, ptable=None, pstride=0, max_prefix=0, plens=None) == pkd.EINVAL and "null" in error(lib)
+
+
+def test_the_most_that_no_requests_bring_is_nothing(lib):
+    """An empty batch whose caller takes the largest of no lengths."""
+    assert attend(lib, T=0, max_q=0) == pkd.OK and attend(lib, B=0, T=0, max_q=0) == pkd.OK
+    assert lib.pkd_paged_attention_workspace_size(0, 0, 0, 4, 2, 128, 16, 100, pkd.BF16, None) > 0
+    assert attend(lib, T=1, max_q=0) == pkd.EINVAL and "max_query_len" in error(lib)
+    assert attend(lib, T=0, max_q=-1) == pkd.EINVAL and "max_query_len" in error(lib)
