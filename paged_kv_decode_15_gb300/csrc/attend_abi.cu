@@ -76,7 +76,7 @@ pkd_status check_shape(int B, long long T, int Hq, int Hkv, int D, int P, int ma
     if (B > pkd::kPtMaxBatch) return report(PKD_EUNSUPPORTED, "batch %d > %d", B, pkd::kPtMaxBatch);
     if (max_kv_len > kMaxKeys) return report(PKD_EUNSUPPORTED, "lengths of up to %d keys are not supported (2^29)", max_kv_len);
     if (Hkv > 65535) return report(PKD_EUNSUPPORTED, "num_kv_heads %d > 65535", Hkv);
-    if (T * Hq >= 1ll << 31) return report(PKD_EUNSUPPORTED, "tokens*num_heads must be < 2^31");
+    if (T > 0x7fffffffll / Hq) return report(PKD_EUNSUPPORTED, "tokens*num_heads must be < 2^31");
     return PKD_OK;
 }
 
@@ -182,7 +182,7 @@ pkd_status plan_prefix(int B, int sq, int Hq, int Hkv, int D, int P, int groups,
     const bool step = (long long)sq * (Hq / Hkv) <= 16;
     st = plan_attend(groups, T, T > 0 ? T : 1, Hq, Hkv, D, P, max_prefix_len, kv, true, false, pl.pre);
     if (st != PKD_OK) return st;
-    st = plan_attend(B, T, sq, Hq, Hkv, D, P, max_kv_len, kv, false, step, pl.own);
+    st = plan_attend(B, T, std::min(sq, std::max(T, 1)), Hq, Hkv, D, P, max_kv_len, kv, false, step, pl.own);
     if (st != PKD_OK) return st;
     pl.off_own = kPartials + pl.pre.bytes();
     pl.off_own_lse = pl.off_own + pl.own.bytes();
@@ -301,8 +301,9 @@ pkd_status check_call(const void* q, pkd_dtype q_dtype, int64_t q_stride, const 
         return report(PKD_EINVAL, "misaligned pointer (q, kv_cache, out: 16 B; workspace: 256 B)");
     if (q_stride < (int64_t)Hq * D || (q_stride * elt_bytes(q_dtype)) % 16)
         return report(PKD_EINVAL, "q_stride must be >= num_heads*head_dim and a multiple of 16 bytes");
+    if (q_stride > (int64_t)1 << 38) return report(PKD_EUNSUPPORTED, "q_stride > 2^38 elements");  // a tensor map's limit
     if (num_pages < 1) return report(PKD_EINVAL, "num_pages must be >= 1");
-    if (num_pages > 0x7fffffff || num_pages * Hkv * P >= (int64_t)1 << 31)
+    if (num_pages > 0x7fffffffll / ((int64_t)Hkv * P))
         return report(PKD_EUNSUPPORTED, "cache too large: num_pages*num_kv_heads*page_size must be < 2^31");
     if (workspace_bytes < need)
         return report(PKD_EINVAL, "workspace too small: %zu < %zu bytes", workspace_bytes, need);

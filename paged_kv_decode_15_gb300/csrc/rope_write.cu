@@ -260,6 +260,8 @@ extern "C" pkd_status pkd_rope_cache_write(const void* q, int64_t q_stride, cons
         return report(PKD_EUNSUPPORTED, "cache dtype %d must equal the input dtype or be fp8-e4m3", (int)kv_dtype);
     if (num_heads > 0 && q_out_dtype != in_dtype && q_out_dtype != PKD_FP8_E4M3)
         return report(PKD_EUNSUPPORTED, "q_out dtype %d must equal the input dtype or be fp8-e4m3", (int)q_out_dtype);
+    if (num_pages > ((int64_t)1 << 50) / ((int64_t)page_size * num_kv_heads))
+        return report(PKD_EUNSUPPORTED, "cache too large: num_pages*num_kv_heads*page_size must be <= 2^50");
     const int64_t qrow = (int64_t)num_heads * head_dim, krow = (int64_t)num_kv_heads * head_dim;
     if (q_stride < qrow || q_out_stride < qrow || key_stride < krow || value_stride < krow || q_stride % 8 ||
         q_out_stride % 8 || key_stride % 8 || value_stride % 8)
