@@ -102,7 +102,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // c tanh(scale q.k / c) in log2 units, y = scale q.k / c, with x = q.k * cap_in =
 // 2 y log2 e: tanh(y) = 1 - 2 / (1 + 2^x), off by 2^-23 of the cap or so; near 0,
 // where that would be lost on a large cap, y times the first terms of tanh's series
-// (|y| < 0.174, the next term below 3e-9 of y).  2^inf and 2^-inf give +-1.
+// (|y| < 0.174, off by 1.8e-8 of y at most).  2^inf and 2^-inf give +-1.
 __device__ __forceinline__ float capped(float qk, float cap_in, float cap_log2) {
     const float x = qk * cap_in, y = x * 0.34657359f, z = y * y;
     const float near = y * fmaf(z, fmaf(z, fmaf(z, -0.053968254f, 0.13333334f), -0.33333334f), 1.f);

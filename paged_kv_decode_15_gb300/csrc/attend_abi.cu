@@ -222,8 +222,9 @@ void fill(pkd::AttendParams& a, const AttendPlan& pl, uint8_t* ws, int pass, siz
         a.cap_in = 2.f * scale2 / softcap;
         a.cap_log2 = softcap * pkd::kLog2e;
         // tanh(y) = y P(y^2) for |y| <= 0.6, P interpolating tanh(y)/y at the five
-        // Chebyshev points of y^2 in [0, 0.36] (off by 4e-8 at most); y = k q.k, and k
-        // and the scale go into the coefficients where they stay in fp32's range
+        // Chebyshev points of y^2 in [0, 0.36] (P off by 7.5e-8 at most, y P by 3.9e-8);
+        // y = k q.k, and k and the scale go into the coefficients where they stay in
+        // fp32's range
         static const double c[5] = {0.99999992596295, -0.3333230204036953, 0.1331006442560933, -0.05209665340812269,
                                     0.015468751301830112};
         const double k = (double)scale2 / ((double)softcap * pkd::kLog2e);

@@ -284,7 +284,7 @@ __device__ __forceinline__ void reg_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// kPartials: every result is left as a partial one (for a merge that follows)
+// partials: every result is left as a partial one (for a merge that follows)
 template <int D, int kType, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kPtThreads, 1)
 attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
