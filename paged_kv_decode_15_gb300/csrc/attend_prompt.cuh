@@ -60,6 +60,7 @@ constexpr int kPtMaxOrder = 512, kPtOrderItems = 16;
 // 2^(logit - m) must not overflow the operand type, which for fp16 ends at 2^16, and with
 // bf16, whose V has fp32's range, they stay at 1 or below, so that O does not leave it.
 // Where the reference lies to begin with is the plan's choice (AttendParams::ref_up).
+// (Taken from the difference: a sum m + 15 of large logits would round up to m + 16.)
 constexpr float kPtRoomBF16 = 0.f, kPtRoomFP16 = 15.f;
 
 // Key tiles after which a row's O is folded away into the workspace and begun anew.
@@ -865,7 +866,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                                 sum += pt_weights<kBF16>(x, pk[c], scale, m);
                                 if (c < 3) tc05::wait_ld(v[(c + 1) & 1]);
                             }
-                            const bool grown = top * scale > m_used + kRoom, out = kCap && far > cap_far;
+                            const bool grown = fmaf(top, scale, -m_used) > kRoom, out = kCap && far > cap_far;
                             done = !__any_sync(kFull, grown || out);
                             if (done) {
                                 l += sum;
@@ -927,7 +928,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                             }
                             if constexpr (!kBias)
                                 top = top == -INFINITY ? top : kCap ? capped(top, p.cap_in, p.cap_log2) : top * p.scale_log2;
-                            const bool need = top > m_used + kRoom;
+                            const bool need = top - m_used > kRoom;
                             if (__any_sync(kFull, need)) {
                                 const float m_new = top + p.ref_up;
                                 const float alpha = need ? fast_exp2(m_used - m_new) : 1.f;

@@ -123,6 +123,18 @@ def test_long_sums_whose_references_move(dtype, D, mod):
     c.check(out, lse, True, slope)
 
 
+@pytest.mark.parametrize("dtype,D", [("fp16", 64), ("fp8", 128)])
+def test_a_long_prefix_and_long_own_keys(dtype, D):
+    """Both passes fold, each in its own part of the workspace, while they may overlap."""
+    import paged_kv_decode_15_gb300 as pkd
+    n, T, cut = 80000, 152, 600
+    c = Long(n, T, 128, 2, D, dtype, ramp(n), [0.0, 1.0, 10.0, 24.0])
+    lens = torch.tensor([cut * 64], dtype=torch.int32, device="cuda")
+    out, lse = pkd.prefix_decode(c.queries.view(1, T, 256, D), c.cache, c.table[:, :cut].contiguous(), lens,
+                                 c.table[:, cut:].contiguous(), c.lens - lens, c.scale, causal=True, out_dtype=torch.float32)
+    c.check(out.view(T, 256, D), lse.view(T, 256), True)
+
+
 SINK = [0.0, 6.0, 10.0, 13.0, 16.0, 18.0, 20.0, 24.0]
 
 
@@ -204,6 +216,29 @@ def test_values_of_any_size(dtype, n, size, mod):
                                    softcap=1e5 if mod == "cap" else 0.0, out_dtype=torch.float32,
                                    alibi_slopes=torch.full((256,), slope, device="cuda") if slope else None)
     c.check(out, lse, True, slope)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("exponent", [22, 24, 25, 26, 27, 28])
+def test_logits_so_large_that_fp32_has_few_digits_left(dtype, exponent):
+    """Logits of 2^exponent (log2 units) that rise by 16 here and there: the largest weight
+    is one whatever the rest, so the result lies among the values."""
+    import paged_kv_decode_15_gb300 as pkd
+    n, T, half = 1024, 304, exponent // 2
+    k = torch.zeros(n, 128)
+    k[:, 0] = 2.0 ** (exponent - half)
+    k[:, 1] = 2.0 * torch.tensor([0, 1, 2, 3, 3, 4, 4, 2]).repeat_interleave(128)  # times 8: key tiles that rise by 16 or not
+    k[:, 64:] = torch.from_numpy(np.random.default_rng(88).uniform(1, 2, (n, 64)).astype(np.float32))
+    q = torch.zeros(T, 128, 64)
+    q[..., 0], q[..., 1] = 2.0 ** half, 8.0
+    t = ref.TORCH[dtype]
+    cache = k.to(t).view(n // 64, 1, 64, 128).contiguous().cuda()
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    out, lse = pkd.paged_attention(q.to(t).cuda(), cache, ints([list(range(n // 64))]), ints([n]), ints([0, T]), float(np.log(2.0)),
+                                   causal=False, out_dtype=torch.float32)
+    assert torch.isfinite(out).all() and out.min() >= 1 - 2.0 ** -7 and out.max() <= 2 + 2.0 ** -6
+    top = np.log(2.0) * (2.0 ** exponent + 64)
+    assert (lse.double().cpu() - top).abs().max() <= 1e-6 * top + np.log(n)
 
 
 @pytest.mark.parametrize("T", [2, 40])
