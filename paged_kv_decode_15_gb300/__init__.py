@@ -599,7 +599,10 @@ def paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, *, c
     slope * distance; window: keys from position - (window - 1) on; prefix_lens
     int32 [B]: keys that all of a request's tokens see; doc_start int32 [T]:
     first key of each token's document.  max_query_len (default T) and
-    max_kv_len (default the table's capacity) bound the lengths on the host.
+    max_kv_len (default the table's capacity) bound the lengths on the host and
+    with them choose the kernel and the split of the keys: give the batch's own
+    (1 for single tokens, which have a kernel of their own; without it T tokens
+    may be one request's).
     Lengths, pages or starts out of range are clamped or skipped; workspace_check
     (of workspace, or of the one kept for calls without) then says so.
     test_timeout sets the diagnostic PKD_FLAG_TEST_TIMEOUT.

@@ -25,8 +25,8 @@
 // Registers follow the roles (setmaxnreg).  (An epilogue group of its own left the
 // softmax 176 registers and spills: 8192-token prompt 523 us, not 416.)
 //
-// What bounds it, D = 128 (32768-token prompt, 32 heads: 6.0 ms, 1470 TFLOP/s, 0.79 of
-// a dense library product; 8192 tokens 416 us): per row tile a loop of the softmax
+// What bounds it, D = 128 (32768-token prompt, 32 heads: 6.1 ms a call, 1440 TFLOP/s,
+// 0.77 of a dense library product; 8192 tokens 414 us): per row tile a loop of the softmax
 // (1540 cycles a key tile: 940 of exponentials and packing, the rest TMEM loads and
 // stores and the arrival), the issuing warp's wake-up (270), the products (1120) and
 // the softmax's (300).  Two row tiles run interleaved, so the tensor cores, 2050

@@ -11,7 +11,7 @@
 // stay in registers; a stage inside every row's interval skips the mask.
 //
 // 64 requests, 145k keys x 8 kv heads in bf16, capped: 94 us, 0.94 of the copy
-// bandwidth.  4 requests, 309k keys x 8 kv heads in e4m3 with a bias: 116 us, 0.81: there
+// bandwidth.  4 requests, 309k keys x 8 kv heads in e4m3 with a bias: 117 us, 0.80: there
 // a key is half the bytes and the same conversions and biases, and the ALU pipe is 49%
 // busy.  One request of 611 keys: 9 us, a chain of start-up loads, stages and join.
 #pragma once
