@@ -421,6 +421,95 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
                              size_t workspace_bytes, unsigned flags, void* stream);
 
 /*
+ * Attention weight that each key of a paged cache received: what keeps a cache of
+ * bounded size (pkd_evict_select, pkd_cache_compact) knows its keys by.
+ *
+ *   weights[b, h, t] = decay * prior[b, h, t]
+ *                    + sum over tokens i of request b and query heads g of kv head h
+ *                      of exp(s(i, g, t) - lse(i, g))
+ * with the scaled (and capped) scores and the masks of pkd_paged_attention, whose LSE
+ * over the same keys makes the exponential a probability.
+ *
+ *   q, kv_cache, block_table, seq_lens, query_start, max_query_len, softcap, window,
+ *                flags  as for pkd_paged_attention (V is not read)
+ *   last_queries w > 0: only the last w tokens of each request weigh its keys
+ *   lse          device fp32 [total_tokens, num_heads]; a token of lse -inf weighs nothing
+ *   prior        device fp32 [batch, num_kv_heads, >= max_kv_len], or NULL: 0.  Rows
+ *                of keys contiguous, strides in elements.  Not read for keys of the
+ *                call's own tokens (the last query_start[b + 1] - query_start[b] of
+ *                seq_lens[b]), nor behind seq_lens[b]: they start at 0
+ *   weights      device fp32, laid out like prior with strides of its own; may be prior
+ *                itself, no other overlap.  Entries behind seq_lens[b] are left as they
+ *                were
+ *   workspace    as for pkd_paged_attention (its status word: lengths, starts and pages
+ *                out of range; keys on such a page receive nothing)
+ *
+ * Sums run in fp32, in an order fixed by the arguments: results repeat bit for bit.  A
+ * key that no token sees receives 0 whatever its K holds.  Limits as for
+ * pkd_paged_attention.  The workspace size is 0 for an invalid request.
+ */
+size_t pkd_key_weights_workspace_size(int batch, int64_t total_tokens, int max_query_len, int last_queries,
+                                      int num_heads, int num_kv_heads, int head_dim, int page_size, int max_kv_len,
+                                      pkd_dtype kv_dtype);
+pkd_status pkd_key_weights(const void* q, pkd_dtype q_dtype, int64_t q_stride, const void* kv_cache,
+                           pkd_dtype kv_dtype, int64_t num_pages, const int32_t* block_table,
+                           int64_t block_table_stride, const int32_t* seq_lens, const int32_t* query_start, int batch,
+                           int64_t total_tokens, int max_query_len, int last_queries, int num_heads,
+                           int num_kv_heads, int head_dim, int page_size, int max_kv_len, float scale, float q_scale,
+                           float k_scale, float softcap, int window, const float* lse, const float* prior,
+                           int64_t prior_batch_stride, int64_t prior_head_stride, float decay, float* weights,
+                           int64_t weights_batch_stride, int64_t weights_head_stride, void* workspace,
+                           size_t workspace_bytes, unsigned flags, void* stream);
+
+/*
+ * The keys of each request and kv head that stay in a cache of at most `budget` keys.
+ *
+ *   weights      device fp32 [batch, num_kv_heads, keys], rows contiguous, strides in
+ *                elements.  NaN counts as -inf
+ *   seq_lens     device int32 [batch], clamped to [0, keys]
+ *   positions    device int32 [batch, num_kv_heads, keys]: where in its request each key
+ *                stood, once earlier compactions have put them out of order, with
+ *                context_lens, device int32 [batch]: the tokens that the request has
+ *                seen.  NULL both: key t stands at t of seq_lens[b]
+ *   kept         device int32 [batch, num_kv_heads, budget]: the indexes of the
+ *                n = min(seq_lens[b], budget) keys that stay, rising; -1 behind them
+ *   kept_lens    device int32 [batch]: n
+ *
+ * Kept are the keys at the first `sinks` and the last `recent` positions, then those of
+ * the largest weight, of equal ones the lowest index.  pool (odd, up to 255): a key's
+ * weight is the largest of the pool keys around it that are neither sinks nor recent.
+ * Limits: sinks + recent <= budget; pool is 1 with positions; keys <= 2^29.
+ */
+pkd_status pkd_evict_select(const float* weights, int64_t weights_batch_stride, int64_t weights_head_stride,
+                            int64_t keys, const int32_t* seq_lens, int batch, int num_kv_heads, int budget, int sinks,
+                            int recent, int pool, const int32_t* positions, int64_t positions_batch_stride,
+                            int64_t positions_head_stride, const int32_t* context_lens, int32_t* kept,
+                            int32_t* kept_lens, void* stream);
+
+/*
+ * Compaction of a paged cache, in place: of the n = kept_lens[b] rows that stay of a
+ * request and kv head, those at index n or behind move into the free slots below n (the
+ * m-th such row into the m-th free slot), so that the request's keys are [0, n).  No
+ * other row moves: the keys' order changes, which attention without a window does not
+ * see (their rotary positions are in them).
+ *
+ *   kept, kept_lens  as pkd_evict_select leaves them: rising indexes per (request, kv head)
+ *   block_table  device int32 [batch, block_table_stride], table_columns of them in use; a
+ *                row whose source or target page lies outside the pool does not move
+ *   weights, positions  device [batch, num_kv_heads, weights_keys / positions_keys] (fp32 /
+ *                int32; rows contiguous, strides in elements) move along, or NULL
+ *
+ * The pages of the slots below n must be one request's own (pages that requests share
+ * behind them are only read).  K and V bits are copied.  Limits: head_dim 64 or 128.
+ */
+pkd_status pkd_cache_compact(void* kv_cache, pkd_dtype kv_dtype, int64_t num_pages, const int32_t* block_table,
+                             int64_t block_table_stride, int table_columns, const int32_t* kept,
+                             const int32_t* kept_lens, int batch, int num_kv_heads, int head_dim, int page_size,
+                             int budget, float* weights, int64_t weights_batch_stride, int64_t weights_head_stride,
+                             int64_t weights_keys, int32_t* positions, int64_t positions_batch_stride,
+                             int64_t positions_head_stride, int64_t positions_keys, void* stream);
+
+/*
  * DASH segmented attention with its combine [DASH flash_dash_attention].
  *
  *   q        device [n, num_heads, head_dim], dtype (bf16 or fp16)

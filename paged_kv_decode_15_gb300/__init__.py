@@ -12,6 +12,9 @@ Entry points (same names as the C ABI in include/pkd.h, without the prefix):
   rope_cache_write(q, key, value, positions, cos_sin, slot_mapping, kv_cache, ...)
   paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, ...)
   prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, scale, ...)
+  key_weights(q, kv_cache, block_table, seq_lens, query_start, lse, scale, ...)
+  evict_select(weights, seq_lens, budget, ...)
+  cache_compact(kv_cache, block_table, kept, kept_lens, ...)
 """
 from __future__ import annotations
 
@@ -37,7 +40,8 @@ SYMBOLS = ("pkd_version", "pkd_last_error", "pkd_paged_decode_workspace_size", "
            "pkd_cache_write",
            "pkd_segmented_attention", "pkd_segmented_attention_paged", "pkd_lse_merge",
            "pkd_rope_cache_write", "pkd_paged_attention_workspace_size", "pkd_paged_attention_kernel_name",
-           "pkd_paged_attention", "pkd_prefix_decode_workspace_size", "pkd_prefix_decode")
+           "pkd_paged_attention", "pkd_prefix_decode_workspace_size", "pkd_prefix_decode",
+           "pkd_key_weights_workspace_size", "pkd_key_weights", "pkd_evict_select", "pkd_cache_compact")
 
 
 class ScoreOptions(ctypes.Structure):
@@ -103,7 +107,13 @@ def load_library(path: str = LIB_PATH):
     lib.pkd_prefix_decode_workspace_size.restype = SZ
     lib.pkd_prefix_decode.argtypes = [P, I, P, I, I64, P, I64, P, P, I, I, P, I64, P, I, I, I, I, I, I, I, F, F, F, F,
                                       F, P, I, P, P, SZ, U, P]
-    for name in ("pkd_rope_cache_write", "pkd_paged_attention", "pkd_prefix_decode", "pkd_workspace_init", "pkd_workspace_check", "pkd_paged_decode", "pkd_paged_decode_static",
+    lib.pkd_key_weights_workspace_size.argtypes = [I, I64, I, I, I, I, I, I, I, I]
+    lib.pkd_key_weights_workspace_size.restype = SZ
+    lib.pkd_key_weights.argtypes = [P, I, I64, P, I, I64, P, I64, P, P, I, I64, I, I, I, I, I, I, I, F, F, F, F, I, P, P,
+                                    I64, I64, F, P, I64, I64, P, SZ, U, P]
+    lib.pkd_evict_select.argtypes = [P, I64, I64, I64, P, I, I, I, I, I, I, P, I64, I64, P, P, P, P]
+    lib.pkd_cache_compact.argtypes = [P, I, I64, P, I64, I, P, P, I, I, I, I, I, P, I64, I64, I64, P, I64, I64, I64, P]
+    for name in ("pkd_key_weights", "pkd_evict_select", "pkd_cache_compact", "pkd_rope_cache_write", "pkd_paged_attention", "pkd_prefix_decode", "pkd_workspace_init", "pkd_workspace_check", "pkd_paged_decode", "pkd_paged_decode_static",
                  "pkd_paged_decode_static_check", "pkd_cache_write", "pkd_segmented_attention", "pkd_segmented_attention_paged", "pkd_lse_merge"):
         getattr(lib, name).restype = I
     _lib = lib
@@ -727,3 +737,173 @@ def prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens,
     if status:
         _check(status)
     return out, lse
+
+
+@functools.lru_cache(maxsize=4096)
+def _weigh_bytes(*plan):
+    """Workspace bytes of a key_weights plan."""
+    n = load_library().pkd_key_weights_workspace_size(*plan)
+    if n == 0:
+        raise PkdError(EUNSUPPORTED, load_library().pkd_last_error().decode())
+    return n
+
+
+def _key_rows(t, B, H, dtype, name):
+    """(address, batch stride, head stride, keys) of t [B, H, keys], rows of keys contiguous; zeros for None."""
+    if t is None:
+        return None, 0, 0, 0
+    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != H or t.dtype is not dtype or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{name} must be {dtype} [{B}, {H}, keys] with contiguous rows of keys")
+    return t.data_ptr(), t.stride(0), t.stride(1), t.shape[2]
+
+
+def key_weights(q, kv_cache, block_table, seq_lens, query_start, lse, scale, *, weights=None, decay=1.0, causal=True,
+                window=0, softcap=0.0, last_queries=0, max_query_len=None, max_kv_len=None, q_scale=1.0, k_scale=1.0,
+                out=None, workspace=None, stream=None):
+    """Attention weight that each cached key received from the call's queries.
+
+    q, kv_cache, block_table, seq_lens, query_start, causal, window, softcap and the
+    host's bounds as for paged_attention, whose lse (fp32 [T, Hq]; of paged_decode
+    lse.view(-1, Hq)) over the same keys turns scores into probabilities: their sum
+    over the tokens (last_queries: the last ones of each request) and the query
+    heads of each kv head is added to decay * weights (fp32 [B, Hkv, keys]; keys of
+    the call's own tokens start at 0).  Returns out, fp32 [B, Hkv, keys]: entries
+    behind seq_lens[b] keep what was in it (0 where the call allocates it).  out may
+    be weights.  workspace_check reads the status, as for paged_attention.
+    """
+    index = q.get_device()
+    if index < 0 or kv_cache.get_device() != index or block_table.get_device() != index or \
+            seq_lens.get_device() != index or query_start.get_device() != index or lse.get_device() != index or \
+            not (weights is out is workspace is None):
+        _device_error(q=q, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, query_start=query_start,
+                      lse=lse, weights=weights, out=out, workspace=workspace)
+    if stream is not None or _current_device() != index:
+        ctx = _elsewhere(index, stream)
+        if ctx is not None:
+            with ctx:
+                return key_weights(q, kv_cache, block_table, seq_lens, query_start, lse, scale, weights=weights,
+                                   decay=decay, causal=causal, window=window, softcap=softcap,
+                                   last_queries=last_queries, max_query_len=max_query_len, max_kv_len=max_kv_len,
+                                   q_scale=q_scale, k_scale=k_scale, out=out, workspace=workspace)
+    T, Hq, D = q.shape
+    qs = _token_stride(q, T, Hq, D, "q")
+    num_pages, Hkv, P = _check_cache(D, kv_cache)
+    B, columns, stride = _check_table(block_table, seq_lens)
+    if query_start.dtype is not _I32 or query_start.dim() != 1 or query_start.numel() != B + 1 or \
+            not query_start.is_contiguous():
+        raise ValueError("query_start must be a contiguous int32 tensor [batch + 1]")
+    if lse.dtype is not _F32 or lse.shape != (T, Hq) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [tokens, num_heads]")
+    if max_query_len is None:
+        max_query_len = max(T, 1)
+    if max_kv_len is None:
+        max_kv_len = columns * P
+    if window >> 31 or max_query_len >> 31 or max_kv_len >> 31 or last_queries >> 31:
+        raise ValueError("window, last_queries, max_query_len and max_kv_len must lie in [0, 2^31)")
+    if out is None:
+        out = torch.zeros((B, Hkv, max_kv_len if weights is None else weights.shape[2]), dtype=_F32, device=q.device)
+    prior, pb, ph, prior_keys = _key_rows(weights, B, Hkv, _F32, "weights")
+    dst, ob, oh, out_keys = _key_rows(out, B, Hkv, _F32, "out")
+    if out_keys < max_kv_len or (weights is not None and prior_keys < max_kv_len):
+        raise ValueError(f"weights and out must have room for max_kv_len = {max_kv_len} keys")
+    q_dt, kv_dt = _code(q.dtype), _code(kv_cache.dtype)
+    s = _raw_stream(index)
+    need = _weigh_bytes(B, T, max_query_len, last_queries, Hq, Hkv, D, P, max_kv_len, kv_dt)
+    if workspace is None:
+        ws, ws_bytes, keep = _call_workspace(need, index, s)
+    else:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    status = (_lib or load_library()).pkd_key_weights(
+        q.data_ptr(), q_dt, qs, kv_cache.data_ptr(), kv_dt, num_pages, block_table.data_ptr(), stride,
+        seq_lens.data_ptr(), query_start.data_ptr(), B, T, max_query_len, last_queries, Hq, Hkv, D, P, max_kv_len, scale,
+        q_scale, k_scale, softcap, window, lse.data_ptr(), prior, pb, ph, decay, dst, ob, oh, ws, ws_bytes,
+        FLAG_CAUSAL if causal else 0, s)
+    if status:
+        _check(status)
+    return out
+
+
+def evict_select(weights, seq_lens, budget, *, sinks=0, recent=0, pool=1, positions=None, context_lens=None, kept=None,
+                 kept_lens=None, stream=None):
+    """The keys of each request and kv head that stay in a cache of at most budget keys.
+
+    weights fp32 [B, Hkv, keys] (key_weights), seq_lens int32 [B].  Kept are the
+    first sinks and the last recent keys, then those of the largest weight (of
+    equal ones the lowest index; NaN counts as -inf); pool (odd): the largest
+    weight of the pool keys around a key that are neither.  After a compaction
+    has put keys out of order, positions (int32 [B, Hkv, keys]) says where each
+    stood and context_lens (int32 [B]) how many tokens the request has seen.
+    Returns (kept int32 [B, Hkv, budget]: rising indexes, -1 behind them,
+    kept_lens int32 [B]: min(seq_lens, budget)).
+    """
+    index = weights.get_device()
+    if index < 0 or seq_lens.get_device() != index or not (positions is context_lens is kept is kept_lens is None):
+        _device_error(weights=weights, seq_lens=seq_lens, positions=positions, context_lens=context_lens, kept=kept,
+                      kept_lens=kept_lens)
+    if stream is not None or _current_device() != index:
+        ctx = _elsewhere(index, stream)
+        if ctx is not None:
+            with ctx:
+                return evict_select(weights, seq_lens, budget, sinks=sinks, recent=recent, pool=pool,
+                                    positions=positions, context_lens=context_lens, kept=kept, kept_lens=kept_lens)
+    B, H, keys = weights.shape
+    w, wb, wh, _ = _key_rows(weights, B, H, _F32, "weights")
+    x, xb, xh, position_keys = _key_rows(positions, B, H, _I32, "positions")
+    if positions is not None and position_keys < keys:
+        raise ValueError("positions must have as many keys as weights")
+    for name, t in (("seq_lens", seq_lens), ("context_lens", context_lens), ("kept_lens", kept_lens)):
+        if t is not None and (t.dtype is not _I32 or t.shape != (B,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous int32 [{B}]")
+    if (positions is None) != (context_lens is None):
+        raise ValueError("positions and context_lens come together")
+    if not 1 <= budget < 1 << 31 or not 0 <= sinks < 1 << 31 or not 0 <= recent < 1 << 31 or not 1 <= pool < 256:
+        raise ValueError("budget must lie in [1, 2^31), sinks and recent in [0, 2^31), pool in [1, 255]")
+    if kept is None:
+        kept = torch.empty((B, H, budget), dtype=_I32, device=weights.device)
+    elif kept.shape != (B, H, budget) or kept.dtype is not _I32 or not kept.is_contiguous():
+        raise ValueError(f"kept must be contiguous int32 [{B}, {H}, {budget}]")
+    if kept_lens is None:
+        kept_lens = torch.empty((B,), dtype=_I32, device=weights.device)
+    status = (_lib or load_library()).pkd_evict_select(
+        w, wb, wh, keys, seq_lens.data_ptr(), B, H, budget, sinks, recent, pool, x, xb, xh,
+        context_lens.data_ptr() if context_lens is not None else None, kept.data_ptr(), kept_lens.data_ptr(),
+        _raw_stream(index))
+    if status:
+        _check(status)
+    return kept, kept_lens
+
+
+def cache_compact(kv_cache, block_table, kept, kept_lens, *, weights=None, positions=None, stream=None):
+    """Move the rows that stay below the new length, in place.
+
+    kept, kept_lens as evict_select returns them: of the kept_lens[b] rows of a
+    request and kv head those behind the new length move into the free slots below
+    it, with their entries of weights (fp32) and positions (int32, both
+    [B, Hkv, keys]); the others stay.  seq_lens is then kept_lens.  The keys' order
+    changes: attend to them without a window.  The pages below the new length
+    must be one request's own.  Returns kv_cache.
+    """
+    index = kv_cache.get_device()
+    if index < 0 or block_table.get_device() != index or kept.get_device() != index or \
+            kept_lens.get_device() != index or not (weights is positions is None):
+        _device_error(kv_cache=kv_cache, block_table=block_table, kept=kept, kept_lens=kept_lens, weights=weights,
+                      positions=positions)
+    if stream is not None or _current_device() != index:
+        ctx = _elsewhere(index, stream)
+        if ctx is not None:
+            with ctx:
+                return cache_compact(kv_cache, block_table, kept, kept_lens, weights=weights, positions=positions)
+    D = kv_cache.shape[-1] // 2
+    num_pages, H, P = _check_cache(D, kv_cache)
+    B, columns, stride = _check_table(block_table, kept_lens)
+    if kept.dim() != 3 or kept.shape[0] != B or kept.shape[1] != H or kept.dtype is not _I32 or not kept.is_contiguous():
+        raise ValueError(f"kept must be contiguous int32 [{B}, {H}, budget]")
+    w, wb, wh, weight_keys = _key_rows(weights, B, H, _F32, "weights")
+    x, xb, xh, position_keys = _key_rows(positions, B, H, _I32, "positions")
+    status = (_lib or load_library()).pkd_cache_compact(
+        kv_cache.data_ptr(), _code(kv_cache.dtype), num_pages, block_table.data_ptr(), stride, columns, kept.data_ptr(),
+        kept_lens.data_ptr(), B, H, D, P, kept.shape[2], w, wb, wh, weight_keys, x, xb, xh, position_keys,
+        _raw_stream(index))
+    if status:
+        _check(status)
+    return kv_cache

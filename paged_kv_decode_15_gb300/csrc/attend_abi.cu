@@ -7,6 +7,7 @@
 #include "attend.cuh"
 #include "attend_launch.h"
 #include "attend_prompt.cuh"
+#include "key_weights.cuh"
 #include "page_math.h"
 
 namespace {
@@ -162,6 +163,28 @@ pkd_status plan_paged_attention(int B, long long T, int max_q, int Hq, int Hkv, 
     if (o.window > 0 && !o.prefix_lens) vis = std::min(vis, (long long)o.window + max_q - 1 + 15);
     const bool step = (long long)max_q * (Hq / Hkv) <= 16;
     return plan_attend(B, T, max_q, Hq, Hkv, D, P, vis, kv, false, step, pl);
+}
+
+struct WeighPlan {
+    long long rows;     // query rows of a request and kv head that weigh, at most
+    int chunk, chunks;  // keys of a CTA
+};
+
+pkd_status plan_key_weights(int B, long long T, int max_q, int last, int Hq, int Hkv, int D, int P, int max_kv_len,
+                            pkd_dtype kv, WeighPlan& pl) {
+    pl = WeighPlan{};
+    pkd_status st = check_shape(B, T, Hq, Hkv, D, P, max_kv_len, kv);
+    if (st != PKD_OK) return st;
+    if (max_q < 0 || (max_q == 0 && T > 0)) return report(PKD_EINVAL, "max_query_len must be >= 1 (got %d)", max_q);
+    if (last < 0) return report(PKD_EINVAL, "last_queries must be >= 0 (got %d)", last);
+    const long long tokens = std::min<long long>(last > 0 ? std::min(last, max_q) : max_q, T);
+    pl.rows = tokens * (Hq / Hkv);
+    // about 16 CTAs per SM, chunks of 128 to 2048 keys
+    const long long units = std::max(1ll, (long long)B * Hkv);
+    const long long chunk = std::min(2048ll, std::max(128ll, max_kv_len * units / (16 * kSms)));
+    pl.chunk = up((int)chunk, 128);
+    pl.chunks = (max_kv_len + pl.chunk - 1) / pl.chunk;
+    return PKD_OK;
 }
 
 struct PrefixPlan {
@@ -337,6 +360,13 @@ pkd_status check_overlap(const void* q, pkd_dtype q_dtype, int64_t q_stride, con
 }
 
 const pkd_score_options kNoOptions = {0.f, nullptr, 0, nullptr, nullptr};
+
+// Rows [B, H] of `keys` contiguous values must not share any (written ones; read ones may).
+bool rows_apart(int64_t sb, int64_t sh, int B, int H, int64_t keys) {
+    if (sb < 0 || sh < 0) return false;
+    return (H == 1 || sh >= keys) && (B == 1 || sb >= (H - 1) * sh + keys) ? true
+         : (B == 1 || sb >= keys) && (H == 1 || sh >= (B - 1) * sb + keys);
+}
 
 }  // namespace
 
@@ -527,6 +557,88 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
     m.v_scale = v_scale;
     const cudaError_t e = pkd::launch_prefix_merge(head_dim, m, s);
     return e == cudaSuccess ? PKD_OK : cuda_fail(e, "pkd_prefix_decode join launch");
+}
+
+size_t pkd_key_weights_workspace_size(int batch, int64_t total_tokens, int max_query_len, int last_queries, int num_heads,
+                                      int num_kv_heads, int head_dim, int page_size, int max_kv_len, pkd_dtype kv_dtype) {
+    WeighPlan pl;
+    return plan_key_weights(batch, total_tokens, max_query_len, last_queries, num_heads, num_kv_heads, head_dim, page_size,
+                            max_kv_len, kv_dtype, pl) == PKD_OK ? kPartials : 0;
+}
+
+pkd_status pkd_key_weights(const void* q, pkd_dtype q_dtype, int64_t q_stride, const void* kv_cache, pkd_dtype kv_dtype,
+                           int64_t num_pages, const int32_t* block_table, int64_t block_table_stride,
+                           const int32_t* seq_lens, const int32_t* query_start, int batch, int64_t total_tokens,
+                           int max_query_len, int last_queries, int num_heads, int num_kv_heads, int head_dim,
+                           int page_size, int max_kv_len, float scale, float q_scale, float k_scale, float softcap,
+                           int window, const float* lse, const float* prior, int64_t prior_batch_stride,
+                           int64_t prior_head_stride, float decay, float* weights, int64_t weights_batch_stride,
+                           int64_t weights_head_stride, void* workspace, size_t workspace_bytes, unsigned flags,
+                           void* stream) {
+    WeighPlan pl;
+    pkd_score_options o = kNoOptions;
+    o.softcap = softcap;
+    pkd_status st = check_options(o);
+    if (st != PKD_OK) return st;
+    st = plan_key_weights(batch, total_tokens, max_query_len, last_queries, num_heads, num_kv_heads, head_dim, page_size,
+                          max_kv_len, kv_dtype, pl);
+    if (st != PKD_OK) return st;
+    if (flags & ~PKD_FLAG_CAUSAL) return report(PKD_EUNSUPPORTED, "pkd_key_weights takes PKD_FLAG_CAUSAL only");
+    if (batch == 0 || max_kv_len == 0) return PKD_OK;
+    if (total_tokens == 0) q = lse = static_cast<const float*>(workspace);  // no row of them is read
+    st = check_call(q, q_dtype, total_tokens ? q_stride : (int64_t)num_heads * head_dim, kv_cache, kv_dtype, num_pages,
+                    num_heads, num_kv_heads, head_dim, page_size, scale, q_scale, k_scale, 1.f, softcap, q, PKD_FP32, lse,
+                    workspace, workspace_bytes, kPartials);
+    if (st != PKD_OK) return st;
+    st = check_table(block_table, block_table_stride, seq_lens, max_kv_len, page_size, "block_table");
+    if (st != PKD_OK) return st;
+    if (!query_start || !aligned(query_start, 4)) return report(PKD_EINVAL, "query_start is null or misaligned");
+    if (!lse || !weights) return report(PKD_EINVAL, "null pointer argument");
+    if (!aligned(lse, 4) || !aligned(prior, 4) || !aligned(weights, 4))
+        return report(PKD_EINVAL, "lse, prior and weights must be 4-byte aligned");
+    if (!std::isfinite(decay)) return report(PKD_EINVAL, "decay must be finite");
+    if (!rows_apart(weights_batch_stride, weights_head_stride, batch, num_kv_heads, max_kv_len))
+        return report(PKD_EINVAL, "weights strides %lld, %lld: rows of max_kv_len keys overlap",
+                      (long long)weights_batch_stride, (long long)weights_head_stride);
+    if (prior) {
+        if (prior_batch_stride < 0 || prior_head_stride < 0) return report(PKD_EINVAL, "prior strides must not be negative");
+        const bool same = prior == weights && (batch == 1 || prior_batch_stride == weights_batch_stride) &&
+                          (num_kv_heads == 1 || prior_head_stride == weights_head_stride);
+        auto past = [&](const float* x, int64_t sb, int64_t sh) { return x + (batch - 1) * sb + (num_kv_heads - 1) * sh + max_kv_len; };
+        if (!same && prior < past(weights, weights_batch_stride, weights_head_stride) &&
+            weights < past(prior, prior_batch_stride, prior_head_stride))
+            return report(PKD_EINVAL, "weights overlaps prior without being it");
+    }
+    pkd::WeighParams w;
+    std::memset(&w, 0, sizeof w);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    AttendPlan none{};
+    none.G = num_heads / num_kv_heads;
+    none.chunk = pl.chunk;
+    fill(w.a, none, ws, 0, kPartials, batch, total_tokens, num_heads, num_kv_heads, page_size, max_kv_len, num_pages,
+         scale * q_scale * k_scale * pkd::kLog2e, softcap, flags);
+    w.a.q = q;
+    w.a.q_stride = q_stride;
+    w.a.block_table = block_table;
+    w.a.bt_stride = block_table_stride;
+    w.a.seq_lens = seq_lens;
+    w.a.query_start = query_start;
+    w.a.max_q = max_query_len;
+    w.a.window = window > 0 ? std::min(window, 2 * kMaxKeys) : 0;
+    w.a.causal = (flags & PKD_FLAG_CAUSAL) ? 1 : 0;
+    w.cache = static_cast<const uint8_t*>(kv_cache);
+    w.lse = lse;
+    w.prior = prior;
+    w.weights = weights;
+    w.prior_b = prior_batch_stride;
+    w.prior_h = prior_head_stride;
+    w.weights_b = weights_batch_stride;
+    w.weights_h = weights_head_stride;
+    w.decay = decay;
+    w.last = last_queries;
+    const cudaError_t e = pkd::launch_key_weights(head_dim, (int)kv_dtype, pl.rows, w, dim3(pl.chunks, num_kv_heads, batch),
+                                                  (cudaStream_t)stream);
+    return e == cudaSuccess ? PKD_OK : cuda_fail(e, "pkd_key_weights launch");
 }
 
 }  // extern "C"
