@@ -385,6 +385,38 @@ pkd_status pkd_paged_attention(const void* q, pkd_dtype q_dtype, int64_t q_strid
                                unsigned flags, void* stream);
 
 /*
+ * Attention over whole prompts, packed one behind the other, from their own
+ * projections: nothing is read from a paged cache.
+ *
+ *   q            device [total_tokens, num_heads, head_dim], dtype (bf16 or fp16)
+ *   k, v         device [total_keys, num_kv_heads, head_dim], dtype; q_stride, k_stride
+ *                and v_stride elements between tokens (multiples of 8), so that all three
+ *                may be parts of one fused projection; 16-byte aligned
+ *   query_start, key_start  device int32 [batch + 1]: prompt b's tokens are rows
+ *                [query_start[b], query_start[b + 1]) of q, at most max_query_len, its
+ *                keys rows [key_start[b], key_start[b + 1]) of k and v, at most
+ *                max_kv_len.  key_start NULL: query_start (total_keys == total_tokens)
+ *   softcap, window  as in pkd_score_options (0: none)
+ *   out, lse     as for pkd_paged_attention; no part of out may lie in q, k or v
+ *   workspace, flags  as for pkd_paged_attention (status: starts that fall, leave the
+ *                tensors or exceed the bounds are clamped)
+ *
+ * Token i of n has position L - n + i among its prompt's L keys: with PKD_FLAG_CAUSAL it
+ * sees keys up to that (fewer tokens than keys are the prompt's last ones).  Rows of no
+ * prompt, tokens that see no key, and which values must be finite: as for
+ * pkd_paged_attention; other prompts' keys and values do not enter a prompt's results.
+ * Limits as there; total_keys <= 2^29.
+ */
+size_t pkd_packed_attention_workspace_size(int batch, int64_t total_tokens, int max_query_len, int num_heads,
+                                           int num_kv_heads, int head_dim, int max_kv_len, pkd_dtype dtype, int window);
+pkd_status pkd_packed_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, pkd_dtype dtype, const int32_t* query_start,
+                                const int32_t* key_start, int batch, int64_t total_tokens, int64_t total_keys,
+                                int max_query_len, int max_kv_len, int num_heads, int num_kv_heads, int head_dim,
+                                float scale, float softcap, int window, void* out, pkd_dtype out_dtype, float* lse,
+                                void* workspace, size_t workspace_bytes, unsigned flags, void* stream);
+
+/*
  * Decode of a batch whose requests share long prefixes, each prefix computed
  * once for all its requests.
  *

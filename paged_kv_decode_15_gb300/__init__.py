@@ -12,6 +12,7 @@ Entry points (same names as the C ABI in include/pkd.h, without the prefix):
   rope_cache_write(q, key, value, positions, cos_sin, slot_mapping, kv_cache, ...)
   paged_attention(q, kv_cache, block_table, seq_lens, query_start, scale, ...)
   prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, scale, ...)
+  packed_attention(q, k, v, query_start, scale, ...)
   key_weights(q, kv_cache, block_table, seq_lens, query_start, lse, scale, ...)
   evict_select(weights, seq_lens, budget, ...)
   cache_compact(kv_cache, block_table, kept, kept_lens, ...)
@@ -41,7 +42,7 @@ SYMBOLS = ("pkd_version", "pkd_last_error", "pkd_paged_decode_workspace_size", "
            "pkd_segmented_attention", "pkd_segmented_attention_paged", "pkd_lse_merge",
            "pkd_rope_cache_write", "pkd_paged_attention_workspace_size", "pkd_paged_attention_kernel_name",
            "pkd_paged_attention", "pkd_prefix_decode_workspace_size", "pkd_prefix_decode",
-           "pkd_key_weights_workspace_size", "pkd_key_weights", "pkd_evict_select", "pkd_cache_compact")
+           "pkd_packed_attention_workspace_size", "pkd_packed_attention", "pkd_key_weights_workspace_size", "pkd_key_weights", "pkd_evict_select", "pkd_cache_compact")
 
 
 class ScoreOptions(ctypes.Structure):
@@ -107,13 +108,17 @@ def load_library(path: str = LIB_PATH):
     lib.pkd_prefix_decode_workspace_size.restype = SZ
     lib.pkd_prefix_decode.argtypes = [P, I, P, I, I64, P, I64, P, P, I, I, P, I64, P, I, I, I, I, I, I, I, F, F, F, F,
                                       F, P, I, P, P, SZ, U, P]
+    lib.pkd_packed_attention_workspace_size.argtypes = [I, I64, I, I, I, I, I, I, I]
+    lib.pkd_packed_attention_workspace_size.restype = SZ
+    lib.pkd_packed_attention.argtypes = [P, I64, P, I64, P, I64, I, P, P, I, I64, I64, I, I, I, I, I, F, F, I, P, I, P, P, SZ,
+                                         U, P]
     lib.pkd_key_weights_workspace_size.argtypes = [I, I64, I, I, I, I, I, I, I, I]
     lib.pkd_key_weights_workspace_size.restype = SZ
     lib.pkd_key_weights.argtypes = [P, I, I64, P, I, I64, P, I64, P, P, I, I64, I, I, I, I, I, I, I, F, F, F, F, I, P, P,
                                     I64, I64, F, P, I64, I64, P, SZ, U, P]
     lib.pkd_evict_select.argtypes = [P, I64, I64, I64, P, I, I, I, I, I, I, P, I64, I64, P, P, P, P]
     lib.pkd_cache_compact.argtypes = [P, I, I64, P, I64, I, P, P, I, I, I, I, I, P, I64, I64, I64, P, I64, I64, I64, P]
-    for name in ("pkd_key_weights", "pkd_evict_select", "pkd_cache_compact", "pkd_rope_cache_write", "pkd_paged_attention", "pkd_prefix_decode", "pkd_workspace_init", "pkd_workspace_check", "pkd_paged_decode", "pkd_paged_decode_static",
+    for name in ("pkd_packed_attention", "pkd_key_weights", "pkd_evict_select", "pkd_cache_compact", "pkd_rope_cache_write", "pkd_paged_attention", "pkd_prefix_decode", "pkd_workspace_init", "pkd_workspace_check", "pkd_paged_decode", "pkd_paged_decode_static",
                  "pkd_paged_decode_static_check", "pkd_cache_write", "pkd_segmented_attention", "pkd_segmented_attention_paged", "pkd_lse_merge"):
         getattr(lib, name).restype = I
     _lib = lib
@@ -733,6 +738,73 @@ def prefix_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens,
         prefix_lens.data_ptr(), group_start.data_ptr() if group_start is not None else None, groups, max_prefix_len,
         block_table.data_ptr(), stride, seq_lens.data_ptr(), B, sq, Hq, Hkv, D, P, max_kv_len, scale, q_scale, k_scale,
         v_scale, softcap, out.data_ptr(), _code(out.dtype), lse.data_ptr(), ws, ws_bytes,
+        (FLAG_CAUSAL if causal else 0) | (FLAG_TEST_TIMEOUT if test_timeout else 0), s)
+    if status:
+        _check(status)
+    return out, lse
+
+
+@functools.lru_cache(maxsize=4096)
+def _packed_bytes(*plan):
+    """Workspace bytes of a packed_attention plan."""
+    n = load_library().pkd_packed_attention_workspace_size(*plan)
+    if n == 0:
+        raise PkdError(EUNSUPPORTED, load_library().pkd_last_error().decode())
+    return n
+
+
+def packed_attention(q, k, v, query_start, scale, *, key_start=None, causal=True, window=0, softcap=0.0,
+                     max_query_len=None, max_kv_len=None, out=None, lse=None, out_dtype=None, workspace=None,
+                     test_timeout=False, stream=None):
+    """Attention over whole prompts, packed one behind the other.
+
+    q [T, Hq, D], k, v [Tk, Hkv, D] (bf16 or fp16; any token strides, so that all may
+    be parts of one projection); prompt b's tokens are rows query_start[b] :
+    query_start[b + 1] of q, its keys the same rows of k and v, or those of
+    key_start (int32 [B + 1] both); its tokens are its last keys' (causal).
+    softcap, window, out, lse, workspace and test_timeout as for paged_attention.
+    max_query_len (default T) and max_kv_len (default max_query_len, with key_start
+    Tk) bound the prompts on the host and with them choose the split of the keys.
+    Returns (out [T, Hq, D], lse fp32 [T, Hq]); rows of no prompt keep what was there.
+    """
+    index = q.get_device()
+    if index < 0 or k.get_device() != index or v.get_device() != index or query_start.get_device() != index or \
+            not (key_start is out is lse is workspace is None):
+        _device_error(q=q, k=k, v=v, query_start=query_start, key_start=key_start, out=out, lse=lse, workspace=workspace)
+    if stream is not None or _current_device() != index:
+        ctx = _elsewhere(index, stream)
+        if ctx is not None:
+            with ctx:
+                return packed_attention(q, k, v, query_start, scale, key_start=key_start, causal=causal, window=window,
+                                        softcap=softcap, max_query_len=max_query_len, max_kv_len=max_kv_len, out=out,
+                                        lse=lse, out_dtype=out_dtype, workspace=workspace, test_timeout=test_timeout)
+    T, Hq, D = shape = q.shape
+    Tk, Hkv, kD = k.shape
+    dtype = q.dtype
+    if v.shape != k.shape or kD != D or k.dtype is not dtype or v.dtype is not dtype:
+        raise ValueError("k and v must be [keys, num_kv_heads, head_dim] of q's dtype and head_dim")
+    qs, ks, vs = _token_stride(q, T, Hq, D, "q"), _token_stride(k, Tk, Hkv, D, "k"), _token_stride(v, Tk, Hkv, D, "v")
+    B = query_start.numel() - 1
+    for name, t in (("query_start", query_start), ("key_start", key_start)):
+        if t is not None and (t.dtype is not _I32 or t.dim() != 1 or t.numel() != B + 1 or B < 0 or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 tensor [batch + 1]")
+    if max_query_len is None:
+        max_query_len = max(T, 1)
+    if max_kv_len is None:
+        max_kv_len = max_query_len if key_start is None else Tk
+    if window >> 31 or max_query_len >> 31 or max_kv_len >> 31:
+        raise ValueError("window, max_query_len and max_kv_len must lie in [0, 2^31)")
+    dt = _code(dtype)
+    out, lse = _results(out, lse, shape, out_dtype or dtype, q.device)
+    s = _raw_stream(index)
+    if workspace is None:
+        ws, ws_bytes, keep = _call_workspace(_packed_bytes(B, T, max_query_len, Hq, Hkv, D, max_kv_len, dt, window), index, s)
+    else:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    status = (_lib or load_library()).pkd_packed_attention(
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, dt, query_start.data_ptr(),
+        key_start.data_ptr() if key_start is not None else None, B, T, Tk, max_query_len, max_kv_len, Hq, Hkv, D, scale,
+        softcap, window, out.data_ptr(), _code(out.dtype), lse.data_ptr(), ws, ws_bytes,
         (FLAG_CAUSAL if causal else 0) | (FLAG_TEST_TIMEOUT if test_timeout else 0), s)
     if status:
         _check(status)

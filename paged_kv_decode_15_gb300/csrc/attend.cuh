@@ -19,6 +19,7 @@ struct AttendParams {
     const int32_t* query_start;   // [B + 1] (times q_mul), or null: sq tokens per request
     const int32_t* prefix_lens;   // [B] or null
     const int32_t* doc_start;     // [T] or null
+    const int32_t* key_start;     // packed keys (pkd_packed_attention): [B + 1], rows of k and v
     const float* slopes;          // [Hq] or null
     void* out;                    // [T, Hq, D]
     float* lse;                   // [T, Hq] or null
@@ -31,6 +32,7 @@ struct AttendParams {
     long long bt_stride, num_pages, q_stride;
     int B, T, Hq, Hkv, G, P;
     int sq, q_mul, max_q, max_kv_len;
+    int total_keys;               // packed keys: rows of k and v
     int max_pairs;                // row-tile pairs of a kv head that the plan has room for (tcgen05 kernel)
     int window, causal;
     int chunk, max_splits, out_dtype;

@@ -165,6 +165,18 @@ pkd_status plan_paged_attention(int B, long long T, int max_q, int Hq, int Hkv, 
     return plan_attend(B, T, max_q, Hq, Hkv, D, P, vis, kv, false, step, pl);
 }
 
+pkd_status plan_packed(int B, long long T, int max_q, int Hq, int Hkv, int D, int max_kv_len, pkd_dtype dt, int window,
+                       AttendPlan& pl) {
+    if (dt != PKD_BF16 && dt != PKD_FP16) return report(PKD_EUNSUPPORTED, "dtype %d not supported (bf16, fp16)", (int)dt);
+    pkd_status st = check_shape(B, T, Hq, Hkv, D, 16, max_kv_len, dt);
+    if (st != PKD_OK) return st;
+    if (max_q < 0 || (max_q == 0 && T > 0)) return report(PKD_EINVAL, "max_query_len must be >= 1 (got %d)", max_q);
+    max_q = (int)std::max(1ll, std::min<long long>(max_q, T));
+    long long vis = max_kv_len;
+    if (window > 0) vis = std::min(vis, (long long)window + max_q - 1 + 15);
+    return plan_attend(B, T, max_q, Hq, Hkv, D, 16, vis, dt, false, false, pl);
+}
+
 struct WeighPlan {
     long long rows;     // query rows of a request and kv head that weigh, at most
     int chunk, chunks;  // keys of a CTA
@@ -352,11 +364,11 @@ pkd_status check_table(const int32_t* table, int64_t stride, const int32_t* lens
 
 // Results may be written while other CTAs still read q.
 pkd_status check_overlap(const void* q, pkd_dtype q_dtype, int64_t q_stride, const void* out, pkd_dtype out_dtype,
-                         int64_t T, int Hq, int D) {
+                         int64_t T, int Hq, int D, int64_t q_rows = 0, int q_heads = 0, const char* what = "out overlaps q") {
     const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
-    const uintptr_t q1 = q0 + ((T - 1) * q_stride + (int64_t)Hq * D) * elt_bytes(q_dtype);
+    const uintptr_t q1 = q0 + (((q_rows ? q_rows : T) - 1) * q_stride + (int64_t)(q_heads ? q_heads : Hq) * D) * elt_bytes(q_dtype);
     const uintptr_t o1 = o0 + T * Hq * D * elt_bytes(out_dtype);
-    return q0 < o1 && o0 < q1 ? report(PKD_EINVAL, "out overlaps q") : PKD_OK;
+    return q0 < o1 && o0 < q1 ? report(PKD_EINVAL, "%s", what) : PKD_OK;
 }
 
 const pkd_score_options kNoOptions = {0.f, nullptr, 0, nullptr, nullptr};
@@ -557,6 +569,81 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
     m.v_scale = v_scale;
     const cudaError_t e = pkd::launch_prefix_merge(head_dim, m, s);
     return e == cudaSuccess ? PKD_OK : cuda_fail(e, "pkd_prefix_decode join launch");
+}
+
+size_t pkd_packed_attention_workspace_size(int batch, int64_t total_tokens, int max_query_len, int num_heads,
+                                           int num_kv_heads, int head_dim, int max_kv_len, pkd_dtype dtype, int window) {
+    AttendPlan pl;
+    return plan_packed(batch, total_tokens, max_query_len, num_heads, num_kv_heads, head_dim, max_kv_len, dtype, window,
+                       pl) == PKD_OK ? kPartials + pl.bytes() : 0;
+}
+
+pkd_status pkd_packed_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, pkd_dtype dtype, const int32_t* query_start, const int32_t* key_start,
+                                int batch, int64_t total_tokens, int64_t total_keys, int max_query_len, int max_kv_len,
+                                int num_heads, int num_kv_heads, int head_dim, float scale, float softcap, int window,
+                                void* out, pkd_dtype out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                                unsigned flags, void* stream) {
+    AttendPlan pl;
+    pkd_score_options o = kNoOptions;
+    o.softcap = softcap;
+    pkd_status st = check_options(o);
+    if (st != PKD_OK) return st;
+    st = plan_packed(batch, total_tokens, max_query_len, num_heads, num_kv_heads, head_dim, max_kv_len, dtype, window, pl);
+    if (st != PKD_OK) return st;
+    if (flags & ~(PKD_FLAG_CAUSAL | PKD_FLAG_TEST_TIMEOUT))
+        return report(PKD_EUNSUPPORTED, "pkd_packed_attention takes PKD_FLAG_CAUSAL (and PKD_FLAG_TEST_TIMEOUT) only");
+    if (total_keys < 0 || total_keys > kMaxKeys)
+        return report(PKD_EINVAL, "total_keys must lie in [0, 2^29] (got %lld)", (long long)total_keys);
+    if (!key_start && total_keys != total_tokens)
+        return report(PKD_EINVAL, "key_start is needed where keys (%lld) are not as many as tokens (%lld)",
+                      (long long)total_keys, (long long)total_tokens);
+    if (batch == 0 || total_tokens == 0) return PKD_OK;
+    // of no keys none is read: the maps lie over q then
+    if (total_keys == 0) k = v = q, k_stride = v_stride = (int64_t)num_kv_heads * head_dim;
+    st = check_call(q, dtype, q_stride, k, dtype, 1, num_heads, num_kv_heads, head_dim, 16, scale, 1.f, 1.f, 1.f, softcap, out,
+                    out_dtype, lse, workspace, workspace_bytes, kPartials + pl.bytes());
+    if (st != PKD_OK) return st;
+    if (!v || !aligned(v, 16)) return report(PKD_EINVAL, "v is null or misaligned (16 B)");
+    for (int64_t s : {k_stride, v_stride})
+        if (s < (int64_t)num_kv_heads * head_dim || s % 8 || s > (int64_t)1 << 38)
+            return report(PKD_EINVAL, "k_stride and v_stride must be >= num_kv_heads*head_dim, multiples of 16 bytes and <= 2^38");
+    if (!query_start || !aligned(query_start, 4) || !aligned(key_start, 4))
+        return report(PKD_EINVAL, "query_start is null, or it or key_start misaligned");
+    st = check_overlap(q, dtype, q_stride, out, out_dtype, total_tokens, num_heads, head_dim);
+    if (st == PKD_OK && total_keys) st = check_overlap(k, dtype, k_stride, out, out_dtype, total_tokens, num_heads, head_dim,
+                                                       total_keys, num_kv_heads, "out overlaps k");
+    if (st == PKD_OK && total_keys) st = check_overlap(v, dtype, v_stride, out, out_dtype, total_tokens, num_heads, head_dim,
+                                                       total_keys, num_kv_heads, "out overlaps v");
+    if (st != PKD_OK) return st;
+    pkd::AttendParams a;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    fill(a, pl, ws, 0, kPartials, batch, total_tokens, num_heads, num_kv_heads, 16, max_kv_len, 1, scale * pkd::kLog2e, softcap,
+         flags);
+    a.q = q;
+    a.q_stride = q_stride;
+    a.query_start = query_start;
+    a.key_start = key_start ? key_start : query_start;
+    a.total_keys = (int)total_keys;
+    a.window = window > 0 ? std::min(window, 2 * kMaxKeys) : 0;
+    a.causal = (flags & PKD_FLAG_CAUSAL) ? 1 : 0;
+    a.max_q = max_query_len;
+    a.out = out;
+    a.lse = lse;
+    a.out_dtype = (int)out_dtype;
+    a.v_scale = 1.f;
+    CUtensorMap kmap, vmap, qmap;
+    const uint64_t rows = std::max<int64_t>(total_keys, 1);
+    st = pkd::query_map(qmap, q, head_dim, num_heads, (uint64_t)total_tokens, q_stride, a.G, pkd::kPtRows / a.G, dtype);
+    if (st == PKD_OK) st = pkd::query_map(kmap, k, head_dim, num_kv_heads, rows, k_stride, 1, pkd::kPtKeys, dtype);
+    if (st == PKD_OK) st = pkd::query_map(vmap, v, head_dim, num_kv_heads, rows, v_stride, 1, pkd::kPtKeys, dtype);
+    if (st != PKD_OK) return st;
+    int grid = 1;
+    cudaError_t e = pkd::persistent_grid(1, (int)std::min<long long>(pl.units * pl.max_splits, kSms), grid);
+    if (e == cudaSuccess)
+        e = dtype == PKD_BF16 ? pkd::launch_packed_bf16(head_dim, kmap, vmap, qmap, a, grid, (cudaStream_t)stream)
+                              : pkd::launch_packed_fp16(head_dim, kmap, vmap, qmap, a, grid, (cudaStream_t)stream);
+    return e == cudaSuccess ? PKD_OK : cuda_fail(e, "pkd_packed_attention launch");
 }
 
 size_t pkd_key_weights_workspace_size(int batch, int64_t total_tokens, int max_query_len, int last_queries, int num_heads,

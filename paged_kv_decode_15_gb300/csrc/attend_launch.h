@@ -43,6 +43,11 @@ cudaError_t launch_attend_prompt(int D, int kv_dtype, const CUtensorMap& kvmap, 
                                      bool partials, bool overlap, int grid, cudaStream_t stream);
 PKD_PROMPT(bf16_d128) PKD_PROMPT(fp16_d128) PKD_PROMPT(fp8_d128) PKD_PROMPT(bf16_d64) PKD_PROMPT(fp16_d64)
 #undef PKD_PROMPT
+// The same on packed keys and values (tensor maps of their own), 16-bit types.
+cudaError_t launch_packed_bf16(int D, const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
+                               const AttendParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_packed_fp16(int D, const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
+                               const AttendParams& p, int grid, cudaStream_t stream);
 
 // Joins the partial results of the shared prefix with those of the requests' own keys.
 struct PrefixMergeParams {

@@ -38,6 +38,8 @@
 // Work items are handed out by an atomic counter in the workspace, the longest of
 // a request first, so CTAs finish together whatever the lengths; results do not
 // depend on who computes an item.  Every wait is bounded.
+// Packed prompts (pkd_packed_attention) run the same kernel on keys and values that lie
+// token by token: K and V of a tile are two boxes each, and nothing is looked up.
 #pragma once
 
 #include <type_traits>
@@ -79,6 +81,7 @@ struct PtItem {
     int split, nsplit, unit;
     int jb[2], je[2];              // steps [jb, je) of row tile t (empty: none); step j is key tile pt_tile(j)
     int bad, end;                  // bad: some page lies outside the pool
+    int key0;                      // packed keys: row of the request's first key
 };
 
 // Types of q and the cache.
@@ -93,7 +96,9 @@ __device__ __forceinline__ int pt_tile(int j, int ntiles) { return kBias ? ntile
 // NU K/V units; K and V of a key tile are one unit each (units of K have even
 // numbers, NU is even, so a slot always holds the one or the other).  e4m3: the
 // raw V units are widened to fp16 into two buffers of their own.
-template <int D, int kType>
+// kPacked: K and V of a tile are one box each per 128-byte region (all 128 keys), not a
+// box per 16 keys of a page with the regions of 8 keys side by side.
+template <int D, int kType, bool kPacked = false>
 struct PtShape {
     static constexpr bool FP8 = kType == kPtFP8;
     static constexpr int ROWB = D * (FP8 ? 1 : 2);
@@ -104,6 +109,9 @@ struct PtShape {
     static constexpr int NV = FP8 ? 2 : 0;               // widened V tiles
     static constexpr int VGROUP = 8 * D * 2;             // 8 keys of V as the O product reads them
     static constexpr int VUNIT = kPtKeys / 8 * VGROUP;
+    // strides of K and V (as the O product reads it) between 128-byte regions and groups of 8 keys
+    static constexpr int KREG = kPacked ? kPtKeys * 128 : 1024, KROW8 = kPacked ? 1024 : GROUP;
+    static constexpr int VREG = kPacked ? kPtKeys * 128 : 1024, VROW8 = kPacked ? 1024 : VGROUP;
     static constexpr int QTILE = kPtRows * ROWB;
     static constexpr int OFF_KV = 0;
     static constexpr int OFF_V = NU * UNIT;
@@ -139,6 +147,21 @@ __device__ __forceinline__ unsigned pt_stages(const AttendParams& p, const PtIte
         if (pg >= 0 && pg < p.num_pages) stages |= 1u << s;
     }
     return stages;
+}
+
+// A request's keys: L, and packed the row of the first (clamped as the lengths are).
+template <bool kPacked>
+__device__ __forceinline__ int pt_keys(const AttendParams& p, int b, bool report, int& key0) {
+    if constexpr (!kPacked) {
+        key0 = 0;
+        return request_len(p, b, report);
+    } else {
+        const int s0 = p.key_start[b], e0 = p.key_start[b + 1];
+        const int s = min(max(s0, 0), p.total_keys), e = min(max(e0, s), p.total_keys), L = min(e - s, p.max_kv_len);
+        if (report && (s != s0 || s + L != e0)) atomicOr(p.status, kErrBounds);
+        key0 = s;
+        return L;
+    }
 }
 
 // The request whose units (row-tile pairs times `mul`) hold unit r; pref: prefix of the pairs.
@@ -286,11 +309,14 @@ __device__ __forceinline__ void reg_dec() {
 }
 
 // partials: every result is left as a partial one (for a merge that follows)
-template <int D, int kType, bool kCap, bool kBias>
+// kPacked: keys and values of a request are rows key0 .. of two tensors (kvmap, vmap),
+// not in pages (kvmap alone)
+template <int D, int kType, bool kCap, bool kBias, bool kPacked = false>
 __global__ void __launch_bounds__(kPtThreads, 1)
-attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
-                     const AttendParams p, const int partials) {
-    using S = PtShape<D, kType>;
+attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap vmap,
+                     const __grid_constant__ CUtensorMap qmap, const AttendParams p, const int partials) {
+    using S = PtShape<D, kType, kPacked>;
+    static_assert(!kPacked || kType != kPtFP8, "packed keys are 16-bit");
     constexpr bool kFp8 = kType == kPtFP8, kBF16 = kType == kPtBF16;  // e4m3: P and V in fp16
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -384,9 +410,9 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
         // order depends on it: a look at every token's document took 10k cycles.)
         for (int x = tid; x < npairs; x += kPtThreads) {
             const int b = pt_request(pref, p.B, 1, x);
-            int q0, n, lo = 0x7fffffff, hi = 0;
+            int q0, n, lo = 0x7fffffff, hi = 0, key0;
             request_tokens(p, b, q0, n, false);
-            const int L = request_len(p, b, false), prefix = p.prefix_lens ? p.prefix_lens[b] : 0;
+            const int L = pt_keys<kPacked>(p, b, false, key0), prefix = p.prefix_lens ? p.prefix_lens[b] : 0;
             const int a0 = (x - pref[b]) * 2 * TOK, a1 = min(a0 + 2 * TOK, n) - 1;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -419,6 +445,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             // ------------------------------------------------------ loads
             if (lane == 0) {
                 prefetch_tmap(&kvmap);
+                if constexpr (kPacked) prefetch_tmap(&vmap);
                 prefetch_tmap(&qmap);
             }
             const uint64_t pol = policy_evict_first();
@@ -460,16 +487,16 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     } else {
                         b = pt_request(pref, p.B, p.Hkv, r1);
                     }
-                    int q0, n;
+                    int q0, n, key0;
                     request_tokens(p, b, q0, n, false);
                     if (!ordered) {
                         const int npair = pref[b + 1] - pref[b], r2 = r1 - pref[b] * p.Hkv;
-                        const int group = max(1, min(p.Hkv, kPtL2Bytes / (2 * S::ROWB) / max(request_len(p, b, false), 1)));
+                        const int group = max(1, min(p.Hkv, kPtL2Bytes / (2 * S::ROWB) / max(pt_keys<kPacked>(p, b, false, key0), 1)));
                         const int g = r2 / (npair * group), width = min(group, p.Hkv - g * group), r3 = r2 - g * npair * group;
                         pair = npair - 1 - r3 / width;
                         hk = g * group + r3 % width;
                     }
-                    const int L = request_len(p, b, pair == 0 && hk == 0 && split == 0 && lane == 0);
+                    const int L = pt_keys<kPacked>(p, b, pair == 0 && hk == 0 && split == 0 && lane == 0, key0);
                     const int prefix = p.prefix_lens ? p.prefix_lens[b] : 0;
                     const int tok0 = pair * 2 * TOK;
                     int lo[2], hi[2];
@@ -505,7 +532,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                     // a page outside the pool anywhere in the item: the softmax checks its keys
                     const int32_t* row = p.block_table + static_cast<long long>(b) * p.bt_stride;
                     int bad = 0;
-                    if (ntiles) {
+                    if (!kPacked && ntiles) {
                         const int c1 = page_div(t1 - 1, p.pmagic, p.pmshift);
                         for (int c = page_div(t0, p.pmagic, p.pmshift) + lane; c <= c1; c += 32)
                             bad |= row[c] < 0 || row[c] >= p.num_pages;
@@ -525,7 +552,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                             I.jb[t] = a >= z ? 0 : kBias ? ntiles - past : first;
                             I.je[t] = a >= z ? 0 : kBias ? ntiles - first : past;
                         }
-                        I.bad = bad; I.end = 0;
+                        I.bad = bad; I.end = 0; I.key0 = key0;
                         mbar_arrive(bar(S::B_IF + slot));
                     }
                     __syncwarp();
@@ -537,9 +564,10 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
             // Round r publishes item r, loads the rest of item r - 1's tiles, then Q and the
             // first tiles of item r.  (An item's slot is not reused before this warp
             // publishes four items on.)
-            int hk = 0, t0 = 0, t1 = 0, ntiles = 0, j = 0, pg = -1;
+            int hk = 0, t0 = 0, t1 = 0, ntiles = 0, j = 0, pg = -1, key0 = 0;
             const int32_t* row = p.block_table;
             auto entry = [&](int x) {
+                if constexpr (kPacked) return -1;
                 const int tok = t0 + pt_tile<kBias>(x, ntiles) * kPtKeys + lane * kStageTok;
                 return lane < kPtKeys / kStageTok && tok < t1 ? row[page_div(tok, p.pmagic, p.pmshift)] : -1;
             };
@@ -557,7 +585,8 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                         t0 = I.t0;
                         t1 = I.t1;
                         ntiles = I.ntiles;
-                        row = p.block_table + static_cast<long long>(I.b) * p.bt_stride;
+                        if constexpr (!kPacked) row = p.block_table + static_cast<long long>(I.b) * p.bt_stride;
+                        key0 = I.key0;
                         j = 0;
                         stop = min(ntiles, S::NU / 2);  // the ring is full behind them
                         if (!ntiles) break;
@@ -581,7 +610,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                         const int pg_next = j + 1 < ntiles ? entry(j + 1) : -1;
                         const int tok = t0 + pt_tile<kBias>(j, ntiles) * kPtKeys + lane * kStageTok;
                         const bool load = pg >= 0 && pg < p.num_pages;
-                        const int bytes = __popc(__ballot_sync(kFull, load)) * 2 * S::GROUP;
+                        const int bytes = kPacked ? S::UNIT : __popc(__ballot_sync(kFull, load)) * 2 * S::GROUP;
                         const int krow = load ? (pg * p.Hkv + hk) * p.P + (tok - page_div(tok, p.pmagic, p.pmshift) * p.P) : 0;
 #pragma unroll 1
                         for (int v = 0; v < 2; ++v, ++u) {
@@ -589,7 +618,12 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                             if (u >= S::NU && !pt_wait(bar(S::B_UE + us), ((u / S::NU) - 1) & 1, p)) { ok = false; break; }
                             if (lane == 0) mbar_arrive_expect_tx(bar(S::B_UF + us), bytes);
                             __syncwarp();
-                            if (load)
+                            if constexpr (kPacked) {
+                                // (rows behind the request's are the next one's, or zeros behind the last)
+                                if (lane < S::REGIONS)
+                                    tma_load_3d(sb0 + S::OFF_KV + us * S::UNIT + lane * S::KREG, v ? &vmap : &kvmap, 64 * lane,
+                                                hk, key0 + t0 + pt_tile<kBias>(j, ntiles) * kPtKeys, bar(S::B_UF + us), keep);
+                            } else if (load)
                                 tma_load_4d(sb0 + S::OFF_KV + us * S::UNIT + 2 * lane * S::GROUP, &kvmap, 0, 0,
                                             v * S::REGIONS, krow >> 3, bar(S::B_UF + us), keep);
                         }
@@ -634,7 +668,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                         ok = kFp8 ? pt_wait(bar(S::B_VF + vb), ((nv + j) >> 1) & 1, p)
                                   : pt_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p);
                     const uint32_t vlo = tc05::uniform(tc05::desc_lo(
-                        sb0 + (kFp8 ? S::OFF_V + vb * S::VUNIT : S::OFF_KV + ((vu + S::NU) % S::NU) * S::UNIT), 1024));
+                        sb0 + (kFp8 ? S::OFF_V + vb * S::VUNIT : S::OFF_KV + ((vu + S::NU) % S::NU) * S::UNIT), S::VREG));
                     const uint32_t klo = tc05::uniform(tc05::desc_lo(sb0 + S::OFF_KV + (ku % S::NU) * S::UNIT, 16));
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
@@ -655,8 +689,8 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
 #pragma unroll
                             for (int kk = 0; kk < kPtKeys / 16; ++kk)
                                 if (one)
-                                    tc05::mma_ts(o_addr, s_addr + 8 * kk, vlo + ((2 * kk * S::VGROUP) >> 4),
-                                                 tc05::desc_hi(S::VGROUP), kIdO, more || kk > 0);
+                                    tc05::mma_ts(o_addr, s_addr + 8 * kk, vlo + ((2 * kk * S::VROW8) >> 4),
+                                                 tc05::desc_hi(S::VROW8), kIdO, more || kk > 0);
                             if (one) {
                                 tc05::commit(bar(S::B_OD + t));
                                 if (j == je - 1) tc05::commit(bar(S::B_OF + t));
@@ -675,8 +709,8 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                                     if (one)
                                         tc05::mma_ss<kFp8>(s_addr,
                                                            qlo + ((t * S::QTILE + (kk >> 2) * kPtRows * 128 + (kk & 3) * 32) >> 4),
-                                                           tc05::desc_hi(1024), klo + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
-                                                           tc05::desc_hi(S::GROUP), kIdS, kk > 0);
+                                                           tc05::desc_hi(1024), klo + (((kk >> 2) * S::KREG + (kk & 3) * 32) >> 4),
+                                                           tc05::desc_hi(S::KROW8), kIdS, kk > 0);
                                 if (one) tc05::commit(bar(S::B_SF + t));
                             }
                             if (t == 1 && one) {
@@ -975,12 +1009,12 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
                         const int vu = u + 2 * j + 1, key = tk + r;
                         if (!pt_wait(bar(S::B_UF + vu % S::NU), (vu / S::NU) & 1, p)) { ok = false; break; }
                         if (key < lo_all || key >= hi_all || (bad && !(pt_stages(p, I, tk) >> (r >> 4) & 1))) {
-                            uint8_t* vrow = smem + S::OFF_KV + (vu % S::NU) * S::UNIT + (r >> 3) * S::GROUP + (r & 7) * 128;
+                            uint8_t* vrow = smem + S::OFF_KV + (vu % S::NU) * S::UNIT + (r >> 3) * S::KROW8 + (r & 7) * 128;
 #pragma unroll
                             for (int h = 0; h < S::REGIONS; ++h)
 #pragma unroll
                                 for (int e = 0; e < 8; ++e)
-                                    *reinterpret_cast<uint4*>(vrow + h * 1024 + ((e + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+                                    *reinterpret_cast<uint4*>(vrow + h * S::KREG + ((e + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async();
                     }

@@ -13,7 +13,7 @@ static cudaError_t launch_prompt_one(const CUtensorMap& kvmap, const CUtensorMap
     static PerDevice state;
     cudaError_t e = kernel_setup(state, kern, kPtThreads, PtShape<D, kType>::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_kernel(kern, dim3(grid), kPtThreads, PtShape<D, kType>::SMEM, overlap, stream, kvmap, qmap, p,
+    return launch_kernel(kern, dim3(grid), kPtThreads, PtShape<D, kType>::SMEM, overlap, stream, kvmap, kvmap, qmap, p,
                          partials ? 1 : 0);
 }
 
@@ -26,6 +26,16 @@ static cudaError_t launch_prompt_typed(const CUtensorMap& kvmap, const CUtensorM
                     : launch_prompt_one<D, kType, true, false>(kvmap, qmap, p, partials, overlap, grid, stream);
     return bias ? launch_prompt_one<D, kType, false, true>(kvmap, qmap, p, partials, overlap, grid, stream)
                 : launch_prompt_one<D, kType, false, false>(kvmap, qmap, p, partials, overlap, grid, stream);
+}
+
+template <int D, int kType, bool kCap>
+static cudaError_t launch_packed_one(const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
+                                     const AttendParams& p, int grid, cudaStream_t stream) {
+    auto kern = attend_prompt_kernel<D, kType, kCap, false, true>;
+    static PerDevice state;
+    cudaError_t e = kernel_setup(state, kern, kPtThreads, PtShape<D, kType, true>::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kern, dim3(grid), kPtThreads, PtShape<D, kType, true>::SMEM, false, stream, kmap, vmap, qmap, p, 0);
 }
 
 }  // namespace pkd

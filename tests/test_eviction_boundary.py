@@ -18,6 +18,36 @@ def lib():
     return pkd.load_library()
 
 
+def packed(lib, **over):
+    a = dict(q=FAKE, qs=512, k=FAKE, ks=256, v=FAKE, vs=256, dt=pkd.BF16, starts=FAKE, key_start=None, B=2, T=20, Tk=20, max_q=16,
+             max_kv=16, Hq=4, Hkv=2, D=128, scale=0.1, softcap=0.0, window=0, out=FAR, out_dt=pkd.BF16, lse=None, ws=FAKE,
+             ws_bytes=1 << 40, flags=pkd.FLAG_CAUSAL, stream=None)
+    a.update(over)
+    return lib.pkd_packed_attention(*a.values())
+
+
+@pytest.mark.parametrize("over,code,needle", [
+    (dict(Hq=5), pkd.EUNSUPPORTED, "multiple of num_kv_heads"), (dict(D=96), pkd.EUNSUPPORTED, "head_dim"),
+    (dict(dt=pkd.FP8_E4M3), pkd.EUNSUPPORTED, "dtype"), (dict(dt=pkd.FP32), pkd.EUNSUPPORTED, "dtype"),
+    (dict(Tk=21), pkd.EINVAL, "key_start"), (dict(Tk=-1), pkd.EINVAL, "total_keys"), (dict(Tk=(1 << 29) + 1), pkd.EINVAL, "total_keys"),
+    (dict(q=None), pkd.EINVAL, "null"), (dict(k=None), pkd.EINVAL, "null"), (dict(v=None), pkd.EINVAL, "null"),
+    (dict(v=ODD), pkd.EINVAL, "misaligned"), (dict(ks=252), pkd.EINVAL, "k_stride"), (dict(vs=260), pkd.EINVAL, "v_stride"),
+    (dict(vs=1 << 39), pkd.EINVAL, "2^38"), (dict(qs=511), pkd.EINVAL, "q_stride"), (dict(starts=None), pkd.EINVAL, "query_start"),
+    (dict(key_start=ODD), pkd.EINVAL, "misaligned"), (dict(max_q=0), pkd.EINVAL, "max_query_len"),
+    (dict(max_kv=-1), pkd.EINVAL, "max_kv_len"), (dict(out=FAKE), pkd.EINVAL, "overlaps q"),
+    (dict(out=FAKE, q=FAR), pkd.EINVAL, "overlaps k"), (dict(out=FAKE, q=FAR, k=FAR), pkd.EINVAL, "overlaps v"),
+    (dict(softcap=-1.0), pkd.EINVAL, "softcap"), (dict(scale=-1.0), pkd.EINVAL, "scale"), (dict(ws_bytes=100), pkd.EINVAL, "workspace"),
+    (dict(out_dt=pkd.FP8_E4M3), pkd.EUNSUPPORTED, "out dtype"), (dict(flags=8), pkd.EUNSUPPORTED, "PKD_FLAG_CAUSAL")])
+def test_packed_refusals(lib, over, code, needle):
+    assert packed(lib, **over) == code
+    assert needle in lib.pkd_last_error().decode()
+
+
+def test_packed_calls_without_rows_are_ok(lib):
+    assert packed(lib, B=0) == pkd.OK
+    assert packed(lib, T=0, Tk=0, max_q=0, q=None, k=None, v=None) == pkd.OK
+
+
 def weigh(lib, **over):
     a = dict(q=FAKE, q_dt=pkd.BF16, q_stride=512, cache=FAKE, kv_dt=pkd.BF16, num_pages=8, table=FAKE, stride=8, lens=FAKE,
              starts=FAKE, B=2, T=20, max_q=16, last=0, Hq=4, Hkv=2, D=128, P=16, max_kv=100, scale=0.1, qs=1.0, ks=1.0,
