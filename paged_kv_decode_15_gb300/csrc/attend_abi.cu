@@ -7,7 +7,7 @@
 #include "attend.cuh"
 #include "attend_launch.h"
 #include "attend_prompt.cuh"
-#include "key_weights.cuh"
+#include "key_weights_tc05.cuh"
 #include "page_math.h"
 
 namespace {
@@ -178,8 +178,13 @@ pkd_status plan_packed(int B, long long T, int max_q, int Hq, int Hkv, int D, in
 }
 
 struct WeighPlan {
+    bool step;          // the mma.sync grid, else the tcgen05 kernel
     long long rows;     // query rows of a request and kv head that weigh, at most
-    int chunk, chunks;  // keys of a CTA
+    int chunk;          // step: keys of a CTA; else tokens of a part
+    int chunks;         // step: CTAs along a request's keys
+    int max_splits;     // parts of a key block's tokens
+    long long units;    // key blocks of all kv heads, at most
+    size_t bytes;       // the parts' sums
 };
 
 pkd_status plan_key_weights(int B, long long T, int max_q, int last, int Hq, int Hkv, int D, int P, int max_kv_len,
@@ -191,11 +196,26 @@ pkd_status plan_key_weights(int B, long long T, int max_q, int last, int Hq, int
     if (last < 0) return report(PKD_EINVAL, "last_queries must be >= 0 (got %d)", last);
     const long long tokens = std::min<long long>(last > 0 ? std::min(last, max_q) : max_q, T);
     pl.rows = tokens * (Hq / Hkv);
-    // about 16 CTAs per SM, chunks of 128 to 2048 keys
-    const long long units = std::max(1ll, (long long)B * Hkv);
-    const long long chunk = std::min(2048ll, std::max(128ll, max_kv_len * units / (16 * kSms)));
-    pl.chunk = up((int)chunk, 128);
-    pl.chunks = (max_kv_len + pl.chunk - 1) / pl.chunk;
+    pl.step = pl.rows <= 16;
+    pl.max_splits = 1;
+    if (pl.step) {
+        // about 16 CTAs per SM, chunks of 128 to 2048 keys
+        const long long units = std::max(1ll, (long long)B * Hkv);
+        const long long chunk = std::min(2048ll, std::max(128ll, max_kv_len * units / (16 * kSms)));
+        pl.chunk = up((int)chunk, 128);
+        pl.chunks = (max_kv_len + pl.chunk - 1) / pl.chunk;
+        return PKD_OK;
+    }
+    const long long tok = pkd::kPtRows / (Hq / Hkv), tiles = (tokens + tok - 1) / tok;
+    pl.units = (long long)B * Hkv * ((max_kv_len + pkd::kWtKeys - 1) / pkd::kWtKeys);
+    // the tokens are split while the key blocks alone leave SMs idle: about four items per
+    // SM, of four query tiles at least
+    const long long splits = pl.units ? std::min((4 * kSms + pl.units - 1) / pl.units, (tiles + 3) / 4) : 1;
+    const long long part = (tiles + splits - 1) / splits * tok;
+    pl.chunk = (int)std::min<long long>(part, 0x7fffffff);
+    pl.max_splits = (int)((tokens + pl.chunk - 1) / pl.chunk);
+    if (pl.units * pl.max_splits >= 1ll << 31) return report(PKD_EUNSUPPORTED, "too many work items");
+    if (pl.max_splits > 1) pl.bytes = up256((size_t)pl.units * pl.max_splits * pkd::kWtKeys * 4);
     return PKD_OK;
 }
 
@@ -650,7 +670,7 @@ size_t pkd_key_weights_workspace_size(int batch, int64_t total_tokens, int max_q
                                       int num_kv_heads, int head_dim, int page_size, int max_kv_len, pkd_dtype kv_dtype) {
     WeighPlan pl;
     return plan_key_weights(batch, total_tokens, max_query_len, last_queries, num_heads, num_kv_heads, head_dim, page_size,
-                            max_kv_len, kv_dtype, pl) == PKD_OK ? kPartials : 0;
+                            max_kv_len, kv_dtype, pl) == PKD_OK ? kPartials + pl.bytes : 0;
 }
 
 pkd_status pkd_key_weights(const void* q, pkd_dtype q_dtype, int64_t q_stride, const void* kv_cache, pkd_dtype kv_dtype,
@@ -675,7 +695,7 @@ pkd_status pkd_key_weights(const void* q, pkd_dtype q_dtype, int64_t q_stride, c
     if (total_tokens == 0) q = lse = static_cast<const float*>(workspace);  // no row of them is read
     st = check_call(q, q_dtype, total_tokens ? q_stride : (int64_t)num_heads * head_dim, kv_cache, kv_dtype, num_pages,
                     num_heads, num_kv_heads, head_dim, page_size, scale, q_scale, k_scale, 1.f, softcap, q, PKD_FP32, lse,
-                    workspace, workspace_bytes, kPartials);
+                    workspace, workspace_bytes, kPartials + pl.bytes);
     if (st != PKD_OK) return st;
     st = check_table(block_table, block_table_stride, seq_lens, max_kv_len, page_size, "block_table");
     if (st != PKD_OK) return st;
@@ -702,6 +722,7 @@ pkd_status pkd_key_weights(const void* q, pkd_dtype q_dtype, int64_t q_stride, c
     AttendPlan none{};
     none.G = num_heads / num_kv_heads;
     none.chunk = pl.chunk;
+    none.max_splits = pl.max_splits;
     fill(w.a, none, ws, 0, kPartials, batch, total_tokens, num_heads, num_kv_heads, page_size, max_kv_len, num_pages,
          scale * q_scale * k_scale * pkd::kLog2e, softcap, flags);
     w.a.q = q;
@@ -723,8 +744,19 @@ pkd_status pkd_key_weights(const void* q, pkd_dtype q_dtype, int64_t q_stride, c
     w.weights_h = weights_head_stride;
     w.decay = decay;
     w.last = last_queries;
-    const cudaError_t e = pkd::launch_key_weights(head_dim, (int)kv_dtype, pl.rows, w, dim3(pl.chunks, num_kv_heads, batch),
-                                                  (cudaStream_t)stream);
+    cudaError_t e;
+    if (pl.step) {
+        e = pkd::launch_key_weights(head_dim, (int)kv_dtype, pl.rows, w, dim3(pl.chunks, num_kv_heads, batch),
+                                    (cudaStream_t)stream);
+    } else {
+        CUtensorMap kvmap, qmap;
+        st = pkd::half_stage_map(kvmap, kv_cache, (uint64_t)num_pages * num_kv_heads * page_size, 2 * head_dim * elt_bytes(kv_dtype),
+                                 kv_dtype);
+        if (st == PKD_OK)
+            st = pkd::query_map(qmap, q, head_dim, num_heads, (uint64_t)total_tokens, q_stride, w.a.G, pkd::kPtRows / w.a.G, kv_dtype);
+        if (st != PKD_OK) return st;
+        e = pkd::launch_key_weights_tc05(head_dim, (int)kv_dtype, kvmap, qmap, w, pl.units * pl.max_splits, (cudaStream_t)stream);
+    }
     return e == cudaSuccess ? PKD_OK : cuda_fail(e, "pkd_key_weights launch");
 }
 

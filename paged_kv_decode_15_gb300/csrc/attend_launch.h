@@ -67,6 +67,9 @@ cudaError_t launch_prefix_merge(int D, const PrefixMergeParams& p, cudaStream_t 
 struct WeighParams;
 // Weights of a paged cache's keys; grid (chunks of a request's keys, Hkv, B).
 cudaError_t launch_key_weights(int D, int kv_dtype, long long rows, const WeighParams& w, dim3 grid, cudaStream_t stream);
+// The same on tcgen05 tensor cores: at most `items` persistent CTAs.
+cudaError_t launch_key_weights_tc05(int D, int kv_dtype, const CUtensorMap& kvmap, const CUtensorMap& qmap,
+                                    const WeighParams& w, long long items, cudaStream_t stream);
 
 // Tensor maps (cached by value; abi.cu).
 pkd_status stage_map(CUtensorMap& out, const void* cache, uint64_t rows, int row_bytes, pkd_dtype dt);

@@ -1,0 +1,529 @@
+// pkd_key_weights on the 5th-generation tensor cores: prompts, whose products bind.
+//
+// A work item is 256 keys of one (request, kv head) -- two tiles of 128 -- against the
+// query rows that see any of them, in tiles of up to 128 rows (TOK = 128 / G whole tokens,
+// packed token-major as in the attention kernel).  Per query tile and key tile
+//   S^T = K Q^T   tcgen05.mma, M = 128 keys, N = 128 rows, operands K-major as TMA lands them
+//   sum           a thread owns a key (TMEM lane): 2^(scale s - lse) of 128 columns, summed
+//                 in registers.  The rows' LSEs, alike for all keys, come from shared memory
+// K stays for the whole item and both key tiles share every query tile, so a 128x128
+// product costs 16 KB out of L2.  Sums: fp32 within a tile, the tiles' sums with
+// compensation, in the order of the tokens: no atomics on results.
+//
+// Warp roles (384 threads): warps 0-3 and 4-7 the exponentials of key tile 0 and 1, warp 8
+// loads (items, K, Q), warp 9 issues the products, warp 10 lays out the LSEs.  K and Q
+// tiles share NU slots: a slot goes to the next tile in the order in which slots become
+// free, which is the same for the warp that fills them and the one that reads them (both
+// keep the queue of free slots), so short items have all slots in flight and long ones
+// NU - 2 query tiles.  Every wait is bounded.
+//
+// A request's query rows are split between items (`span` tokens each) where its key blocks
+// alone leave SMs idle; the sums of the parts are joined in order by the last to arrive.
+#pragma once
+
+#include "attend_prompt.cuh"
+#include "key_weights.cuh"
+
+namespace pkd {
+
+constexpr int kWtKeys = 256, kWtThreads = 384, kWtItems = 4, kWtLse = 4;
+
+struct WtItem {
+    int b, hk, t0, nk;            // keys from t0 on, tiles of 128 of them
+    int first, L, fresh, off;     // row of the first weighing token, whose position is off
+    int i0, i1, steps;            // weighing tokens [i0, i1), in tiles of TOK
+    int split, nsplit, unit;      // parts of the unit that hold any
+    int bad, end;
+};
+
+template <int D, int kType>
+struct WtShape {
+    static constexpr bool FP8 = kType == kPtFP8;
+    static constexpr int ROWB = D * (FP8 ? 1 : 2), REGIONS = ROWB / 128, GROUP = 8 * ROWB;
+    static constexpr int UNIT = 128 * ROWB;
+    static constexpr int NU = UNIT == 32768 ? 6 : 12;
+    static constexpr int OFF_LSE = NU * UNIT;
+    static constexpr int OFF_ITEM = OFF_LSE + kWtLse * 128 * 4;
+    static constexpr int OFF_PREF = OFF_ITEM + kWtItems * static_cast<int>(sizeof(WtItem));
+    static constexpr int OFF_SCAN = OFF_PREF + (kPtMaxBatch + 4) * 4;
+    static constexpr int OFF_BAR = (OFF_SCAN + 64 + 7) & ~7;
+    // slots full/empty, S full/empty [key tile][buffer], LSEs full/empty, items full/empty, drain
+    static constexpr int B_UF = 0, B_UE = B_UF + NU, B_SF = B_UE + NU, B_SE = B_SF + 4, B_LF = B_SE + 4;
+    static constexpr int B_LE = B_LF + kWtLse, B_IF = B_LE + kWtLse, B_IE = B_IF + kWtItems, B_DR = B_IE + kWtItems;
+    static constexpr int NBAR = B_DR + 1;
+    static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
+    static constexpr int SMEM = OFF_TMEM + 16 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
+    static_assert(SMEM > 114 * 1024, "one CTA per SM: all 512 TMEM columns are its own");
+    static_assert(NU <= 15, "the queue of free slots holds 16 of four bits");
+};
+
+// The queue of free slots, four bits each, the next one lowest.
+struct WtSlots {
+    uint64_t queue;
+    int n;
+    __device__ __forceinline__ explicit WtSlots(int slots) : queue(0xfedcba9876543210ull), n(slots) {}
+    __device__ __forceinline__ int take() {
+        const int s = static_cast<int>(queue & 15);
+        queue >>= 4;
+        --n;
+        return s;
+    }
+    __device__ __forceinline__ void give(int s) {
+        queue = (queue & ~(15ull << (4 * n))) | static_cast<uint64_t>(s) << (4 * n);
+        ++n;
+    }
+};
+
+template <int D, int kType, bool kCap>
+__global__ void __launch_bounds__(kWtThreads, 1)
+key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
+                        const WeighParams w) {
+    using S = WtShape<D, kType>;
+    constexpr bool kFp8 = kType == kPtFP8;
+    const AttendParams& p = w.a;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb0 = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);
+    WtItem* items = reinterpret_cast<WtItem*>(smem + S::OFF_ITEM);
+    int* pref = reinterpret_cast<int*>(smem + S::OFF_PREF);
+    int* scan = reinterpret_cast<int*>(smem + S::OFF_SCAN);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + S::OFF_TMEM);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = p.G, TOK = kPtRows / G;
+    auto bar = [&](int i) { return smem_u32(bars + i); };
+
+    // ------------------------------------------------------------ set-up
+    if (tid == 0) {
+        for (int i = 0; i < S::NU; ++i) {
+            mbar_init(bar(S::B_UF + i), 1);
+            mbar_init(bar(S::B_UE + i), 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(S::B_SF + i), 1);
+            mbar_init(bar(S::B_SE + i), 4);
+        }
+        for (int i = 0; i < kWtLse; ++i) {
+            mbar_init(bar(S::B_LF + i), 1);
+            mbar_init(bar(S::B_LE + i), 8);
+        }
+        for (int i = 0; i < kWtItems; ++i) {
+            mbar_init(bar(S::B_IF + i), 1);
+            mbar_init(bar(S::B_IE + i), 10);  // the issuing, LSE and eight exponential warps
+        }
+        mbar_init(bar(S::B_DR), 1);
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tc05::alloc(smem_u32(tslot), 512);  // S^T of (key tile, buffer): columns 128 * (2 * tile + buffer)
+        tc05::relinquish_alloc_permit();
+    }
+    // prefix of the requests' key blocks (units of one kv head)
+    {
+        int run = 0;
+        for (int b0 = 0; b0 < p.B; b0 += kWtThreads) {
+            const int b = b0 + tid;
+            int v = b < p.B ? (request_len(p, b, blockIdx.x == 0) + kWtKeys - 1) / kWtKeys : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, v, o);
+                if (lane >= o) v += y;
+            }
+            if (lane == 31) scan[warp] = v;
+            __syncthreads();
+            int before = run;
+            for (int k = 0; k < kWtThreads / 32; ++k) {
+                if (k < warp) before += scan[k];
+                run += scan[k];
+            }
+            if (b < p.B) pref[b + 1] = before + v;
+            __syncthreads();
+        }
+        if (tid == 0) pref[0] = 0;
+    }
+    tc05::fence_before_sync();
+    __syncthreads();
+    tc05::fence_after_sync();
+    const uint32_t tmem = *tslot;
+
+    if (warp == 8) {
+        // ---------------------------------------------------------- loads
+        if (lane == 0) {
+            prefetch_tmap(&kvmap);
+            prefetch_tmap(&qmap);
+        }
+        const uint64_t pol = policy_evict_first();
+        uint64_t keep;  // other items read the same queries
+        asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
+        const int units = pref[p.B] * p.Hkv, total = units * p.max_splits;
+        WtSlots slots(S::NU);
+        uint32_t phase = 0, used = 0;  // of each slot
+        int idx = blockIdx.x, npub = 0;
+        bool ok = true;
+        // the slot of the next tile, empty
+        auto take = [&]() {
+            const int s = slots.take();
+            ok = pt_wait(bar(S::B_UE + s), (phase >> s & 1) ^ 1, p);
+            if (ok) phase ^= 1u << s, used |= 1u << s;
+            return s;
+        };
+        while (ok) {
+            const int ring = npub % kWtItems;
+            if (npub >= kWtItems && !pt_wait(bar(S::B_IE + ring), ((npub / kWtItems) - 1) & 1, p)) { ok = false; break; }
+            if (idx >= total) {
+                if (lane == 0) {
+                    items[ring].end = 1;
+                    mbar_arrive(bar(S::B_IF + ring));
+                }
+                __syncwarp();
+                break;
+            }
+            int next = 0;
+            if (lane == 0) next = static_cast<int>(gridDim.x) + atomicAdd(p.queue, 1);
+            // item idx: parts innermost, then kv heads, the key blocks of a request from the
+            // first (causal: seen by the most tokens)
+            const int split = idx % p.max_splits, u = idx / p.max_splits;
+            const int b = pt_request(pref, p.B, p.Hkv, u), r = u - pref[b] * p.Hkv;
+            const int hk = r % p.Hkv, t0 = r / p.Hkv * kWtKeys;
+            const WeighRequest q = weigh_request(w, b, r == 0 && split == 0 && lane == 0);
+            const int t1 = min(t0 + kWtKeys, q.L), off = q.L - q.m, nk = t1 - t0 > 128 ? 2 : 1;
+            // tokens that see any of the keys: from the first key's position on, up to a
+            // window behind the last key
+            int i0 = p.causal ? max(0, t0 - off) : 0, i1 = q.m;
+            if (p.window > 0) i1 = static_cast<int>(min(static_cast<long long>(q.m), static_cast<long long>(t1 - 1) - off + p.window));
+            int nsplit = 0;
+            if (i0 < i1) {
+                // parts begin at multiples of span behind i0
+                nsplit = min((i1 - i0 + p.chunk - 1) / p.chunk, p.max_splits);
+                i0 += split * p.chunk;
+                if (split + 1 < nsplit) i1 = min(i1, i0 + p.chunk);
+            }
+            if (split >= max(nsplit, 1)) {  // nothing here
+                idx = __shfl_sync(kFull, next, 0);
+                continue;
+            }
+            const int steps = nsplit ? (i1 - i0 + TOK - 1) / TOK : 0;
+            // the pages of the 16-key stages, a lane each
+            const int t = t0 + kStageTok * lane;
+            int krow = -1;
+            bool bad = false;
+            if (lane < kWtKeys / kStageTok && t < t1) {
+                const int col = page_div(t, p.pmagic, p.pmshift);
+                const int page = p.block_table[static_cast<long long>(b) * p.bt_stride + col];
+                bad = page < 0 || page >= p.num_pages;
+                if (!bad) krow = (page * p.Hkv + hk) * p.P + (t - col * p.P);
+            }
+            bad = __any_sync(kFull, bad);
+            if (lane == 0) {
+                if (bad) atomicOr(p.status, kErrBounds);
+                WtItem& I = items[ring];
+                I.b = b; I.hk = hk; I.t0 = t0; I.nk = nk; I.first = q.first; I.L = q.L; I.fresh = q.fresh; I.off = off;
+                I.i0 = i0; I.i1 = i1; I.steps = steps; I.split = split; I.nsplit = nsplit; I.unit = u; I.bad = bad; I.end = 0;
+                mbar_arrive(bar(S::B_IF + ring));
+            }
+            __syncwarp();
+            ++npub;
+            if (steps) {
+                int ks[2] = {0, 0};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (e >= nk || !ok) continue;
+                    ks[e] = take();
+                    if (!ok) continue;
+                    const bool load = krow >= 0 && (lane >> 3) == e;
+                    const int bytes = __popc(__ballot_sync(kFull, load)) * 2 * S::GROUP;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(S::B_UF + ks[e]), bytes);
+                    __syncwarp();
+                    if (load)
+                        tma_load_4d(sb0 + ks[e] * S::UNIT + 2 * (lane & 7) * S::GROUP, &kvmap, 0, 0, 0, krow >> 3,
+                                    bar(S::B_UF + ks[e]), pol);
+                }
+#pragma unroll 1
+                for (int j = 0; ok && j < steps; ++j) {
+                    const int s = take();
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(S::B_UF + s), S::REGIONS * TOK * G * 128);
+                    __syncwarp();
+                    if (lane < S::REGIONS)
+                        tma_load_3d(sb0 + s * S::UNIT + lane * kPtRows * 128, &qmap, 64 * lane, hk * G, q.first + i0 + j * TOK,
+                                    bar(S::B_UF + s), keep);
+                    slots.give(s);
+                }
+                slots.give(ks[0]);
+                if (nk > 1) slots.give(ks[1]);
+            }
+            idx = __shfl_sync(kFull, next, 0);
+        }
+        // let every issued copy land before the CTA leaves
+        for (int s = 0; s < S::NU; ++s)
+            if (used >> s & 1) mbar_wait(bar(S::B_UF + s), (phase >> s & 1) ^ 1);
+        if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
+    } else if (warp == 9) {
+        // ------------------------------------------------------- products
+        constexpr uint32_t kId = kFp8 ? tc05::idesc_e4m3(128, 128) : tc05::idesc_f16(kType == kPtBF16, 128, 128, false, false);
+        const bool one = tc05::elect_one();
+        const uint32_t tm = tc05::uniform(tmem), lo0 = tc05::uniform(tc05::desc_lo(sb0, 16));
+        WtSlots slots(S::NU);
+        uint32_t phase = 0;
+        int ns[2] = {0, 0};  // S^T tiles begun
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            const int ring = it % kWtItems;
+            if (!pt_wait(bar(S::B_IF + ring), (it / kWtItems) & 1, p)) { ok = false; break; }
+            const WtItem& I = items[ring];
+            if (I.end) break;
+            const int steps = I.steps, nk = I.nk;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(S::B_IE + ring));
+            if (!steps) continue;
+            int ks[2];
+            ks[0] = slots.take();
+            ks[1] = nk > 1 ? slots.take() : 0;
+#pragma unroll 1
+            for (int j = 0; ok && j < steps; ++j) {
+                const int s = slots.take();
+                ok = pt_wait(bar(S::B_UF + s), phase >> s & 1, p);
+                phase ^= 1u << s;
+                const uint32_t qlo = tc05::uniform(lo0 + (s * S::UNIT >> 4));
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t >= nk || !ok) continue;
+                    if (j == 0) {
+                        ok = pt_wait(bar(S::B_UF + ks[t]), phase >> ks[t] & 1, p);
+                        phase ^= 1u << ks[t];
+                    }
+                    const int buf = ns[t] & 1;
+                    ok = ok && pt_wait(bar(S::B_SE + 2 * t + buf), ((ns[t] >> 1) & 1) ^ 1, p);
+                    if (!ok) continue;
+                    ++ns[t];
+                    tc05::fence_after_sync();
+                    const uint32_t klo = tc05::uniform(lo0 + (ks[t] * S::UNIT >> 4));
+                    const uint32_t d = tm + 128 * (2 * t + buf);
+#pragma unroll
+                    for (int kk = 0; kk < S::ROWB / 32; ++kk)
+                        if (one)
+                            tc05::mma_ss<kFp8>(d, klo + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), tc05::desc_hi(S::GROUP),
+                                               qlo + (((kk >> 2) * kPtRows * 128 + (kk & 3) * 32) >> 4), tc05::desc_hi(1024), kId,
+                                               kk > 0);
+                    if (one) tc05::commit(bar(S::B_SF + 2 * t + buf));
+                }
+                if (!ok) break;
+                if (one) tc05::commit(bar(S::B_UE + s));
+                slots.give(s);
+            }
+            if (ok && one) {
+                tc05::commit(bar(S::B_UE + ks[0]));
+                if (nk > 1) tc05::commit(bar(S::B_UE + ks[1]));
+            }
+            slots.give(ks[0]);
+            if (nk > 1) slots.give(ks[1]);
+        }
+        if (!ok && one) atomicOr(p.status, kErrTimeout);
+        // every product issued has completed before TMEM is freed
+        if (one) {
+            tc05::commit(bar(S::B_DR));
+            mbar_wait(bar(S::B_DR), 0);
+        }
+        __syncwarp();
+    } else if (warp == 10) {
+        // ------------------------------------- the rows' LSEs, as added to logits
+        float* lse2 = reinterpret_cast<float*>(smem + S::OFF_LSE);
+        int nl = 0;
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            const int ring = it % kWtItems;
+            if (!pt_wait(bar(S::B_IF + ring), (it / kWtItems) & 1, p)) { ok = false; break; }
+            const WtItem& I = items[ring];
+            if (I.end) break;
+            const int steps = I.steps, i0 = I.i0, i1 = I.i1;
+            const float* lse = w.lse + static_cast<long long>(I.first) * p.Hq + I.hk * G;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(S::B_IE + ring));
+            int tok[4], col[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = 4 * lane + e;
+                tok[e] = c / G;
+                col[e] = tok[e] < TOK ? c - tok[e] * G : -1;
+            }
+            auto load = [&](int j, float (&x)[4]) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = i0 + j * TOK + tok[e];
+                    x[e] = col[e] >= 0 && i < i1 ? lse[static_cast<long long>(i) * p.Hq + col[e]] : -INFINITY;
+                }
+            };
+            float x[4];
+            if (steps) load(0, x);
+#pragma unroll 1
+            for (int j = 0; j < steps; ++j, ++nl) {
+                const int s = nl % kWtLse;
+                float4 v;
+                v.x = x[0] == -INFINITY ? x[0] : -kLog2e * x[0];
+                v.y = x[1] == -INFINITY ? x[1] : -kLog2e * x[1];
+                v.z = x[2] == -INFINITY ? x[2] : -kLog2e * x[2];
+                v.w = x[3] == -INFINITY ? x[3] : -kLog2e * x[3];
+                if (j + 1 < steps) load(j + 1, x);
+                if (!pt_wait(bar(S::B_LE + s), ((nl / kWtLse) & 1) ^ 1, p)) { ok = false; break; }
+                *reinterpret_cast<float4*>(lse2 + 128 * s + 4 * lane) = v;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S::B_LF + s));
+            }
+        }
+        if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
+    } else if (warp < 8) {
+        // --------------------------------------------------- exponentials
+        const int tile = warp >> 2, q4 = warp & 3, r = 128 * tile + 32 * q4 + lane;  // key of the item
+        const float* lse2 = reinterpret_cast<const float*>(smem + S::OFF_LSE);
+        const uint32_t s_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16) + 256 * tile;
+        const int rows = TOK * G;
+        int ns = 0, nl = 0;
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            const int ring = it % kWtItems;
+            if (!pt_wait(bar(S::B_IF + ring), (it / kWtItems) & 1, p)) { ok = false; break; }
+            const WtItem& I = items[ring];
+            if (I.end) break;
+            const int steps = I.steps, i0 = I.i0, i1 = I.i1, key = I.t0 + r;
+            const bool mine = key < I.L;
+            // tokens [lo, hi) see this key; every key of the warp is seen by [wlo, whi)
+            int lo = i0, hi = i1;
+            if (p.causal) lo = max(lo, key - I.off);
+            if (p.window > 0)
+                hi = static_cast<int>(min(static_cast<long long>(hi), static_cast<long long>(key) - I.off + p.window));
+            if (!mine) hi = lo;
+            const int wlo = __reduce_max_sync(kFull, mine ? lo : i0), whi = __reduce_min_sync(kFull, mine ? hi : i1);
+            const bool active = tile < I.nk;
+            float total = 0.f, comp = 0.f;
+#pragma unroll 1
+            for (int j = 0; j < steps; ++j, ++nl) {
+                const int ls = nl % kWtLse;
+                if (!pt_wait(bar(S::B_LF + ls), (nl / kWtLse) & 1, p)) { ok = false; break; }
+                if (active) {
+                    const int buf = ns & 1, a = i0 + j * TOK;
+                    if (!pt_wait(bar(S::B_SF + 2 * tile + buf), (ns >> 1) & 1, p)) { ok = false; break; }
+                    ++ns;
+                    tc05::fence_after_sync();
+                    const float* nl2 = lse2 + 128 * ls;
+                    const bool masked = wlo > a || whi < a + TOK;
+                    const int cols = min(TOK, i1 - a) * G;
+                    // columns [c0, c1) of this key
+                    const int c0 = min(max(lo - a, 0), TOK) * G, c1 = min(max(hi - a, 0), TOK) * G;
+                    uint32_t v[2][32];
+                    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    auto chunk = [&](uint32_t (&x)[32], int c, auto select) {
+                        if constexpr (kCap) {
+                            if (__any_sync(kFull, pt_max<true>(x) > p.cap_far))
+                                pt_cap<false>(x, p);
+                            else
+                                pt_cap<true>(x, p);
+                        }
+                        const float scale = kCap ? 1.f : p.scale_log2;
+                        unsigned seen = 0xffffffffu;
+                        if constexpr (decltype(select)::value) {
+                            const int f = max(c0 - 32 * c, 0), z = min(c1 - 32 * c, 32);
+                            seen = f < z ? (0xffffffffu >> (32 - (z - f))) << f : 0u;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 n = *reinterpret_cast<const float4*>(nl2 + 32 * c + e);
+                            float2 y = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), both(scale), make_float2(n.x, n.y));
+                            float2 z = fma2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), both(scale), make_float2(n.z, n.w));
+                            y.x = fast_exp2(y.x);
+                            y.y = fast_exp2(y.y);
+                            z.x = fast_exp2(z.x);
+                            z.y = fast_exp2(z.y);
+                            if constexpr (decltype(select)::value) {
+                                y.x = seen >> e & 1 ? y.x : 0.f;
+                                y.y = seen >> (e + 1) & 1 ? y.y : 0.f;
+                                z.x = seen >> (e + 2) & 1 ? z.x : 0.f;
+                                z.y = seen >> (e + 3) & 1 ? z.y : 0.f;
+                            }
+                            acc[0] = add2(acc[0], y);
+                            acc[1] = add2(acc[1], z);
+                        }
+                    };
+                    const uint32_t base = s_addr + 128 * buf;
+                    if (!masked && rows == 128) {
+                        tc05::ld_32x32b_x32(base, v[0]);
+                        tc05::wait_ld(v[0]);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (c < 3) tc05::ld_32x32b_x32(base + 32 * (c + 1), v[(c + 1) & 1]);
+                            chunk(v[c & 1], c, std::false_type{});
+                            if (c < 3) tc05::wait_ld(v[(c + 1) & 1]);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; 32 * c < cols; ++c) {
+                            tc05::ld_32x32b_x32(base + 32 * c, v[0]);
+                            tc05::wait_ld(v[0]);
+                            chunk(v[0], c, std::true_type{});
+                        }
+                    }
+                    tc05::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * tile + buf));
+                    // the tiles' sums with compensation: up to 2^23 of them
+                    const float y = ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) - comp, sum = total + y;
+                    comp = (sum - total) - y;
+                    total = sum;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S::B_LE + ls));
+            }
+            if (!ok) break;
+            if (active) {
+                bool good = mine;
+                if (good && I.bad) {
+                    const int page = p.block_table[static_cast<long long>(I.b) * p.bt_stride + page_div(key, p.pmagic, p.pmshift)];
+                    good = page >= 0 && page < p.num_pages;
+                }
+                bool whole = true;
+                if (I.nsplit > 1) {
+                    // the unit's parts, joined in order by the warp whose arrival is the last
+                    float* part = p.part_out + static_cast<long long>(I.unit) * p.max_splits * kWtKeys + r;
+                    __stcg(part + I.split * kWtKeys, total);
+                    __syncwarp();
+                    int prev = 0;
+                    if (lane == 0) prev = atom_add_acq_rel_gpu(p.counters + 8 * I.unit + warp);
+                    prev = __shfl_sync(kFull, prev, 0);
+                    whole = prev == I.nsplit - 1;
+                    if (whole) {
+                        total = 0.f;
+                        for (int s = 0; s < I.nsplit; ++s) total += __ldcg(part + s * kWtKeys);
+                        if (lane == 0) p.counters[8 * I.unit + warp] = 0;  // ready for the next call
+                    }
+                }
+                if (whole && mine) {
+                    const long long at = I.b;
+                    float before = 0.f;
+                    if (w.prior && key < I.fresh) before = w.prior[at * w.prior_b + I.hk * w.prior_h + key];
+                    w.weights[at * w.weights_b + I.hk * w.weights_h + key] = fmaf(w.decay, before, good ? total : 0.f);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(S::B_IE + ring));
+        }
+        if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
+    }
+
+    // ---------------------------------------------------------- tear-down
+    tc05::fence_before_sync();
+    __syncthreads();
+    if (warp == 9) {
+        tc05::fence_after_sync();
+        tc05::dealloc(tmem, 512);
+    }
+    // the last CTA to leave resets the item counter for the next call
+    if (tid == 0) {
+        const int prev = atom_add_acq_rel_gpu(p.queue + 1);
+        if (prev == static_cast<int>(gridDim.x) - 1) {
+            p.queue[0] = 0;
+            p.queue[1] = 0;
+        }
+    }
+}
+
+}  // namespace pkd
