@@ -10,8 +10,9 @@
 // product costs 16 KB out of L2.  Sums: fp32 within a tile, the tiles' sums with
 // compensation, in the order of the tokens: no atomics on results.
 //
-// Warp roles (384 threads): warps 0-3 and 4-7 the exponentials of key tile 0 and 1, warp 8
-// loads (items, K, Q), warp 9 issues the products, warp 10 lays out the LSEs.  K and Q
+// Warp roles (640 threads): warps 0-3 and 4-7 the exponentials of key tile 0 and 1 at even
+// steps, 8-11 and 12-15 at odd ones (two S^T buffers a key tile, one for each), warp 16
+// loads (items, K, Q), warp 17 issues the products, warp 18 lays out the LSEs.  K and Q
 // tiles share NU slots: a slot goes to the next tile in the order in which slots become
 // free, which is the same for the warp that fills them and the one that reads them (both
 // keep the queue of free slots), so short items have all slots in flight and long ones
@@ -26,7 +27,7 @@
 
 namespace pkd {
 
-constexpr int kWtKeys = 256, kWtThreads = 384, kWtItems = 4, kWtLse = 4;
+constexpr int kWtKeys = 256, kWtThreads = 640, kWtItems = 4, kWtLse = 4;
 
 struct WtItem {
     int b, hk, t0, nk;            // keys from t0 on, tiles of 128 of them
@@ -43,13 +44,16 @@ struct WtShape {
     static constexpr int UNIT = 128 * ROWB;
     static constexpr int NU = UNIT == 32768 ? 6 : 12;
     static constexpr int OFF_LSE = NU * UNIT;
-    static constexpr int OFF_ITEM = OFF_LSE + kWtLse * 128 * 4;
+    static constexpr int OFF_SUM = OFF_LSE + kWtLse * 128 * 4;  // the odd steps' sums of an item, for the even ones' warps
+    static constexpr int OFF_ITEM = OFF_SUM + kWtKeys * 4;
     static constexpr int OFF_PREF = OFF_ITEM + kWtItems * static_cast<int>(sizeof(WtItem));
     static constexpr int OFF_SCAN = OFF_PREF + (kPtMaxBatch + 4) * 4;
-    static constexpr int OFF_BAR = (OFF_SCAN + 64 + 7) & ~7;
-    // slots full/empty, S full/empty [key tile][buffer], LSEs full/empty, items full/empty, drain
+    static constexpr int OFF_BAR = (OFF_SCAN + 128 + 7) & ~7;
+    // slots full/empty, S full/empty [key tile][buffer], LSEs full/empty, items full/empty,
+    // odd steps' sums full/empty per warp, drain
     static constexpr int B_UF = 0, B_UE = B_UF + NU, B_SF = B_UE + NU, B_SE = B_SF + 4, B_LF = B_SE + 4;
-    static constexpr int B_LE = B_LF + kWtLse, B_IF = B_LE + kWtLse, B_IE = B_IF + kWtItems, B_DR = B_IE + kWtItems;
+    static constexpr int B_LE = B_LF + kWtLse, B_IF = B_LE + kWtLse, B_IE = B_IF + kWtItems, B_XF = B_IE + kWtItems;
+    static constexpr int B_XE = B_XF + 8, B_DR = B_XE + 8;
     static constexpr int NBAR = B_DR + 1;
     static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_TMEM + 16 + 1024;
@@ -74,6 +78,34 @@ struct WtSlots {
         ++n;
     }
 };
+
+// 16 capped logits in log2 units: by the polynomial, or (far) by exponential and reciprocal.
+__device__ __forceinline__ void wt_cap(uint32_t (&v)[16], const AttendParams& p, bool far) {
+    if (far) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) v[c] = __float_as_uint(capped(__uint_as_float(v[c]), p.cap_in, p.cap_log2));
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+        const float2 x = make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), z = mul2(x, x);
+        float2 t = fma2(z, both(p.cap_c[4]), both(p.cap_c[3]));
+        t = fma2(z, t, both(p.cap_c[2]));
+        t = fma2(z, t, both(p.cap_c[1]));
+        t = mul2(fma2(z, t, both(p.cap_c[0])), x);
+        v[c] = __float_as_uint(t.x);
+        v[c + 1] = __float_as_uint(t.y);
+    }
+}
+
+// Wait for this warp's TMEM loads, with the loaded registers passed through.
+__device__ __forceinline__ void wt_wait_ld(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
 
 template <int D, int kType, bool kCap>
 __global__ void __launch_bounds__(kWtThreads, 1)
@@ -110,12 +142,16 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         }
         for (int i = 0; i < kWtItems; ++i) {
             mbar_init(bar(S::B_IF + i), 1);
-            mbar_init(bar(S::B_IE + i), 10);  // the issuing, LSE and eight exponential warps
+            mbar_init(bar(S::B_IE + i), 18);  // the issuing, LSE and sixteen exponential warps
+        }
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(bar(S::B_XF + i), 1);
+            mbar_init(bar(S::B_XE + i), 1);
         }
         mbar_init(bar(S::B_DR), 1);
         fence_barrier_init();
     }
-    if (warp == 9) {
+    if (warp == 17) {
         tc05::alloc(smem_u32(tslot), 512);  // S^T of (key tile, buffer): columns 128 * (2 * tile + buffer)
         tc05::relinquish_alloc_permit();
     }
@@ -147,7 +183,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
     tc05::fence_after_sync();
     const uint32_t tmem = *tslot;
 
-    if (warp == 8) {
+    if (warp == 16) {
         // ---------------------------------------------------------- loads
         if (lane == 0) {
             prefetch_tmap(&kvmap);
@@ -259,14 +295,14 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         for (int s = 0; s < S::NU; ++s)
             if (used >> s & 1) mbar_wait(bar(S::B_UF + s), (phase >> s & 1) ^ 1);
         if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         // ------------------------------------------------------- products
         constexpr uint32_t kId = kFp8 ? tc05::idesc_e4m3(128, 128) : tc05::idesc_f16(kType == kPtBF16, 128, 128, false, false);
         const bool one = tc05::elect_one();
         const uint32_t tm = tc05::uniform(tmem), lo0 = tc05::uniform(tc05::desc_lo(sb0, 16));
         WtSlots slots(S::NU);
-        uint32_t phase = 0;
-        int ns[2] = {0, 0};  // S^T tiles begun
+        uint32_t phase = 0, sphase = 0;  // of the slots, of the S^T buffers
+        int step = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const int ring = it % kWtItems;
@@ -281,7 +317,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             ks[0] = slots.take();
             ks[1] = nk > 1 ? slots.take() : 0;
 #pragma unroll 1
-            for (int j = 0; ok && j < steps; ++j) {
+            for (int j = 0; ok && j < steps; ++j, ++step) {
                 const int s = slots.take();
                 ok = pt_wait(bar(S::B_UF + s), phase >> s & 1, p);
                 phase ^= 1u << s;
@@ -293,10 +329,10 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         ok = pt_wait(bar(S::B_UF + ks[t]), phase >> ks[t] & 1, p);
                         phase ^= 1u << ks[t];
                     }
-                    const int buf = ns[t] & 1;
-                    ok = ok && pt_wait(bar(S::B_SE + 2 * t + buf), ((ns[t] >> 1) & 1) ^ 1, p);
+                    const int buf = step & 1;
+                    ok = ok && pt_wait(bar(S::B_SE + 2 * t + buf), (sphase >> (2 * t + buf) & 1) ^ 1, p);
                     if (!ok) continue;
-                    ++ns[t];
+                    sphase ^= 1u << (2 * t + buf);
                     tc05::fence_after_sync();
                     const uint32_t klo = tc05::uniform(lo0 + (ks[t] * S::UNIT >> 4));
                     const uint32_t d = tm + 128 * (2 * t + buf);
@@ -326,7 +362,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             mbar_wait(bar(S::B_DR), 0);
         }
         __syncwarp();
-    } else if (warp == 10) {
+    } else if (warp == 18) {
         // ------------------------------------- the rows' LSEs, as added to logits
         float* lse2 = reinterpret_cast<float*>(smem + S::OFF_LSE);
         int nl = 0;
@@ -372,13 +408,16 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             }
         }
         if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
-    } else if (warp < 8) {
+    } else if (warp < 16) {
         // --------------------------------------------------- exponentials
-        const int tile = warp >> 2, q4 = warp & 3, r = 128 * tile + 32 * q4 + lane;  // key of the item
+        const int tile = (warp >> 2) & 1, odd = warp >> 3, q4 = warp & 3, pair = warp & 7;
+        const int r = 128 * tile + 32 * q4 + lane;  // key of the item
+        const uint32_t s_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16) + 128 * (2 * tile + odd);
         const float* lse2 = reinterpret_cast<const float*>(smem + S::OFF_LSE);
-        const uint32_t s_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16) + 256 * tile;
-        const int rows = TOK * G;
-        int ns = 0, nl = 0;
+        float* sums = reinterpret_cast<float*>(smem + S::OFF_SUM);
+        const float scale = kCap ? 1.f : p.scale_log2;
+        int step = 0;                 // steps before the item
+        uint32_t sphase = 0, xphase = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const int ring = it % kWtItems;
@@ -386,7 +425,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             const WtItem& I = items[ring];
             if (I.end) break;
             const int steps = I.steps, i0 = I.i0, i1 = I.i1, key = I.t0 + r;
-            const bool mine = key < I.L;
+            const bool mine = key < I.L, active = tile < I.nk;
             // tokens [lo, hi) see this key; every key of the warp is seen by [wlo, whi)
             int lo = i0, hi = i1;
             if (p.causal) lo = max(lo, key - I.off);
@@ -394,40 +433,29 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 hi = static_cast<int>(min(static_cast<long long>(hi), static_cast<long long>(key) - I.off + p.window));
             if (!mine) hi = lo;
             const int wlo = __reduce_max_sync(kFull, mine ? lo : i0), whi = __reduce_min_sync(kFull, mine ? hi : i1);
-            const bool active = tile < I.nk;
             float total = 0.f, comp = 0.f;
 #pragma unroll 1
-            for (int j = 0; j < steps; ++j, ++nl) {
-                const int ls = nl % kWtLse;
-                if (!pt_wait(bar(S::B_LF + ls), (nl / kWtLse) & 1, p)) { ok = false; break; }
+            for (int j = (odd - step) & 1; j < steps; j += 2) {
+                const int ls = (step + j) % kWtLse;
+                if (!pt_wait(bar(S::B_LF + ls), ((step + j) / kWtLse) & 1, p)) { ok = false; break; }
                 if (active) {
-                    const int buf = ns & 1, a = i0 + j * TOK;
-                    if (!pt_wait(bar(S::B_SF + 2 * tile + buf), (ns >> 1) & 1, p)) { ok = false; break; }
-                    ++ns;
+                    const int a = i0 + j * TOK;
+                    if (!pt_wait(bar(S::B_SF + 2 * tile + odd), sphase, p)) { ok = false; break; }
+                    sphase ^= 1;
                     tc05::fence_after_sync();
                     const float* nl2 = lse2 + 128 * ls;
-                    const bool masked = wlo > a || whi < a + TOK;
-                    const int cols = min(TOK, i1 - a) * G;
-                    // columns [c0, c1) of this key
-                    const int c0 = min(max(lo - a, 0), TOK) * G, c1 = min(max(hi - a, 0), TOK) * G;
-                    uint32_t v[2][32];
                     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    auto chunk = [&](uint32_t (&x)[32], int c, auto select) {
+                    // 16 columns; seen: those that count
+                    auto chunk = [&](uint32_t (&x)[16], int c, auto select, unsigned seen) {
                         if constexpr (kCap) {
-                            if (__any_sync(kFull, pt_max<true>(x) > p.cap_far))
-                                pt_cap<false>(x, p);
-                            else
-                                pt_cap<true>(x, p);
-                        }
-                        const float scale = kCap ? 1.f : p.scale_log2;
-                        unsigned seen = 0xffffffffu;
-                        if constexpr (decltype(select)::value) {
-                            const int f = max(c0 - 32 * c, 0), z = min(c1 - 32 * c, 32);
-                            seen = f < z ? (0xffffffffu >> (32 - (z - f))) << f : 0u;
+                            float top = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) top = max3(top, fabsf(__uint_as_float(x[e])), fabsf(__uint_as_float(x[e + 1])));
+                            wt_cap(x, p, __any_sync(kFull, top > p.cap_far));
                         }
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 n = *reinterpret_cast<const float4*>(nl2 + 32 * c + e);
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 n = *reinterpret_cast<const float4*>(nl2 + 16 * c + e);
                             float2 y = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), both(scale), make_float2(n.x, n.y));
                             float2 z = fma2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), both(scale), make_float2(n.z, n.w));
                             y.x = fast_exp2(y.x);
@@ -444,27 +472,32 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                             acc[1] = add2(acc[1], z);
                         }
                     };
-                    const uint32_t base = s_addr + 128 * buf;
-                    if (!masked && rows == 128) {
-                        tc05::ld_32x32b_x32(base, v[0]);
-                        tc05::wait_ld(v[0]);
+                    if (wlo <= a && whi >= a + TOK && TOK * G == 128) {
+                        uint32_t v[2][16];
+                        tc05::ld_32x32b_x16(s_addr, v[0]);
+                        wt_wait_ld(v[0]);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            if (c < 3) tc05::ld_32x32b_x32(base + 32 * (c + 1), v[(c + 1) & 1]);
-                            chunk(v[c & 1], c, std::false_type{});
-                            if (c < 3) tc05::wait_ld(v[(c + 1) & 1]);
+                        for (int c = 0; c < 8; ++c) {
+                            if (c < 7) tc05::ld_32x32b_x16(s_addr + 16 * (c + 1), v[(c + 1) & 1]);
+                            chunk(v[c & 1], c, std::false_type{}, 0u);
+                            if (c < 7) wt_wait_ld(v[(c + 1) & 1]);
                         }
                     } else {
+                        // columns [c0, c1) of this key
+                        const int cols = min(TOK, i1 - a) * G;
+                        const int c0 = min(max(lo - a, 0), TOK) * G, c1 = min(max(hi - a, 0), TOK) * G;
 #pragma unroll 1
-                        for (int c = 0; 32 * c < cols; ++c) {
-                            tc05::ld_32x32b_x32(base + 32 * c, v[0]);
-                            tc05::wait_ld(v[0]);
-                            chunk(v[0], c, std::true_type{});
+                        for (int c = 0; 16 * c < cols; ++c) {
+                            uint32_t v[16];
+                            tc05::ld_32x32b_x16(s_addr + 16 * c, v);
+                            wt_wait_ld(v);
+                            const int f = max(c0 - 16 * c, 0), z = min(c1 - 16 * c, 16);
+                            chunk(v, c, std::true_type{}, f < z ? (0xffffu >> (16 - (z - f))) << f : 0u);
                         }
                     }
                     tc05::fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * tile + buf));
+                    if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * tile + odd));
                     // the tiles' sums with compensation: up to 2^23 of them
                     const float y = ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) - comp, sum = total + y;
                     comp = (sum - total) - y;
@@ -474,7 +507,24 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 if (lane == 0) mbar_arrive(bar(S::B_LE + ls));
             }
             if (!ok) break;
-            if (active) {
+            step += steps;
+            if (active && steps > 1) {
+                // the odd steps' sums go to the even steps' warps
+                if (odd) {
+                    if (!pt_wait(bar(S::B_XE + pair), xphase ^ 1, p)) { ok = false; break; }
+                    sums[r] = total;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(S::B_XF + pair));
+                } else {
+                    if (!pt_wait(bar(S::B_XF + pair), xphase, p)) { ok = false; break; }
+                    total += sums[r];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(S::B_XE + pair));
+                }
+                xphase ^= 1;
+            }
+            // (of a single step: the warps that took it)
+            if (active && (steps > 1 ? !odd : ((odd - step + steps) & 1) == 0)) {
                 bool good = mine;
                 if (good && I.bad) {
                     const int page = p.block_table[static_cast<long long>(I.b) * p.bt_stride + page_div(key, p.pmagic, p.pmshift)];
@@ -487,13 +537,13 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                     __stcg(part + I.split * kWtKeys, total);
                     __syncwarp();
                     int prev = 0;
-                    if (lane == 0) prev = atom_add_acq_rel_gpu(p.counters + 8 * I.unit + warp);
+                    if (lane == 0) prev = atom_add_acq_rel_gpu(p.counters + 8 * I.unit + pair);
                     prev = __shfl_sync(kFull, prev, 0);
                     whole = prev == I.nsplit - 1;
                     if (whole) {
                         total = 0.f;
                         for (int s = 0; s < I.nsplit; ++s) total += __ldcg(part + s * kWtKeys);
-                        if (lane == 0) p.counters[8 * I.unit + warp] = 0;  // ready for the next call
+                        if (lane == 0) p.counters[8 * I.unit + pair] = 0;  // ready for the next call
                     }
                 }
                 if (whole && mine) {
@@ -512,7 +562,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
     // ---------------------------------------------------------- tear-down
     tc05::fence_before_sync();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tc05::fence_after_sync();
         tc05::dealloc(tmem, 512);
     }
