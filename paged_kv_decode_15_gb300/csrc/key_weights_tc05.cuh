@@ -4,15 +4,21 @@
 // query rows that see any of them, in tiles of up to 128 rows (TOK = 128 / G whole tokens,
 // packed token-major as in the attention kernel).  Per query tile and key tile
 //   S^T = K Q^T   tcgen05.mma, M = 128 keys, N = 128 rows, operands K-major as TMA lands them
-//   sum           a thread owns a key (TMEM lane): 2^(scale s - lse) of 128 columns, summed
-//                 in registers.  The rows' LSEs, alike for all keys, come from shared memory
+//   sum           2^(scale s - lse), summed over the columns in registers.  TMEM is read in
+//                 pieces of 16 keys x 32 rows whose lanes hold two of every eight rows, for
+//                 eight keys each: a lane keeps the LSEs of 16 rows, alike for all keys, and
+//                 the quad's sums meet at the item's end.  (With a key per lane every lane
+//                 needed all LSEs: their loads shared the pipe that TMEM's values come by,
+//                 which bound the kernel: 1005 us for 16384 tokens)
 // K stays for the whole item and both key tiles share every query tile, so a 128x128
-// product costs 16 KB out of L2.  Sums: fp32 within a tile, the tiles' sums with
-// compensation, in the order of the tokens: no atomics on results.
+// product costs 16 KB out of L2.  Sums: fp32, of a tile's columns first, in an order fixed by
+// the sizes: no atomics on results.
 //
-// Warp roles (640 threads): warps 0-3 and 4-7 the exponentials of key tile 0 and 1 at even
-// steps, 8-11 and 12-15 at odd ones (two S^T buffers a key tile, one for each), warp 16
-// loads (items, K, Q), warp 17 issues the products, warp 18 lays out the LSEs.  K and Q
+// Warp roles (640 threads): warps 0-3 and 4-7 the exponentials of rows 0-63 and 64-127 at even
+// steps, 8-15 at odd ones (two S^T buffers a key tile, one for each), both key tiles; warp 16
+// loads (items, K, Q), warps 17 and 19 issue the products of key tile 0 and 1 (one warp for
+// both left the tensor cores idle between them: its waits and the issue of a product take
+// as long as the product), warp 18 lays out the LSEs.  K and Q
 // tiles share NU slots: a slot goes to the next tile in the order in which slots become
 // free, which is the same for the warp that fills them and the one that reads them (both
 // keep the queue of free slots), so short items have all slots in flight and long ones
@@ -44,17 +50,17 @@ struct WtShape {
     static constexpr int UNIT = 128 * ROWB;
     static constexpr int NU = UNIT == 32768 ? 6 : 12;
     static constexpr int OFF_LSE = NU * UNIT;
-    static constexpr int OFF_SUM = OFF_LSE + kWtLse * 128 * 4;  // the odd steps' sums of an item, for the even ones' warps
-    static constexpr int OFF_ITEM = OFF_SUM + kWtKeys * 4;
+    static constexpr int OFF_SUM = OFF_LSE + kWtLse * 128 * 4;  // an item's sums of warps 4-15, for warps 0-3
+    static constexpr int OFF_ITEM = OFF_SUM + 3 * kWtKeys * 4;
     static constexpr int OFF_PREF = OFF_ITEM + kWtItems * static_cast<int>(sizeof(WtItem));
     static constexpr int OFF_SCAN = OFF_PREF + (kPtMaxBatch + 4) * 4;
     static constexpr int OFF_BAR = (OFF_SCAN + 128 + 7) & ~7;
     // slots full/empty, S full/empty [key tile][buffer], LSEs full/empty, items full/empty,
-    // odd steps' sums full/empty per warp, drain
+    // sums full/empty per 32 lanes, drain
     static constexpr int B_UF = 0, B_UE = B_UF + NU, B_SF = B_UE + NU, B_SE = B_SF + 4, B_LF = B_SE + 4;
     static constexpr int B_LE = B_LF + kWtLse, B_IF = B_LE + kWtLse, B_IE = B_IF + kWtItems, B_XF = B_IE + kWtItems;
-    static constexpr int B_XE = B_XF + 8, B_DR = B_XE + 8;
-    static constexpr int NBAR = B_DR + 1;
+    static constexpr int B_XE = B_XF + 4, B_DR = B_XE + 4;
+    static constexpr int NBAR = B_DR + 2;
     static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_TMEM + 16 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
@@ -98,6 +104,18 @@ __device__ __forceinline__ void wt_cap(uint32_t (&v)[16], const AttendParams& p,
     }
 }
 
+// 16 lanes x 32 columns of TMEM: lane i gets columns 8 k + 2 (i % 4) and the next of row
+// i / 4 (r[4 k], r[4 k + 1]) and of row i / 4 + 8 (r[4 k + 2], r[4 k + 3]).
+__device__ __forceinline__ void wt_ld(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 // Wait for this warp's TMEM loads, with the loaded registers passed through.
 __device__ __forceinline__ void wt_wait_ld(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -130,11 +148,11 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
     if (tid == 0) {
         for (int i = 0; i < S::NU; ++i) {
             mbar_init(bar(S::B_UF + i), 1);
-            mbar_init(bar(S::B_UE + i), 1);
+            mbar_init(bar(S::B_UE + i), 2);  // both issuing warps
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(S::B_SF + i), 1);
-            mbar_init(bar(S::B_SE + i), 4);
+            mbar_init(bar(S::B_SE + i), 8);
         }
         for (int i = 0; i < kWtLse; ++i) {
             mbar_init(bar(S::B_LF + i), 1);
@@ -142,13 +160,14 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         }
         for (int i = 0; i < kWtItems; ++i) {
             mbar_init(bar(S::B_IF + i), 1);
-            mbar_init(bar(S::B_IE + i), 18);  // the issuing, LSE and sixteen exponential warps
+            mbar_init(bar(S::B_IE + i), 19);  // the issuing, LSE and sixteen exponential warps
         }
-        for (int i = 0; i < 8; ++i) {
-            mbar_init(bar(S::B_XF + i), 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(S::B_XF + i), 3);
             mbar_init(bar(S::B_XE + i), 1);
         }
         mbar_init(bar(S::B_DR), 1);
+        mbar_init(bar(S::B_DR + 1), 1);
         fence_barrier_init();
     }
     if (warp == 17) {
@@ -295,11 +314,12 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         for (int s = 0; s < S::NU; ++s)
             if (used >> s & 1) mbar_wait(bar(S::B_UF + s), (phase >> s & 1) ^ 1);
         if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
-    } else if (warp == 17) {
-        // ------------------------------------------------------- products
+    } else if (warp == 17 || warp == 19) {
+        // ------------------------------------------- products of key tile t
         constexpr uint32_t kId = kFp8 ? tc05::idesc_e4m3(128, 128) : tc05::idesc_f16(kType == kPtBF16, 128, 128, false, false);
+        const int t = (warp - 17) >> 1;
         const bool one = tc05::elect_one();
-        const uint32_t tm = tc05::uniform(tmem), lo0 = tc05::uniform(tc05::desc_lo(sb0, 16));
+        const uint32_t tm = tc05::uniform(tmem + 256 * t), lo0 = tc05::uniform(tc05::desc_lo(sb0, 16));
         WtSlots slots(S::NU);
         uint32_t phase = 0, sphase = 0;  // of the slots, of the S^T buffers
         int step = 0;
@@ -313,29 +333,27 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(S::B_IE + ring));
             if (!steps) continue;
-            int ks[2];
-            ks[0] = slots.take();
-            ks[1] = nk > 1 ? slots.take() : 0;
+            const int k0 = slots.take(), k1 = nk > 1 ? slots.take() : -1;
+            const int mine = t == 0 ? k0 : k1;
+            uint32_t klo = 0;
+            if (mine >= 0) {
+                ok = pt_wait(bar(S::B_UF + mine), phase >> mine & 1, p);
+                klo = tc05::uniform(lo0 + (mine * S::UNIT >> 4));
+            }
+            phase ^= 1u << k0;
+            if (k1 >= 0) phase ^= 1u << k1;
 #pragma unroll 1
             for (int j = 0; ok && j < steps; ++j, ++step) {
-                const int s = slots.take();
-                ok = pt_wait(bar(S::B_UF + s), phase >> s & 1, p);
+                const int s = slots.take(), buf = step & 1;
+                // (a warp without a key tile keeps step with the other)
+                ok = (mine < 0 || pt_wait(bar(S::B_SE + 2 * t + buf), (sphase >> buf & 1) ^ 1, p)) &&
+                     pt_wait(bar(S::B_UF + s), phase >> s & 1, p);
+                if (!ok) break;
                 phase ^= 1u << s;
-                const uint32_t qlo = tc05::uniform(lo0 + (s * S::UNIT >> 4));
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (t >= nk || !ok) continue;
-                    if (j == 0) {
-                        ok = pt_wait(bar(S::B_UF + ks[t]), phase >> ks[t] & 1, p);
-                        phase ^= 1u << ks[t];
-                    }
-                    const int buf = step & 1;
-                    ok = ok && pt_wait(bar(S::B_SE + 2 * t + buf), (sphase >> (2 * t + buf) & 1) ^ 1, p);
-                    if (!ok) continue;
-                    sphase ^= 1u << (2 * t + buf);
+                if (mine >= 0) {
+                    sphase ^= 1u << buf;
                     tc05::fence_after_sync();
-                    const uint32_t klo = tc05::uniform(lo0 + (ks[t] * S::UNIT >> 4));
-                    const uint32_t d = tm + 128 * (2 * t + buf);
+                    const uint32_t qlo = tc05::uniform(lo0 + (s * S::UNIT >> 4)), d = tm + 128 * buf;
 #pragma unroll
                     for (int kk = 0; kk < S::ROWB / 32; ++kk)
                         if (one)
@@ -344,22 +362,21 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                                                kk > 0);
                     if (one) tc05::commit(bar(S::B_SF + 2 * t + buf));
                 }
-                if (!ok) break;
                 if (one) tc05::commit(bar(S::B_UE + s));
                 slots.give(s);
             }
             if (ok && one) {
-                tc05::commit(bar(S::B_UE + ks[0]));
-                if (nk > 1) tc05::commit(bar(S::B_UE + ks[1]));
+                tc05::commit(bar(S::B_UE + k0));
+                if (k1 >= 0) tc05::commit(bar(S::B_UE + k1));
             }
-            slots.give(ks[0]);
-            if (nk > 1) slots.give(ks[1]);
+            slots.give(k0);
+            if (k1 >= 0) slots.give(k1);
         }
         if (!ok && one) atomicOr(p.status, kErrTimeout);
         // every product issued has completed before TMEM is freed
         if (one) {
-            tc05::commit(bar(S::B_DR));
-            mbar_wait(bar(S::B_DR), 0);
+            tc05::commit(bar(S::B_DR + t));
+            mbar_wait(bar(S::B_DR + t), 0);
         }
         __syncwarp();
     } else if (warp == 18) {
@@ -410,12 +427,12 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
     } else if (warp < 16) {
         // --------------------------------------------------- exponentials
-        const int tile = (warp >> 2) & 1, odd = warp >> 3, q4 = warp & 3, pair = warp & 7;
-        const int r = 128 * tile + 32 * q4 + lane;  // key of the item
-        const uint32_t s_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16) + 128 * (2 * tile + odd);
-        const float* lse2 = reinterpret_cast<const float*>(smem + S::OFF_LSE);
-        float* sums = reinterpret_cast<float*>(smem + S::OFF_SUM);
+        const int odd = warp >> 3, half = (warp >> 2) & 1, q4 = warp & 3, part = warp >> 2, g = lane >> 2, c4 = lane & 3;
+        const uint32_t s_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16) + 128 * odd + 64 * half;
+        const float* lse2 = reinterpret_cast<const float*>(smem + S::OFF_LSE) + 64 * half + 2 * c4;
+        float* sums = reinterpret_cast<float*>(smem + S::OFF_SUM) + 64 * q4;  // [part - 1][4][64 keys]
         const float scale = kCap ? 1.f : p.scale_log2;
+        const int rows = TOK * G;
         int step = 0;                 // steps before the item
         uint32_t sphase = 0, xphase = 0;
         bool ok = true;
@@ -424,133 +441,177 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             if (!pt_wait(bar(S::B_IF + ring), (it / kWtItems) & 1, p)) { ok = false; break; }
             const WtItem& I = items[ring];
             if (I.end) break;
-            const int steps = I.steps, i0 = I.i0, i1 = I.i1, key = I.t0 + r;
-            const bool mine = key < I.L, active = tile < I.nk;
-            // tokens [lo, hi) see this key; every key of the warp is seen by [wlo, whi)
-            int lo = i0, hi = i1;
-            if (p.causal) lo = max(lo, key - I.off);
-            if (p.window > 0)
-                hi = static_cast<int>(min(static_cast<long long>(hi), static_cast<long long>(key) - I.off + p.window));
-            if (!mine) hi = lo;
-            const int wlo = __reduce_max_sync(kFull, mine ? lo : i0), whi = __reduce_min_sync(kFull, mine ? hi : i1);
-            float total = 0.f, comp = 0.f;
+            const int steps = I.steps, i0 = I.i0, i1 = I.i1, nk = I.nk, L = I.L, off = I.off;
+            const int k0 = I.t0 + 32 * q4;  // first key of the warp (of key tile 0)
+            // tokens [lo, hi) see a key
+            auto lo_of = [&](int key) { return p.causal ? max(i0, key - off) : i0; };
+            auto hi_of = [&](int key) {
+                return p.window > 0 ? static_cast<int>(min(static_cast<long long>(i1), static_cast<long long>(key) - off + p.window)) : i1;
+            };
+            // every key of the warp's 32 of a tile is seen by [wlo, whi)
+            int wlo[2], whi[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int first = k0 + 128 * t, last = min(first + 31, L - 1);
+                wlo[t] = lo_of(last);
+                whi[t] = hi_of(min(first, L - 1));
+            }
+            float total[2][2][2] = {};  // of key tile, 16 keys, 8 keys
 #pragma unroll 1
             for (int j = (odd - step) & 1; j < steps; j += 2) {
-                const int ls = (step + j) % kWtLse;
+                const int ls = (step + j) % kWtLse, a = i0 + j * TOK;
                 if (!pt_wait(bar(S::B_LF + ls), ((step + j) / kWtLse) & 1, p)) { ok = false; break; }
-                if (active) {
-                    const int a = i0 + j * TOK;
-                    if (!pt_wait(bar(S::B_SF + 2 * tile + odd), sphase, p)) { ok = false; break; }
-                    sphase ^= 1;
+                float2 n[8];  // LSEs of rows 8 k + 2 c4 and the next
+#pragma unroll
+                for (int k = 0; k < 8; ++k) n[k] = *reinterpret_cast<const float2*>(lse2 + 128 * ls + 8 * k);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S::B_LE + ls));
+                const int cols = min(TOK, i1 - a) * G - 64 * half;  // of this warp's
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t >= nk || !ok) continue;
+                    ok = pt_wait(bar(S::B_SF + 2 * t + odd), sphase >> t & 1, p);
+                    if (!ok) continue;
+                    sphase ^= 1u << t;
                     tc05::fence_after_sync();
-                    const float* nl2 = lse2 + 128 * ls;
-                    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    // 16 columns; seen: those that count
-                    auto chunk = [&](uint32_t (&x)[16], int c, auto select, unsigned seen) {
+                    const uint32_t base = s_addr + 256 * t;
+                    float2 acc[2][2] = {};  // of 16 keys, 8 keys
+                    auto piece = [&](uint32_t (&x)[16], int hl, int cc, auto select) {
                         if constexpr (kCap) {
                             float top = 0.f;
 #pragma unroll
                             for (int e = 0; e < 16; e += 2) top = max3(top, fabsf(__uint_as_float(x[e])), fabsf(__uint_as_float(x[e + 1])));
                             wt_cap(x, p, __any_sync(kFull, top > p.cap_far));
                         }
+                        // columns [c0, c1) of this warp's that see the lane's two keys
+                        int c0[2] = {0, 0}, c1[2] = {0, 0};
+                        if constexpr (decltype(select)::value) {
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float4 n = *reinterpret_cast<const float4*>(nl2 + 16 * c + e);
-                            float2 y = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), both(scale), make_float2(n.x, n.y));
-                            float2 z = fma2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), both(scale), make_float2(n.z, n.w));
-                            y.x = fast_exp2(y.x);
-                            y.y = fast_exp2(y.y);
-                            z.x = fast_exp2(z.x);
-                            z.y = fast_exp2(z.y);
-                            if constexpr (decltype(select)::value) {
-                                y.x = seen >> e & 1 ? y.x : 0.f;
-                                y.y = seen >> (e + 1) & 1 ? y.y : 0.f;
-                                z.x = seen >> (e + 2) & 1 ? z.x : 0.f;
-                                z.y = seen >> (e + 3) & 1 ? z.y : 0.f;
+                            for (int r = 0; r < 2; ++r) {
+                                const int key = k0 + 128 * t + 16 * hl + 8 * r + g;
+                                c0[r] = min(max(lo_of(key) - a, 0), TOK) * G - 64 * half;
+                                c1[r] = key < L ? min(max(hi_of(key) - a, 0), TOK) * G - 64 * half : c0[r];
                             }
-                            acc[0] = add2(acc[0], y);
-                            acc[1] = add2(acc[1], z);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                float2 y = fma2(make_float2(__uint_as_float(x[4 * k + 2 * r]), __uint_as_float(x[4 * k + 2 * r + 1])),
+                                                both(scale), n[4 * cc + k]);
+                                y.x = fast_exp2(y.x);
+                                y.y = fast_exp2(y.y);
+                                if constexpr (decltype(select)::value) {
+                                    const int c = 32 * cc + 8 * k + 2 * c4;
+                                    y.x = c >= c0[r] && c < c1[r] ? y.x : 0.f;
+                                    y.y = c + 1 >= c0[r] && c + 1 < c1[r] ? y.y : 0.f;
+                                }
+                                acc[hl][r] = add2(acc[hl][r], y);
+                            }
                         }
                     };
-                    if (wlo <= a && whi >= a + TOK && TOK * G == 128) {
+                    if (wlo[t] <= a && whi[t] >= a + TOK && rows == 128) {
                         uint32_t v[2][16];
-                        tc05::ld_32x32b_x16(s_addr, v[0]);
+                        wt_ld(base, v[0]);
                         wt_wait_ld(v[0]);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            if (c < 7) tc05::ld_32x32b_x16(s_addr + 16 * (c + 1), v[(c + 1) & 1]);
-                            chunk(v[c & 1], c, std::false_type{}, 0u);
-                            if (c < 7) wt_wait_ld(v[(c + 1) & 1]);
+                        for (int u = 0; u < 4; ++u) {
+                            if (u < 3) wt_ld(base + (static_cast<uint32_t>(16 * ((u + 1) >> 1)) << 16) + 32 * ((u + 1) & 1), v[(u + 1) & 1]);
+                            piece(v[u & 1], u >> 1, u & 1, std::false_type{});
+                            if (u < 3) wt_wait_ld(v[(u + 1) & 1]);
                         }
                     } else {
-                        // columns [c0, c1) of this key
-                        const int cols = min(TOK, i1 - a) * G;
-                        const int c0 = min(max(lo - a, 0), TOK) * G, c1 = min(max(hi - a, 0), TOK) * G;
-#pragma unroll 1
-                        for (int c = 0; 16 * c < cols; ++c) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            if (32 * (u & 1) >= cols) continue;
                             uint32_t v[16];
-                            tc05::ld_32x32b_x16(s_addr + 16 * c, v);
+                            wt_ld(base + (static_cast<uint32_t>(16 * (u >> 1)) << 16) + 32 * (u & 1), v);
                             wt_wait_ld(v);
-                            const int f = max(c0 - 16 * c, 0), z = min(c1 - 16 * c, 16);
-                            chunk(v, c, std::true_type{}, f < z ? (0xffffu >> (16 - (z - f))) << f : 0u);
+                            piece(v, u >> 1, u & 1, std::true_type{});
                         }
                     }
                     tc05::fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * tile + odd));
-                    // the tiles' sums with compensation: up to 2^23 of them
-                    const float y = ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) - comp, sum = total + y;
-                    comp = (sum - total) - y;
-                    total = sum;
+                    if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * t + odd));
+#pragma unroll
+                    for (int hl = 0; hl < 2; ++hl)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) total[t][hl][r] += acc[hl][r].x + acc[hl][r].y;
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(S::B_LE + ls));
+                if (!ok) break;
             }
             if (!ok) break;
             step += steps;
-            if (active && steps > 1) {
-                // the odd steps' sums go to the even steps' warps
-                if (odd) {
-                    if (!pt_wait(bar(S::B_XE + pair), xphase ^ 1, p)) { ok = false; break; }
-                    sums[r] = total;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(S::B_XF + pair));
-                } else {
-                    if (!pt_wait(bar(S::B_XF + pair), xphase, p)) { ok = false; break; }
-                    total += sums[r];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(S::B_XE + pair));
-                }
-                xphase ^= 1;
+            // lane (g, c4) of the quad's sums keeps those of keys 8 c4 + g of its 32
+            float mine[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int hl = 0; hl < 2; ++hl)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float& x = total[t][hl][r];
+                        x += __shfl_xor_sync(kFull, x, 1);
+                        x += __shfl_xor_sync(kFull, x, 2);
+                    }
+                mine[t] = c4 == 0 ? total[t][0][0] : c4 == 1 ? total[t][0][1] : c4 == 2 ? total[t][1][0] : total[t][1][1];
             }
-            // (of a single step: the warps that took it)
-            if (active && (steps > 1 ? !odd : ((odd - step + steps) & 1) == 0)) {
-                bool good = mine;
-                if (good && I.bad) {
-                    const int page = p.block_table[static_cast<long long>(I.b) * p.bt_stride + page_div(key, p.pmagic, p.pmshift)];
-                    good = page >= 0 && page < p.num_pages;
+            const int r = 8 * c4 + g;
+            if (part) {
+                if (steps) {
+                    if (!pt_wait(bar(S::B_XE + q4), xphase ^ 1, p)) { ok = false; break; }
+                    sums[(part - 1) * kWtKeys + r] = mine[0];
+                    sums[(part - 1) * kWtKeys + 32 + r] = mine[1];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(S::B_XF + q4));
+                    xphase ^= 1;
+                }
+            } else {
+                if (steps) {
+                    if (!pt_wait(bar(S::B_XF + q4), xphase, p)) { ok = false; break; }
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) {
+                        mine[0] += sums[e * kWtKeys + r];
+                        mine[1] += sums[e * kWtKeys + 32 + r];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(S::B_XE + q4));
+                    xphase ^= 1;
                 }
                 bool whole = true;
                 if (I.nsplit > 1) {
                     // the unit's parts, joined in order by the warp whose arrival is the last
-                    float* part = p.part_out + static_cast<long long>(I.unit) * p.max_splits * kWtKeys + r;
-                    __stcg(part + I.split * kWtKeys, total);
+                    float* dst = p.part_out + static_cast<long long>(I.unit) * p.max_splits * kWtKeys + 32 * q4 + r;
+                    __stcg(dst + I.split * kWtKeys, mine[0]);
+                    __stcg(dst + I.split * kWtKeys + 128, mine[1]);
                     __syncwarp();
                     int prev = 0;
-                    if (lane == 0) prev = atom_add_acq_rel_gpu(p.counters + 8 * I.unit + pair);
+                    if (lane == 0) prev = atom_add_acq_rel_gpu(p.counters + 4 * I.unit + q4);
                     prev = __shfl_sync(kFull, prev, 0);
                     whole = prev == I.nsplit - 1;
                     if (whole) {
-                        total = 0.f;
-                        for (int s = 0; s < I.nsplit; ++s) total += __ldcg(part + s * kWtKeys);
-                        if (lane == 0) p.counters[8 * I.unit + pair] = 0;  // ready for the next call
+                        mine[0] = mine[1] = 0.f;
+                        for (int s = 0; s < I.nsplit; ++s) {
+                            mine[0] += __ldcg(dst + s * kWtKeys);
+                            mine[1] += __ldcg(dst + s * kWtKeys + 128);
+                        }
+                        if (lane == 0) p.counters[4 * I.unit + q4] = 0;  // ready for the next call
                     }
                 }
-                if (whole && mine) {
-                    const long long at = I.b;
-                    float before = 0.f;
-                    if (w.prior && key < I.fresh) before = w.prior[at * w.prior_b + I.hk * w.prior_h + key];
-                    w.weights[at * w.weights_b + I.hk * w.weights_h + key] = fmaf(w.decay, before, good ? total : 0.f);
+                if (whole) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int key = k0 + 128 * t + r;
+                        if (key >= L) continue;
+                        float x = mine[t];
+                        if (I.bad) {
+                            const int page = p.block_table[static_cast<long long>(I.b) * p.bt_stride + page_div(key, p.pmagic, p.pmshift)];
+                            if (page < 0 || page >= p.num_pages) x = 0.f;
+                        }
+                        float before = 0.f;
+                        if (w.prior && key < I.fresh) before = w.prior[I.b * w.prior_b + I.hk * w.prior_h + key];
+                        w.weights[I.b * w.weights_b + I.hk * w.weights_h + key] = fmaf(w.decay, before, x);
+                    }
                 }
             }
             __syncwarp();
