@@ -183,7 +183,9 @@ struct WeighPlan {
     int chunk;          // step: keys of a CTA; else tokens of a part
     int chunks;         // step: CTAs along a request's keys
     int max_splits;     // parts of a key block's tokens
-    long long units;    // key blocks of all kv heads, at most
+    long long units;    // (runs of) key blocks of all kv heads, at most
+    int run;            // key blocks of an item
+    bool stay;          // query tiles stay in shared memory
     size_t bytes;       // the parts' sums
 };
 
@@ -208,9 +210,20 @@ pkd_status plan_key_weights(int B, long long T, int max_q, int last, int Hq, int
     }
     const long long tok = pkd::kPtRows / (Hq / Hkv), tiles = (tokens + tok - 1) / tok;
     pl.units = (long long)B * Hkv * ((max_kv_len + pkd::kWtKeys - 1) / pkd::kWtKeys);
-    // the tokens are split while the key blocks alone leave SMs idle: about four items per
-    // SM, of four query tiles at least
-    const long long splits = pl.units ? std::min((4 * kSms + pl.units - 1) / pl.units, (tiles + 3) / 4) : 1;
+    // the tokens are split while the key blocks alone leave SMs idle: into sixteen items per
+    // SM (a CTA takes its next item one ahead: four per SM 975 us for 16384 tokens, sixteen
+    // 944), of four query tiles at least
+    pl.run = 1;
+    pl.stay = tiles <= pkd::kWtStay;
+    if (pl.stay) {
+        // runs of key blocks, as many as SMs where the one length is known, else four per SM
+        const long long blocks = (max_kv_len + pkd::kWtKeys - 1) / pkd::kWtKeys, items = B == 1 ? kSms : 4 * kSms;
+        pl.run = (int)std::max(1ll, (pl.units + items - 1) / items);
+        pl.units = (long long)B * Hkv * ((blocks + pl.run - 1) / pl.run);
+        pl.chunk = (int)tokens;
+        return pl.units >= 1ll << 31 ? report(PKD_EUNSUPPORTED, "too many work items") : PKD_OK;
+    }
+    const long long splits = pl.units ? std::min((16 * kSms + pl.units - 1) / pl.units, (tiles + 3) / 4) : 1;
     const long long part = (tiles + splits - 1) / splits * tok;
     pl.chunk = (int)std::min<long long>(part, 0x7fffffff);
     pl.max_splits = (int)((tokens + pl.chunk - 1) / pl.chunk);
@@ -744,6 +757,8 @@ pkd_status pkd_key_weights(const void* q, pkd_dtype q_dtype, int64_t q_stride, c
     w.weights_h = weights_head_stride;
     w.decay = decay;
     w.last = last_queries;
+    w.run = pl.run;
+    w.stay = pl.stay;
     cudaError_t e;
     if (pl.step) {
         e = pkd::launch_key_weights(head_dim, (int)kv_dtype, pl.rows, w, dim3(pl.chunks, num_kv_heads, batch),

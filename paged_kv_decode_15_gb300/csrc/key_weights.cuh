@@ -22,6 +22,7 @@ struct WeighParams {
     long long prior_b, prior_h, weights_b, weights_h;
     float decay;
     int last;                     // the last tokens of each request that weigh (0: all)
+    int run, stay;                // tcgen05 kernel: key blocks of an item; query tiles stay for all of them
 };
 
 // The weighing tokens of a request: token i of m is row first + i of q, at position

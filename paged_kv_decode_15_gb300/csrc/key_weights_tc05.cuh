@@ -6,7 +6,7 @@
 //   S^T = K Q^T   tcgen05.mma, M = 128 keys, N = 128 rows, operands K-major as TMA lands them
 //   sum           2^(scale s - lse), summed over the columns in registers.  TMEM is read in
 //                 pieces of 16 keys x 32 rows whose lanes hold two of every eight rows, for
-//                 eight keys each: a lane keeps the LSEs of 16 rows, alike for all keys, and
+//                 two keys each: a lane keeps the LSEs of 32 rows, alike for all keys, and
 //                 the quad's sums meet at the item's end.  (With a key per lane every lane
 //                 needed all LSEs: their loads shared the pipe that TMEM's values come by,
 //                 which bound the kernel: 1005 us for 16384 tokens)
@@ -14,8 +14,8 @@
 // product costs 16 KB out of L2.  Sums: fp32, of a tile's columns first, in an order fixed by
 // the sizes: no atomics on results.
 //
-// Warp roles (640 threads): warps 0-3 and 4-7 the exponentials of rows 0-63 and 64-127 at even
-// steps, 8-15 at odd ones (two S^T buffers a key tile, one for each), both key tiles; warp 16
+// Warp roles (640 threads): warps 0-3 and 4-7 the exponentials of key tile 0 and 1 at even
+// steps, 8-15 at odd ones (two S^T buffers a key tile, one for each); warp 16
 // loads (items, K, Q), warps 17 and 19 issue the products of key tile 0 and 1 (one warp for
 // both left the tensor cores idle between them: its waits and the issue of a product take
 // as long as the product), warp 18 lays out the LSEs.  K and Q
@@ -24,8 +24,11 @@
 // keep the queue of free slots), so short items have all slots in flight and long ones
 // NU - 2 query tiles.  Every wait is bounded.
 //
-// A request's query rows are split between items (`span` tokens each) where its key blocks
-// alone leave SMs idle; the sums of the parts are joined in order by the last to arrive.
+// Few query tiles (two at most) stay in their slots instead, and an item is a run of key
+// blocks that stream past them: bound by reading K then (the last 64 of 32768 tokens, four
+// heads to a kv head: 34 us with items of one block).
+// A request's query rows are split between items where its key blocks alone leave SMs
+// idle; the sums of the parts are joined in order by the last to arrive.
 #pragma once
 
 #include "attend_prompt.cuh"
@@ -35,12 +38,14 @@ namespace pkd {
 
 constexpr int kWtKeys = 256, kWtThreads = 640, kWtItems = 4, kWtLse = 4;
 
+constexpr int kWtStay = 2;        // query tiles that stay in their slots
+
 struct WtItem {
-    int b, hk, t0, nk;            // keys from t0 on, tiles of 128 of them
+    int b, hk, t0, blocks;        // key blocks from key t0 on
     int first, L, fresh, off;     // row of the first weighing token, whose position is off
-    int i0, i1, steps;            // weighing tokens [i0, i1), in tiles of TOK
+    int i0, i1, steps, stay;      // weighing tokens [i0, i1), in tiles of TOK; stay: in their slots for all blocks
     int split, nsplit, unit;      // parts of the unit that hold any
-    int bad, end;
+    int end;
 };
 
 template <int D, int kType>
@@ -50,16 +55,16 @@ struct WtShape {
     static constexpr int UNIT = 128 * ROWB;
     static constexpr int NU = UNIT == 32768 ? 6 : 12;
     static constexpr int OFF_LSE = NU * UNIT;
-    static constexpr int OFF_SUM = OFF_LSE + kWtLse * 128 * 4;  // an item's sums of warps 4-15, for warps 0-3
-    static constexpr int OFF_ITEM = OFF_SUM + 3 * kWtKeys * 4;
+    static constexpr int OFF_SUM = OFF_LSE + kWtLse * 128 * 4;  // an item's sums of odd steps, for the warps of even ones
+    static constexpr int OFF_ITEM = OFF_SUM + kWtKeys * 4;
     static constexpr int OFF_PREF = OFF_ITEM + kWtItems * static_cast<int>(sizeof(WtItem));
     static constexpr int OFF_SCAN = OFF_PREF + (kPtMaxBatch + 4) * 4;
     static constexpr int OFF_BAR = (OFF_SCAN + 128 + 7) & ~7;
     // slots full/empty, S full/empty [key tile][buffer], LSEs full/empty, items full/empty,
-    // sums full/empty per 32 lanes, drain
+    // sums full/empty per 32 keys, drain
     static constexpr int B_UF = 0, B_UE = B_UF + NU, B_SF = B_UE + NU, B_SE = B_SF + 4, B_LF = B_SE + 4;
     static constexpr int B_LE = B_LF + kWtLse, B_IF = B_LE + kWtLse, B_IE = B_IF + kWtItems, B_XF = B_IE + kWtItems;
-    static constexpr int B_XE = B_XF + 4, B_DR = B_XE + 4;
+    static constexpr int B_XE = B_XF + 8, B_DR = B_XE + 8;
     static constexpr int NBAR = B_DR + 2;
     static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_TMEM + 16 + 1024;
@@ -67,6 +72,22 @@ struct WtShape {
     static_assert(SMEM > 114 * 1024, "one CTA per SM: all 512 TMEM columns are its own");
     static_assert(NU <= 15, "the queue of free slots holds 16 of four bits");
 };
+
+// Block k of an item: its first key, key tiles, and query tiles (none where no token sees a key).
+struct WtBlock {
+    int t0, nk, steps;
+};
+__device__ __forceinline__ WtBlock wt_block(const AttendParams& p, const WtItem& I, int k) {
+    WtBlock x;
+    x.t0 = I.t0 + k * kWtKeys;
+    const int t1 = min(x.t0 + kWtKeys, I.L);
+    x.nk = t1 - x.t0 > 128 ? 2 : 1;
+    x.steps = I.steps;
+    if (I.stay && ((p.causal && x.t0 - I.off >= I.i1) ||
+                   (p.window > 0 && static_cast<long long>(t1 - 1) - I.off + p.window <= I.i0)))
+        x.steps = 0;
+    return x;
+}
 
 // The queue of free slots, four bits each, the next one lowest.
 struct WtSlots {
@@ -152,7 +173,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(S::B_SF + i), 1);
-            mbar_init(bar(S::B_SE + i), 8);
+            mbar_init(bar(S::B_SE + i), 4);
         }
         for (int i = 0; i < kWtLse; ++i) {
             mbar_init(bar(S::B_LF + i), 1);
@@ -162,8 +183,8 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             mbar_init(bar(S::B_IF + i), 1);
             mbar_init(bar(S::B_IE + i), 19);  // the issuing, LSE and sixteen exponential warps
         }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(bar(S::B_XF + i), 3);
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(bar(S::B_XF + i), 1);
             mbar_init(bar(S::B_XE + i), 1);
         }
         mbar_init(bar(S::B_DR), 1);
@@ -174,12 +195,13 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         tc05::alloc(smem_u32(tslot), 512);  // S^T of (key tile, buffer): columns 128 * (2 * tile + buffer)
         tc05::relinquish_alloc_permit();
     }
-    // prefix of the requests' key blocks (units of one kv head)
+    // prefix of the requests' runs of key blocks (units of one kv head)
     {
         int run = 0;
         for (int b0 = 0; b0 < p.B; b0 += kWtThreads) {
             const int b = b0 + tid;
             int v = b < p.B ? (request_len(p, b, blockIdx.x == 0) + kWtKeys - 1) / kWtKeys : 0;
+            v = (v + w.run - 1) / w.run;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(kFull, v, o);
@@ -240,16 +262,15 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             // first (causal: seen by the most tokens)
             const int split = idx % p.max_splits, u = idx / p.max_splits;
             const int b = pt_request(pref, p.B, p.Hkv, u), r = u - pref[b] * p.Hkv;
-            const int hk = r % p.Hkv, t0 = r / p.Hkv * kWtKeys;
+            const int hk = r % p.Hkv, t0 = r / p.Hkv * w.run * kWtKeys;
             const WeighRequest q = weigh_request(w, b, r == 0 && split == 0 && lane == 0);
-            const int t1 = min(t0 + kWtKeys, q.L), off = q.L - q.m, nk = t1 - t0 > 128 ? 2 : 1;
+            const int t1 = min(t0 + w.run * kWtKeys, q.L), off = q.L - q.m;
             // tokens that see any of the keys: from the first key's position on, up to a
             // window behind the last key
-            int i0 = p.causal ? max(0, t0 - off) : 0, i1 = q.m;
+            int i0 = p.causal ? max(0, t0 - off) : 0, i1 = q.m, nsplit = 0;
             if (p.window > 0) i1 = static_cast<int>(min(static_cast<long long>(q.m), static_cast<long long>(t1 - 1) - off + p.window));
-            int nsplit = 0;
             if (i0 < i1) {
-                // parts begin at multiples of span behind i0
+                // parts begin at multiples of their size behind i0
                 nsplit = min((i1 - i0 + p.chunk - 1) / p.chunk, p.max_splits);
                 i0 += split * p.chunk;
                 if (split + 1 < nsplit) i1 = min(i1, i0 + p.chunk);
@@ -258,56 +279,82 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 idx = __shfl_sync(kFull, next, 0);
                 continue;
             }
-            const int steps = nsplit ? (i1 - i0 + TOK - 1) / TOK : 0;
-            // the pages of the 16-key stages, a lane each
-            const int t = t0 + kStageTok * lane;
-            int krow = -1;
-            bool bad = false;
-            if (lane < kWtKeys / kStageTok && t < t1) {
-                const int col = page_div(t, p.pmagic, p.pmshift);
-                const int page = p.block_table[static_cast<long long>(b) * p.bt_stride + col];
-                bad = page < 0 || page >= p.num_pages;
-                if (!bad) krow = (page * p.Hkv + hk) * p.P + (t - col * p.P);
-            }
-            bad = __any_sync(kFull, bad);
+            WtItem I;
+            I.b = b; I.hk = hk; I.t0 = t0; I.blocks = (t1 - t0 + kWtKeys - 1) / kWtKeys;
+            I.first = q.first; I.L = q.L; I.fresh = q.fresh; I.off = off;
+            I.i0 = i0; I.i1 = i1; I.steps = nsplit ? (i1 - i0 + TOK - 1) / TOK : 0; I.stay = w.stay;
+            I.split = split; I.nsplit = nsplit; I.unit = u; I.end = 0;
             if (lane == 0) {
-                if (bad) atomicOr(p.status, kErrBounds);
-                WtItem& I = items[ring];
-                I.b = b; I.hk = hk; I.t0 = t0; I.nk = nk; I.first = q.first; I.L = q.L; I.fresh = q.fresh; I.off = off;
-                I.i0 = i0; I.i1 = i1; I.steps = steps; I.split = split; I.nsplit = nsplit; I.unit = u; I.bad = bad; I.end = 0;
+                items[ring] = I;
                 mbar_arrive(bar(S::B_IF + ring));
             }
             __syncwarp();
             ++npub;
-            if (steps) {
-                int ks[2] = {0, 0};
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (e >= nk || !ok) continue;
-                    ks[e] = take();
-                    if (!ok) continue;
-                    const bool load = krow >= 0 && (lane >> 3) == e;
-                    const int bytes = __popc(__ballot_sync(kFull, load)) * 2 * S::GROUP;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(S::B_UF + ks[e]), bytes);
-                    __syncwarp();
-                    if (load)
-                        tma_load_4d(sb0 + ks[e] * S::UNIT + 2 * (lane & 7) * S::GROUP, &kvmap, 0, 0, 0, krow >> 3,
-                                    bar(S::B_UF + ks[e]), pol);
+            // the cache row of a block's 16-key stage, a lane each; -1: no key, or none in the pool
+            auto stage_row = [&](int k) {
+                const int t = t0 + k * kWtKeys + kStageTok * lane;
+                if (k >= I.blocks || lane >= kWtKeys / kStageTok || t >= t1) return -1;
+                const int col = page_div(t, p.pmagic, p.pmshift);
+                const int page = p.block_table[static_cast<long long>(b) * p.bt_stride + col];
+                if (page < 0 || page >= p.num_pages) {
+                    atomicOr(p.status, kErrBounds);
+                    return -1;
                 }
+                return (page * p.Hkv + hk) * p.P + (t - col * p.P);
+            };
+            int krow = stage_row(0), qs[kWtStay] = {0, 0};
+            bool have = false;
 #pragma unroll 1
-                for (int j = 0; ok && j < steps; ++j) {
-                    const int s = take();
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(S::B_UF + s), S::REGIONS * TOK * G * 128);
-                    __syncwarp();
-                    if (lane < S::REGIONS)
-                        tma_load_3d(sb0 + s * S::UNIT + lane * kPtRows * 128, &qmap, 64 * lane, hk * G, q.first + i0 + j * TOK,
-                                    bar(S::B_UF + s), keep);
-                    slots.give(s);
+            for (int k = 0; ok && k < I.blocks; ++k) {
+                const int krow_next = stage_row(k + 1);
+                const WtBlock x = wt_block(p, I, k);
+                if (x.steps) {
+                    auto load_q = [&](int s, int j) {
+                        if (lane == 0) mbar_arrive_expect_tx(bar(S::B_UF + s), S::REGIONS * TOK * G * 128);
+                        __syncwarp();
+                        if (lane < S::REGIONS)
+                            tma_load_3d(sb0 + s * S::UNIT + lane * kPtRows * 128, &qmap, 64 * lane, hk * G, q.first + i0 + j * TOK,
+                                        bar(S::B_UF + s), keep);
+                    };
+                    if (I.stay && !have) {
+#pragma unroll
+                        for (int j = 0; j < kWtStay; ++j) {
+                            if (j >= x.steps || !ok) continue;
+                            qs[j] = take();
+                            if (ok) load_q(qs[j], j);
+                        }
+                        have = true;
+                    }
+                    int ks[2] = {0, 0};
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (e >= x.nk || !ok) continue;
+                        ks[e] = take();
+                        if (!ok) continue;
+                        const bool load = krow >= 0 && (lane >> 3) == e;
+                        const int bytes = __popc(__ballot_sync(kFull, load)) * 2 * S::GROUP;
+                        if (lane == 0) mbar_arrive_expect_tx(bar(S::B_UF + ks[e]), bytes);
+                        __syncwarp();
+                        if (load)
+                            tma_load_4d(sb0 + ks[e] * S::UNIT + 2 * (lane & 7) * S::GROUP, &kvmap, 0, 0, 0, krow >> 3,
+                                        bar(S::B_UF + ks[e]), pol);
+                    }
+#pragma unroll 1
+                    for (int j = 0; ok && !I.stay && j < x.steps; ++j) {
+                        const int s = take();
+                        if (!ok) break;
+                        load_q(s, j);
+                        slots.give(s);
+                    }
+                    slots.give(ks[0]);
+                    if (x.nk > 1) slots.give(ks[1]);
                 }
-                slots.give(ks[0]);
-                if (nk > 1) slots.give(ks[1]);
+                krow = krow_next;
             }
+            if (have)
+#pragma unroll
+                for (int j = 0; j < kWtStay; ++j)
+                    if (j < I.steps) slots.give(qs[j]);
             idx = __shfl_sync(kFull, next, 0);
         }
         // let every issued copy land before the CTA leaves
@@ -329,48 +376,71 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             if (!pt_wait(bar(S::B_IF + ring), (it / kWtItems) & 1, p)) { ok = false; break; }
             const WtItem& I = items[ring];
             if (I.end) break;
-            const int steps = I.steps, nk = I.nk;
+            const int blocks = I.blocks, tiles = I.steps;
+            const bool stay = I.stay;
+            bool have = false;
+            int qs[kWtStay] = {0, 0};
+#pragma unroll 1
+            for (int k = 0; ok && k < blocks; ++k) {
+                const WtBlock x = wt_block(p, I, k);
+                if (!x.steps) continue;
+                const bool fresh = stay && !have;
+                if (fresh) {
+#pragma unroll
+                    for (int j = 0; j < kWtStay; ++j)
+                        if (j < tiles) qs[j] = slots.take();
+                    have = true;
+                }
+                const int k0 = slots.take(), k1 = x.nk > 1 ? slots.take() : -1;
+                const int mine = t == 0 ? k0 : k1;
+                // both tiles: this warp releases both slots, and only what was filled may be released
+                ok = pt_wait(bar(S::B_UF + k0), phase >> k0 & 1, p) && (k1 < 0 || pt_wait(bar(S::B_UF + k1), phase >> k1 & 1, p));
+                const uint32_t klo = tc05::uniform(lo0 + ((mine < 0 ? 0 : mine) * S::UNIT >> 4));
+                phase ^= 1u << k0;
+                if (k1 >= 0) phase ^= 1u << k1;
+#pragma unroll 1
+                for (int j = 0; ok && j < x.steps; ++j, ++step) {
+                    const int s = stay ? qs[j & 1] : slots.take(), buf = step & 1;
+                    // (a warp without a key tile keeps step with the other)
+                    ok = mine < 0 || pt_wait(bar(S::B_SE + 2 * t + buf), (sphase >> buf & 1) ^ 1, p);
+                    if (ok && (!stay || fresh)) {
+                        ok = pt_wait(bar(S::B_UF + s), phase >> s & 1, p);
+                        phase ^= 1u << s;
+                    }
+                    if (!ok) break;
+                    if (mine >= 0) {
+                        sphase ^= 1u << buf;
+                        tc05::fence_after_sync();
+                        const uint32_t qlo = tc05::uniform(lo0 + (s * S::UNIT >> 4)), d = tm + 128 * buf;
+#pragma unroll
+                        for (int kk = 0; kk < S::ROWB / 32; ++kk)
+                            if (one)
+                                tc05::mma_ss<kFp8>(d, klo + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), tc05::desc_hi(S::GROUP),
+                                                   qlo + (((kk >> 2) * kPtRows * 128 + (kk & 3) * 32) >> 4), tc05::desc_hi(1024), kId,
+                                                   kk > 0);
+                        if (one) tc05::commit(bar(S::B_SF + 2 * t + buf));
+                    }
+                    if (!stay) {
+                        if (one) tc05::commit(bar(S::B_UE + s));
+                        slots.give(s);
+                    }
+                }
+                if (ok && one) {
+                    tc05::commit(bar(S::B_UE + k0));
+                    if (k1 >= 0) tc05::commit(bar(S::B_UE + k1));
+                }
+                slots.give(k0);
+                if (k1 >= 0) slots.give(k1);
+            }
+            if (have)
+#pragma unroll
+                for (int j = 0; j < kWtStay; ++j)
+                    if (j < tiles) {
+                        if (ok && one) tc05::commit(bar(S::B_UE + qs[j]));
+                        slots.give(qs[j]);
+                    }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(S::B_IE + ring));
-            if (!steps) continue;
-            const int k0 = slots.take(), k1 = nk > 1 ? slots.take() : -1;
-            const int mine = t == 0 ? k0 : k1;
-            uint32_t klo = 0;
-            if (mine >= 0) {
-                ok = pt_wait(bar(S::B_UF + mine), phase >> mine & 1, p);
-                klo = tc05::uniform(lo0 + (mine * S::UNIT >> 4));
-            }
-            phase ^= 1u << k0;
-            if (k1 >= 0) phase ^= 1u << k1;
-#pragma unroll 1
-            for (int j = 0; ok && j < steps; ++j, ++step) {
-                const int s = slots.take(), buf = step & 1;
-                // (a warp without a key tile keeps step with the other)
-                ok = (mine < 0 || pt_wait(bar(S::B_SE + 2 * t + buf), (sphase >> buf & 1) ^ 1, p)) &&
-                     pt_wait(bar(S::B_UF + s), phase >> s & 1, p);
-                if (!ok) break;
-                phase ^= 1u << s;
-                if (mine >= 0) {
-                    sphase ^= 1u << buf;
-                    tc05::fence_after_sync();
-                    const uint32_t qlo = tc05::uniform(lo0 + (s * S::UNIT >> 4)), d = tm + 128 * buf;
-#pragma unroll
-                    for (int kk = 0; kk < S::ROWB / 32; ++kk)
-                        if (one)
-                            tc05::mma_ss<kFp8>(d, klo + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), tc05::desc_hi(S::GROUP),
-                                               qlo + (((kk >> 2) * kPtRows * 128 + (kk & 3) * 32) >> 4), tc05::desc_hi(1024), kId,
-                                               kk > 0);
-                    if (one) tc05::commit(bar(S::B_SF + 2 * t + buf));
-                }
-                if (one) tc05::commit(bar(S::B_UE + s));
-                slots.give(s);
-            }
-            if (ok && one) {
-                tc05::commit(bar(S::B_UE + k0));
-                if (k1 >= 0) tc05::commit(bar(S::B_UE + k1));
-            }
-            slots.give(k0);
-            if (k1 >= 0) slots.give(k1);
         }
         if (!ok && one) atomicOr(p.status, kErrTimeout);
         // every product issued has completed before TMEM is freed
@@ -389,10 +459,8 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             if (!pt_wait(bar(S::B_IF + ring), (it / kWtItems) & 1, p)) { ok = false; break; }
             const WtItem& I = items[ring];
             if (I.end) break;
-            const int steps = I.steps, i0 = I.i0, i1 = I.i1;
+            const int i0 = I.i0, i1 = I.i1;
             const float* lse = w.lse + static_cast<long long>(I.first) * p.Hq + I.hk * G;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(S::B_IE + ring));
             int tok[4], col[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -408,29 +476,36 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 }
             };
             float x[4];
-            if (steps) load(0, x);
+            if (I.steps) load(0, x);
 #pragma unroll 1
-            for (int j = 0; j < steps; ++j, ++nl) {
-                const int s = nl % kWtLse;
-                float4 v;
-                v.x = x[0] == -INFINITY ? x[0] : -kLog2e * x[0];
-                v.y = x[1] == -INFINITY ? x[1] : -kLog2e * x[1];
-                v.z = x[2] == -INFINITY ? x[2] : -kLog2e * x[2];
-                v.w = x[3] == -INFINITY ? x[3] : -kLog2e * x[3];
-                if (j + 1 < steps) load(j + 1, x);
-                if (!pt_wait(bar(S::B_LE + s), ((nl / kWtLse) & 1) ^ 1, p)) { ok = false; break; }
-                *reinterpret_cast<float4*>(lse2 + 128 * s + 4 * lane) = v;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(S::B_LF + s));
+            for (int k = 0; ok && k < I.blocks; ++k) {
+                const int steps = wt_block(p, I, k).steps;
+#pragma unroll 1
+                for (int j = 0; j < steps; ++j, ++nl) {
+                    const int s = nl % kWtLse;
+                    float4 v;
+                    v.x = x[0] == -INFINITY ? x[0] : -kLog2e * x[0];
+                    v.y = x[1] == -INFINITY ? x[1] : -kLog2e * x[1];
+                    v.z = x[2] == -INFINITY ? x[2] : -kLog2e * x[2];
+                    v.w = x[3] == -INFINITY ? x[3] : -kLog2e * x[3];
+                    if (steps > 1) load(j + 1 < steps ? j + 1 : 0, x);
+                    if (!pt_wait(bar(S::B_LE + s), ((nl / kWtLse) & 1) ^ 1, p)) { ok = false; break; }
+                    *reinterpret_cast<float4*>(lse2 + 128 * s + 4 * lane) = v;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(S::B_LF + s));
+                }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(S::B_IE + ring));
         }
         if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
     } else if (warp < 16) {
         // --------------------------------------------------- exponentials
-        const int odd = warp >> 3, half = (warp >> 2) & 1, q4 = warp & 3, part = warp >> 2, g = lane >> 2, c4 = lane & 3;
-        const uint32_t s_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16) + 128 * odd + 64 * half;
-        const float* lse2 = reinterpret_cast<const float*>(smem + S::OFF_LSE) + 64 * half + 2 * c4;
-        float* sums = reinterpret_cast<float*>(smem + S::OFF_SUM) + 64 * q4;  // [part - 1][4][64 keys]
+        const int odd = warp >> 3, tile = (warp >> 2) & 1, q4 = warp & 3, pair = warp & 7, g = lane >> 2, c4 = lane & 3;
+        const uint32_t s_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16) + 128 * (2 * tile + odd);
+        const float* lse2 = reinterpret_cast<const float*>(smem + S::OFF_LSE) + 2 * c4;
+        // lane (g, c4) ends up with the sum of key 8 c4 + g of its warp's 32
+        float* sum = reinterpret_cast<float*>(smem + S::OFF_SUM) + 32 * pair + 8 * c4 + g;
         const float scale = kCap ? 1.f : p.scale_log2;
         const int rows = TOK * G;
         int step = 0;                 // steps before the item
@@ -441,179 +516,153 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             if (!pt_wait(bar(S::B_IF + ring), (it / kWtItems) & 1, p)) { ok = false; break; }
             const WtItem& I = items[ring];
             if (I.end) break;
-            const int steps = I.steps, i0 = I.i0, i1 = I.i1, nk = I.nk, L = I.L, off = I.off;
-            const int k0 = I.t0 + 32 * q4;  // first key of the warp (of key tile 0)
-            // tokens [lo, hi) see a key
-            auto lo_of = [&](int key) { return p.causal ? max(i0, key - off) : i0; };
-            auto hi_of = [&](int key) {
-                return p.window > 0 ? static_cast<int>(min(static_cast<long long>(i1), static_cast<long long>(key) - off + p.window)) : i1;
-            };
-            // every key of the warp's 32 of a tile is seen by [wlo, whi)
-            int wlo[2], whi[2];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int first = k0 + 128 * t, last = min(first + 31, L - 1);
-                wlo[t] = lo_of(last);
-                whi[t] = hi_of(min(first, L - 1));
-            }
-            float total[2][2][2] = {};  // of key tile, 16 keys, 8 keys
+            const int i0 = I.i0, i1 = I.i1, L = I.L, off = I.off;
 #pragma unroll 1
-            for (int j = (odd - step) & 1; j < steps; j += 2) {
-                const int ls = (step + j) % kWtLse, a = i0 + j * TOK;
-                if (!pt_wait(bar(S::B_LF + ls), ((step + j) / kWtLse) & 1, p)) { ok = false; break; }
-                float2 n[8];  // LSEs of rows 8 k + 2 c4 and the next
+            for (int kb = 0; ok && kb < I.blocks; ++kb) {
+                const WtBlock x = wt_block(p, I, kb);
+                const int steps = x.steps, k0 = x.t0 + 32 * pair;
+                const bool active = tile < x.nk;
+                // tokens [lo, hi) see a key
+                auto lo_of = [&](int key) { return p.causal ? max(i0, key - off) : i0; };
+                auto hi_of = [&](int key) {
+                    return p.window > 0 ? static_cast<int>(min(static_cast<long long>(i1), static_cast<long long>(key) - off + p.window)) : i1;
+                };
+                // every key of the warp is seen by [wlo, whi)
+                const int wlo = lo_of(min(k0 + 31, L - 1)), whi = hi_of(min(k0, L - 1));
+                float total[2][2] = {};  // of 16 keys, 8 keys
+#pragma unroll 1
+                for (int j = (odd - step) & 1; j < steps; j += 2) {
+                    const int ls = (step + j) % kWtLse, a = i0 + j * TOK;
+                    if (!pt_wait(bar(S::B_LF + ls), ((step + j) / kWtLse) & 1, p)) { ok = false; break; }
+                    if (active) {
+                        float2 n[16];  // LSEs of rows 8 k + 2 c4 and the next
 #pragma unroll
-                for (int k = 0; k < 8; ++k) n[k] = *reinterpret_cast<const float2*>(lse2 + 128 * ls + 8 * k);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(S::B_LE + ls));
-                const int cols = min(TOK, i1 - a) * G - 64 * half;  // of this warp's
+                        for (int k = 0; k < 16; ++k) n[k] = *reinterpret_cast<const float2*>(lse2 + 128 * ls + 8 * k);
+                        if (!pt_wait(bar(S::B_SF + 2 * tile + odd), sphase, p)) { ok = false; break; }
+                        sphase ^= 1u;
+                        tc05::fence_after_sync();
+                        float2 acc[2][2] = {};  // of 16 keys, 8 keys
+                        auto piece = [&](uint32_t (&x)[16], int hl, int cc, auto select) {
+                            if constexpr (kCap) {
+                                float top = 0.f;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (t >= nk || !ok) continue;
-                    ok = pt_wait(bar(S::B_SF + 2 * t + odd), sphase >> t & 1, p);
-                    if (!ok) continue;
-                    sphase ^= 1u << t;
-                    tc05::fence_after_sync();
-                    const uint32_t base = s_addr + 256 * t;
-                    float2 acc[2][2] = {};  // of 16 keys, 8 keys
-                    auto piece = [&](uint32_t (&x)[16], int hl, int cc, auto select) {
-                        if constexpr (kCap) {
-                            float top = 0.f;
-#pragma unroll
-                            for (int e = 0; e < 16; e += 2) top = max3(top, fabsf(__uint_as_float(x[e])), fabsf(__uint_as_float(x[e + 1])));
-                            wt_cap(x, p, __any_sync(kFull, top > p.cap_far));
-                        }
-                        // columns [c0, c1) of this warp's that see the lane's two keys
-                        int c0[2] = {0, 0}, c1[2] = {0, 0};
-                        if constexpr (decltype(select)::value) {
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const int key = k0 + 128 * t + 16 * hl + 8 * r + g;
-                                c0[r] = min(max(lo_of(key) - a, 0), TOK) * G - 64 * half;
-                                c1[r] = key < L ? min(max(hi_of(key) - a, 0), TOK) * G - 64 * half : c0[r];
+                                for (int e = 0; e < 16; e += 2) top = max3(top, fabsf(__uint_as_float(x[e])), fabsf(__uint_as_float(x[e + 1])));
+                                wt_cap(x, p, __any_sync(kFull, top > p.cap_far));
                             }
-                        }
+                            // columns [c0, c1) see the lane's two keys
+                            int c0[2] = {0, 0}, c1[2] = {0, 0};
+                            if constexpr (decltype(select)::value) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                float2 y = fma2(make_float2(__uint_as_float(x[4 * k + 2 * r]), __uint_as_float(x[4 * k + 2 * r + 1])),
-                                                both(scale), n[4 * cc + k]);
-                                y.x = fast_exp2(y.x);
-                                y.y = fast_exp2(y.y);
-                                if constexpr (decltype(select)::value) {
-                                    const int c = 32 * cc + 8 * k + 2 * c4;
-                                    y.x = c >= c0[r] && c < c1[r] ? y.x : 0.f;
-                                    y.y = c + 1 >= c0[r] && c + 1 < c1[r] ? y.y : 0.f;
+                                for (int r = 0; r < 2; ++r) {
+                                    const int key = k0 + 16 * hl + 8 * r + g;
+                                    c0[r] = min(max(lo_of(key) - a, 0), TOK) * G;
+                                    c1[r] = key < L ? min(max(hi_of(key) - a, 0), TOK) * G : c0[r];
                                 }
-                                acc[hl][r] = add2(acc[hl][r], y);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    float2 y = fma2(make_float2(__uint_as_float(x[4 * k + 2 * r]), __uint_as_float(x[4 * k + 2 * r + 1])),
+                                                    both(scale), n[4 * cc + k]);
+                                    y.x = fast_exp2(y.x);
+                                    y.y = fast_exp2(y.y);
+                                    if constexpr (decltype(select)::value) {
+                                        const int c = 32 * cc + 8 * k + 2 * c4;
+                                        y.x = c >= c0[r] && c < c1[r] ? y.x : 0.f;
+                                        y.y = c + 1 >= c0[r] && c + 1 < c1[r] ? y.y : 0.f;
+                                    }
+                                    acc[hl][r] = add2(acc[hl][r], y);
+                                }
+                            }
+                        };
+                        // piece u: 16 keys (u & 1), 32 rows (u >> 1)
+                        auto at = [&](int u) { return s_addr + (static_cast<uint32_t>(16 * (u & 1)) << 16) + 32 * (u >> 1); };
+                        if (wlo <= a && whi >= a + TOK && rows == 128) {
+                            uint32_t v[2][16];
+                            wt_ld(at(0), v[0]);
+                            wt_wait_ld(v[0]);
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) {
+                                if (u < 7) wt_ld(at(u + 1), v[(u + 1) & 1]);
+                                piece(v[u & 1], u & 1, u >> 1, std::false_type{});
+                                if (u < 7) wt_wait_ld(v[(u + 1) & 1]);
+                            }
+                        } else {
+                            const int cols = min(TOK, i1 - a) * G;
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) {
+                                if (32 * (u >> 1) >= cols) continue;
+                                uint32_t v[16];
+                                wt_ld(at(u), v);
+                                wt_wait_ld(v);
+                                piece(v, u & 1, u >> 1, std::true_type{});
                             }
                         }
-                    };
-                    if (wlo[t] <= a && whi[t] >= a + TOK && rows == 128) {
-                        uint32_t v[2][16];
-                        wt_ld(base, v[0]);
-                        wt_wait_ld(v[0]);
+                        tc05::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * tile + odd));
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            if (u < 3) wt_ld(base + (static_cast<uint32_t>(16 * ((u + 1) >> 1)) << 16) + 32 * ((u + 1) & 1), v[(u + 1) & 1]);
-                            piece(v[u & 1], u >> 1, u & 1, std::false_type{});
-                            if (u < 3) wt_wait_ld(v[(u + 1) & 1]);
-                        }
-                    } else {
+                        for (int hl = 0; hl < 2; ++hl)
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            if (32 * (u & 1) >= cols) continue;
-                            uint32_t v[16];
-                            wt_ld(base + (static_cast<uint32_t>(16 * (u >> 1)) << 16) + 32 * (u & 1), v);
-                            wt_wait_ld(v);
-                            piece(v, u >> 1, u & 1, std::true_type{});
-                        }
+                            for (int r = 0; r < 2; ++r) total[hl][r] += acc[hl][r].x + acc[hl][r].y;
                     }
-                    tc05::fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * t + odd));
+                    if (lane == 0) mbar_arrive(bar(S::B_LE + ls));
+                }
+                if (!ok) break;
+                step += steps;
+                if (active) {
 #pragma unroll
                     for (int hl = 0; hl < 2; ++hl)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) total[t][hl][r] += acc[hl][r].x + acc[hl][r].y;
+                        for (int r = 0; r < 2; ++r) {
+                            total[hl][r] += __shfl_xor_sync(kFull, total[hl][r], 1);
+                            total[hl][r] += __shfl_xor_sync(kFull, total[hl][r], 2);
+                        }
+                    float mine = c4 == 0 ? total[0][0] : c4 == 1 ? total[0][1] : c4 == 2 ? total[1][0] : total[1][1];
+                    if (steps && odd) {
+                        if (!pt_wait(bar(S::B_XE + pair), xphase ^ 1, p)) { ok = false; break; }
+                        *sum = mine;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(S::B_XF + pair));
+                    } else if (steps) {
+                        if (!pt_wait(bar(S::B_XF + pair), xphase, p)) { ok = false; break; }
+                        mine += *sum;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(S::B_XE + pair));
+                    }
+                    if (steps) xphase ^= 1;
+                    if (!odd) {
+                        const int key = k0 + 8 * c4 + g;
+                        bool whole = true;
+                        if (I.nsplit > 1) {
+                            // the unit's parts, joined in order by the warp whose arrival is the last
+                            float* part = p.part_out + static_cast<long long>(I.unit) * p.max_splits * kWtKeys + (key - x.t0);
+                            __stcg(part + I.split * kWtKeys, mine);
+                            __syncwarp();
+                            int prev = 0;
+                            if (lane == 0) prev = atom_add_acq_rel_gpu(p.counters + 8 * I.unit + pair);
+                            prev = __shfl_sync(kFull, prev, 0);
+                            whole = prev == I.nsplit - 1;
+                            if (whole) {
+                                mine = 0.f;
+                                for (int s = 0; s < I.nsplit; ++s) mine += __ldcg(part + s * kWtKeys);
+                                if (lane == 0) p.counters[8 * I.unit + pair] = 0;  // ready for the next call
+                            }
+                        }
+                        if (whole && key < L) {
+                            // (a page outside the pool was not loaded)
+                            const int page = p.block_table[static_cast<long long>(I.b) * p.bt_stride + page_div(key, p.pmagic, p.pmshift)];
+                            if (page < 0 || page >= p.num_pages) mine = 0.f;
+                            float before = 0.f;
+                            if (w.prior && key < I.fresh) before = w.prior[I.b * w.prior_b + I.hk * w.prior_h + key];
+                            w.weights[I.b * w.weights_b + I.hk * w.weights_h + key] = fmaf(w.decay, before, mine);
+                        }
+                    }
                 }
-                if (!ok) break;
             }
             if (!ok) break;
-            step += steps;
-            // lane (g, c4) of the quad's sums keeps those of keys 8 c4 + g of its 32
-            float mine[2];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                for (int hl = 0; hl < 2; ++hl)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float& x = total[t][hl][r];
-                        x += __shfl_xor_sync(kFull, x, 1);
-                        x += __shfl_xor_sync(kFull, x, 2);
-                    }
-                mine[t] = c4 == 0 ? total[t][0][0] : c4 == 1 ? total[t][0][1] : c4 == 2 ? total[t][1][0] : total[t][1][1];
-            }
-            const int r = 8 * c4 + g;
-            if (part) {
-                if (steps) {
-                    if (!pt_wait(bar(S::B_XE + q4), xphase ^ 1, p)) { ok = false; break; }
-                    sums[(part - 1) * kWtKeys + r] = mine[0];
-                    sums[(part - 1) * kWtKeys + 32 + r] = mine[1];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(S::B_XF + q4));
-                    xphase ^= 1;
-                }
-            } else {
-                if (steps) {
-                    if (!pt_wait(bar(S::B_XF + q4), xphase, p)) { ok = false; break; }
-#pragma unroll
-                    for (int e = 0; e < 3; ++e) {
-                        mine[0] += sums[e * kWtKeys + r];
-                        mine[1] += sums[e * kWtKeys + 32 + r];
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(S::B_XE + q4));
-                    xphase ^= 1;
-                }
-                bool whole = true;
-                if (I.nsplit > 1) {
-                    // the unit's parts, joined in order by the warp whose arrival is the last
-                    float* dst = p.part_out + static_cast<long long>(I.unit) * p.max_splits * kWtKeys + 32 * q4 + r;
-                    __stcg(dst + I.split * kWtKeys, mine[0]);
-                    __stcg(dst + I.split * kWtKeys + 128, mine[1]);
-                    __syncwarp();
-                    int prev = 0;
-                    if (lane == 0) prev = atom_add_acq_rel_gpu(p.counters + 4 * I.unit + q4);
-                    prev = __shfl_sync(kFull, prev, 0);
-                    whole = prev == I.nsplit - 1;
-                    if (whole) {
-                        mine[0] = mine[1] = 0.f;
-                        for (int s = 0; s < I.nsplit; ++s) {
-                            mine[0] += __ldcg(dst + s * kWtKeys);
-                            mine[1] += __ldcg(dst + s * kWtKeys + 128);
-                        }
-                        if (lane == 0) p.counters[4 * I.unit + q4] = 0;  // ready for the next call
-                    }
-                }
-                if (whole) {
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int key = k0 + 128 * t + r;
-                        if (key >= L) continue;
-                        float x = mine[t];
-                        if (I.bad) {
-                            const int page = p.block_table[static_cast<long long>(I.b) * p.bt_stride + page_div(key, p.pmagic, p.pmshift)];
-                            if (page < 0 || page >= p.num_pages) x = 0.f;
-                        }
-                        float before = 0.f;
-                        if (w.prior && key < I.fresh) before = w.prior[I.b * w.prior_b + I.hk * w.prior_h + key];
-                        w.weights[I.b * w.weights_b + I.hk * w.weights_h + key] = fmaf(w.decay, before, x);
-                    }
-                }
-            }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(S::B_IE + ring));
         }
