@@ -6,7 +6,7 @@
 //   S^T = K Q^T   tcgen05.mma, M = 128 keys, N = 128 rows, operands K-major as TMA lands them
 //   sum           2^(scale s - lse), summed over the columns in registers.  TMEM is read in
 //                 pieces of 16 keys x 32 rows whose lanes hold two of every eight rows, for
-//                 two keys each: a lane keeps the LSEs of 32 rows, alike for all keys, and
+//                 two keys each: a lane keeps the LSEs of 16 rows, alike for all keys, and
 //                 the quad's sums meet at the item's end.  (With a key per lane every lane
 //                 needed all LSEs: their loads shared the pipe that TMEM's values come by,
 //                 which bound the kernel: 1005 us for 16384 tokens)
@@ -14,8 +14,10 @@
 // product costs 16 KB out of L2.  Sums: fp32, of a tile's columns first, in an order fixed by
 // the sizes: no atomics on results.
 //
-// Warp roles (640 threads): warps 0-3 and 4-7 the exponentials of key tile 0 and 1 at even
-// steps, 8-15 at odd ones (two S^T buffers a key tile, one for each); warp 16
+// Warp roles (640 threads): warps 0-3 and 4-7 the exponentials of rows 0-63 of key tile 0 and 1,
+// 8-15 those of rows 64-127 (two S^T buffers a key tile: while one is read, the other's
+// product runs; with a set of warps for each buffer, a warp waited 900 of 3700 cycles for
+// its own); warp 16
 // loads (items, K, Q), warps 17 and 19 issue the products of key tile 0 and 1 (one warp for
 // both left the tensor cores idle between them: its waits and the issue of a product take
 // as long as the product), warp 18 lays out the LSEs.  K and Q
@@ -36,7 +38,7 @@
 
 namespace pkd {
 
-constexpr int kWtKeys = 256, kWtThreads = 640, kWtItems = 4, kWtLse = 4;
+constexpr int kWtKeys = 256, kWtThreads = 640, kWtItems = 4;
 
 constexpr int kWtStay = 2;        // query tiles that stay in their slots
 
@@ -55,15 +57,15 @@ struct WtShape {
     static constexpr int UNIT = 128 * ROWB;
     static constexpr int NU = UNIT == 32768 ? 6 : 12;
     static constexpr int OFF_LSE = NU * UNIT;
-    static constexpr int OFF_SUM = OFF_LSE + kWtLse * 128 * 4;  // an item's sums of odd steps, for the warps of even ones
+    static constexpr int OFF_SUM = OFF_LSE + 2 * 128 * 4;  // a block's sums of rows 64-127, for the warps of the others
     static constexpr int OFF_ITEM = OFF_SUM + kWtKeys * 4;
     static constexpr int OFF_PREF = OFF_ITEM + kWtItems * static_cast<int>(sizeof(WtItem));
     static constexpr int OFF_SCAN = OFF_PREF + (kPtMaxBatch + 4) * 4;
     static constexpr int OFF_BAR = (OFF_SCAN + 128 + 7) & ~7;
-    // slots full/empty, S full/empty [key tile][buffer], LSEs full/empty, items full/empty,
+    // slots full/empty, S full/empty [key tile][buffer], LSEs empty [buffer], items full/empty,
     // sums full/empty per 32 keys, drain
-    static constexpr int B_UF = 0, B_UE = B_UF + NU, B_SF = B_UE + NU, B_SE = B_SF + 4, B_LF = B_SE + 4;
-    static constexpr int B_LE = B_LF + kWtLse, B_IF = B_LE + kWtLse, B_IE = B_IF + kWtItems, B_XF = B_IE + kWtItems;
+    static constexpr int B_UF = 0, B_UE = B_UF + NU, B_SF = B_UE + NU, B_SE = B_SF + 4, B_LE = B_SE + 4;
+    static constexpr int B_IF = B_LE + 2, B_IE = B_IF + kWtItems, B_XF = B_IE + kWtItems;
     static constexpr int B_XE = B_XF + 8, B_DR = B_XE + 8;
     static constexpr int NBAR = B_DR + 2;
     static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
@@ -172,13 +174,10 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             mbar_init(bar(S::B_UE + i), 2);  // both issuing warps
         }
         for (int i = 0; i < 4; ++i) {
-            mbar_init(bar(S::B_SF + i), 1);
-            mbar_init(bar(S::B_SE + i), 4);
+            mbar_init(bar(S::B_SF + i), 2);  // the product, and the rows' LSEs
+            mbar_init(bar(S::B_SE + i), 8);
         }
-        for (int i = 0; i < kWtLse; ++i) {
-            mbar_init(bar(S::B_LF + i), 1);
-            mbar_init(bar(S::B_LE + i), 8);
-        }
+        for (int i = 0; i < 2; ++i) mbar_init(bar(S::B_LE + i), 16);
         for (int i = 0; i < kWtItems; ++i) {
             mbar_init(bar(S::B_IF + i), 1);
             mbar_init(bar(S::B_IE + i), 19);  // the issuing, LSE and sixteen exponential warps
@@ -217,7 +216,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             if (b < p.B) pref[b + 1] = before + v;
             __syncthreads();
         }
-        if (tid == 0) pref[0] = 0;
+        if (tid == 0) pref[0] = scan[24] = 0;
     }
     tc05::fence_before_sync();
     __syncthreads();
@@ -245,6 +244,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             if (ok) phase ^= 1u << s, used |= 1u << s;
             return s;
         };
+        const bool queued = total > static_cast<int>(gridDim.x);  // else: an item per CTA
         while (ok) {
             const int ring = npub % kWtItems;
             if (npub >= kWtItems && !pt_wait(bar(S::B_IE + ring), ((npub / kWtItems) - 1) & 1, p)) { ok = false; break; }
@@ -256,8 +256,8 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 __syncwarp();
                 break;
             }
-            int next = 0;
-            if (lane == 0) next = static_cast<int>(gridDim.x) + atomicAdd(p.queue, 1);
+            int next = total;
+            if (queued && lane == 0) next = static_cast<int>(gridDim.x) + atomicAdd(p.queue, 1);
             // item idx: parts innermost, then kv heads, the key blocks of a request from the
             // first (causal: seen by the most tokens)
             const int split = idx % p.max_splits, u = idx / p.max_splits;
@@ -298,6 +298,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 const int page = p.block_table[static_cast<long long>(b) * p.bt_stride + col];
                 if (page < 0 || page >= p.num_pages) {
                     atomicOr(p.status, kErrBounds);
+                    scan[24] = 1;
                     return -1;
                 }
                 return (page * p.Hkv + hk) * p.P + (t - col * p.P);
@@ -479,20 +480,22 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             if (I.steps) load(0, x);
 #pragma unroll 1
             for (int k = 0; ok && k < I.blocks; ++k) {
-                const int steps = wt_block(p, I, k).steps;
+                const WtBlock blk = wt_block(p, I, k);
+                const int steps = blk.steps;
 #pragma unroll 1
                 for (int j = 0; j < steps; ++j, ++nl) {
-                    const int s = nl % kWtLse;
+                    const int buf = nl & 1;
                     float4 v;
                     v.x = x[0] == -INFINITY ? x[0] : -kLog2e * x[0];
                     v.y = x[1] == -INFINITY ? x[1] : -kLog2e * x[1];
                     v.z = x[2] == -INFINITY ? x[2] : -kLog2e * x[2];
                     v.w = x[3] == -INFINITY ? x[3] : -kLog2e * x[3];
                     if (steps > 1) load(j + 1 < steps ? j + 1 : 0, x);
-                    if (!pt_wait(bar(S::B_LE + s), ((nl / kWtLse) & 1) ^ 1, p)) { ok = false; break; }
-                    *reinterpret_cast<float4*>(lse2 + 128 * s + 4 * lane) = v;
+                    if (!pt_wait(bar(S::B_LE + buf), ((nl >> 1) & 1) ^ 1, p)) { ok = false; break; }
+                    *reinterpret_cast<float4*>(lse2 + 128 * buf + 4 * lane) = v;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(S::B_LF + s));
+                    // (the last step's with this buffer is over: all its readers have said so)
+                    if (lane < blk.nk) mbar_arrive(bar(S::B_SF + 2 * lane + buf));
                 }
             }
             __syncwarp();
@@ -501,15 +504,15 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
     } else if (warp < 16) {
         // --------------------------------------------------- exponentials
-        const int odd = warp >> 3, tile = (warp >> 2) & 1, q4 = warp & 3, pair = warp & 7, g = lane >> 2, c4 = lane & 3;
-        const uint32_t s_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16) + 128 * (2 * tile + odd);
-        const float* lse2 = reinterpret_cast<const float*>(smem + S::OFF_LSE) + 2 * c4;
+        const int half = warp >> 3, tile = (warp >> 2) & 1, q4 = warp & 3, pair = warp & 7, g = lane >> 2, c4 = lane & 3;
+        const uint32_t s_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16) + 256 * tile + 64 * half;
+        const float* lse2 = reinterpret_cast<const float*>(smem + S::OFF_LSE) + 64 * half + 2 * c4;
         // lane (g, c4) ends up with the sum of key 8 c4 + g of its warp's 32
         float* sum = reinterpret_cast<float*>(smem + S::OFF_SUM) + 32 * pair + 8 * c4 + g;
         const float scale = kCap ? 1.f : p.scale_log2;
         const int rows = TOK * G;
         int step = 0;                 // steps before the item
-        uint32_t sphase = 0, xphase = 0;
+        uint32_t sphase = 0, phase0 = 0, xphase = 0;  // per buffer: of this key tile's S, of tile 0's
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const int ring = it % kWtItems;
@@ -522,6 +525,11 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 const WtBlock x = wt_block(p, I, kb);
                 const int steps = x.steps, k0 = x.t0 + 32 * pair;
                 const bool active = tile < x.nk;
+                // (asked for ahead: it is added at the block's end)
+                const int key = k0 + 8 * c4 + g;
+                float before = 0.f;
+                if (!half && w.prior && key < min(L, I.fresh))
+                    before = w.prior[I.b * w.prior_b + I.hk * w.prior_h + key];
                 // tokens [lo, hi) see a key
                 auto lo_of = [&](int key) { return p.causal ? max(i0, key - off) : i0; };
                 auto hi_of = [&](int key) {
@@ -531,15 +539,18 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 const int wlo = lo_of(min(k0 + 31, L - 1)), whi = hi_of(min(k0, L - 1));
                 float total[2][2] = {};  // of 16 keys, 8 keys
 #pragma unroll 1
-                for (int j = (odd - step) & 1; j < steps; j += 2) {
-                    const int ls = (step + j) % kWtLse, a = i0 + j * TOK;
-                    if (!pt_wait(bar(S::B_LF + ls), ((step + j) / kWtLse) & 1, p)) { ok = false; break; }
-                    if (active) {
-                        float2 n[16];  // LSEs of rows 8 k + 2 c4 and the next
+                for (int j = 0; j < steps; ++j) {
+                    const int buf = (step + j) & 1, a = i0 + j * TOK;
+                    // (a warp without a key tile keeps step with tile 0)
+                    if (!pt_wait(bar(S::B_SF + (active ? 2 * tile : 0) + buf), ((active ? sphase : phase0) >> buf) & 1, p)) { ok = false; break; }
+                    phase0 ^= 1u << buf;
+                    if (active) sphase ^= 1u << buf;
+                    float2 n[8];  // LSEs of rows 8 k + 2 c4 and the next
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) n[k] = *reinterpret_cast<const float2*>(lse2 + 128 * ls + 8 * k);
-                        if (!pt_wait(bar(S::B_SF + 2 * tile + odd), sphase, p)) { ok = false; break; }
-                        sphase ^= 1u;
+                    for (int k = 0; k < 8; ++k) n[k] = *reinterpret_cast<const float2*>(lse2 + 128 * buf + 8 * k);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(S::B_LE + buf));
+                    if (active) {
                         tc05::fence_after_sync();
                         float2 acc[2][2] = {};  // of 16 keys, 8 keys
                         auto piece = [&](uint32_t (&x)[16], int hl, int cc, auto select) {
@@ -568,7 +579,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                                     y.x = fast_exp2(y.x);
                                     y.y = fast_exp2(y.y);
                                     if constexpr (decltype(select)::value) {
-                                        const int c = 32 * cc + 8 * k + 2 * c4;
+                                        const int c = 64 * half + 32 * cc + 8 * k + 2 * c4;
                                         y.x = c >= c0[r] && c < c1[r] ? y.x : 0.f;
                                         y.y = c + 1 >= c0[r] && c + 1 < c1[r] ? y.y : 0.f;
                                     }
@@ -577,21 +588,21 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                             }
                         };
                         // piece u: 16 keys (u & 1), 32 rows (u >> 1)
-                        auto at = [&](int u) { return s_addr + (static_cast<uint32_t>(16 * (u & 1)) << 16) + 32 * (u >> 1); };
+                        auto at = [&](int u) { return s_addr + 128 * buf + (static_cast<uint32_t>(16 * (u & 1)) << 16) + 32 * (u >> 1); };
                         if (wlo <= a && whi >= a + TOK && rows == 128) {
                             uint32_t v[2][16];
                             wt_ld(at(0), v[0]);
                             wt_wait_ld(v[0]);
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) {
-                                if (u < 7) wt_ld(at(u + 1), v[(u + 1) & 1]);
+                            for (int u = 0; u < 4; ++u) {
+                                if (u < 3) wt_ld(at(u + 1), v[(u + 1) & 1]);
                                 piece(v[u & 1], u & 1, u >> 1, std::false_type{});
-                                if (u < 7) wt_wait_ld(v[(u + 1) & 1]);
+                                if (u < 3) wt_wait_ld(v[(u + 1) & 1]);
                             }
                         } else {
-                            const int cols = min(TOK, i1 - a) * G;
+                            const int cols = min(TOK, i1 - a) * G - 64 * half;
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) {
+                            for (int u = 0; u < 4; ++u) {
                                 if (32 * (u >> 1) >= cols) continue;
                                 uint32_t v[16];
                                 wt_ld(at(u), v);
@@ -601,14 +612,12 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         }
                         tc05::fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * tile + odd));
+                        if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * tile + buf));
 #pragma unroll
                         for (int hl = 0; hl < 2; ++hl)
 #pragma unroll
                             for (int r = 0; r < 2; ++r) total[hl][r] += acc[hl][r].x + acc[hl][r].y;
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(S::B_LE + ls));
                 }
                 if (!ok) break;
                 step += steps;
@@ -621,7 +630,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                             total[hl][r] += __shfl_xor_sync(kFull, total[hl][r], 2);
                         }
                     float mine = c4 == 0 ? total[0][0] : c4 == 1 ? total[0][1] : c4 == 2 ? total[1][0] : total[1][1];
-                    if (steps && odd) {
+                    if (steps && half) {
                         if (!pt_wait(bar(S::B_XE + pair), xphase ^ 1, p)) { ok = false; break; }
                         *sum = mine;
                         __syncwarp();
@@ -633,8 +642,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         if (lane == 0) mbar_arrive(bar(S::B_XE + pair));
                     }
                     if (steps) xphase ^= 1;
-                    if (!odd) {
-                        const int key = k0 + 8 * c4 + g;
+                    if (!half) {
                         bool whole = true;
                         if (I.nsplit > 1) {
                             // the unit's parts, joined in order by the warp whose arrival is the last
@@ -652,11 +660,10 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                             }
                         }
                         if (whole && key < L) {
-                            // (a page outside the pool was not loaded)
-                            const int page = p.block_table[static_cast<long long>(I.b) * p.bt_stride + page_div(key, p.pmagic, p.pmshift)];
-                            if (page < 0 || page >= p.num_pages) mine = 0.f;
-                            float before = 0.f;
-                            if (w.prior && key < I.fresh) before = w.prior[I.b * w.prior_b + I.hk * w.prior_h + key];
+                            if (scan[24]) {  // a page outside the pool was not loaded
+                                const int page = p.block_table[static_cast<long long>(I.b) * p.bt_stride + page_div(key, p.pmagic, p.pmshift)];
+                                if (page < 0 || page >= p.num_pages) mine = 0.f;
+                            }
                             w.weights[I.b * w.weights_b + I.hk * w.weights_h + key] = fmaf(w.decay, before, mine);
                         }
                     }
@@ -677,7 +684,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         tc05::dealloc(tmem, 512);
     }
     // the last CTA to leave resets the item counter for the next call
-    if (tid == 0) {
+    if (tid == 0 && pref[p.B] * p.Hkv * p.max_splits > static_cast<int>(gridDim.x)) {
         const int prev = atom_add_acq_rel_gpu(p.queue + 1);
         if (prev == static_cast<int>(gridDim.x) - 1) {
             p.queue[0] = 0;
