@@ -13,6 +13,12 @@ static cudaError_t launch_tc05(const CUtensorMap& kvmap, const CUtensorMap& qmap
     cudaError_t e = persistent_grid(1, static_cast<int>(items < 152 ? items : 152), grid);
     if (e == cudaSuccess) e = kernel_setup(state, kern, kWtThreads, WtShape<D, kType>::SMEM);
     if (e != cudaSuccess) return e;
+    // the roles' registers come out of those of the launch: a kernel that got fewer would wait for ever
+    static const bool fits = [&] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs * kWtThreads >= 512 * kWtRegsExp + 128 * kWtRegsOther;
+    }();
+    if (!fits) return cudaErrorInvalidConfiguration;
     return launch_kernel(kern, dim3(grid), kWtThreads, WtShape<D, kType>::SMEM, false, stream, kvmap, qmap, w);
 }
 

@@ -6,7 +6,7 @@
 //   S^T = K Q^T   tcgen05.mma, M = 128 keys, N = 128 rows, operands K-major as TMA lands them
 //   sum           2^(scale s - lse), summed over the columns in registers.  TMEM is read in
 //                 pieces of 16 keys x 32 rows whose lanes hold two of every eight rows, for
-//                 two keys each: a lane keeps the LSEs of 16 rows, alike for all keys, and
+//                 two keys each: a lane keeps the LSEs of 32 rows, alike for all keys, and
 //                 the quad's sums meet at the item's end.  (With a key per lane every lane
 //                 needed all LSEs: their loads shared the pipe that TMEM's values come by,
 //                 which bound the kernel: 1005 us for 16384 tokens)
@@ -14,17 +14,25 @@
 // product costs 16 KB out of L2.  Sums: fp32, of a tile's columns first, in an order fixed by
 // the sizes: no atomics on results.
 //
-// Warp roles (640 threads): warps 0-3 and 4-7 the exponentials of rows 0-63 of key tile 0 and 1,
-// 8-15 those of rows 64-127 (two S^T buffers a key tile: while one is read, the other's
-// product runs; with a set of warps for each buffer, a warp waited 900 of 3700 cycles for
-// its own); warp 16
+// Warp roles (640 threads): warps 0-3 and 4-7 the exponentials of key tile 0 and 1 at even
+// steps, 8-15 at odd ones (two S^T buffers a key tile, one for each; all warps at every step,
+// on 64 rows each, spent more on waits: 896 us
+// for 16384 tokens, not 849); warp 16
 // loads (items, K, Q), warps 17 and 19 issue the products of key tile 0 and 1 (one warp for
 // both left the tensor cores idle between them: its waits and the issue of a product take
 // as long as the product), warp 18 lays out the LSEs.  K and Q
 // tiles share NU slots: a slot goes to the next tile in the order in which slots become
 // free, which is the same for the warp that fills them and the one that reads them (both
 // keep the queue of free slots), so short items have all slots in flight and long ones
-// NU - 2 query tiles.  Every wait is bounded.
+// NU - 2 query tiles.  Registers follow the roles (640 x 96 at launch = 512 x 104 + 128 x 64).
+// Every wait is bounded.
+//
+// What bounds it, D = 128 (16384-token prompt, 32 heads: 849 us, 1295 TFLOP/s, 0.68 of a dense
+// library product): per step of two 128x128 products (1024 cycles) the exponentials take the
+// special-function units 1024 cycles, and a warp that is done with an S^T buffer meets
+// its next one 650 cycles later -- waits on barriers that answer in 200 to 300 cycles while
+// the units' queue is full -- so that neither is busy more than two thirds of the time.
+// Products alone ran at 600 us, without exponentials 747.
 //
 // Few query tiles (two at most) stay in their slots instead, and an item is a run of key
 // blocks that stream past them: bound by reading K then (the last 64 of 32768 tokens, four
@@ -39,6 +47,7 @@
 namespace pkd {
 
 constexpr int kWtKeys = 256, kWtThreads = 640, kWtItems = 4;
+constexpr int kWtRegsExp = 104, kWtRegsOther = 64;  // registers of the exponential warps, of the others
 
 constexpr int kWtStay = 2;        // query tiles that stay in their slots
 
@@ -57,7 +66,7 @@ struct WtShape {
     static constexpr int UNIT = 128 * ROWB;
     static constexpr int NU = UNIT == 32768 ? 6 : 12;
     static constexpr int OFF_LSE = NU * UNIT;
-    static constexpr int OFF_SUM = OFF_LSE + 2 * 128 * 4;  // a block's sums of rows 64-127, for the warps of the others
+    static constexpr int OFF_SUM = OFF_LSE + 2 * 128 * 4;  // a block's sums of odd steps, for the warps of even ones
     static constexpr int OFF_ITEM = OFF_SUM + kWtKeys * 4;
     static constexpr int OFF_PREF = OFF_ITEM + kWtItems * static_cast<int>(sizeof(WtItem));
     static constexpr int OFF_SCAN = OFF_PREF + (kPtMaxBatch + 4) * 4;
@@ -175,9 +184,9 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(S::B_SF + i), 2);  // the product, and the rows' LSEs
-            mbar_init(bar(S::B_SE + i), 8);
+            mbar_init(bar(S::B_SE + i), 4);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(bar(S::B_LE + i), 16);
+        for (int i = 0; i < 2; ++i) mbar_init(bar(S::B_LE + i), 8);
         for (int i = 0; i < kWtItems; ++i) {
             mbar_init(bar(S::B_IF + i), 1);
             mbar_init(bar(S::B_IE + i), 19);  // the issuing, LSE and sixteen exponential warps
@@ -224,6 +233,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
     const uint32_t tmem = *tslot;
 
     if (warp == 16) {
+        reg_dec<kWtRegsOther>();
         // ---------------------------------------------------------- loads
         if (lane == 0) {
             prefetch_tmap(&kvmap);
@@ -363,6 +373,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             if (used >> s & 1) mbar_wait(bar(S::B_UF + s), (phase >> s & 1) ^ 1);
         if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
     } else if (warp == 17 || warp == 19) {
+        reg_dec<kWtRegsOther>();
         // ------------------------------------------- products of key tile t
         constexpr uint32_t kId = kFp8 ? tc05::idesc_e4m3(128, 128) : tc05::idesc_f16(kType == kPtBF16, 128, 128, false, false);
         const int t = (warp - 17) >> 1;
@@ -402,12 +413,12 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 #pragma unroll 1
                 for (int j = 0; ok && j < x.steps; ++j, ++step) {
                     const int s = stay ? qs[j & 1] : slots.take(), buf = step & 1;
-                    // (a warp without a key tile keeps step with the other)
-                    ok = mine < 0 || pt_wait(bar(S::B_SE + 2 * t + buf), (sphase >> buf & 1) ^ 1, p);
-                    if (ok && (!stay || fresh)) {
+                    if (!stay || fresh) {
                         ok = pt_wait(bar(S::B_UF + s), phase >> s & 1, p);
                         phase ^= 1u << s;
                     }
+                    // (a warp without a key tile keeps step with the other)
+                    ok = ok && (mine < 0 || pt_wait(bar(S::B_SE + 2 * t + buf), (sphase >> buf & 1) ^ 1, p));
                     if (!ok) break;
                     if (mine >= 0) {
                         sphase ^= 1u << buf;
@@ -451,6 +462,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         }
         __syncwarp();
     } else if (warp == 18) {
+        reg_dec<kWtRegsOther>();
         // ------------------------------------- the rows' LSEs, as added to logits
         float* lse2 = reinterpret_cast<float*>(smem + S::OFF_LSE);
         int nl = 0;
@@ -502,17 +514,18 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             if (lane == 0) mbar_arrive(bar(S::B_IE + ring));
         }
         if (!ok && lane == 0) atomicOr(p.status, kErrTimeout);
-    } else if (warp < 16) {
+    } else {
+        reg_inc<kWtRegsExp>();
         // --------------------------------------------------- exponentials
-        const int half = warp >> 3, tile = (warp >> 2) & 1, q4 = warp & 3, pair = warp & 7, g = lane >> 2, c4 = lane & 3;
-        const uint32_t s_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16) + 256 * tile + 64 * half;
-        const float* lse2 = reinterpret_cast<const float*>(smem + S::OFF_LSE) + 64 * half + 2 * c4;
+        const int odd = warp >> 3, tile = (warp >> 2) & 1, q4 = warp & 3, pair = warp & 7, g = lane >> 2, c4 = lane & 3;
+        const uint32_t s_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16) + 128 * (2 * tile + odd);
+        const float* lse2 = reinterpret_cast<const float*>(smem + S::OFF_LSE) + 128 * odd + 2 * c4;
         // lane (g, c4) ends up with the sum of key 8 c4 + g of its warp's 32
         float* sum = reinterpret_cast<float*>(smem + S::OFF_SUM) + 32 * pair + 8 * c4 + g;
         const float scale = kCap ? 1.f : p.scale_log2;
         const int rows = TOK * G;
         int step = 0;                 // steps before the item
-        uint32_t sphase = 0, phase0 = 0, xphase = 0;  // per buffer: of this key tile's S, of tile 0's
+        uint32_t sphase = 0, phase0 = 0, xphase = 0;  // of this key tile's S, of tile 0's, of the sums
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const int ring = it % kWtItems;
@@ -528,7 +541,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 // (asked for ahead: it is added at the block's end)
                 const int key = k0 + 8 * c4 + g;
                 float before = 0.f;
-                if (!half && w.prior && key < min(L, I.fresh))
+                if (!odd && w.prior && key < min(L, I.fresh))
                     before = w.prior[I.b * w.prior_b + I.hk * w.prior_h + key];
                 // tokens [lo, hi) see a key
                 auto lo_of = [&](int key) { return p.causal ? max(i0, key - off) : i0; };
@@ -539,17 +552,17 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 const int wlo = lo_of(min(k0 + 31, L - 1)), whi = hi_of(min(k0, L - 1));
                 float total[2][2] = {};  // of 16 keys, 8 keys
 #pragma unroll 1
-                for (int j = 0; j < steps; ++j) {
-                    const int buf = (step + j) & 1, a = i0 + j * TOK;
+                for (int j = (odd - step) & 1; j < steps; j += 2) {
+                    const int a = i0 + j * TOK;
                     // (a warp without a key tile keeps step with tile 0)
-                    if (!pt_wait(bar(S::B_SF + (active ? 2 * tile : 0) + buf), ((active ? sphase : phase0) >> buf) & 1, p)) { ok = false; break; }
-                    phase0 ^= 1u << buf;
-                    if (active) sphase ^= 1u << buf;
-                    float2 n[8];  // LSEs of rows 8 k + 2 c4 and the next
+                    if (!pt_wait(bar(S::B_SF + (active ? 2 * tile : 0) + odd), active ? sphase : phase0, p)) { ok = false; break; }
+                    phase0 ^= 1u;
+                    if (active) sphase ^= 1u;
+                    float2 n[16];  // LSEs of rows 8 k + 2 c4 and the next
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) n[k] = *reinterpret_cast<const float2*>(lse2 + 128 * buf + 8 * k);
+                    for (int k = 0; k < 16; ++k) n[k] = *reinterpret_cast<const float2*>(lse2 + 8 * k);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(S::B_LE + buf));
+                    if (lane == 0) mbar_arrive(bar(S::B_LE + odd));
                     if (active) {
                         tc05::fence_after_sync();
                         float2 acc[2][2] = {};  // of 16 keys, 8 keys
@@ -579,7 +592,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                                     y.x = fast_exp2(y.x);
                                     y.y = fast_exp2(y.y);
                                     if constexpr (decltype(select)::value) {
-                                        const int c = 64 * half + 32 * cc + 8 * k + 2 * c4;
+                                        const int c = 32 * cc + 8 * k + 2 * c4;
                                         y.x = c >= c0[r] && c < c1[r] ? y.x : 0.f;
                                         y.y = c + 1 >= c0[r] && c + 1 < c1[r] ? y.y : 0.f;
                                     }
@@ -588,21 +601,21 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                             }
                         };
                         // piece u: 16 keys (u & 1), 32 rows (u >> 1)
-                        auto at = [&](int u) { return s_addr + 128 * buf + (static_cast<uint32_t>(16 * (u & 1)) << 16) + 32 * (u >> 1); };
+                        auto at = [&](int u) { return s_addr + (static_cast<uint32_t>(16 * (u & 1)) << 16) + 32 * (u >> 1); };
                         if (wlo <= a && whi >= a + TOK && rows == 128) {
                             uint32_t v[2][16];
                             wt_ld(at(0), v[0]);
                             wt_wait_ld(v[0]);
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                if (u < 3) wt_ld(at(u + 1), v[(u + 1) & 1]);
+                            for (int u = 0; u < 8; ++u) {
+                                if (u < 7) wt_ld(at(u + 1), v[(u + 1) & 1]);
                                 piece(v[u & 1], u & 1, u >> 1, std::false_type{});
-                                if (u < 3) wt_wait_ld(v[(u + 1) & 1]);
+                                if (u < 7) wt_wait_ld(v[(u + 1) & 1]);
                             }
                         } else {
-                            const int cols = min(TOK, i1 - a) * G - 64 * half;
+                            const int cols = min(TOK, i1 - a) * G;
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) {
+                            for (int u = 0; u < 8; ++u) {
                                 if (32 * (u >> 1) >= cols) continue;
                                 uint32_t v[16];
                                 wt_ld(at(u), v);
@@ -612,7 +625,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         }
                         tc05::fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * tile + buf));
+                        if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * tile + odd));
 #pragma unroll
                         for (int hl = 0; hl < 2; ++hl)
 #pragma unroll
@@ -630,7 +643,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                             total[hl][r] += __shfl_xor_sync(kFull, total[hl][r], 2);
                         }
                     float mine = c4 == 0 ? total[0][0] : c4 == 1 ? total[0][1] : c4 == 2 ? total[1][0] : total[1][1];
-                    if (steps && half) {
+                    if (steps && odd) {
                         if (!pt_wait(bar(S::B_XE + pair), xphase ^ 1, p)) { ok = false; break; }
                         *sum = mine;
                         __syncwarp();
@@ -642,7 +655,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         if (lane == 0) mbar_arrive(bar(S::B_XE + pair));
                     }
                     if (steps) xphase ^= 1;
-                    if (!half) {
+                    if (!odd) {
                         bool whole = true;
                         if (I.nsplit > 1) {
                             // the unit's parts, joined in order by the warp whose arrival is the last
