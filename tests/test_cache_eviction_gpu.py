@@ -231,7 +231,7 @@ def test_select_clamps_lengths_and_takes_strides():
     assert np.array_equal(kept.cpu().numpy(), want[0]) and n.tolist() == [0, 30]
 
 
-@pytest.mark.parametrize("S,budget", [(70000, 3000), (200001, 150000)])
+@pytest.mark.parametrize("S,budget", [(10000, 164), (70000, 3000), (130001, 128), (200001, 150000)])
 def test_select_long(S, budget):
     g = torch.Generator(device="cuda").manual_seed(S)
     w = torch.exp(2 * torch.randn((2, 2, S), device="cuda", generator=g))
