@@ -7,24 +7,27 @@
 // in shared memory by integer atomics, whose order changes nothing, and a scan from the
 // top.  Keys without any weight, often a third of them, are counted apart by votes.  Then
 // the keys above the threshold, and as many of those on it as are still missing, the
-// lowest indexes first, are written in the order of the keys: a warp owns a run of
-// consecutive keys, counts, and writes behind the warps before it.
+// lowest indexes first, are written in the order of the keys: a thread owns consecutive
+// keys, counts, and writes behind the threads before it.
 //
-// A row is read once; its ranks stay in registers, up to KPT per thread (0: rows too long
-// for that are read again in every pass).  Long rows, and few rows, are spread over a
-// cluster of CTAs that add their histograms up in the first one's shared memory.
+// A row is read once, through shared memory (whose words are spread so that threads KPT
+// keys apart meet in no bank), where the neighbours of a pooled weight are too; ranks stay
+// in registers, up to KPT per thread (0: rows too long for that are read again in every
+// pass).  Long rows, and few rows, are spread over a cluster of CTAs that add their
+// histograms up in the first one's shared memory.
 #include <cooperative_groups.h>
 
 #include "evict.cuh"
 #include "launch.h"
+#include "packed.cuh"
 #include "ptx.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace pkd {
 
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32, kSelBins = 2048;
-constexpr int kSelMaxKpt = 32, kSelMaxCluster = 8;
+constexpr int kSelBins = 2048, kSelMaxCluster = 8;
+constexpr int kSelMaxSide = 127;  // neighbours to either side of a pooled weight
 constexpr uint32_t kRankZero = 0x80000000u, kRankKept = 0xffffffffu;
 
 // The rank of a weight: rises with it, NaN as -inf, -0 as +0, below that of a protected key.
@@ -35,13 +38,15 @@ __device__ __forceinline__ uint32_t rank_of(float x) {
 
 struct SelectShared {
     int hist[kSelBins];
-    int warp_sum[kSelWarps], above[kSelWarps], on[kSelWarps];
+    int warp_sum[16], above[16], on[16];
     int found[3];                           // the threshold's bin, keys still missing in it, its count
     int cta_above[kSelMaxCluster], cta_on[kSelMaxCluster];
 };
 
-template <int KPT, bool kCluster>
-__global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1) evict_select_kernel(const SelectParams p) {
+// Threads x KPT keys of a CTA; 1024 threads' worth of CTAs fit an SM at least.
+template <int kSelThreads, int KPT, bool kCluster>
+__global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_kernel(const SelectParams p) {
+    constexpr int kSelWarps = kSelThreads / 32, kPer = kSelBins / kSelThreads;
     __shared__ SelectShared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int rank = 0, ctas = 1;
@@ -63,37 +68,72 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1) evict_select_k
     const int context = pos ? max(p.context_lens[b], 0) : L;
     const int first = p.sinks, past = context - p.recent, side = p.pool / 2;
 
-    // the warp's run of keys: chunks of 32 from t0 on
-    const int chunks = (L + 32 * kSelWarps * ctas - 1) / (32 * kSelWarps * ctas);
-    const int t0 = (rank * kSelWarps + warp) * 32 * chunks + lane;
-    auto rank_at = [&](int i) -> uint32_t {
-        const int t = t0 + 32 * i;
-        if (i >= chunks || t >= L) return 0;  // no key
-        const int at = pos ? pos[t] : t;
-        float x = w[t];
-        if (at < first || at >= past) return kRankKept;
-        if (side) {
-            const int z = min(t + side, past - 1);
-            for (int s = max(t - side, first); s <= z; ++s) x = fmaxf(x, w[s]);  // (a NaN beside a number counts not)
-        }
-        return rank_of(x);
-    };
+    // the thread's keys: `own` from t0 on
+    const int own = (L + all - 1) / all, t0 = me * own;
+    auto masked = [&](int t) { return t >= first && t < past && t < L ? w[t] : -INFINITY; };
     constexpr bool kKept = KPT > 0;
     uint32_t r[kKept ? KPT : 1];
-    if constexpr (kKept)
+    auto rank_at = [&](int t) -> uint32_t {  // (rows that are read again)
+        if (t >= L) return 0;  // no key
+        const int at = pos ? pos[t] : t;
+        if (at < first || at >= past) return kRankKept;
+        float x = w[t];
+        for (int d = 1; d <= side; ++d) x = fmaxf(x, fmaxf(masked(max(t - d, 0)), masked(t + d)));
+        return rank_of(x);
+    };
+    if constexpr (kKept) {
+        extern __shared__ float stage[];
+        const int c0 = rank * kSelThreads * own, span = kSelThreads * own + 2 * side;  // stage[0] is key c0 - side
+        auto word = [](int i) { return i + i / KPT; };
+        for (int i0 = tid; i0 < span; i0 += 4 * kSelThreads) {
+            float x[4];
 #pragma unroll
-        for (int i = 0; i < KPT; ++i) r[i] = rank_at(i);
-    // f(rank of the lane's key, its index), chunk by chunk
+            for (int e = 0; e < 4; ++e) {
+                const int i = i0 + e * kSelThreads, t = c0 - side + i;
+                x[e] = -INFINITY;
+                if (i < span && t >= 0 && t < L) {
+                    if (pos) {
+                        const int at = pos[t];
+                        x[e] = __uint_as_float(at < first || at >= past ? kRankKept : rank_of(w[t]));
+                    } else {
+                        x[e] = masked(t);
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i0 + e * kSelThreads < span) stage[word(i0 + e * kSelThreads)] = x[e];
+        }
+        __syncthreads();
+        // (a NaN beside a number counts not)
+        const int mine = tid * own + side;
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const int t = t0 + i;
+            r[i] = 0;  // no key
+            if (i >= own || t >= L) continue;
+            float x = stage[word(mine + i)];
+            if (pos) {
+                r[i] = __float_as_uint(x);
+            } else if (t < first || t >= past) {
+                r[i] = kRankKept;
+            } else {
+                for (int d = 1; d <= side; ++d) x = max3(x, stage[word(mine + i - d)], stage[word(mine + i + d)]);
+                r[i] = rank_of(x);
+            }
+        }
+    }
+    // f(rank of the thread's key, its index)
     auto each = [&](auto f) {
         if constexpr (kKept) {
 #pragma unroll
             for (int i = 0; i < KPT; ++i) {
-                if (i >= chunks) break;
-                f(r[i], t0 + 32 * i);
+                if (i >= own) break;
+                f(r[i], t0 + i);
             }
         } else {
 #pragma unroll 1
-            for (int i = 0; i < chunks; ++i) f(rank_at(i), t0 + 32 * i);
+            for (int i = 0; i < own; ++i) f(rank_at(t0 + i), t0 + i);
         }
     };
 
@@ -128,9 +168,9 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1) evict_select_k
         if (rank == 0) {
             // from the top: a thread takes `per` bins, the highest first
             const int per = bins / kSelThreads;
-            int c[4], mine = 0;
+            int c[kPer], mine = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < kPer; ++e) {
                 c[e] = e < per ? sh.hist[bins - 1 - (tid * per + e)] : 0;
                 mine += c[e];
             }
@@ -148,7 +188,7 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1) evict_select_k
                 if (k < warp) before += sh.warp_sum[k];
             // the bin in which the count reaches `missing`
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < kPer; ++e) {
                 if (before < missing && before + c[e] >= missing) {
                     int found[3] = {bins - 1 - (tid * per + e), missing - before, c[e]};
                     for (int k = 0; k < ctas; ++k) {
@@ -169,17 +209,27 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1) evict_select_k
     }
 
     // ------------------------------ those above it, and the first on it
-    int na = 0, no = 0;
+    int ta = 0, to = 0;  // of the thread, then of the threads before it
     each([&](uint32_t x, int) {
-        na += __popc(__ballot_sync(kFull, x >> shift > prefix));
-        no += __popc(__ballot_sync(kFull, x != 0 && x >> shift == prefix));
+        ta += x >> shift > prefix;
+        to += x != 0 && x >> shift == prefix;
     });
-    if (lane == 0) sh.above[warp] = na, sh.on[warp] = no;
+    {
+        const int a = ta, o = to;
+#pragma unroll
+        for (int e = 1; e < 32; e <<= 1) {
+            const int x = __shfl_up_sync(kFull, ta, e), y = __shfl_up_sync(kFull, to, e);
+            if (lane >= e) ta += x, to += y;
+        }
+        if (lane == 31) sh.above[warp] = ta, sh.on[warp] = to;
+        ta -= a;
+        to -= o;
+    }
     __syncthreads();
-    int ta = 0, to = 0, sa = 0, so = 0;  // of the warps before, of the CTA
+    int sa = 0, so = 0;  // of the CTA
 #pragma unroll
     for (int k = 0; k < kSelWarps; ++k) {
-        if (k == warp) ta = sa, to = so;
+        if (k == warp) ta += sa, to += so;
         sa += sh.above[k];
         so += sh.on[k];
     }
@@ -191,22 +241,19 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1) evict_select_k
         cg::this_cluster().sync();
         for (int k = 0; k < rank; ++k) ta += sh.cta_above[k], to += sh.cta_on[k];
     }
-    const unsigned below = (1u << lane) - 1;
     each([&](uint32_t x, int t) {
         const bool over = x >> shift > prefix, at = x != 0 && x >> shift == prefix;
-        const unsigned va = __ballot_sync(kFull, over), vo = __ballot_sync(kFull, at);
-        const int a = ta + __popc(va & below), o = to + __popc(vo & below);
-        if (over || (at && o < missing)) kept[a + min(o, missing)] = t;
-        ta += __popc(va);
-        to += __popc(vo);
+        if (over || (at && to < missing)) kept[ta + min(to, missing)] = t;
+        ta += over;
+        to += at;
     });
 }
 
-template <int KPT>
-static cudaError_t launch_kpt(const SelectParams& p, int cluster, cudaStream_t stream) {
+template <int T, int KPT>
+static cudaError_t launch_one(const SelectParams& p, int cluster, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.H * cluster, p.B);
-    cfg.blockDim = dim3(kSelThreads);
+    cfg.blockDim = dim3(T);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -214,24 +261,30 @@ static cudaError_t launch_kpt(const SelectParams& p, int cluster, cudaStream_t s
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = cluster > 1 ? 1 : 0;
-    return cluster > 1 ? cudaLaunchKernelEx(&cfg, evict_select_kernel<KPT, true>, p)
-                       : cudaLaunchKernelEx(&cfg, evict_select_kernel<KPT, false>, p);
+    // a CTA's keys and their neighbours, a word in KPT left free
+    constexpr int kMost = KPT ? T * KPT + 2 * kSelMaxSide : 0;
+    if constexpr (KPT > 0) cfg.dynamicSmemBytes = (kMost + kMost / KPT + 1) * sizeof(float);
+    static PerDevice state, state_cluster;
+    cudaError_t e = cluster > 1 ? kernel_setup(state_cluster, evict_select_kernel<T, KPT, true>, T, (int)cfg.dynamicSmemBytes)
+                                : kernel_setup(state, evict_select_kernel<T, KPT, false>, T, (int)cfg.dynamicSmemBytes);
+    if (e != cudaSuccess) return e;
+    return cluster > 1 ? cudaLaunchKernelEx(&cfg, evict_select_kernel<T, KPT, true>, p)
+                       : cudaLaunchKernelEx(&cfg, evict_select_kernel<T, KPT, false>, p);
 }
 
 cudaError_t launch_evict_select(const SelectParams& p, cudaStream_t stream) {
-    // CTAs of a row: as many as its ranks need registers, and while SMs are idle and a thread
-    // has more than eight keys
+    // CTAs of a row: as many as its ranks need registers, and while SMs are idle and a CTA
+    // has more than 4096 keys
     const long long rows = static_cast<long long>(p.B) * p.H;
     int cluster = 1;
-    while (cluster < kSelMaxCluster &&
-           (p.keys > cluster * kSelThreads * kSelMaxKpt || (rows * cluster < 152 && p.keys > cluster * kSelThreads * 8)))
-        cluster *= 2;
-    const int kpt = (p.keys + cluster * kSelThreads - 1) / (cluster * kSelThreads);
-    if (kpt <= 4) return launch_kpt<4>(p, cluster, stream);
-    if (kpt <= 8) return launch_kpt<8>(p, cluster, stream);
-    if (kpt <= 16) return launch_kpt<16>(p, cluster, stream);
-    if (kpt <= 32) return launch_kpt<32>(p, cluster, stream);
-    return launch_kpt<0>(p, cluster, stream);
+    while (cluster < kSelMaxCluster && (p.keys > cluster * 16384 || (rows * cluster < 152 && p.keys > cluster * 4096))) cluster *= 2;
+    const int keys = (p.keys + cluster - 1) / cluster;
+    if (keys <= 1024) return launch_one<256, 4>(p, cluster, stream);
+    if (keys <= 2048) return launch_one<256, 8>(p, cluster, stream);
+    if (keys <= 4096) return launch_one<256, 16>(p, cluster, stream);
+    if (keys <= 8192) return launch_one<512, 16>(p, cluster, stream);
+    if (keys <= 16384) return launch_one<512, 32>(p, cluster, stream);
+    return launch_one<512, 0>(p, cluster, stream);
 }
 
 }  // namespace pkd
