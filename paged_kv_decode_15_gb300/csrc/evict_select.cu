@@ -11,11 +11,13 @@
 // keys, counts, and writes behind the threads before it.
 //
 // A row is read once, through shared memory (whose words are spread so that threads KPT
-// keys apart meet in no bank), where the neighbours of a pooled weight are too; ranks stay
+// keys apart seldom meet in a bank), where the neighbours of a pooled weight are too; ranks stay
 // in registers, up to KPT per thread (0: rows too long for that are read again in every
 // pass).  Long rows, and few rows, are spread over a cluster of CTAs that add their
 // histograms up in the first one's shared memory.
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "evict.cuh"
 #include "launch.h"
@@ -84,7 +86,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
     if constexpr (kKept) {
         extern __shared__ float stage[];
         const int c0 = rank * kSelThreads * own, span = kSelThreads * own + 2 * side;  // stage[0] is key c0 - side
-        auto word = [](int i) { return i + i / KPT; };
+        auto word = [](int i) { return i + i / 32; };
         for (int i0 = tid; i0 < span; i0 += 4 * kSelThreads) {
             float x[4];
 #pragma unroll
@@ -105,22 +107,42 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
                 if (i0 + e * kSelThreads < span) stage[word(i0 + e * kSelThreads)] = x[e];
         }
         __syncthreads();
-        // (a NaN beside a number counts not)
+        // the largest weight around each of the thread's keys (a NaN beside a number counts not)
         const int mine = tid * own + side;
+        float x[KPT];
+        auto window = [&](auto reach) {
+            constexpr int kSide = decltype(reach)::value;
+            float v[KPT + 2 * kSide];
+#pragma unroll
+            for (int i = 0; i < KPT + 2 * kSide; ++i) v[i] = i < own + 2 * kSide ? stage[word(mine - kSide + i)] : 0.f;
+#pragma unroll
+            for (int i = 0; i < KPT; ++i) {
+                x[i] = v[i + kSide];
+#pragma unroll
+                for (int d = 1; d <= kSide; ++d) x[i] = max3(x[i], v[i + kSide - d], v[i + kSide + d]);
+            }
+        };
+        switch (side) {
+            case 0: window(std::integral_constant<int, 0>{}); break;
+            case 2: window(std::integral_constant<int, 2>{}); break;
+            case 3: window(std::integral_constant<int, 3>{}); break;
+            default:
+#pragma unroll
+                for (int i = 0; i < KPT; ++i) {
+                    if (i >= own) break;
+                    x[i] = stage[word(mine + i)];
+                    for (int d = 1; d <= side; ++d) x[i] = max3(x[i], stage[word(mine + i - d)], stage[word(mine + i + d)]);
+                }
+        }
 #pragma unroll
         for (int i = 0; i < KPT; ++i) {
             const int t = t0 + i;
             r[i] = 0;  // no key
             if (i >= own || t >= L) continue;
-            float x = stage[word(mine + i)];
-            if (pos) {
-                r[i] = __float_as_uint(x);
-            } else if (t < first || t >= past) {
-                r[i] = kRankKept;
-            } else {
-                for (int d = 1; d <= side; ++d) x = max3(x, stage[word(mine + i - d)], stage[word(mine + i + d)]);
-                r[i] = rank_of(x);
-            }
+            if (pos)
+                r[i] = __float_as_uint(x[i]);
+            else
+                r[i] = t < first || t >= past ? kRankKept : rank_of(x[i]);
         }
     }
     // f(rank of the thread's key, its index)
@@ -138,6 +160,8 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
     };
 
     // ------------------------------------------------------ the threshold
+    // a thread of the scan reads `kPer` neighbouring bins: they lie a row apart, threads side by side
+    auto place = [&](int bin) { return (bin % kPer) * kSelThreads + bin / kPer; };
     uint32_t prefix = 0;
     int missing = n, shift = 32;
 #pragma unroll 1
@@ -145,33 +169,34 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
         const int bits = round < 2 ? 11 : 10, bins = 1 << bits;
         const int up = shift;  // bits below the prefix
         shift -= bits;
-        for (int i = tid; i < bins; i += kSelThreads) sh.hist[i] = 0;
+        for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[i] = 0;
         if constexpr (kCluster) cg::this_cluster().sync(); else __syncthreads();
         int zeros = 0;
         each([&](uint32_t x, int) {
             const bool in = x != 0 && (round == 0 || (x >> (up & 31)) == prefix), zero = in && x == kRankZero;
             zeros += __popc(__ballot_sync(kFull, zero));
-            if (in && !zero) atomicAdd(&sh.hist[(x >> shift) & (bins - 1)], 1);
+            if (in && !zero) atomicAdd(&sh.hist[place((x >> shift) & (bins - 1))], 1);
         });
-        if (lane == 0 && zeros) atomicAdd(&sh.hist[(kRankZero >> shift) & (bins - 1)], zeros);
+        if (lane == 0 && zeros) atomicAdd(&sh.hist[place((kRankZero >> shift) & (bins - 1))], zeros);
         if constexpr (kCluster) {
             // the counts of all CTAs, in the first one's
             __syncthreads();
             int* total = cg::this_cluster().map_shared_rank(sh.hist, 0);
             if (rank)
-                for (int i = tid; i < bins; i += kSelThreads)
+                for (int i = tid; i < kSelBins; i += kSelThreads)
                     if (sh.hist[i]) atomicAdd(total + i, sh.hist[i]);
             cg::this_cluster().sync();
         } else {
             __syncthreads();
         }
         if (rank == 0) {
-            // from the top: a thread takes `per` bins, the highest first
-            const int per = bins / kSelThreads;
+            // from the top: a thread takes kPer bins, the highest first (of the last round's
+            // 1024 bins the upper half of the threads' are empty)
+            const int top = kSelBins / kPer - 1 - tid;  // its row of bins
             int c[kPer], mine = 0;
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
-                c[e] = e < per ? sh.hist[bins - 1 - (tid * per + e)] : 0;
+                c[e] = sh.hist[(kPer - 1 - e) * kSelThreads + top];
                 mine += c[e];
             }
             int sum = mine;
@@ -190,7 +215,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
                 if (before < missing && before + c[e] >= missing) {
-                    int found[3] = {bins - 1 - (tid * per + e), missing - before, c[e]};
+                    int found[3] = {top * kPer + kPer - 1 - e, missing - before, c[e]};
                     for (int k = 0; k < ctas; ++k) {
                         int* dst = sh.found;
                         if constexpr (kCluster) dst = cg::this_cluster().map_shared_rank(sh.found, k);
@@ -261,9 +286,9 @@ static cudaError_t launch_one(const SelectParams& p, int cluster, cudaStream_t s
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = cluster > 1 ? 1 : 0;
-    // a CTA's keys and their neighbours, a word in KPT left free
+    // a CTA's keys and their neighbours, a word in 33 left free
     constexpr int kMost = KPT ? T * KPT + 2 * kSelMaxSide : 0;
-    if constexpr (KPT > 0) cfg.dynamicSmemBytes = (kMost + kMost / KPT + 1) * sizeof(float);
+    if constexpr (KPT > 0) cfg.dynamicSmemBytes = (kMost + kMost / 32 + 1) * sizeof(float);
     static PerDevice state, state_cluster;
     cudaError_t e = cluster > 1 ? kernel_setup(state_cluster, evict_select_kernel<T, KPT, true>, T, (int)cfg.dynamicSmemBytes)
                                 : kernel_setup(state, evict_select_kernel<T, KPT, false>, T, (int)cfg.dynamicSmemBytes);
