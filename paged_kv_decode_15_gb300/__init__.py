@@ -918,16 +918,26 @@ def evict_select(weights, seq_lens, budget, *, sinks=0, recent=0, pool=1, positi
             with ctx:
                 return evict_select(weights, seq_lens, budget, sinks=sinks, recent=recent, pool=pool,
                                     positions=positions, context_lens=context_lens, kept=kept, kept_lens=kept_lens)
-    B, H, keys = weights.shape
-    w, wb, wh, _ = _key_rows(weights, B, H, _F32, "weights")
-    x, xb, xh, position_keys = _key_rows(positions, B, H, _I32, "positions")
-    if positions is not None and position_keys < keys:
-        raise ValueError("positions must have as many keys as weights")
-    for name, t in (("seq_lens", seq_lens), ("context_lens", context_lens), ("kept_lens", kept_lens)):
-        if t is not None and (t.dtype is not _I32 or t.shape != (B,) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous int32 [{B}]")
-    if (positions is None) != (context_lens is None):
-        raise ValueError("positions and context_lens come together")
+    B, H, keys = shape = weights.shape
+    wb, wh, one = weights.stride()
+    if weights.dtype is not _F32 or (one != 1 and keys > 1):
+        _key_rows(weights, B, H, _F32, "weights")
+    if seq_lens.dtype is not _I32 or seq_lens.shape != shape[:1] or seq_lens.stride() != (1,) and B > 1:
+        raise ValueError(f"seq_lens must be contiguous int32 [{B}]")
+    x = xb = xh = context = None
+    if positions is None:
+        if context_lens is not None:
+            raise ValueError("positions and context_lens come together")
+        xb = xh = 0
+    else:
+        x, xb, xh, position_keys = _key_rows(positions, B, H, _I32, "positions")
+        if position_keys < keys:
+            raise ValueError("positions must have as many keys as weights")
+        if context_lens is None:
+            raise ValueError("positions and context_lens come together")
+        if context_lens.dtype is not _I32 or context_lens.shape != shape[:1] or not context_lens.is_contiguous():
+            raise ValueError(f"context_lens must be contiguous int32 [{B}]")
+        context = context_lens.data_ptr()
     if not 1 <= budget < 1 << 31 or not 0 <= sinks < 1 << 31 or not 0 <= recent < 1 << 31 or not 1 <= pool < 256:
         raise ValueError("budget must lie in [1, 2^31), sinks and recent in [0, 2^31), pool in [1, 255]")
     if kept is None:
@@ -936,10 +946,11 @@ def evict_select(weights, seq_lens, budget, *, sinks=0, recent=0, pool=1, positi
         raise ValueError(f"kept must be contiguous int32 [{B}, {H}, {budget}]")
     if kept_lens is None:
         kept_lens = torch.empty((B,), dtype=_I32, device=weights.device)
+    elif kept_lens.shape != (B,) or kept_lens.dtype is not _I32 or not kept_lens.is_contiguous():
+        raise ValueError(f"kept_lens must be contiguous int32 [{B}]")
     status = (_lib or load_library()).pkd_evict_select(
-        w, wb, wh, keys, seq_lens.data_ptr(), B, H, budget, sinks, recent, pool, x, xb, xh,
-        context_lens.data_ptr() if context_lens is not None else None, kept.data_ptr(), kept_lens.data_ptr(),
-        _raw_stream(index))
+        weights.data_ptr(), wb, wh, keys, seq_lens.data_ptr(), B, H, budget, sinks, recent, pool, x, xb, xh, context,
+        kept.data_ptr(), kept_lens.data_ptr(), _raw_stream(index))
     if status:
         _check(status)
     return kept, kept_lens

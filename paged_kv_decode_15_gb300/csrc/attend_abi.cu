@@ -201,9 +201,10 @@ pkd_status plan_key_weights(int B, long long T, int max_q, int last, int Hq, int
     pl.step = pl.rows <= 16;
     pl.max_splits = 1;
     if (pl.step) {
-        // about 16 CTAs per SM, chunks of 128 to 2048 keys
+        // about 32 CTAs per SM, chunks of 128 to 2048 keys (16: 55 and 68 us on the cases of
+        // key_weights.cu, not 55 and 65)
         const long long units = std::max(1ll, (long long)B * Hkv);
-        const long long chunk = std::min(2048ll, std::max(128ll, max_kv_len * units / (16 * kSms)));
+        const long long chunk = std::min(2048ll, std::max(128ll, max_kv_len * units / (32 * kSms)));
         pl.chunk = up((int)chunk, 128);
         pl.chunks = (max_kv_len + pl.chunk - 1) / pl.chunk;
         return PKD_OK;
