@@ -769,7 +769,7 @@ def packed_attention(q, k, v, query_start, scale, *, key_start=None, causal=True
     """
     index = q.get_device()
     if index < 0 or k.get_device() != index or v.get_device() != index or query_start.get_device() != index or \
-            not (key_start is out is lse is workspace is None):
+            (key_start is not None and key_start.get_device() != index) or not (out is lse is workspace is None):
         _device_error(q=q, k=k, v=v, query_start=query_start, key_start=key_start, out=out, lse=lse, workspace=workspace)
     if stream is not None or _current_device() != index:
         ctx = _elsewhere(index, stream)
@@ -846,7 +846,8 @@ def key_weights(q, kv_cache, block_table, seq_lens, query_start, lse, scale, *, 
     index = q.get_device()
     if index < 0 or kv_cache.get_device() != index or block_table.get_device() != index or \
             seq_lens.get_device() != index or query_start.get_device() != index or lse.get_device() != index or \
-            not (weights is out is workspace is None):
+            (weights is not None and weights.get_device() != index) or \
+            (out is not None and out.get_device() != index) or workspace is not None:
         _device_error(q=q, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, query_start=query_start,
                       lse=lse, weights=weights, out=out, workspace=workspace)
     if stream is not None or _current_device() != index:
@@ -909,7 +910,8 @@ def evict_select(weights, seq_lens, budget, *, sinks=0, recent=0, pool=1, positi
     kept_lens int32 [B]: min(seq_lens, budget)).
     """
     index = weights.get_device()
-    if index < 0 or seq_lens.get_device() != index or not (positions is context_lens is kept is kept_lens is None):
+    if index < 0 or seq_lens.get_device() != index or (positions is not None and positions.get_device() != index) or \
+            (context_lens is not None and context_lens.get_device() != index) or not (kept is kept_lens is None):
         _device_error(weights=weights, seq_lens=seq_lens, positions=positions, context_lens=context_lens, kept=kept,
                       kept_lens=kept_lens)
     if stream is not None or _current_device() != index:
@@ -922,7 +924,7 @@ def evict_select(weights, seq_lens, budget, *, sinks=0, recent=0, pool=1, positi
     wb, wh, one = weights.stride()
     if weights.dtype is not _F32 or (one != 1 and keys > 1):
         _key_rows(weights, B, H, _F32, "weights")
-    if seq_lens.dtype is not _I32 or seq_lens.shape != shape[:1] or seq_lens.stride() != (1,) and B > 1:
+    if seq_lens.dtype is not _I32 or seq_lens.shape != shape[:1] or not seq_lens.is_contiguous():
         raise ValueError(f"seq_lens must be contiguous int32 [{B}]")
     x = xb = xh = context = None
     if positions is None:
@@ -930,14 +932,15 @@ def evict_select(weights, seq_lens, budget, *, sinks=0, recent=0, pool=1, positi
             raise ValueError("positions and context_lens come together")
         xb = xh = 0
     else:
-        x, xb, xh, position_keys = _key_rows(positions, B, H, _I32, "positions")
-        if position_keys < keys:
-            raise ValueError("positions must have as many keys as weights")
+        xb, xh, one = positions.stride()
+        if positions.dtype is not _I32 or positions.shape != shape or (one != 1 and keys > 1):
+            if _key_rows(positions, B, H, _I32, "positions")[3] < keys:
+                raise ValueError("positions must have as many keys as weights")
         if context_lens is None:
             raise ValueError("positions and context_lens come together")
         if context_lens.dtype is not _I32 or context_lens.shape != shape[:1] or not context_lens.is_contiguous():
             raise ValueError(f"context_lens must be contiguous int32 [{B}]")
-        context = context_lens.data_ptr()
+        x, context = positions.data_ptr(), context_lens.data_ptr()
     if not 1 <= budget < 1 << 31 or not 0 <= sinks < 1 << 31 or not 0 <= recent < 1 << 31 or not 1 <= pool < 256:
         raise ValueError("budget must lie in [1, 2^31), sinks and recent in [0, 2^31), pool in [1, 255]")
     if kept is None:
@@ -968,7 +971,8 @@ def cache_compact(kv_cache, block_table, kept, kept_lens, *, weights=None, posit
     """
     index = kv_cache.get_device()
     if index < 0 or block_table.get_device() != index or kept.get_device() != index or \
-            kept_lens.get_device() != index or not (weights is positions is None):
+            kept_lens.get_device() != index or (weights is not None and weights.get_device() != index) or \
+            (positions is not None and positions.get_device() != index):
         _device_error(kv_cache=kv_cache, block_table=block_table, kept=kept, kept_lens=kept_lens, weights=weights,
                       positions=positions)
     if stream is not None or _current_device() != index:
