@@ -300,24 +300,28 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             }
             __syncwarp();
             ++npub;
-            // the cache row of a block's 16-key stage, a lane each; -1: no key, or none in the pool
-            auto stage_row = [&](int k) {
-                const int t = t0 + k * kWtKeys + kStageTok * lane;
-                if (k >= I.blocks || lane >= kWtKeys / kStageTok || t >= t1) return -1;
-                const int col = page_div(t, p.pmagic, p.pmshift);
-                const int page = p.block_table[static_cast<long long>(b) * p.bt_stride + col];
+            // the page of a block's 16-key stage, a lane each (asked for a block ahead, and looked
+            // at where it is used), and its cache row; -1: no key, or none in the pool
+            auto stage_key = [&](int k) { return t0 + k * kWtKeys + kStageTok * lane; };
+            auto stage_page = [&](int k) {
+                if (k >= I.blocks || lane >= kWtKeys / kStageTok || stage_key(k) >= t1) return 0;
+                return p.block_table[static_cast<long long>(b) * p.bt_stride + page_div(stage_key(k), p.pmagic, p.pmshift)];
+            };
+            auto stage_row = [&](int k, int page) {
+                const int t = stage_key(k);
+                if (lane >= kWtKeys / kStageTok || t >= t1) return -1;
                 if (page < 0 || page >= p.num_pages) {
                     atomicOr(p.status, kErrBounds);
                     scan[24] = 1;
                     return -1;
                 }
-                return (page * p.Hkv + hk) * p.P + (t - col * p.P);
+                return (page * p.Hkv + hk) * p.P + (t - page_div(t, p.pmagic, p.pmshift) * p.P);
             };
-            int krow = stage_row(0), qs[kWtStay] = {0, 0};
+            int page = stage_page(0), qs[kWtStay] = {0, 0};
             bool have = false;
 #pragma unroll 1
             for (int k = 0; ok && k < I.blocks; ++k) {
-                const int krow_next = stage_row(k + 1);
+                const int page_next = stage_page(k + 1);
                 const WtBlock x = wt_block(p, I, k);
                 if (x.steps) {
                     auto load_q = [&](int s, int j) {
@@ -336,6 +340,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         }
                         have = true;
                     }
+                    const int krow = stage_row(k, page);
                     int ks[2] = {0, 0};
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -360,7 +365,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                     slots.give(ks[0]);
                     if (x.nk > 1) slots.give(ks[1]);
                 }
-                krow = krow_next;
+                page = page_next;
             }
             if (have)
 #pragma unroll
