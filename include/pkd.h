@@ -475,6 +475,8 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
  *                were
  *   workspace    as for pkd_paged_attention (its status word: lengths, starts and pages
  *                out of range; keys on such a page receive nothing)
+ *                (of PKD_FLAG_TEST_TIMEOUT only more than 16 rows, last_queries or
+ *                max_query_len tokens times num_heads / num_kv_heads, take notice)
  *
  * Sums run in fp32, in an order fixed by the arguments: results repeat bit for bit.  A
  * key that no token sees receives 0 whatever its K holds.  Limits as for

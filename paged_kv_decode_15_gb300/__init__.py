@@ -831,7 +831,7 @@ def _key_rows(t, B, H, dtype, name):
 
 def key_weights(q, kv_cache, block_table, seq_lens, query_start, lse, scale, *, weights=None, decay=1.0, causal=True,
                 window=0, softcap=0.0, last_queries=0, max_query_len=None, max_kv_len=None, q_scale=1.0, k_scale=1.0,
-                out=None, workspace=None, stream=None):
+                out=None, workspace=None, test_timeout=False, stream=None):
     """Attention weight that each cached key received from the call's queries.
 
     q, kv_cache, block_table, seq_lens, query_start, causal, window, softcap and the
@@ -842,6 +842,7 @@ def key_weights(q, kv_cache, block_table, seq_lens, query_start, lse, scale, *, 
     the call's own tokens start at 0).  Returns out, fp32 [B, Hkv, keys]: entries
     behind seq_lens[b] keep what was in it (0 where the call allocates it).  out may
     be weights.  workspace_check reads the status, as for paged_attention.
+    test_timeout sets the diagnostic PKD_FLAG_TEST_TIMEOUT (prompts only).
     """
     index = q.get_device()
     if index < 0 or kv_cache.get_device() != index or block_table.get_device() != index or \
@@ -857,7 +858,8 @@ def key_weights(q, kv_cache, block_table, seq_lens, query_start, lse, scale, *, 
                 return key_weights(q, kv_cache, block_table, seq_lens, query_start, lse, scale, weights=weights,
                                    decay=decay, causal=causal, window=window, softcap=softcap,
                                    last_queries=last_queries, max_query_len=max_query_len, max_kv_len=max_kv_len,
-                                   q_scale=q_scale, k_scale=k_scale, out=out, workspace=workspace)
+                                   q_scale=q_scale, k_scale=k_scale, out=out, workspace=workspace,
+                                   test_timeout=test_timeout)
     T, Hq, D = q.shape
     qs = _token_stride(q, T, Hq, D, "q")
     num_pages, Hkv, P = _check_cache(D, kv_cache)
@@ -890,7 +892,7 @@ def key_weights(q, kv_cache, block_table, seq_lens, query_start, lse, scale, *, 
         q.data_ptr(), q_dt, qs, kv_cache.data_ptr(), kv_dt, num_pages, block_table.data_ptr(), stride,
         seq_lens.data_ptr(), query_start.data_ptr(), B, T, max_query_len, last_queries, Hq, Hkv, D, P, max_kv_len, scale,
         q_scale, k_scale, softcap, window, lse.data_ptr(), prior, pb, ph, decay, dst, ob, oh, ws, ws_bytes,
-        FLAG_CAUSAL if causal else 0, s)
+        (FLAG_CAUSAL if causal else 0) | (FLAG_TEST_TIMEOUT if test_timeout else 0), s)
     if status:
         _check(status)
     return out

@@ -933,6 +933,15 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
 #pragma unroll
                                             for (int i = 0; i < 16; ++i) x[16 * e + i] = 0u;
                                         }
+                                    if constexpr (kPacked) {
+                                        // (nor have the next prompt's)
+                                        const int end = hi_all - tk - 32 * c;
+                                        if (end < 32) {
+#pragma unroll
+                                            for (int i = 0; i < 32; ++i)
+                                                if (i >= end) x[i] = 0u;
+                                        }
+                                    }
                                     if (__any_sync(kFull, pt_max<true>(x) > cap_far))
                                         pt_cap<false>(x, p);
                                     else

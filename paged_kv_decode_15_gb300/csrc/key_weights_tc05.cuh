@@ -419,7 +419,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 for (int j = 0; ok && j < x.steps; ++j, ++step) {
                     const int s = stay ? qs[j & 1] : slots.take(), buf = step & 1;
                     if (!stay || fresh) {
-                        ok = pt_wait(bar(S::B_UF + s), phase >> s & 1, p);
+                        ok = pt_wait_queries(bar(S::B_UF + s), phase >> s & 1, p, it);
                         phase ^= 1u << s;
                     }
                     // (a warp without a key tile keeps step with the other)
@@ -572,12 +572,6 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         tc05::fence_after_sync();
                         float2 acc[2][2] = {};  // of 16 keys, 8 keys
                         auto piece = [&](uint32_t (&x)[16], int hl, int cc, auto select) {
-                            if constexpr (kCap) {
-                                float top = 0.f;
-#pragma unroll
-                                for (int e = 0; e < 16; e += 2) top = max3(top, fabsf(__uint_as_float(x[e])), fabsf(__uint_as_float(x[e + 1])));
-                                wt_cap(x, p, __any_sync(kFull, top > p.cap_far));
-                            }
                             // columns [c0, c1) see the lane's two keys
                             int c0[2] = {0, 0}, c1[2] = {0, 0};
                             if constexpr (decltype(select)::value) {
@@ -587,6 +581,22 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                                     c0[r] = min(max(lo_of(key) - a, 0), TOK) * G;
                                     c1[r] = key < L ? min(max(hi_of(key) - a, 0), TOK) * G : c0[r];
                                 }
+                            }
+                            if constexpr (kCap) {
+                                // products of keys behind the last, or of no row, hold what was left in
+                                // shared memory: they have no say in the vote, or the roundings of the
+                                // others would depend on it
+                                if constexpr (decltype(select)::value) {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        const int r = (e >> 1) & 1, c = 32 * cc + 8 * (e >> 2) + 2 * c4 + (e & 1);
+                                        if (c < c0[r] || c >= c1[r]) x[e] = 0u;
+                                    }
+                                }
+                                float top = 0.f;
+#pragma unroll
+                                for (int e = 0; e < 16; e += 2) top = max3(top, fabsf(__uint_as_float(x[e])), fabsf(__uint_as_float(x[e + 1])));
+                                wt_cap(x, p, __any_sync(kFull, top > p.cap_far));
                             }
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -607,7 +617,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         };
                         // piece u: 16 keys (u & 1), 32 rows (u >> 1)
                         auto at = [&](int u) { return s_addr + (static_cast<uint32_t>(16 * (u & 1)) << 16) + 32 * (u >> 1); };
-                        if (wlo <= a && whi >= a + TOK && rows == 128) {
+                        if (wlo <= a && whi >= a + TOK && rows == 128 && (!kCap || k0 + 32 <= L)) {
                             uint32_t v[2][16];
                             wt_ld(at(0), v[0]);
                             wt_wait_ld(v[0]);

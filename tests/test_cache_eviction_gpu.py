@@ -180,6 +180,50 @@ def test_weights_repeat_bit_for_bit():
         assert torch.equal(a, weigh_both(p, max_query_len=200)[0])
 
 
+@pytest.mark.parametrize("softcap", [0.0, 5.0])
+def test_weights_do_not_depend_on_what_ran_before(softcap):
+    """Keys behind the length and columns without a row hold what an earlier call left in shared
+    memory: large values there change no bit."""
+    p = problem(12, new=[90, 41], lens=[150, 41], heads=14, kv=2, dim=128, page=16, dtype="bf16")
+    big = problem(13, new=[300], lens=[900], heads=14, kv=2, dim=128, page=16, dtype="bf16", spread=30.0)
+    lse = torch.full((131, 14), 3.0, device="cuda")
+    args = (p["q"].cuda(), p["cache"].cuda(), dev(p["table"]), dev(p["lens"]), dev(p["starts"]), lse, p["scale"])
+    good = pkd.key_weights(*args, softcap=softcap, max_query_len=90)
+    for huge in (1.0, 50.0):
+        cache = (big["cache"].float() * huge).to(torch.bfloat16).cuda()
+        for _ in range(2):
+            pkd.key_weights(big["q"].cuda(), cache, dev(big["table"]), dev(big["lens"]), dev(big["starts"]),
+                            torch.zeros((300, 14), device="cuda"), big["scale"], max_query_len=300)
+        assert torch.equal(pkd.key_weights(*args, softcap=softcap, max_query_len=90), good)
+
+
+def test_a_timeout_of_weights_is_reported_and_recovered_from():
+    p = problem(14, new=[1500, 700], lens=[1500, 700], heads=16, kv=8, dim=128, page=16, dtype="bf16")
+    lse = torch.full((2200, 16), 5.0, device="cuda")
+    args = (p["q"].cuda(), p["cache"].cuda(), dev(p["table"]), dev(p["lens"]), dev(p["starts"]), lse, p["scale"])
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    good = pkd.key_weights(*args, max_query_len=1500, workspace=ws)
+    assert pkd.workspace_check(ws) == pkd.OK
+    pkd.key_weights(*args, max_query_len=1500, workspace=ws, test_timeout=True)
+    assert pkd.workspace_check(ws) == pkd.ETIMEOUT
+    pkd.workspace_init(ws)
+    again = pkd.key_weights(*args, max_query_len=1500, workspace=ws)
+    assert pkd.workspace_check(ws) == pkd.OK and torch.equal(again, good)
+    pkd.key_weights(*args, max_query_len=1500, test_timeout=True)
+    assert pkd.workspace_check() == pkd.ETIMEOUT
+    assert torch.equal(pkd.key_weights(*args, max_query_len=1500), good)
+
+
+def test_weights_of_a_batch_whose_rows_stay():
+    """Few rows of many requests: runs of key blocks, some behind the last key, one unseen by a window."""
+    lens = [2000, 10, 700, 1300, 0, 257, 256]
+    p = problem(15, new=[12, 5, 9, 12, 0, 1, 12], lens=lens, heads=8, kv=2, dim=64, page=16, dtype="fp16")
+    got, want, err = weigh_both(p, max_query_len=12)
+    close(got, want, err, lens)
+    got, want, err = weigh_both(p, max_query_len=12, window=300, last=7)
+    close(got, want, err, lens)
+
+
 # ------------------------------------------------------------------ choice of the keys
 def select_both(weights, lens, budget, **opt):
     pos, ctx = opt.pop("positions", None), opt.pop("context", None)

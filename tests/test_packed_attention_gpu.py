@@ -104,13 +104,14 @@ def test_output_types(out_dtype):
     Packed([50, 20], Hq=4, Hkv=2, D=128, dtype="fp16", seed=1).verify("types", out_dtype)
 
 
-@pytest.mark.parametrize("bad", ["nan", "inf"])
-def test_other_prompts_do_not_enter(bad):
+@pytest.mark.parametrize("bad", ["nan", "inf", "1e4"])
+@pytest.mark.parametrize("softcap", [0.0, 5.0])
+def test_other_prompts_do_not_enter(bad, softcap):
     """A prompt's values reach its own tokens only, also inside a key tile that holds both."""
     p = Packed([70, 50, 90], Hq=4, Hkv=2, D=128, dtype="bf16", seed=10, extra=0)
-    good, lse = p.run()
+    good, lse = p.run(softcap=softcap)
     p.kv[70:120] = float(bad)
-    out, lse2 = p.run()
+    out, lse2 = p.run(softcap=softcap)
     for a, b in ((good, out), (lse, lse2)):
         assert torch.equal(a[:70], b[:70]) and torch.equal(a[120:210], b[120:210])
 
