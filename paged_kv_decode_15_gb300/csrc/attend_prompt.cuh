@@ -933,16 +933,9 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_con
 #pragma unroll
                                             for (int i = 0; i < 16; ++i) x[16 * e + i] = 0u;
                                         }
-                                    if constexpr (kPacked) {
-                                        // (nor have the next prompt's)
-                                        const int end = hi_all - tk - 32 * c;
-                                        if (end < 32) {
-#pragma unroll
-                                            for (int i = 0; i < 32; ++i)
-                                                if (i >= end) x[i] = 0u;
-                                        }
-                                    }
-                                    if (__any_sync(kFull, pt_max<true>(x) > cap_far))
+                                    // (nor has the next prompt: a chunk that ends in its keys is not polled)
+                                    const int end = kPacked ? hi_all - tk - 32 * c : 32;
+                                    if (end < 32 ? end > 0 : __any_sync(kFull, pt_max<true>(x) > cap_far))
                                         pt_cap<false>(x, p);
                                     else
                                         pt_cap<true>(x, p);
