@@ -422,11 +422,14 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         ok = pt_wait_queries(bar(S::B_UF + s), phase >> s & 1, p, it);
                         phase ^= 1u << s;
                     }
-                    // (a warp without a key tile keeps step with the other)
-                    ok = ok && (mine < 0 || pt_wait(bar(S::B_SE + 2 * t + buf), (sphase >> buf & 1) ^ 1, p));
+                    // (a block without a second key tile goes through all of the second one's
+                    // barriers, with nothing in them: what its warps wait for is then always
+                    // their own.  They once waited for the first tile's instead, whose phase of
+                    // two steps before they could take for the one to come)
+                    ok = ok && pt_wait(bar(S::B_SE + 2 * t + buf), (sphase >> buf & 1) ^ 1, p);
                     if (!ok) break;
+                    sphase ^= 1u << buf;
                     if (mine >= 0) {
-                        sphase ^= 1u << buf;
                         tc05::fence_after_sync();
                         const uint32_t qlo = tc05::uniform(lo0 + (s * S::UNIT >> 4)), d = tm + 128 * buf;
 #pragma unroll
@@ -435,8 +438,8 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                                 tc05::mma_ss<kFp8>(d, klo + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), tc05::desc_hi(S::GROUP),
                                                    qlo + (((kk >> 2) * kPtRows * 128 + (kk & 3) * 32) >> 4), tc05::desc_hi(1024), kId,
                                                    kk > 0);
-                        if (one) tc05::commit(bar(S::B_SF + 2 * t + buf));
                     }
+                    if (one) tc05::commit(bar(S::B_SF + 2 * t + buf));
                     if (!stay) {
                         if (one) tc05::commit(bar(S::B_UE + s));
                         slots.give(s);
@@ -497,8 +500,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             if (I.steps) load(0, x);
 #pragma unroll 1
             for (int k = 0; ok && k < I.blocks; ++k) {
-                const WtBlock blk = wt_block(p, I, k);
-                const int steps = blk.steps;
+                const int steps = wt_block(p, I, k).steps;
 #pragma unroll 1
                 for (int j = 0; j < steps; ++j, ++nl) {
                     const int buf = nl & 1;
@@ -512,7 +514,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                     *reinterpret_cast<float4*>(lse2 + 128 * buf + 4 * lane) = v;
                     __syncwarp();
                     // (the last step's with this buffer is over: all its readers have said so)
-                    if (lane < blk.nk) mbar_arrive(bar(S::B_SF + 2 * lane + buf));
+                    if (lane < 2) mbar_arrive(bar(S::B_SF + 2 * lane + buf));
                 }
             }
             __syncwarp();
@@ -530,7 +532,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         const float scale = kCap ? 1.f : p.scale_log2;
         const int rows = TOK * G;
         int step = 0;                 // steps before the item
-        uint32_t sphase = 0, phase0 = 0, xphase = 0;  // of this key tile's S, of tile 0's, of the sums
+        uint32_t sphase = 0, xphase = 0;  // of this key tile's S, of the sums
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const int ring = it % kWtItems;
@@ -559,10 +561,8 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 #pragma unroll 1
                 for (int j = (odd - step) & 1; j < steps; j += 2) {
                     const int a = i0 + j * TOK;
-                    // (a warp without a key tile keeps step with tile 0)
-                    if (!pt_wait(bar(S::B_SF + (active ? 2 * tile : 0) + odd), active ? sphase : phase0, p)) { ok = false; break; }
-                    phase0 ^= 1u;
-                    if (active) sphase ^= 1u;
+                    if (!pt_wait(bar(S::B_SF + 2 * tile + odd), sphase, p)) { ok = false; break; }
+                    sphase ^= 1u;
                     float2 n[16];  // LSEs of rows 8 k + 2 c4 and the next
 #pragma unroll
                     for (int k = 0; k < 16; ++k) n[k] = *reinterpret_cast<const float2*>(lse2 + 8 * k);
@@ -638,14 +638,14 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                                 piece(v, u & 1, u >> 1, std::true_type{});
                             }
                         }
-                        tc05::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * tile + odd));
 #pragma unroll
                         for (int hl = 0; hl < 2; ++hl)
 #pragma unroll
                             for (int r = 0; r < 2; ++r) total[hl][r] += acc[hl][r].x + acc[hl][r].y;
+                        tc05::fence_before_sync();
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * tile + odd));
                 }
                 if (!ok) break;
                 step += steps;

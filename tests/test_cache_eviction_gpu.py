@@ -214,6 +214,28 @@ def test_a_timeout_of_weights_is_reported_and_recovered_from():
     assert torch.equal(pkd.key_weights(*args, max_query_len=1500), good)
 
 
+@pytest.mark.parametrize("window,softcap", [(0, 0.0), (40, 0.0), (40, 5.0)])
+def test_weights_of_many_short_items(window, softcap):
+    """More items than SMs, of one to four query tiles, on blocks of one key tile and of two in turn:
+    every call has the same bits, and none runs into a wait's limit."""
+    lens = [150, 140, 67, 300, 149, 390, 81, 260]
+    p = problem(16, new=[150, 140, 67, 120, 149, 150, 81, 130], lens=lens, heads=128, kv=2, dim=64, page=16, dtype="bf16")
+    _, lse, _, _ = ragged_ref.attention(p["qv"], p["cv"], p["table"], p["lens"], p["starts"], p["scale"], window=window,
+                                        softcap=softcap)
+    lse = lse.astype(np.float32)
+    opt = dict(window=window, softcap=softcap)
+    got, want, err = weigh_both(p, lse=lse, max_query_len=150, **opt)
+    close(got, want, err, lens)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    args = (p["q"].cuda(), p["cache"].cuda(), dev(p["table"]), dev(p["lens"]), dev(p["starts"]), dev(lse), p["scale"])
+    for _ in range(60):
+        ws[256 + 4 * 65536:] = 255  # parts that are read before they are written show as NaN
+        again = pkd.key_weights(*args, max_query_len=150, workspace=ws, **opt)
+        assert torch.equal(again, got)
+    assert pkd.workspace_check(ws) == pkd.OK
+    assert not ws[256:256 + 4 * 65536].any()
+
+
 def test_weights_of_a_batch_whose_rows_stay():
     """Few rows of many requests: runs of key blocks, some behind the last key, one unseen by a window."""
     lens = [2000, 10, 700, 1300, 0, 257, 256]
