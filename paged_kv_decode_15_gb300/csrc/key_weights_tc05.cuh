@@ -638,14 +638,16 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                                 piece(v, u & 1, u >> 1, std::true_type{});
                             }
                         }
+                        tc05::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * tile + odd));
 #pragma unroll
                         for (int hl = 0; hl < 2; ++hl)
 #pragma unroll
                             for (int r = 0; r < 2; ++r) total[hl][r] += acc[hl][r].x + acc[hl][r].y;
-                        tc05::fence_before_sync();
+                    } else if (lane == 0) {
+                        mbar_arrive(bar(S::B_SE + 2 * tile + odd));
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(S::B_SE + 2 * tile + odd));
                 }
                 if (!ok) break;
                 step += steps;
