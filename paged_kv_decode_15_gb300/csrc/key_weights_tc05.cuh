@@ -545,11 +545,11 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 const WtBlock x = wt_block(p, I, kb);
                 const int steps = x.steps, k0 = x.t0 + 32 * pair;
                 const bool active = tile < x.nk;
-                // (asked for ahead: it is added at the block's end)
+                // the earlier weight of this lane's key comes near while the block is weighed
+                // (in a register all the while it cost a spill)
                 const int key = k0 + 8 * c4 + g;
-                float before = 0.f;
                 if (!odd && w.prior && key < min(L, I.fresh))
-                    before = w.prior[I.b * w.prior_b + I.hk * w.prior_h + key];
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(w.prior + I.b * w.prior_b + I.hk * w.prior_h + key));
                 // tokens [lo, hi) see a key
                 auto lo_of = [&](int key) { return p.causal ? max(i0, key - off) : i0; };
                 auto hi_of = [&](int key) {
@@ -694,6 +694,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                                 const int page = p.block_table[static_cast<long long>(I.b) * p.bt_stride + page_div(key, p.pmagic, p.pmshift)];
                                 if (page < 0 || page >= p.num_pages) mine = 0.f;
                             }
+                            const float before = w.prior && key < I.fresh ? w.prior[I.b * w.prior_b + I.hk * w.prior_h + key] : 0.f;
                             w.weights[I.b * w.weights_b + I.hk * w.weights_h + key] = fmaf(w.decay, before, mine);
                         }
                     }
