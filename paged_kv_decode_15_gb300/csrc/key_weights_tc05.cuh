@@ -17,7 +17,7 @@
 // Warp roles (640 threads): warps 0-3 and 4-7 the exponentials of key tile 0 and 1 at even
 // steps, 8-15 at odd ones (two S^T buffers a key tile, one for each; all warps at every step,
 // on 64 rows each, spent more on waits: 896 us
-// for 16384 tokens, not 849); warp 16
+// for 16384 tokens, not 849 then); warp 16
 // loads (items, K, Q), warps 17 and 19 issue the products of key tile 0 and 1 (one warp for
 // both left the tensor cores idle between them: its waits and the issue of a product take
 // as long as the product), warp 18 lays out the LSEs.  K and Q
@@ -27,7 +27,7 @@
 // NU - 2 query tiles.  Registers follow the roles (640 x 96 at launch = 512 x 104 + 128 x 64).
 // Every wait is bounded.
 //
-// What bounds it, D = 128 (16384-token prompt, 32 heads: 849 us, 1295 TFLOP/s, 0.68 of a dense
+// What bounds it, D = 128 (16384-token prompt, 32 heads: 875 us, 1257 TFLOP/s, 0.66 of a dense
 // library product): per step of two 128x128 products (1024 cycles) the exponentials take the
 // special-function units 1024 cycles, and a warp that is done with an S^T buffer meets
 // its next one 650 cycles later -- waits on barriers that answer in 200 to 300 cycles while
@@ -532,7 +532,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         const float scale = kCap ? 1.f : p.scale_log2;
         const int rows = TOK * G;
         int step = 0;                 // steps before the item
-        uint32_t sphase = 0, xphase = 0;  // of this key tile's S, of the sums
+        uint32_t phase = 0;           // of this key tile's S (bit 0), of the sums (bit 1)
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const int ring = it % kWtItems;
@@ -561,8 +561,8 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 #pragma unroll 1
                 for (int j = (odd - step) & 1; j < steps; j += 2) {
                     const int a = i0 + j * TOK;
-                    if (!pt_wait(bar(S::B_SF + 2 * tile + odd), sphase, p)) { ok = false; break; }
-                    sphase ^= 1u;
+                    if (!pt_wait(bar(S::B_SF + 2 * tile + odd), phase & 1, p)) { ok = false; break; }
+                    phase ^= 1u;
                     float2 n[16];  // LSEs of rows 8 k + 2 c4 and the next
 #pragma unroll
                     for (int k = 0; k < 16; ++k) n[k] = *reinterpret_cast<const float2*>(lse2 + 8 * k);
@@ -661,17 +661,17 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         }
                     float mine = c4 == 0 ? total[0][0] : c4 == 1 ? total[0][1] : c4 == 2 ? total[1][0] : total[1][1];
                     if (steps && odd) {
-                        if (!pt_wait(bar(S::B_XE + pair), xphase ^ 1, p)) { ok = false; break; }
+                        if (!pt_wait(bar(S::B_XE + pair), (phase >> 1) ^ 1, p)) { ok = false; break; }
                         *sum = mine;
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(S::B_XF + pair));
                     } else if (steps) {
-                        if (!pt_wait(bar(S::B_XF + pair), xphase, p)) { ok = false; break; }
+                        if (!pt_wait(bar(S::B_XF + pair), phase >> 1, p)) { ok = false; break; }
                         mine += *sum;
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(S::B_XE + pair));
                     }
-                    if (steps) xphase ^= 1;
+                    if (steps) phase ^= 2u;
                     if (!odd) {
                         bool whole = true;
                         if (I.nsplit > 1) {

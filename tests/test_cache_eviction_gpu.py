@@ -257,7 +257,7 @@ def select_both(weights, lens, budget, **opt):
 
 
 @pytest.mark.parametrize("S,budget", [(1, 1), (5, 5), (40, 8), (513, 512), (700, 1), (1500, 333), (5000, 4000)])
-@pytest.mark.parametrize("pool", [1, 5])
+@pytest.mark.parametrize("pool", [1, 5, 7, 33])
 def test_select(S, budget, pool):
     rng = np.random.default_rng(S + budget)
     lens = [S, S // 2, min(S, budget), min(S, budget + 1), 0]
@@ -311,6 +311,21 @@ def test_select_long(S, budget):
         assert torch.equal(kept[b].long(), want)
 
 
+@pytest.mark.parametrize("S,pool", [(9000, 255), (20000, 7), (140000, 5)])
+def test_select_pooled_over_several_ctas(S, pool):
+    """Neighbours across the CTAs of a row, and rows that are read again."""
+    g = torch.Generator(device="cuda").manual_seed(S)
+    w = torch.exp(2 * torch.randn((1, 2, S), device="cuda", generator=g))
+    lens = torch.tensor([S - 77], dtype=torch.int32, device="cuda")
+    kept, _ = pkd.evict_select(w, lens, 500, sinks=2, recent=30, pool=pool)
+    L, side = S - 77, pool // 2
+    x = w[..., :L].clone()
+    x[..., :2] = x[..., L - 30:] = -torch.inf
+    x = torch.nn.functional.pad(x, (side, side), value=-torch.inf).unfold(-1, pool, 1).amax(-1)
+    x[..., :2] = x[..., L - 30:] = torch.inf
+    assert torch.equal(kept[0].long(), x[0].sort(dim=-1, descending=True, stable=True)[1][:, :500].sort(-1)[0])
+
+
 # ------------------------------------------------------------------ compaction
 @pytest.mark.parametrize("dtype,dim,page", [("bf16", 128, 16), ("fp16", 64, 48), ("fp8", 128, 64), ("fp8", 64, 16)])
 @pytest.mark.parametrize("S,budget", [(40, 40), (300, 1), (300, 17), (900, 512), (900, 899)])
@@ -328,6 +343,19 @@ def test_compact(dtype, dim, page, S, budget):
     ref.cache_compact(want, p["table"], kept, n, (w, x))
     assert np.array_equal(cache.view(torch.uint8).cpu().numpy(), want)
     assert np.array_equal(dw.cpu().numpy(), w) and np.array_equal(dx.cpu().numpy(), x)
+
+
+@pytest.mark.parametrize("budget", [10240, 11000])
+def test_compact_long_lists(budget):
+    """Lists that fill shared memory, and such as are searched where they are."""
+    rng = np.random.default_rng(budget)
+    p = problem(22, new=[1], lens=[12000], heads=2, kv=2, dim=64, page=16, dtype="fp16")
+    kept, n = ref.evict_select(rng.random((1, 2, 12000)), [12000], budget)
+    cache = p["cache"].cuda()
+    pkd.cache_compact(cache, dev(p["table"]), dev(kept), dev(n))
+    want = p["cache"].view(torch.int16).numpy().copy()
+    ref.cache_compact(want, p["table"], kept, n)
+    assert np.array_equal(cache.view(torch.int16).cpu().numpy(), want)
 
 
 def test_compact_bad_pages_and_indexes_move_nothing():
