@@ -6,8 +6,10 @@
 // and no more rows move than must.  The m-th free slot is m + i, i the first kept row
 // with kept[i] - i > m (kept[i] - i slots are free before it): a binary search, in shared
 // memory, where every CTA of a (request, kv head) has its kept list (longer ones are
-// searched where they are).  Bound by the rows' bytes, read and written; for few rows
-// by the chain lengths - list - table - rows of trips to memory.
+// searched where they are).  Bound by the rows' bytes, read and written (32 lists of 4096
+// of up to 32768 keys, 512-byte rows: 24.8 us, 4.5 TB/s, 0.67 of the copy); for few rows by
+// the chain lengths - list - table - rows of trips to memory (512 lists of 1024 of 1088
+// keys: 8.6 us, of which the bytes take 5).  Searched in global memory: 31 and 22 us.
 #include <algorithm>
 
 #include "evict.cuh"

@@ -473,3 +473,32 @@ def test_a_captured_step_of_eviction(side):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(args[1], moved) and torch.equal(kept, kept2) and torch.equal(n, n2)
+
+
+def test_calls_on_two_streams_and_graphs_at_once():
+    """Weights on two streams, each with the workspace kept for it, and in two graphs that are
+    replayed side by side: split tokens, so that counters and parts are in use."""
+    p = problem(41, new=[700], lens=[900], heads=16, kv=2, dim=128, page=16, dtype="bf16")
+    lse = torch.full((700, 16), 6.0, device="cuda")
+    args = (p["q"].cuda(), p["cache"].cuda(), dev(p["table"]), dev(p["lens"]), dev(p["starts"]), lse, p["scale"])
+    good = pkd.key_weights(*args)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs, outs = [], []
+    for _ in streams:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(pkd.key_weights(*args))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(pkd.key_weights(*args))
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, good) for x in got + outs)
+    assert pkd.workspace_check(stream=streams[0]) == pkd.workspace_check(stream=streams[1]) == pkd.OK
