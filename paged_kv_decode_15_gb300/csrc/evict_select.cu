@@ -5,7 +5,7 @@
 // 11 bits, then, among the keys that share those of the threshold, of the next 11 and of
 // the last 10 (fewer where a histogram ends on a bin of which all keys stay): counts
 // in shared memory by integer atomics, whose order changes nothing, and a scan from the
-// top.  Keys without any weight, often a third of them, are counted apart by votes.  Then
+// top.  Keys without any weight, often a third of them, are counted apart, by thread.  Then
 // the keys above the threshold, and as many of those on it as are still missing, the
 // lowest indexes first, are written in the order of the keys: a thread owns consecutive
 // keys, counts, and writes behind the threads before it.
@@ -45,7 +45,7 @@ __device__ __forceinline__ uint32_t rank_of(float x) {
 }
 
 struct SelectShared {
-    int hist[kSelBins];
+    int hist[2][kSelBins];                  // of this round, of the next
     int warp_sum[16], above[16], on[16];
     int found[3];                           // the threshold's bin, keys still missing in it, its count
     int cta_above[kSelMaxCluster], cta_on[kSelMaxCluster];
@@ -93,24 +93,32 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
         extern __shared__ float stage[];
         const int c0 = rank * kSelThreads * own, span = kSelThreads * own + 2 * side;  // stage[0] is key c0 - side
         auto word = [](int i) { return i + i / 32; };
-        for (int i0 = tid; i0 < span; i0 += 4 * kSelThreads) {
-            float x[4];
+        if (pos) {
+            for (int i0 = tid; i0 < span; i0 += 4 * kSelThreads) {
+                uint32_t x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = i0 + e * kSelThreads, t = c0 - side + i;
-                x[e] = -INFINITY;
-                if (i < span && t >= 0 && t < L) {
-                    if (pos) {
+                for (int e = 0; e < 4; ++e) {
+                    const int t = c0 + i0 + e * kSelThreads;
+                    x[e] = 0;
+                    if (i0 + e * kSelThreads < span && t < L) {
                         const int at = pos[t];
-                        x[e] = __uint_as_float(at < first || at >= past ? kRankKept : rank_of(w[t]));
-                    } else {
-                        x[e] = masked(t);
+                        x[e] = at < first || at >= past ? kRankKept : rank_of(w[t]);
                     }
                 }
-            }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (i0 + e * kSelThreads < span) stage[word(i0 + e * kSelThreads)] = x[e];
+                for (int e = 0; e < 4; ++e)
+                    if (i0 + e * kSelThreads < span) stage[word(i0 + e * kSelThreads)] = __uint_as_float(x[e]);
+            }
+        } else {
+            // (asynchronous copies: all of a thread's weights in flight)
+            for (int i = tid; i < span; i += kSelThreads) {
+                const int t = c0 - side + i;
+                if (t >= first && t < past && t < L)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(stage + word(i))), "l"(w + t) : "memory");
+                else
+                    stage[word(i)] = -INFINITY;
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
         __syncthreads();
         // the largest weight around each of the thread's keys (a NaN beside a number counts not)
@@ -168,6 +176,8 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
     // ------------------------------------------------------ the threshold
     // a thread of the scan reads `kPer` neighbouring bins: they lie a row apart, threads side by side
     auto place = [&](int bin) { return (bin % kPer) * kSelThreads + bin / kPer; };
+    for (int i = tid; i < 2 * kSelBins; i += kSelThreads) sh.hist[0][i] = 0;
+    if constexpr (kCluster) cg::this_cluster().sync(); else __syncthreads();
     uint32_t prefix = 0;
     int missing = n, shift = 32;
 #pragma unroll 1
@@ -175,22 +185,24 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
         const int bits = round < 2 ? 11 : 10, bins = 1 << bits;
         const int up = shift;  // bits below the prefix
         shift -= bits;
-        for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[i] = 0;
-        if constexpr (kCluster) cg::this_cluster().sync(); else __syncthreads();
+        int* hist = sh.hist[round & 1];
+        if (round)  // read by the first CTA in the round before, wanted again in the next one
+            for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[(round + 1) & 1][i] = 0;
         int zeros = 0;
         each([&](uint32_t x, int) {
             const bool in = x != 0 && (round == 0 || (x >> (up & 31)) == prefix), zero = in && x == kRankZero;
-            zeros += __popc(__ballot_sync(kFull, zero));
-            if (in && !zero) atomicAdd(&sh.hist[place((x >> shift) & (bins - 1))], 1);
+            zeros += zero;
+            if (in && !zero) atomicAdd(&hist[place((x >> shift) & (bins - 1))], 1);
         });
-        if (lane == 0 && zeros) atomicAdd(&sh.hist[place((kRankZero >> shift) & (bins - 1))], zeros);
+        zeros = __reduce_add_sync(kFull, zeros);
+        if (lane == 0 && zeros) atomicAdd(&hist[place((kRankZero >> shift) & (bins - 1))], zeros);
         if constexpr (kCluster) {
             // the counts of all CTAs, in the first one's
             __syncthreads();
-            int* total = cg::this_cluster().map_shared_rank(sh.hist, 0);
+            int* total = cg::this_cluster().map_shared_rank(hist, 0);
             if (rank)
                 for (int i = tid; i < kSelBins; i += kSelThreads)
-                    if (sh.hist[i]) atomicAdd(total + i, sh.hist[i]);
+                    if (hist[i]) atomicAdd(total + i, hist[i]);
             cg::this_cluster().sync();
         } else {
             __syncthreads();
@@ -202,7 +214,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
             int c[kPer], mine = 0;
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
-                c[e] = sh.hist[(kPer - 1 - e) * kSelThreads + top];
+                c[e] = hist[(kPer - 1 - e) * kSelThreads + top];
                 mine += c[e];
             }
             int sum = mine;
