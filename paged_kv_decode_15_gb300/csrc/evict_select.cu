@@ -11,16 +11,18 @@
 // keys, counts, and writes behind the threads before it.
 //
 // A row is read once, through shared memory (whose words are spread so that threads KPT
-// keys apart seldom meet in a bank), where the neighbours of a pooled weight are too; ranks stay
-// in registers, up to KPT per thread (0: rows too long for that are read again in every
+// keys apart seldom meet in a bank), where the neighbours of a pooled weight are too; ranks
+// stay in registers, up to KPT per thread (0: rows too long for that are read again in every
 // pass).  Long rows, and few rows, are spread over a cluster of CTAs that add their
 // histograms up in the first one's shared memory.
 //
-// What bounds it (512 rows of 1024 to 4096 keys, pooled over 7: 15.6 us; 32 rows of up to
-// 131072 keys, clusters of eight: 27 us; eight rows of 1088 keys: 6.3 us; bytes alone would
-// take 1, 2 and 0 us): instructions and barriers of the two or three rounds.  Three bits a
-// round, counted in registers, took 124 and 567 us; pooled from global memory 18.4; the
-// scan's bins side by side, not a row apart, three more.
+// What bounds it (512 rows of 1024 to 4096 keys, pooled over 7: 15.5 us; 32 rows of up to
+// 131072 keys, clusters of eight: 25.5 us, one such row 23; eight rows of 1088 keys: 6.5 us;
+// bytes alone would take 1, 2, 0 and 0 us): the chain of two or three rounds, each a pass
+// over a thread's keys, a scan and its barriers.  Three bits a round, counted in registers,
+// took 124 and 567 us; pooled from global memory 18.4; three cluster barriers a round, not
+// two, 27; ranks in shared memory, walked in rolled loops (the unrolled ones wait for their
+// instructions), 17.9 and 24.4.
 #include <cooperative_groups.h>
 
 #include <type_traits>
