@@ -7,9 +7,9 @@
 // with kept[i] - i > m (kept[i] - i slots are free before it): a binary search, in shared
 // memory, where every CTA of a (request, kv head) has its kept list (longer ones are
 // searched where they are).  Bound by the rows' bytes, read and written (32 lists of 4096
-// of up to 32768 keys, 512-byte rows: 24.8 us, 4.5 TB/s, 0.67 of the copy); for few rows by
+// of up to 32768 keys, 512-byte rows: 24.1 us, 4.7 TB/s, 0.69 of the copy); for few rows by
 // the chain lengths - list - table - rows of trips to memory (512 lists of 1024 of 1088
-// keys: 8.6 us, of which the bytes take 5).  Searched in global memory: 31 and 22 us.
+// keys: 6.2 us, of which the bytes take 5).  Searched in global memory: 31 and 22 us.
 #include <algorithm>
 
 #include "evict.cuh"
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kCompactThreads, 4) cache_compact_kernel(const
 #pragma unroll
             for (int i = 0; i < kCompactFlight; ++i) {
                 const long long f = __shfl_sync(kFull, from, (k + i * R + lane / LANES) & 31);
-                if (f >= 0) v[i] = __ldcs(reinterpret_cast<const uint4*>(p.cache + f * ROWB) + part);
+                if (f >= 0) v[i] = __ldcg(reinterpret_cast<const uint4*>(p.cache + f * ROWB) + part);
             }
 #pragma unroll
             for (int i = 0; i < kCompactFlight; ++i) {
@@ -114,11 +114,12 @@ __global__ void __launch_bounds__(kCompactThreads, 4) cache_compact_kernel(const
 
 template <int LANES>
 static cudaError_t launch_one(const CompactParams& p, cudaStream_t stream) {
-    // CTAs of a (request, kv head): about four per SM in all, no more than its rows feed
+    // CTAs of a (request, kv head): four per SM in all at most (one wave: a second one cost 1.4
+    // of 7.6 us where 512 lists got two CTAs each), no more than its rows feed
     constexpr int kRows = 32 / LANES * kCompactFlight * kCompactWarps;
     const long long units = static_cast<long long>(p.B) * p.H;
     const int most = std::min((p.budget + kRows - 1) / kRows, 65535);
-    const int parts = static_cast<int>(std::max(1ll, std::min<long long>(most, (4 * 152 + units - 1) / units)));
+    const int parts = static_cast<int>(std::max(1ll, std::min<long long>(most, 4 * 152 / std::max(units, 1ll))));
     const size_t smem = p.budget <= kCompactList ? p.budget * sizeof(int32_t) : 0;
     cache_compact_kernel<LANES><<<dim3(parts, p.H, p.B), kCompactThreads, smem, stream>>>(p);
     return cudaGetLastError();
