@@ -989,6 +989,8 @@ def cache_compact(kv_cache, block_table, kept, kept_lens, *, weights=None, posit
         raise ValueError(f"kept must be contiguous int32 [{B}, {H}, budget]")
     w, wb, wh, weight_keys = _key_rows(weights, B, H, _F32, "weights")
     x, xb, xh, position_keys = _key_rows(positions, B, H, _I32, "positions")
+    if (weights is not None and weight_keys == 0) or (positions is not None and position_keys == 0):
+        raise ValueError("weights and positions must have keys")  # (no address: rows would move without them)
     status = (_lib or load_library()).pkd_cache_compact(
         kv_cache.data_ptr(), _code(kv_cache.dtype), num_pages, block_table.data_ptr(), stride, columns, kept.data_ptr(),
         kept_lens.data_ptr(), B, H, D, P, kept.shape[2], w, wb, wh, weight_keys, x, xb, xh, position_keys,

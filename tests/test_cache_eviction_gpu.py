@@ -358,6 +358,16 @@ def test_compact_long_lists(budget):
     assert np.array_equal(cache.view(torch.int16).cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("name,dtype", [("weights", torch.float32), ("positions", torch.int32)])
+def test_compact_refuses_arrays_without_keys(name, dtype):
+    p = problem(23, new=[1], lens=[40], heads=2, kv=2, dim=64, page=16, dtype="bf16")
+    kept, n = ref.evict_select(np.arange(80.).reshape(1, 2, 40), [40], 8)
+    cache = p["cache"].cuda()
+    with pytest.raises(ValueError, match="must have keys"):
+        pkd.cache_compact(cache, dev(p["table"]), dev(kept), dev(n), **{name: torch.empty((1, 2, 0), dtype=dtype, device="cuda")})
+    assert torch.equal(cache.cpu().view(torch.int16), p["cache"].view(torch.int16))
+
+
 def test_compact_bad_pages_and_indexes_move_nothing():
     rng = np.random.default_rng(21)
     p = problem(21, new=[1] * 2, lens=[200, 200], heads=2, kv=2, dim=128, page=16, dtype="bf16")
