@@ -341,6 +341,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         have = true;
                     }
                     const int krow = stage_row(k, page);
+                    __syncwarp();  // scan[24] before lane 0's arrival
                     int ks[2] = {0, 0};
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
