@@ -67,7 +67,8 @@ struct WtShape {
     static constexpr int NU = UNIT == 32768 ? 6 : 12;
     static constexpr int OFF_LSE = NU * UNIT;
     static constexpr int OFF_SUM = OFF_LSE + 2 * 128 * 4;  // a block's sums of odd steps, for the warps of even ones
-    static constexpr int OFF_ITEM = OFF_SUM + kWtKeys * 4;
+    static constexpr int OFF_NONE = OFF_SUM + kWtKeys * 4;  // per buffer of LSEs: some token's is -inf
+    static constexpr int OFF_ITEM = OFF_NONE + 2 * 4;
     static constexpr int OFF_PREF = OFF_ITEM + kWtItems * static_cast<int>(sizeof(WtItem));
     static constexpr int OFF_SCAN = OFF_PREF + (kPtMaxBatch + 4) * 4;
     static constexpr int OFF_BAR = (OFF_SCAN + 128 + 7) & ~7;
@@ -474,6 +475,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         reg_dec<kWtRegsOther>();
         // ------------------------------------- the rows' LSEs, as added to logits
         float* lse2 = reinterpret_cast<float*>(smem + S::OFF_LSE);
+        int* none = reinterpret_cast<int*>(smem + S::OFF_NONE);
         int nl = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
@@ -505,6 +507,10 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 #pragma unroll 1
                 for (int j = 0; j < steps; ++j, ++nl) {
                     const int buf = nl & 1;
+                    bool dead = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dead |= x[e] == -INFINITY && col[e] >= 0 && i0 + j * TOK + tok[e] < i1;
+                    dead = __any_sync(kFull, dead);
                     float4 v;
                     v.x = x[0] == -INFINITY ? x[0] : -kLog2e * x[0];
                     v.y = x[1] == -INFINITY ? x[1] : -kLog2e * x[1];
@@ -513,6 +519,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                     if (steps > 1) load(j + 1 < steps ? j + 1 : 0, x);
                     if (!pt_wait(bar(S::B_LE + buf), ((nl >> 1) & 1) ^ 1, p)) { ok = false; break; }
                     *reinterpret_cast<float4*>(lse2 + 128 * buf + 4 * lane) = v;
+                    if (lane == 0) none[buf] = dead;
                     __syncwarp();
                     // (the last step's with this buffer is over: all its readers have said so)
                     if (lane < 2) mbar_arrive(bar(S::B_SF + 2 * lane + buf));
@@ -528,6 +535,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         const int odd = warp >> 3, tile = (warp >> 2) & 1, q4 = warp & 3, pair = warp & 7, g = lane >> 2, c4 = lane & 3;
         const uint32_t s_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16) + 128 * (2 * tile + odd);
         const float* lse2 = reinterpret_cast<const float*>(smem + S::OFF_LSE) + 128 * odd + 2 * c4;
+        const int* none = reinterpret_cast<const int*>(smem + S::OFF_NONE) + odd;
         // lane (g, c4) ends up with the sum of key 8 c4 + g of its warp's 32
         float* sum = reinterpret_cast<float*>(smem + S::OFF_SUM) + 32 * pair + 8 * c4 + g;
         const float scale = kCap ? 1.f : p.scale_log2;
@@ -567,6 +575,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                     float2 n[16];  // LSEs of rows 8 k + 2 c4 and the next
 #pragma unroll
                     for (int k = 0; k < 16; ++k) n[k] = *reinterpret_cast<const float2*>(lse2 + 8 * k);
+                    const bool dead = *none;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(S::B_LE + odd));
                     if (active) {
@@ -581,6 +590,17 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                                     const int key = k0 + 16 * hl + 8 * r + g;
                                     c0[r] = min(max(lo_of(key) - a, 0), TOK) * G;
                                     c1[r] = key < L ? min(max(hi_of(key) - a, 0), TOK) * G : c0[r];
+                                }
+                            }
+                            // a token of LSE -inf weighs nothing, whatever its q holds (padding may hold
+                            // NaN, which adding -inf would keep)
+                            if constexpr (decltype(select)::value) {
+                                if (dead) {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        const float2 m = n[4 * cc + (e >> 2)];
+                                        if ((e & 1 ? m.y : m.x) == -INFINITY) x[e] = 0u;
+                                    }
                                 }
                             }
                             if constexpr (kCap) {
@@ -618,7 +638,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         };
                         // piece u: 16 keys (u & 1), 32 rows (u >> 1)
                         auto at = [&](int u) { return s_addr + (static_cast<uint32_t>(16 * (u & 1)) << 16) + 32 * (u >> 1); };
-                        if (wlo <= a && whi >= a + TOK && rows == 128 && (!kCap || k0 + 32 <= L)) {
+                        if (wlo <= a && whi >= a + TOK && rows == 128 && !dead && (!kCap || k0 + 32 <= L)) {
                             uint32_t v[2][16];
                             wt_ld(at(0), v[0]);
                             wt_wait_ld(v[0]);

@@ -1,0 +1,54 @@
+"""Weights of keys where they can go wrong, on each plan of the kernels: the step grid, query
+tiles that stay, query tiles that stream past (their tokens split)."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_decode_15_gb300 as pkd
+from tests import eviction_ref as ref
+from tests import ragged_ref
+from tests.test_cache_eviction_gpu import close, dev, problem
+
+pytestmark = pytest.mark.gpu
+
+# tokens of two requests; 4 heads to a kv head
+PLANS = {"step": (3, 2), "stay": (40, 33), "stream": (700, 90)}
+
+
+def plan(name, seed, *, lens=None, dtype="bf16", dim=128):
+    new = PLANS[name]
+    return problem(seed, new=list(new), lens=lens or [max(new[0], 300), 210], heads=8, kv=2, dim=dim, page=16, dtype=dtype)
+
+
+def lses(p, **mask):
+    return ragged_ref.attention(p["qv"], p["cv"], p["table"], p["lens"], p["starts"], p["scale"], **mask)[1].astype(np.float32)
+
+
+def call(p, lse, *, cache=None, table=None, lens=None, **opt):
+    n = np.diff(p["starts"]).max()
+    return pkd.key_weights(p["q"].cuda(), (p["cache"] if cache is None else cache).cuda(),
+                           dev(p["table"] if table is None else table), dev(p["lens"] if lens is None else lens),
+                           dev(p["starts"]), dev(lse), p["scale"], max_query_len=int(n), **opt)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("opt", [dict(), dict(softcap=5.0), dict(window=50), dict(causal=False, softcap=5.0)])
+@pytest.mark.parametrize("name", PLANS)
+def test_tokens_of_no_lse_weigh_nothing_whatever_they_hold(name, opt, bad):
+    """A padding token: LSE -inf, q not finite; of one head of a token too.  The last key is seen by
+    such a token alone (causal), and holds NaN."""
+    p = plan(name, 1)
+    lse = lses(p, **opt)
+    n = int(p["starts"][1])
+    q, cache = p["q"].clone(), p["cache"].clone()
+    for t in {0, n // 2 if n > 3 else 0, n - 1}:
+        q[t] = bad
+        lse[t] = -np.inf
+    q[n + 1, 3] = bad
+    lse[n + 1, 3] = -np.inf
+    if opt.get("causal", True):
+        t = int(p["lens"][0]) - 1
+        cache[p["table"][0, t // 16], :, t % 16] = float("nan")
+    want, err = ref.key_weights(p["qv"], p["cv"], p["table"], p["lens"], p["starts"], lse.astype(np.float64), p["scale"], **opt)
+    p["q"] = q
+    close(call(p, lse, cache=cache, **opt), want, err, p["lens"])
