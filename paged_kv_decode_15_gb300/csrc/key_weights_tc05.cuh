@@ -703,6 +703,7 @@ key_weights_tc05_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                             int prev = 0;
                             if (lane == 0) prev = atom_add_acq_rel_gpu(p.counters + 8 * I.unit + pair);
                             prev = __shfl_sync(kFull, prev, 0);
+                            __syncwarp();  // lane 0's acquire comes before all lanes' reads of the other parts
                             whole = prev == I.nsplit - 1;
                             if (whole) {
                                 mine = 0.f;

@@ -52,3 +52,19 @@ def test_tokens_of_no_lse_weigh_nothing_whatever_they_hold(name, opt, bad):
     want, err = ref.key_weights(p["qv"], p["cv"], p["table"], p["lens"], p["starts"], lse.astype(np.float64), p["scale"], **opt)
     p["q"] = q
     close(call(p, lse, cache=cache, **opt), want, err, p["lens"])
+
+
+def test_parts_of_split_tokens_are_joined_from_what_other_ctas_wrote():
+    """Six parts of a block's tokens, whose place in the workspace holds NaN before every call: the
+    same bits each time, and the workspace ready for the next call."""
+    p = problem(13, new=[700], lens=[1000], heads=8, kv=2, dim=64, page=16, dtype="bf16")
+    lse = lses(p)
+    want, err = ref.key_weights(p["qv"], p["cv"], p["table"], p["lens"], p["starts"], lse.astype(np.float64), p["scale"])
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    args = (p["q"].cuda(), p["cache"].cuda(), dev(p["table"]), dev(p["lens"]), dev(p["starts"]), dev(lse), p["scale"])
+    good = pkd.key_weights(*args, workspace=ws)
+    close(good, want, err, p["lens"])
+    for _ in range(200):
+        ws[256 + 4 * 65536:] = 255
+        assert torch.equal(pkd.key_weights(*args, workspace=ws), good)
+    assert pkd.workspace_check(ws) == pkd.OK and not ws[256:256 + 4 * 65536].any()
