@@ -507,7 +507,8 @@ pkd_status pkd_key_weights(const void* q, pkd_dtype q_dtype, int64_t q_stride, c
  *                seen.  NULL both: key t stands at t of seq_lens[b]
  *   kept         device int32 [batch, num_kv_heads, budget]: the indexes of the
  *                n = min(seq_lens[b], budget) keys that stay, rising; -1 behind them
- *   kept_lens    device int32 [batch]: n
+ *   kept_lens    device int32 [batch]: n.  Neither kept nor kept_lens may overlap an
+ *                input (kept_lens may not be seq_lens) or the other
  *
  * Kept are the keys at the first `sinks` and the last `recent` positions, then those of
  * the largest weight, of equal ones the lowest index.  pool (odd, up to 255): a key's

@@ -22,6 +22,16 @@ pkd_status check_rows(const void* p, int64_t sb, int64_t sh, int64_t keys, bool 
     return PKD_OK;
 }
 
+// The bytes of 4-byte values [B, H] rows of `keys` (none: not given).
+struct Span {
+    uintptr_t from, past;
+    bool meets(const Span& x) const { return from < x.past && x.from < past; }
+};
+Span span_of(const void* p, int64_t sb, int64_t sh, int64_t B, int64_t H, int64_t keys) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    return {at, p && keys > 0 ? at + 4 * ((B - 1) * sb + (H - 1) * sh + keys) : at};
+}
+
 pkd_status check_sizes(int B, int H, int64_t keys, int budget) {
     if (B < 0 || H < 1 || keys < 0 || budget < 1)
         return report(PKD_EINVAL, "invalid shape: batch=%d num_kv_heads=%d keys=%lld budget=%d", B, H, (long long)keys, budget);
@@ -59,6 +69,16 @@ pkd_status pkd_evict_select(const float* weights, int64_t weights_batch_stride, 
     if (st != PKD_OK) return st;
     st = check_rows(positions, positions_batch_stride, positions_head_stride, keys, false, batch, num_kv_heads, "positions");
     if (st != PKD_OK) return st;
+    // results are written while other CTAs still read: a length that became kept_lens, say
+    const int64_t rows = (int64_t)batch * num_kv_heads;
+    const Span in[4] = {span_of(weights, weights_batch_stride, weights_head_stride, batch, num_kv_heads, keys),
+                        span_of(positions, positions_batch_stride, positions_head_stride, batch, num_kv_heads, keys),
+                        span_of(seq_lens, 1, 0, batch, 1, 1), span_of(context_lens, 1, 0, batch, 1, 1)};
+    const Span to = span_of(kept, budget, 0, rows, 1, budget), lens = span_of(kept_lens, 1, 0, batch, 1, 1);
+    for (const Span& x : in)
+        if (x.meets(to) || x.meets(lens))
+            return report(PKD_EINVAL, "kept or kept_lens overlaps weights, positions, seq_lens or context_lens");
+    if (to.meets(lens)) return report(PKD_EINVAL, "kept overlaps kept_lens");
     pkd::SelectParams p = {};
     p.weights = weights;
     p.positions = positions;

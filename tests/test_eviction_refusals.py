@@ -1,0 +1,30 @@
+"""More refusals of the operators that bound a paged cache, without a GPU: calls that were taken
+and gave wrong results or lost rows."""
+import ctypes
+
+import pytest
+
+import paged_kv_decode_15_gb300 as pkd
+from tests.test_eviction_boundary import lib, select  # noqa: F401  (lib: a fixture)
+
+
+def at(address):
+    return ctypes.c_void_p(address)
+
+
+# one call's arrays, far apart: 2 requests, 2 kv heads, 100 keys in rows of 200 and 100 values, budget 50
+APART = dict(weights=at(1 << 20), lens=at(2 << 20), kept=at(3 << 20), kept_lens=at(4 << 20))
+MOVED = dict(APART, positions=at(5 << 20), context=at(6 << 20))
+
+
+@pytest.mark.parametrize("base,over,needle", [
+    (APART, dict(kept_lens=at(2 << 20)), "overlaps weights, positions, seq_lens"),       # lengths that change under the readers
+    (APART, dict(kept_lens=at((2 << 20) + 4)), "overlaps"), (APART, dict(kept_lens=at((2 << 20) - 4)), "overlaps"),
+    (APART, dict(kept=at(1 << 20)), "overlaps"), (APART, dict(kept=at((1 << 20) + 4 * 399)), "overlaps"),
+    (APART, dict(kept=at((1 << 20) - 4 * 199)), "overlaps"), (APART, dict(kept_lens=at((1 << 20) + 4 * 150)), "overlaps"),
+    (APART, dict(kept=at((2 << 20) - 4 * 199)), "overlaps"), (APART, dict(kept_lens=at((3 << 20) + 4 * 199)), "kept overlaps kept_lens"),
+    (MOVED, dict(kept=at(5 << 20)), "overlaps"), (MOVED, dict(kept_lens=at(6 << 20)), "overlaps")])
+def test_select_refuses_results_that_lie_in_its_inputs(lib, base, over, needle):
+    assert select(lib, **{**base, **over}) == pkd.EINVAL
+    assert needle in lib.pkd_last_error().decode()
+
