@@ -467,7 +467,7 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
  *   last_queries w > 0: only the last w tokens of each request weigh its keys
  *   lse          device fp32 [total_tokens, num_heads]; a token of lse -inf weighs nothing
  *   prior        device fp32 [batch, num_kv_heads, >= max_kv_len], or NULL: 0.  Rows
- *                of keys contiguous, strides in elements.  Not read for keys of the
+ *                of keys contiguous, strides in elements (up to 2^40).  Not read for keys of the
  *                call's own tokens (the last query_start[b + 1] - query_start[b] of
  *                seq_lens[b]), nor behind seq_lens[b]: they start at 0
  *   weights      device fp32, laid out like prior with strides of its own; may be prior
@@ -499,7 +499,7 @@ pkd_status pkd_key_weights(const void* q, pkd_dtype q_dtype, int64_t q_stride, c
  * The keys of each request and kv head that stay in a cache of at most `budget` keys.
  *
  *   weights      device fp32 [batch, num_kv_heads, keys], rows contiguous, strides in
- *                elements.  NaN counts as -inf
+ *                elements (up to 2^40).  NaN counts as -inf
  *   seq_lens     device int32 [batch], clamped to [0, keys]
  *   positions    device int32 [batch, num_kv_heads, keys]: where in its request each key
  *                stood, once earlier compactions have put them out of order, with

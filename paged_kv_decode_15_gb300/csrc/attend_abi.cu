@@ -721,6 +721,11 @@ pkd_status pkd_key_weights(const void* q, pkd_dtype q_dtype, int64_t q_stride, c
     if (!aligned(lse, 4) || !aligned(prior, 4) || !aligned(weights, 4))
         return report(PKD_EINVAL, "lse, prior and weights must be 4-byte aligned");
     if (!std::isfinite(decay)) return report(PKD_EINVAL, "decay must be finite");
+    // (sums of strides and keys stay far from 2^63)
+    const int64_t most = (int64_t)1 << 40;
+    if ((batch > 1 && (weights_batch_stride > most || (prior && prior_batch_stride > most))) ||
+        (num_kv_heads > 1 && (weights_head_stride > most || (prior && prior_head_stride > most))))
+        return report(PKD_EUNSUPPORTED, "weights and prior strides must not be above 2^40");
     if (!rows_apart(weights_batch_stride, weights_head_stride, batch, num_kv_heads, max_kv_len))
         return report(PKD_EINVAL, "weights strides %lld, %lld: rows of max_kv_len keys overlap",
                       (long long)weights_batch_stride, (long long)weights_head_stride);

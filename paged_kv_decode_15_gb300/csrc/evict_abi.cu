@@ -8,6 +8,7 @@ namespace {
 using pkd::report;
 
 constexpr int kMaxKeys = 1 << 29;
+constexpr int64_t kMaxStride = (int64_t)1 << 40;
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -15,6 +16,9 @@ bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 pkd_status check_rows(const void* p, int64_t sb, int64_t sh, int64_t keys, bool written, int B, int H, const char* name) {
     if (!p) return PKD_OK;
     if (!aligned(p, 4)) return report(PKD_EINVAL, "%s must be 4-byte aligned", name);
+    // (sums of strides and keys stay far from 2^63)
+    if ((B > 1 && sb > kMaxStride) || (H > 1 && sh > kMaxStride))
+        return report(PKD_EUNSUPPORTED, "%s strides %lld, %lld: more than 2^40", name, (long long)sb, (long long)sh);
     const bool apart = ((H == 1 || sh >= keys) && (B == 1 || sb >= (H - 1) * sh + keys)) ||
                        ((B == 1 || sb >= keys) && (H == 1 || sh >= (B - 1) * sb + keys));
     if (sb < 0 || sh < 0 || (written && !apart))

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 import paged_kv_decode_15_gb300 as pkd
-from tests.test_eviction_boundary import lib, select  # noqa: F401  (lib: a fixture)
+from tests.test_eviction_boundary import compact, lib, select, weigh  # noqa: F401  (lib: a fixture)
 
 
 def at(address):
@@ -28,3 +28,15 @@ def test_select_refuses_results_that_lie_in_its_inputs(lib, base, over, needle):
     assert select(lib, **{**base, **over}) == pkd.EINVAL
     assert needle in lib.pkd_last_error().decode()
 
+
+WRAP = (1 << 63) // 7 + 1  # seven such head strides are past 2^63, where a batch stride of 0 seemed to be enough
+
+
+@pytest.mark.parametrize("call,over", [
+    (weigh, dict(Hq=8, Hkv=8, q_stride=1024, wh=WRAP, wb=0)), (weigh, dict(wb=1 << 41)), (weigh, dict(wh=1 << 41, wb=1 << 42)),
+    (weigh, dict(prior=at(1 << 20), pb=1 << 62)), (weigh, dict(prior=at(1 << 20), ph=(1 << 40) + 1)),
+    (compact, dict(H=8, weights=at(1 << 20), wh=WRAP, wb=0)), (compact, dict(positions=at(1 << 20), pb=1 << 41)),
+    (select, dict(APART, wb=1 << 41)), (select, dict(MOVED, ph=1 << 62))])
+def test_strides_whose_sums_could_wrap_are_refused(lib, call, over):
+    assert call(lib, **over) == pkd.EUNSUPPORTED
+    assert "2^40" in lib.pkd_last_error().decode()
