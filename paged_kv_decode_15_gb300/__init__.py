@@ -189,9 +189,9 @@ def workspace_init(ws: torch.Tensor, stream=None):
 def workspace_check(ws: torch.Tensor = None, stream=None) -> int:
     """Synchronise, read and clear the workspace status word; returns the status code.
 
-    Without ws: that of the workspace which paged_attention and prefix_decode
-    keep for this host thread and stream (default: the current one) when they
-    are given none.  Such a workspace is ready for the next call afterwards,
+    Without ws: that of the workspace which paged_attention, prefix_decode,
+    packed_attention and key_weights keep for this host thread and stream
+    (default: the current one) when they are given none.  Such a workspace is ready for the next call afterwards,
     also after ETIMEOUT (its counters are zeroed again).  A call captured into
     a graph has its workspace in the graph: pass it one of your own to read
     its status.
@@ -207,14 +207,18 @@ def workspace_check(ws: torch.Tensor = None, stream=None) -> int:
         status = load_library().pkd_workspace_check(kept[0], kept[1], s.cuda_stream)
         if status == ETIMEOUT:
             _check(load_library().pkd_workspace_init(kept[0], _WS_HEAD, s.cuda_stream))
+        late = _kept.late.pop((index, s.cuda_stream), None)
+        if late is not None:
+            status = max(status, load_library().pkd_workspace_check(late.data_ptr(), late.numel(), s.cuda_stream))
     return status
 
 
 def release_workspaces():
-    """Free the workspaces that paged_attention and prefix_decode keep for this host
-    thread (the next call makes a new one); those of other threads go with their
-    threads.  Calls already queued keep theirs until they are done."""
+    """Free the workspaces that calls without one keep for this host thread, and what
+    they had to report (the next call makes a new one); those of other threads go with
+    their threads.  Calls already queued keep theirs until they are done."""
     _kept.workspaces.clear()
+    _kept.late.clear()
 
 
 _ws_cache: dict = {}
@@ -442,14 +446,17 @@ def _token_stride(t, T, H, D, name):
 
 
 class _Kept(threading.local):
-    """Workspaces of a host thread's calls: (device index, stream) -> (address, bytes, tensor)."""
+    """Workspaces of a host thread's calls: (device index, stream) -> (address, bytes, tensor),
+    and the heads, with the status not yet read, of those that grew out of use."""
 
     def __init__(self):
         self.workspaces = {}
+        self.late = {}
 
 
 _kept = _Kept()
 _WS_HEAD = 256 + 4 * 65536  # PKD_ATTENTION_WORKSPACE_HEAD
+_STATUS_BYTES = 256  # what pkd_workspace_check takes at least
 
 
 def _call_workspace(nbytes, index, stream):
@@ -469,6 +476,11 @@ def _call_workspace(nbytes, index, stream):
     _check(load_library().pkd_workspace_init(t.data_ptr(), _WS_HEAD, stream))
     ws = (t.data_ptr(), nbytes, t)
     if key is not None:
+        old = _kept.workspaces.get(key)
+        if old is not None:
+            late = _kept.late.get(key)
+            head = old[2][:_STATUS_BYTES]
+            _kept.late[key] = head.clone() if late is None else late.bitwise_or_(head)
         _kept.workspaces[key] = ws
     return ws
 
