@@ -532,7 +532,8 @@ pkd_status pkd_evict_select(const float* weights, int64_t weights_batch_stride, 
  *   block_table  device int32 [batch, block_table_stride], table_columns of them in use; a
  *                row whose source or target page lies outside the pool does not move
  *   weights, positions  device [batch, num_kv_heads, weights_keys / positions_keys] (fp32 /
- *                int32; rows contiguous, strides in elements) move along, or NULL
+ *                int32; rows contiguous, strides in elements up to 2^40; a key or more)
+ *                move along, or NULL
  *
  * The pages of the slots below n must be one request's own (pages that requests share
  * behind them are only read).  K and V bits are copied.  Limits: head_dim 64 or 128.

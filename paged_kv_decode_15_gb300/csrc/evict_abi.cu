@@ -131,6 +131,8 @@ pkd_status pkd_cache_compact(void* kv_cache, pkd_dtype kv_dtype, int64_t num_pag
     if (weights && weights_keys < keys) keys = weights_keys;
     if (positions && positions_keys < keys) keys = positions_keys;
     if (keys < 0) return report(PKD_EINVAL, "negative number of keys");
+    if ((weights && weights_keys == 0) || (positions && positions_keys == 0))
+        return report(PKD_EINVAL, "weights and positions must have keys");  // no row could move with its values
     if (keys > kMaxKeys) keys = kMaxKeys;
     st = check_rows(weights, weights_batch_stride, weights_head_stride, keys, true, batch, num_kv_heads, "weights");
     if (st != PKD_OK) return st;

@@ -40,3 +40,11 @@ WRAP = (1 << 63) // 7 + 1  # seven such head strides are past 2^63, where a batc
 def test_strides_whose_sums_could_wrap_are_refused(lib, call, over):
     assert call(lib, **over) == pkd.EUNSUPPORTED
     assert "2^40" in lib.pkd_last_error().decode()
+
+
+@pytest.mark.parametrize("over", [dict(weights=at(1 << 20), wkeys=0), dict(positions=at(1 << 20), pkeys=0),
+                                  dict(weights=at(1 << 20), positions=at(2 << 20), pkeys=0)])
+def test_compact_refuses_arrays_without_keys(lib, over):
+    """No row could move with its values, and kept_lens would count rows that were not there."""
+    assert compact(lib, **over) == pkd.EINVAL
+    assert "must have keys" in lib.pkd_last_error().decode()
