@@ -114,7 +114,8 @@ pkd_status pkd_workspace_init(void* workspace, size_t workspace_bytes, void* str
  * Synchronise `stream`, read the workspace's status word and clear it.
  * Returns PKD_OK, PKD_EDEVICE_BOUNDS (a seq_lens entry above max_kv_len or
  * below 0, or a block-table entry outside [0, num_pages): the kernel skipped
- * those keys) or PKD_ETIMEOUT.  The kernels never trap.
+ * those keys; or what a call's own comment says) or PKD_ETIMEOUT.  The kernels
+ * never trap.
  */
 pkd_status pkd_workspace_check(void* workspace, size_t workspace_bytes, void* stream);
 
@@ -520,6 +521,14 @@ pkd_status pkd_evict_select(const float* weights, int64_t weights_batch_stride, 
                             int recent, int pool, const int32_t* positions, int64_t positions_batch_stride,
                             int64_t positions_head_stride, const int32_t* context_lens, int32_t* kept,
                             int32_t* kept_lens, void* stream);
+/* The same with a workspace (256-byte aligned, 256 bytes or more, zeroed once; any other
+ * call's on the stream will do), whose status word reports seq_lens outside [0, keys]. */
+pkd_status pkd_evict_select_checked(const float* weights, int64_t weights_batch_stride, int64_t weights_head_stride,
+                                    int64_t keys, const int32_t* seq_lens, int batch, int num_kv_heads, int budget,
+                                    int sinks, int recent, int pool, const int32_t* positions,
+                                    int64_t positions_batch_stride, int64_t positions_head_stride,
+                                    const int32_t* context_lens, int32_t* kept, int32_t* kept_lens, void* workspace,
+                                    size_t workspace_bytes, void* stream);
 
 /*
  * Compaction of a paged cache, in place: of the n = kept_lens[b] rows that stay of a
@@ -529,12 +538,16 @@ pkd_status pkd_evict_select(const float* weights, int64_t weights_batch_stride, 
  * see (their rotary positions are in them).
  *
  *   kept, kept_lens  as pkd_evict_select leaves them: rising indexes per (request, kv head)
- *   block_table  device int32 [batch, block_table_stride], table_columns of them in use; a
- *                row whose source or target page lies outside the pool does not move
+ *   block_table  device int32 [batch, block_table_stride], table_columns of them in use
  *   weights, positions  device [batch, num_kv_heads, weights_keys / positions_keys] (fp32 /
  *                int32; rows contiguous, strides in elements up to 2^40; a key or more)
  *                move along, or NULL
  *
+ * A row moves with its weight and position or not at all: not where its index lies behind
+ * the table, weights or positions, or its source or target page outside the pool.  Its
+ * slot then holds what it held, an evicted key, and kept_lens still counts it: give the
+ * arrays that the choice was made from, and look at the status of
+ * pkd_cache_compact_checked.
  * The pages of the slots below n must be one request's own (pages that requests share
  * behind them are only read).  K and V bits are copied.  Limits: head_dim 64 or 128.
  */
@@ -544,6 +557,15 @@ pkd_status pkd_cache_compact(void* kv_cache, pkd_dtype kv_dtype, int64_t num_pag
                              int budget, float* weights, int64_t weights_batch_stride, int64_t weights_head_stride,
                              int64_t weights_keys, int32_t* positions, int64_t positions_batch_stride,
                              int64_t positions_head_stride, int64_t positions_keys, void* stream);
+/* The same with a workspace (as for pkd_evict_select_checked), whose status word reports
+ * rows that did not move, and kept_lens outside [0, budget]. */
+pkd_status pkd_cache_compact_checked(void* kv_cache, pkd_dtype kv_dtype, int64_t num_pages, const int32_t* block_table,
+                                     int64_t block_table_stride, int table_columns, const int32_t* kept,
+                                     const int32_t* kept_lens, int batch, int num_kv_heads, int head_dim, int page_size,
+                                     int budget, float* weights, int64_t weights_batch_stride, int64_t weights_head_stride,
+                                     int64_t weights_keys, int32_t* positions, int64_t positions_batch_stride,
+                                     int64_t positions_head_stride, int64_t positions_keys, void* workspace,
+                                     size_t workspace_bytes, void* stream);
 
 /*
  * DASH segmented attention with its combine [DASH flash_dash_attention].

@@ -42,7 +42,8 @@ SYMBOLS = ("pkd_version", "pkd_last_error", "pkd_paged_decode_workspace_size", "
            "pkd_segmented_attention", "pkd_segmented_attention_paged", "pkd_lse_merge",
            "pkd_rope_cache_write", "pkd_paged_attention_workspace_size", "pkd_paged_attention_kernel_name",
            "pkd_paged_attention", "pkd_prefix_decode_workspace_size", "pkd_prefix_decode",
-           "pkd_packed_attention_workspace_size", "pkd_packed_attention", "pkd_key_weights_workspace_size", "pkd_key_weights", "pkd_evict_select", "pkd_cache_compact")
+           "pkd_packed_attention_workspace_size", "pkd_packed_attention", "pkd_key_weights_workspace_size", "pkd_key_weights",
+           "pkd_evict_select", "pkd_evict_select_checked", "pkd_cache_compact", "pkd_cache_compact_checked")
 
 
 class ScoreOptions(ctypes.Structure):
@@ -118,6 +119,9 @@ def load_library(path: str = LIB_PATH):
                                     I64, I64, F, P, I64, I64, P, SZ, U, P]
     lib.pkd_evict_select.argtypes = [P, I64, I64, I64, P, I, I, I, I, I, I, P, I64, I64, P, P, P, P]
     lib.pkd_cache_compact.argtypes = [P, I, I64, P, I64, I, P, P, I, I, I, I, I, P, I64, I64, I64, P, I64, I64, I64, P]
+    for name in ("pkd_evict_select", "pkd_cache_compact"):
+        getattr(lib, name + "_checked").argtypes = getattr(lib, name).argtypes[:-1] + [P, SZ, P]
+        getattr(lib, name + "_checked").restype = I
     for name in ("pkd_packed_attention", "pkd_key_weights", "pkd_evict_select", "pkd_cache_compact", "pkd_rope_cache_write", "pkd_paged_attention", "pkd_prefix_decode", "pkd_workspace_init", "pkd_workspace_check", "pkd_paged_decode", "pkd_paged_decode_static",
                  "pkd_paged_decode_static_check", "pkd_cache_write", "pkd_segmented_attention", "pkd_segmented_attention_paged", "pkd_lse_merge"):
         getattr(lib, name).restype = I
@@ -190,11 +194,12 @@ def workspace_check(ws: torch.Tensor = None, stream=None) -> int:
     """Synchronise, read and clear the workspace status word; returns the status code.
 
     Without ws: that of the workspace which paged_attention, prefix_decode,
-    packed_attention and key_weights keep for this host thread and stream
-    (default: the current one) when they are given none.  Such a workspace is ready for the next call afterwards,
-    also after ETIMEOUT (its counters are zeroed again).  A call captured into
-    a graph has its workspace in the graph: pass it one of your own to read
-    its status.
+    packed_attention, key_weights, evict_select and cache_compact keep for this
+    host thread and stream (default: the current one) when they are given none.
+    Such a workspace is ready for the next call afterwards, also after ETIMEOUT
+    (its counters are zeroed again).  A call captured into a graph has its
+    workspace in the graph (evict_select and cache_compact none): pass it one of
+    your own to read its status.
     """
     if ws is not None:
         return load_library().pkd_workspace_check(_ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
@@ -836,9 +841,13 @@ def _key_rows(t, B, H, dtype, name):
     """(address, batch stride, head stride, keys) of t [B, H, keys], rows of keys contiguous; zeros for None."""
     if t is None:
         return None, 0, 0, 0
-    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != H or t.dtype is not dtype or (t.stride(2) != 1 and t.shape[2] > 1):
-        raise ValueError(f"{name} must be {dtype} [{B}, {H}, keys] with contiguous rows of keys")
-    return t.data_ptr(), t.stride(0), t.stride(1), t.shape[2]
+    shape = t.shape
+    if len(shape) == 3:
+        b, h, keys = shape
+        sb, sh, one = t.stride()
+        if b == B and h == H and t.dtype is dtype and (one == 1 or keys <= 1):
+            return t.data_ptr(), sb, sh, keys
+    raise ValueError(f"{name} must be {dtype} [{B}, {H}, keys] with contiguous rows of keys")
 
 
 def key_weights(q, kv_cache, block_table, seq_lens, query_start, lse, scale, *, weights=None, decay=1.0, causal=True,
@@ -910,8 +919,18 @@ def key_weights(q, kv_cache, block_table, seq_lens, query_start, lse, scale, *, 
     return out
 
 
+def _status_workspace(workspace, index, stream):
+    """(address, bytes, tensor) of the workspace that a call reports to: the given one, or the one kept
+    for the host thread and stream; none while the stream is capturing (a graph's could not be read)."""
+    if workspace is not None:
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if _capturing():
+        return None, 0, None
+    return _kept.workspaces.get((index, stream)) or _call_workspace(_WS_HEAD, index, stream)
+
+
 def evict_select(weights, seq_lens, budget, *, sinks=0, recent=0, pool=1, positions=None, context_lens=None, kept=None,
-                 kept_lens=None, stream=None):
+                 kept_lens=None, workspace=None, stream=None):
     """The keys of each request and kv head that stay in a cache of at most budget keys.
 
     weights fp32 [B, Hkv, keys] (key_weights), seq_lens int32 [B].  Kept are the
@@ -920,20 +939,23 @@ def evict_select(weights, seq_lens, budget, *, sinks=0, recent=0, pool=1, positi
     weight of the pool keys around a key that are neither.  After a compaction
     has put keys out of order, positions (int32 [B, Hkv, keys]) says where each
     stood and context_lens (int32 [B]) how many tokens the request has seen.
+    Lengths outside [0, keys] are clamped; workspace_check (of workspace, 256 bytes
+    or more, or of the one kept for calls without) then says so.
     Returns (kept int32 [B, Hkv, budget]: rising indexes, -1 behind them,
     kept_lens int32 [B]: min(seq_lens, budget)).
     """
     index = weights.get_device()
     if index < 0 or seq_lens.get_device() != index or (positions is not None and positions.get_device() != index) or \
-            (context_lens is not None and context_lens.get_device() != index) or not (kept is kept_lens is None):
+            (context_lens is not None and context_lens.get_device() != index) or not (kept is kept_lens is workspace is None):
         _device_error(weights=weights, seq_lens=seq_lens, positions=positions, context_lens=context_lens, kept=kept,
-                      kept_lens=kept_lens)
+                      kept_lens=kept_lens, workspace=workspace)
     if stream is not None or _current_device() != index:
         ctx = _elsewhere(index, stream)
         if ctx is not None:
             with ctx:
                 return evict_select(weights, seq_lens, budget, sinks=sinks, recent=recent, pool=pool,
-                                    positions=positions, context_lens=context_lens, kept=kept, kept_lens=kept_lens)
+                                    positions=positions, context_lens=context_lens, kept=kept, kept_lens=kept_lens,
+                                    workspace=workspace)
     B, H, keys = shape = weights.shape
     wb, wh, one = weights.stride()
     if weights.dtype is not _F32 or (one != 1 and keys > 1):
@@ -962,18 +984,20 @@ def evict_select(weights, seq_lens, budget, *, sinks=0, recent=0, pool=1, positi
     elif kept.shape != (B, H, budget) or kept.dtype is not _I32 or not kept.is_contiguous():
         raise ValueError(f"kept must be contiguous int32 [{B}, {H}, {budget}]")
     if kept_lens is None:
-        kept_lens = torch.empty((B,), dtype=_I32, device=weights.device)
+        kept_lens = torch.empty_like(seq_lens)
     elif kept_lens.shape != (B,) or kept_lens.dtype is not _I32 or not kept_lens.is_contiguous():
         raise ValueError(f"kept_lens must be contiguous int32 [{B}]")
-    status = (_lib or load_library()).pkd_evict_select(
+    s = _raw_stream(index)
+    ws, ws_bytes, keep = _status_workspace(workspace, index, s)
+    status = (_lib or load_library()).pkd_evict_select_checked(
         weights.data_ptr(), wb, wh, keys, seq_lens.data_ptr(), B, H, budget, sinks, recent, pool, x, xb, xh, context,
-        kept.data_ptr(), kept_lens.data_ptr(), _raw_stream(index))
+        kept.data_ptr(), kept_lens.data_ptr(), ws, ws_bytes, s)
     if status:
         _check(status)
     return kept, kept_lens
 
 
-def cache_compact(kv_cache, block_table, kept, kept_lens, *, weights=None, positions=None, stream=None):
+def cache_compact(kv_cache, block_table, kept, kept_lens, *, weights=None, positions=None, workspace=None, stream=None):
     """Move the rows that stay below the new length, in place.
 
     kept, kept_lens as evict_select returns them: of the kept_lens[b] rows of a
@@ -981,19 +1005,23 @@ def cache_compact(kv_cache, block_table, kept, kept_lens, *, weights=None, posit
     it, with their entries of weights (fp32) and positions (int32, both
     [B, Hkv, keys]); the others stay.  seq_lens is then kept_lens.  The keys' order
     changes: attend to them without a window.  The pages below the new length
-    must be one request's own.  Returns kv_cache.
+    must be one request's own.  A row whose index lies behind the table, weights
+    or positions, or its way on a page outside the pool, does not move, and its
+    slot keeps an evicted key; workspace_check (as for evict_select) then says so.
+    Returns kv_cache.
     """
     index = kv_cache.get_device()
     if index < 0 or block_table.get_device() != index or kept.get_device() != index or \
             kept_lens.get_device() != index or (weights is not None and weights.get_device() != index) or \
-            (positions is not None and positions.get_device() != index):
+            (positions is not None and positions.get_device() != index) or workspace is not None:
         _device_error(kv_cache=kv_cache, block_table=block_table, kept=kept, kept_lens=kept_lens, weights=weights,
-                      positions=positions)
+                      positions=positions, workspace=workspace)
     if stream is not None or _current_device() != index:
         ctx = _elsewhere(index, stream)
         if ctx is not None:
             with ctx:
-                return cache_compact(kv_cache, block_table, kept, kept_lens, weights=weights, positions=positions)
+                return cache_compact(kv_cache, block_table, kept, kept_lens, weights=weights, positions=positions,
+                                     workspace=workspace)
     D = kv_cache.shape[-1] // 2
     num_pages, H, P = _check_cache(D, kv_cache)
     B, columns, stride = _check_table(block_table, kept_lens)
@@ -1003,10 +1031,11 @@ def cache_compact(kv_cache, block_table, kept, kept_lens, *, weights=None, posit
     x, xb, xh, position_keys = _key_rows(positions, B, H, _I32, "positions")
     if (weights is not None and weight_keys == 0) or (positions is not None and position_keys == 0):
         raise ValueError("weights and positions must have keys")  # (no address: rows would move without them)
-    status = (_lib or load_library()).pkd_cache_compact(
+    s = _raw_stream(index)
+    ws, ws_bytes, keep = _status_workspace(workspace, index, s)
+    status = (_lib or load_library()).pkd_cache_compact_checked(
         kv_cache.data_ptr(), _code(kv_cache.dtype), num_pages, block_table.data_ptr(), stride, columns, kept.data_ptr(),
-        kept_lens.data_ptr(), B, H, D, P, kept.shape[2], w, wb, wh, weight_keys, x, xb, xh, position_keys,
-        _raw_stream(index))
+        kept_lens.data_ptr(), B, H, D, P, kept.shape[2], w, wb, wh, weight_keys, x, xb, xh, position_keys, ws, ws_bytes, s)
     if status:
         _check(status)
     return kv_cache

@@ -31,11 +31,14 @@ __global__ void __launch_bounds__(kCompactThreads, 4) cache_compact_kernel(const
     extern __shared__ int32_t list[];
     __shared__ int stays;
     const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int n = min(max(p.kept_lens[b], 0), p.budget);
+    const int given = p.kept_lens[b], n = min(max(given, 0), p.budget);
     const int32_t* kept = p.kept + (static_cast<long long>(b) * p.H + h) * p.budget;
     const int32_t* table = p.block_table + b * p.bt_stride;
     const bool local = p.budget <= kCompactList;
-    if (tid == 0) stays = 0;
+    if (tid == 0) {
+        stays = 0;
+        if (p.status && n != given) atomicOr(p.status, kErrBounds);
+    }
     __syncthreads();
     // rows that stay where they are, and the list
     int count = 0;
@@ -92,6 +95,7 @@ __global__ void __launch_bounds__(kCompactThreads, 4) cache_compact_kernel(const
                     }
                 }
             }
+            if (from < 0 && p.status) atomicOr(p.status, kErrBounds);  // the row is lost to the new length
         }
         const int part = lane % LANES;
 #pragma unroll 1

@@ -13,6 +13,7 @@ struct SelectParams {
     const int32_t* context_lens;  // [B] with positions, else null: seq_lens
     int32_t* kept;                // [B, H, budget]
     int32_t* kept_lens;           // [B]
+    int32_t* status;              // or null
     long long weights_b, weights_h, positions_b, positions_h;
     int B, H, keys, budget, sinks, recent, pool;
 };
@@ -24,6 +25,7 @@ struct CompactParams {
     const int32_t* kept_lens;     // [B]
     float* weights;               // [B, H, keys], strides, or null
     int32_t* positions;           // the same with strides of its own, or null
+    int32_t* status;              // or null
     long long bt_stride, num_pages, weights_b, weights_h, positions_b, positions_h;
     int B, H, P, keys, budget, row_bytes;  // keys: those of the table (and of weights and positions)
     uint32_t pmagic;

@@ -45,6 +45,13 @@ pkd_status check_sizes(int B, int H, int64_t keys, int budget) {
     return PKD_OK;
 }
 
+// The status word of a call's workspace; none without one.
+pkd_status check_workspace(const void* workspace, size_t bytes) {
+    if (workspace && (!aligned(workspace, 256) || bytes < 256))
+        return report(PKD_EINVAL, "the workspace must be 256-byte aligned and hold 256 bytes or more");
+    return PKD_OK;
+}
+
 pkd_status done(cudaError_t e, const char* what) {
     return e == cudaSuccess ? PKD_OK : report(PKD_ECUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
@@ -53,12 +60,14 @@ pkd_status done(cudaError_t e, const char* what) {
 
 extern "C" {
 
-pkd_status pkd_evict_select(const float* weights, int64_t weights_batch_stride, int64_t weights_head_stride, int64_t keys,
-                            const int32_t* seq_lens, int batch, int num_kv_heads, int budget, int sinks, int recent,
-                            int pool, const int32_t* positions, int64_t positions_batch_stride,
-                            int64_t positions_head_stride, const int32_t* context_lens, int32_t* kept,
-                            int32_t* kept_lens, void* stream) {
+pkd_status pkd_evict_select_checked(const float* weights, int64_t weights_batch_stride, int64_t weights_head_stride,
+                                    int64_t keys, const int32_t* seq_lens, int batch, int num_kv_heads, int budget,
+                                    int sinks, int recent, int pool, const int32_t* positions,
+                                    int64_t positions_batch_stride, int64_t positions_head_stride,
+                                    const int32_t* context_lens, int32_t* kept, int32_t* kept_lens, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
     pkd_status st = check_sizes(batch, num_kv_heads, keys, budget);
+    if (st == PKD_OK) st = check_workspace(workspace, workspace_bytes);
     if (st != PKD_OK) return st;
     if (sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
         return report(PKD_EINVAL, "sinks (%d) and recent (%d) must be >= 0 and together within the budget (%d)", sinks, recent, budget);
@@ -90,6 +99,7 @@ pkd_status pkd_evict_select(const float* weights, int64_t weights_batch_stride, 
     p.context_lens = context_lens;
     p.kept = kept;
     p.kept_lens = kept_lens;
+    p.status = static_cast<int32_t*>(workspace);
     p.weights_b = weights_batch_stride;
     p.weights_h = weights_head_stride;
     p.positions_b = positions_batch_stride;
@@ -104,13 +114,25 @@ pkd_status pkd_evict_select(const float* weights, int64_t weights_batch_stride, 
     return done(pkd::launch_evict_select(p, (cudaStream_t)stream), "pkd_evict_select launch");
 }
 
-pkd_status pkd_cache_compact(void* kv_cache, pkd_dtype kv_dtype, int64_t num_pages, const int32_t* block_table,
-                             int64_t block_table_stride, int table_columns, const int32_t* kept, const int32_t* kept_lens,
-                             int batch, int num_kv_heads, int head_dim, int page_size, int budget, float* weights,
-                             int64_t weights_batch_stride, int64_t weights_head_stride, int64_t weights_keys,
-                             int32_t* positions, int64_t positions_batch_stride, int64_t positions_head_stride,
-                             int64_t positions_keys, void* stream) {
+pkd_status pkd_evict_select(const float* weights, int64_t weights_batch_stride, int64_t weights_head_stride, int64_t keys,
+                            const int32_t* seq_lens, int batch, int num_kv_heads, int budget, int sinks, int recent,
+                            int pool, const int32_t* positions, int64_t positions_batch_stride,
+                            int64_t positions_head_stride, const int32_t* context_lens, int32_t* kept,
+                            int32_t* kept_lens, void* stream) {
+    return pkd_evict_select_checked(weights, weights_batch_stride, weights_head_stride, keys, seq_lens, batch, num_kv_heads,
+                                    budget, sinks, recent, pool, positions, positions_batch_stride, positions_head_stride,
+                                    context_lens, kept, kept_lens, nullptr, 0, stream);
+}
+
+pkd_status pkd_cache_compact_checked(void* kv_cache, pkd_dtype kv_dtype, int64_t num_pages, const int32_t* block_table,
+                                     int64_t block_table_stride, int table_columns, const int32_t* kept,
+                                     const int32_t* kept_lens, int batch, int num_kv_heads, int head_dim, int page_size,
+                                     int budget, float* weights, int64_t weights_batch_stride, int64_t weights_head_stride,
+                                     int64_t weights_keys, int32_t* positions, int64_t positions_batch_stride,
+                                     int64_t positions_head_stride, int64_t positions_keys, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
     pkd_status st = check_sizes(batch, num_kv_heads, 0, budget);
+    if (st == PKD_OK) st = check_workspace(workspace, workspace_bytes);
     if (st != PKD_OK) return st;
     if (table_columns < 0 || page_size < 1 || num_pages < 1)
         return report(PKD_EINVAL, "invalid shape: table_columns=%d page_size=%d num_pages=%lld", table_columns, page_size,
@@ -145,6 +167,7 @@ pkd_status pkd_cache_compact(void* kv_cache, pkd_dtype kv_dtype, int64_t num_pag
     p.kept_lens = kept_lens;
     p.weights = weights;
     p.positions = positions;
+    p.status = static_cast<int32_t*>(workspace);
     p.bt_stride = block_table_stride;
     p.num_pages = num_pages;
     p.weights_b = weights_batch_stride;
@@ -159,6 +182,18 @@ pkd_status pkd_cache_compact(void* kv_cache, pkd_dtype kv_dtype, int64_t num_pag
     p.row_bytes = 2 * head_dim * (kv_dtype == PKD_FP8_E4M3 ? 1 : 2);
     pkd::page_magic(page_size, p.pmagic, p.pmshift);
     return done(pkd::launch_cache_compact(p, (cudaStream_t)stream), "pkd_cache_compact launch");
+}
+
+pkd_status pkd_cache_compact(void* kv_cache, pkd_dtype kv_dtype, int64_t num_pages, const int32_t* block_table,
+                             int64_t block_table_stride, int table_columns, const int32_t* kept, const int32_t* kept_lens,
+                             int batch, int num_kv_heads, int head_dim, int page_size, int budget, float* weights,
+                             int64_t weights_batch_stride, int64_t weights_head_stride, int64_t weights_keys,
+                             int32_t* positions, int64_t positions_batch_stride, int64_t positions_head_stride,
+                             int64_t positions_keys, void* stream) {
+    return pkd_cache_compact_checked(kv_cache, kv_dtype, num_pages, block_table, block_table_stride, table_columns, kept,
+                                     kept_lens, batch, num_kv_heads, head_dim, page_size, budget, weights,
+                                     weights_batch_stride, weights_head_stride, weights_keys, positions,
+                                     positions_batch_stride, positions_head_stride, positions_keys, nullptr, 0, stream);
 }
 
 }  // extern "C"

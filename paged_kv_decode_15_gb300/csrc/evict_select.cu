@@ -65,9 +65,12 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
         ctas = static_cast<int>(cg::this_cluster().num_blocks());
     }
     const int h = blockIdx.x / ctas, b = blockIdx.y, all = ctas * kSelThreads, me = rank * kSelThreads + tid;
-    const int L = min(max(p.seq_lens[b], 0), p.keys), n = min(L, p.budget);
+    const int given = p.seq_lens[b], L = min(max(given, 0), p.keys), n = min(L, p.budget);
     int32_t* kept = p.kept + (static_cast<long long>(b) * p.H + h) * p.budget;
-    if (h == 0 && me == 0) p.kept_lens[b] = n;
+    if (h == 0 && me == 0) {
+        p.kept_lens[b] = n;
+        if (p.status && L != given) atomicOr(p.status, kErrBounds);
+    }
     for (int i = n + me; i < p.budget; i += all) kept[i] = -1;
     if (L <= p.budget) {
         for (int i = me; i < n; i += all) kept[i] = i;

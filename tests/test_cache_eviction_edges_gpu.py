@@ -29,3 +29,108 @@ def test_select_writes_right_beside_its_inputs():
     with pytest.raises(pkd.PkdError, match="overlaps"):
         pkd.evict_select(at, lens, budget, sinks=2, recent=4, kept_lens=lens)
     assert lens.tolist() == [90, 41]
+
+
+def status(call, **kw):
+    """Results of a call, and the status that it leaves in a workspace of its own and in the kept one."""
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    got = call(workspace=ws, **kw)
+    own = pkd.workspace_check(ws)
+    assert pkd.workspace_check(ws) == pkd.OK
+    pkd.workspace_check()
+    call(**kw)
+    assert pkd.workspace_check() == own and pkd.workspace_check() == pkd.OK
+    return got, own
+
+
+@pytest.mark.parametrize("S", [90, 9000])
+@pytest.mark.parametrize("lens,code", [([5, 90], pkd.OK), ([0, 30], pkd.OK), ([91, 3], pkd.EDEVICE_BOUNDS), ([3, -1], pkd.EDEVICE_BOUNDS)])
+def test_select_reports_lengths_out_of_range(S, lens, code):
+    """Alone and by clusters; the lengths are clamped, as before."""
+    rng = np.random.default_rng(2)
+    lens = [n if n <= 90 and S == 90 else n - 90 + S if n > 90 else n for n in lens]
+    w = rng.random((2, 2, S)).astype(np.float32)
+    (kept, n), got = status(lambda **kw: pkd.evict_select(dev(w), dev(np.array(lens, np.int32)), 30, recent=4, **kw))
+    want = ref.evict_select(w, lens, 30, recent=4)
+    assert got == code and np.array_equal(kept.cpu().numpy(), want[0]) and np.array_equal(n.cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("what,code", [("none", pkd.OK), ("narrow weights", pkd.EDEVICE_BOUNDS), ("narrow positions", pkd.EDEVICE_BOUNDS),
+                                       ("just wide enough", pkd.OK), ("source page", pkd.EDEVICE_BOUNDS),
+                                       ("target page", pkd.EDEVICE_BOUNDS), ("behind the table", pkd.EDEVICE_BOUNDS),
+                                       ("kept_lens", pkd.EDEVICE_BOUNDS), ("page of no way", pkd.OK)])
+def test_compact_reports_rows_that_do_not_move(what, code):
+    """A row moves with its weight and position or not at all, and the status says when one did not."""
+    p = problem(3, new=[1, 1], lens=[200, 200], heads=2, kv=2, dim=64, page=16, dtype="bf16")
+    rng = np.random.default_rng(4)
+    x = rng.random((2, 2, 200))
+    x[..., 185:] = 2  # keys 185 to 199 stay, and move
+    x[..., :20] = np.where(np.arange(20) % 2, 3, -1)  # of the first twenty every other stays
+    if what == "page of no way":
+        x[..., 176:192] = -1
+    kept, n = ref.evict_select(x, [200, 200], 60)
+    table, keys = p["table"].copy(), p["table"].shape[1] * 16
+    w, pos = rng.random((2, 2, keys)).astype(np.float32), rng.integers(0, 9999, (2, 2, keys)).astype(np.int32)
+    limit = keys
+    if what == "narrow weights":
+        w, limit = np.ascontiguousarray(w[..., :190]), 190
+    if what == "narrow positions":
+        pos, limit = np.ascontiguousarray(pos[..., :199]), 199
+    if what == "just wide enough":
+        w, pos = np.ascontiguousarray(w[..., :200]), np.ascontiguousarray(pos[..., :200])
+    if what == "source page":
+        table[1, 12] = -1
+    if what == "target page":
+        table[0, 0] = len(p["cache"])
+    if what == "behind the table":
+        kept[0, 1, -1] = keys
+    if what == "kept_lens":
+        n[1] = 61
+    if what == "page of no way":
+        table[0, 11] = table[1, 11] = 10 ** 6  # (no key of it stays)
+    want, rows = p["cache"].view(torch.int16).numpy().copy(), [w.copy(), pos.copy()]
+    for b in range(2):
+        m = min(int(n[b]), 60)
+        for h in range(2):
+            stay = [int(s) for s in kept[b, h, :m]]
+            for s, t in zip([s for s in stay if s >= m], sorted(set(range(m)) - set(stay))):
+                if s >= limit or not 0 <= table[b, s // 16] < len(want) or not 0 <= table[b, t // 16] < len(want):
+                    continue
+                want[table[b, t // 16], h, t % 16] = want[table[b, s // 16], h, s % 16]
+                for r in rows:
+                    r[b, h, t] = r[b, h, s]
+
+    def call(**kw):
+        cache, dw, dx = p["cache"].cuda(), dev(w), dev(pos)
+        pkd.cache_compact(cache, dev(table), dev(kept), dev(n), weights=dw, positions=dx, **kw)
+        return cache, dw, dx
+
+    (cache, dw, dx), got = status(call)
+    assert got == code
+    assert np.array_equal(cache.view(torch.int16).cpu().numpy(), want)
+    assert np.array_equal(dw.cpu().numpy(), rows[0]) and np.array_equal(dx.cpu().numpy(), rows[1])
+
+
+def test_captured_choice_and_compaction_report_to_a_workspace_given():
+    p = problem(5, new=[1], lens=[100], heads=2, kv=2, dim=64, page=16, dtype="fp16")
+    w, lens, table = torch.rand((1, 2, 100), device="cuda"), dev(np.array([100], np.int32)), dev(p["table"])
+    cache, ws = p["cache"].cuda(), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    pkd.workspace_check()
+
+    def step(**kw):
+        kept, n = pkd.evict_select(w, lens, 50, **kw)
+        pkd.cache_compact(cache, table, kept, n, **kw)
+
+    with torch.cuda.stream(torch.cuda.Stream()):
+        step()
+        torch.cuda.synchronize()
+    for kw in (dict(), dict(workspace=ws)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(**kw)
+        for bad in (False, True):
+            lens.fill_(101 if bad else 100)
+            g.replay()
+            torch.cuda.synchronize()
+            assert pkd.workspace_check(ws) == (pkd.EDEVICE_BOUNDS if kw and bad else pkd.OK)
+    assert pkd.workspace_check() == pkd.OK

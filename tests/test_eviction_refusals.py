@@ -48,3 +48,14 @@ def test_compact_refuses_arrays_without_keys(lib, over):
     """No row could move with its values, and kept_lens would count rows that were not there."""
     assert compact(lib, **over) == pkd.EINVAL
     assert "must have keys" in lib.pkd_last_error().decode()
+
+
+@pytest.mark.parametrize("ws,size", [(at((1 << 20) + 128), 1 << 20), (at(1 << 20), 255)])
+def test_workspaces_of_choice_and_compaction_are_checked(lib, ws, size):
+    a = dict(weights=at(1 << 20), wb=200, wh=100, keys=100, lens=at(2 << 20), B=2, H=2, budget=50, sinks=4, recent=16, pool=1,
+             positions=None, pb=200, ph=100, context=None, kept=at(3 << 20), kept_lens=at(4 << 20), ws=ws, size=size, stream=None)
+    assert lib.pkd_evict_select_checked(*a.values()) == pkd.EINVAL and "workspace" in lib.pkd_last_error().decode()
+    a = dict(cache=at(1 << 20), kv_dt=pkd.BF16, num_pages=8, table=at(2 << 20), stride=8, columns=8, kept=at(3 << 20),
+             kept_lens=at(4 << 20), B=2, H=2, D=128, P=16, budget=50, weights=None, wb=256, wh=128, wkeys=128, positions=None,
+             pb=256, ph=128, pkeys=128, ws=ws, size=size, stream=None)
+    assert lib.pkd_cache_compact_checked(*a.values()) == pkd.EINVAL and "workspace" in lib.pkd_last_error().decode()
