@@ -464,7 +464,8 @@ pkd_status pkd_prefix_decode(const void* q, pkd_dtype q_dtype, const void* kv_ca
  * over the same keys makes the exponential a probability.
  *
  *   q, kv_cache, block_table, seq_lens, query_start, max_query_len, softcap, window,
- *                flags  as for pkd_paged_attention (V is not read)
+ *                flags  as for pkd_paged_attention (V is not read; of the table the columns
+ *                of max_kv_len keys are read, and those behind a length not used)
  *   last_queries w > 0: only the last w tokens of each request weigh its keys
  *   lse          device fp32 [total_tokens, num_heads]; a token of lse -inf weighs nothing
  *   prior        device fp32 [batch, num_kv_heads, >= max_kv_len], or NULL: 0.  Rows

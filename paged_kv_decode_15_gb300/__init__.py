@@ -894,10 +894,13 @@ def key_weights(q, kv_cache, block_table, seq_lens, query_start, lse, scale, *, 
         max_query_len = max(T, 1)
     if max_kv_len is None:
         max_kv_len = columns * P
+    keys = max_kv_len
+    if columns * P < max_kv_len <= stride * P:
+        max_kv_len = columns * P  # part of a wider table: what lies behind its columns is not the call's to read
     if window >> 31 or max_query_len >> 31 or max_kv_len >> 31 or last_queries >> 31:
         raise ValueError("window, last_queries, max_query_len and max_kv_len must lie in [0, 2^31)")
     if out is None:
-        out = torch.zeros((B, Hkv, max_kv_len if weights is None else weights.shape[2]), dtype=_F32, device=q.device)
+        out = torch.zeros((B, Hkv, keys if weights is None else weights.shape[2]), dtype=_F32, device=q.device)
     prior, pb, ph, prior_keys = _key_rows(weights, B, Hkv, _F32, "weights")
     dst, ob, oh, out_keys = _key_rows(out, B, Hkv, _F32, "out")
     if out_keys < max_kv_len or (weights is not None and prior_keys < max_kv_len):

@@ -68,3 +68,30 @@ def test_parts_of_split_tokens_are_joined_from_what_other_ctas_wrote():
         ws[256 + 4 * 65536:] = 255
         assert torch.equal(pkd.key_weights(*args, workspace=ws), good)
     assert pkd.workspace_check(ws) == pkd.OK and not ws[256:256 + 4 * 65536].any()
+
+
+def test_parts_of_a_wider_table_are_not_read_past_their_columns(monkeypatch):
+    """Columns of a larger table, whose last row ends with the memory: max_kv_len for the larger one
+    reaches the library as what the columns hold, and the weights are right."""
+    p = problem(14, new=[1, 1, 1], lens=[60, 33, 64], heads=4, kv=2, dim=64, page=16, dtype="bf16")
+    store = torch.full((3 * 8,), -5, dtype=torch.int32, device="cuda")
+    table = store.as_strided((3, 4), (8, 1), 4)  # the last four columns of eight
+    table.copy_(torch.as_tensor(p["table"]))
+    lse = lses(p)
+    args = (p["q"].cuda(), p["cache"].cuda(), table, dev(p["lens"]), dev(p["starts"]), dev(lse), p["scale"])
+    lib, asked = pkd.load_library(), []
+
+    class Recorder:
+        def __getattr__(self, name):
+            return (lambda *a: asked.append(a) or 0) if name == "pkd_key_weights" else getattr(lib, name)
+
+    monkeypatch.setattr(pkd, "_lib", Recorder())
+    pkd.key_weights(*args, max_query_len=1, max_kv_len=128)
+    monkeypatch.undo()
+    assert asked[0][18] == 64 and asked[0][7] == 8  # max_kv_len, the table's stride
+    want, err = ref.key_weights(p["qv"], p["cv"], p["table"], p["lens"], p["starts"], lse.astype(np.float64), p["scale"])
+    got = pkd.key_weights(*args, max_query_len=1, max_kv_len=128)
+    assert got.shape == (3, 2, 128)
+    close(got, want, err, p["lens"])
+    with pytest.raises(pkd.PkdError, match="stride"):  # a table that does not have the columns
+        pkd.key_weights(*args, max_query_len=1, max_kv_len=256)
