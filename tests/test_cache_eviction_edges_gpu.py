@@ -134,3 +134,48 @@ def test_captured_choice_and_compaction_report_to_a_workspace_given():
             torch.cuda.synchronize()
             assert pkd.workspace_check(ws) == (pkd.EDEVICE_BOUNDS if kw and bad else pkd.OK)
     assert pkd.workspace_check() == pkd.OK
+
+
+@pytest.mark.parametrize("B,S,budget", [(40, 3000, 900), (12, 9000, 1000), (1, 16000, 15000), (1, 70000, 4096), (1, 140001, 3000)])
+def test_select_of_long_rows_out_of_order(B, S, budget):
+    """Positions in every tier: a CTA to a row, clusters, and rows that are read again; ties of weight
+    and of nothing received, lengths around the budget."""
+    H = 2
+    g = torch.Generator(device="cuda").manual_seed(S)
+    w = torch.exp(2 * torch.randn((B, H, S), device="cuda", generator=g))
+    w[torch.rand(w.shape, device="cuda", generator=g) < 0.4] = 0
+    w = (w * 64).round() / 64
+    context = [S + 500 + 7 * b for b in range(B)]
+    pos = torch.stack([torch.rand((H, context[b]), device="cuda", generator=g).argsort(-1)[:, :S] for b in range(B)]).int()
+    lens = [S, budget, budget + 1, S - 3][:B] + [S - 31 * b for b in range(4, B)]
+    sinks, recent = 5, min(700, budget // 2)
+    kept, n = pkd.evict_select(w, dev(np.array(lens, np.int32)), budget, sinks=sinks, recent=recent, positions=pos,
+                               context_lens=dev(np.array(context, np.int32)))
+    assert n.tolist() == [min(L, budget) for L in lens]
+    for b, L in enumerate(lens):
+        x, at, m = w[b, :, :L].clone(), pos[b, :, :L], min(L, budget)
+        x[(at < sinks) | (at >= context[b] - recent)] = torch.inf
+        want = x.sort(dim=-1, descending=True, stable=True)[1][:, :m].sort(-1)[0]
+        assert torch.equal(kept[b, :, :m].long(), want) and (kept[b, :, m:] == -1).all()
+
+
+@pytest.mark.parametrize("dtype,dim", [("fp8", 64), ("bf16", 64), ("fp16", 128)])
+def test_compact_of_many_lists_with_many_moves(dtype, dim):
+    """More moves than the one CTA of a list takes at a time: rows of 128, 256 and 512 bytes, with
+    weights and positions."""
+    B, H, S, budget = 40, 16, 1500, 700
+    rng = np.random.default_rng(6)
+    need, order = -(-S // 16), rng.permutation(B * -(-S // 16)).astype(np.int32)
+    table = order.reshape(B, need)
+    bits = rng.integers(0, 256, (B * need, H, 16, 2 * dim * (1 if dtype == "fp8" else 2)), dtype=np.uint8)
+    lens = [S - 3 * b for b in range(B)]
+    kept = np.stack([np.stack([np.sort(rng.permutation(L)[:budget]) for _ in range(H)]) for L in lens]).astype(np.int32)
+    n = np.full(B, budget, np.int32)
+    w, x = rng.random((B, H, need * 16)).astype(np.float32), rng.integers(0, 9999, (B, H, need * 16)).astype(np.int32)
+    cache, dw, dx = dev(bits), dev(w), dev(x)
+    view = cache.view({"fp8": torch.float8_e4m3fn, "bf16": torch.bfloat16, "fp16": torch.float16}[dtype])
+    pkd.cache_compact(view, dev(table), dev(kept), dev(n), weights=dw, positions=dx)
+    assert min((kept[b, h] >= budget).sum() for b in range(B) for h in range(H)) > 256
+    ref.cache_compact(bits, table, kept, n, (w, x))
+    assert np.array_equal(cache.cpu().numpy(), bits)
+    assert np.array_equal(dw.cpu().numpy(), w) and np.array_equal(dx.cpu().numpy(), x)
