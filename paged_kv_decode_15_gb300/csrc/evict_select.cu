@@ -141,8 +141,13 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
                 for (int d = 1; d <= kSide; ++d) x[i] = max3(x[i], v[i + kSide - d], v[i + kSide + d]);
             }
         };
+        // Windows of up to seven keys are in registers, unrolled for their reach; wider ones loop
+        // over shared memory (512 rows of 1024 to 4096 keys: 3 keys 13.8 us, looped over 14.6; 7 keys
+        // 14.9; 9 keys looped over 17.5, unrolled 15.1: every reach more is one more copy of this
+        // pass in twelve kernels)
         switch (side) {
             case 0: window(std::integral_constant<int, 0>{}); break;
+            case 1: window(std::integral_constant<int, 1>{}); break;
             case 2: window(std::integral_constant<int, 2>{}); break;
             case 3: window(std::integral_constant<int, 3>{}); break;
             default:

@@ -179,3 +179,21 @@ def test_compact_of_many_lists_with_many_moves(dtype, dim):
     ref.cache_compact(bits, table, kept, n, (w, x))
     assert np.array_equal(cache.cpu().numpy(), bits)
     assert np.array_equal(dw.cpu().numpy(), w) and np.array_equal(dx.cpu().numpy(), x)
+
+
+@pytest.mark.parametrize("S", [300, 3000, 20000])
+@pytest.mark.parametrize("pool", [3, 7, 9, 11, 255])
+def test_select_with_windows_in_registers_and_looped_over(S, pool):
+    """Both sides of the rule; neighbours across threads and CTAs, at both ends, beside sinks and the recent."""
+    g = torch.Generator(device="cuda").manual_seed(S + pool)
+    w = torch.exp(2 * torch.randn((2, 2, S), device="cuda", generator=g))
+    w[torch.rand(w.shape, device="cuda", generator=g) < 0.3] = 0
+    lens, side = [S, S - 101], pool // 2
+    for sinks, recent in ((0, 0), (3, 20)):
+        kept, _ = pkd.evict_select(w, dev(np.array(lens, np.int32)), 100, sinks=sinks, recent=recent, pool=pool)
+        for b, L in enumerate(lens):
+            x = w[b, :, :L].clone()
+            x[:, :sinks] = x[:, L - recent:] = -torch.inf
+            x = torch.nn.functional.pad(x, (side, side), value=-torch.inf).unfold(-1, pool, 1).amax(-1)
+            x[:, :sinks] = x[:, L - recent:] = torch.inf
+            assert torch.equal(kept[b].long(), x.sort(dim=-1, descending=True, stable=True)[1][:, :100].sort(-1)[0])
