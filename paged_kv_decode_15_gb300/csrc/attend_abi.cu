@@ -221,7 +221,8 @@ pkd_status plan_key_weights(int B, long long T, int max_q, int last, int Hq, int
         // (64 requests of 1024 to 4096 keys, 32 and 128 rows: 76 and 97 us, four 81 and 118,
         // thirty-two 92 and 102)
         const long long blocks = (max_kv_len + pkd::kWtKeys - 1) / pkd::kWtKeys, items = B == 1 ? kSms : 8 * kSms;
-        pl.run = (int)std::max(1ll, (pl.units + items - 1) / items);
+        // (a request has no more: a first key plus a run stays far below 2^31)
+        pl.run = (int)std::min(std::max(blocks, 1ll), std::max(1ll, (pl.units + items - 1) / items));
         pl.units = (long long)B * Hkv * ((blocks + pl.run - 1) / pl.run);
         pl.chunk = (int)tokens;
         return pl.units >= 1ll << 31 ? report(PKD_EUNSUPPORTED, "too many work items") : PKD_OK;

@@ -239,3 +239,19 @@ def test_parts_of_a_wider_table_are_not_read_past_their_columns(monkeypatch):
     close(got, want, err, p["lens"])
     with pytest.raises(pkd.PkdError, match="stride"):  # a table that does not have the columns
         pkd.key_weights(*args, max_query_len=1, max_kv_len=256)
+
+
+def test_more_requests_than_runs_of_key_blocks():
+    """Few rows of many short requests: runs end with a request's blocks."""
+    rng = np.random.default_rng(15)
+    new = rng.integers(0, 10, 180).tolist()
+    lens = [n + int(rng.integers(0, 60)) for n in new]
+    lens[7], lens[90] = 700, 300
+    p = problem(16, new=new, lens=lens, heads=16, kv=8, dim=64, page=16, dtype="bf16")
+    lse = lses(p)
+    want, err = ref.key_weights(p["qv"], p["cv"], p["table"], p["lens"], p["starts"], lse.astype(np.float64), p["scale"])
+    args = (p["q"].cuda(), p["cache"].cuda(), dev(p["table"]), dev(p["lens"]), dev(p["starts"]), dev(lse), p["scale"])
+    got = pkd.key_weights(*args, max_query_len=9)
+    close(got, want, err, lens)
+    for most in (700, 704):  # the table's columns hold no more
+        assert torch.equal(pkd.key_weights(*args, max_query_len=9, max_kv_len=most)[..., :700], got[..., :700])
