@@ -862,7 +862,9 @@ def key_weights(q, kv_cache, block_table, seq_lens, query_start, lse, scale, *, 
     heads of each kv head is added to decay * weights (fp32 [B, Hkv, keys]; keys of
     the call's own tokens start at 0).  Returns out, fp32 [B, Hkv, keys]: entries
     behind seq_lens[b] keep what was in it (0 where the call allocates it).  out may
-    be weights.  workspace_check reads the status, as for paged_attention.
+    be weights.  max_kv_len chooses how a prompt's work is split: give the batch's
+    own where the table is far wider.  workspace_check reads the status, as for
+    paged_attention.
     test_timeout sets the diagnostic PKD_FLAG_TEST_TIMEOUT (prompts only).
     """
     index = q.get_device()
@@ -942,6 +944,8 @@ def evict_select(weights, seq_lens, budget, *, sinks=0, recent=0, pool=1, positi
     weight of the pool keys around a key that are neither.  After a compaction
     has put keys out of order, positions (int32 [B, Hkv, keys]) says where each
     stood and context_lens (int32 [B]) how many tokens the request has seen.
+    The width of weights chooses how many threads a row gets: give
+    weights[..., :longest] of a tensor that is far wider than the lengths.
     Lengths outside [0, keys] are clamped; workspace_check (of workspace, 256 bytes
     or more, or of the one kept for calls without) then says so.
     Returns (kept int32 [B, Hkv, budget]: rising indexes, -1 behind them,

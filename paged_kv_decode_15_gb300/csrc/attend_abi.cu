@@ -201,8 +201,8 @@ pkd_status plan_key_weights(int B, long long T, int max_q, int last, int Hq, int
     pl.step = pl.rows <= 16;
     pl.max_splits = 1;
     if (pl.step) {
-        // about 32 CTAs per SM, chunks of 128 to 2048 keys (16: 55 and 68 us on the cases of
-        // key_weights.cu, not 55 and 65)
+        // about 32 CTAs per SM, chunks of 128 to 2048 keys (16: 53 and 68 us on the cases of
+        // key_weights.cu, not 54 and 64)
         const long long units = std::max(1ll, (long long)B * Hkv);
         const long long chunk = std::min(2048ll, std::max(128ll, max_kv_len * units / (32 * kSms)));
         pl.chunk = up((int)chunk, 128);
@@ -212,14 +212,14 @@ pkd_status plan_key_weights(int B, long long T, int max_q, int last, int Hq, int
     const long long tok = pkd::kPtRows / (Hq / Hkv), tiles = (tokens + tok - 1) / tok;
     pl.units = (long long)B * Hkv * ((max_kv_len + pkd::kWtKeys - 1) / pkd::kWtKeys);
     // the tokens are split while the key blocks alone leave SMs idle: into sixteen items per
-    // SM (a CTA takes its next item one ahead: four per SM 975 us for 16384 tokens, sixteen
-    // 944), of four query tiles at least
+    // SM (a CTA takes its next item one ahead: four per SM 912 us for 16384 tokens, sixteen
+    // 876), of four query tiles at least
     pl.run = 1;
     pl.stay = tiles <= pkd::kWtStay;
     if (pl.stay) {
         // runs of key blocks, as many as SMs where the one length is known, else eight per SM
-        // (64 requests of 1024 to 4096 keys, 32 and 128 rows: 76 and 97 us, four 81 and 118,
-        // thirty-two 92 and 102)
+        // (64 requests of 1024 to 4096 keys, up to 32 and 128 rows: 83 and 109 us, four 91 and
+        // 130, thirty-two 97 and 111)
         const long long blocks = (max_kv_len + pkd::kWtKeys - 1) / pkd::kWtKeys, items = B == 1 ? kSms : 8 * kSms;
         // (a request has no more: a first key plus a run stays far below 2^31)
         pl.run = (int)std::min(std::max(blocks, 1ll), std::max(1ll, (pl.units + items - 1) / items));

@@ -271,7 +271,10 @@ __device__ __forceinline__ float pt_max(const uint32_t (&v)[32]) {
 }
 
 // The weights 2^(scale x - m) of a chunk, packed to the operand type, and their sum:
-// l sums the fp32 weights, the product takes them rounded.
+// l sums the fp32 weights, the product takes them rounded: its operands are of one type, and
+// 32-bit ones would run at half the rate or less.  Each is off by half a step of its own, in
+// either direction: a 16384-token bf16 prompt is off by 2.3e-3 of its norm, 1.65e-3 of which is
+// the rounding of the results.
 template <bool kBF16>
 __device__ __forceinline__ float pt_weights(const uint32_t (&v)[32], uint32_t (&pk)[16], float scale, float m) {
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};

@@ -9,7 +9,7 @@
 // searched where they are).  Bound by the rows' bytes, read and written (32 lists of 4096
 // of up to 32768 keys, 512-byte rows: 24.1 us, 4.7 TB/s, 0.69 of the copy); for few rows by
 // the chain lengths - list - table - rows of trips to memory (512 lists of 1024 of 1088
-// keys: 6.2 us, of which the bytes take 5).  Searched in global memory: 31 and 22 us.
+// keys: 6.6 us, of which the bytes take 5).  Searched in global memory: 31 and 22 us.
 #include <algorithm>
 
 #include "evict.cuh"

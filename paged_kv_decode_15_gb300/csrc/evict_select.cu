@@ -16,13 +16,14 @@
 // pass).  Long rows, and few rows, are spread over a cluster of CTAs that add their
 // histograms up in the first one's shared memory.
 //
-// What bounds it (512 rows of 1024 to 4096 keys, pooled over 7: 15.5 us; 32 rows of up to
-// 131072 keys, clusters of eight: 25.5 us, one such row 23; eight rows of 1088 keys: 6.5 us;
-// bytes alone would take 1, 2, 0 and 0 us): the chain of two or three rounds, each a pass
-// over a thread's keys, a scan and its barriers.  Three bits a round, counted in registers,
-// took 124 and 567 us; pooled from global memory 18.4; three cluster barriers a round, not
-// two, 27; ranks in shared memory, walked in rolled loops (the unrolled ones wait for their
-// instructions), 17.9 and 24.4.
+// What bounds it (512 rows of 1024 to 4096 keys, pooled over 7: 16.4 us; 32 rows of up to
+// 131072 keys, clusters of eight: 26.5 us, one such row 23; eight rows of 1088 keys: 7.0 us;
+// bytes alone would take 1, 2, 0 and 0 us): instructions where there are many rows (issue slots
+// 63 % active, 235 instructions to 32 keys: each of the two or three rounds walks all of a
+// thread's ranks again), the chain of the rounds' scans and barriers where there are few.
+// Three bits a round, counted in registers, took 124 and 567 us; pooled from global memory 18.4;
+// three cluster barriers a round, not two, 27; ranks in shared memory, walked in rolled loops
+// (the unrolled ones wait for their instructions), 17.9 and 24.4.
 #include <cooperative_groups.h>
 
 #include <type_traits>

@@ -9,8 +9,8 @@
 // finds the bytes that it copied itself: no barrier and no swizzle.  Then exp2(logit - lse),
 // the sum over a lane's rows and over its quad, and one 4-byte store per key.
 //
-// What bounds it (64 requests of 1024 to 4096 keys, 8 kv heads, bf16: 55 us, 5.6 TB/s of the
-// copy's 6.8; 4 contexts of up to 131072 keys, e4m3, 8 rows: 65 us, 5.4 TB/s): a warp's step
+// What bounds it (64 requests of 1024 to 4096 keys, 8 kv heads, bf16: 54 us, 5.7 TB/s of the
+// copy's 6.8; 4 contexts of up to 131072 keys, e4m3, 8 rows: 64 us, 5.5 TB/s): a warp's step
 // is a chain of products, exponentials and votes of its quad, and a CTA's first keys wait
 // for two trips to memory, so that warps in number count for more than bytes in flight:
 // twenty warps of two stages each, not eight of six (78 us), with the table asked for
