@@ -41,7 +41,8 @@
 // once per row, and 2^x the hardware's: off by 2^-24 of |lse log2 e| and by 2^-22.  The tensor
 // cores' sums lie towards zero by more than that; the attention kernel's LSE, of the same sums, is
 // low by as much (1.1e-6 on average for the last 64 of 32768 tokens), so that beside it the weights
-// are off by 7e-7 of their norm, beside an LSE of 64 bits by 1.6e-6.  A row of LSE -inf weighs nothing: tiles with one take the masked pass.
+// are off by 7e-7 of their norm, beside an LSE of 64 bits by 1.6e-6.  A row of LSE -inf weighs
+// nothing: tiles with one take the masked pass.
 // A request's query rows are split between items where its key blocks alone leave SMs
 // idle; the sums of the parts are joined in order by the last to arrive.
 #pragma once
